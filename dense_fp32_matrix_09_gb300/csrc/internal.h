@@ -213,4 +213,70 @@ long long launch_tf32_probe(int *status, int clusters, int iters, cudaStream_t s
 // sink: ctas * 32 floats.
 cudaError_t launch_bank_probe(float *sink, int padded, int ctas, int iters, cudaStream_t stream);
 
+// ---- rows to 8 bits, rows to the experts and back (sgemm_experts.cu) -------------
+constexpr int kMaxExperts = 1024;
+
+// One call's arguments after validation.  X: the tokens' rows (tokens x width);
+// Y, dY: the sorted rows (tokens * choices x width); rows: the sorted row of
+// each (token, choice) slot, or a value outside [0, tokens * choices).
+struct MoveArgs {
+    const void *X;
+    long long ldx;
+    int tokens, choices, width;
+    const int *rows;       // NULL (launch_quantize only): slot i goes to row i
+    const float *weights;  // NULL (launch_gather only): all ones
+    void *Y;
+    long long ldy;
+    void *dY;
+    long long lddy;
+    float *scale;  // launch_quantize: the rows' scales; launch_combine_grad: the weights' gradient
+};
+// Y (int8) and scale = the quantized rows of X.
+cudaError_t launch_quantize(int type, const MoveArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t sort_prepare();
+// hist: hist_ints ints of workspace.
+cudaError_t launch_sort(const int *ids, int slots, int experts, int *offsets, int *rows, int *source, int *hist,
+                        size_t hist_ints, int *launches, cudaStream_t stream);
+cudaError_t launch_dispatch(int type, const MoveArgs &a, cudaStream_t stream);
+// X (written) = the weighted sums of Y's rows.
+cudaError_t launch_gather(int type, const MoveArgs &a, cudaStream_t stream);
+// X: the gradient of the tokens' rows.
+cudaError_t launch_combine_grad(int type, const MoveArgs &a, cudaStream_t stream);
+
+// ---- int8 products (sgemm_int8.cu) ----------------------------------------------
+// C[i][j] = (sum_p A[i][p] B_e[j][p]) * scaleB[e][j] * scaleA[i] + bias[e][j] for
+// the rows i of [row0, row0 + rows) that expert e owns (offsets[e] <= i <
+// offsets[e+1]; offsets NULL: one expert, every row).
+struct Int8Args {
+    int rows, N, K, experts;
+    int row0, total_rows;  // this launch's rows are row0 .. row0 + rows - 1 of total_rows
+    const int *offsets;
+    const int8_t *A;
+    long long lda;
+    const int8_t *B;
+    long long ldb, strideB;
+    int transB;  // B stored N x K
+    const float *scaleA, *scaleB, *bias;
+    void *C;
+    long long ldc;
+    int out_type;
+    int *status;
+    // tensor-core kernel: token tile, CTAs that share a tile's K range
+    int nt, ksplit;
+};
+cudaError_t launch_int8_generic(const Int8Args &a, cudaStream_t stream);
+// dst (rows x ldd FP16, ldd a multiple of 8) = the int8 rows of A, columns K..ldd-1 zero.
+cudaError_t launch_int8_to_f16(const int8_t *A, long long lda, int rows, int K, void *dst, int ldd,
+                               cudaStream_t stream);
+// dst (experts x N x ldd, columns K..ldd-1 zero) = B_e, stored N x K (trans = 1) or K x N (0).
+cudaError_t launch_int8_relayout(const int8_t *B, long long ldb, long long strideB, int trans, int experts, int N,
+                                 int K, int8_t *dst, int ldd, cudaStream_t stream);
+constexpr int kI8TileN = 128, kI8StageK = 128;  // channels and k of one B stage (TMA box, 128-byte swizzle)
+constexpr int kI8TokenTiles[] = {16, 32, 64, 128};
+cudaError_t int8_prepare();
+// tmB: int8, 3-D (k, channel, expert), box 128 x 128 x 1; tmA: FP16, 2-D (k, row),
+// box 64 x nt; both with the 128-byte swizzle.
+cudaError_t launch_int8_tc(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
+                           int smem_override, cudaStream_t stream);
+
 }  // namespace sg

@@ -1,7 +1,7 @@
 /*
- * Argument marshalling for the two enqueue calls of the Python binding
- * (sgemm_run, sgemm_run_ex) through the CPython C API.  The binding's other
- * calls go through ctypes; these two are on the per-call path, where
+ * Argument marshalling for the enqueue calls of the Python binding (sgemm_run,
+ * sgemm_run_ex, and the int8 and expert calls) through the CPython C API.  The
+ * binding's other calls go through ctypes; these are on the per-call path, where
  * ctypes' generic conversion of a dozen arguments costs a few microseconds
  * -- as much as a small GEMM takes on the GPU.  Nothing here computes: each
  * function converts Python ints, floats, buffers (ints or objects with a
@@ -16,11 +16,79 @@
 
 #include <dlfcn.h>
 #include <limits.h>
+#include <string.h>
 
 typedef int (*run_fn)(void *, int, int, int, float, const float *, int, const float *, int, float, float *, int,
                       void *);
 typedef int (*run_ex_fn)(void *, int, int, int, int, int, float, const float *, int, long long, const float *, int,
                          long long, float, float *, int, long long, int, void *);
+
+/* The int8 and expert calls: every argument between the handle and the stream
+ * is an int (i), a long long (l) or a buffer (p), so one parser serves them
+ * all and a function of each call's own type passes the values on. */
+typedef union {
+    int i;
+    long long l;
+    void *p;
+} arg;
+#define KMAX_ARGS 18
+typedef int (*dispatch_fn)(void *fn, void *h, const arg *v, void *stream);
+
+static int d_run_int8(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, int, const void *, int, const void *, const void *, int, const void *,
+                     const void *, void *, int, void *))fn)(h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].i, v[5].p, v[6].i,
+                                                            v[7].p, v[8].p, v[9].i, v[10].p, v[11].p, v[12].p,
+                                                            v[13].i, s);
+}
+static int d_run_int8_experts(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, int, int, const void *, const void *, int, const void *, const void *,
+                     int, long long, const void *, const void *, void *, int, void *))fn)(
+        h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].i, v[5].i, v[6].p, v[7].p, v[8].i, v[9].p, v[10].p, v[11].i, v[12].l,
+        v[13].p, v[14].p, v[15].p, v[16].i, s);
+}
+static int d_quantize_rows(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, const void *, int, void *, int, void *, void *))fn)(
+        h, v[0].i, v[1].i, v[2].i, v[3].p, v[4].i, v[5].p, v[6].i, v[7].p, s);
+}
+static int d_sort(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, const void *, void *, void *, void *, void *))fn)(
+        h, v[0].i, v[1].i, v[2].i, v[3].p, v[4].p, v[5].p, v[6].p, s);
+}
+/* dispatch and its gradient: rows in, row numbers, rows out */
+static int d_move(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, const void *, int, const void *, void *, int, void *))fn)(
+        h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].p, v[5].i, v[6].p, v[7].p, v[8].i, s);
+}
+static int d_dispatch_int8(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, const void *, int, const void *, void *, int, void *, void *))fn)(
+        h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].p, v[5].i, v[6].p, v[7].p, v[8].i, v[9].p, s);
+}
+static int d_combine(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, const void *, int, const void *, const void *, void *, int,
+                     void *))fn)(h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].p, v[5].i, v[6].p, v[7].p, v[8].p, v[9].i, s);
+}
+static int d_combine_grad(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, const void *, int, const void *, int, const void *, const void *,
+                     void *, int, void *, void *))fn)(h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].p, v[5].i, v[6].p,
+                                                      v[7].i, v[8].p, v[9].p, v[10].p, v[11].i, v[12].p, s);
+}
+
+static struct {
+    const char *name, *kinds;
+    dispatch_fn call;
+    void *fn;
+} g_calls[] = {
+    {"sgemm_run_int8", "iiiiipippipppi", d_run_int8, NULL},
+    {"sgemm_run_int8_experts", "iiiiiippippilpppi", d_run_int8_experts, NULL},
+    {"sgemm_quantize_rows", "iiipipip", d_quantize_rows, NULL},
+    {"sgemm_expert_sort", "iiipppp", d_sort, NULL},
+    {"sgemm_expert_dispatch", "iiiipippi", d_move, NULL},
+    {"sgemm_expert_dispatch_int8", "iiiipippip", d_dispatch_int8, NULL},
+    {"sgemm_expert_dispatch_grad", "iiiipippi", d_move, NULL},
+    {"sgemm_expert_combine", "iiiipipppi", d_combine, NULL},
+    {"sgemm_expert_combine_grad", "iiiipipipppip", d_combine_grad, NULL},
+};
+#define KCALLS ((int)(sizeof(g_calls) / sizeof(g_calls[0])))
 
 static run_fn g_run = NULL;
 static run_ex_fn g_run_ex = NULL;
@@ -123,6 +191,13 @@ static PyObject *py_init(PyObject *self, PyObject *args) {
         PyErr_SetString(PyExc_OSError, "the library exports no sgemm_run / sgemm_run_ex");
         return NULL;
     }
+    for (int c = 0; c < KCALLS; ++c) {
+        g_calls[c].fn = dlsym(lib, g_calls[c].name);
+        if (g_calls[c].fn == NULL) {
+            PyErr_Format(PyExc_OSError, "the library exports no %s", g_calls[c].name);
+            return NULL;
+        }
+    }
     Py_XDECREF(g_current_stream);
     Py_INCREF(cur);
     g_current_stream = cur;
@@ -178,11 +253,47 @@ static PyObject *py_run_ex(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                                     beta, (float *)C, ldc, sC, batch, stream));
 }
 
+/* enqueue(name, h, args, stream) -> status: one of g_calls, args the tuple of
+ * the arguments between the handle and the stream */
+static PyObject *py_enqueue(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    if (n != 4 || !PyUnicode_Check(a[0]) || !PyTuple_Check(a[2])) {
+        PyErr_SetString(PyExc_TypeError, "enqueue takes a name, a handle, a tuple and a stream");
+        return NULL;
+    }
+    const char *name = PyUnicode_AsUTF8(a[0]);
+    if (name == NULL) return NULL;
+    int c = 0;
+    while (c < KCALLS && strcmp(g_calls[c].name, name) != 0) ++c;
+    if (c == KCALLS || g_calls[c].fn == NULL) {
+        PyErr_Format(PyExc_RuntimeError, "no call %s (or init was not called)", name);
+        return NULL;
+    }
+    const char *kinds = g_calls[c].kinds;
+    const Py_ssize_t want = (Py_ssize_t)strlen(kinds);
+    if (PyTuple_GET_SIZE(a[2]) != want) {
+        PyErr_Format(PyExc_TypeError, "%s takes %zd arguments between handle and stream", name, want);
+        return NULL;
+    }
+    void *h, *stream;
+    arg v[KMAX_ARGS];
+    if (as_handle(a[1], &h)) return NULL;
+    for (Py_ssize_t k = 0; k < want; ++k) {
+        PyObject *o = PyTuple_GET_ITEM(a[2], k);
+        const int bad = kinds[k] == 'i' ? as_int(o, &v[k].i) : kinds[k] == 'l' ? as_ll(o, &v[k].l) : as_ptr(o, &v[k].p);
+        if (bad) return NULL;
+    }
+    if (as_stream(a[3], &stream)) return NULL;
+    return PyLong_FromLong(g_calls[c].call(g_calls[c].fn, h, v, stream));
+}
+
 static PyMethodDef kMethods[] = {
     {"init", py_init, METH_VARARGS, "init(library_path, current_stream): bind the library's enqueue calls"},
     {"run", (PyCFunction)(void (*)(void))py_run, METH_FASTCALL, "sgemm_run through the C ABI; returns the status"},
     {"run_ex", (PyCFunction)(void (*)(void))py_run_ex, METH_FASTCALL,
      "sgemm_run_ex through the C ABI; returns the status"},
+    {"enqueue", (PyCFunction)(void (*)(void))py_enqueue, METH_FASTCALL,
+     "an int8 or expert call through the C ABI; returns the status"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_sgemm_calls", NULL, -1, kMethods, NULL, NULL, NULL,

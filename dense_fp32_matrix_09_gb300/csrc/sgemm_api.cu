@@ -15,6 +15,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include "context.h"
 #include "internal.h"
 #include "sgemm.h"
 
@@ -742,8 +743,9 @@ CallPlan plan_call(const sgemm_ctx *h, int transA, int transB, int M, int N, int
     int variant = h->pinned;
     if (!tc_reachable && (variant == SGEMM_VARIANT_TC_3XTF32 || variant == SGEMM_VARIANT_TC_3XTF32_PAIR))
         variant = SGEMM_VARIANT_AUTO;
-    if (variant == SGEMM_VARIANT_TC_F16_PAIR || variant == SGEMM_VARIANT_GENERIC_F16)
-        variant = SGEMM_VARIANT_AUTO;  // 16-bit-input variants: sgemm_run_mixed only
+    if (variant == SGEMM_VARIANT_TC_F16_PAIR || variant == SGEMM_VARIANT_GENERIC_F16 ||
+        variant == SGEMM_VARIANT_TC_I8 || variant == SGEMM_VARIANT_GENERIC_I8)
+        variant = SGEMM_VARIANT_AUTO;  // variants of the 16-bit and 8-bit calls only
     if (variant == SGEMM_VARIANT_AUTO) {
         // 3xTF32 mode: the CTA-pair tensor-core kernel once there are at least
         // about half as many 256 x 256 tiles as CTA pairs and K fills its pipeline
@@ -839,6 +841,37 @@ bool cached_encode(sgemm_ctx *h, CUtensorMap *map, const float *base, int rows, 
 
 }  // namespace
 
+namespace sg {
+
+bool is_live(sgemm_handle_t h) { return alive(h); }
+
+void view_of(sgemm_handle_t h, HandleView *v) {
+    *v = HandleView{h->device, h->num_sms, h->d_status, h->d_ws, h->ws_floats, h->d_rl,
+                    h->rl_floats * sizeof(float), h->pinned, h->relayout_mode, h->smem_override};
+}
+
+void record_call(sgemm_handle_t h, int variant, int splits, int launches, int copied) {
+    h->last_variant = variant;
+    h->last_splits = splits;
+    h->last_launches = launches;
+    h->last_relayout = copied;
+}
+
+bool encode_map(CUtensorMap *map, MapType type, int dims, const void *base, long long cols, long long rows,
+                long long planes, long long row_bytes, long long plane_bytes, int box_cols, int box_rows) {
+    cuuint64_t dim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                         static_cast<cuuint64_t>(planes)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(plane_bytes)};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode(map, type == MapType::kInt8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    static_cast<cuuint32_t>(dims), const_cast<void *>(base), dim, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace sg
+
 extern "C" {
 
 int sgemm_version(void) { return 10000; }
@@ -875,6 +908,8 @@ const char *sgemm_variant_name(int v) {
         case SGEMM_VARIANT_TC_3XTF32_PAIR: return "tc_3xtf32_pair";
         case SGEMM_VARIANT_TC_F16_PAIR: return "tc_f16_pair";
         case SGEMM_VARIANT_GENERIC_F16: return "generic_f16";
+        case SGEMM_VARIANT_TC_I8: return "tc_i8";
+        case SGEMM_VARIANT_GENERIC_I8: return "generic_i8";
         default: return "unknown";
     }
 }
@@ -936,7 +971,7 @@ int sgemm_create(sgemm_handle_t *out) {
         if (occupancy[v] < 1) return SGEMM_ERR_CUDA;
     }
     if (sg::tc3x_prepare() != cudaSuccess || sg::tc3x_pair_prepare() != cudaSuccess ||
-        sg::tc16_prepare() != cudaSuccess)
+        sg::tc16_prepare() != cudaSuccess || sg::int8_prepare() != cudaSuccess || sg::sort_prepare() != cudaSuccess)
         return SGEMM_ERR_CUDA;
     occupancy[SGEMM_VARIANT_TC_3XTF32] = 1;
     occupancy[SGEMM_VARIANT_TC_3XTF32_PAIR] = 1;

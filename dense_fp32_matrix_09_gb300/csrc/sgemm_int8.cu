@@ -1,0 +1,706 @@
+// 8-bit integer products for sm_103a:
+//
+//   C[i][j] = (sum_p A[i][p] * B_e[j][p]) * scaleB[e][j] * scaleA[i] + bias[e][j]
+//
+// with A (tokens x K) and B_e (channels x K) in int8, one scale a token and one
+// a channel, C in FP32, BF16 or FP16; e is the expert that owns row i (one
+// expert owns every row in the dense call).  The sum is exact in 32-bit
+// integers; float(sum) * scaleB * scaleA (+ bias) is rounded to the output type
+// once.
+//
+// The tensor cores of sm_103a have no 8-bit integer MMA (.kind::i8 is not
+// assembled for it) and the CUDA cores' and mma.sync's integer rates are far
+// below the 16-bit rate of tcgen05.  An int8 is exact in FP16, a product of two
+// in FP32, and a sum of 1024 such products has magnitude <= 2^24, so it is an
+// integer that FP32 holds exactly: the kernel multiplies with .kind::f16, FP32
+// accumulators in tensor memory, and moves them into int32 registers every
+// 1024 k.  Sums of integers do not depend on their order, so every split of K
+// gives the same bits.
+//
+//  * int8_tc_kernel -- D[channel][token] = B * A^T with the channels as the
+//    MMA's M (128 rows) and a tile of NT tokens as its N, so that few tokens
+//    cost a narrow tile and not a padded one.  B crosses HBM and shared memory
+//    as int8 (half the bytes of 16-bit operands; it is what a decode step is
+//    bound by) and becomes FP16 only on its way into tensor memory, where the
+//    MMA reads it as its A operand: shared memory sees one 8-bit write and one
+//    8-bit read of it.  The tokens' rows are converted to FP16 once, by
+//    int8_to_f16_kernel, and read by TMA.
+//      warp 0     TMA producer: a ring of stages of 128 k (B: 128 x 128 bytes,
+//                 tokens: two swizzled boxes of 64 k x NT)
+//      warp 1     one lane issues the MMAs; owns the tensor memory
+//      warp 2     sums up the experts' token tiles once, at the start
+//      warps 4-11 two warpgroups convert half of each stage: a thread reads 64
+//                 bytes of its channel (16 at a time, conflict-free through the
+//                 swizzle), turns byte b into the FP16 bits 0x6400 + (b ^ 0x80)
+//                 = 1152 + b, subtracts 1152 (exact), and stores 32 columns of
+//                 tensor memory.  (Alternate stages would not do: a warp that
+//                 skips a phase of a stage's barrier cannot tell by its parity
+//                 whether the phase before has ended when the ring is odd.)
+//      warps 12.. one or two warpgroups drain the accumulators (two of NT
+//                 columns each, so that the next 1024 k start at once) and
+//                 write C: a warp's lanes are 32 consecutive channels of a token
+//    Tensor memory: 2 x NT accumulator columns and 4 stages of 64 columns of B.
+//    Persistent over (expert, token tile, channel tile) units, token tiles
+//    innermost within groups of 16 so that concurrent CTAs share B's tiles in L2.
+//    With few tiles the 2, 4 or 8 CTAs of a cluster share a tile's K range;
+//    each sends the others their columns' int32 partial sums through
+//    distributed shared memory.
+//  * int8_generic_kernel -- any layout and alignment, dp4a on the CUDA cores.
+//  * int8_to_f16_kernel, int8_relayout_kernel -- the tokens' rows as FP16, and B
+//    as the TMA can read it (stored K x N, or not on 16-byte boundaries).
+// Every wait is bounded; on a timeout the kernel records it, waits (bounded)
+// for its own copies and MMAs in flight, frees the tensor memory and returns.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "device_common.cuh"
+#include "internal.h"
+#include "sgemm.h"
+#include "tcgen05.cuh"
+
+namespace sg {
+namespace {
+
+// ---- epilogue arithmetic, common to both kernels --------------------------------
+__device__ __forceinline__ float int8_value(int sum, float sb, float sa, float bias) {
+    return fmaf(__int2float_rn(sum) * sb, sa, bias);
+}
+
+template <class T>
+__device__ __forceinline__ T int8_out(float v);
+template <>
+__device__ __forceinline__ float int8_out<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 int8_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half int8_out<__half>(float v) { return __float2half_rn(v); }
+
+// Call f with a value of the output type.
+template <class F>
+__device__ __forceinline__ void with_out_type(int type, F &&f) {
+    if (type == SGEMM_IN_BF16) f(__nv_bfloat16{});
+    else if (type == SGEMM_IN_F16) f(__half{});
+    else f(0.f);
+}
+
+// offsets[e], kept within the rows there are (whatever the array holds).
+__device__ __forceinline__ int bound_of(const Int8Args &a, int e) {
+    if (!a.offsets) return e == 0 ? 0 : a.total_rows;
+    return min(max(__ldg(a.offsets + e), 0), a.total_rows);
+}
+
+// ---- generic kernel -----------------------------------------------------------
+// 64 x 64 tile of C, 64 k a step as 16 packed words a row, 4 x 4 sums a thread.
+constexpr int kGTile = 64, kGWords = 16;
+
+__global__ void __launch_bounds__(256) int8_generic_kernel(const Int8Args a) {
+    __shared__ int As[kGWords][kGTile + 1], Bs[kGWords][kGTile + 1];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+    const int n0 = blockIdx.x * kGTile;
+    for (int e = blockIdx.z; e < a.experts; e += gridDim.z) {
+        const int8_t *B = a.B + e * a.strideB;
+        const int lo = max(bound_of(a, e), a.row0), hi = min(bound_of(a, e + 1), a.row0 + a.rows);
+        for (int m0 = lo + static_cast<int>(blockIdx.y) * kGTile; m0 < hi; m0 += static_cast<int>(gridDim.y) * kGTile) {
+            int acc[4][4] = {};
+            for (int k0 = 0; k0 < a.K; k0 += 4 * kGWords) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = tid + r * 256, w = at % kGWords, i = at / kGWords;
+                    unsigned av = 0, bv = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const int k = k0 + 4 * w + b;
+                        if (k >= a.K) break;
+                        if (m0 + i < hi)
+                            av |= static_cast<unsigned>(static_cast<uint8_t>(a.A[static_cast<long long>(m0 + i) * a.lda + k])) << (8 * b);
+                        if (n0 + i < a.N)
+                            bv |= static_cast<unsigned>(static_cast<uint8_t>(
+                                      a.transB ? B[static_cast<long long>(n0 + i) * a.ldb + k]
+                                               : B[static_cast<long long>(k) * a.ldb + n0 + i])) << (8 * b);
+                    }
+                    As[w][i] = static_cast<int>(av);
+                    Bs[w][i] = static_cast<int>(bv);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int w = 0; w < kGWords; ++w) {
+                    int x[4], y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = As[w][ty + 16 * i];
+                        y[i] = Bs[w][tx + 16 * i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(x[i], y[j], acc[i][j]);
+                }
+                __syncthreads();
+            }
+            with_out_type(a.out_type, [&](auto zero) {
+                using T = decltype(zero);
+                T *C = static_cast<T *>(a.C);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = m0 + ty + 16 * i;
+                    if (row >= hi) continue;
+                    const float sa = __ldg(a.scaleA + row);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int ch = n0 + tx + 16 * j;
+                        if (ch >= a.N) continue;
+                        const long long at = static_cast<long long>(e) * a.N + ch;
+                        C[static_cast<long long>(row) * a.ldc + ch] = int8_out<T>(
+                            int8_value(acc[i][j], __ldg(a.scaleB + at), sa, a.bias ? __ldg(a.bias + at) : 0.f));
+                    }
+                }
+            });
+        }
+    }
+}
+
+// ---- operand copies -------------------------------------------------------------
+// Four int8 (a word) as two pairs of FP16: 0x6400 + u is the FP16 value 1024 + u,
+// u = b + 128 the biased byte; minus 1152 gives b, exactly.
+__device__ __forceinline__ void int8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t p = __byte_perm(u, 0x64646464u, 0x4140), q = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&p), off);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&q), off);
+    lo = *reinterpret_cast<const uint32_t *>(&a);
+    hi = *reinterpret_cast<const uint32_t *>(&b);
+}
+
+// Bytes p[0..15] of a row of which `n` remain (zeros beyond).
+__device__ __forceinline__ uint4 load_int8x16(const int8_t *p, int n, bool vec) {
+    if (vec && n >= 16) return __ldg(reinterpret_cast<const uint4 *>(p));
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 16 k a thread; ldd is a multiple of 64, so its rows divide into whole threads.
+__global__ void __launch_bounds__(256)
+int8_to_f16_kernel(const int8_t *__restrict__ A, long long lda, int rows, int K, uint4 *__restrict__ dst, int ldd,
+                   int vec) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int per_row = ldd / 16;
+    const long long total = static_cast<long long>(rows) * per_row;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const long long row = div_floor(i, per_row);
+        const int k = static_cast<int>(i - row * per_row) * 16;
+        const uint4 v = k < K ? load_int8x16(A + row * lda + k, K - k, vec) : make_uint4(0, 0, 0, 0);
+        uint4 o0, o1;
+        int8x4_to_f16(v.x, o0.x, o0.y);
+        int8x4_to_f16(v.y, o0.z, o0.w);
+        int8x4_to_f16(v.z, o1.x, o1.y);
+        int8x4_to_f16(v.w, o1.z, o1.w);
+        dst[2 * i] = o0;
+        dst[2 * i + 1] = o1;
+    }
+}
+
+// B stored N x K, rows copied onto 16-byte boundaries: 16 k a thread.
+__global__ void __launch_bounds__(256)
+int8_realign_kernel(const int8_t *__restrict__ B, long long ldb, long long strideB, int N, int K,
+                    int8_t *__restrict__ dst, int ldd) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int per_row = ldd / 16;
+    const int8_t *src = B + blockIdx.y * strideB;
+    int8_t *d = dst + static_cast<long long>(blockIdx.y) * N * ldd;
+    const long long total = static_cast<long long>(N) * per_row;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const long long row = div_floor(i, per_row);
+        const int k = static_cast<int>(i - row * per_row) * 16;
+        reinterpret_cast<uint4 *>(d)[i] = load_int8x16(src + row * ldb + k, K - k, false);
+    }
+}
+
+// B stored K x N -> N x ldd: a tile of 128 k x 64 channels through shared memory
+// (rows of 65 bytes: the 8 lanes that gather 16 k each of one channel fall in
+// distinct banks).
+constexpr int kTK = 128, kTN = 64;
+
+__global__ void __launch_bounds__(256)
+int8_transpose_kernel(const int8_t *__restrict__ B, long long ldb, long long strideB, int N, int K,
+                      int8_t *__restrict__ dst, int ldd) {
+    __shared__ uint8_t tile[kTK][kTN + 1];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int8_t *src = B + blockIdx.z * strideB;
+    int8_t *d = dst + static_cast<long long>(blockIdx.z) * N * ldd;
+    const int k0 = blockIdx.x * kTK;
+    for (int n0 = blockIdx.y * kTN; n0 < N; n0 += gridDim.y * kTN) {
+        uint8_t v[kTK * kTN / 256];
+#pragma unroll
+        for (int r = 0; r < kTK * kTN / 256; ++r) {
+            const int at = threadIdx.x + r * 256, k = at / kTN, n = at % kTN;
+            v[r] = (k0 + k < K && n0 + n < N) ? static_cast<uint8_t>(src[static_cast<long long>(k0 + k) * ldb + n0 + n]) : 0;
+        }
+#pragma unroll
+        for (int r = 0; r < kTK * kTN / 256; ++r) {
+            const int at = threadIdx.x + r * 256;
+            tile[at / kTN][at % kTN] = v[r];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kTN * (kTK / 16) / 256; ++r) {
+            const int at = threadIdx.x + r * 256, kg = at % (kTK / 16), n = at / (kTK / 16);
+            if (n0 + n < N && k0 + kg * 16 < ldd) {
+                uint32_t w[4] = {};
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i / 4] |= static_cast<uint32_t>(tile[kg * 16 + i][n]) << (8 * (i % 4));
+                *reinterpret_cast<uint4 *>(d + static_cast<long long>(n0 + n) * ldd + k0 + kg * 16) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---- tensor-core kernel -----------------------------------------------------------
+constexpr int kBBytes = kI8TileN * kI8StageK;  // 16 KiB of B a stage
+constexpr int kAStages = 4, kACols = kI8StageK / 2;  // stages of B in tensor memory, 32-bit columns each
+constexpr int kChunk = 8;                       // stages (1024 k) between drains of an accumulator
+constexpr int kConvWGs = 2;
+constexpr uint32_t kI8TmemCols = 512;
+constexpr int kMaxStages = 10;
+constexpr int kSmemLimit = 232448;
+
+struct I8Shared {
+    uint64_t full[kMaxStages];   // B and the tokens of the stage have landed
+    uint64_t empty[kMaxStages];  // the converting warps have read B, the MMAs have read the tokens
+    uint64_t afull[kAStages];    // the stage's B stands in tensor memory (the converting warps)
+    uint64_t aempty[kAStages];   // the MMAs that read it have finished
+    uint64_t dfull[2];           // an accumulator holds up to 1024 k
+    uint64_t dempty[2];          // it has been read
+    uint64_t drained;            // abort only: every MMA issued has finished
+    uint32_t tmem_base;
+    int abort;
+    int units;                   // units of this launch
+    int bound[kMaxExperts + 1];  // first row of each expert, nondecreasing
+    int tiles[kMaxExperts + 1];  // token tiles of the experts before
+};
+
+template <int NT, bool SPLIT>
+struct I8Cfg {
+    static constexpr int kTokenBytes = NT * kI8StageK * 2;
+    static constexpr int kStage = kBBytes + kTokenBytes;
+    static constexpr int kXchg = SPLIT ? kI8TileN * NT * 4 : 0;  // partial sums from the cluster's CTAs
+    static constexpr int kFree = kSmemLimit - 1024 - static_cast<int>(sizeof(I8Shared)) - kXchg;
+    static constexpr int kStages = kFree / kStage < kMaxStages ? kFree / kStage : kMaxStages;
+    static constexpr int kSmem = 1024 + kStages * kStage + kXchg + static_cast<int>(sizeof(I8Shared));
+    static constexpr int kEpiWGs = NT > 64 ? 2 : 1;
+    static constexpr int kCols = NT / kEpiWGs;  // accumulator columns a thread drains
+    static constexpr int kThreads = 128 * (1 + kConvWGs + kEpiWGs);
+    static_assert(2 * NT + kAStages * kACols <= static_cast<int>(kI8TmemCols), "tensor memory");
+    static_assert(kStages >= 3 && kSmem <= kSmemLimit, "shared memory");
+};
+
+struct I8Unit {
+    int e, ch0, t0, tend;
+};
+
+// Unit u: the expert by bisection of the tile counts; within the expert groups
+// of 16 token tiles, channel tiles outer and token tiles inner.
+__device__ __forceinline__ I8Unit unit_of(const I8Shared *sh, const Int8Args &a, int nt, int ch_tiles, int u) {
+    int lo = 0, hi = a.experts;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (sh->tiles[mid] * ch_tiles <= u) lo = mid; else hi = mid;
+    }
+    constexpr int kGroup = 16;
+    const int mine = sh->tiles[lo + 1] - sh->tiles[lo];
+    const int l = u - sh->tiles[lo] * ch_tiles;
+    const int grp = l / (kGroup * ch_tiles), first = grp * kGroup;
+    const int rows = min(mine - first, kGroup);
+    const int r = l - grp * kGroup * ch_tiles;
+    I8Unit q;
+    q.e = lo;
+    q.ch0 = r / rows * kI8TileN;
+    q.t0 = max(sh->bound[lo], a.row0) + (first + r % rows) * nt;
+    q.tend = min(sh->bound[lo + 1], a.row0 + a.rows);
+    return q;
+}
+
+// One warp: the experts' first rows and the sums of their token tiles.
+__device__ __forceinline__ void sum_tiles(I8Shared *sh, const Int8Args &a, int nt, int ch_tiles, int lane) {
+    int top = 0, sum = 0;
+    for (int e0 = 0; e0 <= a.experts; e0 += 32) {
+        const int e = e0 + lane;
+        int b = e <= a.experts ? bound_of(a, e) : 0;
+        b = max(b, top);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, b, d);
+            if (lane >= d) b = max(b, up);
+        }
+        if (e <= a.experts) sh->bound[e] = b;
+        top = __shfl_sync(0xffffffffu, b, 31);
+    }
+    __syncwarp();
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+        const int e = e0 + lane;
+        int n = 0;
+        if (e < a.experts) {
+            const int lo = max(sh->bound[e], a.row0), hi = min(sh->bound[e + 1], a.row0 + a.rows);
+            n = hi > lo ? (hi - lo + nt - 1) / nt : 0;
+        }
+        int s = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += up;
+        }
+        if (e < a.experts) sh->tiles[e] = sum + s - n;
+        sum += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) {
+        sh->tiles[a.experts] = sum;
+        sh->units = sum * ch_tiles;
+    }
+}
+
+template <int NT, bool SPLIT>
+__global__ void __launch_bounds__(I8Cfg<NT, SPLIT>::kThreads, 1)
+int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA, const Int8Args a) {
+    using Cf = I8Cfg<NT, SPLIT>;
+    constexpr int S = Cf::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+    uint8_t *ring = smem_raw + pad;
+    int *xchg = reinterpret_cast<int *>(ring + S * Cf::kStage);
+    I8Shared *sh = reinterpret_cast<I8Shared *>(ring + S * Cf::kStage + Cf::kXchg);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int splits = SPLIT ? a.ksplit : 1;
+    const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+    const int first_unit = SPLIT ? static_cast<int>(blockIdx.x) / splits : static_cast<int>(blockIdx.x);
+    const int unit_step = SPLIT ? static_cast<int>(gridDim.x) / splits : static_cast<int>(gridDim.x);
+    const int ch_tiles = (a.N + kI8TileN - 1) / kI8TileN;
+    const int kt = (a.K + kI8StageK - 1) / kI8StageK;
+    // this CTA's stages of every unit
+    const int kb = SPLIT ? rank * kt / splits : 0, ke = SPLIT ? (rank + 1) * kt / splits : kt;
+
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], 4 * kConvWGs + 1);
+        }
+        for (int s = 0; s < kAStages; ++s) {
+            mbar_init(&sh->afull[s], 4 * kConvWGs);
+            mbar_init(&sh->aempty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh->dfull[s], 1);
+            mbar_init(&sh->dempty[s], 4 * Cf::kEpiWGs);
+        }
+        mbar_init(&sh->drained, 1);
+        sh->abort = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmA);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&sh->tmem_base, kI8TmemCols);
+        tc::tmem_relinquish();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    if (warp == 2) sum_tiles(sh, a, NT, ch_tiles, lane);
+    tc::fence_before_sync();
+    __syncthreads();
+    if (SPLIT) cluster_sync();  // every CTA runs before another writes into it
+    tc::fence_after_sync();
+    const uint32_t tmem = sh->tmem_base;
+    const uint32_t tmem_a = tmem + 2 * NT;
+    volatile int *abort_flag = &sh->abort;
+    const int units = sh->units;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (*abort_flag) return false;
+        if (mbar_wait(bar, parity, a.status)) return true;
+        *abort_flag = 1;
+        return false;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        int it = 0;
+        bool ok = true;
+        for (int u = first_unit; u < units; u += unit_step) {
+            if (lane == 0 && ok) {
+                const I8Unit q = unit_of(sh, a, NT, ch_tiles, u);
+                for (int i = kb; i < ke; ++i, ++it) {
+                    const int s = it % S;
+                    if (it >= S && !wait(&sh->empty[s], (it / S - 1) & 1)) { ok = false; break; }
+                    uint8_t *st = ring + s * Cf::kStage;
+                    mbar_arrive_expect_tx(&sh->full[s], Cf::kStage);
+                    tma_load_3d(st, &tmB, &sh->full[s], i * kI8StageK, q.ch0, q.e);
+                    tma_load_2d(st + kBBytes, &tmA, &sh->full[s], i * kI8StageK, q.t0 - a.row0);
+                    tma_load_2d(st + kBBytes + NT * 128, &tmA, &sh->full[s], i * kI8StageK + 64, q.t0 - a.row0);
+                }
+            }
+            __syncwarp();
+            if (SPLIT) {
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+        if (lane == 0)  // no copy outlives the CTA
+            for (int t = max(0, it - S); t < it; ++t) mbar_wait(&sh->full[t % S], (t / S) & 1, a.status);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        constexpr uint32_t idesc = tc::idesc_f16_kmajor(kI8TileN, NT);
+        int it = 0, chunk = 0;
+        bool ok = true;
+        for (int u = first_unit; u < units; u += unit_step) {
+            if (lane == 0 && ok) {
+                for (int i = kb; i < ke; ++i, ++it) {
+                    const int s = it % S, t = it % kAStages, d = chunk & 1;
+                    const bool start = (i - kb) % kChunk == 0;
+                    if ((start && chunk >= 2 && !wait(&sh->dempty[d], (chunk / 2 - 1) & 1)) ||
+                        !wait(&sh->full[s], (it / S) & 1) || !wait(&sh->afull[t], (it / kAStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t b = smem_u32(ring + s * Cf::kStage + kBBytes);
+#pragma unroll
+                    for (int kk = 0; kk < kI8StageK / 16; ++kk)
+                        tc::mma_f16_ta(tmem + d * NT, tmem_a + t * kACols + kk * 8,
+                                       tc::smem_desc(b + (kk / 4) * NT * 128 + (kk % 4) * 32, 16, 1024,
+                                                     tc::kLayoutSwizzle128),
+                                       idesc, (start && kk == 0) ? 0u : 1u);
+                    tc::commit(&sh->empty[s]);
+                    tc::commit(&sh->aempty[t]);
+                    if (i + 1 == ke || (i + 1 - kb) % kChunk == 0) {
+                        tc::commit(&sh->dfull[d]);
+                        ++chunk;
+                    }
+                }
+            }
+            __syncwarp();
+            if (SPLIT) {
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+        if (lane == 0 && !ok) {  // no teardown under a running MMA
+            tc::commit(&sh->drained);
+            mbar_wait(&sh->drained, 0, a.status);
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 4 + 4 * kConvWGs) {
+        // ------------------------------------------------ B to FP16, into tensor memory
+        const int half = (warp - 4) / 4;
+        const int row = (warp % 4) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        int it = 0;
+        bool ok = true;
+        for (int u = first_unit; u < units; u += unit_step) {
+            for (int i = kb; i < ke; ++i, ++it) {
+                const int s = it % S, t = it % kAStages;
+                ok = ok && wait(&sh->full[s], (it / S) & 1) &&
+                     (it < kAStages || wait(&sh->aempty[t], (it / kAStages - 1) & 1));
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint8_t *src = ring + s * Cf::kStage + row * kI8StageK;
+                uint4 w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    w[c] = *reinterpret_cast<const uint4 *>(src + (((half * 4 + c) ^ (row & 7)) * 16));
+                uint32_t o[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    int8x4_to_f16(w[c].x, o[c * 8 + 0], o[c * 8 + 1]);
+                    int8x4_to_f16(w[c].y, o[c * 8 + 2], o[c * 8 + 3]);
+                    int8x4_to_f16(w[c].z, o[c * 8 + 4], o[c * 8 + 5]);
+                    int8x4_to_f16(w[c].w, o[c * 8 + 6], o[c * 8 + 7]);
+                }
+                tc::tmem_st32(tmem_a + t * kACols + half * 32 + lanes, o);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->empty[s]);
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->afull[t]);
+            }
+            if (SPLIT) {
+                __syncwarp();
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+    } else if (warp >= 4 + 4 * kConvWGs) {
+        // ------------------------------------------------ accumulators to C
+        const int wg = (warp - 4 - 4 * kConvWGs) / 4;
+        const int ch = (warp % 4) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        int chunk = 0;
+        bool ok = true;
+        for (int u = first_unit; u < units; u += unit_step) {
+            const I8Unit q = unit_of(sh, a, NT, ch_tiles, u);
+            int acc[Cf::kCols];
+#pragma unroll
+            for (int j = 0; j < Cf::kCols; ++j) acc[j] = 0;
+            for (int i = kb; i < ke && ok; i += kChunk, ++chunk) {
+                const int d = chunk & 1;
+                ok = __all_sync(0xffffffffu, wait(&sh->dfull[d], (chunk / 2) & 1));
+                if (!ok) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < Cf::kCols / 16; ++c) {
+                    float v[16];
+                    tc::tmem_ld16(tmem + d * NT + wg * Cf::kCols + c * 16 + lanes, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[c * 16 + j] += __float2int_rn(v[j]);
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->dempty[d]);
+            }
+            const int n = q.ch0 + ch;
+            const long long at = static_cast<long long>(q.e) * a.N + n;
+            const float sb = n < a.N ? __ldg(a.scaleB + at) : 0.f;
+            const float bias = n < a.N && a.bias ? __ldg(a.bias + at) : 0.f;
+            if (!SPLIT) {
+                if (ok && n < a.N)
+                    with_out_type(a.out_type, [&](auto zero) {
+                        using T = decltype(zero);
+                        T *C = static_cast<T *>(a.C) + n;
+#pragma unroll
+                        for (int j = 0; j < Cf::kCols; ++j) {
+                            const int t = q.t0 + wg * Cf::kCols + j;
+                            if (t < q.tend)
+                                C[static_cast<long long>(t) * a.ldc] =
+                                    int8_out<T>(int8_value(acc[j], sb, __ldg(a.scaleA + t), bias));
+                        }
+                    });
+            } else {
+                // column j belongs to CTA j / (NT / splits) of the cluster
+                const int per = NT / splits;
+                if (ok) {
+#pragma unroll
+                    for (int j = 0; j < Cf::kCols; ++j) {
+                        const int col = wg * Cf::kCols + j;
+                        const int owner = col / per;
+                        const uint32_t to = dsmem_addr(
+                            xchg + (rank * per + (col - owner * per)) * kI8TileN + ch, static_cast<uint32_t>(owner));
+                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(acc[j]) : "memory");
+                    }
+                }
+                __syncwarp();
+                cluster_sync();
+                if (ok && n < a.N)
+                    with_out_type(a.out_type, [&](auto zero) {
+                        using T = decltype(zero);
+                        T *C = static_cast<T *>(a.C) + n;
+                        for (int c = wg; c < per; c += Cf::kEpiWGs) {
+                            const int t = q.t0 + rank * per + c;
+                            if (t >= q.tend) break;
+                            int sum = 0;
+                            for (int r = 0; r < splits; ++r) sum += xchg[(r * per + c) * kI8TileN + ch];
+                            C[static_cast<long long>(t) * a.ldc] =
+                                int8_out<T>(int8_value(sum, sb, __ldg(a.scaleA + t), bias));
+                        }
+                    });
+                __syncwarp();
+                cluster_sync();
+            }
+        }
+    } else {
+        for (int u = first_unit; SPLIT && u < units; u += unit_step) {
+            cluster_sync();
+            cluster_sync();
+        }
+    }
+    // ---------------------------------------------------- teardown
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, kI8TmemCols);
+    }
+}
+
+template <int NT, bool SPLIT>
+cudaError_t prepare_one() {
+    return cudaFuncSetAttribute(int8_tc_kernel<NT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                I8Cfg<NT, SPLIT>::kSmem);
+}
+
+template <int NT>
+cudaError_t launch_nt(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
+                      int smem_override, cudaStream_t stream) {
+    const int ch_tiles = (a.N + kI8TileN - 1) / kI8TileN;
+    const long long tiles = static_cast<long long>(a.rows) / NT + (a.experts < a.rows ? a.experts : a.rows);
+    const long long units = (a.experts == 1 ? (a.rows + NT - 1) / NT : tiles) * ch_tiles;
+    if (a.ksplit > 1) {
+        using Cf = I8Cfg<NT, true>;
+        const long long most = num_sms / a.ksplit;
+        return launch_dependent(int8_tc_kernel<NT, true>, dim3(a.ksplit * (units < most ? units : most)),
+                                dim3(Cf::kThreads), smem_override > 0 ? smem_override : Cf::kSmem, stream, a.ksplit,
+                                tmB, tmA, a);
+    }
+    using Cf = I8Cfg<NT, false>;
+    return launch_dependent(int8_tc_kernel<NT, false>, dim3(units < num_sms ? units : num_sms), dim3(Cf::kThreads),
+                            smem_override > 0 ? smem_override : Cf::kSmem, stream, 1, tmB, tmA, a);
+}
+
+}  // namespace
+
+cudaError_t int8_prepare() {
+    cudaError_t e = cudaSuccess;
+    for (cudaError_t r : {prepare_one<16, false>(), prepare_one<32, false>(), prepare_one<64, false>(),
+                          prepare_one<128, false>(), prepare_one<16, true>(), prepare_one<32, true>(),
+                          prepare_one<64, true>(), prepare_one<128, true>()})
+        if (e == cudaSuccess) e = r;
+    return e;
+}
+
+cudaError_t launch_int8_tc(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
+                           int smem_override, cudaStream_t stream) {
+    switch (a.nt) {
+        case 16: return launch_nt<16>(a, tmB, tmA, num_sms, smem_override, stream);
+        case 32: return launch_nt<32>(a, tmB, tmA, num_sms, smem_override, stream);
+        case 64: return launch_nt<64>(a, tmB, tmA, num_sms, smem_override, stream);
+        default: return launch_nt<128>(a, tmB, tmA, num_sms, smem_override, stream);
+    }
+}
+
+cudaError_t launch_int8_generic(const Int8Args &a, cudaStream_t stream) {
+    const int y = (a.rows + kGTile - 1) / kGTile;
+    const dim3 grid((a.N + kGTile - 1) / kGTile, y < 65535 ? y : 65535, a.experts);
+    return launch_dependent(int8_generic_kernel, grid, dim3(256), 0, stream, 1, a);
+}
+
+cudaError_t launch_int8_to_f16(const int8_t *A, long long lda, int rows, int K, void *dst, int ldd,
+                               cudaStream_t stream) {
+    const int vec = reinterpret_cast<uintptr_t>(A) % 16 == 0 && lda % 16 == 0;
+    const long long blocks = (static_cast<long long>(rows) * (ldd / 16) + 255) / 256;
+    return launch_dependent(int8_to_f16_kernel, dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20))),
+                            dim3(256), 0, stream, 1, A, lda, rows, K, static_cast<uint4 *>(dst), ldd, vec);
+}
+
+cudaError_t launch_int8_relayout(const int8_t *B, long long ldb, long long strideB, int trans, int experts, int N,
+                                 int K, int8_t *dst, int ldd, cudaStream_t stream) {
+    if (trans) {
+        const long long blocks = (static_cast<long long>(N) * (ldd / 16) + 255) / 256;
+        return launch_dependent(int8_realign_kernel,
+                                dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)), experts),
+                                dim3(256), 0, stream, 1, B, ldb, strideB, N, K, dst, ldd);
+    }
+    const int y = (N + kTN - 1) / kTN;
+    return launch_dependent(int8_transpose_kernel, dim3((ldd + kTK - 1) / kTK, y < 65535 ? y : 65535, experts),
+                            dim3(256), 0, stream, 1, B, ldb, strideB, N, K, dst, ldd);
+}
+
+}  // namespace sg

@@ -1,0 +1,443 @@
+// C ABI of the int8 products and of the expert routing (declared in
+// include/sgemm.h): argument validation, the choice of path, tile and split,
+// the TMA descriptors and the launches.  Every computation is done by the
+// kernels in sgemm_int8.cu and sgemm_experts.cu.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "context.h"
+#include "internal.h"
+#include "sgemm.h"
+
+namespace {
+
+int from_cuda(cudaError_t e) {
+    switch (e) {
+        case cudaSuccess: return SGEMM_OK;
+        case cudaErrorInvalidValue:
+        case cudaErrorInvalidConfiguration:
+        case cudaErrorLaunchOutOfResources:
+        case cudaErrorInvalidDeviceFunction:
+        case cudaErrorNoKernelImageForDevice: return SGEMM_ERR_LAUNCH;
+        default: return SGEMM_ERR_CUDA;
+    }
+}
+
+inline bool aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+inline bool known_type(int t) { return t == SGEMM_IN_F32 || t == SGEMM_IN_BF16 || t == SGEMM_IN_F16; }
+inline int size_of(int t) { return t == SGEMM_IN_F32 ? 4 : 2; }
+
+// Byte range of a buffer that a call reads or writes.
+struct Range {
+    uintptr_t lo = 0, hi = 0;
+    Range() {}
+    Range(const void *p, long long rows, long long cols, long long ld, int size)
+        : lo(reinterpret_cast<uintptr_t>(p)),
+          hi(rows > 0 && cols > 0 ? lo + ((rows - 1) * static_cast<uintptr_t>(ld) + cols) * size : lo) {}
+    bool meets(const Range &o) const { return lo < o.hi && o.lo < hi && lo < hi && o.lo < o.hi; }
+};
+
+// K up to which a sum of K products of two int8 stays inside int32.
+constexpr int kMaxInt8K = 131071;
+
+// The tile's tokens for products of `rows` rows a B matrix: the narrowest tile
+// that holds them, 128 beyond 64.
+int token_tile(long long rows) {
+    for (int nt : sg::kI8TokenTiles)
+        if (rows <= nt) return nt;
+    return 128;
+}
+
+int check_int8(int transB, int out_type, int experts, int rows, int N, int K, const int *offsets, bool grouped,
+               const int8_t *A, int lda, const float *scaleA, const int8_t *B, int ldb, long long strideB,
+               const float *scaleB, const float *bias, const void *C, int ldc) {
+    if (!known_type(out_type) || (transB != 0 && transB != 1)) return SGEMM_ERR_INVALID_VALUE;
+    if (rows < 0 || N < 0 || K < 0 || K > kMaxInt8K) return SGEMM_ERR_INVALID_VALUE;
+    if (experts < 1 || experts > sg::kMaxExperts) return SGEMM_ERR_INVALID_VALUE;
+    const int b_rows = transB ? N : K, b_cols = transB ? K : N;  // B as stored
+    if (lda < std::max(1, K) || ldb < std::max(1, b_cols) || ldc < std::max(1, N) || strideB < 0)
+        return SGEMM_ERR_INVALID_VALUE;
+    if (rows == 0 || N == 0) return SGEMM_OK;
+    if (C == nullptr || scaleA == nullptr || scaleB == nullptr) return SGEMM_ERR_NULL;
+    if (K > 0 && (A == nullptr || B == nullptr)) return SGEMM_ERR_NULL;
+    if (grouped && offsets == nullptr) return SGEMM_ERR_NULL;
+    if (!aligned(C, size_of(out_type)) || !aligned(scaleA, 4) || !aligned(scaleB, 4) || !aligned(bias, 4) ||
+        !aligned(offsets, 4))
+        return SGEMM_ERR_INVALID_VALUE;
+    const Range c(C, rows, N, ldc, size_of(out_type)), a(A, rows, K, lda, 1), sa(scaleA, 1, rows, rows, 4);
+    const Range sb(scaleB, experts, N, N, 4), bi(bias, bias ? experts : 0, N, N, 4);
+    const Range of(offsets, offsets ? 1 : 0, experts + 1, experts + 1, 4);
+    Range b(B, b_rows, b_cols, ldb, 1);
+    if (K > 0) b.hi += static_cast<uintptr_t>(experts - 1) * static_cast<uintptr_t>(strideB);
+    if ((K > 0 && (c.meets(a) || c.meets(b))) || c.meets(sa) || c.meets(sb) || c.meets(bi) || c.meets(of))
+        return SGEMM_ERR_ALIAS;
+    return SGEMM_OK;
+}
+
+// CTAs that share a tile's K range: doubled while a wave has CTAs for it and
+// each keeps at least two stages of 128 k.
+int split_of(long long tiles, int stages, int num_sms) {
+    int s = 1;
+    while (s < 8 && tiles * s * 2 <= num_sms && stages >= s * 4) s *= 2;
+    return s;
+}
+
+int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, int N, int K, const int *offsets,
+             const int8_t *A, int lda, const float *scaleA, const int8_t *B, int ldb, long long strideB,
+             const float *scaleB, const float *bias, void *C, int ldc, cudaStream_t stream) {
+    sg::HandleView v;
+    sg::view_of(h, &v);
+    int launches = 0, copied = 0, variant = SGEMM_VARIANT_GENERIC_I8;
+    sg::Int8Args a{};
+    a.rows = a.total_rows = rows;
+    a.N = N;
+    a.K = K;
+    a.experts = experts;
+    a.offsets = offsets;
+    a.A = A;
+    a.lda = lda;
+    a.B = B;
+    a.ldb = ldb;
+    a.strideB = strideB;
+    a.transB = transB;
+    a.scaleA = scaleA;
+    a.scaleB = scaleB;
+    a.bias = bias;
+    a.C = C;
+    a.ldc = ldc;
+    a.out_type = out_type;
+    a.status = v.d_status;
+    a.ksplit = 1;
+
+    // The re-layout workspace: B where the TMA cannot read it as stored, then
+    // the tokens' rows in FP16, as many at a time as fit.
+    uint8_t *ws = reinterpret_cast<uint8_t *>(v.d_rl);
+    size_t room = v.rl_bytes;
+    const int kp = static_cast<int>(cdiv(K, 64) * 64), kb = static_cast<int>(cdiv(K, 16) * 16);
+    const bool as_stored = transB && aligned(B, 16) && ldb % 16 == 0 && (experts == 1 || strideB % 16 == 0);
+    const size_t b_bytes = as_stored ? 0 : static_cast<size_t>(experts) * N * kb;
+    const size_t b_room = (b_bytes + 1023) / 1024 * 1024;
+    bool tc = v.pinned != SGEMM_VARIANT_GENERIC && v.pinned != SGEMM_VARIANT_GENERIC_I8 && K > 0 && ws != nullptr &&
+              (as_stored || v.relayout_mode != SGEMM_RELAYOUT_OFF) && b_room < room &&
+              room - b_room >= static_cast<size_t>(kp) * 2 * std::min(rows, 128);
+    const long long ch_tiles = cdiv(N, sg::kI8TileN);
+    int per = 0;  // rows of one pass
+    if (tc) {
+        const long long fit = static_cast<long long>((room - b_room) / (static_cast<size_t>(kp) * 2));
+        per = static_cast<int>(std::min<long long>(rows, fit >= 128 ? fit / 128 * 128 : fit));
+        const int owners = std::min(experts, rows);
+        a.nt = token_tile(cdiv(rows, owners));
+        const long long tiles = (experts == 1 ? cdiv(per, a.nt) : per / a.nt + owners) * ch_tiles;
+        tc = tiles < INT_MAX && (static_cast<long long>(per / a.nt) + experts) * ch_tiles < INT_MAX;
+        a.ksplit = split_of(tiles, static_cast<int>(cdiv(K, sg::kI8StageK)), v.num_sms);
+    }
+    CUtensorMap tmB, tmA;
+    if (tc) {
+        if (!as_stored) {
+            const cudaError_t e =
+                sg::launch_int8_relayout(B, ldb, strideB, transB, experts, N, K, reinterpret_cast<int8_t *>(ws), kb, stream);
+            if (e != cudaSuccess) return from_cuda(e);
+            ++launches;
+            copied |= 2;
+            a.B = reinterpret_cast<int8_t *>(ws);
+            a.ldb = kb;
+            a.strideB = static_cast<long long>(N) * kb;
+            a.transB = 1;
+        }
+        ws += b_room;
+        // a single matrix has any (aligned) matrix stride
+        const long long stride = experts > 1 ? a.strideB : a.ldb * static_cast<long long>(N);
+        tc = sg::encode_map(&tmB, sg::MapType::kInt8, 3, a.B, K, N, experts, a.ldb, stride, sg::kI8StageK,
+                            sg::kI8TileN) &&
+             sg::encode_map(&tmA, sg::MapType::kF16, 2, ws, kp, per, 1, static_cast<long long>(kp) * 2, 0, 64, a.nt);
+    }
+    if (tc) {
+        variant = SGEMM_VARIANT_TC_I8;
+        for (int r0 = 0; r0 < rows; r0 += per) {
+            a.row0 = r0;
+            a.rows = std::min(per, rows - r0);
+            cudaError_t e = sg::launch_int8_to_f16(A + static_cast<long long>(r0) * lda, lda, a.rows, K, ws, kp, stream);
+            if (e == cudaSuccess) e = sg::launch_int8_tc(a, tmB, tmA, v.num_sms, v.smem_override, stream);
+            if (e != cudaSuccess) return from_cuda(e);
+            launches += 2;
+        }
+    } else {
+        a.ksplit = 1;
+        const cudaError_t e = sg::launch_int8_generic(a, stream);
+        if (e != cudaSuccess) return from_cuda(e);
+        ++launches;
+    }
+    sg::record_call(h, variant, a.ksplit, launches, copied);
+    return SGEMM_OK;
+}
+
+// The checks every call starts with.
+int enter(sgemm_handle_t h) {
+    if (!sg::is_live(h)) return SGEMM_ERR_BAD_HANDLE;
+    sg::HandleView v;
+    sg::view_of(h, &v);
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != v.device) return SGEMM_ERR_WRONG_DEVICE;
+    return SGEMM_OK;
+}
+
+// Sizes and the slots of a routing call.
+int check_slots(int tokens, int choices) {
+    if (tokens < 0 || choices < 1) return SGEMM_ERR_INVALID_VALUE;
+    if (static_cast<long long>(tokens) * choices > INT_MAX) return SGEMM_ERR_INVALID_VALUE;
+    return SGEMM_OK;
+}
+
+int check_row(int type, int width, int ld) {
+    return known_type(type) && width >= 0 && ld >= std::max(1, width) ? SGEMM_OK : SGEMM_ERR_INVALID_VALUE;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sgemm_check_args_int8(int transB, int out_type, int M, int N, int K, const int8_t *A, int lda,
+                          const float *scaleA, const int8_t *B, int ldb, const float *scaleB, const float *bias,
+                          const void *C, int ldc) {
+    return check_int8(transB, out_type, 1, M, N, K, nullptr, false, A, lda, scaleA, B, ldb, 0, scaleB, bias, C, ldc);
+}
+
+int sgemm_check_args_int8_experts(int transB, int out_type, int experts, int rows, int N, int K, const int *offsets,
+                                  const int8_t *A, int lda, const float *scaleA, const int8_t *B, int ldb,
+                                  long long strideB, const float *scaleB, const float *bias, const void *C, int ldc) {
+    return check_int8(transB, out_type, experts, rows, N, K, offsets, true, A, lda, scaleA, B, ldb, strideB, scaleB,
+                      bias, C, ldc);
+}
+
+int sgemm_run_int8(sgemm_handle_t h, int transB, int out_type, int M, int N, int K, const int8_t *A, int lda,
+                   const float *scaleA, const int8_t *B, int ldb, const float *scaleB, const float *bias, void *C,
+                   int ldc, void *stream) {
+    int st = enter(h);
+    if (st == SGEMM_OK)
+        st = check_int8(transB, out_type, 1, M, N, K, nullptr, false, A, lda, scaleA, B, ldb, 0, scaleB, bias, C, ldc);
+    if (st != SGEMM_OK) return st;
+    if (M == 0 || N == 0) {
+        sg::record_call(h, -1, 1, 0, 0);
+        return SGEMM_OK;
+    }
+    return run_int8(h, transB, out_type, 1, M, N, K, nullptr, A, lda, scaleA, B, ldb, 0, scaleB, bias, C, ldc,
+                    static_cast<cudaStream_t>(stream));
+}
+
+int sgemm_run_int8_experts(sgemm_handle_t h, int transB, int out_type, int experts, int rows, int N, int K,
+                           const int *offsets, const int8_t *A, int lda, const float *scaleA, const int8_t *B,
+                           int ldb, long long strideB, const float *scaleB, const float *bias, void *C, int ldc,
+                           void *stream) {
+    int st = enter(h);
+    if (st == SGEMM_OK)
+        st = check_int8(transB, out_type, experts, rows, N, K, offsets, true, A, lda, scaleA, B, ldb, strideB,
+                        scaleB, bias, C, ldc);
+    if (st != SGEMM_OK) return st;
+    if (rows == 0 || N == 0) {
+        sg::record_call(h, -1, 1, 0, 0);
+        return SGEMM_OK;
+    }
+    return run_int8(h, transB, out_type, experts, rows, N, K, offsets, A, lda, scaleA, B, ldb, strideB, scaleB, bias,
+                    C, ldc, static_cast<cudaStream_t>(stream));
+}
+
+int sgemm_quantize_rows(sgemm_handle_t h, int type, int M, int K, const void *X, int ldx, int8_t *Q, int ldq,
+                        float *scale, void *stream) {
+    int st = enter(h);
+    if (st != SGEMM_OK) return st;
+    if (M < 0 || check_row(type, K, ldx) != SGEMM_OK || ldq < std::max(1, K)) return SGEMM_ERR_INVALID_VALUE;
+    sg::HandleView v;
+    sg::view_of(h, &v);
+    sg::record_call(h, -1, 1, 0, 0);
+    if (M == 0) return SGEMM_OK;
+    if (scale == nullptr || (K > 0 && (X == nullptr || Q == nullptr))) return SGEMM_ERR_NULL;
+    if (!aligned(X, size_of(type)) || !aligned(scale, 4)) return SGEMM_ERR_INVALID_VALUE;
+    const Range x(X, M, K, ldx, size_of(type)), q(Q, M, K, ldq, 1), s(scale, 1, M, M, 4);
+    if (x.meets(q) || x.meets(s) || q.meets(s)) return SGEMM_ERR_ALIAS;
+    sg::MoveArgs a{};
+    a.X = X;
+    a.ldx = ldx;
+    a.tokens = M;
+    a.choices = 1;
+    a.width = K;
+    a.Y = Q;
+    a.ldy = ldq;
+    a.scale = scale;
+    const int rc = from_cuda(sg::launch_quantize(type, a, v.num_sms, static_cast<cudaStream_t>(stream)));
+    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 1, 0);
+    return rc;
+}
+
+int sgemm_expert_sort(sgemm_handle_t h, int tokens, int choices, int experts, const int *ids, int *offsets,
+                      int *rows, int *source, void *stream) {
+    int st = enter(h);
+    if (st == SGEMM_OK) st = check_slots(tokens, choices);
+    if (st != SGEMM_OK) return st;
+    if (experts < 1 || experts > sg::kMaxExperts) return SGEMM_ERR_INVALID_VALUE;
+    const int slots = tokens * choices;
+    if (offsets == nullptr || (slots > 0 && (ids == nullptr || rows == nullptr || source == nullptr)))
+        return SGEMM_ERR_NULL;
+    if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(source, 4))
+        return SGEMM_ERR_INVALID_VALUE;
+    const Range i(ids, 1, slots, slots, 4), o(offsets, 1, experts + 1, experts + 1, 4), r(rows, 1, slots, slots, 4),
+        s(source, 1, slots, slots, 4);
+    if (i.meets(o) || i.meets(r) || i.meets(s) || o.meets(r) || o.meets(s) || r.meets(s)) return SGEMM_ERR_ALIAS;
+    sg::HandleView v;
+    sg::view_of(h, &v);
+    int launches = 0;
+    const int rc = from_cuda(sg::launch_sort(ids, slots, experts, offsets, rows, source, reinterpret_cast<int *>(v.d_ws),
+                                             v.ws_floats, &launches, static_cast<cudaStream_t>(stream)));
+    sg::record_call(h, -1, 1, rc == SGEMM_OK ? launches : 0, 0);
+    return rc;
+}
+
+int sgemm_expert_dispatch(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *X, int ldx,
+                          const int *rows, void *Y, int ldy, void *stream) {
+    int st = enter(h);
+    if (st == SGEMM_OK) st = check_slots(tokens, choices);
+    if (st == SGEMM_OK) st = check_row(type, width, ldx);
+    if (st == SGEMM_OK) st = check_row(type, width, ldy);
+    if (st != SGEMM_OK) return st;
+    sg::record_call(h, -1, 1, 0, 0);
+    if (tokens == 0 || width == 0) return SGEMM_OK;
+    if (X == nullptr || Y == nullptr || rows == nullptr) return SGEMM_ERR_NULL;
+    const int size = size_of(type);
+    if (!aligned(X, size) || !aligned(Y, size) || !aligned(rows, 4)) return SGEMM_ERR_INVALID_VALUE;
+    const int slots = tokens * choices;
+    const Range x(X, tokens, width, ldx, size), y(Y, slots, width, ldy, size), r(rows, 1, slots, slots, 4);
+    if (y.meets(x) || y.meets(r)) return SGEMM_ERR_ALIAS;
+    sg::MoveArgs a{};
+    a.X = X;
+    a.ldx = ldx;
+    a.tokens = tokens;
+    a.choices = choices;
+    a.width = width;
+    a.rows = rows;
+    a.Y = Y;
+    a.ldy = ldy;
+    const int rc = from_cuda(sg::launch_dispatch(type, a, static_cast<cudaStream_t>(stream)));
+    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 1, 0);
+    return rc;
+}
+
+int sgemm_expert_dispatch_int8(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *X, int ldx,
+                               const int *rows, int8_t *Q, int ldq, float *scale, void *stream) {
+    int st = enter(h);
+    if (st == SGEMM_OK) st = check_slots(tokens, choices);
+    if (st == SGEMM_OK) st = check_row(type, width, ldx);
+    if (st != SGEMM_OK) return st;
+    if (ldq < std::max(1, width)) return SGEMM_ERR_INVALID_VALUE;
+    sg::record_call(h, -1, 1, 0, 0);
+    if (tokens == 0) return SGEMM_OK;
+    if (rows == nullptr || scale == nullptr || (width > 0 && (X == nullptr || Q == nullptr))) return SGEMM_ERR_NULL;
+    const int size = size_of(type), slots = tokens * choices;
+    if (!aligned(X, size) || !aligned(scale, 4) || !aligned(rows, 4)) return SGEMM_ERR_INVALID_VALUE;
+    const Range x(X, tokens, width, ldx, size), q(Q, slots, width, ldq, 1), r(rows, 1, slots, slots, 4),
+        s(scale, 1, slots, slots, 4);
+    if (q.meets(x) || q.meets(r) || q.meets(s) || s.meets(x) || s.meets(r)) return SGEMM_ERR_ALIAS;
+    sg::HandleView v;
+    sg::view_of(h, &v);
+    sg::MoveArgs a{};
+    a.X = X;
+    a.ldx = ldx;
+    a.tokens = tokens;
+    a.choices = choices;
+    a.width = width;
+    a.rows = rows;
+    a.Y = Q;
+    a.ldy = ldq;
+    a.scale = scale;
+    const int rc = from_cuda(sg::launch_quantize(type, a, v.num_sms, static_cast<cudaStream_t>(stream)));
+    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 1, 0);
+    return rc;
+}
+
+// out[t] = sum_j w[t][j] * Y[rows[t][j]] (weights NULL only from dispatch_grad).
+static int run_gather(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *Y, int ldy,
+                      const int *rows, bool weighted, const float *weights, void *out, int ldo, void *stream) {
+    int st = enter(h);
+    if (st == SGEMM_OK) st = check_slots(tokens, choices);
+    if (st == SGEMM_OK) st = check_row(type, width, ldy);
+    if (st == SGEMM_OK) st = check_row(type, width, ldo);
+    if (st != SGEMM_OK) return st;
+    sg::record_call(h, -1, 1, 0, 0);
+    if (tokens == 0 || width == 0) return SGEMM_OK;
+    if (Y == nullptr || rows == nullptr || out == nullptr || (weighted && weights == nullptr)) return SGEMM_ERR_NULL;
+    const int size = size_of(type), slots = tokens * choices;
+    if (!aligned(Y, size) || !aligned(out, size) || !aligned(rows, 4) || !aligned(weights, 4))
+        return SGEMM_ERR_INVALID_VALUE;
+    const Range y(Y, slots, width, ldy, size), o(out, tokens, width, ldo, size), r(rows, 1, slots, slots, 4),
+        w(weights, weights ? 1 : 0, slots, slots, 4);
+    if (o.meets(y) || o.meets(r) || o.meets(w)) return SGEMM_ERR_ALIAS;
+    sg::MoveArgs a{};
+    a.X = out;
+    a.ldx = ldo;
+    a.tokens = tokens;
+    a.choices = choices;
+    a.width = width;
+    a.rows = rows;
+    a.weights = weights;
+    a.Y = const_cast<void *>(Y);
+    a.ldy = ldy;
+    const int rc = from_cuda(sg::launch_gather(type, a, static_cast<cudaStream_t>(stream)));
+    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 1, 0);
+    return rc;
+}
+
+int sgemm_expert_dispatch_grad(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *dY,
+                               int lddy, const int *rows, void *dX, int lddx, void *stream) {
+    return run_gather(h, type, tokens, choices, width, dY, lddy, rows, false, nullptr, dX, lddx, stream);
+}
+
+int sgemm_expert_combine(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *Y, int ldy,
+                         const int *rows, const float *weights, void *out, int ldo, void *stream) {
+    return run_gather(h, type, tokens, choices, width, Y, ldy, rows, true, weights, out, ldo, stream);
+}
+
+int sgemm_expert_combine_grad(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *dout,
+                              int lddo, const void *Y, int ldy, const int *rows, const float *weights, void *dY,
+                              int lddy, float *dweights, void *stream) {
+    int st = enter(h);
+    if (st == SGEMM_OK) st = check_slots(tokens, choices);
+    if (st == SGEMM_OK) st = check_row(type, width, lddo);
+    if (st == SGEMM_OK) st = check_row(type, width, ldy);
+    if (st == SGEMM_OK) st = check_row(type, width, lddy);
+    if (st != SGEMM_OK) return st;
+    sg::record_call(h, -1, 1, 0, 0);
+    if (tokens == 0) return SGEMM_OK;
+    if (rows == nullptr || weights == nullptr || dweights == nullptr ||
+        (width > 0 && (dout == nullptr || Y == nullptr || dY == nullptr)))
+        return SGEMM_ERR_NULL;
+    const int size = size_of(type), slots = tokens * choices;
+    if (!aligned(dout, size) || !aligned(Y, size) || !aligned(dY, size) || !aligned(rows, 4) ||
+        !aligned(weights, 4) || !aligned(dweights, 4))
+        return SGEMM_ERR_INVALID_VALUE;
+    const Range g(dout, tokens, width, lddo, size), y(Y, slots, width, ldy, size), d(dY, slots, width, lddy, size),
+        r(rows, 1, slots, slots, 4), w(weights, 1, slots, slots, 4), dw(dweights, 1, slots, slots, 4);
+    if (d.meets(g) || d.meets(y) || d.meets(r) || d.meets(w) || d.meets(dw) || dw.meets(g) || dw.meets(y) ||
+        dw.meets(r) || dw.meets(w))
+        return SGEMM_ERR_ALIAS;
+    sg::MoveArgs a{};
+    a.X = dout;
+    a.ldx = lddo;
+    a.tokens = tokens;
+    a.choices = choices;
+    a.width = width;
+    a.rows = rows;
+    a.weights = weights;
+    a.Y = const_cast<void *>(Y);
+    a.ldy = ldy;
+    a.dY = dY;
+    a.lddy = lddy;
+    a.scale = dweights;
+    const int rc = from_cuda(sg::launch_combine_grad(type, a, static_cast<cudaStream_t>(stream)));
+    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 1, 0);
+    return rc;
+}
+
+}  // extern "C"

@@ -39,9 +39,12 @@ VARIANT_TC_3XTF32_PAIR = 8
 VARIANT_TC_F16_PAIR = 9
 VARIANT_GENERIC_F16 = 10
 VARIANT_TMA_256x128 = 11
-VARIANT_COUNT = 12
+VARIANT_TC_I8 = 12
+VARIANT_GENERIC_I8 = 13
+VARIANT_COUNT = 14
 MATH_FP32 = 0
 MATH_3XTF32 = 1
+IN_F32 = 0
 IN_BF16 = 1
 IN_F16 = 2
 RELAYOUT_AUTO = 0
@@ -62,7 +65,10 @@ EXPORTS = ("sgemm_create", "sgemm_run", "sgemm_check_args", "sgemm_destroy", "sg
            "sgemm_set_relayout", "sgemm_last_relayout", "sgemm_relayout_capacity", "sgemm_debug_plan",
            "sgemm_debug_set_stream_k_sums", "sgemm_debug_set_cluster_split", "sgemm_debug_set_stream_k_ctas",
            "sgemm_debug_set_stream_k_gap", "sgemm_debug_leave_aborted_state", "sgemm_debug_tf32_probe",
-           "sgemm_debug_set_workspace_limit")
+           "sgemm_debug_set_workspace_limit", "sgemm_run_int8", "sgemm_check_args_int8",
+           "sgemm_run_int8_experts", "sgemm_check_args_int8_experts", "sgemm_quantize_rows", "sgemm_expert_sort",
+           "sgemm_expert_dispatch", "sgemm_expert_dispatch_int8", "sgemm_expert_dispatch_grad",
+           "sgemm_expert_combine", "sgemm_expert_combine_grad")
 
 
 class SgemmError(RuntimeError):
@@ -132,6 +138,19 @@ def lib() -> ctypes.CDLL:
                                           i64, i32]
         L.sgemm_run_host.argtypes = [vp, i32, i32, i32, f32, vp, i32, vp, i32, f32, vp, i32, vp, vp, vp, vp]
         L.sgemm_run_noalloc.argtypes = [i32, i32, i32, f32, vp, i32, vp, i32, f32, vp, i32, vp]
+        int8_args = [i32, i32, i32, i32, i32, vp, i32, vp, vp, i32, vp, vp, vp, i32]
+        L.sgemm_run_int8.argtypes = [vp, *int8_args, vp]
+        L.sgemm_check_args_int8.argtypes = int8_args
+        experts_args = [i32, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, i32, i64, vp, vp, vp, i32]
+        L.sgemm_run_int8_experts.argtypes = [vp, *experts_args, vp]
+        L.sgemm_check_args_int8_experts.argtypes = experts_args
+        L.sgemm_quantize_rows.argtypes = [vp, i32, i32, i32, vp, i32, vp, i32, vp, vp]
+        L.sgemm_expert_sort.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp]
+        L.sgemm_expert_dispatch.argtypes = [vp, i32, i32, i32, i32, vp, i32, vp, vp, i32, vp]
+        L.sgemm_expert_dispatch_int8.argtypes = [vp, i32, i32, i32, i32, vp, i32, vp, vp, i32, vp, vp]
+        L.sgemm_expert_dispatch_grad.argtypes = [vp, i32, i32, i32, i32, vp, i32, vp, vp, i32, vp]
+        L.sgemm_expert_combine.argtypes = [vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, i32, vp]
+        L.sgemm_expert_combine_grad.argtypes = [vp, i32, i32, i32, i32, vp, i32, vp, i32, vp, vp, vp, i32, vp, vp]
         _lib = L
     return _lib
 
@@ -293,6 +312,80 @@ def sgemm_check_args_mixed(in_type, transA, transB, M, N, K, alpha, A, lda, B, l
     return lib().sgemm_check_args_mixed(int(in_type), int(transA), int(transB), int(M), int(N), int(K),
                                         float(alpha), _ptr(A), int(lda), _ptr(B), int(ldb), float(beta), _ptr(C),
                                         int(ldc))
+
+
+def _enqueue(name: str, h, args, stream) -> None:
+    """Call an enqueue function of the library through the marshalling module
+    (every argument an int or a buffer), or through ctypes without it."""
+    calls = _calls if _calls is not None else calls_module()
+    if calls is not None:
+        rc = calls.enqueue(name, h, args, stream)
+    else:
+        rc = getattr(lib(), name)(h, *[a if isinstance(a, int) else _ptr(a) for a in args], _stream(stream))
+    if rc != OK:
+        raise SgemmError(rc, name)
+
+
+def sgemm_run_int8(h, transB, out_type, M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, C, ldc, stream=None) -> None:
+    """C = scaleA * scaleB * (A @ op(B)) + bias with int8 A and B (see include/sgemm.h)."""
+    _enqueue("sgemm_run_int8", h, (transB, out_type, M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, C, ldc), stream)
+
+
+def sgemm_check_args_int8(transB, out_type, M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, C, ldc) -> int:
+    return lib().sgemm_check_args_int8(int(transB), int(out_type), int(M), int(N), int(K), _ptr(A), int(lda),
+                                       _ptr(scaleA), _ptr(B), int(ldb), _ptr(scaleB), _ptr(bias), _ptr(C), int(ldc))
+
+
+def sgemm_run_int8_experts(h, transB, out_type, experts, rows, N, K, offsets, A, lda, scaleA, B, ldb, strideB,
+                           scaleB, bias, C, ldc, stream=None) -> None:
+    """The int8 product over rows sorted by expert, each expert with its own B
+    (offsets: experts + 1 ints on the device; see include/sgemm.h)."""
+    _enqueue("sgemm_run_int8_experts", h, (transB, out_type, experts, rows, N, K, offsets, A, lda, scaleA, B, ldb,
+                                           strideB, scaleB, bias, C, ldc), stream)
+
+
+def sgemm_check_args_int8_experts(transB, out_type, experts, rows, N, K, offsets, A, lda, scaleA, B, ldb, strideB,
+                                  scaleB, bias, C, ldc) -> int:
+    return lib().sgemm_check_args_int8_experts(
+        int(transB), int(out_type), int(experts), int(rows), int(N), int(K), _ptr(offsets), _ptr(A), int(lda),
+        _ptr(scaleA), _ptr(B), int(ldb), int(strideB), _ptr(scaleB), _ptr(bias), _ptr(C), int(ldc))
+
+
+def sgemm_quantize_rows(h, in_type, M, K, X, ldx, Q, ldq, scale, stream=None) -> None:
+    """Q (int8), scale (FP32) = the rows of X, each divided by its scale and rounded."""
+    _enqueue("sgemm_quantize_rows", h, (in_type, M, K, X, ldx, Q, ldq, scale), stream)
+
+
+def sgemm_expert_sort(h, tokens, choices, experts, ids, offsets, rows, source, stream=None) -> None:
+    """The (token, choice) slots in a stable order by expert."""
+    _enqueue("sgemm_expert_sort", h, (tokens, choices, experts, ids, offsets, rows, source), stream)
+
+
+def sgemm_expert_dispatch(h, in_type, tokens, choices, width, X, ldx, rows, Y, ldy, stream=None) -> None:
+    """Y[rows[t, j]] = X[t]."""
+    _enqueue("sgemm_expert_dispatch", h, (in_type, tokens, choices, width, X, ldx, rows, Y, ldy), stream)
+
+
+def sgemm_expert_dispatch_int8(h, in_type, tokens, choices, width, X, ldx, rows, Q, ldq, scale, stream=None) -> None:
+    """Q[rows[t, j]], scale[rows[t, j]] = row t of X, quantized."""
+    _enqueue("sgemm_expert_dispatch_int8", h, (in_type, tokens, choices, width, X, ldx, rows, Q, ldq, scale), stream)
+
+
+def sgemm_expert_dispatch_grad(h, in_type, tokens, choices, width, dY, lddy, rows, dX, lddx, stream=None) -> None:
+    """dX[t] = sum_j dY[rows[t, j]]."""
+    _enqueue("sgemm_expert_dispatch_grad", h, (in_type, tokens, choices, width, dY, lddy, rows, dX, lddx), stream)
+
+
+def sgemm_expert_combine(h, in_type, tokens, choices, width, Y, ldy, rows, weights, out, ldo, stream=None) -> None:
+    """out[t] = sum_j weights[t, j] * Y[rows[t, j]]."""
+    _enqueue("sgemm_expert_combine", h, (in_type, tokens, choices, width, Y, ldy, rows, weights, out, ldo), stream)
+
+
+def sgemm_expert_combine_grad(h, in_type, tokens, choices, width, dout, lddo, Y, ldy, rows, weights, dY, lddy,
+                              dweights, stream=None) -> None:
+    """dY[rows[t, j]] = weights[t, j] * dout[t]; dweights[t, j] = <dout[t], Y[rows[t, j]]>."""
+    _enqueue("sgemm_expert_combine_grad", h, (in_type, tokens, choices, width, dout, lddo, Y, ldy, rows, weights,
+                                              dY, lddy, dweights), stream)
 
 
 def sgemm_debug_fma_probe(h, sink, ctas=0, iters=4096, stream=None) -> int:

@@ -106,7 +106,10 @@ typedef enum {
                                         inputs (any alignment)                                */
     SGEMM_VARIANT_TMA_256x128 = 11,  /* TMA-fed SIMT, 256 x 128 CTA tile, 16 warps, 8 x 8 per
                                         thread (fastest on large problems)                    */
-    SGEMM_VARIANT_COUNT_ = 12
+    SGEMM_VARIANT_TC_I8 = 12,        /* sgemm_run_int8, sgemm_run_int8_experts only: int8 operands
+                                        as exact FP16 on the tensor cores, int32 sums         */
+    SGEMM_VARIANT_GENERIC_I8 = 13,   /* the same calls: any layout and alignment, CUDA cores  */
+    SGEMM_VARIANT_COUNT_ = 14
     /* sgemm_run_ex: the TMA variants serve every (transA, transB) and any
      * batch up to 65535 when A and B are 16-byte aligned and lda, ldb (and,
      * for batch > 1, strideA, strideB) are multiples of 4, and operands that
@@ -168,8 +171,11 @@ typedef enum {
     SGEMM_RELAYOUT_ALWAYS = 2
 } sgemm_relayout_t;
 
-/* Element type of A and B for sgemm_run_mixed (C is always FP32). */
+/* Element type of A and B for sgemm_run_mixed (BF16 and FP16; C is always
+ * FP32), of the rows that the quantization and expert calls read and write,
+ * and of the int8 products' C (any of the three). */
 typedef enum {
+    SGEMM_IN_F32 = 0,   /* FP32 (not for sgemm_run_mixed) */
     SGEMM_IN_BF16 = 1,  /* bfloat16: 1 sign, 8 exponent, 7 fraction bits */
     SGEMM_IN_F16 = 2    /* IEEE binary16 */
 } sgemm_input_t;
@@ -238,6 +244,130 @@ int sgemm_run_mixed(sgemm_handle_t h, int in_type, int transA, int transB, int M
 int sgemm_check_args_mixed(int in_type, int transA, int transB, int M, int N, int K, float alpha, const void *A,
                            int lda, const void *B, int ldb, float beta, const float *C, int ldc);
 
+/* ---- 8-bit integer products ------------------------------------------------
+ *
+ *     C[i][j] = scaleA[i] * scaleB[j] * sum_p A[i][p] * op(B)[p][j] + bias[j]
+ *
+ * with int8 A (M x K, M tokens) and B, one FP32 scale a row of A (a token) and
+ * one a column of op(B) (a channel), an optional FP32 bias a channel (NULL:
+ * none), and C of type `out_type` (an sgemm_input_t).  B is stored N x K
+ * (transB = 1, a linear layer's weights; fastest) or K x N (transB = 0), all
+ * row-major, leading dimensions in elements.  The sum is exact (32-bit
+ * integers; K <= 131071, the longest that cannot overflow, else
+ * SGEMM_ERR_INVALID_VALUE) and float(sum) * scaleB * scaleA + bias is rounded
+ * to C's type once, so results do not depend on the variant or on how the work
+ * was split.  All 256 values of an int8 are taken as they are.  C is output
+ * only.  K == 0 gives C = bias.  FP16 results beyond 65504 become infinite.
+ *
+ * A may have any alignment and leading dimension.  B is read in place when
+ * transB = 1, B is 16-byte aligned and ldb is a multiple of 16 (in the expert
+ * form strideB too); otherwise it is first copied into the re-layout workspace
+ * (sgemm_last_relayout then reports bit 1; one more launch).  The rows of A are
+ * expanded to FP16 in the same workspace, in several passes where they do not
+ * fit.  Without the workspace, with SGEMM_RELAYOUT_OFF where B would be copied,
+ * where the copy does not fit, or with SGEMM_VARIANT_GENERIC or _GENERIC_I8
+ * pinned, the generic kernel runs.  Otherwise as sgemm_run: no allocation, no
+ * synchronization, device pointers, one handle per concurrently running stream.
+ *
+ * Checks, in order: handle, device, then (sgemm_check_args_int8)
+ * SGEMM_ERR_INVALID_VALUE for an unknown out_type or transB, a negative size, K
+ * above 131071, lda < max(1, K), ldb or ldc below its minimum; nothing is done
+ * when M == 0 or N == 0; SGEMM_ERR_NULL if C, scaleA or scaleB (or A or B while
+ * K > 0) is NULL; SGEMM_ERR_INVALID_VALUE if C, a scale array or the bias is
+ * not aligned to its element size; SGEMM_ERR_ALIAS if C overlaps an input. */
+int sgemm_run_int8(sgemm_handle_t h, int transB, int out_type, int M, int N, int K, const int8_t *A, int lda,
+                   const float *scaleA, const int8_t *B, int ldb, const float *scaleB, const float *bias, void *C,
+                   int ldc, void *stream);
+
+/* Host-only validation of sgemm_run_int8's arguments (same rules, no CUDA call). */
+int sgemm_check_args_int8(int transB, int out_type, int M, int N, int K, const int8_t *A, int lda,
+                          const float *scaleA, const int8_t *B, int ldb, const float *scaleB, const float *bias,
+                          const void *C, int ldc);
+
+/* The same product over rows sorted by expert: rows offsets[e] .. offsets[e+1]-1
+ * of A and C use B_e = B + e*strideB, scaleB + e*N and bias + e*N (e = 0 ..
+ * experts-1; scaleB and bias hold experts*N values).  `offsets` (experts + 1
+ * ints) is in DEVICE memory, as sgemm_expert_sort writes it: the call needs no
+ * host copy of it.  Rows before offsets[0] or from offsets[experts] on belong
+ * to no expert: their A is not used and their C is not written.  Offsets
+ * outside [0, rows] or out of order are taken as the nearest bounds that are
+ * in order, so no access leaves the buffers.  experts is 1 .. 1024; strideB
+ * (elements) >= 0, 0 giving every expert the same B.  Checks as above, plus
+ * SGEMM_ERR_NULL for NULL offsets. */
+int sgemm_run_int8_experts(sgemm_handle_t h, int transB, int out_type, int experts, int rows, int N, int K,
+                           const int *offsets, const int8_t *A, int lda, const float *scaleA, const int8_t *B,
+                           int ldb, long long strideB, const float *scaleB, const float *bias, void *C, int ldc,
+                           void *stream);
+
+/* Host-only validation of sgemm_run_int8_experts's arguments. */
+int sgemm_check_args_int8_experts(int transB, int out_type, int experts, int rows, int N, int K, const int *offsets,
+                                  const int8_t *A, int lda, const float *scaleA, const int8_t *B, int ldb,
+                                  long long strideB, const float *scaleB, const float *bias, const void *C, int ldc);
+
+/* Rows to 8-bit integers: for each row i of X (M x K, of `type`), with m the
+ * largest |X[i][p]|,
+ *     scale[i] = m / 127,    Q[i][p] = rint(X[i][p] * (127 / m))
+ * (each operation correctly rounded in FP32, ties to even), so that
+ * Q[i][p] * scale[i] is X[i][p] to within scale[i] / 2 and a rounding.  A row
+ * with m < 127 * 2^-126 (all zeros among them) gives Q = 0, scale = 0; a row
+ * with an infinity or a NaN gives Q = 0, scale = NaN, so that every product
+ * with it is NaN.  K == 0 gives scales of 0.  Checks: handle, device,
+ * SGEMM_ERR_INVALID_VALUE (unknown type, negative size, leading dimension
+ * below max(1, K)), M == 0 does nothing, SGEMM_ERR_NULL,
+ * SGEMM_ERR_INVALID_VALUE (a pointer not aligned to its element size),
+ * SGEMM_ERR_ALIAS (any two of the three overlap). */
+int sgemm_quantize_rows(sgemm_handle_t h, int type, int M, int K, const void *X, int ldx, int8_t *Q, int ldq,
+                        float *scale, void *stream);
+
+/* ---- tokens to their experts and back ----------------------------------------
+ *
+ * A router gives each of `tokens` tokens `choices` experts: ids[t*choices + j].
+ * Slot s = t*choices + j is choice j of token t; a slot whose id is outside
+ * [0, experts) is dropped (a capacity limit's way to say so).
+ *
+ * sgemm_expert_sort orders the slots by expert, slots of one expert in
+ * ascending order: offsets[e] is the first row of expert e and
+ * offsets[experts] the number of slots kept; rows[s] the row of slot s, -1 for
+ * a dropped one; source[r] the slot of row r, -1 for the rows from
+ * offsets[experts] on.  (experts + 1, tokens*choices and tokens*choices ints.)
+ * The order is the same on every call.  experts is 1 .. 1024 and
+ * tokens*choices < 2^31.
+ *
+ * The other calls move rows of `width` elements of `type`; the tokens' side has
+ * `tokens` rows, the experts' side tokens*choices rows, of which those that no
+ * slot has are neither read nor written.  A value of rows[] outside
+ * [0, tokens*choices) is a dropped slot; a row that two slots name is the
+ * caller's mistake (which one is written is not defined).  With r = rows[t*choices + j]:
+ *   sgemm_expert_dispatch       Y[r] = X[t]
+ *   sgemm_expert_dispatch_int8  Q[r], scale[r] = row t of X as by sgemm_quantize_rows
+ *   sgemm_expert_dispatch_grad  dX[t] = sum over j of dY[r]           (dispatch's gradient)
+ *   sgemm_expert_combine        out[t] = sum over j of weights[t*choices + j] * Y[r]
+ *   sgemm_expert_combine_grad   dY[r] = weights[t*choices + j] * dout[t],
+ *                               dweights[t*choices + j] = sum over p of dout[t][p] * Y[r][p]
+ * Sums run over the slots that are kept, in FP32 and in a fixed order (a token
+ * with none gets zeros, a dropped slot's dweights is 0), and are rounded to
+ * `type` once; weights and dweights are FP32.
+ *
+ * Checks, in order: handle, device, SGEMM_ERR_INVALID_VALUE (a negative size,
+ * choices < 1, too many slots or experts, an unknown type, a leading dimension
+ * below max(1, width)), nothing is done when there is nothing to write,
+ * SGEMM_ERR_NULL, SGEMM_ERR_INVALID_VALUE (a pointer not aligned to its element
+ * size), SGEMM_ERR_ALIAS (an output overlaps an input or another output).  All
+ * enqueue on `stream`, allocate nothing and do not synchronize. */
+int sgemm_expert_sort(sgemm_handle_t h, int tokens, int choices, int experts, const int *ids, int *offsets,
+                      int *rows, int *source, void *stream);
+int sgemm_expert_dispatch(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *X, int ldx,
+                          const int *rows, void *Y, int ldy, void *stream);
+int sgemm_expert_dispatch_int8(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *X, int ldx,
+                               const int *rows, int8_t *Q, int ldq, float *scale, void *stream);
+int sgemm_expert_dispatch_grad(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *dY,
+                               int lddy, const int *rows, void *dX, int lddx, void *stream);
+int sgemm_expert_combine(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *Y, int ldy,
+                         const int *rows, const float *weights, void *out, int ldo, void *stream);
+int sgemm_expert_combine_grad(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *dout,
+                              int lddo, const void *Y, int ldy, const int *rows, const float *weights, void *dY,
+                              int lddy, float *dweights, void *stream);
+
 /* C <- alpha*A*B + beta*C with A, B, C in HOST memory, transfers overlapped
  * with compute.  dA, dB, dC are caller-owned DEVICE buffers of the same
  * shapes and leading dimensions (M*lda, K*ldb, M*ldc floats at least).  On a
@@ -283,8 +413,8 @@ int sgemm_destroy(sgemm_handle_t h);
  * let the library choose).  SGEMM_ERR_INVALID_VALUE for an unknown value or
  * SGEMM_VARIANT_SCALE, which is chosen only by the alpha == 0 / K == 0 rule.
  * A pinned TMA variant fixes the tile; the re-layout mode still decides
- * whether operands are transposed first.  The 16-bit-input variants act as
- * SGEMM_VARIANT_AUTO for FP32 calls. */
+ * whether operands are transposed first.  The 16-bit-input and int8 variants
+ * act as SGEMM_VARIANT_AUTO for FP32 calls. */
 int sgemm_set_variant(sgemm_handle_t h, int variant);
 
 /* Set the handle's math mode (an sgemm_math_mode_t) for SGEMM_VARIANT_AUTO.
@@ -314,8 +444,8 @@ int64_t sgemm_relayout_capacity(sgemm_handle_t h);
  * a stream-K tile (rounded up; 1 when no tile was split). */
 int sgemm_last_variant(sgemm_handle_t h, int *splits);
 
-/* Number of kernel launches the handle's last successful sgemm_run /
- * sgemm_run_ex enqueued: 0 (nothing to do), one per transposed operand
+/* Number of kernel launches the handle's last successful call enqueued.
+ * sgemm_run / sgemm_run_ex: 0 (nothing to do), one per transposed operand
  * (sgemm_last_relayout), then 1 to 3 for the GEMM: complete waves of whole
  * tiles; the stream-K CTAs of the last wave; and, for tiles larger than
  * 64 x 64, the kernel that adds the stream-K parts.  All on the same stream.
