@@ -274,8 +274,9 @@ cudaError_t launch_int8_relayout(const int8_t *B, long long ldb, long long strid
 constexpr int kI8TileN = 128, kI8StageK = 128;  // channels and k of one B stage (TMA box, 128-byte swizzle)
 constexpr int kI8TokenTiles[] = {16, 32, 64, 128};
 cudaError_t int8_prepare();
-// tmB: int8, 3-D (k, channel, expert), box 128 x 128 x 1; tmA: FP16, 2-D (k, row),
-// box 64 x nt; both with the 128-byte swizzle.
+// tmB: int8, 3-D (k, channel, expert), box 128 x 128 x 1; tmA: 2-D (k, row - row0),
+// for nt <= 64 int8, box 128 x nt, else FP16, box 64 x nt; both with the 128-byte
+// swizzle.
 cudaError_t launch_int8_tc(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
                            int smem_override, cudaStream_t stream);
 

@@ -269,39 +269,54 @@ int8_transpose_kernel(const int8_t *__restrict__ B, long long ldb, long long str
 constexpr int kBBytes = kI8TileN * kI8StageK;  // 16 KiB of B a stage
 constexpr int kAStages = 4, kACols = kI8StageK / 2;  // stages of B in tensor memory, 32-bit columns each
 constexpr int kChunk = 8;                       // stages (1024 k) between drains of an accumulator
-constexpr int kConvWGs = 2;
+constexpr int kConvWGs = 2;                     // warpgroups that convert B, alternate stages
 constexpr uint32_t kI8TmemCols = 512;
 constexpr int kMaxStages = 10;
 constexpr int kSmemLimit = 232448;
 
 struct I8Shared {
-    uint64_t full[kMaxStages];   // B and the tokens of the stage have landed
-    uint64_t empty[kMaxStages];  // the converting warps have read B, the MMAs have read the tokens
-    uint64_t afull[kAStages];    // the stage's B stands in tensor memory (the converting warps)
-    uint64_t aempty[kAStages];   // the MMAs that read it have finished
-    uint64_t dfull[2];           // an accumulator holds up to 1024 k
-    uint64_t dempty[2];          // it has been read
-    uint64_t drained;            // abort only: every MMA issued has finished
+    uint64_t bfull[kMaxStages];   // B (DIRECT: and the tokens' int8) of the stage has landed
+    uint64_t bempty[kMaxStages];  // a warpgroup's four warps (DIRECT: and four more) have read it
+    uint64_t xfull[kMaxStages];   // the tokens of the stage stand in shared memory
+    uint64_t xempty[kMaxStages];  // the MMAs have read them
+    uint64_t afull[kAStages];     // the stage's B stands in tensor memory (four warps)
+    uint64_t aempty[kAStages];    // the MMAs that read it have finished
+    uint64_t dfull[2];            // an accumulator holds up to 1024 k
+    uint64_t dempty[2];           // it has been read
+    uint64_t drained;             // abort only: every MMA issued has finished
     uint32_t tmem_base;
     int abort;
-    int units;                   // units of this launch
-    int bound[kMaxExperts + 1];  // first row of each expert, nondecreasing
-    int tiles[kMaxExperts + 1];  // token tiles of the experts before
+    int units;                    // units of this launch
+    int bound[kMaxExperts + 1];   // first row of each expert, nondecreasing
+    int tiles[kMaxExperts + 1];   // token tiles of the experts before
 };
 
-template <int NT, bool SPLIT>
+// DIRECT: the tokens' int8 rows come with B's stages and are expanded to FP16
+// here, by four warps; else they are read as FP16 by TMA.
+template <int NT, bool SPLIT, bool DIRECT>
 struct I8Cfg {
-    static constexpr int kTokenBytes = NT * kI8StageK * 2;
-    static constexpr int kStage = kBBytes + kTokenBytes;
+    static constexpr int kXBytes = NT * kI8StageK * 2;
     static constexpr int kXchg = SPLIT ? kI8TileN * NT * 4 : 0;  // partial sums from the cluster's CTAs
     static constexpr int kFree = kSmemLimit - 1024 - static_cast<int>(sizeof(I8Shared)) - kXchg;
-    static constexpr int kStages = kFree / kStage < kMaxStages ? kFree / kStage : kMaxStages;
-    static constexpr int kSmem = 1024 + kStages * kStage + kXchg + static_cast<int>(sizeof(I8Shared));
+    static constexpr int kStage = kBBytes + (DIRECT ? NT * kI8StageK : 0);
+    // Rings: up to 32 KiB of FP16 tokens (at least two stages, three where TMA
+    // fetches them from L2), and the stages of B in what is left.  An even
+    // number of B's stages, so that a converting warpgroup sees every phase of
+    // the stages it reads: the parity of a phase tells it from the one before
+    // only.
+    static constexpr int kXStages = !DIRECT ? 3 : 32768 / kXBytes < 4 ? 32768 / kXBytes : 4;
+    static constexpr int kBFit = (kFree - kXStages * kXBytes) / kStage / 2 * 2;
+    static constexpr int kBStages = kBFit < kMaxStages ? kBFit : kMaxStages;
+    static constexpr int kRing = kBStages * kStage + kXStages * kXBytes;
+    static constexpr int kSmem = 1024 + kRing + kXchg + static_cast<int>(sizeof(I8Shared));
     static constexpr int kEpiWGs = NT > 64 ? 2 : 1;
     static constexpr int kCols = NT / kEpiWGs;  // accumulator columns a thread drains
-    static constexpr int kThreads = 128 * (1 + kConvWGs + kEpiWGs);
+    static constexpr int kWarpX = 4, kWarpConv = kWarpX + (DIRECT ? 4 : 0), kWarpEpi = kWarpConv + 4 * kConvWGs;
+    static constexpr int kThreads = 32 * (kWarpEpi + 4 * kEpiWGs);
+    static constexpr int kPieces = NT / 16;              // 16-byte pieces of a stage's tokens a thread expands
     static_assert(2 * NT + kAStages * kACols <= static_cast<int>(kI8TmemCols), "tensor memory");
-    static_assert(kStages >= 3 && kSmem <= kSmemLimit, "shared memory");
+    static_assert(kBStages >= 4 && kBStages % kConvWGs == 0 && kXStages >= 2 && kXStages <= kMaxStages, "rings");
+    static_assert(kAStages % kConvWGs == 0 && kSmem <= kSmemLimit, "shared memory");
 };
 
 struct I8Unit {
@@ -368,17 +383,18 @@ __device__ __forceinline__ void sum_tiles(I8Shared *sh, const Int8Args &a, int n
     }
 }
 
-template <int NT, bool SPLIT>
-__global__ void __launch_bounds__(I8Cfg<NT, SPLIT>::kThreads, 1)
+template <int NT, bool SPLIT, bool DIRECT>
+__global__ void __launch_bounds__(I8Cfg<NT, SPLIT, DIRECT>::kThreads, 1)
 int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA, const Int8Args a) {
-    using Cf = I8Cfg<NT, SPLIT>;
-    constexpr int S = Cf::kStages;
+    using Cf = I8Cfg<NT, SPLIT, DIRECT>;
+    constexpr int SB = Cf::kBStages, SX = Cf::kXStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-    uint8_t *ring = smem_raw + pad;
-    int *xchg = reinterpret_cast<int *>(ring + S * Cf::kStage);
-    I8Shared *sh = reinterpret_cast<I8Shared *>(ring + S * Cf::kStage + Cf::kXchg);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint8_t *ring_b = smem_raw + pad, *ring_x = ring_b + SB * Cf::kStage;
+    int *xchg = reinterpret_cast<int *>(ring_b + Cf::kRing);
+    I8Shared *sh = reinterpret_cast<I8Shared *>(ring_b + Cf::kRing + Cf::kXchg);
+    // warp number and tensor-memory address through a shuffle: uniform to the compiler too
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int splits = SPLIT ? a.ksplit : 1;
     const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
     const int first_unit = SPLIT ? static_cast<int>(blockIdx.x) / splits : static_cast<int>(blockIdx.x);
@@ -389,12 +405,16 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
     const int kb = SPLIT ? rank * kt / splits : 0, ke = SPLIT ? (rank + 1) * kt / splits : kt;
 
     if (tid == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(&sh->full[s], 1);
-            mbar_init(&sh->empty[s], 4 * kConvWGs + 1);
+        for (int s = 0; s < SB; ++s) {
+            mbar_init(&sh->bfull[s], 1);
+            mbar_init(&sh->bempty[s], DIRECT ? 8 : 4);
+        }
+        for (int s = 0; s < SX; ++s) {
+            mbar_init(&sh->xfull[s], DIRECT ? 4 : 1);
+            mbar_init(&sh->xempty[s], 1);
         }
         for (int s = 0; s < kAStages; ++s) {
-            mbar_init(&sh->afull[s], 4 * kConvWGs);
+            mbar_init(&sh->afull[s], 4);
             mbar_init(&sh->aempty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -418,11 +438,12 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
     __syncthreads();
     if (SPLIT) cluster_sync();  // every CTA runs before another writes into it
     tc::fence_after_sync();
-    const uint32_t tmem = sh->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem_base, 0);
     const uint32_t tmem_a = tmem + 2 * NT;
     volatile int *abort_flag = &sh->abort;
     const int units = sh->units;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (mbar_wait(bar, parity, a.status)) return true;
         *abort_flag = 1;
@@ -437,13 +458,12 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             if (lane == 0 && ok) {
                 const I8Unit q = unit_of(sh, a, NT, ch_tiles, u);
                 for (int i = kb; i < ke; ++i, ++it) {
-                    const int s = it % S;
-                    if (it >= S && !wait(&sh->empty[s], (it / S - 1) & 1)) { ok = false; break; }
-                    uint8_t *st = ring + s * Cf::kStage;
-                    mbar_arrive_expect_tx(&sh->full[s], Cf::kStage);
-                    tma_load_3d(st, &tmB, &sh->full[s], i * kI8StageK, q.ch0, q.e);
-                    tma_load_2d(st + kBBytes, &tmA, &sh->full[s], i * kI8StageK, q.t0 - a.row0);
-                    tma_load_2d(st + kBBytes + NT * 128, &tmA, &sh->full[s], i * kI8StageK + 64, q.t0 - a.row0);
+                    const int s = it % SB;
+                    if (it >= SB && !wait(&sh->bempty[s], (it / SB - 1) & 1)) { ok = false; break; }
+                    uint8_t *st = ring_b + s * Cf::kStage;
+                    mbar_arrive_expect_tx(&sh->bfull[s], Cf::kStage);
+                    tma_load_3d(st, &tmB, &sh->bfull[s], i * kI8StageK, q.ch0, q.e);
+                    if (DIRECT) tma_load_2d(st + kBBytes, &tmA, &sh->bfull[s], i * kI8StageK, q.t0 - a.row0);
                 }
             }
             __syncwarp();
@@ -453,37 +473,63 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             }
         }
         if (lane == 0)  // no copy outlives the CTA
-            for (int t = max(0, it - S); t < it; ++t) mbar_wait(&sh->full[t % S], (t / S) & 1, a.status);
+            for (int t = max(0, it - SB); t < it; ++t) mbar_wait(&sh->bfull[t % SB], (t / SB) & 1, a.status);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
+        // The whole warp walks the stages and waits; one elected lane issues.
         constexpr uint32_t idesc = tc::idesc_f16_kmajor(kI8TileN, NT);
+        const uint64_t xdesc = tc::smem_desc(smem_u32(ring_x), 16, 1024, tc::kLayoutSwizzle128);
         int it = 0, chunk = 0;
         bool ok = true;
         for (int u = first_unit; u < units; u += unit_step) {
-            if (lane == 0 && ok) {
-                for (int i = kb; i < ke; ++i, ++it) {
-                    const int s = it % S, t = it % kAStages, d = chunk & 1;
-                    const bool start = (i - kb) % kChunk == 0;
-                    if ((start && chunk >= 2 && !wait(&sh->dempty[d], (chunk / 2 - 1) & 1)) ||
-                        !wait(&sh->full[s], (it / S) & 1) || !wait(&sh->afull[t], (it / kAStages) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after_sync();
-                    const uint32_t b = smem_u32(ring + s * Cf::kStage + kBBytes);
+            for (int i = kb; i < ke && ok; ++i, ++it) {
+                const int x = it % SX, t = it % kAStages, d = chunk & 1;
+                const bool start = (i - kb) % kChunk == 0, end = i + 1 == ke || (i + 1 - kb) % kChunk == 0;
+                ok = (!start || chunk < 2 || wait(&sh->dempty[d], (chunk / 2 - 1) & 1)) &&
+                     wait(&sh->xfull[x], (it / SX) & 1) && wait(&sh->afull[t], (it / kAStages) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    const uint64_t b = xdesc + static_cast<uint64_t>(x * (Cf::kXBytes / 16));
 #pragma unroll
                     for (int kk = 0; kk < kI8StageK / 16; ++kk)
                         tc::mma_f16_ta(tmem + d * NT, tmem_a + t * kACols + kk * 8,
-                                       tc::smem_desc(b + (kk / 4) * NT * 128 + (kk % 4) * 32, 16, 1024,
-                                                     tc::kLayoutSwizzle128),
-                                       idesc, (start && kk == 0) ? 0u : 1u);
-                    tc::commit(&sh->empty[s]);
+                                       b + ((kk / 4) * NT * 128 + (kk % 4) * 32) / 16, idesc,
+                                       (start && kk == 0) ? 0u : 1u);
+                    tc::commit(&sh->xempty[x]);
                     tc::commit(&sh->aempty[t]);
-                    if (i + 1 == ke || (i + 1 - kb) % kChunk == 0) {
-                        tc::commit(&sh->dfull[d]);
-                        ++chunk;
-                    }
+                    if (end) tc::commit(&sh->dfull[d]);
+                }
+                __syncwarp();
+                if (end) ++chunk;
+            }
+            if (SPLIT) {
+                __syncwarp();
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+        if (!ok && tc::elect_one()) {  // no teardown under a running MMA
+            tc::commit(&sh->drained);
+            mbar_wait(&sh->drained, 0, a.status);
+        }
+        __syncwarp();
+    } else if (!DIRECT && warp == 2) {
+        // ------------------------------------------------ TMA producer of the tokens
+        int it = 0;
+        bool ok = true;
+        for (int u = first_unit; u < units; u += unit_step) {
+            if (lane == 0 && ok) {
+                const I8Unit q = unit_of(sh, a, NT, ch_tiles, u);
+                for (int i = kb; i < ke; ++i, ++it) {
+                    const int x = it % SX;
+                    if (it >= SX && !wait(&sh->xempty[x], (it / SX - 1) & 1)) { ok = false; break; }
+                    uint8_t *st = ring_x + x * Cf::kXBytes;
+                    mbar_arrive_expect_tx(&sh->xfull[x], Cf::kXBytes);
+                    tma_load_2d(st, &tmA, &sh->xfull[x], i * kI8StageK, q.t0 - a.row0);
+                    tma_load_2d(st + NT * 128, &tmA, &sh->xfull[x], i * kI8StageK + 64, q.t0 - a.row0);
                 }
             }
             __syncwarp();
@@ -492,46 +538,46 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                 cluster_sync();
             }
         }
-        if (lane == 0 && !ok) {  // no teardown under a running MMA
-            tc::commit(&sh->drained);
-            mbar_wait(&sh->drained, 0, a.status);
-        }
+        if (lane == 0)
+            for (int t = max(0, it - SX); t < it; ++t) mbar_wait(&sh->xfull[t % SX], (t / SX) & 1, a.status);
         __syncwarp();
-    } else if (warp >= 4 && warp < 4 + 4 * kConvWGs) {
-        // ------------------------------------------------ B to FP16, into tensor memory
-        const int half = (warp - 4) / 4;
-        const int row = (warp % 4) * 32 + lane;
-        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+    } else if (DIRECT && warp >= Cf::kWarpX && warp < Cf::kWarpConv) {
+        // ------------------------------------------------ the tokens' rows to FP16
+        const int me = tid - 32 * Cf::kWarpX;
+        const int kc = me % 8;  // 16 k of a row; rows me / 8, me / 8 + 16, ..
         int it = 0;
         bool ok = true;
         for (int u = first_unit; u < units; u += unit_step) {
-            for (int i = kb; i < ke; ++i, ++it) {
-                const int s = it % S, t = it % kAStages;
-                ok = ok && wait(&sh->full[s], (it / S) & 1) &&
-                     (it < kAStages || wait(&sh->aempty[t], (it / kAStages - 1) & 1));
+            for (int i = kb; i < ke && ok; ++i, ++it) {
+                const int s = it % SB, x = it % SX;
+                ok = wait(&sh->bfull[s], (it / SB) & 1) && (it < SX || wait(&sh->xempty[x], (it / SX - 1) & 1));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                tc::fence_after_sync();
-                const uint8_t *src = ring + s * Cf::kStage + row * kI8StageK;
-                uint4 w[4];
+                const uint8_t *src = ring_b + s * Cf::kStage + kBBytes;
+                uint8_t *st = ring_x + x * Cf::kXBytes + (kc / 4) * NT * 128;
+                uint4 v[Cf::kPieces];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    w[c] = *reinterpret_cast<const uint4 *>(src + (((half * 4 + c) ^ (row & 7)) * 16));
-                uint32_t o[32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    int8x4_to_f16(w[c].x, o[c * 8 + 0], o[c * 8 + 1]);
-                    int8x4_to_f16(w[c].y, o[c * 8 + 2], o[c * 8 + 3]);
-                    int8x4_to_f16(w[c].z, o[c * 8 + 4], o[c * 8 + 5]);
-                    int8x4_to_f16(w[c].w, o[c * 8 + 6], o[c * 8 + 7]);
+                for (int j = 0; j < Cf::kPieces; ++j) {
+                    const int row = me / 8 + 16 * j;
+                    v[j] = *reinterpret_cast<const uint4 *>(src + row * 128 + ((kc ^ (row & 7)) * 16));
                 }
-                tc::tmem_st32(tmem_a + t * kACols + half * 32 + lanes, o);
+#pragma unroll
+                for (int j = 0; j < Cf::kPieces; ++j) {
+                    const int row = me / 8 + 16 * j, c = (kc % 4) * 2;
+                    uint4 o0, o1;
+                    int8x4_to_f16(v[j].x, o0.x, o0.y);
+                    int8x4_to_f16(v[j].y, o0.z, o0.w);
+                    int8x4_to_f16(v[j].z, o1.x, o1.y);
+                    int8x4_to_f16(v[j].w, o1.z, o1.w);
+                    *reinterpret_cast<uint4 *>(st + row * 128 + ((c ^ (row & 7)) * 16)) = o0;
+                    *reinterpret_cast<uint4 *>(st + row * 128 + (((c + 1) ^ (row & 7)) * 16)) = o1;
+                }
+                tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->empty[s]);
-                tc::tmem_st_wait();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->afull[t]);
+                if (lane == 0) {
+                    mbar_arrive(&sh->bempty[s]);
+                    mbar_arrive(&sh->xfull[x]);
+                }
             }
             if (SPLIT) {
                 __syncwarp();
@@ -539,9 +585,67 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                 cluster_sync();
             }
         }
-    } else if (warp >= 4 + 4 * kConvWGs) {
+    } else if (warp >= Cf::kWarpConv && warp < Cf::kWarpEpi) {
+        // ------------------------------------------------ B to FP16, into tensor memory
+        const int wg = (warp - Cf::kWarpConv) / 4;
+        const int row = (warp % 4) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        int it = 0, stored = -1;  // stored: the stage in tensor memory whose stores have not been waited for
+        bool ok = true;
+        auto flush = [&]() {
+            if (stored < 0) return;
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->afull[stored]);
+            stored = -1;
+        };
+        for (int u = first_unit; u < units; u += unit_step) {
+            for (int i = kb; i < ke && ok; ++i, ++it) {
+                if (it % kConvWGs != wg) continue;
+                const int s = it % SB, t = it % kAStages;
+                // the stage before is handed on while this one is read, unless
+                // this one has yet to land
+                if (!__all_sync(0xffffffffu, mbar_try_wait(&sh->bfull[s], (it / SB) & 1))) {
+                    flush();
+                    ok = __all_sync(0xffffffffu, wait(&sh->bfull[s], (it / SB) & 1));
+                    if (!ok) break;
+                }
+                const uint8_t *src = ring_b + s * Cf::kStage + row * kI8StageK;
+                uint4 w[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + ((c ^ (row & 7)) * 16));
+                flush();
+                ok = it < kAStages || wait(&sh->aempty[t], (it / kAStages - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        int8x4_to_f16(w[h * 4 + c].x, o[c * 8 + 0], o[c * 8 + 1]);
+                        int8x4_to_f16(w[h * 4 + c].y, o[c * 8 + 2], o[c * 8 + 3]);
+                        int8x4_to_f16(w[h * 4 + c].z, o[c * 8 + 4], o[c * 8 + 5]);
+                        int8x4_to_f16(w[h * 4 + c].w, o[c * 8 + 6], o[c * 8 + 7]);
+                    }
+                    tc::tmem_st32(tmem_a + t * kACols + h * 32 + lanes, o);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->bempty[s]);
+                stored = t;
+            }
+            flush();
+            if (SPLIT) {
+                __syncwarp();
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+    } else if (warp >= Cf::kWarpEpi) {
         // ------------------------------------------------ accumulators to C
-        const int wg = (warp - 4 - 4 * kConvWGs) / 4;
+        const int wg = (warp - Cf::kWarpEpi) / 4;
         const int ch = (warp % 4) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
         int chunk = 0;
@@ -631,37 +735,41 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
     }
 }
 
-template <int NT, bool SPLIT>
+template <int NT, bool SPLIT, bool DIRECT>
 cudaError_t prepare_one() {
-    return cudaFuncSetAttribute(int8_tc_kernel<NT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                I8Cfg<NT, SPLIT>::kSmem);
+    return cudaFuncSetAttribute(int8_tc_kernel<NT, SPLIT, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                I8Cfg<NT, SPLIT, DIRECT>::kSmem);
+}
+
+template <int NT, bool SPLIT, bool DIRECT>
+cudaError_t launch_one(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
+                       int smem_override, cudaStream_t stream) {
+    using Cf = I8Cfg<NT, SPLIT, DIRECT>;
+    const int ch_tiles = (a.N + kI8TileN - 1) / kI8TileN, splits = SPLIT ? a.ksplit : 1;
+    // at most this many units (the experts' row counts are on the device)
+    const long long tiles = a.experts == 1 ? (a.rows + NT - 1) / NT
+                                           : static_cast<long long>(a.rows) / NT + (a.experts < a.rows ? a.experts : a.rows);
+    const long long units = tiles * ch_tiles, most = num_sms / splits;
+    return launch_dependent(int8_tc_kernel<NT, SPLIT, DIRECT>,
+                            dim3(static_cast<unsigned>(splits * (units < most ? units : most))), dim3(Cf::kThreads),
+                            smem_override > 0 ? smem_override : Cf::kSmem, stream, splits, tmB, tmA, a);
 }
 
 template <int NT>
-cudaError_t launch_nt(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
-                      int smem_override, cudaStream_t stream) {
-    const int ch_tiles = (a.N + kI8TileN - 1) / kI8TileN;
-    const long long tiles = static_cast<long long>(a.rows) / NT + (a.experts < a.rows ? a.experts : a.rows);
-    const long long units = (a.experts == 1 ? (a.rows + NT - 1) / NT : tiles) * ch_tiles;
-    if (a.ksplit > 1) {
-        using Cf = I8Cfg<NT, true>;
-        const long long most = num_sms / a.ksplit;
-        return launch_dependent(int8_tc_kernel<NT, true>, dim3(a.ksplit * (units < most ? units : most)),
-                                dim3(Cf::kThreads), smem_override > 0 ? smem_override : Cf::kSmem, stream, a.ksplit,
-                                tmB, tmA, a);
-    }
-    using Cf = I8Cfg<NT, false>;
-    return launch_dependent(int8_tc_kernel<NT, false>, dim3(units < num_sms ? units : num_sms), dim3(Cf::kThreads),
-                            smem_override > 0 ? smem_override : Cf::kSmem, stream, 1, tmB, tmA, a);
+cudaError_t launch_direct(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
+                          int smem_override, cudaStream_t stream) {
+    return a.ksplit > 1 ? launch_one<NT, true, true>(a, tmB, tmA, num_sms, smem_override, stream)
+                        : launch_one<NT, false, true>(a, tmB, tmA, num_sms, smem_override, stream);
 }
 
 }  // namespace
 
 cudaError_t int8_prepare() {
     cudaError_t e = cudaSuccess;
-    for (cudaError_t r : {prepare_one<16, false>(), prepare_one<32, false>(), prepare_one<64, false>(),
-                          prepare_one<128, false>(), prepare_one<16, true>(), prepare_one<32, true>(),
-                          prepare_one<64, true>(), prepare_one<128, true>()})
+    for (cudaError_t r : {prepare_one<16, false, true>(), prepare_one<32, false, true>(),
+                          prepare_one<64, false, true>(), prepare_one<16, true, true>(),
+                          prepare_one<32, true, true>(), prepare_one<64, true, true>(),
+                          prepare_one<128, false, false>()})
         if (e == cudaSuccess) e = r;
     return e;
 }
@@ -669,10 +777,10 @@ cudaError_t int8_prepare() {
 cudaError_t launch_int8_tc(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
                            int smem_override, cudaStream_t stream) {
     switch (a.nt) {
-        case 16: return launch_nt<16>(a, tmB, tmA, num_sms, smem_override, stream);
-        case 32: return launch_nt<32>(a, tmB, tmA, num_sms, smem_override, stream);
-        case 64: return launch_nt<64>(a, tmB, tmA, num_sms, smem_override, stream);
-        default: return launch_nt<128>(a, tmB, tmA, num_sms, smem_override, stream);
+        case 16: return launch_direct<16>(a, tmB, tmA, num_sms, smem_override, stream);
+        case 32: return launch_direct<32>(a, tmB, tmA, num_sms, smem_override, stream);
+        case 64: return launch_direct<64>(a, tmB, tmA, num_sms, smem_override, stream);
+        default: return launch_one<128, false, false>(a, tmB, tmA, num_sms, smem_override, stream);
     }
 }
 

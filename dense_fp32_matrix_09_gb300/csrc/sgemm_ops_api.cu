@@ -114,29 +114,37 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
     a.status = v.d_status;
     a.ksplit = 1;
 
+    // Tiles of up to 64 tokens read the tokens' int8 rows, by TMA: rows on other
+    // than 16-byte boundaries are copied first.  Wider tiles read them as FP16.
+    const int owners = std::min(experts, std::max(rows, 1));
+    a.nt = token_tile(cdiv(rows, owners));
+    const bool direct = a.nt <= 64;
+    const bool a_as_stored = direct && aligned(A, 16) && lda % 16 == 0;
+    const int kp = static_cast<int>(cdiv(K, 64) * 64), kb = static_cast<int>(cdiv(K, 16) * 16);
+    const size_t a_row = a_as_stored ? 0 : direct ? static_cast<size_t>(kb) : static_cast<size_t>(kp) * 2;
+
     // The re-layout workspace: B where the TMA cannot read it as stored, then
-    // the tokens' rows in FP16, as many at a time as fit.
+    // the tokens' rows, as many at a time as fit.
     uint8_t *ws = reinterpret_cast<uint8_t *>(v.d_rl);
     size_t room = v.rl_bytes;
-    const int kp = static_cast<int>(cdiv(K, 64) * 64), kb = static_cast<int>(cdiv(K, 16) * 16);
     const bool as_stored = transB && aligned(B, 16) && ldb % 16 == 0 && (experts == 1 || strideB % 16 == 0);
     const size_t b_bytes = as_stored ? 0 : static_cast<size_t>(experts) * N * kb;
     const size_t b_room = (b_bytes + 1023) / 1024 * 1024;
-    bool tc = v.pinned != SGEMM_VARIANT_GENERIC && v.pinned != SGEMM_VARIANT_GENERIC_I8 && K > 0 && ws != nullptr &&
-              (as_stored || v.relayout_mode != SGEMM_RELAYOUT_OFF) && b_room < room &&
-              room - b_room >= static_cast<size_t>(kp) * 2 * std::min(rows, 128);
+    bool tc = v.pinned != SGEMM_VARIANT_GENERIC && v.pinned != SGEMM_VARIANT_GENERIC_I8 && K > 0 &&
+              ((as_stored && a_as_stored) || ws != nullptr) && (as_stored || v.relayout_mode != SGEMM_RELAYOUT_OFF) &&
+              b_room <= room && room - b_room >= a_row * std::min(rows, a.nt);
     const long long ch_tiles = cdiv(N, sg::kI8TileN);
-    int per = 0;  // rows of one pass
+    int per = rows;  // rows of one pass
     if (tc) {
-        const long long fit = static_cast<long long>((room - b_room) / (static_cast<size_t>(kp) * 2));
-        per = static_cast<int>(std::min<long long>(rows, fit >= 128 ? fit / 128 * 128 : fit));
-        const int owners = std::min(experts, rows);
-        a.nt = token_tile(cdiv(rows, owners));
+        if (a_row) {
+            const long long fit = static_cast<long long>((room - b_room) / a_row);
+            if (fit < rows) per = static_cast<int>(fit / a.nt * a.nt);
+        }
         const long long tiles = (experts == 1 ? cdiv(per, a.nt) : per / a.nt + owners) * ch_tiles;
         tc = tiles < INT_MAX && (static_cast<long long>(per / a.nt) + experts) * ch_tiles < INT_MAX;
-        a.ksplit = split_of(tiles, static_cast<int>(cdiv(K, sg::kI8StageK)), v.num_sms);
+        a.ksplit = direct ? split_of(tiles, static_cast<int>(cdiv(K, sg::kI8StageK)), v.num_sms) : 1;
     }
-    CUtensorMap tmB, tmA;
+    CUtensorMap tmB, tmA{};
     if (tc) {
         if (!as_stored) {
             const cudaError_t e =
@@ -154,17 +162,27 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
         const long long stride = experts > 1 ? a.strideB : a.ldb * static_cast<long long>(N);
         tc = sg::encode_map(&tmB, sg::MapType::kInt8, 3, a.B, K, N, experts, a.ldb, stride, sg::kI8StageK,
                             sg::kI8TileN) &&
-             sg::encode_map(&tmA, sg::MapType::kF16, 2, ws, kp, per, 1, static_cast<long long>(kp) * 2, 0, 64, a.nt);
+             (direct ? sg::encode_map(&tmA, sg::MapType::kInt8, 2, a_as_stored ? static_cast<const void *>(A) : ws, K, per,
+                                      1, a_as_stored ? lda : kb, 0, sg::kI8StageK, a.nt)
+                     : sg::encode_map(&tmA, sg::MapType::kF16, 2, ws, kp, per, 1, static_cast<long long>(kp) * 2, 0,
+                                      64, a.nt));
     }
     if (tc) {
         variant = SGEMM_VARIANT_TC_I8;
         for (int r0 = 0; r0 < rows; r0 += per) {
             a.row0 = r0;
             a.rows = std::min(per, rows - r0);
-            cudaError_t e = sg::launch_int8_to_f16(A + static_cast<long long>(r0) * lda, lda, a.rows, K, ws, kp, stream);
+            const int8_t *src = A + static_cast<long long>(r0) * lda;
+            cudaError_t e = cudaSuccess;
+            if (!direct) {
+                e = sg::launch_int8_to_f16(src, lda, a.rows, K, ws, kp, stream);
+            } else if (!a_as_stored) {
+                e = sg::launch_int8_relayout(src, lda, 0, 1, 1, a.rows, K, reinterpret_cast<int8_t *>(ws), kb, stream);
+            }
+            if (a_row) ++launches;
             if (e == cudaSuccess) e = sg::launch_int8_tc(a, tmB, tmA, v.num_sms, v.smem_override, stream);
             if (e != cudaSuccess) return from_cuda(e);
-            launches += 2;
+            ++launches;
         }
     } else {
         a.ksplit = 1;

@@ -178,6 +178,16 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar, uint16_t cta_mask) {
         ::"r"(smem_u32(bar)), "h"(cta_mask) : "memory");
 }
 
+// One lane of the (converged) warp, the same each time.  A branch on it, unlike
+// one on the lane number, leaves the compiler sure that what the warp computed
+// is uniform: the MMA's descriptors then stay in uniform registers instead of
+// being moved there, one by one, before every instruction.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ---- .kind::f16 with the A operand in tensor memory -------------------------
 // Instruction descriptor of tcgen05.mma .kind::f16, both operands FP16 and
 // K-major, D FP32 (fields as for .kind::tf32; FP16 is format 0).
