@@ -44,7 +44,7 @@
 //    innermost within groups of 16 so that concurrent CTAs share B's tiles in L2.
 //    With few tiles the 2, 4 or 8 CTAs of a cluster share a tile's K range;
 //    each sends the others their columns' int32 partial sums through
-//    distributed shared memory.
+//    distributed shared memory (tiles of up to 64 tokens, one epilogue warpgroup).
 //  * int8_generic_kernel -- any layout and alignment, dp4a on the CUDA cores.
 //  * int8_to_f16_kernel, int8_relayout_kernel -- the tokens' rows as FP16, and B
 //    as the TMA can read it (stored K x N, or not on 16-byte boundaries).
@@ -316,6 +316,7 @@ struct I8Cfg {
     static constexpr int kPieces = NT / 16;              // 16-byte pieces of a stage's tokens a thread expands
     static_assert(2 * NT + kAStages * kACols <= static_cast<int>(kI8TmemCols), "tensor memory");
     static_assert(kBStages >= 4 && kBStages % kConvWGs == 0 && kXStages >= 2 && kXStages <= kMaxStages, "rings");
+    static_assert(!SPLIT || (kEpiWGs == 1 && NT / 2 <= 32), "a lane holds a token scale");
     static_assert(kAStages % kConvWGs == 0 && kSmem <= kSmemLimit, "shared memory");
 };
 
@@ -469,7 +470,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             __syncwarp();
             if (SPLIT) {
                 cluster_sync();
-                cluster_sync();
+                if (u + unit_step < units) cluster_sync();
             }
         }
         if (lane == 0)  // no copy outlives the CTA
@@ -508,7 +509,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             if (SPLIT) {
                 __syncwarp();
                 cluster_sync();
-                cluster_sync();
+                if (u + unit_step < units) cluster_sync();
             }
         }
         if (!ok && tc::elect_one()) {  // no teardown under a running MMA
@@ -535,7 +536,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             __syncwarp();
             if (SPLIT) {
                 cluster_sync();
-                cluster_sync();
+                if (u + unit_step < units) cluster_sync();
             }
         }
         if (lane == 0)
@@ -582,7 +583,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             if (SPLIT) {
                 __syncwarp();
                 cluster_sync();
-                cluster_sync();
+                if (u + unit_step < units) cluster_sync();
             }
         }
     } else if (warp >= Cf::kWarpConv && warp < Cf::kWarpEpi) {
@@ -640,7 +641,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             if (SPLIT) {
                 __syncwarp();
                 cluster_sync();
-                cluster_sync();
+                if (u + unit_step < units) cluster_sync();
             }
         }
     } else if (warp >= Cf::kWarpEpi) {
@@ -652,6 +653,20 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
         bool ok = true;
         for (int u = first_unit; u < units; u += unit_step) {
             const I8Unit q = unit_of(sh, a, NT, ch_tiles, u);
+            // What the epilogue needs of global memory, asked for before the sums
+            // are ready: the channel's scale and bias, and lane l's share of the
+            // token scales (handed round by shuffles).
+            const int n = q.ch0 + ch;
+            const long long at = static_cast<long long>(q.e) * a.N + n;
+            const float sb = n < a.N ? __ldg(a.scaleB + at) : 0.f;
+            const float bias = n < a.N && a.bias ? __ldg(a.bias + at) : 0.f;
+            const int per = SPLIT ? NT / splits : Cf::kCols;  // this CTA's (warpgroup's) columns of the result
+            const int shift = 31 - __clz(per);
+            const int first = q.t0 + (SPLIT ? rank * per : wg * Cf::kCols);
+            float sa[(Cf::kCols + 31) / 32];
+#pragma unroll
+            for (int c = 0; c < (Cf::kCols + 31) / 32; ++c)
+                sa[c] = c * 32 + lane < per && first + c * 32 + lane < q.tend ? __ldg(a.scaleA + first + c * 32 + lane) : 0.f;
             int acc[Cf::kCols];
 #pragma unroll
             for (int j = 0; j < Cf::kCols; ++j) acc[j] = 0;
@@ -671,59 +686,61 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->dempty[d]);
             }
-            const int n = q.ch0 + ch;
-            const long long at = static_cast<long long>(q.e) * a.N + n;
-            const float sb = n < a.N ? __ldg(a.scaleB + at) : 0.f;
-            const float bias = n < a.N && a.bias ? __ldg(a.bias + at) : 0.f;
             if (!SPLIT) {
-                if (ok && n < a.N)
+                if (ok)
                     with_out_type(a.out_type, [&](auto zero) {
                         using T = decltype(zero);
-                        T *C = static_cast<T *>(a.C) + n;
+                        T *C = static_cast<T *>(a.C) + static_cast<long long>(first) * a.ldc + n;
 #pragma unroll
                         for (int j = 0; j < Cf::kCols; ++j) {
-                            const int t = q.t0 + wg * Cf::kCols + j;
-                            if (t < q.tend)
-                                C[static_cast<long long>(t) * a.ldc] =
-                                    int8_out<T>(int8_value(acc[j], sb, __ldg(a.scaleA + t), bias));
+                            const float s = __shfl_sync(0xffffffffu, sa[j / 32], j % 32);
+                            if (first + j < q.tend && n < a.N)
+                                C[static_cast<long long>(j) * a.ldc] = int8_out<T>(int8_value(acc[j], sb, s, bias));
                         }
                     });
             } else {
-                // column j belongs to CTA j / (NT / splits) of the cluster
-                const int per = NT / splits;
+                // column j belongs to CTA j / per of the cluster
                 if (ok) {
+                    // (splits and per are powers of two)
+                    const uint32_t mine = smem_u32(xchg + rank * per * kI8TileN + ch);
+                    uint32_t to = 0;
 #pragma unroll
                     for (int j = 0; j < Cf::kCols; ++j) {
-                        const int col = wg * Cf::kCols + j;
-                        const int owner = col / per;
-                        const uint32_t to = dsmem_addr(
-                            xchg + (rank * per + (col - owner * per)) * kI8TileN + ch, static_cast<uint32_t>(owner));
-                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(acc[j]) : "memory");
+                        if ((j & (per - 1)) == 0)
+                            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(j >> shift));
+                        asm volatile("st.shared::cluster.u32 [%0], %1;"
+                                     ::"r"(to + (j & (per - 1)) * kI8TileN * 4), "r"(acc[j]) : "memory");
                     }
                 }
                 __syncwarp();
                 cluster_sync();
-                if (ok && n < a.N)
+                if (ok)
                     with_out_type(a.out_type, [&](auto zero) {
                         using T = decltype(zero);
-                        T *C = static_cast<T *>(a.C) + n;
-                        for (int c = wg; c < per; c += Cf::kEpiWGs) {
-                            const int t = q.t0 + rank * per + c;
-                            if (t >= q.tend) break;
-                            int sum = 0;
-                            for (int r = 0; r < splits; ++r) sum += xchg[(r * per + c) * kI8TileN + ch];
-                            C[static_cast<long long>(t) * a.ldc] =
-                                int8_out<T>(int8_value(sum, sb, __ldg(a.scaleA + t), bias));
+                        T *C = static_cast<T *>(a.C) + static_cast<long long>(first) * a.ldc + n;
+                        for (int c0 = 0; c0 < per; c0 += 8) {
+                            int sum[8] = {};
+                            for (int r = 0; r < splits; ++r)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    if (c0 + c < per) sum[c] += xchg[(r * per + c0 + c) * kI8TileN + ch];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const float s = __shfl_sync(0xffffffffu, sa[0], (c0 + c) & 31);
+                                if (c0 + c < per && first + c0 + c < q.tend && n < a.N)
+                                    C[static_cast<long long>(c0 + c) * a.ldc] =
+                                        int8_out<T>(int8_value(sum[c], sb, s, bias));
+                            }
                         }
                     });
                 __syncwarp();
-                cluster_sync();
+                if (u + unit_step < units) cluster_sync();
             }
         }
     } else {
         for (int u = first_unit; SPLIT && u < units; u += unit_step) {
             cluster_sync();
-            cluster_sync();
+            if (u + unit_step < units) cluster_sync();
         }
     }
     // ---------------------------------------------------- teardown
