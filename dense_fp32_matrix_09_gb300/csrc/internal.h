@@ -272,11 +272,11 @@ cudaError_t launch_int8_to_f16(const int8_t *A, long long lda, int rows, int K, 
 cudaError_t launch_int8_relayout(const int8_t *B, long long ldb, long long strideB, int trans, int experts, int N,
                                  int K, int8_t *dst, int ldd, cudaStream_t stream);
 constexpr int kI8TileN = 128, kI8StageK = 128;  // channels and k of one B stage (TMA box, 128-byte swizzle)
-constexpr int kI8TokenTiles[] = {16, 32, 64, 128};
+constexpr int kI8TokenTiles[] = {16, 32, 64, 128, 256};  // 256: CTA pairs, 256 channels
 cudaError_t int8_prepare();
 // tmB: int8, 3-D (k, channel, expert), box 128 x 128 x 1; tmA: 2-D (k, row - row0),
-// for nt <= 64 int8, box 128 x nt, else FP16, box 64 x nt; both with the 128-byte
-// swizzle.
+// for nt <= 64 int8, box 128 x nt, else FP16, box 64 x nt (64 x 64 for nt = 256); both
+// with the 128-byte swizzle.
 cudaError_t launch_int8_tc(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
                            int smem_override, cudaStream_t stream);
 

@@ -320,19 +320,37 @@ struct I8Cfg {
     static_assert(kAStages % kConvWGs == 0 && kSmem <= kSmemLimit, "shared memory");
 };
 
+// acc[j] += column j of an accumulator (integers): the load of the next 16
+// columns is in flight while 16 are converted.
+template <int COLS>
+__device__ __forceinline__ void drain(uint32_t tmem, int (&acc)[COLS]) {
+    uint32_t v[2][16];
+    tc::tmem_ld16_begin(tmem, v[0]);
+    tc::tmem_ld_wait(v[0]);
+#pragma unroll
+    for (int c = 0; c < COLS / 16; ++c) {
+        if (c + 1 < COLS / 16) tc::tmem_ld16_begin(tmem + (c + 1) * 16, v[(c + 1) & 1]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[c * 16 + j] += __float2int_rn(__uint_as_float(v[c & 1][j]));
+        if (c + 1 < COLS / 16) tc::tmem_ld_wait(v[(c + 1) & 1]);
+    }
+}
+
 struct I8Unit {
     int e, ch0, t0, tend;
 };
 
-// Unit u: the expert by bisection of the tile counts; within the expert groups
-// of 16 token tiles, channel tiles outer and token tiles inner.
-__device__ __forceinline__ I8Unit unit_of(const I8Shared *sh, const Int8Args &a, int nt, int ch_tiles, int u) {
+// Unit u of tiles of NT tokens x CH channels: the expert by bisection of the
+// tile counts; within the expert groups of 2048 tokens or 16 tiles, channel
+// tiles outer and token tiles inner.
+template <int NT, int CH, class Shared>
+__device__ __forceinline__ I8Unit unit_of(const Shared *sh, const Int8Args &a, int ch_tiles, int u) {
     int lo = 0, hi = a.experts;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if (sh->tiles[mid] * ch_tiles <= u) lo = mid; else hi = mid;
     }
-    constexpr int kGroup = 16;
+    constexpr int kGroup = 2048 / NT < 16 ? 2048 / NT : 16;
     const int mine = sh->tiles[lo + 1] - sh->tiles[lo];
     const int l = u - sh->tiles[lo] * ch_tiles;
     const int grp = l / (kGroup * ch_tiles), first = grp * kGroup;
@@ -340,14 +358,15 @@ __device__ __forceinline__ I8Unit unit_of(const I8Shared *sh, const Int8Args &a,
     const int r = l - grp * kGroup * ch_tiles;
     I8Unit q;
     q.e = lo;
-    q.ch0 = r / rows * kI8TileN;
-    q.t0 = max(sh->bound[lo], a.row0) + (first + r % rows) * nt;
+    q.ch0 = r / rows * CH;
+    q.t0 = max(sh->bound[lo], a.row0) + (first + r % rows) * NT;
     q.tend = min(sh->bound[lo + 1], a.row0 + a.rows);
     return q;
 }
 
 // One warp: the experts' first rows and the sums of their token tiles.
-__device__ __forceinline__ void sum_tiles(I8Shared *sh, const Int8Args &a, int nt, int ch_tiles, int lane) {
+template <class Shared>
+__device__ __forceinline__ void sum_tiles(Shared *sh, const Int8Args &a, int nt, int ch_tiles, int lane) {
     int top = 0, sum = 0;
     for (int e0 = 0; e0 <= a.experts; e0 += 32) {
         const int e = e0 + lane;
@@ -457,7 +476,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
         bool ok = true;
         for (int u = first_unit; u < units; u += unit_step) {
             if (lane == 0 && ok) {
-                const I8Unit q = unit_of(sh, a, NT, ch_tiles, u);
+                const I8Unit q = unit_of<NT, kI8TileN>(sh, a, ch_tiles, u);
                 for (int i = kb; i < ke; ++i, ++it) {
                     const int s = it % SB;
                     if (it >= SB && !wait(&sh->bempty[s], (it / SB - 1) & 1)) { ok = false; break; }
@@ -523,7 +542,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
         bool ok = true;
         for (int u = first_unit; u < units; u += unit_step) {
             if (lane == 0 && ok) {
-                const I8Unit q = unit_of(sh, a, NT, ch_tiles, u);
+                const I8Unit q = unit_of<NT, kI8TileN>(sh, a, ch_tiles, u);
                 for (int i = kb; i < ke; ++i, ++it) {
                     const int x = it % SX;
                     if (it >= SX && !wait(&sh->xempty[x], (it / SX - 1) & 1)) { ok = false; break; }
@@ -652,7 +671,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
         int chunk = 0;
         bool ok = true;
         for (int u = first_unit; u < units; u += unit_step) {
-            const I8Unit q = unit_of(sh, a, NT, ch_tiles, u);
+            const I8Unit q = unit_of<NT, kI8TileN>(sh, a, ch_tiles, u);
             // What the epilogue needs of global memory, asked for before the sums
             // are ready: the channel's scale and bias, and lane l's share of the
             // token scales (handed round by shuffles).
@@ -675,13 +694,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                 ok = __all_sync(0xffffffffu, wait(&sh->dfull[d], (chunk / 2) & 1));
                 if (!ok) break;
                 tc::fence_after_sync();
-#pragma unroll
-                for (int c = 0; c < Cf::kCols / 16; ++c) {
-                    float v[16];
-                    tc::tmem_ld16(tmem + d * NT + wg * Cf::kCols + c * 16 + lanes, v);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[c * 16 + j] += __float2int_rn(v[j]);
-                }
+                drain(tmem + d * NT + wg * Cf::kCols + lanes, acc);
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->dempty[d]);
@@ -752,6 +765,307 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
     }
 }
 
+// ---- CTA pairs: 256 channels x 256 tokens -------------------------------------------
+constexpr int kPairN = 256, kPairT = 256;        // channels and tokens of a pair's tile
+constexpr int kPairXBytes = 128 * kI8StageK * 2;  // this CTA's half of the tokens, FP16: 32 KiB a stage
+constexpr int kPairBStages = 5, kPairXStages = 4;
+constexpr int kPairThreads = 512;
+
+struct PairShared {
+    uint64_t bfull[kPairBStages], bempty[kPairBStages];
+    uint64_t xfull[kPairXStages];   // (even CTA) both CTAs' tokens of the stage have landed
+    uint64_t xempty[kPairXStages];  // the MMAs have read them (both CTAs are told)
+    uint64_t afull[kAStages];       // (even CTA) B stands in both CTAs' tensor memory
+    uint64_t aempty[kAStages];
+    uint64_t dfull[2];              // a half accumulator holds up to 1024 k
+    uint64_t dempty[2];             // (even CTA) both CTAs have read it
+    uint64_t drained;
+    uint32_t tmem_base;
+    int abort;
+    int units;
+    int bound[kMaxExperts + 1];
+    int tiles[kMaxExperts + 1];
+};
+constexpr int kPairSmem = 1024 + kPairBStages * kBBytes + kPairXStages * kPairXBytes + static_cast<int>(sizeof(PairShared));
+static_assert(kPairSmem <= kSmemLimit, "shared memory");
+
+// Registers a thread of each warpgroup: control, conversion, two epilogue
+// warpgroups (128 sums a thread).  Their sum stays below 4 x 128, what the
+// block is launched with.
+constexpr int kRegsControl = 56, kRegsConvert = 96, kRegsEpilogue = 176;
+static_assert(kRegsControl + kRegsConvert + 2 * kRegsEpilogue <= 4 * 128, "register split");
+template <int R>
+__device__ __forceinline__ void regs_fewer() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA, const Int8Args a) {
+    constexpr int SB = kPairBStages, SX = kPairXStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;  // the same in both CTAs
+    uint8_t *ring_x = smem_raw + pad, *ring_b = ring_x + SX * kPairXBytes;
+    PairShared *sh = reinterpret_cast<PairShared *>(ring_b + SB * kBBytes);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int rank = static_cast<int>(cluster_ctarank());  // 0: issues the MMAs
+    const int first_unit = static_cast<int>(blockIdx.x) >> 1, unit_step = static_cast<int>(gridDim.x) >> 1;
+    const int ch_tiles = (a.N + kPairN - 1) / kPairN;
+    const int kt = (a.K + kI8StageK - 1) / kI8StageK;
+
+    if (tid == 0) {
+        for (int s = 0; s < SB; ++s) {
+            mbar_init(&sh->bfull[s], 1);
+            mbar_init(&sh->bempty[s], 4);
+        }
+        for (int s = 0; s < SX; ++s) {
+            mbar_init(&sh->xfull[s], 1);
+            mbar_init(&sh->xempty[s], 1);
+        }
+        for (int s = 0; s < kAStages; ++s) {
+            mbar_init(&sh->afull[s], 8);
+            mbar_init(&sh->aempty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh->dfull[s], 1);
+            mbar_init(&sh->dempty[s], 8);
+        }
+        mbar_init(&sh->drained, 1);
+        sh->abort = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmA);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc_pair(&sh->tmem_base, kI8TmemCols);
+        tc::tmem_relinquish_pair();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    if (warp == 2) sum_tiles(sh, a, kPairT, ch_tiles, lane);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_sync_all();  // both CTAs' barriers are initialised before any cross-CTA arrive
+    tc::fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem_base, 0);
+    const uint32_t tmem_a = tmem + kPairT;
+    volatile int *abort_flag = &sh->abort;
+    const int units = sh->units;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (mbar_wait(bar, parity, a.status)) return true;
+        *abort_flag = 1;
+        return false;
+    };
+
+    if (warp < 4) {
+        regs_fewer<kRegsControl>();
+        if (warp == 0) {
+            // -------------------------------------------- TMA producer of B
+            int it = 0;
+            bool ok = true;
+            if (lane == 0) {
+                for (int u = first_unit; u < units && ok; u += unit_step) {
+                    const I8Unit q = unit_of<kPairT, kPairN>(sh, a, ch_tiles, u);
+                    for (int i = 0; i < kt; ++i, ++it) {
+                        const int s = it % SB;
+                        if (it >= SB && !wait(&sh->bempty[s], (it / SB - 1) & 1)) { ok = false; break; }
+                        mbar_arrive_expect_tx(&sh->bfull[s], kBBytes);
+                        tma_load_3d(ring_b + s * kBBytes, &tmB, &sh->bfull[s], i * kI8StageK, q.ch0 + rank * kI8TileN, q.e);
+                    }
+                }
+                for (int t = max(0, it - SB); t < it; ++t) mbar_wait(&sh->bfull[t % SB], (t / SB) & 1, a.status);
+            }
+            __syncwarp();
+        } else if (warp == 1 && rank == 0) {
+            // -------------------------------------------- MMA issuer (even CTA)
+            constexpr uint32_t idesc = tc::idesc_f16_kmajor(2 * kI8TileN, kPairT / 2);
+            const uint64_t xdesc = tc::smem_desc(smem_u32(ring_x), 16, 1024, tc::kLayoutSwizzle128);
+            int it = 0, chunk = 0;
+            bool ok = true;
+            for (int u = first_unit; u < units && ok; u += unit_step) {
+                // Two stages at a time: both for half 0 of the accumulators, then
+                // both for half 1, so that at the end of 1024 k either half has the
+                // time of 16 MMAs (1024 cycles) to be drained in while the other
+                // is added to.
+                for (int i = 0; i < kt; i += 2) {
+                    const int two = i + 1 < kt ? 2 : 1;
+                    const bool start = i % kChunk == 0, end = i + two == kt || (i + two) % kChunk == 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && (!start || chunk == 0 || wait(&sh->dempty[h], (chunk - 1) & 1));
+                        for (int j = 0; j < two; ++j) {
+                            const int x = (it + j) % SX, t = (it + j) % kAStages;
+                            if (h == 0)
+                                ok = ok && wait(&sh->xfull[x], ((it + j) / SX) & 1) &&
+                                     wait(&sh->afull[t], ((it + j) / kAStages) & 1);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            if (tc::elect_one()) {
+                                const uint64_t b =
+                                    xdesc + static_cast<uint64_t>(x * (kPairXBytes / 16) + h * (64 * 128 / 16));
+#pragma unroll
+                                for (int kk = 0; kk < kI8StageK / 16; ++kk)
+                                    tc::mma_f16_ta_pair(tmem + h * (kPairT / 2), tmem_a + t * kACols + kk * 8,
+                                                        b + ((kk / 4) * 16384 + (kk % 4) * 32) / 16, idesc,
+                                                        (start && j == 0 && kk == 0) ? 0u : 1u);
+                                if (h == 1) {
+                                    tc::commit_pair(&sh->xempty[x], 0x3);
+                                    tc::commit_pair(&sh->aempty[t], 0x3);
+                                }
+                                if (end && j + 1 == two) tc::commit_pair(&sh->dfull[h], 0x3);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (!ok) break;
+                    it += two;
+                    if (end) ++chunk;
+                }
+            }
+            if (!ok && tc::elect_one()) {  // no teardown under a running MMA
+                tc::commit_pair(&sh->drained, 0x1);
+                mbar_wait(&sh->drained, 0, a.status);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // -------------------------------------------- TMA producer of the tokens
+            // Half h of the accumulators covers tokens t0 + 128 h ..+127, 64 from
+            // each CTA: this CTA's rows 64 h .. 64 h + 63 of a stage.  Both CTAs'
+            // bytes count on the even CTA's barrier.
+            int it = 0;
+            bool ok = true;
+            if (lane == 0) {
+                const uint32_t xfull = tc::map_shared_rank(smem_u32(&sh->xfull[0]), 0);
+                for (int u = first_unit; u < units && ok; u += unit_step) {
+                    const I8Unit q = unit_of<kPairT, kPairN>(sh, a, ch_tiles, u);
+                    const int row = q.t0 - a.row0 + rank * 64;
+                    for (int i = 0; i < kt; ++i, ++it) {
+                        const int x = it % SX;
+                        if (it >= SX && !wait(&sh->xempty[x], (it / SX - 1) & 1)) { ok = false; break; }
+                        uint8_t *st = ring_x + x * kPairXBytes;
+                        if (rank == 0) mbar_arrive_expect_tx(&sh->xfull[x], 2 * kPairXBytes);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                tc::tma_load_2d_pair(st + k * 16384 + h * 8192, &tmA, xfull + x * 8,
+                                                     i * kI8StageK + k * 64, row + h * 128);
+                    }
+                }
+                // no copy outlives its CTA: the MMAs that read the last ones have finished
+                for (int t = max(0, it - SX); t < it; ++t) mbar_wait(&sh->xempty[t % SX], (t / SX) & 1, a.status);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------ B to FP16, into tensor memory
+        regs_fewer<kRegsConvert>();
+        const int row = (warp % 4) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
+        const uint32_t afull = tc::map_shared_rank(smem_u32(&sh->afull[0]), 0);
+        int it = 0, stored = -1;
+        bool ok = true;
+        auto flush = [&]() {
+            if (stored < 0) return;
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_remote(afull + stored * 8);
+            stored = -1;
+        };
+        for (int u = first_unit; u < units && ok; u += unit_step) {
+            for (int i = 0; i < kt; ++i, ++it) {
+                const int s = it % SB, t = it % kAStages;
+                if (!__all_sync(0xffffffffu, mbar_try_wait(&sh->bfull[s], (it / SB) & 1))) {
+                    flush();
+                    ok = __all_sync(0xffffffffu, wait(&sh->bfull[s], (it / SB) & 1));
+                    if (!ok) break;
+                }
+                const uint8_t *src = ring_b + s * kBBytes + row * kI8StageK;
+                uint4 w[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + ((c ^ (row & 7)) * 16));
+                flush();
+                ok = it < kAStages || wait(&sh->aempty[t], (it / kAStages - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        int8x4_to_f16(w[h * 4 + c].x, o[c * 8 + 0], o[c * 8 + 1]);
+                        int8x4_to_f16(w[h * 4 + c].y, o[c * 8 + 2], o[c * 8 + 3]);
+                        int8x4_to_f16(w[h * 4 + c].z, o[c * 8 + 4], o[c * 8 + 5]);
+                        int8x4_to_f16(w[h * 4 + c].w, o[c * 8 + 6], o[c * 8 + 7]);
+                    }
+                    tc::tmem_st32(tmem_a + t * kACols + h * 32 + lanes, o);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->bempty[s]);
+                stored = t;
+            }
+            flush();
+        }
+    } else {
+        // ------------------------------------------------ accumulators to C: warpgroup h reads half h
+        regs_more<kRegsEpilogue>();
+        constexpr int kCols = kPairT / 2;
+        const int h = (warp - 8) / 4;
+        const int ch = (warp % 4) * 32 + lane;
+        const uint32_t src = tmem + h * kCols + (static_cast<uint32_t>(warp % 4 * 32) << 16);
+        const uint32_t dempty = tc::map_shared_rank(smem_u32(&sh->dempty[h]), 0);
+        int chunk = 0;
+        bool ok = true;
+        for (int u = first_unit; u < units && ok; u += unit_step) {
+            const I8Unit q = unit_of<kPairT, kPairN>(sh, a, ch_tiles, u);
+            const int n = q.ch0 + rank * kI8TileN + ch;
+            const long long at = static_cast<long long>(q.e) * a.N + n;
+            const float sb = n < a.N ? __ldg(a.scaleB + at) : 0.f;
+            const float bias = n < a.N && a.bias ? __ldg(a.bias + at) : 0.f;
+            const int first = q.t0 + h * kCols;
+            float sa[kCols / 32];
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c)
+                sa[c] = first + c * 32 + lane < q.tend ? __ldg(a.scaleA + first + c * 32 + lane) : 0.f;
+            int acc[kCols];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) acc[j] = 0;
+            for (int i = 0; i < kt; i += kChunk, ++chunk) {
+                ok = __all_sync(0xffffffffu, wait(&sh->dfull[h], chunk & 1));
+                if (!ok) break;
+                tc::fence_after_sync();
+                drain(src, acc);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_remote(dempty);
+            }
+            if (ok)
+                with_out_type(a.out_type, [&](auto zero) {
+                    using T = decltype(zero);
+                    T *C = static_cast<T *>(a.C) + static_cast<long long>(first) * a.ldc + n;
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) {
+                        const float s = __shfl_sync(0xffffffffu, sa[j / 32], j % 32);
+                        if (first + j < q.tend && n < a.N)
+                            C[static_cast<long long>(j) * a.ldc] = int8_out<T>(int8_value(acc[j], sb, s, bias));
+                    }
+                });
+        }
+    }
+    // ---------------------------------------------------- teardown
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_sync_all();  // the peer is done with this CTA's barriers and tensor memory
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc_pair(tmem, kI8TmemCols);
+    }
+}
+
 template <int NT, bool SPLIT, bool DIRECT>
 cudaError_t prepare_one() {
     return cudaFuncSetAttribute(int8_tc_kernel<NT, SPLIT, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -772,6 +1086,17 @@ cudaError_t launch_one(const Int8Args &a, const CUtensorMap &tmB, const CUtensor
                             smem_override > 0 ? smem_override : Cf::kSmem, stream, splits, tmB, tmA, a);
 }
 
+cudaError_t launch_pair(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
+                        int smem_override, cudaStream_t stream) {
+    const int ch_tiles = (a.N + kPairN - 1) / kPairN;
+    const long long tiles = a.experts == 1
+                                ? (a.rows + kPairT - 1) / kPairT
+                                : static_cast<long long>(a.rows) / kPairT + (a.experts < a.rows ? a.experts : a.rows);
+    const long long units = tiles * ch_tiles, most = num_sms / 2;
+    return launch_dependent(int8_tc_pair_kernel, dim3(static_cast<unsigned>(2 * (units < most ? units : most))),
+                            dim3(kPairThreads), smem_override > 0 ? smem_override : kPairSmem, stream, 2, tmB, tmA, a);
+}
+
 template <int NT>
 cudaError_t launch_direct(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
                           int smem_override, cudaStream_t stream) {
@@ -786,7 +1111,9 @@ cudaError_t int8_prepare() {
     for (cudaError_t r : {prepare_one<16, false, true>(), prepare_one<32, false, true>(),
                           prepare_one<64, false, true>(), prepare_one<16, true, true>(),
                           prepare_one<32, true, true>(), prepare_one<64, true, true>(),
-                          prepare_one<128, false, false>()})
+                          prepare_one<128, false, false>(),
+                          cudaFuncSetAttribute(int8_tc_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kPairSmem)})
         if (e == cudaSuccess) e = r;
     return e;
 }
@@ -797,6 +1124,7 @@ cudaError_t launch_int8_tc(const Int8Args &a, const CUtensorMap &tmB, const CUte
         case 16: return launch_direct<16>(a, tmB, tmA, num_sms, smem_override, stream);
         case 32: return launch_direct<32>(a, tmB, tmA, num_sms, smem_override, stream);
         case 64: return launch_direct<64>(a, tmB, tmA, num_sms, smem_override, stream);
+        case 256: return launch_pair(a, tmB, tmA, num_sms, smem_override, stream);
         default: return launch_one<128, false, false>(a, tmB, tmA, num_sms, smem_override, stream);
     }
 }

@@ -4,6 +4,7 @@
 // kernels in sgemm_int8.cu and sgemm_experts.cu.
 #include <algorithm>
 #include <climits>
+#include <cstdlib>
 #include <cstdint>
 
 #include <cuda.h>
@@ -46,11 +47,11 @@ struct Range {
 constexpr int kMaxInt8K = 131071;
 
 // The tile's tokens for products of `rows` rows a B matrix: the narrowest tile
-// that holds them, 128 beyond 64.
+// that holds them, 256 beyond.
 int token_tile(long long rows) {
     for (int nt : sg::kI8TokenTiles)
         if (rows <= nt) return nt;
-    return 128;
+    return 256;
 }
 
 int check_int8(int transB, int out_type, int experts, int rows, int N, int K, const int *offsets, bool grouped,
@@ -118,6 +119,7 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
     // than 16-byte boundaries are copied first.  Wider tiles read them as FP16.
     const int owners = std::min(experts, std::max(rows, 1));
     a.nt = token_tile(cdiv(rows, owners));
+    if (const char *f = getenv("I8_NT")) a.nt = atoi(f);
     const bool direct = a.nt <= 64;
     const bool a_as_stored = direct && aligned(A, 16) && lda % 16 == 0;
     const int kp = static_cast<int>(cdiv(K, 64) * 64), kb = static_cast<int>(cdiv(K, 16) * 16);
@@ -165,7 +167,7 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
              (direct ? sg::encode_map(&tmA, sg::MapType::kInt8, 2, a_as_stored ? static_cast<const void *>(A) : ws, K, per,
                                       1, a_as_stored ? lda : kb, 0, sg::kI8StageK, a.nt)
                      : sg::encode_map(&tmA, sg::MapType::kF16, 2, ws, kp, per, 1, static_cast<long long>(kp) * 2, 0,
-                                      64, a.nt));
+                                      64, std::min(a.nt, a.nt == 256 ? 64 : 128)));
     }
     if (tc) {
         variant = SGEMM_VARIANT_TC_I8;
