@@ -261,13 +261,19 @@ struct Int8Args {
     long long ldc;
     int out_type;
     int *status;
-    // tensor-core kernel: token tile, CTAs that share a tile's K range
+    // tensor-core kernels: token tile, CTAs that share a tile's K range
     int nt, ksplit;
+    // token tiles above 64: for each block that converted the tokens to FP16 the
+    // largest sum of |a| over 512 consecutive k
+    const int *peaks;
+    int n_peaks;
 };
 cudaError_t launch_int8_generic(const Int8Args &a, cudaStream_t stream);
-// dst (rows x ldd FP16, ldd a multiple of 8) = the int8 rows of A, columns K..ldd-1 zero.
-cudaError_t launch_int8_to_f16(const int8_t *A, long long lda, int rows, int K, void *dst, int ldd,
-                               cudaStream_t stream);
+// dst (rows x ldd FP16, ldd a multiple of 64) = the int8 rows of A, columns K..ldd-1
+// zero; peaks (room for kI8Peaks) gets *n_peaks sums of magnitudes (Int8Args).
+constexpr int kI8Peaks = 2048;
+cudaError_t launch_int8_to_f16(const int8_t *A, long long lda, int rows, int K, void *dst, int ldd, int *peaks,
+                               int *n_peaks, cudaStream_t stream);
 // dst (experts x N x ldd, columns K..ldd-1 zero) = B_e, stored N x K (trans = 1) or K x N (0).
 cudaError_t launch_int8_relayout(const int8_t *B, long long ldb, long long strideB, int trans, int experts, int N,
                                  int K, int8_t *dst, int ldd, cudaStream_t stream);

@@ -66,21 +66,70 @@ __device__ __forceinline__ float int8_value(int sum, float sb, float sa, float b
     return fmaf(__int2float_rn(sum) * sb, sa, bias);
 }
 
-template <class T>
-__device__ __forceinline__ T int8_out(float v);
-template <>
-__device__ __forceinline__ float int8_out<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 int8_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half int8_out<__half>(float v) { return __float2half_rn(v); }
+// Two values of the output type from one conversion, and the store of one or
+// the other.
+struct OutF32 {
+    using T = float;
+    using Two = float2;
+    static __device__ __forceinline__ Two two(float a, float b) { return make_float2(a, b); }
+    static __device__ __forceinline__ T lo(Two v) { return v.x; }
+    static __device__ __forceinline__ T hi(Two v) { return v.y; }
+};
+struct OutBF16 {
+    using T = __nv_bfloat16;
+    using Two = __nv_bfloat162;
+    static __device__ __forceinline__ Two two(float a, float b) { return __floats2bfloat162_rn(a, b); }
+    static __device__ __forceinline__ T lo(Two v) { return __low2bfloat16(v); }
+    static __device__ __forceinline__ T hi(Two v) { return __high2bfloat16(v); }
+};
+struct OutF16 {
+    using T = __half;
+    using Two = __half2;
+    static __device__ __forceinline__ Two two(float a, float b) { return __floats2half2_rn(a, b); }
+    static __device__ __forceinline__ T lo(Two v) { return __low2half(v); }
+    static __device__ __forceinline__ T hi(Two v) { return __high2half(v); }
+};
 
-// Call f with a value of the output type.
+// Call f with the output type's traits.
 template <class F>
 __device__ __forceinline__ void with_out_type(int type, F &&f) {
-    if (type == SGEMM_IN_BF16) f(__nv_bfloat16{});
-    else if (type == SGEMM_IN_F16) f(__half{});
-    else f(0.f);
+    if (type == SGEMM_IN_BF16) f(OutBF16{});
+    else if (type == SGEMM_IN_F16) f(OutF16{});
+    else f(OutF32{});
+}
+
+// A thread's COLS sums (one channel, COLS tokens) to C: C points at the first
+// token's element of the channel, `live` tokens exist (live <= 0: none, and a
+// channel that does not exist has none).  sa: lane l holds the scales of tokens
+// l, l + 32, ..  The whole warp takes part.  A warp whose tokens and channels all
+// exist, as in every tile but those at the edges, runs without predicates: the
+// code is unrolled over the registers that hold the sums, and its size counts
+// (it is fetched anew for every tile).
+template <class Out, int COLS>
+__device__ __forceinline__ void write_columns(typename Out::T *C, long long ldc, int live, const int (&acc)[COLS],
+                                              const float (&sa)[(COLS + 31) / 32], float sb, float bias) {
+    if (__all_sync(0xffffffffu, live >= COLS)) {
+#pragma unroll
+        for (int j = 0; j < COLS; j += 2) {
+            const float s0 = __shfl_sync(0xffffffffu, sa[j / 32], j % 32);
+            const float s1 = __shfl_sync(0xffffffffu, sa[j / 32], j % 32 + 1);
+            const typename Out::Two v =
+                Out::two(int8_value(acc[j], sb, s0, bias), int8_value(acc[j + 1], sb, s1, bias));
+            C[0] = Out::lo(v);
+            C[ldc] = Out::hi(v);
+            C += 2 * ldc;
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < COLS; j += 2) {
+        const float s0 = __shfl_sync(0xffffffffu, sa[j / 32], j % 32);
+        const float s1 = __shfl_sync(0xffffffffu, sa[j / 32], j % 32 + 1);
+        const typename Out::Two v = Out::two(int8_value(acc[j], sb, s0, bias), int8_value(acc[j + 1], sb, s1, bias));
+        if (j < live) C[0] = Out::lo(v);
+        if (j + 1 < live) C[ldc] = Out::hi(v);
+        C += 2 * ldc;
+    }
 }
 
 // offsets[e], kept within the rows there are (whatever the array holds).
@@ -139,9 +188,9 @@ __global__ void __launch_bounds__(256) int8_generic_kernel(const Int8Args a) {
                 }
                 __syncthreads();
             }
-            with_out_type(a.out_type, [&](auto zero) {
-                using T = decltype(zero);
-                T *C = static_cast<T *>(a.C);
+            with_out_type(a.out_type, [&](auto out) {
+                using Out = decltype(out);
+                auto *C = static_cast<typename Out::T *>(a.C);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = m0 + ty + 16 * i;
@@ -152,8 +201,9 @@ __global__ void __launch_bounds__(256) int8_generic_kernel(const Int8Args a) {
                         const int ch = n0 + tx + 16 * j;
                         if (ch >= a.N) continue;
                         const long long at = static_cast<long long>(e) * a.N + ch;
-                        C[static_cast<long long>(row) * a.ldc + ch] = int8_out<T>(
-                            int8_value(acc[i][j], __ldg(a.scaleB + at), sa, a.bias ? __ldg(a.bias + at) : 0.f));
+                        const float v =
+                            int8_value(acc[i][j], __ldg(a.scaleB + at), sa, a.bias ? __ldg(a.bias + at) : 0.f);
+                        C[static_cast<long long>(row) * a.ldc + ch] = Out::lo(Out::two(v, 0.f));
                     }
                 }
             });
@@ -185,24 +235,44 @@ __device__ __forceinline__ uint4 load_int8x16(const int8_t *p, int n, bool vec) 
 }
 
 // 16 k a thread; ldd is a multiple of 64, so its rows divide into whole threads.
+// peaks[block]: the largest sum of |a| over the 512 k (of one row, or the end of
+// one and the start of the next) that a warp of the block converts at a time.
 __global__ void __launch_bounds__(256)
 int8_to_f16_kernel(const int8_t *__restrict__ A, long long lda, int rows, int K, uint4 *__restrict__ dst, int ldd,
-                   int vec) {
+                   int vec, int *__restrict__ peaks) {
+    __shared__ int part[8];
     griddep_wait();
     griddep_launch_dependents();
     const int per_row = ldd / 16;
     const long long total = static_cast<long long>(rows) * per_row;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const long long row = div_floor(i, per_row);
-        const int k = static_cast<int>(i - row * per_row) * 16;
-        const uint4 v = k < K ? load_int8x16(A + row * lda + k, K - k, vec) : make_uint4(0, 0, 0, 0);
-        uint4 o0, o1;
-        int8x4_to_f16(v.x, o0.x, o0.y);
-        int8x4_to_f16(v.y, o0.z, o0.w);
-        int8x4_to_f16(v.z, o1.x, o1.y);
-        int8x4_to_f16(v.w, o1.z, o1.w);
-        dst[2 * i] = o0;
-        dst[2 * i + 1] = o1;
+    int top = 0;
+    for (long long i0 = blockIdx.x * 256ll; i0 < total; i0 += gridDim.x * 256ll) {
+        const long long i = i0 + threadIdx.x;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i < total) {
+            const long long row = div_floor(i, per_row);
+            const int k = static_cast<int>(i - row * per_row) * 16;
+            if (k < K) v = load_int8x16(A + row * lda + k, K - k, vec);
+            uint4 o0, o1;
+            int8x4_to_f16(v.x, o0.x, o0.y);
+            int8x4_to_f16(v.y, o0.z, o0.w);
+            int8x4_to_f16(v.z, o1.x, o1.y);
+            int8x4_to_f16(v.w, o1.z, o1.w);
+            dst[2 * i] = o0;
+            dst[2 * i + 1] = o1;
+        }
+        unsigned sum = 0;  // |-128| is the byte 128 to an unsigned dot product
+        sum = __dp4a(__vabs4(v.x), 0x01010101u, sum);
+        sum = __dp4a(__vabs4(v.y), 0x01010101u, sum);
+        sum = __dp4a(__vabs4(v.z), 0x01010101u, sum);
+        sum = __dp4a(__vabs4(v.w), 0x01010101u, sum);
+        top = max(top, static_cast<int>(__reduce_add_sync(0xffffffffu, sum)));
+    }
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) top = max(top, part[w]);
+        peaks[blockIdx.x] = top;
     }
 }
 
@@ -268,7 +338,7 @@ int8_transpose_kernel(const int8_t *__restrict__ B, long long ldb, long long str
 // ---- tensor-core kernel -----------------------------------------------------------
 constexpr int kBBytes = kI8TileN * kI8StageK;  // 16 KiB of B a stage
 constexpr int kAStages = 4, kACols = kI8StageK / 2;  // stages of B in tensor memory, 32-bit columns each
-constexpr int kChunk = 8;                       // stages (1024 k) between drains of an accumulator
+constexpr int kChunk = 8;                       // stages (1024 k) whose sums fit an accumulator whatever the data
 constexpr int kConvWGs = 2;                     // warpgroups that convert B, alternate stages
 constexpr uint32_t kI8TmemCols = 512;
 constexpr int kMaxStages = 10;
@@ -287,6 +357,7 @@ struct I8Shared {
     uint32_t tmem_base;
     int abort;
     int units;                    // units of this launch
+    int chunk;                    // stages between drains of an accumulator
     int bound[kMaxExperts + 1];   // first row of each expert, nondecreasing
     int tiles[kMaxExperts + 1];   // token tiles of the experts before
 };
@@ -403,6 +474,21 @@ __device__ __forceinline__ void sum_tiles(Shared *sh, const Int8Args &a, int nt,
     }
 }
 
+// Stages between drains, from the tokens' own size.  int8_to_f16_kernel leaves in
+// peaks the largest sum of |a| over any 512 consecutive k that one of its warps
+// saw; a run of c * 512 k touches at most c + 1 of those windows and |b| <= 128,
+// so no partial sum over it exceeds 128 * (c + 1) * peak, and up to 2^24 FP32
+// holds it exactly.  Real activations stay well below 127 on average (a normal
+// distribution quantized to its largest value: 4096 k and more), which leaves
+// an eighth to a quarter of the drains; data at the extremes gets 1024 k.  An
+// even number, for the pair kernel's two stages at a time.  One warp.
+__device__ __forceinline__ int chunk_of(const Int8Args &a, int lane) {
+    int top = 1;
+    for (int i = lane; i < a.n_peaks; i += 32) top = max(top, __ldcg(a.peaks + i));
+    top = __reduce_max_sync(0xffffffffu, top);
+    return max(((1 << 17) / top - 1) * (512 / kI8StageK) & ~1, kChunk);
+}
+
 template <int NT, bool SPLIT, bool DIRECT>
 __global__ void __launch_bounds__(I8Cfg<NT, SPLIT, DIRECT>::kThreads, 1)
 int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA, const Int8Args a) {
@@ -454,6 +540,10 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 2) sum_tiles(sh, a, NT, ch_tiles, lane);
+    if (!DIRECT && warp == 3) {
+        const int c = chunk_of(a, lane);
+        if (lane == 0) sh->chunk = c;
+    }
     tc::fence_before_sync();
     __syncthreads();
     if (SPLIT) cluster_sync();  // every CTA runs before another writes into it
@@ -461,7 +551,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem_base, 0);
     const uint32_t tmem_a = tmem + 2 * NT;
     volatile int *abort_flag = &sh->abort;
-    const int units = sh->units;
+    const int units = sh->units, chunk_stages = DIRECT ? kChunk : sh->chunk;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
@@ -503,9 +593,10 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
         int it = 0, chunk = 0;
         bool ok = true;
         for (int u = first_unit; u < units; u += unit_step) {
+            int run = 0;  // stages in the accumulator so far
             for (int i = kb; i < ke && ok; ++i, ++it) {
                 const int x = it % SX, t = it % kAStages, d = chunk & 1;
-                const bool start = (i - kb) % kChunk == 0, end = i + 1 == ke || (i + 1 - kb) % kChunk == 0;
+                const bool start = run == 0, end = i + 1 == ke || run + 1 == chunk_stages;
                 ok = (!start || chunk < 2 || wait(&sh->dempty[d], (chunk / 2 - 1) & 1)) &&
                      wait(&sh->xfull[x], (it / SX) & 1) && wait(&sh->afull[t], (it / kAStages) & 1);
                 ok = __all_sync(0xffffffffu, ok);
@@ -523,6 +614,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                     if (end) tc::commit(&sh->dfull[d]);
                 }
                 __syncwarp();
+                run = end ? 0 : run + 1;
                 if (end) ++chunk;
             }
             if (SPLIT) {
@@ -689,7 +781,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             int acc[Cf::kCols];
 #pragma unroll
             for (int j = 0; j < Cf::kCols; ++j) acc[j] = 0;
-            for (int i = kb; i < ke && ok; i += kChunk, ++chunk) {
+            for (int i = kb; i < ke && ok; i += chunk_stages, ++chunk) {
                 const int d = chunk & 1;
                 ok = __all_sync(0xffffffffu, wait(&sh->dfull[d], (chunk / 2) & 1));
                 if (!ok) break;
@@ -701,15 +793,10 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             }
             if (!SPLIT) {
                 if (ok)
-                    with_out_type(a.out_type, [&](auto zero) {
-                        using T = decltype(zero);
-                        T *C = static_cast<T *>(a.C) + static_cast<long long>(first) * a.ldc + n;
-#pragma unroll
-                        for (int j = 0; j < Cf::kCols; ++j) {
-                            const float s = __shfl_sync(0xffffffffu, sa[j / 32], j % 32);
-                            if (first + j < q.tend && n < a.N)
-                                C[static_cast<long long>(j) * a.ldc] = int8_out<T>(int8_value(acc[j], sb, s, bias));
-                        }
+                    with_out_type(a.out_type, [&](auto out) {
+                        using Out = decltype(out);
+                        write_columns<Out>(static_cast<typename Out::T *>(a.C) + static_cast<long long>(first) * a.ldc + n,
+                                           a.ldc, n < a.N ? q.tend - first : 0, acc, sa, sb, bias);
                     });
             } else {
                 // column j belongs to CTA j / per of the cluster
@@ -728,9 +815,9 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                 __syncwarp();
                 cluster_sync();
                 if (ok)
-                    with_out_type(a.out_type, [&](auto zero) {
-                        using T = decltype(zero);
-                        T *C = static_cast<T *>(a.C) + static_cast<long long>(first) * a.ldc + n;
+                    with_out_type(a.out_type, [&](auto out) {
+                        using Out = decltype(out);
+                        auto *C = static_cast<typename Out::T *>(a.C) + static_cast<long long>(first) * a.ldc + n;
                         for (int c0 = 0; c0 < per; c0 += 8) {
                             int sum[8] = {};
                             for (int r = 0; r < splits; ++r)
@@ -742,7 +829,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                                 const float s = __shfl_sync(0xffffffffu, sa[0], (c0 + c) & 31);
                                 if (c0 + c < per && first + c0 + c < q.tend && n < a.N)
                                     C[static_cast<long long>(c0 + c) * a.ldc] =
-                                        int8_out<T>(int8_value(sum[c], sb, s, bias));
+                                        Out::lo(Out::two(int8_value(sum[c], sb, s, bias), 0.f));
                             }
                         }
                     });
@@ -782,7 +869,7 @@ struct PairShared {
     uint64_t drained;
     uint32_t tmem_base;
     int abort;
-    int units;
+    int units, chunk;
     int bound[kMaxExperts + 1];
     int tiles[kMaxExperts + 1];
 };
@@ -842,6 +929,10 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 2) sum_tiles(sh, a, kPairT, ch_tiles, lane);
+    if (warp == 3) {
+        const int c = chunk_of(a, lane);
+        if (lane == 0) sh->chunk = c;
+    }
     tc::fence_before_sync();
     __syncthreads();
     tc::cluster_sync_all();  // both CTAs' barriers are initialised before any cross-CTA arrive
@@ -849,7 +940,7 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem_base, 0);
     const uint32_t tmem_a = tmem + kPairT;
     volatile int *abort_flag = &sh->abort;
-    const int units = sh->units;
+    const int units = sh->units, chunk_stages = sh->chunk;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
@@ -888,9 +979,10 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
                 // both for half 1, so that at the end of 1024 k either half has the
                 // time of 16 MMAs (1024 cycles) to be drained in while the other
                 // is added to.
+                int run = 0;  // stages in the accumulators so far
                 for (int i = 0; i < kt; i += 2) {
                     const int two = i + 1 < kt ? 2 : 1;
-                    const bool start = i % kChunk == 0, end = i + two == kt || (i + two) % kChunk == 0;
+                    const bool start = run == 0, end = i + two == kt || run + two == chunk_stages;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         ok = ok && (!start || chunk == 0 || wait(&sh->dempty[h], (chunk - 1) & 1));
@@ -921,6 +1013,7 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
                     }
                     if (!ok) break;
                     it += two;
+                    run = end ? 0 : run + two;
                     if (end) ++chunk;
                 }
             }
@@ -1034,7 +1127,7 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             int acc[kCols];
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] = 0;
-            for (int i = 0; i < kt; i += kChunk, ++chunk) {
+            for (int i = 0; i < kt; i += chunk_stages, ++chunk) {
                 ok = __all_sync(0xffffffffu, wait(&sh->dfull[h], chunk & 1));
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -1044,15 +1137,10 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
                 if (lane == 0) tc::mbar_arrive_remote(dempty);
             }
             if (ok)
-                with_out_type(a.out_type, [&](auto zero) {
-                    using T = decltype(zero);
-                    T *C = static_cast<T *>(a.C) + static_cast<long long>(first) * a.ldc + n;
-#pragma unroll
-                    for (int j = 0; j < kCols; ++j) {
-                        const float s = __shfl_sync(0xffffffffu, sa[j / 32], j % 32);
-                        if (first + j < q.tend && n < a.N)
-                            C[static_cast<long long>(j) * a.ldc] = int8_out<T>(int8_value(acc[j], sb, s, bias));
-                    }
+                with_out_type(a.out_type, [&](auto out) {
+                    using Out = decltype(out);
+                    write_columns<Out>(static_cast<typename Out::T *>(a.C) + static_cast<long long>(first) * a.ldc + n,
+                                       a.ldc, n < a.N ? q.tend - first : 0, acc, sa, sb, bias);
                 });
         }
     }
@@ -1135,12 +1223,13 @@ cudaError_t launch_int8_generic(const Int8Args &a, cudaStream_t stream) {
     return launch_dependent(int8_generic_kernel, grid, dim3(256), 0, stream, 1, a);
 }
 
-cudaError_t launch_int8_to_f16(const int8_t *A, long long lda, int rows, int K, void *dst, int ldd,
-                               cudaStream_t stream) {
+cudaError_t launch_int8_to_f16(const int8_t *A, long long lda, int rows, int K, void *dst, int ldd, int *peaks,
+                               int *n_peaks, cudaStream_t stream) {
     const int vec = reinterpret_cast<uintptr_t>(A) % 16 == 0 && lda % 16 == 0;
     const long long blocks = (static_cast<long long>(rows) * (ldd / 16) + 255) / 256;
-    return launch_dependent(int8_to_f16_kernel, dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20))),
-                            dim3(256), 0, stream, 1, A, lda, rows, K, static_cast<uint4 *>(dst), ldd, vec);
+    *n_peaks = static_cast<int>(blocks < kI8Peaks ? blocks : kI8Peaks);
+    return launch_dependent(int8_to_f16_kernel, dim3(*n_peaks), dim3(256), 0, stream, 1, A, lda, rows, K,
+                            static_cast<uint4 *>(dst), ldd, vec, peaks);
 }
 
 cudaError_t launch_int8_relayout(const int8_t *B, long long ldb, long long strideB, int trans, int experts, int N,

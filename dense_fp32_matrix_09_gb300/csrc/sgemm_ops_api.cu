@@ -131,7 +131,8 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
     size_t room = v.rl_bytes;
     const bool as_stored = transB && aligned(B, 16) && ldb % 16 == 0 && (experts == 1 || strideB % 16 == 0);
     const size_t b_bytes = as_stored ? 0 : static_cast<size_t>(experts) * N * kb;
-    const size_t b_room = (b_bytes + 1023) / 1024 * 1024;
+    const size_t peak_room = direct ? 0 : sg::kI8Peaks * sizeof(int);
+    const size_t b_room = (b_bytes + 1023) / 1024 * 1024 + peak_room;
     bool tc = v.pinned != SGEMM_VARIANT_GENERIC && v.pinned != SGEMM_VARIANT_GENERIC_I8 && K > 0 &&
               ((as_stored && a_as_stored) || ws != nullptr) && (as_stored || v.relayout_mode != SGEMM_RELAYOUT_OFF) &&
               b_room <= room && room - b_room >= a_row * std::min(rows, a.nt);
@@ -147,6 +148,7 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
         a.ksplit = direct ? split_of(tiles, static_cast<int>(cdiv(K, sg::kI8StageK)), v.num_sms) : 1;
     }
     CUtensorMap tmB, tmA{};
+    int *peaks = nullptr;
     if (tc) {
         if (!as_stored) {
             const cudaError_t e =
@@ -159,6 +161,7 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
             a.strideB = static_cast<long long>(N) * kb;
             a.transB = 1;
         }
+        if (!direct) a.peaks = peaks = reinterpret_cast<int *>(ws + b_room - peak_room);
         ws += b_room;
         // a single matrix has any (aligned) matrix stride
         const long long stride = experts > 1 ? a.strideB : a.ldb * static_cast<long long>(N);
@@ -177,7 +180,7 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
             const int8_t *src = A + static_cast<long long>(r0) * lda;
             cudaError_t e = cudaSuccess;
             if (!direct) {
-                e = sg::launch_int8_to_f16(src, lda, a.rows, K, ws, kp, stream);
+                e = sg::launch_int8_to_f16(src, lda, a.rows, K, ws, kp, peaks, &a.n_peaks, stream);
             } else if (!a_as_stored) {
                 e = sg::launch_int8_relayout(src, lda, 0, 1, 1, a.rows, K, reinterpret_cast<int8_t *>(ws), kb, stream);
             }
