@@ -278,11 +278,19 @@ cudaError_t launch_int8_to_f16(const int8_t *A, long long lda, int rows, int K, 
 cudaError_t launch_int8_relayout(const int8_t *B, long long ldb, long long strideB, int trans, int experts, int N,
                                  int K, int8_t *dst, int ldd, cudaStream_t stream);
 constexpr int kI8TileN = 128, kI8StageK = 128;  // channels and k of one B stage (TMA box, 128-byte swizzle)
-constexpr int kI8TokenTiles[] = {16, 32, 64, 128, 256};  // 256: CTA pairs, 256 channels
+// Token tiles: up to 64 by one CTA (or a cluster that splits K), 128 and 256 by CTA
+// pairs with 256 channels.
+constexpr int kI8TokenTiles[] = {16, 32, 64, 128, 256};
+// The most tiles of nt tokens that `rows` rows of `experts` experts make (the
+// experts' row counts are on the device).
+constexpr long long int8_most_tiles(int rows, int experts, int nt) {
+    return experts == 1 ? (rows + static_cast<long long>(nt) - 1) / nt
+                        : static_cast<long long>(rows) / nt + (experts < rows ? experts : rows);
+}
 cudaError_t int8_prepare();
 // tmB: int8, 3-D (k, channel, expert), box 128 x 128 x 1; tmA: 2-D (k, row - row0),
-// for nt <= 64 int8, box 128 x nt, else FP16, box 64 x nt (64 x 64 for nt = 256); both
-// with the 128-byte swizzle.
+// for nt <= 64 int8, box 128 x nt, else FP16, box 64 x (nt / 4); both with the
+// 128-byte swizzle.
 cudaError_t launch_int8_tc(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
                            int smem_override, cudaStream_t stream);
 

@@ -335,61 +335,28 @@ int8_transpose_kernel(const int8_t *__restrict__ B, long long ldb, long long str
     }
 }
 
-// ---- tensor-core kernel -----------------------------------------------------------
+// ---- tensor-core kernels -----------------------------------------------------------
 constexpr int kBBytes = kI8TileN * kI8StageK;  // 16 KiB of B a stage
-constexpr int kAStages = 4, kACols = kI8StageK / 2;  // stages of B in tensor memory, 32-bit columns each
-constexpr int kChunk = 8;                       // stages (1024 k) whose sums fit an accumulator whatever the data
-constexpr int kConvWGs = 2;                     // warpgroups that convert B, alternate stages
-constexpr uint32_t kI8TmemCols = 512;
-constexpr int kMaxStages = 10;
-constexpr int kSmemLimit = 232448;
+constexpr int kACols = kI8StageK / 2;          // 32-bit columns of tensor memory that hold a stage of B
+constexpr int kChunk = 8;                      // stages (1024 k) whose sums fit an accumulator whatever the data
+constexpr int kSmemLimit = 232448;             // dynamic shared memory of a CTA that has the SM to itself
 
-struct I8Shared {
-    uint64_t bfull[kMaxStages];   // B (DIRECT: and the tokens' int8) of the stage has landed
-    uint64_t bempty[kMaxStages];  // a warpgroup's four warps (DIRECT: and four more) have read it
-    uint64_t xfull[kMaxStages];   // the tokens of the stage stand in shared memory
-    uint64_t xempty[kMaxStages];  // the MMAs have read them
-    uint64_t afull[kAStages];     // the stage's B stands in tensor memory (four warps)
-    uint64_t aempty[kAStages];    // the MMAs that read it have finished
-    uint64_t dfull[2];            // an accumulator holds up to 1024 k
-    uint64_t dempty[2];           // it has been read
-    uint64_t drained;             // abort only: every MMA issued has finished
-    uint32_t tmem_base;
-    int abort;
-    int units;                    // units of this launch
-    int chunk;                    // stages between drains of an accumulator
-    int bound[kMaxExperts + 1];   // first row of each expert, nondecreasing
-    int tiles[kMaxExperts + 1];   // token tiles of the experts before
+// A place in a ring of stages and the parity of its current round.
+struct Ring {
+    int s = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void step(int stages) {
+        if (++s == stages) {
+            s = 0;
+            round ^= 1u;
+        }
+    }
 };
 
-// DIRECT: the tokens' int8 rows come with B's stages and are expanded to FP16
-// here, by four warps; else they are read as FP16 by TMA.
-template <int NT, bool SPLIT, bool DIRECT>
-struct I8Cfg {
-    static constexpr int kXBytes = NT * kI8StageK * 2;
-    static constexpr int kXchg = SPLIT ? kI8TileN * NT * 4 : 0;  // partial sums from the cluster's CTAs
-    static constexpr int kFree = kSmemLimit - 1024 - static_cast<int>(sizeof(I8Shared)) - kXchg;
-    static constexpr int kStage = kBBytes + (DIRECT ? NT * kI8StageK : 0);
-    // Rings: up to 32 KiB of FP16 tokens (at least two stages, three where TMA
-    // fetches them from L2), and the stages of B in what is left.  An even
-    // number of B's stages, so that a converting warpgroup sees every phase of
-    // the stages it reads: the parity of a phase tells it from the one before
-    // only.
-    static constexpr int kXStages = !DIRECT ? 3 : 32768 / kXBytes < 4 ? 32768 / kXBytes : 4;
-    static constexpr int kBFit = (kFree - kXStages * kXBytes) / kStage / 2 * 2;
-    static constexpr int kBStages = kBFit < kMaxStages ? kBFit : kMaxStages;
-    static constexpr int kRing = kBStages * kStage + kXStages * kXBytes;
-    static constexpr int kSmem = 1024 + kRing + kXchg + static_cast<int>(sizeof(I8Shared));
-    static constexpr int kEpiWGs = NT > 64 ? 2 : 1;
-    static constexpr int kCols = NT / kEpiWGs;  // accumulator columns a thread drains
-    static constexpr int kWarpX = 4, kWarpConv = kWarpX + (DIRECT ? 4 : 0), kWarpEpi = kWarpConv + 4 * kConvWGs;
-    static constexpr int kThreads = 32 * (kWarpEpi + 4 * kEpiWGs);
-    static constexpr int kPieces = NT / 16;              // 16-byte pieces of a stage's tokens a thread expands
-    static_assert(2 * NT + kAStages * kACols <= static_cast<int>(kI8TmemCols), "tensor memory");
-    static_assert(kBStages >= 4 && kBStages % kConvWGs == 0 && kXStages >= 2 && kXStages <= kMaxStages, "rings");
-    static_assert(!SPLIT || (kEpiWGs == 1 && NT / 2 <= 32), "a lane holds a token scale");
-    static_assert(kAStages % kConvWGs == 0 && kSmem <= kSmemLimit, "shared memory");
-};
+template <int R>
+__device__ __forceinline__ void regs_fewer() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // acc[j] += column j of an accumulator (integers): the load of the next 16
 // columns is in flight while 16 are converted.
@@ -414,30 +381,30 @@ struct I8Unit {
 // Unit u of tiles of NT tokens x CH channels: the expert by bisection of the
 // tile counts; within the expert groups of 2048 tokens or 16 tiles, channel
 // tiles outer and token tiles inner.
-template <int NT, int CH, class Shared>
-__device__ __forceinline__ I8Unit unit_of(const Shared *sh, const Int8Args &a, int ch_tiles, int u) {
+template <int NT, int CH>
+__device__ __forceinline__ I8Unit unit_of(const int *bound, const int *tiles, const Int8Args &a, int ch_tiles, int u) {
     int lo = 0, hi = a.experts;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (sh->tiles[mid] * ch_tiles <= u) lo = mid; else hi = mid;
+        if (tiles[mid] * ch_tiles <= u) lo = mid; else hi = mid;
     }
     constexpr int kGroup = 2048 / NT < 16 ? 2048 / NT : 16;
-    const int mine = sh->tiles[lo + 1] - sh->tiles[lo];
-    const int l = u - sh->tiles[lo] * ch_tiles;
+    const int mine = tiles[lo + 1] - tiles[lo];
+    const int l = u - tiles[lo] * ch_tiles;
     const int grp = l / (kGroup * ch_tiles), first = grp * kGroup;
     const int rows = min(mine - first, kGroup);
     const int r = l - grp * kGroup * ch_tiles;
     I8Unit q;
     q.e = lo;
     q.ch0 = r / rows * CH;
-    q.t0 = max(sh->bound[lo], a.row0) + (first + r % rows) * NT;
-    q.tend = min(sh->bound[lo + 1], a.row0 + a.rows);
+    q.t0 = max(bound[lo], a.row0) + (first + r % rows) * NT;
+    q.tend = min(bound[lo + 1], a.row0 + a.rows);
     return q;
 }
 
-// One warp: the experts' first rows and the sums of their token tiles.
-template <class Shared>
-__device__ __forceinline__ void sum_tiles(Shared *sh, const Int8Args &a, int nt, int ch_tiles, int lane) {
+// One warp: bound[e], the experts' first rows (nondecreasing), and tiles[e], the
+// token tiles of the experts before e (experts + 1 of each); returns all of them.
+__device__ __forceinline__ int sum_tiles(int *bound, int *tiles, const Int8Args &a, int nt, int lane) {
     int top = 0, sum = 0;
     for (int e0 = 0; e0 <= a.experts; e0 += 32) {
         const int e = e0 + lane;
@@ -448,7 +415,7 @@ __device__ __forceinline__ void sum_tiles(Shared *sh, const Int8Args &a, int nt,
             const int up = __shfl_up_sync(0xffffffffu, b, d);
             if (lane >= d) b = max(b, up);
         }
-        if (e <= a.experts) sh->bound[e] = b;
+        if (e <= a.experts) bound[e] = b;
         top = __shfl_sync(0xffffffffu, b, 31);
     }
     __syncwarp();
@@ -456,7 +423,7 @@ __device__ __forceinline__ void sum_tiles(Shared *sh, const Int8Args &a, int nt,
         const int e = e0 + lane;
         int n = 0;
         if (e < a.experts) {
-            const int lo = max(sh->bound[e], a.row0), hi = min(sh->bound[e + 1], a.row0 + a.rows);
+            const int lo = max(bound[e], a.row0), hi = min(bound[e + 1], a.row0 + a.rows);
             n = hi > lo ? (hi - lo + nt - 1) / nt : 0;
         }
         int s = n;
@@ -465,13 +432,11 @@ __device__ __forceinline__ void sum_tiles(Shared *sh, const Int8Args &a, int nt,
             const int up = __shfl_up_sync(0xffffffffu, s, d);
             if (lane >= d) s += up;
         }
-        if (e < a.experts) sh->tiles[e] = sum + s - n;
+        if (e < a.experts) tiles[e] = sum + s - n;
         sum += __shfl_sync(0xffffffffu, s, 31);
     }
-    if (lane == 0) {
-        sh->tiles[a.experts] = sum;
-        sh->units = sum * ch_tiles;
-    }
+    if (lane == 0) tiles[a.experts] = sum;
+    return sum;
 }
 
 // Stages between drains, from the tokens' own size.  int8_to_f16_kernel leaves in
@@ -489,16 +454,85 @@ __device__ __forceinline__ int chunk_of(const Int8Args &a, int lane) {
     return max(((1 << 17) / top - 1) * (512 / kI8StageK) & ~1, kChunk);
 }
 
-template <int NT, bool SPLIT, bool DIRECT>
-__global__ void __launch_bounds__(I8Cfg<NT, SPLIT, DIRECT>::kThreads, 1)
+// 128 k of this thread's channel (128 bytes) as FP16 into 64 columns of its lane
+// of tensor memory (whole warp; the stores are still to be waited for).
+__device__ __forceinline__ void expand_to_tmem(const uint4 (&w)[8], uint32_t taddr) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t o[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            int8x4_to_f16(w[h * 4 + c].x, o[c * 8 + 0], o[c * 8 + 1]);
+            int8x4_to_f16(w[h * 4 + c].y, o[c * 8 + 2], o[c * 8 + 3]);
+            int8x4_to_f16(w[h * 4 + c].z, o[c * 8 + 4], o[c * 8 + 5]);
+            int8x4_to_f16(w[h * 4 + c].w, o[c * 8 + 6], o[c * 8 + 7]);
+        }
+        tc::tmem_st32(taddr + h * 32, o);
+    }
+}
+
+// ---- up to 64 tokens a tile: 128 channels x NT tokens, two CTAs an SM -----------------
+// Four warpgroup-sized parts in 12 warps, so that two CTAs share an SM: each
+// hides the other's waits, and the next call's CTAs set themselves up while
+// the last ones of this call finish.
+constexpr int kMaxStages = 6, kXStages = 2, kAStages = 2;
+constexpr int kDirectThreads = 384;
+constexpr uint32_t kDirectTmemCols = 256;
+// Two CTAs an SM: half of its 228 KiB less 1 KiB each that the system reserves.
+constexpr int kHalfSmem = 233472 / 2 - 1024;
+
+struct DirectShared {
+    uint64_t full[kMaxStages];    // B and the tokens' int8 of the stage have landed
+    uint64_t empty[kMaxStages];   // four warps have read B, two the tokens
+    uint64_t xfull[kXStages];     // the stage's tokens stand in shared memory as FP16 (two warps)
+    uint64_t xempty[kXStages];    // the MMAs have read them
+    uint64_t afull[kAStages];     // the stage's B stands in tensor memory (four warps)
+    uint64_t aempty[kAStages];    // the MMAs have read it
+    uint64_t dfull[2];            // an accumulator holds up to 1024 k
+    uint64_t dempty[2];           // it has been read (four warps)
+    uint64_t xchg_read;           // the cluster's partial sums have been read (four warps)
+    uint64_t drained;             // abort only: every MMA issued has finished
+    uint32_t tmem_base;
+    int abort;
+    int units;                    // units of this launch
+    // then bound[experts + 1], tiles[experts + 1]
+};
+
+template <int NT, bool SPLIT>
+struct DirectCfg {
+    static constexpr int kStage = kBBytes + NT * kI8StageK;
+    static constexpr int kXBytes = NT * kI8StageK * 2;
+    // The partial sums from the cluster's CTAs: in place of the FP16 tokens, which
+    // are done with by then, except in the narrowest tile, whose 8 KiB fit beside.
+    static constexpr int kXchgBytes = SPLIT ? kI8TileN * NT * 4 : 0;
+    static constexpr bool kXchgOwn = NT == 16;
+    static constexpr int kFixed = 1024 + kXStages * kXBytes + (kXchgOwn ? kXchgBytes : 0) + static_cast<int>(sizeof(DirectShared));
+    static constexpr int kFit = (kHalfSmem - kFixed - 64) / kStage;
+    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+    static constexpr int smem(int experts) { return kFixed + kStages * kStage + 2 * 4 * (experts + 1); }
+    // Registers (80 a thread at launch): a thread of the widest tile's epilogue
+    // holds 64 sums.
+    static constexpr bool kRegs = NT == 64;
+    static constexpr int kRegsControl = 56, kRegsEpilogue = 104;
+    static_assert(kXchgOwn || kXchgBytes <= kXStages * kXBytes, "partial sums");
+    static_assert(2 * NT + kAStages * kACols <= static_cast<int>(kDirectTmemCols), "tensor memory");
+    static_assert(kStages >= 3, "shared memory");
+    static_assert(!kRegs || kRegsControl + 80 + kRegsEpilogue <= 3 * 80, "register split");
+    static_assert(!SPLIT || NT / 2 <= 32, "a lane holds a token scale");
+};
+
+template <int NT, bool SPLIT>
+__global__ void __launch_bounds__(kDirectThreads, 2)
 int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA, const Int8Args a) {
-    using Cf = I8Cfg<NT, SPLIT, DIRECT>;
-    constexpr int SB = Cf::kBStages, SX = Cf::kXStages;
+    using Cf = DirectCfg<NT, SPLIT>;
+    constexpr int S = Cf::kStages;
     extern __shared__ uint8_t smem_raw[];
-    const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-    uint8_t *ring_b = smem_raw + pad, *ring_x = ring_b + SB * Cf::kStage;
-    int *xchg = reinterpret_cast<int *>(ring_b + Cf::kRing);
-    I8Shared *sh = reinterpret_cast<I8Shared *>(ring_b + Cf::kRing + Cf::kXchg);
+    const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;  // the same in every CTA
+    uint8_t *ring = smem_raw + pad, *ring_x = ring + S * Cf::kStage;
+    uint8_t *after = ring_x + kXStages * Cf::kXBytes;
+    int *xchg = reinterpret_cast<int *>(Cf::kXchgOwn ? after : ring_x);
+    DirectShared *sh = reinterpret_cast<DirectShared *>(after + (Cf::kXchgOwn ? Cf::kXchgBytes : 0));
+    int *bound = reinterpret_cast<int *>(sh + 1), *tiles = bound + a.experts + 1;
     // warp number and tensor-memory address through a shuffle: uniform to the compiler too
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int splits = SPLIT ? a.ksplit : 1;
@@ -511,22 +545,19 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
     const int kb = SPLIT ? rank * kt / splits : 0, ke = SPLIT ? (rank + 1) * kt / splits : kt;
 
     if (tid == 0) {
-        for (int s = 0; s < SB; ++s) {
-            mbar_init(&sh->bfull[s], 1);
-            mbar_init(&sh->bempty[s], DIRECT ? 8 : 4);
-        }
-        for (int s = 0; s < SX; ++s) {
-            mbar_init(&sh->xfull[s], DIRECT ? 4 : 1);
-            mbar_init(&sh->xempty[s], 1);
-        }
-        for (int s = 0; s < kAStages; ++s) {
-            mbar_init(&sh->afull[s], 4);
-            mbar_init(&sh->aempty[s], 1);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], 4 + 2);
         }
         for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh->xfull[s], 2);
+            mbar_init(&sh->xempty[s], 1);
+            mbar_init(&sh->afull[s], 4);
+            mbar_init(&sh->aempty[s], 1);
             mbar_init(&sh->dfull[s], 1);
-            mbar_init(&sh->dempty[s], 4 * Cf::kEpiWGs);
+            mbar_init(&sh->dempty[s], 4);
         }
+        mbar_init(&sh->xchg_read, 4);
         mbar_init(&sh->drained, 1);
         sh->abort = 0;
         fence_barrier_init();
@@ -534,24 +565,22 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
         prefetch_tensormap(&tmA);
     }
     if (warp == 1) {
-        tc::tmem_alloc(&sh->tmem_base, kI8TmemCols);
+        tc::tmem_alloc(&sh->tmem_base, kDirectTmemCols);
         tc::tmem_relinquish();
     }
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 2) sum_tiles(sh, a, NT, ch_tiles, lane);
-    if (!DIRECT && warp == 3) {
-        const int c = chunk_of(a, lane);
-        if (lane == 0) sh->chunk = c;
+    if (warp == 2) {
+        const int n = sum_tiles(bound, tiles, a, NT, lane);
+        if (lane == 0) sh->units = n * ch_tiles;
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (SPLIT) cluster_sync();  // every CTA runs before another writes into it
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem_base, 0);
     const uint32_t tmem_a = tmem + 2 * NT;
     volatile int *abort_flag = &sh->abort;
-    const int units = sh->units, chunk_stages = DIRECT ? kChunk : sh->chunk;
+    const int units = sh->units;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
@@ -559,150 +588,133 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
         *abort_flag = 1;
         return false;
     };
+    // Every thread of the cluster passes two barriers a unit: every CTA is ready
+    // for the others' partial sums; all partial sums have been sent.
+    auto pass_exchange = [&]() {
+        if (SPLIT) {
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
+        }
+    };
 
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer
-        int it = 0;
-        bool ok = true;
-        for (int u = first_unit; u < units; u += unit_step) {
-            if (lane == 0 && ok) {
-                const I8Unit q = unit_of<NT, kI8TileN>(sh, a, ch_tiles, u);
-                for (int i = kb; i < ke; ++i, ++it) {
-                    const int s = it % SB;
-                    if (it >= SB && !wait(&sh->bempty[s], (it / SB - 1) & 1)) { ok = false; break; }
-                    uint8_t *st = ring_b + s * Cf::kStage;
-                    mbar_arrive_expect_tx(&sh->bfull[s], Cf::kStage);
-                    tma_load_3d(st, &tmB, &sh->bfull[s], i * kI8StageK, q.ch0, q.e);
-                    if (DIRECT) tma_load_2d(st + kBBytes, &tmA, &sh->bfull[s], i * kI8StageK, q.t0 - a.row0);
+    if (warp < 4) {
+        if (Cf::kRegs) regs_fewer<Cf::kRegsControl>();
+        if (warp == 0) {
+            // -------------------------------------------- TMA producer
+            Ring r;
+            int issued = 0;
+            bool ok = true;
+            for (int u = first_unit; u < units; u += unit_step) {
+                if (lane == 0 && ok) {
+                    const I8Unit q = unit_of<NT, kI8TileN>(bound, tiles, a, ch_tiles, u);
+                    for (int i = kb; i < ke; ++i, r.step(S), ++issued) {
+                        if (!wait(&sh->empty[r.s], r.round ^ 1u)) { ok = false; break; }
+                        uint8_t *st = ring + r.s * Cf::kStage;
+                        mbar_arrive_expect_tx(&sh->full[r.s], Cf::kStage);
+                        tma_load_3d(st, &tmB, &sh->full[r.s], i * kI8StageK, q.ch0, q.e);
+                        tma_load_2d(st + kBBytes, &tmA, &sh->full[r.s], i * kI8StageK, q.t0 - a.row0);
+                    }
                 }
+                pass_exchange();
+            }
+            if (lane == 0)  // no copy outlives the CTA
+                for (int t = max(0, issued - S); t < issued; ++t) mbar_wait(&sh->full[t % S], (t / S) & 1, a.status);
+            __syncwarp();
+        } else if (warp == 1) {
+            // -------------------------------------------- MMA issuer
+            // The whole warp walks the stages and waits; one elected lane issues.
+            constexpr uint32_t idesc = tc::idesc_f16_kmajor(kI8TileN, NT);
+            const uint64_t xdesc = tc::smem_desc(smem_u32(ring_x), 16, 1024, tc::kLayoutSwizzle128);
+            Ring x, t, d;  // stages of tokens and of B in tensor memory, accumulators
+            bool ok = true;
+            for (int u = first_unit; u < units; u += unit_step) {
+                int run = 0;  // stages in the accumulator so far
+                for (int i = kb; i < ke && ok; ++i) {
+                    const bool start = run == 0, end = i + 1 == ke || run + 1 == kChunk;
+                    ok = (!start || wait(&sh->dempty[d.s], d.round ^ 1u)) && wait(&sh->xfull[x.s], x.round) &&
+                         wait(&sh->afull[t.s], t.round);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (tc::elect_one()) {
+                        const uint64_t b = xdesc + static_cast<uint64_t>(x.s * (Cf::kXBytes / 16));
+#pragma unroll
+                        for (int kk = 0; kk < kI8StageK / 16; ++kk)
+                            tc::mma_f16_ta(tmem + d.s * NT, tmem_a + t.s * kACols + kk * 8,
+                                           b + ((kk / 4) * NT * 128 + (kk % 4) * 32) / 16, idesc,
+                                           (start && kk == 0) ? 0u : 1u);
+                        tc::commit(&sh->xempty[x.s]);
+                        tc::commit(&sh->aempty[t.s]);
+                        if (end) tc::commit(&sh->dfull[d.s]);
+                    }
+                    __syncwarp();
+                    x.step(kXStages);
+                    t.step(kAStages);
+                    run = end ? 0 : run + 1;
+                    if (end) d.step(2);
+                }
+                pass_exchange();
+            }
+            if (!ok && tc::elect_one()) {  // no teardown under a running MMA
+                tc::commit(&sh->drained);
+                mbar_wait(&sh->drained, 0, a.status);
             }
             __syncwarp();
-            if (SPLIT) {
-                cluster_sync();
-                if (u + unit_step < units) cluster_sync();
-            }
-        }
-        if (lane == 0)  // no copy outlives the CTA
-            for (int t = max(0, it - SB); t < it; ++t) mbar_wait(&sh->bfull[t % SB], (t / SB) & 1, a.status);
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer
-        // The whole warp walks the stages and waits; one elected lane issues.
-        constexpr uint32_t idesc = tc::idesc_f16_kmajor(kI8TileN, NT);
-        const uint64_t xdesc = tc::smem_desc(smem_u32(ring_x), 16, 1024, tc::kLayoutSwizzle128);
-        int it = 0, chunk = 0;
-        bool ok = true;
-        for (int u = first_unit; u < units; u += unit_step) {
-            int run = 0;  // stages in the accumulator so far
-            for (int i = kb; i < ke && ok; ++i, ++it) {
-                const int x = it % SX, t = it % kAStages, d = chunk & 1;
-                const bool start = run == 0, end = i + 1 == ke || run + 1 == chunk_stages;
-                ok = (!start || chunk < 2 || wait(&sh->dempty[d], (chunk / 2 - 1) & 1)) &&
-                     wait(&sh->xfull[x], (it / SX) & 1) && wait(&sh->afull[t], (it / kAStages) & 1);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc::fence_after_sync();
-                if (tc::elect_one()) {
-                    const uint64_t b = xdesc + static_cast<uint64_t>(x * (Cf::kXBytes / 16));
+        } else {
+            // -------------------------------------------- the tokens' rows to FP16 (two warps)
+            constexpr int kPieces = NT / 8, kBatch = kPieces < 4 ? kPieces : 4;  // 16-byte pieces of a stage a thread expands
+            const int me = tid - 64;
+            const int kc = me % 8, up = kc / 4, c = (kc % 4) * 2;  // 16 k of a row; rows me / 8, me / 8 + 8, ..
+            const int sw = (me / 8) & 7;                           // a row's place in its group of 8
+            Ring r, x;
+            int unit = 0;
+            bool ok = true;
+            for (int u = first_unit; u < units; u += unit_step, ++unit) {
+                if (SPLIT && !Cf::kXchgOwn && unit > 0)
+                    ok = __all_sync(0xffffffffu, ok && wait(&sh->xchg_read, (unit - 1) & 1));
+                for (int i = kb; i < ke && ok; ++i, r.step(S), x.step(kXStages)) {
+                    ok = wait(&sh->full[r.s], r.round) && wait(&sh->xempty[x.s], x.round ^ 1u);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint8_t *src = ring + r.s * Cf::kStage + kBBytes + (me / 8) * 128 + (kc ^ sw) * 16;
+                    uint8_t *dst = ring_x + x.s * Cf::kXBytes + up * NT * 128 + (me / 8) * 128;
 #pragma unroll
-                    for (int kk = 0; kk < kI8StageK / 16; ++kk)
-                        tc::mma_f16_ta(tmem + d * NT, tmem_a + t * kACols + kk * 8,
-                                       b + ((kk / 4) * NT * 128 + (kk % 4) * 32) / 16, idesc,
-                                       (start && kk == 0) ? 0u : 1u);
-                    tc::commit(&sh->xempty[x]);
-                    tc::commit(&sh->aempty[t]);
-                    if (end) tc::commit(&sh->dfull[d]);
-                }
-                __syncwarp();
-                run = end ? 0 : run + 1;
-                if (end) ++chunk;
-            }
-            if (SPLIT) {
-                __syncwarp();
-                cluster_sync();
-                if (u + unit_step < units) cluster_sync();
-            }
-        }
-        if (!ok && tc::elect_one()) {  // no teardown under a running MMA
-            tc::commit(&sh->drained);
-            mbar_wait(&sh->drained, 0, a.status);
-        }
-        __syncwarp();
-    } else if (!DIRECT && warp == 2) {
-        // ------------------------------------------------ TMA producer of the tokens
-        int it = 0;
-        bool ok = true;
-        for (int u = first_unit; u < units; u += unit_step) {
-            if (lane == 0 && ok) {
-                const I8Unit q = unit_of<NT, kI8TileN>(sh, a, ch_tiles, u);
-                for (int i = kb; i < ke; ++i, ++it) {
-                    const int x = it % SX;
-                    if (it >= SX && !wait(&sh->xempty[x], (it / SX - 1) & 1)) { ok = false; break; }
-                    uint8_t *st = ring_x + x * Cf::kXBytes;
-                    mbar_arrive_expect_tx(&sh->xfull[x], Cf::kXBytes);
-                    tma_load_2d(st, &tmA, &sh->xfull[x], i * kI8StageK, q.t0 - a.row0);
-                    tma_load_2d(st + NT * 128, &tmA, &sh->xfull[x], i * kI8StageK + 64, q.t0 - a.row0);
-                }
-            }
-            __syncwarp();
-            if (SPLIT) {
-                cluster_sync();
-                if (u + unit_step < units) cluster_sync();
-            }
-        }
-        if (lane == 0)
-            for (int t = max(0, it - SX); t < it; ++t) mbar_wait(&sh->xfull[t % SX], (t / SX) & 1, a.status);
-        __syncwarp();
-    } else if (DIRECT && warp >= Cf::kWarpX && warp < Cf::kWarpConv) {
-        // ------------------------------------------------ the tokens' rows to FP16
-        const int me = tid - 32 * Cf::kWarpX;
-        const int kc = me % 8;  // 16 k of a row; rows me / 8, me / 8 + 16, ..
-        int it = 0;
-        bool ok = true;
-        for (int u = first_unit; u < units; u += unit_step) {
-            for (int i = kb; i < ke && ok; ++i, ++it) {
-                const int s = it % SB, x = it % SX;
-                ok = wait(&sh->bfull[s], (it / SB) & 1) && (it < SX || wait(&sh->xempty[x], (it / SX - 1) & 1));
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const uint8_t *src = ring_b + s * Cf::kStage + kBBytes;
-                uint8_t *st = ring_x + x * Cf::kXBytes + (kc / 4) * NT * 128;
-                uint4 v[Cf::kPieces];
+                    for (int j0 = 0; j0 < kPieces; j0 += kBatch) {
+                        uint4 v[kBatch];
 #pragma unroll
-                for (int j = 0; j < Cf::kPieces; ++j) {
-                    const int row = me / 8 + 16 * j;
-                    v[j] = *reinterpret_cast<const uint4 *>(src + row * 128 + ((kc ^ (row & 7)) * 16));
-                }
+                        for (int j = 0; j < kBatch; ++j)
+                            v[j] = *reinterpret_cast<const uint4 *>(src + (j0 + j) * 1024);
 #pragma unroll
-                for (int j = 0; j < Cf::kPieces; ++j) {
-                    const int row = me / 8 + 16 * j, c = (kc % 4) * 2;
-                    uint4 o0, o1;
-                    int8x4_to_f16(v[j].x, o0.x, o0.y);
-                    int8x4_to_f16(v[j].y, o0.z, o0.w);
-                    int8x4_to_f16(v[j].z, o1.x, o1.y);
-                    int8x4_to_f16(v[j].w, o1.z, o1.w);
-                    *reinterpret_cast<uint4 *>(st + row * 128 + ((c ^ (row & 7)) * 16)) = o0;
-                    *reinterpret_cast<uint4 *>(st + row * 128 + (((c + 1) ^ (row & 7)) * 16)) = o1;
+                        for (int j = 0; j < kBatch; ++j) {
+                            // a row's eight lanes write 16-byte columns 2 kc (kc < 4) and
+                            // 2 kc + 1 (kc >= 4, in the other box) first, then the other of
+                            // the two: eight distinct columns either time
+                            uint4 o0, o1;
+                            int8x4_to_f16(up ? v[j].z : v[j].x, o0.x, o0.y);
+                            int8x4_to_f16(up ? v[j].w : v[j].y, o0.z, o0.w);
+                            int8x4_to_f16(up ? v[j].x : v[j].z, o1.x, o1.y);
+                            int8x4_to_f16(up ? v[j].y : v[j].w, o1.z, o1.w);
+                            *reinterpret_cast<uint4 *>(dst + (j0 + j) * 1024 + (((c + up) ^ sw) * 16)) = o0;
+                            *reinterpret_cast<uint4 *>(dst + (j0 + j) * 1024 + (((c + 1 - up) ^ sw) * 16)) = o1;
+                        }
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sh->xfull[x.s]);
+                        mbar_arrive(&sh->empty[r.s]);
+                    }
                 }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sh->bempty[s]);
-                    mbar_arrive(&sh->xfull[x]);
-                }
-            }
-            if (SPLIT) {
-                __syncwarp();
-                cluster_sync();
-                if (u + unit_step < units) cluster_sync();
+                pass_exchange();
             }
         }
-    } else if (warp >= Cf::kWarpConv && warp < Cf::kWarpEpi) {
+    } else if (warp < 8) {
         // ------------------------------------------------ B to FP16, into tensor memory
-        const int wg = (warp - Cf::kWarpConv) / 4;
         const int row = (warp % 4) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
-        int it = 0, stored = -1;  // stored: the stage in tensor memory whose stores have not been waited for
+        Ring r, t;
+        int stored = -1;  // the stage in tensor memory whose stores have not been waited for
         bool ok = true;
         auto flush = [&]() {
             if (stored < 0) return;
@@ -713,57 +725,39 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             stored = -1;
         };
         for (int u = first_unit; u < units; u += unit_step) {
-            for (int i = kb; i < ke && ok; ++i, ++it) {
-                if (it % kConvWGs != wg) continue;
-                const int s = it % SB, t = it % kAStages;
+            for (int i = kb; i < ke && ok; ++i, r.step(S), t.step(kAStages)) {
                 // the stage before is handed on while this one is read, unless
                 // this one has yet to land
-                if (!__all_sync(0xffffffffu, mbar_try_wait(&sh->bfull[s], (it / SB) & 1))) {
+                if (!__all_sync(0xffffffffu, mbar_try_wait(&sh->full[r.s], r.round))) {
                     flush();
-                    ok = __all_sync(0xffffffffu, wait(&sh->bfull[s], (it / SB) & 1));
+                    ok = __all_sync(0xffffffffu, wait(&sh->full[r.s], r.round));
                     if (!ok) break;
                 }
-                const uint8_t *src = ring_b + s * Cf::kStage + row * kI8StageK;
+                const uint8_t *src = ring + r.s * Cf::kStage + row * kI8StageK;
                 uint4 w[8];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + ((c ^ (row & 7)) * 16));
                 flush();
-                ok = it < kAStages || wait(&sh->aempty[t], (it / kAStages - 1) & 1);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, wait(&sh->aempty[t.s], t.round ^ 1u));
                 if (!ok) break;
                 tc::fence_after_sync();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t o[32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        int8x4_to_f16(w[h * 4 + c].x, o[c * 8 + 0], o[c * 8 + 1]);
-                        int8x4_to_f16(w[h * 4 + c].y, o[c * 8 + 2], o[c * 8 + 3]);
-                        int8x4_to_f16(w[h * 4 + c].z, o[c * 8 + 4], o[c * 8 + 5]);
-                        int8x4_to_f16(w[h * 4 + c].w, o[c * 8 + 6], o[c * 8 + 7]);
-                    }
-                    tc::tmem_st32(tmem_a + t * kACols + h * 32 + lanes, o);
-                }
+                expand_to_tmem(w, tmem_a + t.s * kACols + lanes);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->bempty[s]);
-                stored = t;
+                if (lane == 0) mbar_arrive(&sh->empty[r.s]);
+                stored = t.s;
             }
             flush();
-            if (SPLIT) {
-                __syncwarp();
-                cluster_sync();
-                if (u + unit_step < units) cluster_sync();
-            }
+            pass_exchange();
         }
-    } else if (warp >= Cf::kWarpEpi) {
+    } else {
         // ------------------------------------------------ accumulators to C
-        const int wg = (warp - Cf::kWarpEpi) / 4;
+        if (Cf::kRegs) regs_more<Cf::kRegsEpilogue>();
         const int ch = (warp % 4) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
-        int chunk = 0;
+        Ring d;
         bool ok = true;
         for (int u = first_unit; u < units; u += unit_step) {
-            const I8Unit q = unit_of<NT, kI8TileN>(sh, a, ch_tiles, u);
+            const I8Unit q = unit_of<NT, kI8TileN>(bound, tiles, a, ch_tiles, u);
             // What the epilogue needs of global memory, asked for before the sums
             // are ready: the channel's scale and bias, and lane l's share of the
             // token scales (handed round by shuffles).
@@ -771,25 +765,28 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             const long long at = static_cast<long long>(q.e) * a.N + n;
             const float sb = n < a.N ? __ldg(a.scaleB + at) : 0.f;
             const float bias = n < a.N && a.bias ? __ldg(a.bias + at) : 0.f;
-            const int per = SPLIT ? NT / splits : Cf::kCols;  // this CTA's (warpgroup's) columns of the result
-            const int shift = 31 - __clz(per);
-            const int first = q.t0 + (SPLIT ? rank * per : wg * Cf::kCols);
-            float sa[(Cf::kCols + 31) / 32];
+            const int per = SPLIT ? NT / splits : NT;  // this CTA's columns of the result
+            const int first = q.t0 + (SPLIT ? rank * per : 0);
+            float sa[(NT + 31) / 32];
 #pragma unroll
-            for (int c = 0; c < (Cf::kCols + 31) / 32; ++c)
+            for (int c = 0; c < (NT + 31) / 32; ++c)
                 sa[c] = c * 32 + lane < per && first + c * 32 + lane < q.tend ? __ldg(a.scaleA + first + c * 32 + lane) : 0.f;
-            int acc[Cf::kCols];
+            // (its own room: ready as soon as the last unit's sums have been read)
+            if (SPLIT && Cf::kXchgOwn) {
+                __syncwarp();
+                cluster_arrive();
+            }
+            int acc[NT];
 #pragma unroll
-            for (int j = 0; j < Cf::kCols; ++j) acc[j] = 0;
-            for (int i = kb; i < ke && ok; i += chunk_stages, ++chunk) {
-                const int d = chunk & 1;
-                ok = __all_sync(0xffffffffu, wait(&sh->dfull[d], (chunk / 2) & 1));
+            for (int j = 0; j < NT; ++j) acc[j] = 0;
+            for (int i = kb; i < ke && ok; i += kChunk, d.step(2)) {
+                ok = __all_sync(0xffffffffu, wait(&sh->dfull[d.s], d.round));
                 if (!ok) break;
                 tc::fence_after_sync();
-                drain(tmem + d * NT + wg * Cf::kCols + lanes, acc);
+                drain(tmem + d.s * NT + lanes, acc);
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->dempty[d]);
+                if (lane == 0) mbar_arrive(&sh->dempty[d.s]);
             }
             if (!SPLIT) {
                 if (ok)
@@ -799,13 +796,16 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                                            a.ldc, n < a.N ? q.tend - first : 0, acc, sa, sb, bias);
                     });
             } else {
-                // column j belongs to CTA j / per of the cluster
+                __syncwarp();
+                if (!Cf::kXchgOwn) cluster_arrive();
+                cluster_wait_acquire();
+                // column j belongs to CTA j / per of the cluster (powers of two)
                 if (ok) {
-                    // (splits and per are powers of two)
+                    const int shift = 31 - __clz(per);
                     const uint32_t mine = smem_u32(xchg + rank * per * kI8TileN + ch);
                     uint32_t to = 0;
 #pragma unroll
-                    for (int j = 0; j < Cf::kCols; ++j) {
+                    for (int j = 0; j < NT; ++j) {
                         if ((j & (per - 1)) == 0)
                             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(j >> shift));
                         asm volatile("st.shared::cluster.u32 [%0], %1;"
@@ -834,13 +834,8 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                         }
                     });
                 __syncwarp();
-                if (u + unit_step < units) cluster_sync();
+                if (lane == 0) mbar_arrive(&sh->xchg_read);
             }
-        }
-    } else {
-        for (int u = first_unit; SPLIT && u < units; u += unit_step) {
-            cluster_sync();
-            if (u + unit_step < units) cluster_sync();
         }
     }
     // ---------------------------------------------------- teardown
@@ -848,51 +843,57 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
     __syncthreads();
     if (warp == 1) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, kI8TmemCols);
+        tc::tmem_dealloc(tmem, kDirectTmemCols);
     }
 }
 
-// ---- CTA pairs: 256 channels x 256 tokens -------------------------------------------
-constexpr int kPairN = 256, kPairT = 256;        // channels and tokens of a pair's tile
-constexpr int kPairXBytes = 128 * kI8StageK * 2;  // this CTA's half of the tokens, FP16: 32 KiB a stage
-constexpr int kPairBStages = 5, kPairXStages = 4;
+// ---- CTA pairs: 256 channels x T = 128 or 256 tokens ---------------------------------
+constexpr int kPairN = 256;  // channels of a pair's tile
+constexpr int kPairAStages = 4, kPairMaxB = 8, kPairMaxX = 6;
 constexpr int kPairThreads = 512;
+constexpr uint32_t kPairTmemCols = 512;
 
 struct PairShared {
-    uint64_t bfull[kPairBStages], bempty[kPairBStages];
-    uint64_t xfull[kPairXStages];   // (even CTA) both CTAs' tokens of the stage have landed
-    uint64_t xempty[kPairXStages];  // the MMAs have read them (both CTAs are told)
-    uint64_t afull[kAStages];       // (even CTA) B stands in both CTAs' tensor memory
-    uint64_t aempty[kAStages];
-    uint64_t dfull[2];              // a half accumulator holds up to 1024 k
+    uint64_t bfull[kPairMaxB], bempty[kPairMaxB];
+    uint64_t xfull[kPairMaxX];      // (even CTA) both CTAs' tokens of the stage have landed
+    uint64_t xempty[kPairMaxX];     // the MMAs have read them (both CTAs are told)
+    uint64_t afull[kPairAStages];   // (even CTA) B stands in both CTAs' tensor memory
+    uint64_t aempty[kPairAStages];
+    uint64_t dfull[2];              // a half accumulator holds up to `chunk` stages
     uint64_t dempty[2];             // (even CTA) both CTAs have read it
     uint64_t drained;
     uint32_t tmem_base;
     int abort;
-    int units, chunk;
-    int bound[kMaxExperts + 1];
-    int tiles[kMaxExperts + 1];
+    int units;
+    int chunk;                      // stages between drains of an accumulator
+    // then bound[experts + 1], tiles[experts + 1]
 };
-constexpr int kPairSmem = 1024 + kPairBStages * kBBytes + kPairXStages * kPairXBytes + static_cast<int>(sizeof(PairShared));
-static_assert(kPairSmem <= kSmemLimit, "shared memory");
 
-// Registers a thread of each warpgroup: control, conversion, two epilogue
-// warpgroups (128 sums a thread).  Their sum stays below 4 x 128, what the
-// block is launched with.
-constexpr int kRegsControl = 56, kRegsConvert = 96, kRegsEpilogue = 176;
-static_assert(kRegsControl + kRegsConvert + 2 * kRegsEpilogue <= 4 * 128, "register split");
-template <int R>
-__device__ __forceinline__ void regs_fewer() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R>
-__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int T>
+struct PairCfg {
+    static constexpr int kXBytes = T / 2 * kI8StageK * 2;  // this CTA's half of the tokens, FP16
+    static constexpr int kBStages = T == 256 ? 5 : 6, kXStages = T == 256 ? 4 : 6;
+    static constexpr int kFixed = 1024 + kBStages * kBBytes + kXStages * kXBytes + static_cast<int>(sizeof(PairShared));
+    static constexpr int smem(int experts) { return kFixed + 2 * 4 * (experts + 1); }
+    // Registers a thread of each warpgroup: control, conversion, two epilogue
+    // warpgroups (T / 2 sums a thread).  Their sum stays within 4 x 128, what the
+    // block is launched with.
+    static constexpr int kRegsControl = 56, kRegsConvert = 96, kRegsEpilogue = 176;
+    static_assert(kRegsControl + kRegsConvert + 2 * kRegsEpilogue <= 4 * 128, "register split");
+    static_assert(T + kPairAStages * kACols <= static_cast<int>(kPairTmemCols), "tensor memory");
+    static_assert(smem(kMaxExperts) <= kSmemLimit && kBStages <= kPairMaxB && kXStages <= kPairMaxX, "shared memory");
+};
 
+template <int T>
 __global__ void __launch_bounds__(kPairThreads, 1)
 int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA, const Int8Args a) {
-    constexpr int SB = kPairBStages, SX = kPairXStages;
+    using Cf = PairCfg<T>;
+    constexpr int SB = Cf::kBStages, SX = Cf::kXStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;  // the same in both CTAs
-    uint8_t *ring_x = smem_raw + pad, *ring_b = ring_x + SX * kPairXBytes;
+    uint8_t *ring_x = smem_raw + pad, *ring_b = ring_x + SX * Cf::kXBytes;
     PairShared *sh = reinterpret_cast<PairShared *>(ring_b + SB * kBBytes);
+    int *bound = reinterpret_cast<int *>(sh + 1), *tiles = bound + a.experts + 1;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rank = static_cast<int>(cluster_ctarank());  // 0: issues the MMAs
     const int first_unit = static_cast<int>(blockIdx.x) >> 1, unit_step = static_cast<int>(gridDim.x) >> 1;
@@ -908,7 +909,7 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             mbar_init(&sh->xfull[s], 1);
             mbar_init(&sh->xempty[s], 1);
         }
-        for (int s = 0; s < kAStages; ++s) {
+        for (int s = 0; s < kPairAStages; ++s) {
             mbar_init(&sh->afull[s], 8);
             mbar_init(&sh->aempty[s], 1);
         }
@@ -923,12 +924,15 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
         prefetch_tensormap(&tmA);
     }
     if (warp == 1) {
-        tc::tmem_alloc_pair(&sh->tmem_base, kI8TmemCols);
+        tc::tmem_alloc_pair(&sh->tmem_base, kPairTmemCols);
         tc::tmem_relinquish_pair();
     }
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 2) sum_tiles(sh, a, kPairT, ch_tiles, lane);
+    if (warp == 2) {
+        const int n = sum_tiles(bound, tiles, a, T, lane);
+        if (lane == 0) sh->units = n * ch_tiles;
+    }
     if (warp == 3) {
         const int c = chunk_of(a, lane);
         if (lane == 0) sh->chunk = c;
@@ -938,7 +942,7 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     tc::cluster_sync_all();  // both CTAs' barriers are initialised before any cross-CTA arrive
     tc::fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem_base, 0);
-    const uint32_t tmem_a = tmem + kPairT;
+    const uint32_t tmem_a = tmem + T;
     volatile int *abort_flag = &sh->abort;
     const int units = sh->units, chunk_stages = sh->chunk;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -950,29 +954,32 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     };
 
     if (warp < 4) {
-        regs_fewer<kRegsControl>();
+        regs_fewer<Cf::kRegsControl>();
         if (warp == 0) {
             // -------------------------------------------- TMA producer of B
-            int it = 0;
+            Ring r;
+            int issued = 0;
             bool ok = true;
             if (lane == 0) {
                 for (int u = first_unit; u < units && ok; u += unit_step) {
-                    const I8Unit q = unit_of<kPairT, kPairN>(sh, a, ch_tiles, u);
-                    for (int i = 0; i < kt; ++i, ++it) {
-                        const int s = it % SB;
-                        if (it >= SB && !wait(&sh->bempty[s], (it / SB - 1) & 1)) { ok = false; break; }
-                        mbar_arrive_expect_tx(&sh->bfull[s], kBBytes);
-                        tma_load_3d(ring_b + s * kBBytes, &tmB, &sh->bfull[s], i * kI8StageK, q.ch0 + rank * kI8TileN, q.e);
+                    const I8Unit q = unit_of<T, kPairN>(bound, tiles, a, ch_tiles, u);
+                    for (int i = 0; i < kt; ++i, r.step(SB), ++issued) {
+                        if (!wait(&sh->bempty[r.s], r.round ^ 1u)) { ok = false; break; }
+                        mbar_arrive_expect_tx(&sh->bfull[r.s], kBBytes);
+                        tma_load_3d(ring_b + r.s * kBBytes, &tmB, &sh->bfull[r.s], i * kI8StageK, q.ch0 + rank * kI8TileN,
+                                    q.e);
                     }
                 }
-                for (int t = max(0, it - SB); t < it; ++t) mbar_wait(&sh->bfull[t % SB], (t / SB) & 1, a.status);
+                // no copy outlives the CTA
+                for (int t = max(0, issued - SB); t < issued; ++t) mbar_wait(&sh->bfull[t % SB], (t / SB) & 1, a.status);
             }
             __syncwarp();
         } else if (warp == 1 && rank == 0) {
             // -------------------------------------------- MMA issuer (even CTA)
-            constexpr uint32_t idesc = tc::idesc_f16_kmajor(2 * kI8TileN, kPairT / 2);
+            constexpr uint32_t idesc = tc::idesc_f16_kmajor(2 * kI8TileN, T / 2);
             const uint64_t xdesc = tc::smem_desc(smem_u32(ring_x), 16, 1024, tc::kLayoutSwizzle128);
-            int it = 0, chunk = 0;
+            Ring xr, tr;
+            uint32_t round = 0;  // of the accumulators
             bool ok = true;
             for (int u = first_unit; u < units && ok; u += unit_step) {
                 // Two stages at a time: both for half 0 of the accumulators, then
@@ -985,26 +992,24 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
                     const bool start = run == 0, end = i + two == kt || run + two == chunk_stages;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        ok = ok && (!start || chunk == 0 || wait(&sh->dempty[h], (chunk - 1) & 1));
-                        for (int j = 0; j < two; ++j) {
-                            const int x = (it + j) % SX, t = (it + j) % kAStages;
-                            if (h == 0)
-                                ok = ok && wait(&sh->xfull[x], ((it + j) / SX) & 1) &&
-                                     wait(&sh->afull[t], ((it + j) / kAStages) & 1);
+                        Ring x = xr, t = tr;
+                        ok = ok && (!start || wait(&sh->dempty[h], round ^ 1u));
+                        for (int j = 0; j < two; ++j, x.step(SX), t.step(kPairAStages)) {
+                            if (h == 0) ok = ok && wait(&sh->xfull[x.s], x.round) && wait(&sh->afull[t.s], t.round);
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) break;
                             tc::fence_after_sync();
                             if (tc::elect_one()) {
                                 const uint64_t b =
-                                    xdesc + static_cast<uint64_t>(x * (kPairXBytes / 16) + h * (64 * 128 / 16));
+                                    xdesc + static_cast<uint64_t>(x.s * (Cf::kXBytes / 16) + h * (T / 4 * 128 / 16));
 #pragma unroll
                                 for (int kk = 0; kk < kI8StageK / 16; ++kk)
-                                    tc::mma_f16_ta_pair(tmem + h * (kPairT / 2), tmem_a + t * kACols + kk * 8,
-                                                        b + ((kk / 4) * 16384 + (kk % 4) * 32) / 16, idesc,
+                                    tc::mma_f16_ta_pair(tmem + h * (T / 2), tmem_a + t.s * kACols + kk * 8,
+                                                        b + ((kk / 4) * (T / 2 * 128) + (kk % 4) * 32) / 16, idesc,
                                                         (start && j == 0 && kk == 0) ? 0u : 1u);
                                 if (h == 1) {
-                                    tc::commit_pair(&sh->xempty[x], 0x3);
-                                    tc::commit_pair(&sh->aempty[t], 0x3);
+                                    tc::commit_pair(&sh->xempty[x.s], 0x3);
+                                    tc::commit_pair(&sh->aempty[t.s], 0x3);
                                 }
                                 if (end && j + 1 == two) tc::commit_pair(&sh->dfull[h], 0x3);
                             }
@@ -1012,9 +1017,12 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
                         }
                     }
                     if (!ok) break;
-                    it += two;
+                    for (int j = 0; j < two; ++j) {
+                        xr.step(SX);
+                        tr.step(kPairAStages);
+                    }
                     run = end ? 0 : run + two;
-                    if (end) ++chunk;
+                    if (end) round ^= 1u;
                 }
             }
             if (!ok && tc::elect_one()) {  // no teardown under a running MMA
@@ -1024,41 +1032,42 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             __syncwarp();
         } else if (warp == 2) {
             // -------------------------------------------- TMA producer of the tokens
-            // Half h of the accumulators covers tokens t0 + 128 h ..+127, 64 from
-            // each CTA: this CTA's rows 64 h .. 64 h + 63 of a stage.  Both CTAs'
-            // bytes count on the even CTA's barrier.
-            int it = 0;
+            // Half h of the accumulators covers T / 2 tokens from t0 + h T / 2, half of
+            // them from each CTA: this CTA's rows h T / 4 .. of a stage.  Both
+            // CTAs' bytes count on the even CTA's barrier.
+            Ring r;
+            int issued = 0;
             bool ok = true;
             if (lane == 0) {
                 const uint32_t xfull = tc::map_shared_rank(smem_u32(&sh->xfull[0]), 0);
                 for (int u = first_unit; u < units && ok; u += unit_step) {
-                    const I8Unit q = unit_of<kPairT, kPairN>(sh, a, ch_tiles, u);
-                    const int row = q.t0 - a.row0 + rank * 64;
-                    for (int i = 0; i < kt; ++i, ++it) {
-                        const int x = it % SX;
-                        if (it >= SX && !wait(&sh->xempty[x], (it / SX - 1) & 1)) { ok = false; break; }
-                        uint8_t *st = ring_x + x * kPairXBytes;
-                        if (rank == 0) mbar_arrive_expect_tx(&sh->xfull[x], 2 * kPairXBytes);
+                    const I8Unit q = unit_of<T, kPairN>(bound, tiles, a, ch_tiles, u);
+                    const int row = q.t0 - a.row0 + rank * (T / 4);
+                    for (int i = 0; i < kt; ++i, r.step(SX), ++issued) {
+                        if (!wait(&sh->xempty[r.s], r.round ^ 1u)) { ok = false; break; }
+                        uint8_t *st = ring_x + r.s * Cf::kXBytes;
+                        if (rank == 0) mbar_arrive_expect_tx(&sh->xfull[r.s], 2 * Cf::kXBytes);
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                tc::tma_load_2d_pair(st + k * 16384 + h * 8192, &tmA, xfull + x * 8,
-                                                     i * kI8StageK + k * 64, row + h * 128);
+                                tc::tma_load_2d_pair(st + k * (T / 2 * 128) + h * (T / 4 * 128), &tmA, xfull + r.s * 8,
+                                                     i * kI8StageK + k * 64, row + h * (T / 2));
                     }
                 }
                 // no copy outlives its CTA: the MMAs that read the last ones have finished
-                for (int t = max(0, it - SX); t < it; ++t) mbar_wait(&sh->xempty[t % SX], (t / SX) & 1, a.status);
+                for (int t = max(0, issued - SX); t < issued; ++t) mbar_wait(&sh->xempty[t % SX], (t / SX) & 1, a.status);
             }
             __syncwarp();
         }
     } else if (warp < 8) {
         // ------------------------------------------------ B to FP16, into tensor memory
-        regs_fewer<kRegsConvert>();
+        regs_fewer<Cf::kRegsConvert>();
         const int row = (warp % 4) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
         const uint32_t afull = tc::map_shared_rank(smem_u32(&sh->afull[0]), 0);
-        int it = 0, stored = -1;
+        Ring r, t;
+        int stored = -1;
         bool ok = true;
         auto flush = [&]() {
             if (stored < 0) return;
@@ -1069,52 +1078,39 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             stored = -1;
         };
         for (int u = first_unit; u < units && ok; u += unit_step) {
-            for (int i = 0; i < kt; ++i, ++it) {
-                const int s = it % SB, t = it % kAStages;
-                if (!__all_sync(0xffffffffu, mbar_try_wait(&sh->bfull[s], (it / SB) & 1))) {
+            for (int i = 0; i < kt; ++i, r.step(SB), t.step(kPairAStages)) {
+                if (!__all_sync(0xffffffffu, mbar_try_wait(&sh->bfull[r.s], r.round))) {
                     flush();
-                    ok = __all_sync(0xffffffffu, wait(&sh->bfull[s], (it / SB) & 1));
+                    ok = __all_sync(0xffffffffu, wait(&sh->bfull[r.s], r.round));
                     if (!ok) break;
                 }
-                const uint8_t *src = ring_b + s * kBBytes + row * kI8StageK;
+                const uint8_t *src = ring_b + r.s * kBBytes + row * kI8StageK;
                 uint4 w[8];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + ((c ^ (row & 7)) * 16));
                 flush();
-                ok = it < kAStages || wait(&sh->aempty[t], (it / kAStages - 1) & 1);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, wait(&sh->aempty[t.s], t.round ^ 1u));
                 if (!ok) break;
                 tc::fence_after_sync();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t o[32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        int8x4_to_f16(w[h * 4 + c].x, o[c * 8 + 0], o[c * 8 + 1]);
-                        int8x4_to_f16(w[h * 4 + c].y, o[c * 8 + 2], o[c * 8 + 3]);
-                        int8x4_to_f16(w[h * 4 + c].z, o[c * 8 + 4], o[c * 8 + 5]);
-                        int8x4_to_f16(w[h * 4 + c].w, o[c * 8 + 6], o[c * 8 + 7]);
-                    }
-                    tc::tmem_st32(tmem_a + t * kACols + h * 32 + lanes, o);
-                }
+                expand_to_tmem(w, tmem_a + t.s * kACols + lanes);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->bempty[s]);
-                stored = t;
+                if (lane == 0) mbar_arrive(&sh->bempty[r.s]);
+                stored = t.s;
             }
             flush();
         }
     } else {
         // ------------------------------------------------ accumulators to C: warpgroup h reads half h
-        regs_more<kRegsEpilogue>();
-        constexpr int kCols = kPairT / 2;
+        regs_more<Cf::kRegsEpilogue>();
+        constexpr int kCols = T / 2;
         const int h = (warp - 8) / 4;
         const int ch = (warp % 4) * 32 + lane;
         const uint32_t src = tmem + h * kCols + (static_cast<uint32_t>(warp % 4 * 32) << 16);
         const uint32_t dempty = tc::map_shared_rank(smem_u32(&sh->dempty[h]), 0);
-        int chunk = 0;
+        uint32_t round = 0;
         bool ok = true;
         for (int u = first_unit; u < units && ok; u += unit_step) {
-            const I8Unit q = unit_of<kPairT, kPairN>(sh, a, ch_tiles, u);
+            const I8Unit q = unit_of<T, kPairN>(bound, tiles, a, ch_tiles, u);
             const int n = q.ch0 + rank * kI8TileN + ch;
             const long long at = static_cast<long long>(q.e) * a.N + n;
             const float sb = n < a.N ? __ldg(a.scaleB + at) : 0.f;
@@ -1127,8 +1123,8 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             int acc[kCols];
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] = 0;
-            for (int i = 0; i < kt; i += chunk_stages, ++chunk) {
-                ok = __all_sync(0xffffffffu, wait(&sh->dfull[h], chunk & 1));
+            for (int i = 0; i < kt; i += chunk_stages, round ^= 1u) {
+                ok = __all_sync(0xffffffffu, wait(&sh->dfull[h], round));
                 if (!ok) break;
                 tc::fence_after_sync();
                 drain(src, acc);
@@ -1150,58 +1146,59 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     tc::cluster_sync_all();  // the peer is done with this CTA's barriers and tensor memory
     if (warp == 1) {
         tc::fence_after_sync();
-        tc::tmem_dealloc_pair(tmem, kI8TmemCols);
+        tc::tmem_dealloc_pair(tmem, kPairTmemCols);
     }
 }
 
-template <int NT, bool SPLIT, bool DIRECT>
-cudaError_t prepare_one() {
-    return cudaFuncSetAttribute(int8_tc_kernel<NT, SPLIT, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                I8Cfg<NT, SPLIT, DIRECT>::kSmem);
-}
-
-template <int NT, bool SPLIT, bool DIRECT>
-cudaError_t launch_one(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
-                       int smem_override, cudaStream_t stream) {
-    using Cf = I8Cfg<NT, SPLIT, DIRECT>;
+template <int NT, bool SPLIT>
+cudaError_t launch_split(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
+                         int smem_override, cudaStream_t stream) {
+    using Cf = DirectCfg<NT, SPLIT>;
     const int ch_tiles = (a.N + kI8TileN - 1) / kI8TileN, splits = SPLIT ? a.ksplit : 1;
-    // at most this many units (the experts' row counts are on the device)
-    const long long tiles = a.experts == 1 ? (a.rows + NT - 1) / NT
-                                           : static_cast<long long>(a.rows) / NT + (a.experts < a.rows ? a.experts : a.rows);
-    const long long units = tiles * ch_tiles, most = num_sms / splits;
-    return launch_dependent(int8_tc_kernel<NT, SPLIT, DIRECT>,
-                            dim3(static_cast<unsigned>(splits * (units < most ? units : most))), dim3(Cf::kThreads),
-                            smem_override > 0 ? smem_override : Cf::kSmem, stream, splits, tmB, tmA, a);
-}
-
-cudaError_t launch_pair(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
-                        int smem_override, cudaStream_t stream) {
-    const int ch_tiles = (a.N + kPairN - 1) / kPairN;
-    const long long tiles = a.experts == 1
-                                ? (a.rows + kPairT - 1) / kPairT
-                                : static_cast<long long>(a.rows) / kPairT + (a.experts < a.rows ? a.experts : a.rows);
-    const long long units = tiles * ch_tiles, most = num_sms / 2;
-    return launch_dependent(int8_tc_pair_kernel, dim3(static_cast<unsigned>(2 * (units < most ? units : most))),
-                            dim3(kPairThreads), smem_override > 0 ? smem_override : kPairSmem, stream, 2, tmB, tmA, a);
+    const long long units = int8_most_tiles(a.rows, a.experts, NT) * ch_tiles, most = 2 * num_sms / splits;
+    return launch_dependent(int8_tc_kernel<NT, SPLIT>,
+                            dim3(static_cast<unsigned>(splits * (units < most ? units : most))), dim3(kDirectThreads),
+                            smem_override > 0 ? smem_override : Cf::smem(a.experts), stream, splits, tmB, tmA, a);
 }
 
 template <int NT>
 cudaError_t launch_direct(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
                           int smem_override, cudaStream_t stream) {
-    return a.ksplit > 1 ? launch_one<NT, true, true>(a, tmB, tmA, num_sms, smem_override, stream)
-                        : launch_one<NT, false, true>(a, tmB, tmA, num_sms, smem_override, stream);
+    return a.ksplit > 1 ? launch_split<NT, true>(a, tmB, tmA, num_sms, smem_override, stream)
+                        : launch_split<NT, false>(a, tmB, tmA, num_sms, smem_override, stream);
+}
+
+template <int T>
+cudaError_t launch_pair(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
+                        int smem_override, cudaStream_t stream) {
+    const int ch_tiles = (a.N + kPairN - 1) / kPairN;
+    const long long units = int8_most_tiles(a.rows, a.experts, T) * ch_tiles, most = num_sms / 2;
+    return launch_dependent(int8_tc_pair_kernel<T>, dim3(static_cast<unsigned>(2 * (units < most ? units : most))),
+                            dim3(kPairThreads), smem_override > 0 ? smem_override : PairCfg<T>::smem(a.experts), stream,
+                            2, tmB, tmA, a);
+}
+
+template <int NT>
+cudaError_t prepare_direct() {
+    const cudaError_t e = cudaFuncSetAttribute(int8_tc_kernel<NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               DirectCfg<NT, false>::smem(kMaxExperts));
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(int8_tc_kernel<NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   DirectCfg<NT, true>::smem(kMaxExperts));
+}
+
+template <int T>
+cudaError_t prepare_pair() {
+    return cudaFuncSetAttribute(int8_tc_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                PairCfg<T>::smem(kMaxExperts));
 }
 
 }  // namespace
 
 cudaError_t int8_prepare() {
     cudaError_t e = cudaSuccess;
-    for (cudaError_t r : {prepare_one<16, false, true>(), prepare_one<32, false, true>(),
-                          prepare_one<64, false, true>(), prepare_one<16, true, true>(),
-                          prepare_one<32, true, true>(), prepare_one<64, true, true>(),
-                          prepare_one<128, false, false>(),
-                          cudaFuncSetAttribute(int8_tc_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kPairSmem)})
+    for (cudaError_t r : {prepare_direct<16>(), prepare_direct<32>(), prepare_direct<64>(), prepare_pair<128>(),
+                          prepare_pair<256>()})
         if (e == cudaSuccess) e = r;
     return e;
 }
@@ -1212,8 +1209,8 @@ cudaError_t launch_int8_tc(const Int8Args &a, const CUtensorMap &tmB, const CUte
         case 16: return launch_direct<16>(a, tmB, tmA, num_sms, smem_override, stream);
         case 32: return launch_direct<32>(a, tmB, tmA, num_sms, smem_override, stream);
         case 64: return launch_direct<64>(a, tmB, tmA, num_sms, smem_override, stream);
-        case 256: return launch_pair(a, tmB, tmA, num_sms, smem_override, stream);
-        default: return launch_one<128, false, false>(a, tmB, tmA, num_sms, smem_override, stream);
+        case 128: return launch_pair<128>(a, tmB, tmA, num_sms, smem_override, stream);
+        default: return launch_pair<256>(a, tmB, tmA, num_sms, smem_override, stream);
     }
 }
 

@@ -84,7 +84,7 @@ int check_int8(int transB, int out_type, int experts, int rows, int N, int K, co
 // each keeps at least two stages of 128 k.
 int split_of(long long tiles, int stages, int num_sms) {
     int s = 1;
-    while (s < 8 && tiles * s * 2 <= num_sms && stages >= s * 4) s *= 2;
+    while (s < 8 && tiles * s * 2 <= 2 * num_sms && stages >= s * 4) s *= 2;
     return s;
 }
 
@@ -143,7 +143,7 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
             const long long fit = static_cast<long long>((room - b_room) / a_row);
             if (fit < rows) per = static_cast<int>(fit / a.nt * a.nt);
         }
-        const long long tiles = (experts == 1 ? cdiv(per, a.nt) : per / a.nt + owners) * ch_tiles;
+        const long long tiles = sg::int8_most_tiles(per, experts, a.nt) * ch_tiles;
         tc = tiles < INT_MAX && (static_cast<long long>(per / a.nt) + experts) * ch_tiles < INT_MAX;
         a.ksplit = direct ? split_of(tiles, static_cast<int>(cdiv(K, sg::kI8StageK)), v.num_sms) : 1;
     }
@@ -170,7 +170,7 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
              (direct ? sg::encode_map(&tmA, sg::MapType::kInt8, 2, a_as_stored ? static_cast<const void *>(A) : ws, K, per,
                                       1, a_as_stored ? lda : kb, 0, sg::kI8StageK, a.nt)
                      : sg::encode_map(&tmA, sg::MapType::kF16, 2, ws, kp, per, 1, static_cast<long long>(kp) * 2, 0,
-                                      64, std::min(a.nt, a.nt == 256 ? 64 : 128)));
+                                      64, a.nt / 4));
     }
     if (tc) {
         variant = SGEMM_VARIANT_TC_I8;
