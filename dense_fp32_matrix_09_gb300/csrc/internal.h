@@ -269,14 +269,29 @@ struct Int8Args {
     int n_peaks;
 };
 cudaError_t launch_int8_generic(const Int8Args &a, cudaStream_t stream);
-// dst (rows x ldd FP16, ldd a multiple of 64) = the int8 rows of A, columns K..ldd-1
-// zero; peaks (room for kI8Peaks) gets *n_peaks sums of magnitudes (Int8Args).
+// The copies of a call's operands, one launch.  a_dst (NULL: none): the rows of A,
+// a_rows x a_ld, as FP16 where peaks is not NULL (a_ld a multiple of 64; peaks has
+// room for kI8Peaks sums of magnitudes, see Int8Args, of which a_blocks are
+// written), else as int8 on 16-byte boundaries (a_ld a multiple of 16).  b_dst
+// (NULL: none): experts x N x b_ld int8 of B_e, stored N x K (b_trans) or K x N.
+// Columns from K on are zero.
 constexpr int kI8Peaks = 2048;
-cudaError_t launch_int8_to_f16(const int8_t *A, long long lda, int rows, int K, void *dst, int ldd, int *peaks,
-                               int *n_peaks, cudaStream_t stream);
-// dst (experts x N x ldd, columns K..ldd-1 zero) = B_e, stored N x K (trans = 1) or K x N (0).
-cudaError_t launch_int8_relayout(const int8_t *B, long long ldb, long long strideB, int trans, int experts, int N,
-                                 int K, int8_t *dst, int ldd, cudaStream_t stream);
+struct Int8Copies {
+    const int8_t *A;
+    long long lda;
+    int a_rows, K;
+    void *a_dst;
+    int a_ld;
+    int *peaks;
+    const int8_t *B;
+    long long ldb, strideB;
+    int b_trans, experts, N;
+    int8_t *b_dst;
+    int b_ld;
+    // set by launch_int8_copies
+    int a_vec, b_vec, a_blocks, b_blocks;
+};
+cudaError_t launch_int8_copies(Int8Copies *c, cudaStream_t stream);
 constexpr int kI8TileN = 128, kI8StageK = 128;  // channels and k of one B stage (TMA box, 128-byte swizzle)
 // Token tiles: up to 64 by one CTA (or a cluster that splits K), 128 and 256 by CTA
 // pairs with 256 channels.

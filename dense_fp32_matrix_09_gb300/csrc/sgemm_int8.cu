@@ -46,7 +46,7 @@
 //    each sends the others their columns' int32 partial sums through
 //    distributed shared memory (tiles of up to 64 tokens, one epilogue warpgroup).
 //  * int8_generic_kernel -- any layout and alignment, dp4a on the CUDA cores.
-//  * int8_to_f16_kernel, int8_relayout_kernel -- the tokens' rows as FP16, and B
+//  * int8_copies_kernel -- the tokens' rows as FP16 or on 16-byte boundaries, and B
 //    as the TMA can read it (stored K x N, or not on 16-byte boundaries).
 // Every wait is bounded; on a timeout the kernel records it, waits (bounded)
 // for its own copies and MMAs in flight, frees the tensor memory and returns.
@@ -224,35 +224,45 @@ __device__ __forceinline__ void int8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t
     hi = *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// Bytes p[0..15] of a row of which `n` remain (zeros beyond).
-__device__ __forceinline__ uint4 load_int8x16(const int8_t *p, int n, bool vec) {
-    if (vec && n >= 16) return __ldg(reinterpret_cast<const uint4 *>(p));
-    uint32_t w[4] = {};
+// Bytes p[k..k+15] of a row of K (zeros from K on): 16 bytes at once where `vec`
+// says that rows start on 16-byte boundaries; otherwise five words and a shift,
+// away from the row's ends (no byte outside the row is read).
+__device__ __forceinline__ uint4 load_int8x16(const int8_t *row, int k, int K, bool vec) {
+    const int8_t *p = row + k;
+    if (vec && k + 16 <= K) return __ldg(reinterpret_cast<const uint4 *>(p));
+    uint32_t w[5] = {};
+    if (k >= 16 && k + 20 <= K) {
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < n) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i % 4));
+        for (int i = 0; i < 5; ++i) w[i] = __ldg(q + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * off);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (k + i < K) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i % 4));
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 16 k a thread; ldd is a multiple of 64, so its rows divide into whole threads.
-// peaks[block]: the largest sum of |a| over the 512 k (of one row, or the end of
-// one and the start of the next) that a warp of the block converts at a time.
-__global__ void __launch_bounds__(256)
-int8_to_f16_kernel(const int8_t *__restrict__ A, long long lda, int rows, int K, uint4 *__restrict__ dst, int ldd,
-                   int vec, int *__restrict__ peaks) {
+// The tokens' rows as FP16, 16 k a thread; ldd is a multiple of 64, so its rows
+// divide into whole threads.  *peak: the largest sum of |a| over the 512 k (of
+// one row, or the end of one and the start of the next) that a warp of the block
+// converts at a time.
+__device__ __forceinline__ void rows_to_f16(const Int8Copies &c, int block, int blocks, int *peak) {
     __shared__ int part[8];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int per_row = ldd / 16;
-    const long long total = static_cast<long long>(rows) * per_row;
+    uint4 *dst = static_cast<uint4 *>(c.a_dst);
+    const int per_row = c.a_ld / 16;
+    const long long total = static_cast<long long>(c.a_rows) * per_row;
     int top = 0;
-    for (long long i0 = blockIdx.x * 256ll; i0 < total; i0 += gridDim.x * 256ll) {
+    for (long long i0 = block * 256ll; i0 < total; i0 += blocks * 256ll) {
         const long long i = i0 + threadIdx.x;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (i < total) {
             const long long row = div_floor(i, per_row);
             const int k = static_cast<int>(i - row * per_row) * 16;
-            if (k < K) v = load_int8x16(A + row * lda + k, K - k, vec);
+            if (k < c.K) v = load_int8x16(c.A + row * c.lda, k, c.K, c.a_vec);
             uint4 o0, o1;
             int8x4_to_f16(v.x, o0.x, o0.y);
             int8x4_to_f16(v.y, o0.z, o0.w);
@@ -272,66 +282,100 @@ int8_to_f16_kernel(const int8_t *__restrict__ A, long long lda, int rows, int K,
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < 8; ++w) top = max(top, part[w]);
-        peaks[blockIdx.x] = top;
+        *peak = top;
     }
 }
 
-// B stored N x K, rows copied onto 16-byte boundaries: 16 k a thread.
-__global__ void __launch_bounds__(256)
-int8_realign_kernel(const int8_t *__restrict__ B, long long ldb, long long strideB, int N, int K,
-                    int8_t *__restrict__ dst, int ldd) {
-    griddep_wait();
-    griddep_launch_dependents();
+// Rows of int8 copied onto 16-byte boundaries (ldd a multiple of 16, columns
+// K..ldd-1 zero), 16 k a thread; row r of matrix m is m * rows + r of dst.
+__device__ __forceinline__ void realign(const int8_t *src, long long ld, long long stride, int matrices, int rows, int K,
+                                        int8_t *dst, int ldd, int block, int blocks) {
     const int per_row = ldd / 16;
-    const int8_t *src = B + blockIdx.y * strideB;
-    int8_t *d = dst + static_cast<long long>(blockIdx.y) * N * ldd;
-    const long long total = static_cast<long long>(N) * per_row;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const long long row = div_floor(i, per_row);
+    const long long total = static_cast<long long>(matrices) * rows * per_row;
+    for (long long i = block * 256ll + threadIdx.x; i < total; i += blocks * 256ll) {
+        const long long row = div_floor(i, per_row), m = div_floor(row, rows);
         const int k = static_cast<int>(i - row * per_row) * 16;
-        reinterpret_cast<uint4 *>(d)[i] = load_int8x16(src + row * ldb + k, K - k, false);
+        reinterpret_cast<uint4 *>(dst)[i] = load_int8x16(src + m * stride + (row - m * rows) * ld, k, K, false);
     }
 }
 
-// B stored K x N -> N x ldd: a tile of 128 k x 64 channels through shared memory
-// (rows of 65 bytes: the 8 lanes that gather 16 k each of one channel fall in
-// distinct banks).
+// B stored K x N -> N x ldd: a tile of 128 k x 64 channels.  A thread reads four
+// channels of four rows, turns the 4 x 4 bytes round and stores four words, four
+// k of a channel each, in shared memory rows of 33 words: the writes of a warp
+// (8 x 4 channels, 4 k words) and its reads (4 channels, 16 k of each of 8
+// threads) fall in 32 distinct banks.
 constexpr int kTK = 128, kTN = 64;
 
-__global__ void __launch_bounds__(256)
-int8_transpose_kernel(const int8_t *__restrict__ B, long long ldb, long long strideB, int N, int K,
-                      int8_t *__restrict__ dst, int ldd) {
-    __shared__ uint8_t tile[kTK][kTN + 1];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int8_t *src = B + blockIdx.z * strideB;
-    int8_t *d = dst + static_cast<long long>(blockIdx.z) * N * ldd;
-    const int k0 = blockIdx.x * kTK;
-    for (int n0 = blockIdx.y * kTN; n0 < N; n0 += gridDim.y * kTN) {
-        uint8_t v[kTK * kTN / 256];
+__device__ __forceinline__ void transpose(const Int8Copies &c, int block, int blocks) {
+    __shared__ uint32_t tile[kTN][kTK / 4 + 1];
+    const int tiles_k = (c.b_ld + kTK - 1) / kTK, tiles_n = (c.N + kTN - 1) / kTN;
+    const long long total = static_cast<long long>(c.experts) * tiles_k * tiles_n;
+    for (long long t = block; t < total; t += blocks) {
+        const long long e = div_floor(t, tiles_k * static_cast<long long>(tiles_n));
+        const int r = static_cast<int>(t - e * tiles_k * tiles_n);
+        const int n0 = r % tiles_n * kTN, k0 = r / tiles_n * kTK;
+        const int8_t *src = c.B + e * c.strideB;
+        int8_t *d = c.b_dst + e * c.N * c.b_ld;
+        uint32_t w[2][4];
 #pragma unroll
-        for (int r = 0; r < kTK * kTN / 256; ++r) {
-            const int at = threadIdx.x + r * 256, k = at / kTN, n = at % kTN;
-            v[r] = (k0 + k < K && n0 + n < N) ? static_cast<uint8_t>(src[static_cast<long long>(k0 + k) * ldb + n0 + n]) : 0;
-        }
+        for (int h = 0; h < 2; ++h) {
+            const int at = threadIdx.x + h * 256, n4 = at % 8 + at / 256 % 2 * 8, k4 = at / 8 % 32;
+            const int n = n0 + n4 * 4;
 #pragma unroll
-        for (int r = 0; r < kTK * kTN / 256; ++r) {
-            const int at = threadIdx.x + r * 256;
-            tile[at / kTN][at % kTN] = v[r];
-        }
-        __syncthreads();
+            for (int j = 0; j < 4; ++j) {
+                const int k = k0 + k4 * 4 + j;
+                uint32_t v = 0;
+                if (k < c.K) {
+                    const int8_t *p = src + static_cast<long long>(k) * c.ldb + n;
+                    if (c.b_vec && n + 4 <= c.N) {
+                        v = __ldg(reinterpret_cast<const uint32_t *>(p));
+                    } else if (n >= 4 && n + 8 <= c.N) {
+                        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+                        const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
+                        v = __funnelshift_r(__ldg(q), __ldg(q + 1), 8 * off);
+                    } else {
 #pragma unroll
-        for (int r = 0; r < kTN * (kTK / 16) / 256; ++r) {
-            const int at = threadIdx.x + r * 256, kg = at % (kTK / 16), n = at / (kTK / 16);
-            if (n0 + n < N && k0 + kg * 16 < ldd) {
-                uint32_t w[4] = {};
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i / 4] |= static_cast<uint32_t>(tile[kg * 16 + i][n]) << (8 * (i % 4));
-                *reinterpret_cast<uint4 *>(d + static_cast<long long>(n0 + n) * ldd + k0 + kg * 16) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int b = 0; b < 4; ++b)
+                            if (n + b < c.N) v |= static_cast<uint32_t>(static_cast<uint8_t>(p[b])) << (8 * b);
+                    }
+                }
+                w[h][j] = v;
             }
         }
+        __syncthreads();  // the tile before has been read
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = threadIdx.x + h * 256, n4 = at % 8 + at / 256 % 2 * 8, k4 = at / 8 % 32;
+            const uint32_t a = __byte_perm(w[h][0], w[h][1], 0x5140), b = __byte_perm(w[h][2], w[h][3], 0x5140);
+            const uint32_t x = __byte_perm(w[h][0], w[h][1], 0x7362), y = __byte_perm(w[h][2], w[h][3], 0x7362);
+            tile[n4 * 4 + 0][k4] = __byte_perm(a, b, 0x5410);
+            tile[n4 * 4 + 1][k4] = __byte_perm(a, b, 0x7632);
+            tile[n4 * 4 + 2][k4] = __byte_perm(x, y, 0x5410);
+            tile[n4 * 4 + 3][k4] = __byte_perm(x, y, 0x7632);
+        }
         __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = threadIdx.x + h * 256, kg = at % 8, n = at / 8;
+            if (n0 + n < c.N && k0 + kg * 16 < c.b_ld)
+                *reinterpret_cast<uint4 *>(d + static_cast<long long>(n0 + n) * c.b_ld + k0 + kg * 16) =
+                    make_uint4(tile[n][kg * 4], tile[n][kg * 4 + 1], tile[n][kg * 4 + 2], tile[n][kg * 4 + 3]);
+        }
+    }
+}
+
+// Both operands' copies in one launch: blocks [0, b_blocks) copy B, the rest A.
+__global__ void __launch_bounds__(256) int8_copies_kernel(const Int8Copies c) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int block = static_cast<int>(blockIdx.x);
+    if (block < c.b_blocks) {
+        if (c.b_trans) realign(c.B, c.ldb, c.strideB, c.experts, c.N, c.K, c.b_dst, c.b_ld, block, c.b_blocks);
+        else transpose(c, block, c.b_blocks);
+    } else if (c.peaks) {
+        rows_to_f16(c, block - c.b_blocks, c.a_blocks, c.peaks + block - c.b_blocks);
+    } else {
+        realign(c.A, c.lda, 0, 1, c.a_rows, c.K, static_cast<int8_t *>(c.a_dst), c.a_ld, block - c.b_blocks, c.a_blocks);
     }
 }
 
@@ -439,7 +483,7 @@ __device__ __forceinline__ int sum_tiles(int *bound, int *tiles, const Int8Args 
     return sum;
 }
 
-// Stages between drains, from the tokens' own size.  int8_to_f16_kernel leaves in
+// Stages between drains, from the tokens' own size.  rows_to_f16 leaves in
 // peaks the largest sum of |a| over any 512 consecutive k that one of its warps
 // saw; a run of c * 512 k touches at most c + 1 of those windows and |b| <= 128,
 // so no partial sum over it exceeds 128 * (c + 1) * peak, and up to 2^24 FP32
@@ -496,6 +540,23 @@ struct DirectShared {
     int abort;
     int units;                    // units of this launch
     // then bound[experts + 1], tiles[experts + 1]
+};
+
+// Partial sums of a channel that cross the cluster together.
+template <int V>
+struct ExchangeVec;
+template <>
+struct ExchangeVec<2> {
+    using T = int2;
+    static __device__ __forceinline__ void rest(int2, int (&)[2]) {}
+};
+template <>
+struct ExchangeVec<4> {
+    using T = int4;
+    static __device__ __forceinline__ void rest(int4 v, int (&sum)[4]) {
+        sum[2] += v.z;
+        sum[3] += v.w;
+    }
 };
 
 template <int NT, bool SPLIT>
@@ -568,9 +629,22 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
         tc::tmem_alloc(&sh->tmem_base, kDirectTmemCols);
         tc::tmem_relinquish();
     }
+    // One expert's tiles do not depend on device memory.  Its first stages of B
+    // are fetched into L2 ahead of the wait for the kernel before this one (a
+    // prefetch returns no data, so it does not matter whether that kernel has
+    // yet to write them).
+    if (!a.offsets && warp == 2) {
+        const int n = sum_tiles(bound, tiles, a, NT, lane);
+        if (lane == 0) sh->units = n * ch_tiles;
+        __syncwarp();
+        if (first_unit < n * ch_tiles) {
+            const I8Unit q = unit_of<NT, kI8TileN>(bound, tiles, a, ch_tiles, first_unit);
+            if (lane < S && kb + lane < ke) tma_prefetch_3d(&tmB, (kb + lane) * kI8StageK, q.ch0, q.e);
+        }
+    }
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 2) {
+    if (a.offsets && warp == 2) {
         const int n = sum_tiles(bound, tiles, a, NT, lane);
         if (lane == 0) sh->units = n * ch_tiles;
     }
@@ -799,17 +873,29 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                 __syncwarp();
                 if (!Cf::kXchgOwn) cluster_arrive();
                 cluster_wait_acquire();
-                // column j belongs to CTA j / per of the cluster (powers of two)
+                // Column j belongs to CTA j / per of the cluster (powers of two).  The
+                // partial sums of a channel stand kV columns together, so that they
+                // cross in pieces of up to 16 bytes.
+                constexpr int kV = NT == 16 ? 2 : 4;  // at most NT / 8, the fewest columns a CTA has
+                using Vec = typename ExchangeVec<kV>::T;
+                Vec *slots = reinterpret_cast<Vec *>(xchg);  // [CTA][column / kV][channel]
+                const int groups = per / kV;
                 if (ok) {
-                    const int shift = 31 - __clz(per);
-                    const uint32_t mine = smem_u32(xchg + rank * per * kI8TileN + ch);
+                    const int shift = 31 - __clz(groups);
+                    const uint32_t mine = smem_u32(slots + rank * groups * kI8TileN + ch);
                     uint32_t to = 0;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        if ((j & (per - 1)) == 0)
+                    for (int j = 0; j < NT / kV; ++j) {
+                        if ((j & (groups - 1)) == 0)
                             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(j >> shift));
-                        asm volatile("st.shared::cluster.u32 [%0], %1;"
-                                     ::"r"(to + (j & (per - 1)) * kI8TileN * 4), "r"(acc[j]) : "memory");
+                        const uint32_t at = to + (j & (groups - 1)) * (kI8TileN * kV * 4);
+                        if (kV == 2)
+                            asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};"
+                                         ::"r"(at), "r"(acc[kV * j]), "r"(acc[kV * j + 1]) : "memory");
+                        else
+                            asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
+                                         ::"r"(at), "r"(acc[kV * j]), "r"(acc[kV * j + 1]), "r"(acc[kV * j + kV - 2]),
+                                           "r"(acc[kV * j + kV - 1]) : "memory");
                     }
                 }
                 __syncwarp();
@@ -818,18 +904,24 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                     with_out_type(a.out_type, [&](auto out) {
                         using Out = decltype(out);
                         auto *C = static_cast<typename Out::T *>(a.C) + static_cast<long long>(first) * a.ldc + n;
-                        for (int c0 = 0; c0 < per; c0 += 8) {
-                            int sum[8] = {};
-                            for (int r = 0; r < splits; ++r)
+                        for (int g = 0; g < groups; ++g) {
+                            int sum[kV] = {};
 #pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    if (c0 + c < per) sum[c] += xchg[(r * per + c0 + c) * kI8TileN + ch];
+                            for (int r = 0; r < 8; ++r)  // all loads in flight at once
+                                if (r < splits) {
+                                    const Vec v = slots[(r * groups + g) * kI8TileN + ch];
+                                    sum[0] += v.x;
+                                    sum[1] += v.y;
+                                    ExchangeVec<kV>::rest(v, sum);
+                                }
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const float s = __shfl_sync(0xffffffffu, sa[0], (c0 + c) & 31);
-                                if (c0 + c < per && first + c0 + c < q.tend && n < a.N)
-                                    C[static_cast<long long>(c0 + c) * a.ldc] =
-                                        Out::lo(Out::two(int8_value(sum[c], sb, s, bias), 0.f));
+                            for (int c = 0; c < kV; c += 2) {
+                                const int col = g * kV + c;
+                                const float f0 = __shfl_sync(0xffffffffu, sa[0], col), f1 = __shfl_sync(0xffffffffu, sa[0], col + 1);
+                                const typename Out::Two v =
+                                    Out::two(int8_value(sum[c], sb, f0, bias), int8_value(sum[c + 1], sb, f1, bias));
+                                if (n < a.N && first + col < q.tend) C[static_cast<long long>(col) * a.ldc] = Out::lo(v);
+                                if (n < a.N && first + col + 1 < q.tend) C[static_cast<long long>(col + 1) * a.ldc] = Out::hi(v);
                             }
                         }
                     });
@@ -1220,26 +1312,15 @@ cudaError_t launch_int8_generic(const Int8Args &a, cudaStream_t stream) {
     return launch_dependent(int8_generic_kernel, grid, dim3(256), 0, stream, 1, a);
 }
 
-cudaError_t launch_int8_to_f16(const int8_t *A, long long lda, int rows, int K, void *dst, int ldd, int *peaks,
-                               int *n_peaks, cudaStream_t stream) {
-    const int vec = reinterpret_cast<uintptr_t>(A) % 16 == 0 && lda % 16 == 0;
-    const long long blocks = (static_cast<long long>(rows) * (ldd / 16) + 255) / 256;
-    *n_peaks = static_cast<int>(blocks < kI8Peaks ? blocks : kI8Peaks);
-    return launch_dependent(int8_to_f16_kernel, dim3(*n_peaks), dim3(256), 0, stream, 1, A, lda, rows, K,
-                            static_cast<uint4 *>(dst), ldd, vec, peaks);
-}
-
-cudaError_t launch_int8_relayout(const int8_t *B, long long ldb, long long strideB, int trans, int experts, int N,
-                                 int K, int8_t *dst, int ldd, cudaStream_t stream) {
-    if (trans) {
-        const long long blocks = (static_cast<long long>(N) * (ldd / 16) + 255) / 256;
-        return launch_dependent(int8_realign_kernel,
-                                dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20)), experts),
-                                dim3(256), 0, stream, 1, B, ldb, strideB, N, K, dst, ldd);
-    }
-    const int y = (N + kTN - 1) / kTN;
-    return launch_dependent(int8_transpose_kernel, dim3((ldd + kTK - 1) / kTK, y < 65535 ? y : 65535, experts),
-                            dim3(256), 0, stream, 1, B, ldb, strideB, N, K, dst, ldd);
+cudaError_t launch_int8_copies(Int8Copies *c, cudaStream_t stream) {
+    c->a_vec = reinterpret_cast<uintptr_t>(c->A) % 16 == 0 && c->lda % 16 == 0;
+    c->b_vec = reinterpret_cast<uintptr_t>(c->B) % 4 == 0 && c->ldb % 4 == 0 && c->strideB % 4 == 0;
+    auto capped = [](long long blocks) { return static_cast<int>(blocks < kI8Peaks ? blocks : kI8Peaks); };
+    c->a_blocks = c->a_dst ? capped((static_cast<long long>(c->a_rows) * (c->a_ld / 16) + 255) / 256) : 0;
+    if (!c->b_dst) c->b_blocks = 0;
+    else if (c->b_trans) c->b_blocks = capped((static_cast<long long>(c->experts) * c->N * (c->b_ld / 16) + 255) / 256);
+    else c->b_blocks = capped(static_cast<long long>(c->experts) * ((c->b_ld + kTK - 1) / kTK) * ((c->N + kTN - 1) / kTN));
+    return launch_dependent(int8_copies_kernel, dim3(c->a_blocks + c->b_blocks), dim3(256), 0, stream, 1, *c);
 }
 
 }  // namespace sg

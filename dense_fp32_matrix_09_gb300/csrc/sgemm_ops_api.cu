@@ -4,7 +4,6 @@
 // kernels in sgemm_int8.cu and sgemm_experts.cu.
 #include <algorithm>
 #include <climits>
-#include <cstdlib>
 #include <cstdint>
 
 #include <cuda.h>
@@ -46,12 +45,60 @@ struct Range {
 // K up to which a sum of K products of two int8 stays inside int32.
 constexpr int kMaxInt8K = 131071;
 
-// The tile's tokens for products of `rows` rows a B matrix: the narrowest tile
-// that holds them, 256 beyond.
-int token_tile(long long rows) {
-    for (int nt : sg::kI8TokenTiles)
-        if (rows <= nt) return nt;
-    return 256;
+// Token tile and K split of a tensor-core call, by the time that this model
+// gives each choice (microseconds, from calls measured back to back in CUDA
+// graphs over M 1 .. 8192, N and K 256 .. 8192; it orders the choices right
+// where they differ by more than a tenth):
+//   direct tiles: a launch, the exchange of partial sums, and a stage of 128 k at
+//     a time -- `alone` with one CTA on an SM, `shared` a CTA with two;
+//   pair tiles: two launches, the conversion of the tokens to FP16 (one read and
+//     one write of HBM), and the stages of complete waves of pairs.
+// E.g. 4096 x 4096 weights: M = 16 on tiles of 16, four-way split, 7.7 us (whole
+// K 15.8, tiles of 64 11.0); M = 256 on tiles of 64, two-way, 20.8 (pairs of
+// 128: 22.3, whole K 22.0); M = 512 on pairs of 128 24.8 (tiles of 64 32.2, pairs of
+// 256 30.0); M = 2048 on pairs of 256 56 (of 128 72).
+struct TileChoice {
+    int nt, ksplit;
+};
+TileChoice choose_tile(int rows, int experts, int N, int K, int num_sms, bool direct_copy) {
+    struct Direct {
+        int nt;
+        double alone, shared, exchange;
+    };
+    constexpr Direct kDirect[] = {{16, 0.36, 0.35, 0.7}, {32, 0.42, 0.34, 1.2}, {64, 0.53, 0.43, 2.2}};
+    struct Pair {
+        int nt;
+        double fixed, stage;
+    };
+    constexpr Pair kPair[] = {{128, 7.0, 0.49}, {256, 7.5, 0.68}};
+    const int owners = std::min(experts, std::max(rows, 1));
+    const long long each = cdiv(rows, owners);
+    const int stages = static_cast<int>(cdiv(K, sg::kI8StageK));
+    TileChoice best{256, 1};
+    double least = 1e30;
+    for (const Direct &d : kDirect) {
+        const long long tiles = owners * cdiv(each, d.nt) * cdiv(N, sg::kI8TileN);
+        for (int s = 1; s <= 8 && s <= stages; s *= 2) {
+            const long long ctas = tiles * s;
+            if (s > 1 && ctas > 2 * num_sms) break;
+            const double stage = ctas <= num_sms ? d.alone : 2 * d.shared;
+            const double t = 4.3 + (direct_copy ? 2.0 : 0.0) + (s > 1 ? d.exchange + 0.1 * s : 0.0) +
+                             static_cast<double>(cdiv(ctas, 2LL * num_sms)) * static_cast<double>(cdiv(stages, s)) * stage;
+            if (t < least) {
+                least = t;
+                best = {d.nt, s};
+            }
+        }
+    }
+    for (const Pair &p : kPair) {
+        const long long units = owners * cdiv(each, p.nt) * cdiv(N, 2 * sg::kI8TileN);
+        const double t = p.fixed + 3.0 * rows * K / 5.5e6 + static_cast<double>(cdiv(units, num_sms / 2)) * stages * p.stage;
+        if (t < least) {
+            least = t;
+            best = {p.nt, 1};
+        }
+    }
+    return best;
 }
 
 int check_int8(int transB, int out_type, int experts, int rows, int N, int K, const int *offsets, bool grouped,
@@ -78,14 +125,6 @@ int check_int8(int transB, int out_type, int experts, int rows, int N, int K, co
     if ((K > 0 && (c.meets(a) || c.meets(b))) || c.meets(sa) || c.meets(sb) || c.meets(bi) || c.meets(of))
         return SGEMM_ERR_ALIAS;
     return SGEMM_OK;
-}
-
-// CTAs that share a tile's K range: doubled while a wave has CTAs for it and
-// each keeps at least two stages of 128 k.
-int split_of(long long tiles, int stages, int num_sms) {
-    int s = 1;
-    while (s < 8 && tiles * s * 2 <= 2 * num_sms && stages >= s * 4) s *= 2;
-    return s;
 }
 
 int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, int N, int K, const int *offsets,
@@ -117,11 +156,11 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
 
     // Tiles of up to 64 tokens read the tokens' int8 rows, by TMA: rows on other
     // than 16-byte boundaries are copied first.  Wider tiles read them as FP16.
-    const int owners = std::min(experts, std::max(rows, 1));
-    a.nt = token_tile(cdiv(rows, owners));
-    if (const char *f = getenv("I8_NT")) a.nt = atoi(f);
+    const bool a_aligned = aligned(A, 16) && lda % 16 == 0;
+    const TileChoice tile = choose_tile(rows, experts, N, std::max(K, 1), v.num_sms, !a_aligned);
+    a.nt = tile.nt;
     const bool direct = a.nt <= 64;
-    const bool a_as_stored = direct && aligned(A, 16) && lda % 16 == 0;
+    const bool a_as_stored = direct && a_aligned;
     const int kp = static_cast<int>(cdiv(K, 64) * 64), kb = static_cast<int>(cdiv(K, 16) * 16);
     const size_t a_row = a_as_stored ? 0 : direct ? static_cast<size_t>(kb) : static_cast<size_t>(kp) * 2;
 
@@ -145,24 +184,32 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
         }
         const long long tiles = sg::int8_most_tiles(per, experts, a.nt) * ch_tiles;
         tc = tiles < INT_MAX && (static_cast<long long>(per / a.nt) + experts) * ch_tiles < INT_MAX;
-        a.ksplit = direct ? split_of(tiles, static_cast<int>(cdiv(K, sg::kI8StageK)), v.num_sms) : 1;
+        a.ksplit = tile.ksplit;
     }
-    CUtensorMap tmB, tmA{};
-    int *peaks = nullptr;
+    CUtensorMap tmB, tmA;
+    sg::Int8Copies copies{};
     if (tc) {
         if (!as_stored) {
-            const cudaError_t e =
-                sg::launch_int8_relayout(B, ldb, strideB, transB, experts, N, K, reinterpret_cast<int8_t *>(ws), kb, stream);
-            if (e != cudaSuccess) return from_cuda(e);
-            ++launches;
-            copied |= 2;
-            a.B = reinterpret_cast<int8_t *>(ws);
+            copies.B = B;
+            copies.ldb = ldb;
+            copies.strideB = strideB;
+            copies.b_trans = transB;
+            copies.b_dst = reinterpret_cast<int8_t *>(ws);
+            copies.b_ld = kb;
+            a.B = copies.b_dst;
             a.ldb = kb;
             a.strideB = static_cast<long long>(N) * kb;
-            a.transB = 1;
         }
-        if (!direct) a.peaks = peaks = reinterpret_cast<int *>(ws + b_room - peak_room);
-        ws += b_room;
+        copies.lda = lda;
+        copies.K = K;
+        copies.experts = experts;
+        copies.N = N;
+        if (a_row) {
+            if (!direct) a.peaks = copies.peaks = reinterpret_cast<int *>(ws + b_room - peak_room);
+            ws += b_room;
+            copies.a_dst = ws;
+            copies.a_ld = direct ? kb : kp;
+        }
         // a single matrix has any (aligned) matrix stride
         const long long stride = experts > 1 ? a.strideB : a.ldb * static_cast<long long>(N);
         tc = sg::encode_map(&tmB, sg::MapType::kInt8, 3, a.B, K, N, experts, a.ldb, stride, sg::kI8StageK,
@@ -174,23 +221,28 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
     }
     if (tc) {
         variant = SGEMM_VARIANT_TC_I8;
+        if (copies.b_dst) copied = 2;
         for (int r0 = 0; r0 < rows; r0 += per) {
             a.row0 = r0;
             a.rows = std::min(per, rows - r0);
-            const int8_t *src = A + static_cast<long long>(r0) * lda;
             cudaError_t e = cudaSuccess;
-            if (!direct) {
-                e = sg::launch_int8_to_f16(src, lda, a.rows, K, ws, kp, peaks, &a.n_peaks, stream);
-            } else if (!a_as_stored) {
-                e = sg::launch_int8_relayout(src, lda, 0, 1, 1, a.rows, K, reinterpret_cast<int8_t *>(ws), kb, stream);
+            if (copies.a_dst || copies.b_dst) {
+                copies.A = A + static_cast<long long>(r0) * lda;
+                copies.a_rows = a.rows;
+                e = sg::launch_int8_copies(&copies, stream);
+                a.n_peaks = copies.a_blocks;
+                copies.b_dst = nullptr;  // once
+                ++launches;
             }
-            if (a_row) ++launches;
             if (e == cudaSuccess) e = sg::launch_int8_tc(a, tmB, tmA, v.num_sms, v.smem_override, stream);
             if (e != cudaSuccess) return from_cuda(e);
             ++launches;
         }
     } else {
         a.ksplit = 1;
+        a.B = B;  // as stored
+        a.ldb = ldb;
+        a.strideB = strideB;
         const cudaError_t e = sg::launch_int8_generic(a, stream);
         if (e != cudaSuccess) return from_cuda(e);
         ++launches;
