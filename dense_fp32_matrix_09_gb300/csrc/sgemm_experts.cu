@@ -53,33 +53,47 @@ struct alignas(16) Pack8 {
     T v[kV];
 };
 
-// p[0..7] (n < 8 at the end of a row: zeros beyond); VEC: p is 16-byte aligned.
-template <class T, bool VEC>
-__device__ __forceinline__ Pack8<T> load8(const T *p, int n) {
+// Piece c of a row of `width` elements that `TPR` threads share: 8 consecutive
+// elements a thread where VEC says that rows start on 16-byte boundaries and
+// divide into eights, else 8 elements TPR apart, so that a warp's loads and
+// stores are contiguous either way.  One layout for loads and stores, and no
+// branch between the loads of several pieces: they are all in flight together.
+template <int TPR, bool VEC>
+__device__ __forceinline__ bool inside(int c, int lane, int width) {
+    return (VEC ? (c * TPR + lane) * kV : c * kV * TPR + lane) < width;
+}
+template <class T, int TPR, bool VEC>
+__device__ __forceinline__ Pack8<T> load8(const T *row, int c, int lane, int width) {
     Pack8<T> r;
-    if (VEC && n >= kV) {
+    if (VEC) {
         constexpr int kWords = static_cast<int>(sizeof(T)) * kV / 16;
+        const uint4 *p = reinterpret_cast<const uint4 *>(row + (c * TPR + lane) * kV);
         uint4 *d = reinterpret_cast<uint4 *>(&r);
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) d[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        for (int i = 0; i < kWords; ++i) d[i] = inside<TPR, VEC>(c, lane, width) ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
     } else {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) r.v[i] = i < n ? p[i] : T(0.f);
+        for (int e = 0; e < kV; ++e) {
+            const int at = (c * kV + e) * TPR + lane;
+            r.v[e] = at < width ? row[at] : T(0.f);
+        }
     }
     return r;
 }
-
-template <class T, bool VEC>
-__device__ __forceinline__ void store8(T *p, const Pack8<T> &r, int n) {
-    if (VEC && n >= kV) {
+template <class T, int TPR, bool VEC>
+__device__ __forceinline__ void store8(T *row, int c, int lane, int width, const Pack8<T> &r) {
+    if (VEC) {
         constexpr int kWords = static_cast<int>(sizeof(T)) * kV / 16;
         const uint4 *s = reinterpret_cast<const uint4 *>(&r);
+        if (inside<TPR, VEC>(c, lane, width))
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4 *>(p)[i] = s[i];
+            for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4 *>(row + (c * TPR + lane) * kV)[i] = s[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-            if (i < n) p[i] = r.v[i];
+        for (int e = 0; e < kV; ++e) {
+            const int at = (c * kV + e) * TPR + lane;
+            if (at < width) row[at] = r.v[e];
+        }
     }
 }
 
@@ -102,7 +116,7 @@ constexpr float kRoundMagic = 12582912.f;
 template <class El, int TPR, bool VEC>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int K, int8_t *__restrict__ Q,
-                long long ldq, float *__restrict__ scale, const int *__restrict__ rows, int choices, int vec_q) {
+                long long ldq, float *__restrict__ scale, const int *__restrict__ rows, int choices) {
     using T = typename El::T;
     constexpr int kThreads = TPR < 256 ? 256 : TPR;
     constexpr int kRows = kThreads / TPR, kHeld = 4;
@@ -112,25 +126,20 @@ quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int 
     const int i = blockIdx.x * kRows + threadIdx.x / TPR;
     const bool live = i < M;
     const T *x = X + static_cast<long long>(live ? i : 0) * ldx;
+    const int width = live ? K : 0;
 
     Pack8<T> held[kHeld];
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c) held[c] = load8<T, TPR, VEC>(x, c, lane, width);
     unsigned top = 0;  // max of |x| as bits: NaN above infinity above every number
-    if (live) {
 #pragma unroll
-        for (int c = 0; c < kHeld; ++c) {
-            const int p = (c * TPR + lane) * kV;
-            if (p < K) held[c] = load8<T, VEC>(x + p, K - p);
-        }
+    for (int c = 0; c < kHeld; ++c)
 #pragma unroll
-        for (int c = 0; c < kHeld; ++c)
-            if ((c * TPR + lane) * kV < K)
+        for (int e = 0; e < kV; ++e) top = max(top, __float_as_uint(El::up(held[c].v[e])) & 0x7fffffffu);
+    for (int c = kHeld; c * kV * TPR < width; ++c) {
+        const Pack8<T> h = load8<T, TPR, VEC>(x, c, lane, width);
 #pragma unroll
-                for (int e = 0; e < kV; ++e) top = max(top, __float_as_uint(El::up(held[c].v[e])) & 0x7fffffffu);
-        for (int p = (kHeld * TPR + lane) * kV; p < K; p += TPR * kV) {
-            const Pack8<T> h = load8<T, VEC>(x + p, K - p);
-#pragma unroll
-            for (int e = 0; e < kV; ++e) top = max(top, __float_as_uint(El::up(h.v[e])) & 0x7fffffffu);
-        }
+        for (int e = 0; e < kV; ++e) top = max(top, __float_as_uint(El::up(h.v[e])) & 0x7fffffffu);
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if (TPR > 32) {
@@ -149,38 +158,39 @@ quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int 
     const bool zero = !finite || m < kSmallestMax;
     const float inv = zero ? 0.f : __fdiv_rn(127.f, m);
     const float s = !finite ? __uint_as_float(0x7fc00000u) : zero ? 0.f : __fdiv_rn(m, 127.f);
+    const unsigned keep = zero ? 0u : 0xffffffffu;
 
     auto quantized = [&](const Pack8<T> &h) {
-        uint2 w;
         unsigned b[kV];
 #pragma unroll
         for (int e = 0; e < kV; ++e)
-            b[e] = __float_as_uint(__fadd_rn(__fmul_rn(zero ? 0.f : El::up(h.v[e]), inv), kRoundMagic));
-        w.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-        w.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+            b[e] = __float_as_uint(__fadd_rn(__fmul_rn(El::up(h.v[e]), inv), kRoundMagic));
+        uint2 w;
+        w.x = keep & __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        w.y = keep & __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
         return w;
     };
-    auto put = [&](int8_t *q, int p, uint2 w) {
-        if (vec_q && p + kV <= K) {
-            *reinterpret_cast<uint2 *>(q + p) = w;
+    auto put = [&](int8_t *q, int c, uint2 w) {
+        if (VEC) {
+            if (inside<TPR, VEC>(c, lane, K)) *reinterpret_cast<uint2 *>(q + (c * TPR + lane) * kV) = w;
         } else {
 #pragma unroll
-            for (int e = 0; e < kV; ++e)
-                if (p + e < K) q[p + e] = static_cast<int8_t>((e < 4 ? w.x >> (8 * e) : w.y >> (8 * (e - 4))) & 0xffu);
+            for (int e = 0; e < kV; ++e) {
+                const int at = (c * kV + e) * TPR + lane;
+                if (at < K) q[at] = static_cast<int8_t>((e < 4 ? w.x >> (8 * e) : w.y >> (8 * (e - 4))) & 0xffu);
+            }
         }
     };
     uint2 packed[kHeld];
 #pragma unroll
-    for (int c = 0; c < kHeld; ++c)
-        if ((c * TPR + lane) * kV < K) packed[c] = quantized(held[c]);
+    for (int c = 0; c < kHeld; ++c) packed[c] = quantized(held[c]);
     for (int j = 0; j < choices; ++j) {
         const int r = rows ? row_of(rows, static_cast<long long>(i) * choices + j, M * choices) : i;
         if (r < 0) continue;
         int8_t *q = Q + static_cast<long long>(r) * ldq;
 #pragma unroll
-        for (int c = 0; c < kHeld; ++c)
-            if ((c * TPR + lane) * kV < K) put(q, (c * TPR + lane) * kV, packed[c]);
-        for (int p = (kHeld * TPR + lane) * kV; p < K; p += TPR * kV) put(q, p, quantized(load8<T, VEC>(x + p, K - p)));
+        for (int c = 0; c < kHeld; ++c) put(q, c, packed[c]);
+        for (int c = kHeld; c * kV * TPR < K; ++c) put(q, c, quantized(load8<T, TPR, VEC>(x, c, lane, K)));
         if (lane == 0) scale[r] = s;
     }
 }
@@ -190,7 +200,6 @@ cudaError_t quantize_typed(const MoveArgs &a, int num_sms, cudaStream_t stream) 
     using T = typename El::T;
     const T *X = static_cast<const T *>(a.X);
     int8_t *Q = static_cast<int8_t *>(a.Y);
-    const int vec_q = (reinterpret_cast<uintptr_t>(Q) % 8 == 0 && a.ldy % 8 == 0) ? 1 : 0;
     // Threads a row: enough that it stays in registers (32 elements a thread),
     // and, with too few rows to fill the GPU, more of them so that each thread
     // loads less.
@@ -201,7 +210,7 @@ cudaError_t quantize_typed(const MoveArgs &a, int num_sms, cudaStream_t stream) 
     return launch_dependent(quantize_kernel<El, TPR, VEC>,                                                       \
                             dim3((a.tokens + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1)),    \
                             dim3(TPR < 256 ? 256 : TPR), 0, stream, 1, X, a.ldx, a.tokens, a.width, Q, a.ldy,    \
-                            a.scale, a.rows, a.choices, vec_q)
+                            a.scale, a.rows, a.choices)
     if (want <= 32) SG_QUANT(32);
     if (want <= 128) SG_QUANT(128);
     if (want <= 256) SG_QUANT(256);
@@ -316,8 +325,10 @@ sort_kernel(const int *__restrict__ ids, int slots, int experts, int steps, int 
 
 // ---- rows to the experts --------------------------------------------------------
 // Row t of X to rows[t * choices + j] of Y: read once, written up to `choices`
-// times.  One thread and step: U units of 16 bytes (or one element without
-// VEC), the loads of all of them in flight before the first store.
+// times.  kMoves units (the widest that the rows' alignment allows, up to 16
+// bytes) a thread, all loaded before the first store.
+constexpr int kMoves = 4;
+
 template <class Unit>
 __global__ void __launch_bounds__(256)
 move_kernel(const Unit *__restrict__ X, long long ldx, int tokens, int choices, int width, const int *__restrict__ rows,
@@ -325,19 +336,26 @@ move_kernel(const Unit *__restrict__ X, long long ldx, int tokens, int choices, 
     griddep_wait();
     griddep_launch_dependents();
     const int slots = tokens * choices;
+    const int c0 = blockIdx.x * (256 * kMoves) + threadIdx.x;
     for (int t = blockIdx.y; t < tokens; t += gridDim.y) {
-        const int c = blockIdx.x * 256 + threadIdx.x;
-        if (c >= width) continue;
-        const Unit v = X[static_cast<long long>(t) * ldx + c];
+        const Unit *x = X + static_cast<long long>(t) * ldx;
+        Unit v[kMoves];
+#pragma unroll
+        for (int m = 0; m < kMoves; ++m) v[m] = c0 + m * 256 < width ? x[c0 + m * 256] : Unit{};
         for (int j = 0; j < choices; ++j) {
             const int r = row_of(rows, static_cast<long long>(t) * choices + j, slots);
-            if (r >= 0) Y[static_cast<long long>(r) * ldy + c] = v;
+            if (r < 0) continue;
+            Unit *y = Y + static_cast<long long>(r) * ldy;
+#pragma unroll
+            for (int m = 0; m < kMoves; ++m)
+                if (c0 + m * 256 < width) y[c0 + m * 256] = v[m];
         }
     }
 }
 
 // ---- rows from the experts ------------------------------------------------------
-// out[t] = sum_j w[t,j] * Y[rows[t,j]] (w NULL: the plain sum).
+// out[t] = sum_j w[t,j] * Y[rows[t,j]] (w NULL: the plain sum); four rows' loads
+// in flight at a time.
 template <class El, bool VEC>
 __global__ void __launch_bounds__(256)
 gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, int choices, int width,
@@ -346,10 +364,8 @@ gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, i
     using T = typename El::T;
     griddep_wait();
     griddep_launch_dependents();
-    const int slots = tokens * choices;
+    const int slots = tokens * choices, c = blockIdx.x, lane = threadIdx.x;
     for (int t = blockIdx.y; t < tokens; t += gridDim.y) {
-        const int p = (blockIdx.x * 256 + threadIdx.x) * kV;
-        if (p >= width) continue;
         float sum[kV] = {};
         for (int j0 = 0; j0 < choices; j0 += 4) {
             Pack8<T> y[4];
@@ -359,12 +375,8 @@ gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, i
                 const long long slot = static_cast<long long>(t) * choices + j0 + j;
                 const int r = j0 + j < choices ? row_of(rows, slot, slots) : -1;
                 w[j] = r >= 0 && weights ? __ldg(weights + slot) : 1.f;
-                if (r >= 0) {
-                    y[j] = load8<T, VEC>(Y + static_cast<long long>(r) * ldy + p, width - p);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kV; ++e) y[j].v[e] = T(0.f);
-                }
+                // (a row that does not exist has no elements: zeros)
+                y[j] = load8<T, 256, VEC>(Y + static_cast<long long>(r >= 0 ? r : 0) * ldy, c, lane, r >= 0 ? width : 0);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -374,7 +386,7 @@ gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, i
         Pack8<T> o;
 #pragma unroll
         for (int e = 0; e < kV; ++e) o.v[e] = El::down(sum[e]);
-        store8<T, VEC>(out + static_cast<long long>(t) * ldo + p, o, width - p);
+        store8<T, 256, VEC>(out + static_cast<long long>(t) * ldo, c, lane, width, o);
     }
 }
 
@@ -392,7 +404,7 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
     __shared__ float part[8][J];
     griddep_wait();
     griddep_launch_dependents();
-    const int slots = tokens * choices;
+    const int slots = tokens * choices, lane = threadIdx.x;
     for (int t = blockIdx.x; t < tokens; t += gridDim.x) {
         const T *g = dO + static_cast<long long>(t) * lddo;
         for (int j0 = 0; j0 < choices; j0 += J) {
@@ -405,27 +417,28 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
                 w[j] = r[j] >= 0 ? __ldg(weights + slot) : 0.f;
                 dot[j] = 0.f;
             }
-            for (int p = threadIdx.x * kV; p < width; p += 256 * kV) {
-                const Pack8<T> gv = load8<T, VEC>(g + p, width - p);
+            for (int c = 0; c * 256 * kV < width; ++c) {
+                const Pack8<T> gv = load8<T, 256, VEC>(g, c, lane, width);
                 Pack8<T> y[J];
 #pragma unroll
                 for (int j = 0; j < J; ++j)
-                    if (r[j] >= 0) y[j] = load8<T, VEC>(Y + static_cast<long long>(r[j]) * ldy + p, width - p);
+                    y[j] = load8<T, 256, VEC>(Y + static_cast<long long>(r[j] >= 0 ? r[j] : 0) * ldy, c, lane,
+                                              r[j] >= 0 ? width : 0);
 #pragma unroll
-                for (int j = 0; j < J; ++j)
-                    if (r[j] >= 0) {
-                        Pack8<T> o;
+                for (int j = 0; j < J; ++j) {
+                    Pack8<T> o;
 #pragma unroll
-                        for (int e = 0; e < kV; ++e) {
-                            const float d = El::up(gv.v[e]);
-                            dot[j] = fmaf(d, El::up(y[j].v[e]), dot[j]);
-                            o.v[e] = El::down(w[j] * d);
-                        }
-                        store8<T, VEC>(dY + static_cast<long long>(r[j]) * lddy + p, o, width - p);
+                    for (int e = 0; e < kV; ++e) {
+                        const float d = El::up(gv.v[e]);
+                        dot[j] = fmaf(d, El::up(y[j].v[e]), dot[j]);
+                        o.v[e] = El::down(w[j] * d);
                     }
+                    if (r[j] >= 0) store8<T, 256, VEC>(dY + static_cast<long long>(r[j]) * lddy, c, lane, width, o);
+                }
             }
 #pragma unroll
             for (int j = 0; j < J; ++j) {
+                if (r[j] < 0) dot[j] = 0.f;  // not 0 * dO, which a non-finite dO makes NaN
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
                 if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = dot[j];
@@ -451,7 +464,7 @@ constexpr int kMaxGridY = 65535;
 template <class El>
 cudaError_t gather_typed(const MoveArgs &a, cudaStream_t stream) {
     using T = typename El::T;
-    const bool vec = vec_ok(a.Y, a.ldy, sizeof(T)) && vec_ok(a.X, a.ldx, sizeof(T));
+    const bool vec = a.width % kV == 0 && vec_ok(a.Y, a.ldy, sizeof(T)) && vec_ok(a.X, a.ldx, sizeof(T));
     const dim3 grid((a.width + 256 * kV - 1) / (256 * kV), a.tokens < kMaxGridY ? a.tokens : kMaxGridY);
     return launch_dependent(vec ? gather_kernel<El, true> : gather_kernel<El, false>, grid, dim3(256), 0, stream, 1,
                             static_cast<const T *>(a.Y), a.ldy, a.tokens, a.choices, a.width, a.rows, a.weights,
@@ -461,7 +474,8 @@ cudaError_t gather_typed(const MoveArgs &a, cudaStream_t stream) {
 template <class El, int J>
 cudaError_t combine_grad_j(const MoveArgs &a, cudaStream_t stream) {
     using T = typename El::T;
-    const bool vec = vec_ok(a.X, a.ldx, sizeof(T)) && vec_ok(a.Y, a.ldy, sizeof(T)) && vec_ok(a.dY, a.lddy, sizeof(T));
+    const bool vec = a.width % kV == 0 && vec_ok(a.X, a.ldx, sizeof(T)) && vec_ok(a.Y, a.ldy, sizeof(T)) &&
+                     vec_ok(a.dY, a.lddy, sizeof(T));
     return launch_dependent(vec ? combine_grad_kernel<El, J, true> : combine_grad_kernel<El, J, false>,
                             dim3(a.tokens), dim3(256), 0, stream, 1, static_cast<const T *>(a.X), a.ldx,
                             static_cast<const T *>(a.Y), a.ldy, a.tokens, a.choices, a.width, a.rows, a.weights,
@@ -477,24 +491,24 @@ cudaError_t combine_grad_typed(const MoveArgs &a, cudaStream_t stream) {
 
 template <class Unit>
 cudaError_t move_units(const MoveArgs &a, int size, cudaStream_t stream) {
-    const int per = static_cast<int>(sizeof(Unit)) / size;
-    const int width = a.width / per;
-    const dim3 grid((width + 255) / 256, a.tokens < kMaxGridY ? a.tokens : kMaxGridY);
+    const int width = static_cast<int>(static_cast<long long>(a.width) * size / static_cast<int>(sizeof(Unit)));
+    const dim3 grid((width + 256 * kMoves - 1) / (256 * kMoves), a.tokens < kMaxGridY ? a.tokens : kMaxGridY);
     return launch_dependent(move_kernel<Unit>, grid, dim3(256), 0, stream, 1, static_cast<const Unit *>(a.X),
-                            a.ldx / per, a.tokens, a.choices, width, a.rows, static_cast<Unit *>(a.Y), a.ldy / per);
+                            a.ldx * size / static_cast<int>(sizeof(Unit)), a.tokens, a.choices, width, a.rows,
+                            static_cast<Unit *>(a.Y), a.ldy * size / static_cast<int>(sizeof(Unit)));
 }
 
 }  // namespace
 
 cudaError_t launch_quantize(int type, const MoveArgs &a, int num_sms, cudaStream_t stream) {
+    const bool vec = a.width % kV == 0 && vec_ok(a.X, a.ldx, type == SGEMM_IN_F32 ? 4 : 2) &&
+                     reinterpret_cast<uintptr_t>(a.Y) % kV == 0 && a.ldy % kV == 0;
     if (type == SGEMM_IN_F32)
-        return vec_ok(a.X, a.ldx, 4) ? quantize_typed<ElF32, true>(a, num_sms, stream)
-                                     : quantize_typed<ElF32, false>(a, num_sms, stream);
+        return vec ? quantize_typed<ElF32, true>(a, num_sms, stream) : quantize_typed<ElF32, false>(a, num_sms, stream);
     if (type == SGEMM_IN_BF16)
-        return vec_ok(a.X, a.ldx, 2) ? quantize_typed<ElBF16, true>(a, num_sms, stream)
-                                     : quantize_typed<ElBF16, false>(a, num_sms, stream);
-    return vec_ok(a.X, a.ldx, 2) ? quantize_typed<ElF16, true>(a, num_sms, stream)
-                                 : quantize_typed<ElF16, false>(a, num_sms, stream);
+        return vec ? quantize_typed<ElBF16, true>(a, num_sms, stream)
+                   : quantize_typed<ElBF16, false>(a, num_sms, stream);
+    return vec ? quantize_typed<ElF16, true>(a, num_sms, stream) : quantize_typed<ElF16, false>(a, num_sms, stream);
 }
 
 cudaError_t sort_prepare() {
@@ -533,9 +547,14 @@ cudaError_t launch_sort(const int *ids, int slots, int experts, int *offsets, in
 
 cudaError_t launch_dispatch(int type, const MoveArgs &a, cudaStream_t stream) {
     const int size = type == SGEMM_IN_F32 ? 4 : 2;
-    const bool vec = vec_ok(a.X, a.ldx, size) && vec_ok(a.Y, a.ldy, size) && (a.width * size) % 16 == 0;
-    if (vec) return move_units<uint4>(a, size, stream);
-    return size == 4 ? move_units<uint32_t>(a, size, stream) : move_units<uint16_t>(a, size, stream);
+    // the largest power of two that divides every row's start and length
+    const uintptr_t all = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.Y) |
+                          static_cast<uintptr_t>(a.ldx * size) | static_cast<uintptr_t>(a.ldy * size) |
+                          static_cast<uintptr_t>(static_cast<long long>(a.width) * size);
+    if (all % 16 == 0) return move_units<uint4>(a, size, stream);
+    if (all % 8 == 0) return move_units<uint2>(a, size, stream);
+    if (all % 4 == 0) return move_units<uint32_t>(a, size, stream);
+    return move_units<uint16_t>(a, size, stream);
 }
 
 cudaError_t launch_gather(int type, const MoveArgs &a, cudaStream_t stream) {
