@@ -234,9 +234,10 @@ struct MoveArgs {
 // Y (int8) and scale = the quantized rows of X.
 cudaError_t launch_quantize(int type, const MoveArgs &a, int num_sms, cudaStream_t stream);
 cudaError_t sort_prepare();
-// hist: hist_ints ints of workspace.
+// hist: workspace; with hist_ints ints of it up to sort_most_slots slots can be sorted.
+int sort_most_slots(size_t hist_ints, int experts);
 cudaError_t launch_sort(const int *ids, int slots, int experts, int *offsets, int *rows, int *source, int *hist,
-                        size_t hist_ints, int *launches, cudaStream_t stream);
+                        int *launches, cudaStream_t stream);
 cudaError_t launch_dispatch(int type, const MoveArgs &a, cudaStream_t stream);
 // X (written) = the weighted sums of Y's rows.
 cudaError_t launch_gather(int type, const MoveArgs &a, cudaStream_t stream);

@@ -10,14 +10,17 @@
 //    read a second time, from L2).
 //  * sort_kernel -- the (token, choice) slots in a stable order by expert: a
 //    counting sort.  Within a warp the 32 slots of one step that name the same
-//    expert find one another with match.any and take consecutive places; every
-//    warp keeps its own counts in shared memory, whose exclusive sums over the
-//    warps (and, with several CTAs, over the CTAs before) place each slot.
+//    expert find one another with match.any and take consecutive places, which
+//    stay in registers; every warp keeps its own counts in shared memory, whose
+//    exclusive sums over the warps (and, with several CTAs, over the CTAs before)
+//    place each slot.
 //    Integers only and no atomic whose order matters: the same order every time.
 //  * move_kernel, gather_kernel, combine_grad_kernel -- the rows' way to the
 //    experts, back, and the gradients; each reads and writes every row once
 //    (16 bytes a thread and step where alignment allows), sums in FP32 in
 //    ascending choice order and rounds once.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -53,48 +56,43 @@ struct alignas(16) Pack8 {
     T v[kV];
 };
 
-// Piece c of a row of `width` elements that `TPR` threads share: 8 consecutive
-// elements a thread where VEC says that rows start on 16-byte boundaries and
-// divide into eights, else 8 elements TPR apart, so that a warp's loads and
-// stores are contiguous either way.  One layout for loads and stores, and no
-// branch between the loads of several pieces: they are all in flight together.
-template <int TPR, bool VEC>
-__device__ __forceinline__ bool inside(int c, int lane, int width) {
-    return (VEC ? (c * TPR + lane) * kV : c * kV * TPR + lane) < width;
-}
-template <class T, int TPR, bool VEC>
+// Piece c of a row of `width` elements that `TPR` threads share: 8 elements a
+// thread, in accesses of A consecutive elements (up to 16 bytes; rows start on
+// such boundaries and divide into them) that are TPR * A elements apart, so that
+// a warp's loads and stores are contiguous.  One layout for loads and stores,
+// and no branch between the loads of several pieces: they are all in flight
+// together.
+template <int BYTES>
+struct AccessOf;
+template <>
+struct AccessOf<2> { using T = uint16_t; };
+template <>
+struct AccessOf<4> { using T = uint32_t; };
+template <>
+struct AccessOf<8> { using T = uint2; };
+template <>
+struct AccessOf<16> { using T = uint4; };
+
+template <class T, int TPR, int A>
 __device__ __forceinline__ Pack8<T> load8(const T *row, int c, int lane, int width) {
+    using W = typename AccessOf<static_cast<int>(sizeof(T)) * A>::T;
     Pack8<T> r;
-    if (VEC) {
-        constexpr int kWords = static_cast<int>(sizeof(T)) * kV / 16;
-        const uint4 *p = reinterpret_cast<const uint4 *>(row + (c * TPR + lane) * kV);
-        uint4 *d = reinterpret_cast<uint4 *>(&r);
+    const int at = c * kV * TPR + lane * A;
+    const W *p = reinterpret_cast<const W *>(row + at);
+    W *d = reinterpret_cast<W *>(&r);
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) d[i] = inside<TPR, VEC>(c, lane, width) ? __ldg(p + i) : make_uint4(0, 0, 0, 0);
-    } else {
-#pragma unroll
-        for (int e = 0; e < kV; ++e) {
-            const int at = (c * kV + e) * TPR + lane;
-            r.v[e] = at < width ? row[at] : T(0.f);
-        }
-    }
+    for (int i = 0; i < kV / A; ++i) d[i] = at + i * TPR * A < width ? __ldg(p + i * TPR) : W{};
     return r;
 }
-template <class T, int TPR, bool VEC>
+template <class T, int TPR, int A>
 __device__ __forceinline__ void store8(T *row, int c, int lane, int width, const Pack8<T> &r) {
-    if (VEC) {
-        constexpr int kWords = static_cast<int>(sizeof(T)) * kV / 16;
-        const uint4 *s = reinterpret_cast<const uint4 *>(&r);
-        if (inside<TPR, VEC>(c, lane, width))
+    using W = typename AccessOf<static_cast<int>(sizeof(T)) * A>::T;
+    const int at = c * kV * TPR + lane * A;
+    W *p = reinterpret_cast<W *>(row + at);
+    const W *s = reinterpret_cast<const W *>(&r);
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4 *>(row + (c * TPR + lane) * kV)[i] = s[i];
-    } else {
-#pragma unroll
-        for (int e = 0; e < kV; ++e) {
-            const int at = (c * kV + e) * TPR + lane;
-            if (at < width) row[at] = r.v[e];
-        }
-    }
+    for (int i = 0; i < kV / A; ++i)
+        if (at + i * TPR * A < width) p[i * TPR] = s[i];
 }
 
 // Sorted row of a slot, or -1 for one that has none: a value outside [0, slots)
@@ -113,7 +111,7 @@ constexpr float kSmallestMax = 127.f * 1.17549435e-38f;
 // to even) that sits in the low bits of the sum.
 constexpr float kRoundMagic = 12582912.f;
 
-template <class El, int TPR, bool VEC>
+template <class El, int TPR, int A>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int K, int8_t *__restrict__ Q,
                 long long ldq, float *__restrict__ scale, const int *__restrict__ rows, int choices) {
@@ -130,14 +128,14 @@ quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int 
 
     Pack8<T> held[kHeld];
 #pragma unroll
-    for (int c = 0; c < kHeld; ++c) held[c] = load8<T, TPR, VEC>(x, c, lane, width);
+    for (int c = 0; c < kHeld; ++c) held[c] = load8<T, TPR, A>(x, c, lane, width);
     unsigned top = 0;  // max of |x| as bits: NaN above infinity above every number
 #pragma unroll
     for (int c = 0; c < kHeld; ++c)
 #pragma unroll
         for (int e = 0; e < kV; ++e) top = max(top, __float_as_uint(El::up(held[c].v[e])) & 0x7fffffffu);
     for (int c = kHeld; c * kV * TPR < width; ++c) {
-        const Pack8<T> h = load8<T, TPR, VEC>(x, c, lane, width);
+        const Pack8<T> h = load8<T, TPR, A>(x, c, lane, width);
 #pragma unroll
         for (int e = 0; e < kV; ++e) top = max(top, __float_as_uint(El::up(h.v[e])) & 0x7fffffffu);
     }
@@ -170,15 +168,18 @@ quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int 
         w.y = keep & __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
         return w;
     };
+    // the quantized bytes in the accesses' layout: A at a time
     auto put = [&](int8_t *q, int c, uint2 w) {
-        if (VEC) {
-            if (inside<TPR, VEC>(c, lane, K)) *reinterpret_cast<uint2 *>(q + (c * TPR + lane) * kV) = w;
-        } else {
+        const int at = c * kV * TPR + lane * A;
 #pragma unroll
-            for (int e = 0; e < kV; ++e) {
-                const int at = (c * kV + e) * TPR + lane;
-                if (at < K) q[at] = static_cast<int8_t>((e < 4 ? w.x >> (8 * e) : w.y >> (8 * (e - 4))) & 0xffu);
-            }
+        for (int i = 0; i < kV / A; ++i) {
+            if (at + i * TPR * A >= K) continue;
+            int8_t *p = q + at + i * TPR * A;
+            const uint32_t word = i * A < 4 ? w.x >> (8 * (i * A % 4)) : w.y >> (8 * (i * A % 4));
+            if (A == 8) *reinterpret_cast<uint2 *>(p) = w;
+            else if (A == 4) *reinterpret_cast<uint32_t *>(p) = word;
+            else if (A == 2) *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(word);
+            else *p = static_cast<int8_t>(word);
         }
     };
     uint2 packed[kHeld];
@@ -190,12 +191,12 @@ quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int 
         int8_t *q = Q + static_cast<long long>(r) * ldq;
 #pragma unroll
         for (int c = 0; c < kHeld; ++c) put(q, c, packed[c]);
-        for (int c = kHeld; c * kV * TPR < K; ++c) put(q, c, quantized(load8<T, TPR, VEC>(x, c, lane, K)));
+        for (int c = kHeld; c * kV * TPR < K; ++c) put(q, c, quantized(load8<T, TPR, A>(x, c, lane, K)));
         if (lane == 0) scale[r] = s;
     }
 }
 
-template <class El, bool VEC>
+template <class El, int A>
 cudaError_t quantize_typed(const MoveArgs &a, int num_sms, cudaStream_t stream) {
     using T = typename El::T;
     const T *X = static_cast<const T *>(a.X);
@@ -207,7 +208,7 @@ cudaError_t quantize_typed(const MoveArgs &a, int num_sms, cudaStream_t stream) 
     const int per = few ? kV : 4 * kV;
     const int want = (a.width + per - 1) / per;
 #define SG_QUANT(TPR)                                                                                            \
-    return launch_dependent(quantize_kernel<El, TPR, VEC>,                                                       \
+    return launch_dependent(quantize_kernel<El, TPR, A>,                                                       \
                             dim3((a.tokens + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1)),    \
                             dim3(TPR < 256 ? 256 : TPR), 0, stream, 1, X, a.ldx, a.tokens, a.width, Q, a.ldy,    \
                             a.scale, a.rows, a.choices)
@@ -219,107 +220,112 @@ cudaError_t quantize_typed(const MoveArgs &a, int num_sms, cudaStream_t stream) 
 }
 
 // ---- sort ---------------------------------------------------------------------
-constexpr int kSortWarps = 8, kSortThreads = kSortWarps * 32;
-
-// Shared memory: kSortWarps * E counts of the warps, E places of the CTA.
+// A CTA takes STEPS * 1024 slots, its 32 warps runs of STEPS * 32.  Shared memory:
+// 32 * E counts of the warps, E places of the CTA.
 // PASS 0: one CTA does it all.  PASS 1: each CTA writes the counts of its own
 // slots to hist[cta][E].  PASS 2: each CTA places its slots.
-template <int PASS>
+constexpr int kSortWarps = 32, kSortThreads = kSortWarps * 32;
+
+template <int PASS, int STEPS>
 __global__ void __launch_bounds__(kSortThreads)
-sort_kernel(const int *__restrict__ ids, int slots, int experts, int steps, int *__restrict__ offsets,
-            int *__restrict__ rows, int *__restrict__ source, int *__restrict__ hist) {
+sort_kernel(const int *__restrict__ ids, int slots, int experts, int *__restrict__ offsets, int *__restrict__ rows,
+            int *__restrict__ source, int *__restrict__ hist) {
     extern __shared__ int sh[];
     int *counts = sh, *place = sh + kSortWarps * experts;
     __shared__ int carry[kSortWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const unsigned below = (1u << lane) - 1u;
+    for (int e = tid; e < kSortWarps * experts; e += kSortThreads) counts[e] = 0;
     griddep_wait();
     griddep_launch_dependents();
-    for (int e = tid; e < kSortWarps * experts; e += kSortThreads) counts[e] = 0;
+    const long long first = (static_cast<long long>(blockIdx.x) * kSortWarps + warp) * (STEPS * 32) + lane;
+    int e[STEPS], rank[STEPS];  // the slots' experts (-1: dropped), their places among the warp's
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        e[s] = first + s * 32 < slots ? __ldg(ids + first + s * 32) : -1;
+        if (static_cast<unsigned>(e[s]) >= static_cast<unsigned>(experts)) e[s] = -1;
+    }
     __syncthreads();
-
-    // the CTA's slots: kSortWarps runs of steps * 32, one a warp
-    const long long first = (static_cast<long long>(blockIdx.x) * kSortWarps + warp) * steps * 32;
     int *mine = counts + warp * experts;
-    auto expert_of = [&](long long slot) {
-        const int e = slot < slots ? __ldg(ids + slot) : -1;
-        return static_cast<unsigned>(e) < static_cast<unsigned>(experts) ? e : -1;
-    };
-    for (int s = 0; s < steps; ++s) {
-        const int e = expert_of(first + s * 32 + lane);
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && (same & below) == 0) mine[e] += __popc(same);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const unsigned same = __match_any_sync(0xffffffffu, e[s]);
+        rank[s] = (e[s] >= 0 ? mine[e[s]] : 0) + __popc(same & below);
+        __syncwarp();
+        if (e[s] >= 0 && (same & below) == 0) mine[e[s]] += __popc(same);
         __syncwarp();
     }
     __syncthreads();
-    // counts -> exclusive sums over the warps; place[e] = the CTA's slots of expert e
-    for (int e = tid; e < experts; e += kSortThreads) {
+    // counts -> exclusive sums over the warps; place[x] = the CTA's slots of expert x
+    for (int x = tid; x < experts; x += kSortThreads) {
         int n = 0;
 #pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int c = counts[w * experts + e];
-            counts[w * experts + e] = n;
-            n += c;
+        for (int w0 = 0; w0 < kSortWarps; w0 += 16) {
+            int c[16];
+#pragma unroll
+            for (int w = 0; w < 16; ++w) c[w] = counts[(w0 + w) * experts + x];
+#pragma unroll
+            for (int w = 0; w < 16; ++w) {
+                counts[(w0 + w) * experts + x] = n;
+                n += c[w];
+            }
         }
-        if (PASS == 1) hist[static_cast<long long>(blockIdx.x) * experts + e] = n;
-        place[e] = n;
+        if (PASS == 1) hist[static_cast<long long>(blockIdx.x) * experts + x] = n;
+        place[x] = n;
     }
     if (PASS == 1) return;
     __syncthreads();
-    // total[e] over all CTAs, its exclusive sum over the experts (offsets), and
-    // the slots of earlier CTAs
-    int base = 0;  // sum over the experts done so far
-    for (int e0 = 0; e0 < experts; e0 += kSortThreads) {
-        const int e = e0 + tid;
-        int total = 0, before = 0;
-        if (e < experts) {
-            if (PASS == 0) {
-                total = place[e];
-            } else {
-                for (int c = 0; c < static_cast<int>(gridDim.x); ++c) {
-                    const int n = __ldcg(hist + static_cast<long long>(c) * experts + e);
-                    if (c < static_cast<int>(blockIdx.x)) before += n;
-                    total += n;
+    // the slots of every expert, their exclusive sum over the experts (offsets),
+    // and those of the CTAs before (at most kMaxExperts experts: one each)
+    const int ctas = static_cast<int>(gridDim.x);
+    int total = 0, before = 0;
+    if (tid < experts) {
+        if (PASS == 0) {
+            total = place[tid];
+        } else {
+            for (int c0 = 0; c0 < ctas; c0 += 8) {
+                int n[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    n[c] = c0 + c < ctas ? __ldcg(hist + static_cast<long long>(c0 + c) * experts + tid) : 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    total += n[c];
+                    if (c0 + c < static_cast<int>(blockIdx.x)) before += n[c];
                 }
             }
         }
-        int sum = total;  // inclusive over the warp
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += up;
-        }
-        if (lane == 31) carry[warp] = sum;
-        __syncthreads();
-        int all = 0, lower = 0;
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
-            if (w < warp) lower += carry[w];
-            all += carry[w];
-        }
-        const int start = base + lower + sum - total;
-        if (e < experts) {
-            place[e] = start + before;
-            if (blockIdx.x == 0) offsets[e] = start;
-        }
-        base += all;
-        __syncthreads();
     }
-    if (blockIdx.x == 0 && tid == 0) offsets[experts] = base;
-    for (int s = 0; s < steps; ++s) {
-        const long long slot = first + s * 32 + lane;
-        const int e = expert_of(slot);
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        int r = -1;
-        if (e >= 0) r = place[e] + mine[e] + __popc(same & below);
-        __syncwarp();
-        if (e >= 0 && (same & below) == 0) mine[e] += __popc(same);
-        __syncwarp();
-        if (slot < slots) {
-            rows[slot] = r;
-            if (r >= 0) source[r] = static_cast<int>(slot);
-            if (slot >= base) source[slot] = -1;  // rows past the last expert's hold no slot
-        }
+    int sum = total;  // inclusive over the warp
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += up;
+    }
+    if (lane == 31) carry[warp] = sum;
+    __syncthreads();
+    int all = carry[lane];  // of warp `lane`; then inclusive over the warps
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, all, d);
+        if (lane >= d) all += up;
+    }
+    const int kept = __shfl_sync(0xffffffffu, all, 31);
+    const int lower = warp > 0 ? __shfl_sync(0xffffffffu, all, warp - 1) : 0;
+    if (tid < experts) {
+        place[tid] = lower + sum - total + before;
+        if (blockIdx.x == 0) offsets[tid] = lower + sum - total;
+    }
+    if (blockIdx.x == 0 && tid == 0) offsets[experts] = kept;
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const long long slot = first + s * 32;
+        if (slot >= slots) continue;
+        const int r = e[s] >= 0 ? place[e[s]] + mine[e[s]] + rank[s] : -1;
+        rows[slot] = r;
+        if (r >= 0) source[r] = static_cast<int>(slot);
+        if (slot >= kept) source[slot] = -1;  // rows past the last expert's hold no slot
     }
 }
 
@@ -356,7 +362,7 @@ move_kernel(const Unit *__restrict__ X, long long ldx, int tokens, int choices, 
 // ---- rows from the experts ------------------------------------------------------
 // out[t] = sum_j w[t,j] * Y[rows[t,j]] (w NULL: the plain sum); four rows' loads
 // in flight at a time.
-template <class El, bool VEC>
+template <class El, int A>
 __global__ void __launch_bounds__(256)
 gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, int choices, int width,
               const int *__restrict__ rows, const float *__restrict__ weights, typename El::T *__restrict__ out,
@@ -376,7 +382,7 @@ gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, i
                 const int r = j0 + j < choices ? row_of(rows, slot, slots) : -1;
                 w[j] = r >= 0 && weights ? __ldg(weights + slot) : 1.f;
                 // (a row that does not exist has no elements: zeros)
-                y[j] = load8<T, 256, VEC>(Y + static_cast<long long>(r >= 0 ? r : 0) * ldy, c, lane, r >= 0 ? width : 0);
+                y[j] = load8<T, 256, A>(Y + static_cast<long long>(r >= 0 ? r : 0) * ldy, c, lane, r >= 0 ? width : 0);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -386,7 +392,7 @@ gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, i
         Pack8<T> o;
 #pragma unroll
         for (int e = 0; e < kV; ++e) o.v[e] = El::down(sum[e]);
-        store8<T, 256, VEC>(out + static_cast<long long>(t) * ldo, c, lane, width, o);
+        store8<T, 256, A>(out + static_cast<long long>(t) * ldo, c, lane, width, o);
     }
 }
 
@@ -394,7 +400,7 @@ gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, i
 // dY[rows[t,j]] = w[t,j] * dO[t] and dw[t,j] = <dO[t], Y[rows[t,j]]>: 256
 // threads a token, J choices at a time; the dot products are reduced in a
 // fixed order (within the warp, then over the warps).
-template <class El, int J, bool VEC>
+template <class El, int J, int A>
 __global__ void __launch_bounds__(256)
 combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const typename El::T *__restrict__ Y,
                     long long ldy, int tokens, int choices, int width, const int *__restrict__ rows,
@@ -418,11 +424,11 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
                 dot[j] = 0.f;
             }
             for (int c = 0; c * 256 * kV < width; ++c) {
-                const Pack8<T> gv = load8<T, 256, VEC>(g, c, lane, width);
+                const Pack8<T> gv = load8<T, 256, A>(g, c, lane, width);
                 Pack8<T> y[J];
 #pragma unroll
                 for (int j = 0; j < J; ++j)
-                    y[j] = load8<T, 256, VEC>(Y + static_cast<long long>(r[j] >= 0 ? r[j] : 0) * ldy, c, lane,
+                    y[j] = load8<T, 256, A>(Y + static_cast<long long>(r[j] >= 0 ? r[j] : 0) * ldy, c, lane,
                                               r[j] >= 0 ? width : 0);
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
@@ -433,7 +439,7 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
                         dot[j] = fmaf(d, El::up(y[j].v[e]), dot[j]);
                         o.v[e] = El::down(w[j] * d);
                     }
-                    if (r[j] >= 0) store8<T, 256, VEC>(dY + static_cast<long long>(r[j]) * lddy, c, lane, width, o);
+                    if (r[j] >= 0) store8<T, 256, A>(dY + static_cast<long long>(r[j]) * lddy, c, lane, width, o);
                 }
             }
 #pragma unroll
@@ -455,8 +461,21 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
     }
 }
 
-inline bool vec_ok(const void *p, long long ld, int size) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * size) % 16 == 0;
+// The largest power of two, up to 16, that divides every row's start and length in
+// bytes.
+template <class... Rows>
+int common_alignment(Rows... rows) {
+    const uintptr_t all = (static_cast<uintptr_t>(rows) | ...) | 16u;
+    return static_cast<int>(all & (~all + 1));
+}
+
+// Call f with the elements of an access (an integral constant): 16 bytes, 4 bytes
+// or one element.
+template <int SIZE, class F>
+cudaError_t with_access(int alignment, F &&f) {
+    if (alignment >= 16) return f(std::integral_constant<int, 16 / SIZE>{});
+    if (SIZE < 4 && alignment >= 4) return f(std::integral_constant<int, SIZE < 4 ? 4 / SIZE : 1>{});
+    return f(std::integral_constant<int, 1>{});
 }
 
 constexpr int kMaxGridY = 65535;
@@ -464,22 +483,29 @@ constexpr int kMaxGridY = 65535;
 template <class El>
 cudaError_t gather_typed(const MoveArgs &a, cudaStream_t stream) {
     using T = typename El::T;
-    const bool vec = a.width % kV == 0 && vec_ok(a.Y, a.ldy, sizeof(T)) && vec_ok(a.X, a.ldx, sizeof(T));
+    constexpr int kSize = sizeof(T);
+    const int al = common_alignment(reinterpret_cast<uintptr_t>(a.X), reinterpret_cast<uintptr_t>(a.Y), a.ldx * kSize,
+                                    a.ldy * kSize, static_cast<long long>(a.width) * kSize);
     const dim3 grid((a.width + 256 * kV - 1) / (256 * kV), a.tokens < kMaxGridY ? a.tokens : kMaxGridY);
-    return launch_dependent(vec ? gather_kernel<El, true> : gather_kernel<El, false>, grid, dim3(256), 0, stream, 1,
-                            static_cast<const T *>(a.Y), a.ldy, a.tokens, a.choices, a.width, a.rows, a.weights,
-                            static_cast<T *>(const_cast<void *>(a.X)), a.ldx);
+    return with_access<kSize>(al, [&](auto n) {
+        return launch_dependent(gather_kernel<El, decltype(n)::value>, grid, dim3(256), 0, stream, 1,
+                                static_cast<const T *>(a.Y), a.ldy, a.tokens, a.choices, a.width, a.rows, a.weights,
+                                static_cast<T *>(const_cast<void *>(a.X)), a.ldx);
+    });
 }
 
 template <class El, int J>
 cudaError_t combine_grad_j(const MoveArgs &a, cudaStream_t stream) {
     using T = typename El::T;
-    const bool vec = a.width % kV == 0 && vec_ok(a.X, a.ldx, sizeof(T)) && vec_ok(a.Y, a.ldy, sizeof(T)) &&
-                     vec_ok(a.dY, a.lddy, sizeof(T));
-    return launch_dependent(vec ? combine_grad_kernel<El, J, true> : combine_grad_kernel<El, J, false>,
-                            dim3(a.tokens), dim3(256), 0, stream, 1, static_cast<const T *>(a.X), a.ldx,
-                            static_cast<const T *>(a.Y), a.ldy, a.tokens, a.choices, a.width, a.rows, a.weights,
-                            static_cast<T *>(a.dY), a.lddy, a.scale);
+    constexpr int kSize = sizeof(T);
+    const int al = common_alignment(reinterpret_cast<uintptr_t>(a.X), reinterpret_cast<uintptr_t>(a.Y),
+                                    reinterpret_cast<uintptr_t>(a.dY), a.ldx * kSize, a.ldy * kSize, a.lddy * kSize,
+                                    static_cast<long long>(a.width) * kSize);
+    return with_access<kSize>(al, [&](auto n) {
+        return launch_dependent(combine_grad_kernel<El, J, decltype(n)::value>, dim3(a.tokens), dim3(256), 0, stream, 1,
+                                static_cast<const T *>(a.X), a.ldx, static_cast<const T *>(a.Y), a.ldy, a.tokens,
+                                a.choices, a.width, a.rows, a.weights, static_cast<T *>(a.dY), a.lddy, a.scale);
+    });
 }
 
 template <class El>
@@ -500,60 +526,76 @@ cudaError_t move_units(const MoveArgs &a, int size, cudaStream_t stream) {
 
 }  // namespace
 
+template <class El>
+static cudaError_t quantize_aligned(const MoveArgs &a, int num_sms, cudaStream_t stream) {
+    constexpr int kSize = sizeof(typename El::T);
+    // an access's bytes of Q are aligned as its elements of X are
+    const int al = common_alignment(reinterpret_cast<uintptr_t>(a.X), a.ldx * kSize, static_cast<long long>(a.width) * kSize,
+                                    reinterpret_cast<uintptr_t>(a.Y) * kSize, a.ldy * kSize);
+    return with_access<kSize>(al, [&](auto n) { return quantize_typed<El, decltype(n)::value>(a, num_sms, stream); });
+}
+
 cudaError_t launch_quantize(int type, const MoveArgs &a, int num_sms, cudaStream_t stream) {
-    const bool vec = a.width % kV == 0 && vec_ok(a.X, a.ldx, type == SGEMM_IN_F32 ? 4 : 2) &&
-                     reinterpret_cast<uintptr_t>(a.Y) % kV == 0 && a.ldy % kV == 0;
-    if (type == SGEMM_IN_F32)
-        return vec ? quantize_typed<ElF32, true>(a, num_sms, stream) : quantize_typed<ElF32, false>(a, num_sms, stream);
-    if (type == SGEMM_IN_BF16)
-        return vec ? quantize_typed<ElBF16, true>(a, num_sms, stream)
-                   : quantize_typed<ElBF16, false>(a, num_sms, stream);
-    return vec ? quantize_typed<ElF16, true>(a, num_sms, stream) : quantize_typed<ElF16, false>(a, num_sms, stream);
+    if (type == SGEMM_IN_F32) return quantize_aligned<ElF32>(a, num_sms, stream);
+    if (type == SGEMM_IN_BF16) return quantize_aligned<ElBF16>(a, num_sms, stream);
+    return quantize_aligned<ElF16>(a, num_sms, stream);
 }
 
 cudaError_t sort_prepare() {
     const int most = (kSortWarps + 1) * kMaxExperts * static_cast<int>(sizeof(int));
-    for (auto *k : {sort_kernel<0>, sort_kernel<1>, sort_kernel<2>}) {
+    for (auto *k : {sort_kernel<0, 1>, sort_kernel<0, 2>, sort_kernel<0, 4>, sort_kernel<1, 1>, sort_kernel<2, 1>,
+                    sort_kernel<1, 4>, sort_kernel<2, 4>, sort_kernel<1, 16>, sort_kernel<2, 16>}) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
-cudaError_t launch_sort(const int *ids, int slots, int experts, int *offsets, int *rows, int *source, int *hist,
-                        size_t hist_ints, int *launches, cudaStream_t stream) {
-    const int smem = (kSortWarps + 1) * experts * static_cast<int>(sizeof(int));
-    // Up to 16 steps of 256 slots in one CTA (one launch); beyond, CTAs of 4
-    // steps, or as many steps as keep the counts within the workspace and
-    // under 256 CTAs (each CTA reads the counts of all).
-    *launches = 1;
-    if (slots <= 16 * kSortThreads) {
-        const int steps = slots > kSortThreads ? (slots + kSortThreads - 1) / kSortThreads : 1;
-        return launch_dependent(sort_kernel<0>, dim3(1), dim3(kSortThreads), smem, stream, 1, ids, slots, experts,
-                                steps, offsets, rows, source, hist);
-    }
-    const long long most = static_cast<long long>(hist_ints) / experts;
-    const int ctas_most = static_cast<int>(most < 256 ? most : 256);
-    int steps = (slots + kSortThreads * ctas_most - 1) / (kSortThreads * ctas_most);
-    if (steps < 4) steps = 4;
-    const int ctas = (slots + kSortThreads * steps - 1) / (kSortThreads * steps);
-    *launches = 2;
-    const cudaError_t e = launch_dependent(sort_kernel<1>, dim3(ctas), dim3(kSortThreads), smem, stream, 1, ids, slots,
-                                           experts, steps, offsets, rows, source, hist);
+// Counting and placing in two launches, each CTA reading the counts of all.
+template <int STEPS>
+static cudaError_t sort_two(const int *ids, int slots, int experts, int *offsets, int *rows, int *source, int *hist,
+                            int smem, cudaStream_t stream) {
+    const dim3 ctas(static_cast<unsigned>((static_cast<long long>(slots) + kSortThreads * STEPS - 1) / (kSortThreads * STEPS)));
+    const cudaError_t e = launch_dependent(sort_kernel<1, STEPS>, ctas, dim3(kSortThreads), smem, stream, 1, ids, slots,
+                                           experts, offsets, rows, source, hist);
     if (e != cudaSuccess) return e;
-    return launch_dependent(sort_kernel<2>, dim3(ctas), dim3(kSortThreads), smem, stream, 1, ids, slots, experts,
-                            steps, offsets, rows, source, hist);
+    return launch_dependent(sort_kernel<2, STEPS>, ctas, dim3(kSortThreads), smem, stream, 1, ids, slots, experts,
+                            offsets, rows, source, hist);
+}
+
+int sort_most_slots(size_t hist_ints, int experts) {
+    const unsigned long long most = hist_ints / experts * (16ull * kSortThreads);
+    return most < 0x7fffffffull ? static_cast<int>(most) : 0x7fffffff;
+}
+
+cudaError_t launch_sort(const int *ids, int slots, int experts, int *offsets, int *rows, int *source, int *hist,
+                        int *launches, cudaStream_t stream) {
+    const int smem = (kSortWarps + 1) * experts * static_cast<int>(sizeof(int));
+    // Up to 4096 slots in one CTA, one launch; beyond, CTAs of 1024 slots up to 32
+    // of them, then 4096, and 16384 where that would be more than 128 (each CTA
+    // reads the counts of all).
+    *launches = slots <= 4 * kSortThreads ? 1 : 2;
+    if (slots <= kSortThreads)
+        return launch_dependent(sort_kernel<0, 1>, dim3(1), dim3(kSortThreads), smem, stream, 1, ids, slots, experts,
+                                offsets, rows, source, hist);
+    if (slots <= 2 * kSortThreads)
+        return launch_dependent(sort_kernel<0, 2>, dim3(1), dim3(kSortThreads), smem, stream, 1, ids, slots, experts,
+                                offsets, rows, source, hist);
+    if (slots <= 4 * kSortThreads)
+        return launch_dependent(sort_kernel<0, 4>, dim3(1), dim3(kSortThreads), smem, stream, 1, ids, slots, experts,
+                                offsets, rows, source, hist);
+    if (slots <= 32 * kSortThreads) return sort_two<1>(ids, slots, experts, offsets, rows, source, hist, smem, stream);
+    if (slots <= 512 * kSortThreads) return sort_two<4>(ids, slots, experts, offsets, rows, source, hist, smem, stream);
+    return sort_two<16>(ids, slots, experts, offsets, rows, source, hist, smem, stream);
 }
 
 cudaError_t launch_dispatch(int type, const MoveArgs &a, cudaStream_t stream) {
     const int size = type == SGEMM_IN_F32 ? 4 : 2;
-    // the largest power of two that divides every row's start and length
-    const uintptr_t all = reinterpret_cast<uintptr_t>(a.X) | reinterpret_cast<uintptr_t>(a.Y) |
-                          static_cast<uintptr_t>(a.ldx * size) | static_cast<uintptr_t>(a.ldy * size) |
-                          static_cast<uintptr_t>(static_cast<long long>(a.width) * size);
-    if (all % 16 == 0) return move_units<uint4>(a, size, stream);
-    if (all % 8 == 0) return move_units<uint2>(a, size, stream);
-    if (all % 4 == 0) return move_units<uint32_t>(a, size, stream);
+    const int al = common_alignment(reinterpret_cast<uintptr_t>(a.X), reinterpret_cast<uintptr_t>(a.Y), a.ldx * size,
+                                    a.ldy * size, static_cast<long long>(a.width) * size);
+    if (al >= 16) return move_units<uint4>(a, size, stream);
+    if (al >= 8) return move_units<uint2>(a, size, stream);
+    if (al >= 4) return move_units<uint32_t>(a, size, stream);
     return move_units<uint16_t>(a, size, stream);
 }
 

@@ -364,9 +364,10 @@ int sgemm_expert_sort(sgemm_handle_t h, int tokens, int choices, int experts, co
     if (i.meets(o) || i.meets(r) || i.meets(s) || o.meets(r) || o.meets(s) || r.meets(s)) return SGEMM_ERR_ALIAS;
     sg::HandleView v;
     sg::view_of(h, &v);
+    if (slots > sg::sort_most_slots(v.ws_floats, experts)) return SGEMM_ERR_INVALID_VALUE;
     int launches = 0;
     const int rc = from_cuda(sg::launch_sort(ids, slots, experts, offsets, rows, source, reinterpret_cast<int *>(v.d_ws),
-                                             v.ws_floats, &launches, static_cast<cudaStream_t>(stream)));
+                                             &launches, static_cast<cudaStream_t>(stream)));
     sg::record_call(h, -1, 1, rc == SGEMM_OK ? launches : 0, 0);
     return rc;
 }

@@ -331,7 +331,9 @@ int sgemm_quantize_rows(sgemm_handle_t h, int type, int M, int K, const void *X,
  * a dropped one; source[r] the slot of row r, -1 for the rows from
  * offsets[experts] on.  (experts + 1, tokens*choices and tokens*choices ints.)
  * The order is the same on every call.  experts is 1 .. 1024 and
- * tokens*choices < 2^31.
+ * tokens*choices < 2^31 (sort: at most 2^14 * floor(12582912 / experts) slots, 201
+ * million with 1024 experts -- the counts that its workspace holds -- else
+ * SGEMM_ERR_INVALID_VALUE).
  *
  * The other calls move rows of `width` elements of `type`; the tokens' side has
  * `tokens` rows, the experts' side tokens*choices rows, of which those that no
