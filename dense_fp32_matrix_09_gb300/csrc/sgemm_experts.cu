@@ -10,7 +10,7 @@
 //    read a second time, from L2).
 //  * sort_kernel -- the (token, choice) slots in a stable order by expert: a
 //    counting sort.  Within a warp the 32 slots of one step that name the same
-//    expert find one another with match.any and take consecutive places, which
+//    expert find one another by ballots and take consecutive places, which
 //    stay in registers; every warp keeps its own counts in shared memory, whose
 //    exclusive sums over the warps (and, with several CTAs, over the CTAs before)
 //    place each slot.
@@ -226,6 +226,17 @@ cudaError_t quantize_typed(const MoveArgs &a, int num_sms, cudaStream_t stream) 
 // slots to hist[cta][E].  PASS 2: each CTA places its slots.
 constexpr int kSortWarps = 32, kSortThreads = kSortWarps * 32;
 
+// The lanes whose key agrees with this lane's in its lowest `bits` bits: a ballot a
+// bit (7 for 64 experts; match.any takes about as long for every distinct key).
+__device__ __forceinline__ unsigned same_key(int key, int bits) {
+    unsigned same = 0xffffffffu;
+    for (int b = 0; b < bits; ++b) {
+        const unsigned v = __ballot_sync(0xffffffffu, (key >> b) & 1);
+        same &= (key >> b) & 1 ? v : ~v;
+    }
+    return same;
+}
+
 template <int PASS, int STEPS>
 __global__ void __launch_bounds__(kSortThreads)
 sort_kernel(const int *__restrict__ ids, int slots, int experts, int *__restrict__ offsets, int *__restrict__ rows,
@@ -235,6 +246,7 @@ sort_kernel(const int *__restrict__ ids, int slots, int experts, int *__restrict
     __shared__ int carry[kSortWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const unsigned below = (1u << lane) - 1u;
+    const int bits = 33 - __clz(experts - 1);  // of 0 .. experts - 1 and of -1, told apart by one bit more
     for (int e = tid; e < kSortWarps * experts; e += kSortThreads) counts[e] = 0;
     griddep_wait();
     griddep_launch_dependents();
@@ -249,7 +261,7 @@ sort_kernel(const int *__restrict__ ids, int slots, int experts, int *__restrict
     int *mine = counts + warp * experts;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-        const unsigned same = __match_any_sync(0xffffffffu, e[s]);
+        const unsigned same = same_key(e[s], bits);
         rank[s] = (e[s] >= 0 ? mine[e[s]] : 0) + __popc(same & below);
         __syncwarp();
         if (e[s] >= 0 && (same & below) == 0) mine[e[s]] += __popc(same);
@@ -543,7 +555,7 @@ cudaError_t launch_quantize(int type, const MoveArgs &a, int num_sms, cudaStream
 
 cudaError_t sort_prepare() {
     const int most = (kSortWarps + 1) * kMaxExperts * static_cast<int>(sizeof(int));
-    for (auto *k : {sort_kernel<0, 1>, sort_kernel<0, 2>, sort_kernel<0, 4>, sort_kernel<1, 1>, sort_kernel<2, 1>,
+    for (auto *k : {sort_kernel<0, 1>, sort_kernel<0, 2>, sort_kernel<1, 1>, sort_kernel<2, 1>,
                     sort_kernel<1, 4>, sort_kernel<2, 4>, sort_kernel<1, 16>, sort_kernel<2, 16>}) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
@@ -571,18 +583,15 @@ int sort_most_slots(size_t hist_ints, int experts) {
 cudaError_t launch_sort(const int *ids, int slots, int experts, int *offsets, int *rows, int *source, int *hist,
                         int *launches, cudaStream_t stream) {
     const int smem = (kSortWarps + 1) * experts * static_cast<int>(sizeof(int));
-    // Up to 4096 slots in one CTA, one launch; beyond, CTAs of 1024 slots up to 32
-    // of them, then 4096, and 16384 where that would be more than 128 (each CTA
-    // reads the counts of all).
-    *launches = slots <= 4 * kSortThreads ? 1 : 2;
+    // Up to 2048 slots in one CTA, one launch; beyond (4096 slots, 64 experts: 4.8 us
+    // against 6.2), CTAs of 1024 slots up to 32 of them, then 4096, and 16384
+    // where that would be more than 128 (each CTA reads the counts of all).
+    *launches = slots <= 2 * kSortThreads ? 1 : 2;
     if (slots <= kSortThreads)
         return launch_dependent(sort_kernel<0, 1>, dim3(1), dim3(kSortThreads), smem, stream, 1, ids, slots, experts,
                                 offsets, rows, source, hist);
     if (slots <= 2 * kSortThreads)
         return launch_dependent(sort_kernel<0, 2>, dim3(1), dim3(kSortThreads), smem, stream, 1, ids, slots, experts,
-                                offsets, rows, source, hist);
-    if (slots <= 4 * kSortThreads)
-        return launch_dependent(sort_kernel<0, 4>, dim3(1), dim3(kSortThreads), smem, stream, 1, ids, slots, experts,
                                 offsets, rows, source, hist);
     if (slots <= 32 * kSortThreads) return sort_two<1>(ids, slots, experts, offsets, rows, source, hist, smem, stream);
     if (slots <= 512 * kSortThreads) return sort_two<4>(ids, slots, experts, offsets, rows, source, hist, smem, stream);

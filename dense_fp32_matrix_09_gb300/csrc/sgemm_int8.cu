@@ -422,34 +422,54 @@ struct I8Unit {
     int e, ch0, t0, tend;
 };
 
-// Unit u of tiles of NT tokens x CH channels: the expert by bisection of the
-// tile counts; within the expert groups of 2048 tokens or 16 tiles, channel
-// tiles outer and token tiles inner.
-template <int NT, int CH>
-__device__ __forceinline__ I8Unit unit_of(const int *bound, const int *tiles, const Int8Args &a, int ch_tiles, int u) {
-    int lo = 0, hi = a.experts;
+// The largest e with before[e] * each <= u.
+__device__ __forceinline__ int owner_of(const int *before, int experts, int each, int u) {
+    int lo = 0, hi = experts;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (tiles[mid] * ch_tiles <= u) lo = mid; else hi = mid;
+        if (before[mid] * each <= u) lo = mid; else hi = mid;
     }
-    constexpr int kGroup = 2048 / NT < 16 ? 2048 / NT : 16;
-    const int mine = tiles[lo + 1] - tiles[lo];
-    const int l = u - tiles[lo] * ch_tiles;
-    const int grp = l / (kGroup * ch_tiles), first = grp * kGroup;
-    const int rows = min(mine - first, kGroup);
-    const int r = l - grp * kGroup * ch_tiles;
+    return lo;
+}
+
+// Unit u of tiles of NT tokens x CH channels: the expert by bisection of the
+// tile counts; within the expert groups of 2048 tokens or 16 tiles, channel
+// tiles outer and token tiles inner.  TAILS: then the experts' last tiles of up to
+// NT / 2 tokens, which take half the time: in this order the CTAs that get one
+// tile more than others get a short one.
+template <int NT, int CH, bool TAILS>
+__device__ __forceinline__ I8Unit unit_of(const int *bound, const int *tiles, const int *tails, const Int8Args &a,
+                                          int ch_tiles, int u) {
     I8Unit q;
-    q.e = lo;
-    q.ch0 = r / rows * CH;
-    q.t0 = max(bound[lo], a.row0) + (first + r % rows) * NT;
-    q.tend = min(bound[lo + 1], a.row0 + a.rows);
+    int tile;
+    const int whole = tiles[a.experts] * ch_tiles;
+    if (!TAILS || u < whole) {
+        constexpr int kGroup = 2048 / NT < 16 ? 2048 / NT : 16;
+        q.e = owner_of(tiles, a.experts, ch_tiles, u);
+        const int mine = tiles[q.e + 1] - tiles[q.e];
+        const int l = u - tiles[q.e] * ch_tiles;
+        const int grp = l / (kGroup * ch_tiles), first = grp * kGroup;
+        const int rows = min(mine - first, kGroup);
+        const int r = l - grp * kGroup * ch_tiles;
+        q.ch0 = r / rows * CH;
+        tile = first + r % rows;
+    } else {
+        q.e = owner_of(tails, a.experts, ch_tiles, u - whole);
+        q.ch0 = (u - whole - tails[q.e] * ch_tiles) * CH;
+        tile = tiles[q.e + 1] - tiles[q.e];
+    }
+    q.t0 = max(bound[q.e], a.row0) + tile * NT;
+    q.tend = min(bound[q.e + 1], a.row0 + a.rows);
     return q;
 }
 
 // One warp: bound[e], the experts' first rows (nondecreasing), and tiles[e], the
 // token tiles of the experts before e (experts + 1 of each); returns all of them.
-__device__ __forceinline__ int sum_tiles(int *bound, int *tiles, const Int8Args &a, int nt, int lane) {
-    int top = 0, sum = 0;
+// TAILS: tiles[] counts the tiles of more than nt / 2 tokens, tails[] the rest (an
+// expert has one at most), and the tiles of tails[] come after all of tiles[].
+template <bool TAILS>
+__device__ __forceinline__ int sum_tiles(int *bound, int *tiles, int *tails, const Int8Args &a, int nt, int lane) {
+    int top = 0, sum = 0, tail_sum = 0;
     for (int e0 = 0; e0 <= a.experts; e0 += 32) {
         const int e = e0 + lane;
         int b = e <= a.experts ? bound_of(a, e) : 0;
@@ -465,22 +485,33 @@ __device__ __forceinline__ int sum_tiles(int *bound, int *tiles, const Int8Args 
     __syncwarp();
     for (int e0 = 0; e0 < a.experts; e0 += 32) {
         const int e = e0 + lane;
-        int n = 0;
+        int n = 0, tail = 0;
         if (e < a.experts) {
-            const int lo = max(bound[e], a.row0), hi = min(bound[e + 1], a.row0 + a.rows);
-            n = hi > lo ? (hi - lo + nt - 1) / nt : 0;
+            const int rows = max(min(bound[e + 1], a.row0 + a.rows) - max(bound[e], a.row0), 0);
+            n = (rows + (TAILS ? nt / 2 : nt) - 1) / nt;
+            tail = TAILS && rows > n * nt ? 1 : 0;
         }
-        int s = n;
+        int s = n, t = tail;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d) s += up;
+            const int up = __shfl_up_sync(0xffffffffu, s, d), upt = __shfl_up_sync(0xffffffffu, t, d);
+            if (lane >= d) {
+                s += up;
+                t += upt;
+            }
         }
-        if (e < a.experts) tiles[e] = sum + s - n;
+        if (e < a.experts) {
+            tiles[e] = sum + s - n;
+            if (TAILS) tails[e] = tail_sum + t - tail;
+        }
         sum += __shfl_sync(0xffffffffu, s, 31);
+        tail_sum += __shfl_sync(0xffffffffu, t, 31);
     }
-    if (lane == 0) tiles[a.experts] = sum;
-    return sum;
+    if (lane == 0) {
+        tiles[a.experts] = sum;
+        if (TAILS) tails[a.experts] = tail_sum;
+    }
+    return sum + tail_sum;
 }
 
 // Stages between drains, from the tokens' own size.  rows_to_f16 leaves in
@@ -634,18 +665,18 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
     // prefetch returns no data, so it does not matter whether that kernel has
     // yet to write them).
     if (!a.offsets && warp == 2) {
-        const int n = sum_tiles(bound, tiles, a, NT, lane);
+        const int n = sum_tiles<false>(bound, tiles, nullptr, a, NT, lane);
         if (lane == 0) sh->units = n * ch_tiles;
         __syncwarp();
         if (first_unit < n * ch_tiles) {
-            const I8Unit q = unit_of<NT, kI8TileN>(bound, tiles, a, ch_tiles, first_unit);
+            const I8Unit q = unit_of<NT, kI8TileN, false>(bound, tiles, nullptr, a, ch_tiles, first_unit);
             if (lane < S && kb + lane < ke) tma_prefetch_3d(&tmB, (kb + lane) * kI8StageK, q.ch0, q.e);
         }
     }
     griddep_wait();
     griddep_launch_dependents();
     if (a.offsets && warp == 2) {
-        const int n = sum_tiles(bound, tiles, a, NT, lane);
+        const int n = sum_tiles<false>(bound, tiles, nullptr, a, NT, lane);
         if (lane == 0) sh->units = n * ch_tiles;
     }
     tc::fence_before_sync();
@@ -681,7 +712,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             bool ok = true;
             for (int u = first_unit; u < units; u += unit_step) {
                 if (lane == 0 && ok) {
-                    const I8Unit q = unit_of<NT, kI8TileN>(bound, tiles, a, ch_tiles, u);
+                    const I8Unit q = unit_of<NT, kI8TileN, false>(bound, tiles, nullptr, a, ch_tiles, u);
                     for (int i = kb; i < ke; ++i, r.step(S), ++issued) {
                         if (!wait(&sh->empty[r.s], r.round ^ 1u)) { ok = false; break; }
                         uint8_t *st = ring + r.s * Cf::kStage;
@@ -831,7 +862,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
         Ring d;
         bool ok = true;
         for (int u = first_unit; u < units; u += unit_step) {
-            const I8Unit q = unit_of<NT, kI8TileN>(bound, tiles, a, ch_tiles, u);
+            const I8Unit q = unit_of<NT, kI8TileN, false>(bound, tiles, nullptr, a, ch_tiles, u);
             // What the epilogue needs of global memory, asked for before the sums
             // are ready: the channel's scale and bias, and lane l's share of the
             // token scales (handed round by shuffles).
@@ -958,7 +989,7 @@ struct PairShared {
     int abort;
     int units;
     int chunk;                      // stages between drains of an accumulator
-    // then bound[experts + 1], tiles[experts + 1]
+    // then bound[experts + 1], tiles[experts + 1], tails[experts + 1]
 };
 
 template <int T>
@@ -966,7 +997,7 @@ struct PairCfg {
     static constexpr int kXBytes = T / 2 * kI8StageK * 2;  // this CTA's half of the tokens, FP16
     static constexpr int kBStages = T == 256 ? 5 : 6, kXStages = T == 256 ? 4 : 6;
     static constexpr int kFixed = 1024 + kBStages * kBBytes + kXStages * kXBytes + static_cast<int>(sizeof(PairShared));
-    static constexpr int smem(int experts) { return kFixed + 2 * 4 * (experts + 1); }
+    static constexpr int smem(int experts) { return kFixed + 3 * 4 * (experts + 1); }
     // Registers a thread of each warpgroup: control, conversion, two epilogue
     // warpgroups (T / 2 sums a thread).  Their sum stays within 4 x 128, what the
     // block is launched with.
@@ -985,7 +1016,7 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;  // the same in both CTAs
     uint8_t *ring_x = smem_raw + pad, *ring_b = ring_x + SX * Cf::kXBytes;
     PairShared *sh = reinterpret_cast<PairShared *>(ring_b + SB * kBBytes);
-    int *bound = reinterpret_cast<int *>(sh + 1), *tiles = bound + a.experts + 1;
+    int *bound = reinterpret_cast<int *>(sh + 1), *tiles = bound + a.experts + 1, *tails = tiles + a.experts + 1;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rank = static_cast<int>(cluster_ctarank());  // 0: issues the MMAs
     const int first_unit = static_cast<int>(blockIdx.x) >> 1, unit_step = static_cast<int>(gridDim.x) >> 1;
@@ -1022,7 +1053,7 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 2) {
-        const int n = sum_tiles(bound, tiles, a, T, lane);
+        const int n = sum_tiles<true>(bound, tiles, tails, a, T, lane);
         if (lane == 0) sh->units = n * ch_tiles;
     }
     if (warp == 3) {
@@ -1037,6 +1068,8 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
     const uint32_t tmem_a = tmem + T;
     volatile int *abort_flag = &sh->abort;
     const int units = sh->units, chunk_stages = sh->chunk;
+    // A tile of up to T / 2 tokens (the last of an expert) leaves half 1 out.
+    auto halves_of = [](const I8Unit &q) { return q.tend - q.t0 > T / 2 ? 2 : 1; };
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
@@ -1054,7 +1087,7 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             bool ok = true;
             if (lane == 0) {
                 for (int u = first_unit; u < units && ok; u += unit_step) {
-                    const I8Unit q = unit_of<T, kPairN>(bound, tiles, a, ch_tiles, u);
+                    const I8Unit q = unit_of<T, kPairN, true>(bound, tiles, tails, a, ch_tiles, u);
                     for (int i = 0; i < kt; ++i, r.step(SB), ++issued) {
                         if (!wait(&sh->bempty[r.s], r.round ^ 1u)) { ok = false; break; }
                         mbar_arrive_expect_tx(&sh->bfull[r.s], kBBytes);
@@ -1071,9 +1104,10 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             constexpr uint32_t idesc = tc::idesc_f16_kmajor(2 * kI8TileN, T / 2);
             const uint64_t xdesc = tc::smem_desc(smem_u32(ring_x), 16, 1024, tc::kLayoutSwizzle128);
             Ring xr, tr;
-            uint32_t round = 0;  // of the accumulators
+            uint32_t round[2] = {};  // of the half accumulators
             bool ok = true;
             for (int u = first_unit; u < units && ok; u += unit_step) {
+                const int halves = halves_of(unit_of<T, kPairN, true>(bound, tiles, tails, a, ch_tiles, u));
                 // Two stages at a time: both for half 0 of the accumulators, then
                 // both for half 1, so that at the end of 1024 k either half has the
                 // time of 16 MMAs (1024 cycles) to be drained in while the other
@@ -1084,8 +1118,9 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
                     const bool start = run == 0, end = i + two == kt || run + two == chunk_stages;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        if (h >= halves) break;
                         Ring x = xr, t = tr;
-                        ok = ok && (!start || wait(&sh->dempty[h], round ^ 1u));
+                        ok = ok && (!start || wait(&sh->dempty[h], round[h] ^ 1u));
                         for (int j = 0; j < two; ++j, x.step(SX), t.step(kPairAStages)) {
                             if (h == 0) ok = ok && wait(&sh->xfull[x.s], x.round) && wait(&sh->afull[t.s], t.round);
                             ok = __all_sync(0xffffffffu, ok);
@@ -1099,7 +1134,7 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
                                     tc::mma_f16_ta_pair(tmem + h * (T / 2), tmem_a + t.s * kACols + kk * 8,
                                                         b + ((kk / 4) * (T / 2 * 128) + (kk % 4) * 32) / 16, idesc,
                                                         (start && j == 0 && kk == 0) ? 0u : 1u);
-                                if (h == 1) {
+                                if (h + 1 == halves) {
                                     tc::commit_pair(&sh->xempty[x.s], 0x3);
                                     tc::commit_pair(&sh->aempty[t.s], 0x3);
                                 }
@@ -1114,7 +1149,10 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
                         tr.step(kPairAStages);
                     }
                     run = end ? 0 : run + two;
-                    if (end) round ^= 1u;
+                    if (end) {
+                        round[0] ^= 1u;
+                        if (halves == 2) round[1] ^= 1u;
+                    }
                 }
             }
             if (!ok && tc::elect_one()) {  // no teardown under a running MMA
@@ -1133,17 +1171,17 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             if (lane == 0) {
                 const uint32_t xfull = tc::map_shared_rank(smem_u32(&sh->xfull[0]), 0);
                 for (int u = first_unit; u < units && ok; u += unit_step) {
-                    const I8Unit q = unit_of<T, kPairN>(bound, tiles, a, ch_tiles, u);
-                    const int row = q.t0 - a.row0 + rank * (T / 4);
+                    const I8Unit q = unit_of<T, kPairN, true>(bound, tiles, tails, a, ch_tiles, u);
+                    const int row = q.t0 - a.row0 + rank * (T / 4), halves = halves_of(q);
                     for (int i = 0; i < kt; ++i, r.step(SX), ++issued) {
                         if (!wait(&sh->xempty[r.s], r.round ^ 1u)) { ok = false; break; }
                         uint8_t *st = ring_x + r.s * Cf::kXBytes;
-                        if (rank == 0) mbar_arrive_expect_tx(&sh->xfull[r.s], 2 * Cf::kXBytes);
+                        if (rank == 0) mbar_arrive_expect_tx(&sh->xfull[r.s], halves * Cf::kXBytes);
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                tc::tma_load_2d_pair(st + k * (T / 2 * 128) + h * (T / 4 * 128), &tmA, xfull + r.s * 8,
+                                if (h < halves) tc::tma_load_2d_pair(st + k * (T / 2 * 128) + h * (T / 4 * 128), &tmA, xfull + r.s * 8,
                                                      i * kI8StageK + k * 64, row + h * (T / 2));
                     }
                 }
@@ -1202,7 +1240,8 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
         uint32_t round = 0;
         bool ok = true;
         for (int u = first_unit; u < units && ok; u += unit_step) {
-            const I8Unit q = unit_of<T, kPairN>(bound, tiles, a, ch_tiles, u);
+            const I8Unit q = unit_of<T, kPairN, true>(bound, tiles, tails, a, ch_tiles, u);
+            if (h >= halves_of(q)) continue;
             const int n = q.ch0 + rank * kI8TileN + ch;
             const long long at = static_cast<long long>(q.e) * a.N + n;
             const float sb = n < a.N ? __ldg(a.scaleB + at) : 0.f;
