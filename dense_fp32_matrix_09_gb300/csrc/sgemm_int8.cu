@@ -50,6 +50,8 @@
 //    as the TMA can read it (stored K x N, or not on 16-byte boundaries).
 // Every wait is bounded; on a timeout the kernel records it, waits (bounded)
 // for its own copies and MMAs in flight, frees the tensor memory and returns.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -62,8 +64,11 @@ namespace sg {
 namespace {
 
 // ---- epilogue arithmetic, common to both kernels --------------------------------
+__device__ __forceinline__ float int8_value(float sum, float sb, float sa, float bias) {
+    return fmaf(sum * sb, sa, bias);
+}
 __device__ __forceinline__ float int8_value(int sum, float sb, float sa, float bias) {
-    return fmaf(__int2float_rn(sum) * sb, sa, bias);
+    return int8_value(__int2float_rn(sum), sb, sa, bias);
 }
 
 // Two values of the output type from one conversion, and the store of one or
@@ -105,16 +110,19 @@ __device__ __forceinline__ void with_out_type(int type, F &&f) {
 // exist, as in every tile but those at the edges, runs without predicates: the
 // code is unrolled over the registers that hold the sums, and its size counts
 // (it is fetched anew for every tile).
-template <class Out, int COLS>
+// FLOATS: the sums are the bits of FP32 values.
+template <class Out, bool FLOATS, int COLS>
 __device__ __forceinline__ void write_columns(typename Out::T *C, long long ldc, int live, const int (&acc)[COLS],
                                               const float (&sa)[(COLS + 31) / 32], float sb, float bias) {
+    auto value = [&](int sum, float s) {
+        return FLOATS ? int8_value(__int_as_float(sum), sb, s, bias) : int8_value(sum, sb, s, bias);
+    };
     if (__all_sync(0xffffffffu, live >= COLS)) {
 #pragma unroll
         for (int j = 0; j < COLS; j += 2) {
             const float s0 = __shfl_sync(0xffffffffu, sa[j / 32], j % 32);
             const float s1 = __shfl_sync(0xffffffffu, sa[j / 32], j % 32 + 1);
-            const typename Out::Two v =
-                Out::two(int8_value(acc[j], sb, s0, bias), int8_value(acc[j + 1], sb, s1, bias));
+            const typename Out::Two v = Out::two(value(acc[j], s0), value(acc[j + 1], s1));
             C[0] = Out::lo(v);
             C[ldc] = Out::hi(v);
             C += 2 * ldc;
@@ -125,7 +133,7 @@ __device__ __forceinline__ void write_columns(typename Out::T *C, long long ldc,
     for (int j = 0; j < COLS; j += 2) {
         const float s0 = __shfl_sync(0xffffffffu, sa[j / 32], j % 32);
         const float s1 = __shfl_sync(0xffffffffu, sa[j / 32], j % 32 + 1);
-        const typename Out::Two v = Out::two(int8_value(acc[j], sb, s0, bias), int8_value(acc[j + 1], sb, s1, bias));
+        const typename Out::Two v = Out::two(value(acc[j], s0), value(acc[j + 1], s1));
         if (j < live) C[0] = Out::lo(v);
         if (j + 1 < live) C[ldc] = Out::hi(v);
         C += 2 * ldc;
@@ -402,9 +410,28 @@ __device__ __forceinline__ void regs_fewer() { asm volatile("setmaxnreg.dec.sync
 template <int R>
 __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// acc[j] += column j of an accumulator (integers): the load of the next 16
-// columns is in flight while 16 are converted.
-template <int COLS>
+// sum + f for an integer f of magnitude <= 2^24, by the FP32 and integer pipes:
+// adding M = 1.5 * 2^23 leaves a value below 2^22 rounded to an integer in the low
+// bits, so h = f / 4096 + M holds round(f / 4096), r = f - 4096 * (h - M) the rest
+// (exact, at most 2048), and the bits of h, shifted, and of r + M add up to f but
+// for a constant (arithmetic modulo 2^32).
+__device__ __forceinline__ int add_integer(int sum, float f) {
+    constexpr float kM = 12582912.f;
+    constexpr unsigned kBits = 0x4b400000u, kConst = (kBits << 12) + kBits;
+    const float h = fmaf(f, 1.f / 4096.f, kM);
+    const float r = __fadd_rn(fmaf(__fadd_rn(h, -kM), -4096.f, f), kM);
+    return static_cast<int>(static_cast<unsigned>(sum) + ((__float_as_uint(h) << 12) + __float_as_uint(r)) - kConst);
+}
+
+// How an accumulator is taken over: its integers added to sums of which they are
+// a part, or kept as the FP32 values that they are where one holds all of K.
+enum class Take { kAdd, kOnly };
+
+// acc[j] += column j of an accumulator (kOnly: acc[j] = its bits): the load of
+// the next 16 columns is in flight while 16 are converted.  The conversion
+// instruction runs at an eighth of the rate of an addition (128 columns in two
+// warpgroups: 2300 cycles), so 9 of 16 columns go round it.
+template <Take TAKE, int COLS>
 __device__ __forceinline__ void drain(uint32_t tmem, int (&acc)[COLS]) {
     uint32_t v[2][16];
     tc::tmem_ld16_begin(tmem, v[0]);
@@ -413,7 +440,13 @@ __device__ __forceinline__ void drain(uint32_t tmem, int (&acc)[COLS]) {
     for (int c = 0; c < COLS / 16; ++c) {
         if (c + 1 < COLS / 16) tc::tmem_ld16_begin(tmem + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) acc[c * 16 + j] += __float2int_rn(__uint_as_float(v[c & 1][j]));
+        for (int j = 0; j < 16; ++j) {
+            int &sum = acc[c * 16 + j];
+            const float f = __uint_as_float(v[c & 1][j]);
+            if (TAKE == Take::kOnly) sum = static_cast<int>(v[c & 1][j]);
+            else if (j % 2 == 1 && j < 15) sum += __float2int_rn(f);
+            else sum = add_integer(sum, f);
+        }
         if (c + 1 < COLS / 16) tc::tmem_ld_wait(v[(c + 1) & 1]);
     }
 }
@@ -888,7 +921,7 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                 ok = __all_sync(0xffffffffu, wait(&sh->dfull[d.s], d.round));
                 if (!ok) break;
                 tc::fence_after_sync();
-                drain(tmem + d.s * NT + lanes, acc);
+                drain<Take::kAdd>(tmem + d.s * NT + lanes, acc);
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->dempty[d.s]);
@@ -897,8 +930,8 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
                 if (ok)
                     with_out_type(a.out_type, [&](auto out) {
                         using Out = decltype(out);
-                        write_columns<Out>(static_cast<typename Out::T *>(a.C) + static_cast<long long>(first) * a.ldc + n,
-                                           a.ldc, n < a.N ? q.tend - first : 0, acc, sa, sb, bias);
+                        write_columns<Out, false>(static_cast<typename Out::T *>(a.C) + static_cast<long long>(first) * a.ldc + n,
+                                                  a.ldc, n < a.N ? q.tend - first : 0, acc, sa, sb, bias);
                     });
             } else {
                 __syncwarp();
@@ -972,16 +1005,18 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
 
 // ---- CTA pairs: 256 channels x T = 128 or 256 tokens ---------------------------------
 constexpr int kPairN = 256;  // channels of a pair's tile
-constexpr int kPairAStages = 4, kPairMaxB = 8, kPairMaxX = 6;
+constexpr int kPairASlots = 2, kPairMaxB = 8, kPairMaxX = 3;  // a slot: two stages
 constexpr int kPairThreads = 512;
 constexpr uint32_t kPairTmemCols = 512;
 
 struct PairShared {
     uint64_t bfull[kPairMaxB], bempty[kPairMaxB];
-    uint64_t xfull[kPairMaxX];      // (even CTA) both CTAs' tokens of the stage have landed
-    uint64_t xempty[kPairMaxX];     // the MMAs have read them (both CTAs are told)
-    uint64_t afull[kPairAStages];   // (even CTA) B stands in both CTAs' tensor memory
-    uint64_t aempty[kPairAStages];
+    // Tokens, and B in tensor memory, two stages (256 k) at a time: what the
+    // issuing lane spends on a wait and on a commit it spends half as often.
+    uint64_t xfull[2][kPairMaxX];   // (even CTA) both CTAs' tokens of a half have landed
+    uint64_t xempty[2][kPairMaxX];  // the MMAs have read them (both CTAs are told)
+    uint64_t afull[kPairASlots];    // (even CTA) B stands in both CTAs' tensor memory
+    uint64_t aempty[kPairASlots];
     uint64_t dfull[2];              // a half accumulator holds up to `chunk` stages
     uint64_t dempty[2];             // (even CTA) both CTAs have read it
     uint64_t drained;
@@ -995,26 +1030,26 @@ struct PairShared {
 template <int T>
 struct PairCfg {
     static constexpr int kXBytes = T / 2 * kI8StageK * 2;  // this CTA's half of the tokens, FP16
-    static constexpr int kBStages = T == 256 ? 5 : 6, kXStages = T == 256 ? 4 : 6;
-    static constexpr int kFixed = 1024 + kBStages * kBBytes + kXStages * kXBytes + static_cast<int>(sizeof(PairShared));
+    static constexpr int kBStages = T == 256 ? 5 : 6, kXSlots = T == 256 ? 2 : 3;
+    static constexpr int kFixed = 1024 + kBStages * kBBytes + kXSlots * 2 * kXBytes + static_cast<int>(sizeof(PairShared));
     static constexpr int smem(int experts) { return kFixed + 3 * 4 * (experts + 1); }
     // Registers a thread of each warpgroup: control, conversion, two epilogue
     // warpgroups (T / 2 sums a thread).  Their sum stays within 4 x 128, what the
     // block is launched with.
     static constexpr int kRegsControl = 56, kRegsConvert = 96, kRegsEpilogue = 176;
     static_assert(kRegsControl + kRegsConvert + 2 * kRegsEpilogue <= 4 * 128, "register split");
-    static_assert(T + kPairAStages * kACols <= static_cast<int>(kPairTmemCols), "tensor memory");
-    static_assert(smem(kMaxExperts) <= kSmemLimit && kBStages <= kPairMaxB && kXStages <= kPairMaxX, "shared memory");
+    static_assert(T + kPairASlots * 2 * kACols <= static_cast<int>(kPairTmemCols), "tensor memory");
+    static_assert(smem(kMaxExperts) <= kSmemLimit && kBStages <= kPairMaxB && kXSlots <= kPairMaxX, "shared memory");
 };
 
 template <int T>
 __global__ void __launch_bounds__(kPairThreads, 1)
 int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA, const Int8Args a) {
     using Cf = PairCfg<T>;
-    constexpr int SB = Cf::kBStages, SX = Cf::kXStages;
+    constexpr int SB = Cf::kBStages, SX = Cf::kXSlots;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;  // the same in both CTAs
-    uint8_t *ring_x = smem_raw + pad, *ring_b = ring_x + SX * Cf::kXBytes;
+    uint8_t *ring_x = smem_raw + pad, *ring_b = ring_x + SX * 2 * Cf::kXBytes;
     PairShared *sh = reinterpret_cast<PairShared *>(ring_b + SB * kBBytes);
     int *bound = reinterpret_cast<int *>(sh + 1), *tiles = bound + a.experts + 1, *tails = tiles + a.experts + 1;
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -1029,10 +1064,12 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             mbar_init(&sh->bempty[s], 4);
         }
         for (int s = 0; s < SX; ++s) {
-            mbar_init(&sh->xfull[s], 1);
-            mbar_init(&sh->xempty[s], 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sh->xfull[h][s], 1);
+                mbar_init(&sh->xempty[h][s], 1);
+            }
         }
-        for (int s = 0; s < kPairAStages; ++s) {
+        for (int s = 0; s < kPairASlots; ++s) {
             mbar_init(&sh->afull[s], 8);
             mbar_init(&sh->aempty[s], 1);
         }
@@ -1103,51 +1140,49 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             // -------------------------------------------- MMA issuer (even CTA)
             constexpr uint32_t idesc = tc::idesc_f16_kmajor(2 * kI8TileN, T / 2);
             const uint64_t xdesc = tc::smem_desc(smem_u32(ring_x), 16, 1024, tc::kLayoutSwizzle128);
-            Ring xr, tr;
+            Ring xr[2], tr;          // each half of the tokens goes round a ring of its own
             uint32_t round[2] = {};  // of the half accumulators
             bool ok = true;
             for (int u = first_unit; u < units && ok; u += unit_step) {
                 const int halves = halves_of(unit_of<T, kPairN, true>(bound, tiles, tails, a, ch_tiles, u));
-                // Two stages at a time: both for half 0 of the accumulators, then
-                // both for half 1, so that at the end of 1024 k either half has the
-                // time of 16 MMAs (1024 cycles) to be drained in while the other
-                // is added to.
+                // A slot of two stages at a time: both for half 0 of the accumulators,
+                // then both for half 1, so that at the end of `chunk` stages either
+                // half has the time of 16 MMAs (1024 cycles) to be drained in while
+                // the other is added to.
                 int run = 0;  // stages in the accumulators so far
                 for (int i = 0; i < kt; i += 2) {
                     const int two = i + 1 < kt ? 2 : 1;
                     const bool start = run == 0, end = i + two == kt || run + two == chunk_stages;
+                    ok = wait(&sh->afull[tr.s], tr.round);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (h >= halves) break;
-                        Ring x = xr, t = tr;
-                        ok = ok && (!start || wait(&sh->dempty[h], round[h] ^ 1u));
-                        for (int j = 0; j < two; ++j, x.step(SX), t.step(kPairAStages)) {
-                            if (h == 0) ok = ok && wait(&sh->xfull[x.s], x.round) && wait(&sh->afull[t.s], t.round);
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            if (tc::elect_one()) {
-                                const uint64_t b =
-                                    xdesc + static_cast<uint64_t>(x.s * (Cf::kXBytes / 16) + h * (T / 4 * 128 / 16));
+                        const int x = xr[h].s;
+                        ok = ok && (!start || wait(&sh->dempty[h], round[h] ^ 1u)) && wait(&sh->xfull[h][x], xr[h].round);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        if (tc::elect_one()) {
+                            const uint64_t b = xdesc + static_cast<uint64_t>(x * (2 * Cf::kXBytes / 16) + h * (T / 4 * 128 / 16));
+                            const uint32_t ta = tmem_a + tr.s * (2 * kACols);
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                if (j >= two) break;
 #pragma unroll
                                 for (int kk = 0; kk < kI8StageK / 16; ++kk)
-                                    tc::mma_f16_ta_pair(tmem + h * (T / 2), tmem_a + t.s * kACols + kk * 8,
-                                                        b + ((kk / 4) * (T / 2 * 128) + (kk % 4) * 32) / 16, idesc,
-                                                        (start && j == 0 && kk == 0) ? 0u : 1u);
-                                if (h + 1 == halves) {
-                                    tc::commit_pair(&sh->xempty[x.s], 0x3);
-                                    tc::commit_pair(&sh->aempty[t.s], 0x3);
-                                }
-                                if (end && j + 1 == two) tc::commit_pair(&sh->dfull[h], 0x3);
+                                    tc::mma_f16_ta_pair(tmem + h * (T / 2), ta + j * kACols + kk * 8,
+                                                        b + (j * Cf::kXBytes + (kk / 4) * (T / 2 * 128) + (kk % 4) * 32) / 16,
+                                                        idesc, (start && j == 0 && kk == 0) ? 0u : 1u);
                             }
-                            __syncwarp();
+                            tc::commit_pair(&sh->xempty[h][x], 0x3);
+                            if (h + 1 == halves) tc::commit_pair(&sh->aempty[tr.s], 0x3);
+                            if (end) tc::commit_pair(&sh->dfull[h], 0x3);
                         }
+                        __syncwarp();
+                        xr[h].step(SX);
                     }
                     if (!ok) break;
-                    for (int j = 0; j < two; ++j) {
-                        xr.step(SX);
-                        tr.step(kPairAStages);
-                    }
+                    tr.step(kPairASlots);
                     run = end ? 0 : run + two;
                     if (end) {
                         round[0] ^= 1u;
@@ -1165,28 +1200,36 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             // Half h of the accumulators covers T / 2 tokens from t0 + h T / 2, half of
             // them from each CTA: this CTA's rows h T / 4 .. of a stage.  Both
             // CTAs' bytes count on the even CTA's barrier.
-            Ring r;
-            int issued = 0;
+            // They are fetched in the MMAs' order: half 0 of two stages, then half 1.
+            Ring r[2];
             bool ok = true;
             if (lane == 0) {
-                const uint32_t xfull = tc::map_shared_rank(smem_u32(&sh->xfull[0]), 0);
+                const uint32_t xfull = tc::map_shared_rank(smem_u32(&sh->xfull[0][0]), 0);
                 for (int u = first_unit; u < units && ok; u += unit_step) {
                     const I8Unit q = unit_of<T, kPairN, true>(bound, tiles, tails, a, ch_tiles, u);
                     const int row = q.t0 - a.row0 + rank * (T / 4), halves = halves_of(q);
-                    for (int i = 0; i < kt; ++i, r.step(SX), ++issued) {
-                        if (!wait(&sh->xempty[r.s], r.round ^ 1u)) { ok = false; break; }
-                        uint8_t *st = ring_x + r.s * Cf::kXBytes;
-                        if (rank == 0) mbar_arrive_expect_tx(&sh->xfull[r.s], halves * Cf::kXBytes);
+                    for (int i = 0; i < kt && ok; i += 2) {
+                        const int two = i + 1 < kt ? 2 : 1;
+                        for (int h = 0; h < halves; ++h) {
+                            const int x = r[h].s;
+                            ok = ok && wait(&sh->xempty[h][x], r[h].round ^ 1u);
+                            if (!ok) break;
+                            uint8_t *st = ring_x + x * (2 * Cf::kXBytes) + h * (T / 4 * 128);
+                            if (rank == 0) mbar_arrive_expect_tx(&sh->xfull[h][x], two * Cf::kXBytes);
+                            for (int j = 0; j < two; ++j)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                if (h < halves) tc::tma_load_2d_pair(st + k * (T / 2 * 128) + h * (T / 4 * 128), &tmA, xfull + r.s * 8,
-                                                     i * kI8StageK + k * 64, row + h * (T / 2));
+                                for (int k = 0; k < 2; ++k)
+                                    tc::tma_load_2d_pair(st + j * Cf::kXBytes + k * (T / 2 * 128), &tmA,
+                                                         xfull + (h * kPairMaxX + x) * 8, (i + j) * kI8StageK + k * 64,
+                                                         row + h * (T / 2));
+                            r[h].step(SX);
+                        }
                     }
                 }
-                // no copy outlives its CTA: the MMAs that read the last ones have finished
-                for (int t = max(0, issued - SX); t < issued; ++t) mbar_wait(&sh->xempty[t % SX], (t / SX) & 1, a.status);
+                // No copy outlives its CTA: the MMAs that read the last ones have
+                // finished (a slot that was never loaded stands at its first round).
+                for (int h = 0; h < 2; ++h)
+                    for (int x = 0; x < SX; ++x, r[h].step(SX)) mbar_wait(&sh->xempty[h][r[h].s], r[h].round ^ 1u, a.status);
             }
             __syncwarp();
         }
@@ -1197,7 +1240,7 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
         const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16;
         const uint32_t afull = tc::map_shared_rank(smem_u32(&sh->afull[0]), 0);
         Ring r, t;
-        int stored = -1;
+        int stored = -1;  // the slot in tensor memory whose stores have not been waited for
         bool ok = true;
         auto flush = [&]() {
             if (stored < 0) return;
@@ -1208,24 +1251,30 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             stored = -1;
         };
         for (int u = first_unit; u < units && ok; u += unit_step) {
-            for (int i = 0; i < kt; ++i, r.step(SB), t.step(kPairAStages)) {
-                if (!__all_sync(0xffffffffu, mbar_try_wait(&sh->bfull[r.s], r.round))) {
-                    flush();
-                    ok = __all_sync(0xffffffffu, wait(&sh->bfull[r.s], r.round));
-                    if (!ok) break;
-                }
-                const uint8_t *src = ring_b + r.s * kBBytes + row * kI8StageK;
-                uint4 w[8];
+            for (int i = 0; i < kt && ok; i += 2) {
+                const int two = i + 1 < kt ? 2 : 1;
+                for (int j = 0; j < two; ++j, r.step(SB)) {
+                    if (!__all_sync(0xffffffffu, mbar_try_wait(&sh->bfull[r.s], r.round))) {
+                        flush();
+                        ok = __all_sync(0xffffffffu, wait(&sh->bfull[r.s], r.round));
+                        if (!ok) break;
+                    }
+                    const uint8_t *src = ring_b + r.s * kBBytes + row * kI8StageK;
+                    uint4 w[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + ((c ^ (row & 7)) * 16));
-                flush();
-                ok = __all_sync(0xffffffffu, wait(&sh->aempty[t.s], t.round ^ 1u));
-                if (!ok) break;
-                tc::fence_after_sync();
-                expand_to_tmem(w, tmem_a + t.s * kACols + lanes);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->bempty[r.s]);
+                    for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + ((c ^ (row & 7)) * 16));
+                    if (j == 0) {
+                        flush();
+                        ok = __all_sync(0xffffffffu, wait(&sh->aempty[t.s], t.round ^ 1u));
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                    }
+                    expand_to_tmem(w, tmem_a + t.s * (2 * kACols) + j * kACols + lanes);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->bempty[r.s]);
+                }
                 stored = t.s;
+                t.step(kPairASlots);
             }
             flush();
         }
@@ -1252,23 +1301,33 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             for (int c = 0; c < kCols / 32; ++c)
                 sa[c] = first + c * 32 + lane < q.tend ? __ldg(a.scaleA + first + c * 32 + lane) : 0.f;
             int acc[kCols];
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) acc[j] = 0;
-            for (int i = 0; i < kt; i += chunk_stages, round ^= 1u) {
+            auto take = [&](auto how) {
                 ok = __all_sync(0xffffffffu, wait(&sh->dfull[h], round));
-                if (!ok) break;
+                if (!ok) return;
                 tc::fence_after_sync();
-                drain(src, acc);
+                drain<decltype(how)::value>(src, acc);
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive_remote(dempty);
-            }
-            if (ok)
+                round ^= 1u;
+            };
+            auto write = [&](auto floats) {
                 with_out_type(a.out_type, [&](auto out) {
                     using Out = decltype(out);
-                    write_columns<Out>(static_cast<typename Out::T *>(a.C) + static_cast<long long>(first) * a.ldc + n,
-                                       a.ldc, n < a.N ? q.tend - first : 0, acc, sa, sb, bias);
+                    write_columns<Out, decltype(floats)::value>(
+                        static_cast<typename Out::T *>(a.C) + static_cast<long long>(first) * a.ldc + n, a.ldc,
+                        n < a.N ? q.tend - first : 0, acc, sa, sb, bias);
                 });
+            };
+            if (kt <= chunk_stages) {
+                take(std::integral_constant<Take, Take::kOnly>{});
+                if (ok) write(std::true_type{});
+            } else {
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) acc[j] = 0;
+                for (int i = 0; i < kt && ok; i += chunk_stages) take(std::integral_constant<Take, Take::kAdd>{});
+                if (ok) write(std::false_type{});
+            }
         }
     }
     // ---------------------------------------------------- teardown
