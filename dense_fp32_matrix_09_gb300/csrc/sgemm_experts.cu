@@ -19,6 +19,10 @@
 //    experts, back, and the gradients; each reads and writes every row once
 //    (16 bytes a thread and step where alignment allows), sums in FP32 in
 //    ascending choice order and rounds once.
+// No load is a read-only-cache load (ld.global.nc): what is read may have been
+// written by the kernel before, whose end the launch overlaps.  Rows, read once, go
+// past L1 (ld.global.cg); row numbers and weights, which a block's warps share, do
+// not (ld.global.ca; past L1 the gathers take 61 us instead of 55).
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -81,7 +85,7 @@ __device__ __forceinline__ Pack8<T> load8(const T *row, int c, int lane, int wid
     const W *p = reinterpret_cast<const W *>(row + at);
     W *d = reinterpret_cast<W *>(&r);
 #pragma unroll
-    for (int i = 0; i < kV / A; ++i) d[i] = at + i * TPR * A < width ? __ldg(p + i * TPR) : W{};
+    for (int i = 0; i < kV / A; ++i) d[i] = at + i * TPR * A < width ? __ldcg(p + i * TPR) : W{};
     return r;
 }
 template <class T, int TPR, int A>
@@ -98,7 +102,7 @@ __device__ __forceinline__ void store8(T *row, int c, int lane, int width, const
 // Sorted row of a slot, or -1 for one that has none: a value outside [0, slots)
 // is no row, whatever wrote it.
 __device__ __forceinline__ int row_of(const int *rows, long long slot, int slots) {
-    const int r = __ldg(rows + slot);
+    const int r = __ldca(rows + slot);
     return static_cast<unsigned>(r) < static_cast<unsigned>(slots) ? r : -1;
 }
 
@@ -254,7 +258,7 @@ sort_kernel(const int *__restrict__ ids, int slots, int experts, int *__restrict
     int e[STEPS], rank[STEPS];  // the slots' experts (-1: dropped), their places among the warp's
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-        e[s] = first + s * 32 < slots ? __ldg(ids + first + s * 32) : -1;
+        e[s] = first + s * 32 < slots ? __ldcg(ids + first + s * 32) : -1;
         if (static_cast<unsigned>(e[s]) >= static_cast<unsigned>(experts)) e[s] = -1;
     }
     __syncthreads();
@@ -392,7 +396,7 @@ gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, i
             for (int j = 0; j < 4; ++j) {
                 const long long slot = static_cast<long long>(t) * choices + j0 + j;
                 const int r = j0 + j < choices ? row_of(rows, slot, slots) : -1;
-                w[j] = r >= 0 && weights ? __ldg(weights + slot) : 1.f;
+                w[j] = r >= 0 && weights ? __ldca(weights + slot) : 1.f;
                 // (a row that does not exist has no elements: zeros)
                 y[j] = load8<T, 256, A>(Y + static_cast<long long>(r >= 0 ? r : 0) * ldy, c, lane, r >= 0 ? width : 0);
             }
@@ -432,7 +436,7 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
             for (int j = 0; j < J; ++j) {
                 const long long slot = static_cast<long long>(t) * choices + j0 + j;
                 r[j] = j0 + j < choices ? row_of(rows, slot, slots) : -1;
-                w[j] = r[j] >= 0 ? __ldg(weights + slot) : 0.f;
+                w[j] = r[j] >= 0 ? __ldca(weights + slot) : 0.f;
                 dot[j] = 0.f;
             }
             for (int c = 0; c * 256 * kV < width; ++c) {

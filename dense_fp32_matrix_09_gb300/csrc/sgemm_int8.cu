@@ -50,6 +50,8 @@
 //    as the TMA can read it (stored K x N, or not on 16-byte boundaries).
 // Every wait is bounded; on a timeout the kernel records it, waits (bounded)
 // for its own copies and MMAs in flight, frees the tensor memory and returns.
+// Plain loads go past L1 (ld.global.cg): what they read may have been written by
+// the kernel before, whose end the launch overlaps.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -143,7 +145,7 @@ __device__ __forceinline__ void write_columns(typename Out::T *C, long long ldc,
 // offsets[e], kept within the rows there are (whatever the array holds).
 __device__ __forceinline__ int bound_of(const Int8Args &a, int e) {
     if (!a.offsets) return e == 0 ? 0 : a.total_rows;
-    return min(max(__ldg(a.offsets + e), 0), a.total_rows);
+    return min(max(__ldcg(a.offsets + e), 0), a.total_rows);
 }
 
 // ---- generic kernel -----------------------------------------------------------
@@ -203,14 +205,14 @@ __global__ void __launch_bounds__(256) int8_generic_kernel(const Int8Args a) {
                 for (int i = 0; i < 4; ++i) {
                     const int row = m0 + ty + 16 * i;
                     if (row >= hi) continue;
-                    const float sa = __ldg(a.scaleA + row);
+                    const float sa = __ldcg(a.scaleA + row);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int ch = n0 + tx + 16 * j;
                         if (ch >= a.N) continue;
                         const long long at = static_cast<long long>(e) * a.N + ch;
                         const float v =
-                            int8_value(acc[i][j], __ldg(a.scaleB + at), sa, a.bias ? __ldg(a.bias + at) : 0.f);
+                            int8_value(acc[i][j], __ldcg(a.scaleB + at), sa, a.bias ? __ldcg(a.bias + at) : 0.f);
                         C[static_cast<long long>(row) * a.ldc + ch] = Out::lo(Out::two(v, 0.f));
                     }
                 }
@@ -237,13 +239,13 @@ __device__ __forceinline__ void int8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t
 // away from the row's ends (no byte outside the row is read).
 __device__ __forceinline__ uint4 load_int8x16(const int8_t *row, int k, int K, bool vec) {
     const int8_t *p = row + k;
-    if (vec && k + 16 <= K) return __ldg(reinterpret_cast<const uint4 *>(p));
+    if (vec && k + 16 <= K) return __ldcg(reinterpret_cast<const uint4 *>(p));
     uint32_t w[5] = {};
     if (k >= 16 && k + 20 <= K) {
         const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
         const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
 #pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = __ldg(q + i);
+        for (int i = 0; i < 5; ++i) w[i] = __ldcg(q + i);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * off);
     } else {
@@ -336,11 +338,11 @@ __device__ __forceinline__ void transpose(const Int8Copies &c, int block, int bl
                 if (k < c.K) {
                     const int8_t *p = src + static_cast<long long>(k) * c.ldb + n;
                     if (c.b_vec && n + 4 <= c.N) {
-                        v = __ldg(reinterpret_cast<const uint32_t *>(p));
+                        v = __ldcg(reinterpret_cast<const uint32_t *>(p));
                     } else if (n >= 4 && n + 8 <= c.N) {
                         const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
                         const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
-                        v = __funnelshift_r(__ldg(q), __ldg(q + 1), 8 * off);
+                        v = __funnelshift_r(__ldcg(q), __ldcg(q + 1), 8 * off);
                     } else {
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
@@ -901,14 +903,14 @@ int8_tc_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ 
             // token scales (handed round by shuffles).
             const int n = q.ch0 + ch;
             const long long at = static_cast<long long>(q.e) * a.N + n;
-            const float sb = n < a.N ? __ldg(a.scaleB + at) : 0.f;
-            const float bias = n < a.N && a.bias ? __ldg(a.bias + at) : 0.f;
+            const float sb = n < a.N ? __ldcg(a.scaleB + at) : 0.f;
+            const float bias = n < a.N && a.bias ? __ldcg(a.bias + at) : 0.f;
             const int per = SPLIT ? NT / splits : NT;  // this CTA's columns of the result
             const int first = q.t0 + (SPLIT ? rank * per : 0);
             float sa[(NT + 31) / 32];
 #pragma unroll
             for (int c = 0; c < (NT + 31) / 32; ++c)
-                sa[c] = c * 32 + lane < per && first + c * 32 + lane < q.tend ? __ldg(a.scaleA + first + c * 32 + lane) : 0.f;
+                sa[c] = c * 32 + lane < per && first + c * 32 + lane < q.tend ? __ldcg(a.scaleA + first + c * 32 + lane) : 0.f;
             // (its own room: ready as soon as the last unit's sums have been read)
             if (SPLIT && Cf::kXchgOwn) {
                 __syncwarp();
@@ -1293,13 +1295,13 @@ int8_tc_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_consta
             if (h >= halves_of(q)) continue;
             const int n = q.ch0 + rank * kI8TileN + ch;
             const long long at = static_cast<long long>(q.e) * a.N + n;
-            const float sb = n < a.N ? __ldg(a.scaleB + at) : 0.f;
-            const float bias = n < a.N && a.bias ? __ldg(a.bias + at) : 0.f;
+            const float sb = n < a.N ? __ldcg(a.scaleB + at) : 0.f;
+            const float bias = n < a.N && a.bias ? __ldcg(a.bias + at) : 0.f;
             const int first = q.t0 + h * kCols;
             float sa[kCols / 32];
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c)
-                sa[c] = first + c * 32 + lane < q.tend ? __ldg(a.scaleA + first + c * 32 + lane) : 0.f;
+                sa[c] = first + c * 32 + lane < q.tend ? __ldcg(a.scaleA + first + c * 32 + lane) : 0.f;
             int acc[kCols];
             auto take = [&](auto how) {
                 ok = __all_sync(0xffffffffu, wait(&sh->dfull[h], round));

@@ -42,6 +42,10 @@ struct Range {
     bool meets(const Range &o) const { return lo < o.hi && o.lo < hi && lo < hi && o.lo < o.hi; }
 };
 
+// Rows, channels and elements of a row that the kernels' 32-bit indices reach with
+// a tile to spare.
+constexpr int kMaxExtent = 1 << 30;
+
 // K up to which a sum of K products of two int8 stays inside int32.
 constexpr int kMaxInt8K = 131071;
 
@@ -105,7 +109,7 @@ int check_int8(int transB, int out_type, int experts, int rows, int N, int K, co
                const int8_t *A, int lda, const float *scaleA, const int8_t *B, int ldb, long long strideB,
                const float *scaleB, const float *bias, const void *C, int ldc) {
     if (!known_type(out_type) || (transB != 0 && transB != 1)) return SGEMM_ERR_INVALID_VALUE;
-    if (rows < 0 || N < 0 || K < 0 || K > kMaxInt8K) return SGEMM_ERR_INVALID_VALUE;
+    if (rows < 0 || N < 0 || K < 0 || K > kMaxInt8K || rows > kMaxExtent || N > kMaxExtent) return SGEMM_ERR_INVALID_VALUE;
     if (experts < 1 || experts > sg::kMaxExperts) return SGEMM_ERR_INVALID_VALUE;
     const int b_rows = transB ? N : K, b_cols = transB ? K : N;  // B as stored
     if (lda < std::max(1, K) || ldb < std::max(1, b_cols) || ldc < std::max(1, N) || strideB < 0)
@@ -269,7 +273,7 @@ int check_slots(int tokens, int choices) {
 }
 
 int check_row(int type, int width, int ld) {
-    return known_type(type) && width >= 0 && ld >= std::max(1, width) ? SGEMM_OK : SGEMM_ERR_INVALID_VALUE;
+    return known_type(type) && width >= 0 && width <= kMaxExtent && ld >= std::max(1, width) ? SGEMM_OK : SGEMM_ERR_INVALID_VALUE;
 }
 
 }  // namespace

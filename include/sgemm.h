@@ -262,16 +262,20 @@ int sgemm_check_args_mixed(int in_type, int transA, int transB, int M, int N, in
  * A may have any alignment and leading dimension.  B is read in place when
  * transB = 1, B is 16-byte aligned and ldb is a multiple of 16 (in the expert
  * form strideB too); otherwise it is first copied into the re-layout workspace
- * (sgemm_last_relayout then reports bit 1; one more launch).  The rows of A are
- * expanded to FP16 in the same workspace, in several passes where they do not
- * fit.  Without the workspace, with SGEMM_RELAYOUT_OFF where B would be copied,
- * where the copy does not fit, or with SGEMM_VARIANT_GENERIC or _GENERIC_I8
- * pinned, the generic kernel runs.  Otherwise as sgemm_run: no allocation, no
+ * (sgemm_last_relayout then reports bit 1).  A's rows are copied there where they
+ * do not start on 16-byte boundaries and, by the calls with many rows, expanded
+ * to FP16 (2 bytes an element), in several passes where they do not fit.  One
+ * launch makes all copies of a pass, and one multiplies: 1 launch for aligned
+ * calls of few rows, else 2 a pass (sgemm_last_launches); sgemm_last_variant
+ * reports the CTAs that share a tile's K range.  Without the workspace where a
+ * copy is needed, with SGEMM_RELAYOUT_OFF where B would be copied, where the
+ * copies do not fit, or with SGEMM_VARIANT_GENERIC or _GENERIC_I8 pinned, the
+ * generic kernel runs.  Otherwise as sgemm_run: no allocation, no
  * synchronization, device pointers, one handle per concurrently running stream.
  *
  * Checks, in order: handle, device, then (sgemm_check_args_int8)
- * SGEMM_ERR_INVALID_VALUE for an unknown out_type or transB, a negative size, K
- * above 131071, lda < max(1, K), ldb or ldc below its minimum; nothing is done
+ * SGEMM_ERR_INVALID_VALUE for an unknown out_type or transB, a negative size, M or
+ * N above 2^30, K above 131071, lda < max(1, K), ldb or ldc below its minimum; nothing is done
  * when M == 0 or N == 0; SGEMM_ERR_NULL if C, scaleA or scaleB (or A or B while
  * K > 0) is NULL; SGEMM_ERR_INVALID_VALUE if C, a scale array or the bias is
  * not aligned to its element size; SGEMM_ERR_ALIAS if C overlaps an input. */
@@ -312,8 +316,8 @@ int sgemm_check_args_int8_experts(int transB, int out_type, int experts, int row
  * with m < 127 * 2^-126 (all zeros among them) gives Q = 0, scale = 0; a row
  * with an infinity or a NaN gives Q = 0, scale = NaN, so that every product
  * with it is NaN.  K == 0 gives scales of 0.  Checks: handle, device,
- * SGEMM_ERR_INVALID_VALUE (unknown type, negative size, leading dimension
- * below max(1, K)), M == 0 does nothing, SGEMM_ERR_NULL,
+ * SGEMM_ERR_INVALID_VALUE (unknown type, negative size, K above 2^30, leading
+ * dimension below max(1, K)), M == 0 does nothing, SGEMM_ERR_NULL,
  * SGEMM_ERR_INVALID_VALUE (a pointer not aligned to its element size),
  * SGEMM_ERR_ALIAS (any two of the three overlap). */
 int sgemm_quantize_rows(sgemm_handle_t h, int type, int M, int K, const void *X, int ldx, int8_t *Q, int ldq,
@@ -351,8 +355,8 @@ int sgemm_quantize_rows(sgemm_handle_t h, int type, int M, int K, const void *X,
  * `type` once; weights and dweights are FP32.
  *
  * Checks, in order: handle, device, SGEMM_ERR_INVALID_VALUE (a negative size,
- * choices < 1, too many slots or experts, an unknown type, a leading dimension
- * below max(1, width)), nothing is done when there is nothing to write,
+ * choices < 1, too many slots or experts, width above 2^30, an unknown type, a
+ * leading dimension below max(1, width)), nothing is done when there is nothing to write,
  * SGEMM_ERR_NULL, SGEMM_ERR_INVALID_VALUE (a pointer not aligned to its element
  * size), SGEMM_ERR_ALIAS (an output overlaps an input or another output).  All
  * enqueue on `stream`, allocate nothing and do not synchronize. */
