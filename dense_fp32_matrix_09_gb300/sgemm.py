@@ -1,7 +1,7 @@
 """ctypes binding of libsgemm.so, with the entry-point names of include/sgemm.h.
 
-Argument marshalling only: every step of C = alpha*A*B + beta*C runs in the
-CUDA library.  Matrix arguments may be raw device addresses (int) or objects
+Argument marshalling only: every step of C = alpha*A*B + beta*C, of the int8
+products and of the expert routing runs in the CUDA library.  Matrix arguments may be raw device addresses (int) or objects
 with ``data_ptr()`` (torch tensors); streams may be an int handle, a
 ``torch.cuda.Stream`` or ``None`` (torch's current stream).  A non-zero
 status raises ``SgemmError``.  If the library has not been built the first
@@ -507,6 +507,58 @@ def sgemm_debug_set_stream_k_sums(h, mode: int) -> None:
     _check(lib().sgemm_debug_set_stream_k_sums(h, int(mode)), "sgemm_debug_set_stream_k_sums")
 
 
+def _element_type(t) -> int:
+    """The library's value of a tensor's element type (FP32, BF16, FP16)."""
+    import torch
+    kinds = {torch.float32: IN_F32, torch.bfloat16: IN_BF16, torch.float16: IN_F16}
+    if t.dtype not in kinds:
+        raise ValueError(f"FP32, BF16 or FP16 is wanted, got {t.dtype}")
+    return kinds[t.dtype]
+
+
+def _ld(t) -> int:
+    """Leading dimension of a 2-D tensor (one row: any value that its columns fit)."""
+    return max(t.stride(0), t.shape[1], 1)
+
+
+def _rows_of(name, t, dtype=None) -> None:
+    if t.dim() != 2 or (t.numel() and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be 2-D with unit column stride and rows that do not overlap")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _vector(name, t, n, dtype=None) -> None:
+    import torch
+    want = dtype or torch.float32
+    if tuple(t.shape) != (n,) or t.dtype != want or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {want} vector of {n}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _weights(t, tokens, choices) -> None:
+    import torch
+    if tuple(t.shape) != (tokens, choices) or t.dtype != torch.float32 or not t.is_contiguous():
+        raise ValueError(f"weights must be a contiguous {tokens} x {choices} FP32 tensor")
+
+
+def _slots(rows, tokens=None) -> tuple[int, int]:
+    import torch
+    if rows.dim() != 2 or rows.dtype != torch.int32 or not rows.is_contiguous() or \
+            (tokens is not None and rows.shape[0] != tokens):
+        raise ValueError("rows must be a contiguous tokens x choices int32 tensor")
+    return rows.shape[0], rows.shape[1]
+
+
+def _result(out, M, N, out_dtype, device):
+    import torch
+    if out is None:
+        return torch.empty(M, N, dtype=out_dtype or torch.bfloat16, device=device)
+    _rows_of("out", out, out_dtype)
+    if tuple(out.shape) != (M, N):
+        raise ValueError(f"out must be {M} x {N}, got {tuple(out.shape)}")
+    return out
+
+
 class Sgemm:
     """A handle as a context manager: ``with Sgemm() as g: g.run(...)``."""
 
@@ -530,6 +582,130 @@ class Sgemm:
         sgemm_run(self.h, M, N, K, alpha, A, max(A.stride(0), 1), B, max(B.stride(0), 1), beta, C,
                   max(C.stride(0), 1), stream)
         return C
+
+    # -- 8-bit products and expert routing on torch tensors: shapes and types are
+    #    checked here, results are new tensors on the inputs' device --------------
+    def quantize(self, X, stream=None):
+        """(Q, scale): the rows of X (2-D, FP32/BF16/FP16) in int8 and their FP32 scales."""
+        import torch
+        kind = _element_type(X)
+        _rows_of("X", X)
+        M, K = X.shape
+        Q = torch.empty(M, K, dtype=torch.int8, device=X.device)
+        scale = torch.empty(M, dtype=torch.float32, device=X.device)
+        sgemm_quantize_rows(self.h, kind, M, K, X, _ld(X), Q, max(K, 1), scale, stream)
+        return Q, scale
+
+    def matmul_int8(self, A, scaleA, B, scaleB, bias=None, out_dtype=None, out=None, stream=None):
+        """scaleA[:, None] * scaleB * (A @ B.T) + bias for int8 A (M x K) and B (N x K);
+        `out_dtype` (BF16 unless given) or `out` says of which type."""
+        import torch
+        _rows_of("A", A, torch.int8)
+        _rows_of("B", B, torch.int8)
+        (M, K), (N, K2) = A.shape, B.shape
+        if K2 != K:
+            raise ValueError(f"shape mismatch: {tuple(A.shape)} @ {tuple(B.shape)}.T")
+        _vector("scaleA", scaleA, M)
+        _vector("scaleB", scaleB, N)
+        if bias is not None:
+            _vector("bias", bias, N)
+        out = _result(out, M, N, out_dtype, A.device)
+        sgemm_run_int8(self.h, 1, _element_type(out), M, N, K, A, _ld(A), scaleA, B, _ld(B), scaleB, bias, out, _ld(out),
+                       stream)
+        return out
+
+    def matmul_int8_experts(self, offsets, A, scaleA, B, scaleB, bias=None, out_dtype=None, out=None, stream=None):
+        """As matmul_int8 for rows sorted by expert: rows offsets[e] .. offsets[e+1]-1
+        of A with B[e] (experts x N x K, contiguous); scaleB, bias: experts x N.  Rows of
+        no expert are left as they are in `out` (zeros without it)."""
+        import torch
+        _rows_of("A", A, torch.int8)
+        if B.dim() != 3 or B.dtype != torch.int8 or not B.is_contiguous() or B.shape[2] != A.shape[1]:
+            raise ValueError(f"B must be a contiguous experts x N x {A.shape[1]} int8 tensor, got {tuple(B.shape)}")
+        (E, N, K), R = B.shape, A.shape[0]
+        _vector("offsets", offsets, E + 1, torch.int32)
+        _vector("scaleA", scaleA, R)
+        for name, t in (("scaleB", scaleB), ("bias", bias)):
+            if t is not None and (tuple(t.shape) != (E, N) or t.dtype != torch.float32 or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {E} x {N} FP32 tensor")
+        if out is None:
+            out = torch.zeros(R, N, dtype=out_dtype or torch.bfloat16, device=A.device)
+        out = _result(out, R, N, out_dtype, A.device)
+        sgemm_run_int8_experts(self.h, 1, _element_type(out), E, R, N, K, offsets, A, _ld(A), scaleA, B, max(K, 1),
+                               N * K, scaleB, bias, out, _ld(out), stream)
+        return out
+
+    def expert_sort(self, ids, experts, stream=None):
+        """(offsets, rows, source) of ids (tokens x choices, int32)."""
+        import torch
+        if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
+            raise ValueError("ids must be a contiguous tokens x choices int32 tensor")
+        tokens, choices = ids.shape
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+        rows = torch.empty(tokens, choices, dtype=torch.int32, device=ids.device)
+        source = torch.empty(tokens * choices, dtype=torch.int32, device=ids.device)
+        sgemm_expert_sort(self.h, tokens, choices, experts, ids, offsets, rows, source, stream)
+        return offsets, rows, source
+
+    def expert_dispatch(self, X, rows, stream=None):
+        """The tokens' rows in the experts' order (tokens * choices rows; those of no slot are zero)."""
+        import torch
+        _rows_of("X", X)
+        tokens, choices = _slots(rows, X.shape[0])
+        Y = torch.zeros(tokens * choices, X.shape[1], dtype=X.dtype, device=X.device)
+        sgemm_expert_dispatch(self.h, _element_type(X), tokens, choices, X.shape[1], X, _ld(X), rows, Y, _ld(Y), stream)
+        return Y
+
+    def expert_dispatch_int8(self, X, rows, stream=None):
+        """(Q, scale): expert_dispatch and quantize in one pass."""
+        import torch
+        _rows_of("X", X)
+        tokens, choices = _slots(rows, X.shape[0])
+        Q = torch.zeros(tokens * choices, X.shape[1], dtype=torch.int8, device=X.device)
+        scale = torch.zeros(tokens * choices, dtype=torch.float32, device=X.device)
+        sgemm_expert_dispatch_int8(self.h, _element_type(X), tokens, choices, X.shape[1], X, _ld(X), rows, Q, _ld(Q),
+                                   scale, stream)
+        return Q, scale
+
+    def expert_dispatch_grad(self, dY, rows, stream=None):
+        """dX from the gradient of expert_dispatch's result."""
+        import torch
+        tokens, choices = _slots(rows)
+        _rows_of("dY", dY)
+        if dY.shape[0] != tokens * choices:
+            raise ValueError(f"dY must have {tokens * choices} rows, got {dY.shape[0]}")
+        dX = torch.empty(tokens, dY.shape[1], dtype=dY.dtype, device=dY.device)
+        sgemm_expert_dispatch_grad(self.h, _element_type(dY), tokens, choices, dY.shape[1], dY, _ld(dY), rows, dX, _ld(dX),
+                                   stream)
+        return dX
+
+    def expert_combine(self, Y, rows, weights, stream=None):
+        """sum_j weights[t, j] * Y[rows[t, j]]."""
+        import torch
+        tokens, choices = _slots(rows)
+        _rows_of("Y", Y)
+        _weights(weights, tokens, choices)
+        if Y.shape[0] != tokens * choices:
+            raise ValueError(f"Y must have {tokens * choices} rows, got {Y.shape[0]}")
+        out = torch.empty(tokens, Y.shape[1], dtype=Y.dtype, device=Y.device)
+        sgemm_expert_combine(self.h, _element_type(Y), tokens, choices, Y.shape[1], Y, _ld(Y), rows, weights, out, _ld(out),
+                             stream)
+        return out
+
+    def expert_combine_grad(self, dout, Y, rows, weights, stream=None):
+        """(dY, dweights) of expert_combine; rows of no slot have a zero gradient."""
+        import torch
+        tokens, choices = _slots(rows, dout.shape[0])
+        _rows_of("dout", dout, Y.dtype)
+        _rows_of("Y", Y)
+        _weights(weights, tokens, choices)
+        if tuple(Y.shape) != (tokens * choices, dout.shape[1]):
+            raise ValueError(f"Y must be {tokens * choices} x {dout.shape[1]}, got {tuple(Y.shape)}")
+        dY = torch.zeros_like(Y, memory_format=torch.contiguous_format)
+        dweights = torch.empty(tokens, choices, dtype=torch.float32, device=Y.device)
+        sgemm_expert_combine_grad(self.h, _element_type(Y), tokens, choices, Y.shape[1], dout, _ld(dout), Y, _ld(Y), rows,
+                                  weights, dY, _ld(dY), dweights, stream)
+        return dY, dweights
 
     @property
     def last_variant(self):
