@@ -5,7 +5,7 @@ Each translation unit under csrc/ is compiled for sm_103a only
 ``_build/libsgemm.so`` next to this file.  A rebuild happens only when a
 source or header is newer than the library.  Next to it, the host compiler
 builds ``_build/_sgemm_calls.so`` from csrc/pycalls.c: the CPython module that
-marshals the arguments of the binding's two enqueue calls (the binding falls
+marshals the arguments of the binding's enqueue calls (the binding falls
 back to ctypes without it).
 """
 from __future__ import annotations
@@ -27,7 +27,7 @@ LIB = os.path.join(BUILD, "libsgemm.so")
 BUILD_CHECKED = os.path.join(HERE, "_build_checks")
 LIB_CHECKED = os.path.join(BUILD_CHECKED, "libsgemm_checks.so")
 CHECK_FLAGS = ["-DSGEMM_DEVICE_CHECKS"]
-# The CPython argument-marshalling module for sgemm_run / sgemm_run_ex
+# The CPython argument-marshalling module of the enqueue calls
 CALLS_SRC = os.path.join(CSRC, "pycalls.c")
 CALLS = os.path.join(BUILD, "_sgemm_calls.so")
 calls_build_error: str | None = None

@@ -7,7 +7,9 @@
 //    destinations (dispatch): it is read and quantized once, written
 //    `choices` times.  One pass over HBM: a row stays in the registers of the
 //    TPR threads that share it (up to 4 x 8 elements a thread; longer rows are
-//    read a second time, from L2).
+//    read a second time, from L2).  8192 x 8192 BF16: 31 us, 6.5 TB/s (with a
+//    branch for the end of a row around each load, and so one load in flight at a
+//    time, 58 us).
 //  * sort_kernel -- the (token, choice) slots in a stable order by expert: a
 //    counting sort.  Within a warp the 32 slots of one step that name the same
 //    expert find one another by ballots and take consecutive places, which
@@ -15,10 +17,15 @@
 //    exclusive sums over the warps (and, with several CTAs, over the CTAs before)
 //    place each slot.
 //    Integers only and no atomic whose order matters: the same order every time.
+//    32768 slots over 64 experts: 6.9 us, of which two launches are about 5.5;
+//    2048 slots and fewer take one CTA and one launch (2.7 us).
 //  * move_kernel, gather_kernel, combine_grad_kernel -- the rows' way to the
 //    experts, back, and the gradients; each reads and writes every row once
 //    (16 bytes a thread and step where alignment allows), sums in FP32 in
-//    ascending choice order and rounds once.
+//    ascending choice order and rounds once.  8192 tokens, 4 choices, 4096 elements
+//    of 16 bits: 51.6 us out (6.5 TB/s), 54.7 back (6.1), the weighted gradient 89.9
+//    (6.7); rows of an odd number of 16-bit elements, which take 2-byte accesses,
+//    run at half of that (2475 elements: 43, 59 and 90 us).
 // No load is a read-only-cache load (ld.global.nc): what is read may have been
 // written by the kernel before, whose end the launch overlaps.  Rows, read once, go
 // past L1 (ld.global.cg); row numbers and weights, which a block's warps share, do

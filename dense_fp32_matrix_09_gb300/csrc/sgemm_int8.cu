@@ -12,39 +12,59 @@
 // assembled for it) and the CUDA cores' and mma.sync's integer rates are far
 // below the 16-bit rate of tcgen05.  An int8 is exact in FP16, a product of two
 // in FP32, and a sum of 1024 such products has magnitude <= 2^24, so it is an
-// integer that FP32 holds exactly: the kernel multiplies with .kind::f16, FP32
-// accumulators in tensor memory, and moves them into int32 registers every
-// 1024 k.  Sums of integers do not depend on their order, so every split of K
-// gives the same bits.
+// integer that FP32 holds exactly: the kernels multiply with .kind::f16, FP32
+// accumulators in tensor memory, and move them into int32 registers at least
+// that often.  Sums of integers do not depend on their order, so every tile and
+// every split of K gives the same bits.
 //
-//  * int8_tc_kernel -- D[channel][token] = B * A^T with the channels as the
-//    MMA's M (128 rows) and a tile of NT tokens as its N, so that few tokens
-//    cost a narrow tile and not a padded one.  B crosses HBM and shared memory
-//    as int8 (half the bytes of 16-bit operands; it is what a decode step is
-//    bound by) and becomes FP16 only on its way into tensor memory, where the
-//    MMA reads it as its A operand: shared memory sees one 8-bit write and one
-//    8-bit read of it.  The tokens' rows are converted to FP16 once, by
-//    int8_to_f16_kernel, and read by TMA.
-//      warp 0     TMA producer: a ring of stages of 128 k (B: 128 x 128 bytes,
-//                 tokens: two swizzled boxes of 64 k x NT)
-//      warp 1     one lane issues the MMAs; owns the tensor memory
-//      warp 2     sums up the experts' token tiles once, at the start
-//      warps 4-11 two warpgroups convert half of each stage: a thread reads 64
-//                 bytes of its channel (16 at a time, conflict-free through the
-//                 swizzle), turns byte b into the FP16 bits 0x6400 + (b ^ 0x80)
-//                 = 1152 + b, subtracts 1152 (exact), and stores 32 columns of
-//                 tensor memory.  (Alternate stages would not do: a warp that
-//                 skips a phase of a stage's barrier cannot tell by its parity
-//                 whether the phase before has ended when the ring is odd.)
-//      warps 12.. one or two warpgroups drain the accumulators (two of NT
-//                 columns each, so that the next 1024 k start at once) and
-//                 write C: a warp's lanes are 32 consecutive channels of a token
-//    Tensor memory: 2 x NT accumulator columns and 4 stages of 64 columns of B.
-//    Persistent over (expert, token tile, channel tile) units, token tiles
-//    innermost within groups of 16 so that concurrent CTAs share B's tiles in L2.
-//    With few tiles the 2, 4 or 8 CTAs of a cluster share a tile's K range;
-//    each sends the others their columns' int32 partial sums through
-//    distributed shared memory (tiles of up to 64 tokens, one epilogue warpgroup).
+// Both tensor-core kernels compute D[channel][token] = B * A^T, the channels as
+// the MMA's M and a tile of tokens as its N, so that few tokens cost a narrow tile
+// and not a padded one.  B crosses HBM, L2 and shared memory as int8 (half the
+// bytes of 16-bit operands; a decode step is bound by them) and becomes FP16
+// only on its way into tensor memory, where the MMA reads it as its A operand:
+// a converting thread reads its channel's 128 bytes of a stage (16 at a time,
+// conflict-free through the TMA's swizzle), makes of byte b the FP16 bits
+// 0x6400 + (b ^ 0x80) = 1152 + b, subtracts 1152 (exact: 5 instructions for 4
+// bytes) and stores 64 columns of its lane.  A stage's stores are waited for
+// while the next one is read.  Both are persistent over (expert, token tile,
+// channel tile) units, token tiles innermost within groups so that concurrent
+// CTAs share B's tiles in L2; the MMAs are issued by an elected lane of a warp
+// whose addresses are uniform (from one lane of a divergent warp, with its
+// descriptors moved to uniform registers one by one, an MMA takes about 150
+// cycles to issue: 8192^3 1138 us instead of 783).
+//
+//  * int8_tc_kernel -- up to 64 tokens a tile, 128 channels, two CTAs an SM, the
+//    tokens' int8 rows expanded here too:
+//      warp 0     TMA producer: stages of 128 k, B 128 x 128 bytes and the tokens
+//      warp 1     MMA issuer; owns the tensor memory (two accumulators of NT
+//                 columns, drained in turn, and two stages of B)
+//      warps 2-3  the stage's tokens to FP16 in the MMA's layout
+//      warps 4-7  B to FP16 in tensor memory
+//      warps 8-11 accumulators to C: a warp's lanes are 32 consecutive channels of
+//                 a token; its scales are asked for before the sums are ready
+//    With few tiles the 2, 4 or 8 CTAs of a cluster share a tile's K range and
+//    send one another their columns' int32 partial sums through distributed
+//    shared memory.  Bound by HBM once B is large (32 experts x 4096 x 4096 and
+//    128 rows: 86 us, 6.3 TB/s), by the chain of latencies before (one token x 4096 x
+//    4096: 6.4 us from one call's end to the next's, 3.9 of them from the first
+//    load to the last sum; 64 x 8192 x 8192: 20 us, 12.5 of them at 5.3 TB/s).
+//    Prefetching further stages into L2 made both slower.
+//  * int8_tc_pair_kernel -- 256 channels x 128 or 256 tokens on a CTA pair
+//    (cta_group::2), the tokens as FP16 from int8_copies_kernel: at this size
+//    expanding them in the kernel would take all of the shared memory's
+//    bandwidth.  Accumulators of 256 columns leave no room for a second set, so
+//    they are worked on as halves of the tokens, two stages of one and two of the
+//    other in turn, and each half is drained while the other is added to; data
+//    whose tokens are not at the extremes needs a drain every 4096 k or so only
+//    (chunk_of).  Warpgroups: control (B and token producers, MMA issuer),
+//    conversion, and two that take 128 columns a thread (setmaxnreg).
+//    Signals that only guard tensor memory go to the other CTA without a release
+//    at cluster scope, which costs its thread 1500 cycles (8192^3 1184 us instead
+//    of 693).  8192^3: 581 us in short runs, 1890 TFLOP/s, as much as the
+//    measured rate of cuBLAS in BF16, and 635 us (1730) when repeated until the
+//    power limit shows; 31 us of it are the tokens' conversion.  Of a stage of
+//    1130 cycles the MMAs take 1024; without the conversion and all loads it
+//    would be 1070.
 //  * int8_generic_kernel -- any layout and alignment, dp4a on the CUDA cores.
 //  * int8_copies_kernel -- the tokens' rows as FP16 or on 16-byte boundaries, and B
 //    as the TMA can read it (stored K x N, or not on 16-byte boundaries).

@@ -78,7 +78,7 @@ class SgemmError(RuntimeError):
 
 
 _lib = None
-_calls = None          # the compiled marshalling module for sgemm_run / sgemm_run_ex, when built
+_calls = None          # the compiled marshalling module of the enqueue calls, when built
 _calls_tried = False
 
 
@@ -175,7 +175,7 @@ def _current_stream_handle() -> int:
 
 
 def calls_module():
-    """The CPython module that marshals sgemm_run / sgemm_run_ex arguments
+    """The CPython module that marshals the arguments of the enqueue calls
     (built next to the library by build.py), bound to the loaded library; None
     when it was not built -- the two calls then go through ctypes."""
     global _calls, _calls_tried
