@@ -270,6 +270,13 @@ struct Int8Args {
     int n_peaks;
 };
 cudaError_t launch_int8_generic(const Int8Args &a, cudaStream_t stream);
+// One expert, B stored N x K on any alignment, up to kI8FewRows rows (rounded up to
+// 1, 2, 4 or 8), which take up to kI8FewBytes of shared memory.
+constexpr int kI8FewRows = 8, kI8FewBytes = 64 << 10;
+constexpr int int8_few_bytes(int rows, int K) {
+    return (rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8) * ((K + 15) / 16 * 16);
+}
+cudaError_t launch_int8_few(const Int8Args &a, int num_sms, cudaStream_t stream);
 // The copies of a call's operands, one launch.  a_dst (NULL: none): the rows of A,
 // a_rows x a_ld, as FP16 where peaks is not NULL (a_ld a multiple of 64; peaks has
 // room for kI8Peaks sums of magnitudes, see Int8Args, of which a_blocks are

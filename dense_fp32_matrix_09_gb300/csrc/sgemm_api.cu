@@ -744,7 +744,7 @@ CallPlan plan_call(const sgemm_ctx *h, int transA, int transB, int M, int N, int
     if (!tc_reachable && (variant == SGEMM_VARIANT_TC_3XTF32 || variant == SGEMM_VARIANT_TC_3XTF32_PAIR))
         variant = SGEMM_VARIANT_AUTO;
     if (variant == SGEMM_VARIANT_TC_F16_PAIR || variant == SGEMM_VARIANT_GENERIC_F16 ||
-        variant == SGEMM_VARIANT_TC_I8 || variant == SGEMM_VARIANT_GENERIC_I8)
+        variant == SGEMM_VARIANT_TC_I8 || variant == SGEMM_VARIANT_GENERIC_I8 || variant == SGEMM_VARIANT_FEW_I8)
         variant = SGEMM_VARIANT_AUTO;  // variants of the 16-bit and 8-bit calls only
     if (variant == SGEMM_VARIANT_AUTO) {
         // 3xTF32 mode: the CTA-pair tensor-core kernel once there are at least
@@ -910,6 +910,7 @@ const char *sgemm_variant_name(int v) {
         case SGEMM_VARIANT_GENERIC_F16: return "generic_f16";
         case SGEMM_VARIANT_TC_I8: return "tc_i8";
         case SGEMM_VARIANT_GENERIC_I8: return "generic_i8";
+        case SGEMM_VARIANT_FEW_I8: return "few_i8";
         default: return "unknown";
     }
 }

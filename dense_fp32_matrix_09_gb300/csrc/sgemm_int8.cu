@@ -276,6 +276,38 @@ __device__ __forceinline__ uint4 load_int8x16(const int8_t *row, int k, int K, b
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Rows on any alignment, a warp at a time: lane l reads the aligned 16 bytes in
+// which bytes k .. k + 15 of the row begin (ALIGNED: that is those bytes), and
+// takes their end from lane l + 1, which reads the next ones; so 31 lanes get 16
+// bytes each.  No byte outside [row, row + K) is read: the chunks at a row's
+// ends are put together byte by byte, with zeros outside.
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 load_chunk(const int8_t *row, int k, int K) {
+    const int off = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u);
+    const int first = k - off;  // of the row, the chunk's first byte
+    if (first >= 0 && first + 16 <= K) return __ldcg(reinterpret_cast<const uint4 *>(row + first));
+    uint32_t w[4] = {};
+    if (first < K)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (first + i >= 0 && first + i < K) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(row[first + i])) << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The 16 bytes that begin in this lane's chunk (lane 31: not its own).
+__device__ __forceinline__ uint4 join_next(const uint4 &v, const int8_t *row) {
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15u);
+    uint32_t w[8] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[4 + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = off & 8u ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = off & 4u ? w[i + 1] : w[i];
+    const uint32_t bits = 8 * (off & 3u);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
 // The tokens' rows as FP16, 16 k a thread; ldd is a multiple of 64, so its rows
 // divide into whole threads.  *peak: the largest sum of |a| over the 512 k (of
 // one row, or the end of one and the start of the next) that a warp of the block
@@ -317,16 +349,30 @@ __device__ __forceinline__ void rows_to_f16(const Int8Copies &c, int block, int 
 }
 
 // Rows of int8 copied onto 16-byte boundaries (ldd a multiple of 16, columns
-// K..ldd-1 zero), 16 k a thread; row r of matrix m is m * rows + r of dst.
+// K..ldd-1 zero), 31 pieces of a row a warp and load, four loads at a time; row r of
+// matrix m is m * rows + r of dst.
+constexpr int kRealignRuns = 4;
 __device__ __forceinline__ void realign(const int8_t *src, long long ld, long long stride, int matrices, int rows, int K,
                                         int8_t *dst, int ldd, int block, int blocks) {
-    const int per_row = ldd / 16;
-    const long long total = static_cast<long long>(matrices) * rows * per_row;
-    for (long long i = block * 256ll + threadIdx.x; i < total; i += blocks * 256ll) {
-        const long long row = div_floor(i, per_row), m = div_floor(row, rows);
-        const int k = static_cast<int>(i - row * per_row) * 16;
-        reinterpret_cast<uint4 *>(dst)[i] = load_int8x16(src + m * stride + (row - m * rows) * ld, k, K, false);
+    const int pieces = ldd / 16, tasks = (pieces + 31 * kRealignRuns - 1) / (31 * kRealignRuns), lane = threadIdx.x & 31;
+    const long long total = static_cast<long long>(matrices) * rows * tasks;
+    for (long long i = block * 8ll + (threadIdx.x >> 5); i < total; i += blocks * 8ll) {
+        const long long row = div_floor(i, tasks), m = matrices > 1 ? div_floor(row, rows) : 0;
+        const int piece = static_cast<int>(i - row * tasks) * (31 * kRealignRuns) + lane;
+        const int8_t *s = src + m * stride + (row - m * rows) * ld;
+        uint4 v[kRealignRuns];
+#pragma unroll
+        for (int r = 0; r < kRealignRuns; ++r) v[r] = load_chunk<false>(s, (piece + 31 * r) * 16, K);
+#pragma unroll
+        for (int r = 0; r < kRealignRuns; ++r) {
+            const uint4 o = join_next(v[r], s);
+            if (lane < 31 && piece + 31 * r < pieces) reinterpret_cast<uint4 *>(dst + row * ldd)[piece + 31 * r] = o;
+        }
     }
+}
+// Blocks for it: a warp a task.
+long long realign_blocks(long long rows, int ldd) {
+    return (rows * ((ldd / 16 + 31 * kRealignRuns - 1) / (31 * kRealignRuns)) + 7) / 8;
 }
 
 // B stored K x N -> N x ldd: a tile of 128 k x 64 channels.  A thread reads four
@@ -406,6 +452,111 @@ __global__ void __launch_bounds__(256) int8_copies_kernel(const Int8Copies c) {
         rows_to_f16(c, block - c.b_blocks, c.a_blocks, c.peaks + block - c.b_blocks);
     } else {
         realign(c.A, c.lda, 0, 1, c.a_rows, c.K, static_cast<int8_t *>(c.a_dst), c.a_ld, block - c.b_blocks, c.a_blocks);
+    }
+}
+
+// ---- few tokens: the CUDA cores -----------------------------------------------------
+// Up to 8 tokens: a warp takes two channels, its lanes 16 k each of a step, dp4a
+// against the tokens' rows in shared memory; warps of a CTA may share a channel's
+// K range (`split`).  One launch, no copies (B on any alignment), no cluster: a
+// step of one or a few tokens is made of the launch and one latency of HBM, and
+// for so few sums dp4a's rate does not show.  One token x 4096 x 4096 4.8 us (on the
+// tensor cores 7.6), x 8192 x 8192 13.7 (15.8; 4.9 TB/s), x 8190 x 8190 20.7 (36, with
+// B's copy); 4 tokens 6.9, 17.9, 30.4; 8 tokens 9.7 or more: choose_few in
+// sgemm_ops_api.cu says which kernel runs.
+constexpr int kFewThreads = 256;
+
+constexpr int kFewC = 2, kFewAhead = 2;  // channels a warp; steps whose loads are in flight
+
+// Four CTAs an SM (64 registers a thread) where the sums leave room for it: more
+// warps hide more than more loads a warp do (one token x 4096 x 4096: 4.8 us; four
+// steps ahead at two CTAs 6.2; 8 tokens spill at four).
+template <int MT, bool VEC>
+__global__ void __launch_bounds__(kFewThreads, MT <= 4 ? 4 : 2) int8_few_kernel(const Int8Args a, int split, int a_vec) {
+    constexpr int C = kFewC, AHEAD = kFewAhead;
+    constexpr int L = VEC ? 32 : 31;  // pieces of 16 k a step (join_next)
+    extern __shared__ uint4 rows[];   // [token][16 k], zeros beyond K and beyond the last token
+    __shared__ int part[kFewThreads / 32][MT * C];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pieces = (a.K + 15) / 16, steps = (pieces + L - 1) / L;
+    const int group = warp / split, member = warp % split, groups = kFewThreads / 32 / split;
+    const int n0 = (static_cast<int>(blockIdx.x) * groups + group) * C;
+    const int8_t *b[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) b[c] = a.B + static_cast<long long>(n0 + c < a.N ? n0 + c : a.N - 1) * a.ldb;
+    // the first steps of B into L2 while the kernel before this one ends
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) {
+        const int k = ((s * split + member) * L + lane) * 16;
+        if (k < a.K)
+#pragma unroll
+            for (int c = 0; c < C; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(b[c] + k));
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+
+    int sum[MT][C] = {};
+    uint4 raw[AHEAD][C];
+    auto fetch = [&](int s0) {
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s) {
+            const int k = (((s0 + s) * split + member) * L + lane) * 16;
+#pragma unroll
+            for (int c = 0; c < C; ++c) raw[s][c] = load_chunk<VEC>(b[c], k, a.K);
+        }
+    };
+    fetch(0);
+    for (int i = threadIdx.x; i < MT * pieces; i += kFewThreads) {
+        const int t = i / pieces, k = (i - t * pieces) * 16;
+        rows[i] = t < a.rows ? load_int8x16(a.A + static_cast<long long>(t) * a.lda, k, a.K, a_vec) : make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    const int mine = (steps - member + split - 1) / split;  // this warp's steps
+    for (int s0 = 0; s0 < mine; s0 += AHEAD) {
+        uint4 w[AHEAD][C];
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s)
+#pragma unroll
+            for (int c = 0; c < C; ++c) w[s][c] = VEC ? raw[s][c] : join_next(raw[s][c], b[c]);
+        if (s0 + AHEAD < mine) fetch(s0 + AHEAD);
+#pragma unroll
+        for (int s = 0; s < AHEAD; ++s) {
+            const int piece = ((s0 + s) * split + member) * L + lane;
+            if (piece < pieces && (VEC || lane < L)) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const uint4 x = rows[t * pieces + piece];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        sum[t][c] = __dp4a(static_cast<int>(x.x), static_cast<int>(w[s][c].x), sum[t][c]);
+                        sum[t][c] = __dp4a(static_cast<int>(x.y), static_cast<int>(w[s][c].y), sum[t][c]);
+                        sum[t][c] = __dp4a(static_cast<int>(x.z), static_cast<int>(w[s][c].z), sum[t][c]);
+                        sum[t][c] = __dp4a(static_cast<int>(x.w), static_cast<int>(w[s][c].w), sum[t][c]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int all = __reduce_add_sync(0xffffffffu, sum[t][c]);
+            if (lane == t * C + c) part[warp][lane] = all;
+        }
+    __syncthreads();
+    // one thread a token and channel: consecutive channels of a token together
+    for (int i = threadIdx.x; i < MT * groups * C; i += kFewThreads) {
+        const int t = i / (groups * C), ch = i % (groups * C);
+        const int n = static_cast<int>(blockIdx.x) * groups * C + ch;
+        if (t >= a.rows || n >= a.N) continue;
+        int total = 0;
+        for (int m = 0; m < split; ++m) total += part[ch / C * split + m][t * C + ch % C];
+        const float v = int8_value(total, __ldcg(a.scaleB + n), __ldcg(a.scaleA + t), a.bias ? __ldcg(a.bias + n) : 0.f);
+        with_out_type(a.out_type, [&](auto out) {
+            using Out = decltype(out);
+            static_cast<typename Out::T *>(a.C)[static_cast<long long>(t) * a.ldc + n] = Out::lo(Out::two(v, 0.f));
+        });
     }
 }
 
@@ -1412,6 +1563,11 @@ cudaError_t int8_prepare() {
     for (cudaError_t r : {prepare_direct<16>(), prepare_direct<32>(), prepare_direct<64>(), prepare_pair<128>(),
                           prepare_pair<256>()})
         if (e == cudaSuccess) e = r;
+    for (auto *k : {int8_few_kernel<1, false>, int8_few_kernel<1, true>, int8_few_kernel<2, false>,
+                    int8_few_kernel<2, true>, int8_few_kernel<4, false>, int8_few_kernel<4, true>,
+                    int8_few_kernel<8, false>, int8_few_kernel<8, true>})
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kI8FewBytes);
     return e;
 }
 
@@ -1426,6 +1582,29 @@ cudaError_t launch_int8_tc(const Int8Args &a, const CUtensorMap &tmB, const CUte
     }
 }
 
+template <int MT>
+static cudaError_t launch_few(const Int8Args &a, int num_sms, cudaStream_t stream) {
+    const bool vec = reinterpret_cast<uintptr_t>(a.B) % 16 == 0 && a.ldb % 16 == 0;
+    const int a_vec = reinterpret_cast<uintptr_t>(a.A) % 16 == 0 && a.lda % 16 == 0;
+    const int pieces = (a.K + 15) / 16, steps = (pieces + 31) / 32;
+    // warps share a channel's K range while that leaves each of them a step and
+    // all CTAs run at once (32 warps an SM)
+    constexpr int C = kFewC;
+    int split = 1;
+    const long long warps = (static_cast<long long>(a.N) + C - 1) / C;
+    while (split < kFewThreads / 32 && steps >= 2 * split && warps * split * 2 <= 32ll * num_sms) split *= 2;
+    const int per = kFewThreads / 32 / split * C;
+    return launch_dependent(vec ? int8_few_kernel<MT, true> : int8_few_kernel<MT, false>,
+                            dim3((a.N + per - 1) / per), dim3(kFewThreads), MT * pieces * 16, stream, 1, a, split, a_vec);
+}
+
+cudaError_t launch_int8_few(const Int8Args &a, int num_sms, cudaStream_t stream) {
+    if (a.rows <= 1) return launch_few<1>(a, num_sms, stream);
+    if (a.rows <= 2) return launch_few<2>(a, num_sms, stream);
+    if (a.rows <= 4) return launch_few<4>(a, num_sms, stream);
+    return launch_few<8>(a, num_sms, stream);
+}
+
 cudaError_t launch_int8_generic(const Int8Args &a, cudaStream_t stream) {
     const int y = (a.rows + kGTile - 1) / kGTile;
     const dim3 grid((a.N + kGTile - 1) / kGTile, y < 65535 ? y : 65535, a.experts);
@@ -1436,9 +1615,11 @@ cudaError_t launch_int8_copies(Int8Copies *c, cudaStream_t stream) {
     c->a_vec = reinterpret_cast<uintptr_t>(c->A) % 16 == 0 && c->lda % 16 == 0;
     c->b_vec = reinterpret_cast<uintptr_t>(c->B) % 4 == 0 && c->ldb % 4 == 0 && c->strideB % 4 == 0;
     auto capped = [](long long blocks) { return static_cast<int>(blocks < kI8Peaks ? blocks : kI8Peaks); };
-    c->a_blocks = c->a_dst ? capped((static_cast<long long>(c->a_rows) * (c->a_ld / 16) + 255) / 256) : 0;
+    c->a_blocks = !c->a_dst ? 0
+                  : c->peaks ? capped((static_cast<long long>(c->a_rows) * (c->a_ld / 16) + 255) / 256)
+                             : capped(realign_blocks(c->a_rows, c->a_ld));
     if (!c->b_dst) c->b_blocks = 0;
-    else if (c->b_trans) c->b_blocks = capped((static_cast<long long>(c->experts) * c->N * (c->b_ld / 16) + 255) / 256);
+    else if (c->b_trans) c->b_blocks = capped(realign_blocks(static_cast<long long>(c->experts) * c->N, c->b_ld));
     else c->b_blocks = capped(static_cast<long long>(c->experts) * ((c->b_ld + kTK - 1) / kTK) * ((c->N + kTN - 1) / kTN));
     return launch_dependent(int8_copies_kernel, dim3(c->a_blocks + c->b_blocks), dim3(256), 0, stream, 1, *c);
 }

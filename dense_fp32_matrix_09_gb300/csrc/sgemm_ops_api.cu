@@ -63,6 +63,7 @@ constexpr int kMaxInt8K = 131071;
 // 256 30.0); M = 2048 on pairs of 256 56 (of 128 72).
 struct TileChoice {
     int nt, ksplit;
+    double us;
 };
 TileChoice choose_tile(int rows, int experts, int N, int K, int num_sms, bool direct_copy) {
     struct Direct {
@@ -78,8 +79,7 @@ TileChoice choose_tile(int rows, int experts, int N, int K, int num_sms, bool di
     const int owners = std::min(experts, std::max(rows, 1));
     const long long each = cdiv(rows, owners);
     const int stages = static_cast<int>(cdiv(K, sg::kI8StageK));
-    TileChoice best{256, 1};
-    double least = 1e30;
+    TileChoice best{256, 1, 1e30};
     for (const Direct &d : kDirect) {
         const long long tiles = owners * cdiv(each, d.nt) * cdiv(N, sg::kI8TileN);
         for (int s = 1; s <= 8 && s <= stages; s *= 2) {
@@ -88,21 +88,29 @@ TileChoice choose_tile(int rows, int experts, int N, int K, int num_sms, bool di
             const double stage = ctas <= num_sms ? d.alone : 2 * d.shared;
             const double t = 4.3 + (direct_copy ? 2.0 : 0.0) + (s > 1 ? d.exchange + 0.1 * s : 0.0) +
                              static_cast<double>(cdiv(ctas, 2LL * num_sms)) * static_cast<double>(cdiv(stages, s)) * stage;
-            if (t < least) {
-                least = t;
-                best = {d.nt, s};
-            }
+            if (t < best.us) best = {d.nt, s, t};
         }
     }
     for (const Pair &p : kPair) {
         const long long units = owners * cdiv(each, p.nt) * cdiv(N, 2 * sg::kI8TileN);
         const double t = p.fixed + 3.0 * rows * K / 5.5e6 + static_cast<double>(cdiv(units, num_sms / 2)) * stages * p.stage;
-        if (t < least) {
-            least = t;
-            best = {p.nt, 1};
-        }
+        if (t < best.us) best = {p.nt, 1, t};
     }
     return best;
+}
+
+// Whether the kernel for few tokens beats the tensor cores' `tc_us` (by the same
+// kind of model; B's copy, which only they need, counted): a launch, B at the rate
+// that a warp's arithmetic leaves (lower on rows that have to be shifted), and
+// the tokens' way into shared memory.  E.g. one token 4.8 us against 7.6 (4096 x 4096),
+// 4 tokens 17.9 against 15.8 (8192 x 8192) and 4.2 against 6.9 (700 x 700), 8 tokens 9.7
+// against 7.7 and 5.5 against 6.9.
+bool choose_few(int rows, int N, int K, bool b_aligned, double tc_us) {
+    constexpr double kAligned[] = {0.14, 0.17, 0.23, 0.43}, kShifted[] = {0.27, 0.33, 0.41, 0.75};  // us a MB
+    const int i = rows <= 1 ? 0 : rows <= 2 ? 1 : rows <= 4 ? 2 : 3;
+    const double mb = 1e-6 * N * K;
+    const double few = b_aligned ? 2.9 + kAligned[i] * mb : 4.0 + kShifted[i] * mb;
+    return few + 5e-5 * rows * K < tc_us + (b_aligned ? 0.0 : 2.0 + 0.28 * mb);
 }
 
 int check_int8(int transB, int out_type, int experts, int rows, int N, int K, const int *offsets, bool grouped,
@@ -173,6 +181,16 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
     uint8_t *ws = reinterpret_cast<uint8_t *>(v.d_rl);
     size_t room = v.rl_bytes;
     const bool as_stored = transB && aligned(B, 16) && ldb % 16 == 0 && (experts == 1 || strideB % 16 == 0);
+    if (experts == 1 && !offsets && transB && K > 0 && rows <= sg::kI8FewRows &&
+        sg::int8_few_bytes(rows, K) <= sg::kI8FewBytes &&
+        (v.pinned == SGEMM_VARIANT_FEW_I8 ||
+         (v.pinned != SGEMM_VARIANT_TC_I8 && v.pinned != SGEMM_VARIANT_GENERIC_I8 && v.pinned != SGEMM_VARIANT_GENERIC &&
+          choose_few(rows, N, K, as_stored, tile.us)))) {
+        const cudaError_t e = sg::launch_int8_few(a, v.num_sms, stream);
+        if (e != cudaSuccess) return from_cuda(e);
+        sg::record_call(h, SGEMM_VARIANT_FEW_I8, 1, 1, 0);
+        return SGEMM_OK;
+    }
     const size_t b_bytes = as_stored ? 0 : static_cast<size_t>(experts) * N * kb;
     const size_t peak_room = direct ? 0 : sg::kI8Peaks * sizeof(int);
     const size_t b_room = (b_bytes + 1023) / 1024 * 1024 + peak_room;

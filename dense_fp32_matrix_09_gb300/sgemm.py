@@ -41,7 +41,8 @@ VARIANT_GENERIC_F16 = 10
 VARIANT_TMA_256x128 = 11
 VARIANT_TC_I8 = 12
 VARIANT_GENERIC_I8 = 13
-VARIANT_COUNT = 14
+VARIANT_FEW_I8 = 14
+VARIANT_COUNT = 15
 MATH_FP32 = 0
 MATH_3XTF32 = 1
 IN_F32 = 0

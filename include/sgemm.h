@@ -109,7 +109,9 @@ typedef enum {
     SGEMM_VARIANT_TC_I8 = 12,        /* sgemm_run_int8, sgemm_run_int8_experts only: int8 operands
                                         as exact FP16 on the tensor cores, int32 sums         */
     SGEMM_VARIANT_GENERIC_I8 = 13,   /* the same calls: any layout and alignment, CUDA cores  */
-    SGEMM_VARIANT_COUNT_ = 14
+    SGEMM_VARIANT_FEW_I8 = 14,       /* sgemm_run_int8 only: up to 8 rows of A, CUDA cores, B
+                                        stored N x K on any alignment                         */
+    SGEMM_VARIANT_COUNT_ = 15
     /* sgemm_run_ex: the TMA variants serve every (transA, transB) and any
      * batch up to 65535 when A and B are 16-byte aligned and lda, ldb (and,
      * for batch > 1, strideA, strideB) are multiples of 4, and operands that
@@ -262,11 +264,12 @@ int sgemm_check_args_mixed(int in_type, int transA, int transB, int M, int N, in
  * A may have any alignment and leading dimension.  B is read in place when
  * transB = 1, B is 16-byte aligned and ldb is a multiple of 16 (in the expert
  * form strideB too); otherwise it is first copied into the re-layout workspace
- * (sgemm_last_relayout then reports bit 1).  A's rows are copied there where they
+ * (sgemm_last_relayout then reports bit 1; calls of up to 8 rows of A may read
+ * it in place on any alignment).  A's rows are copied there where they
  * do not start on 16-byte boundaries and, by the calls with many rows, expanded
  * to FP16 (2 bytes an element), in several passes where they do not fit.  One
- * launch makes all copies of a pass, and one multiplies: 1 launch for aligned
- * calls of few rows, else 2 a pass (sgemm_last_launches); sgemm_last_variant
+ * launch makes all copies of a pass, and one multiplies: 1 launch where nothing
+ * is copied, else 2 a pass (sgemm_last_launches); sgemm_last_variant
  * reports the CTAs that share a tile's K range.  Without the workspace where a
  * copy is needed, with SGEMM_RELAYOUT_OFF where B would be copied, where the
  * copies do not fit, or with SGEMM_VARIANT_GENERIC or _GENERIC_I8 pinned, the

@@ -132,7 +132,8 @@ def test_parity(handle, M, N, K, dtype):
 @pytest.mark.parametrize("trans_b", [0, 1])
 @pytest.mark.parametrize("pads,offsets", [((0, 0, 0), (0, 0, 0)), ((3, 0, 5), (0, 0, 0)), ((16, 16, 4), (16, 16, 4)),
                                           ((1, 7, 1), (3, 5, 1)), ((0, 0, 0), (1, 1, 1))])
-def test_layouts_strides_and_alignment(handle, M, N, K, trans_b, pads, offsets):
+def test_layouts_strides_and_alignment(handle, pinned, M, N, K, trans_b, pads, offsets):
+    pinned(V.VARIANT_TC_I8)
     p = Problem(M, N, K, "bf16", trans_b=trans_b, bias=True, pads=pads, offsets=offsets, seed=2)
     p.check(p.run(handle))
     in_place = trans_b and (K + pads[1]) % 16 == 0 and offsets[1] % 16 == 0
@@ -158,13 +159,40 @@ def test_sums_are_exact_integers(handle, kind, M, N, K):
 def test_generic_variant_gives_the_same_bits(handle, pinned, variant, trans_b):
     for M, N, K in [(3, 70, 65), (100, 129, 1500)]:
         p = Problem(M, N, K, "f16", trans_b=trans_b, bias=True, pads=(1, 2, 3), seed=4)
-        pinned(V.VARIANT_AUTO)
+        pinned(V.VARIANT_TC_I8)
         first = p.run(handle)
         assert sgemm.sgemm_last_variant(handle)[0] == V.VARIANT_TC_I8
         pinned(variant)
         assert torch.equal(p.run(handle).view(torch.int16), first.view(torch.int16))
         assert sgemm.sgemm_last_variant(handle)[0] == V.VARIANT_GENERIC_I8
         p.check(first)
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 7, 8])
+@pytest.mark.parametrize("N,K", [(1, 1), (5, 15), (130, 16), (33, 17), (129, 496), (64, 511), (70, 1000), (3, 5000), (2000, 300)])
+@pytest.mark.parametrize("pads,offsets", [((0, 0, 0), (0, 0, 0)), ((16, 32, 2), (16, 16, 2)), ((1, 7, 1), (3, 5, 1)),
+                                          ((0, 4, 0), (2, 8, 0)), ((5, 1, 0), (0, 15, 3))])
+def test_few_tokens(handle, pinned, M, N, K, pads, offsets):
+    """The kernel for up to 8 tokens against the exact form and, bit for bit, the generic one."""
+    p = Problem(M, N, K, ["f32", "bf16", "f16"][M % 3], bias=N % 2 == 0, pads=pads, offsets=offsets, seed=10)
+    pinned(V.VARIANT_FEW_I8)
+    first = p.run(handle)
+    assert sgemm.sgemm_last_variant(handle)[0] == V.VARIANT_FEW_I8 and sgemm.sgemm_last_launches(handle) == 1
+    p.check(first)
+    pinned(V.VARIANT_GENERIC_I8)
+    assert torch.equal(p.run(handle), first)
+
+
+def test_few_tokens_at_the_extremes(handle, pinned):
+    """Its sums are the integers at -128 * -128 too, and calls beyond its reach run elsewhere."""
+    pinned(V.VARIANT_FEW_I8)
+    p = Problem(3, 40, 16000, "f32", kind="low", unit=True, seed=11)
+    assert torch.equal(p.run(handle), (p.a.double() @ p.b.double().t()).float())
+    assert sgemm.sgemm_last_variant(handle)[0] == V.VARIANT_FEW_I8
+    for M, K, trans_b in [(9, 64, 1), (3, 16400, 1), (2, 64, 0)]:   # rows, shared memory, layout
+        q = Problem(M, 40, K, "f32", trans_b=trans_b, seed=12)
+        q.check(q.run(handle))
+        assert sgemm.sgemm_last_variant(handle)[0] == V.VARIANT_TC_I8
 
 
 def test_relayout_off_runs_the_generic_kernel(handle, pinned):
