@@ -282,7 +282,7 @@ cudaError_t launch_int8_few(const Int8Args &a, int num_sms, cudaStream_t stream)
 // room for kI8Peaks sums of magnitudes, see Int8Args, of which a_blocks are
 // written), else as int8 on 16-byte boundaries (a_ld a multiple of 16).  b_dst
 // (NULL: none): experts x N x b_ld int8 of B_e, stored N x K (b_trans) or K x N.
-// Columns from K on are zero.
+// Columns from K on are zero in FP16 rows and hold anything in int8 ones.
 constexpr int kI8Peaks = 2048;
 struct Int8Copies {
     const int8_t *A;

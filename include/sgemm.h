@@ -259,7 +259,8 @@ int sgemm_check_args_mixed(int in_type, int transA, int transB, int M, int N, in
  * SGEMM_ERR_INVALID_VALUE) and float(sum) * scaleB * scaleA + bias is rounded
  * to C's type once, so results do not depend on the variant or on how the work
  * was split.  All 256 values of an int8 are taken as they are.  C is output
- * only.  K == 0 gives C = bias.  FP16 results beyond 65504 become infinite.
+ * only.  Bytes between the rows of A and of B may be read together with their
+ * neighbours, and do not matter.  K == 0 gives C = bias.  FP16 results beyond 65504 become infinite.
  *
  * A may have any alignment and leading dimension.  B is read in place when
  * transB = 1, B is 16-byte aligned and ldb is a multiple of 16 (in the expert
