@@ -301,9 +301,8 @@ struct Int8Copies {
 };
 cudaError_t launch_int8_copies(Int8Copies *c, cudaStream_t stream);
 constexpr int kI8TileN = 128, kI8StageK = 128;  // channels and k of one B stage (TMA box, 128-byte swizzle)
-// Token tiles: up to 64 by one CTA (or a cluster that splits K), 128 and 256 by CTA
-// pairs with 256 channels.
-constexpr int kI8TokenTiles[] = {16, 32, 64, 128, 256};
+// Token tiles (Int8Args::nt): 16, 32 and 64 by one CTA (or a cluster that splits K),
+// 128 and 256 by CTA pairs with 256 channels.
 // The most tiles of nt tokens that `rows` rows of `experts` experts make (the
 // experts' row counts are on the device).
 constexpr long long int8_most_tiles(int rows, int experts, int nt) {

@@ -80,8 +80,6 @@ struct AccessOf<2> { using T = uint16_t; };
 template <>
 struct AccessOf<4> { using T = uint32_t; };
 template <>
-struct AccessOf<8> { using T = uint2; };
-template <>
 struct AccessOf<16> { using T = uint4; };
 
 template <class T, int TPR, int A>

@@ -45,9 +45,9 @@
 //    With few tiles the 2, 4 or 8 CTAs of a cluster share a tile's K range and
 //    send one another their columns' int32 partial sums through distributed
 //    shared memory.  Bound by HBM once B is large (32 experts x 4096 x 4096 and
-//    128 rows: 86 us, 6.3 TB/s), by the chain of latencies before (one token x 4096 x
-//    4096: 6.4 us from one call's end to the next's, 3.9 of them from the first
-//    load to the last sum; 64 x 8192 x 8192: 20 us, 12.5 of them at 5.3 TB/s).
+//    128 rows: 86 us, 6.3 TB/s), by the chain of latencies before (16 x 4096 x 4096:
+//    6.4 us from one call's end to the next's, 3.9 of them from the first load to
+//    the last sum; 64 x 8192 x 8192: 20 us, 12.5 of them at 5.3 TB/s).
 //    Prefetching further stages into L2 made both slower.
 //  * int8_tc_pair_kernel -- 256 channels x 128 or 256 tokens on a CTA pair
 //    (cta_group::2), the tokens as FP16 from int8_copies_kernel: at this size
@@ -65,6 +65,7 @@
 //    power limit shows; 31 us of it are the tokens' conversion.  Of a stage of
 //    1130 cycles the MMAs take 1024; without the conversion and all loads it
 //    would be 1070.
+//  * int8_few_kernel -- up to 8 tokens on the CUDA cores, B on any alignment (below).
 //  * int8_generic_kernel -- any layout and alignment, dp4a on the CUDA cores.
 //  * int8_copies_kernel -- the tokens' rows as FP16 or on 16-byte boundaries, and B
 //    as the TMA can read it (stored K x N, or not on 16-byte boundaries).
