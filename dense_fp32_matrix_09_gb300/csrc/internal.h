@@ -297,7 +297,7 @@ struct Int8Copies {
     int8_t *b_dst;
     int b_ld;
     // set by launch_int8_copies
-    int a_vec, b_vec, a_blocks, b_blocks;
+    int a_vec, a_blocks, b_blocks;
 };
 cudaError_t launch_int8_copies(Int8Copies *c, cudaStream_t stream);
 constexpr int kI8TileN = 128, kI8StageK = 128;  // channels and k of one B stage (TMA box, 128-byte swizzle)

@@ -394,6 +394,7 @@ long long realign_blocks(long long rows, int ldd) {
 // threads) fall in 32 distinct banks.
 constexpr int kTK = 128, kTN = 64;
 
+template <bool WORDS>
 __device__ __forceinline__ void transpose(const Int8Copies &c, int block, int blocks) {
     __shared__ uint32_t tile[kTN][kTK / 4 + 1];
     const int tiles_k = (c.b_ld + kTK - 1) / kTK, tiles_n = (c.N + kTN - 1) / kTN;
@@ -404,32 +405,52 @@ __device__ __forceinline__ void transpose(const Int8Copies &c, int block, int bl
         const int n0 = r % tiles_n * kTN, k0 = r / tiles_n * kTK;
         const int8_t *src = c.B + e * c.strideB;
         int8_t *d = c.b_dst + e * c.N * c.b_ld;
+        // All words are asked for before any is used; of a misaligned four bytes the
+        // two words that they lie in, read whole.  What is beyond the row goes to
+        // channels that do not exist; only at the matrix's own ends (rows on word
+        // boundaries: at theirs) the bytes are read one by one.  (Byte by byte at every
+        // row's ends: 40 x 133 x 266 7.9 us instead of 6.2, 1000 x 1500 x 777 15.1
+        // instead of 14.1.)
+        const Bytes all = matrix_of(src, c.K, c.ldb, c.N);
         uint32_t w[2][4];
+        uint32_t next[2][4];
+        bool ends = false;
+        auto each = [&](auto f) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int at = threadIdx.x + h * 256, n4 = at % 8 + at / 256 % 2 * 8, k4 = at / 8 % 32;
-            const int n = n0 + n4 * 4;
+            for (int h = 0; h < 2; ++h) {
+                const int at = threadIdx.x + h * 256, n = n0 + (at % 8 + at / 256 % 2 * 8) * 4, k = k0 + at / 8 % 32 * 4;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = k0 + k4 * 4 + j;
-                uint32_t v = 0;
-                if (k < c.K) {
-                    const int8_t *p = src + static_cast<long long>(k) * c.ldb + n;
-                    if (c.b_vec && n + 4 <= c.N) {
-                        v = __ldcg(reinterpret_cast<const uint32_t *>(p));
-                    } else if (n >= 4 && n + 8 <= c.N) {
-                        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
-                        const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
-                        v = __funnelshift_r(__ldcg(q), __ldcg(q + 1), 8 * off);
-                    } else {
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            if (n + b < c.N) v |= static_cast<uint32_t>(static_cast<uint8_t>(p[b])) << (8 * b);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const int8_t *p = src + static_cast<long long>(k + j) * c.ldb + n;
+                    const uint32_t off = WORDS ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+                    const bool some = k + j < c.K && n < c.N;
+                    const bool whole =
+                        some && (WORDS ? n + 4 <= c.N : p - off >= all.lo && p - off + (off ? 8 : 4) <= all.hi);
+                    f(h, j, n, p, off, some, whole);
                 }
-                w[h][j] = v;
             }
-        }
+        };
+        auto bytes = [&](const int8_t *p, int n) {
+            uint32_t v = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (n + b < c.N) v |= static_cast<uint32_t>(static_cast<uint8_t>(p[b])) << (8 * b);
+            return v;
+        };
+        each([&](int h, int j, int n, const int8_t *p, uint32_t off, bool some, bool whole) {
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
+            w[h][j] = whole ? __ldcg(q) : WORDS && some ? bytes(p, n) : 0u;
+            next[h][j] = !WORDS && whole && off ? __ldcg(q + 1) : 0u;
+            ends |= !WORDS && some && !whole;
+        });
+        if (!WORDS)
+            each([&](int h, int j, int, const int8_t *, uint32_t off, bool, bool) {
+                w[h][j] = __funnelshift_r(w[h][j], next[h][j], 8 * off);
+            });
+        if (ends)
+            each([&](int h, int j, int n, const int8_t *p, uint32_t, bool some, bool whole) {
+                if (some && !whole) w[h][j] = bytes(p, n);
+            });
         __syncthreads();  // the tile before has been read
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -453,13 +474,16 @@ __device__ __forceinline__ void transpose(const Int8Copies &c, int block, int bl
 }
 
 // Both operands' copies in one launch: blocks [0, b_blocks) copy B, the rest A.
-__global__ void __launch_bounds__(256) int8_copies_kernel(const Int8Copies c) {
+// WORDS: B's rows start on word boundaries (fewer registers, five CTAs an SM instead
+// of four: B 8192 x 8192 stored K x N, 16 tokens 48 us instead of 52).
+template <bool WORDS>
+__global__ void __launch_bounds__(256, WORDS ? 5 : 4) int8_copies_kernel(const Int8Copies c) {
     griddep_wait();
     griddep_launch_dependents();
     const int block = static_cast<int>(blockIdx.x);
     if (block < c.b_blocks) {
         if (c.b_trans) realign(c.B, c.ldb, c.strideB, c.experts, c.N, c.K, c.b_dst, c.b_ld, block, c.b_blocks);
-        else transpose(c, block, c.b_blocks);
+        else transpose<WORDS>(c, block, c.b_blocks);
     } else if (c.peaks) {
         rows_to_f16(c, block - c.b_blocks, c.a_blocks, c.peaks + block - c.b_blocks);
     } else {
@@ -474,7 +498,7 @@ __global__ void __launch_bounds__(256) int8_copies_kernel(const Int8Copies c) {
 // step of one or a few tokens is made of the launch and one latency of HBM, and
 // for so few sums dp4a's rate does not show.  One token x 4096 x 4096 4.8 us (on the
 // tensor cores 7.6), x 8192 x 8192 13.7 (15.8; 4.9 TB/s), x 8190 x 8190 20.7 (36, with
-// B's copy); 4 tokens 6.9, 17.9, 30.4; 8 tokens 9.7 or more: choose_few in
+// B's copy); 4 tokens 6.9, 17.9, 30.4; 8 tokens 11.6 or more: choose_few in
 // sgemm_ops_api.cu says which kernel runs.
 constexpr int kFewThreads = 256;
 
@@ -1626,7 +1650,7 @@ cudaError_t launch_int8_generic(const Int8Args &a, cudaStream_t stream) {
 
 cudaError_t launch_int8_copies(Int8Copies *c, cudaStream_t stream) {
     c->a_vec = reinterpret_cast<uintptr_t>(c->A) % 16 == 0 && c->lda % 16 == 0;
-    c->b_vec = reinterpret_cast<uintptr_t>(c->B) % 4 == 0 && c->ldb % 4 == 0 && c->strideB % 4 == 0;
+    const bool words = reinterpret_cast<uintptr_t>(c->B) % 4 == 0 && c->ldb % 4 == 0 && c->strideB % 4 == 0;
     auto capped = [](long long blocks) { return static_cast<int>(blocks < kI8Peaks ? blocks : kI8Peaks); };
     c->a_blocks = !c->a_dst ? 0
                   : c->peaks ? capped((static_cast<long long>(c->a_rows) * (c->a_ld / 16) + 255) / 256)
@@ -1634,7 +1658,8 @@ cudaError_t launch_int8_copies(Int8Copies *c, cudaStream_t stream) {
     if (!c->b_dst) c->b_blocks = 0;
     else if (c->b_trans) c->b_blocks = capped(realign_blocks(static_cast<long long>(c->experts) * c->N, c->b_ld));
     else c->b_blocks = capped(static_cast<long long>(c->experts) * ((c->b_ld + kTK - 1) / kTK) * ((c->N + kTN - 1) / kTN));
-    return launch_dependent(int8_copies_kernel, dim3(c->a_blocks + c->b_blocks), dim3(256), 0, stream, 1, *c);
+    return launch_dependent(words ? int8_copies_kernel<true> : int8_copies_kernel<false>, dim3(c->a_blocks + c->b_blocks),
+                            dim3(256), 0, stream, 1, *c);
 }
 
 }  // namespace sg

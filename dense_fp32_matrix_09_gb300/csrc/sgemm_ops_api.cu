@@ -103,7 +103,7 @@ TileChoice choose_tile(int rows, int experts, int N, int K, int num_sms, bool di
 // kind of model; B's copy, which only they need, counted): a launch, B at the rate
 // that a warp's arithmetic leaves (lower on rows that have to be shifted), and
 // the tokens' way into shared memory.  E.g. one token 4.8 us against 7.6 (4096 x 4096),
-// 4 tokens 17.9 against 15.8 (8192 x 8192) and 4.2 against 6.9 (700 x 700), 8 tokens 9.7
+// 4 tokens 17.9 against 15.8 (8192 x 8192) and 4.2 against 6.9 (700 x 700), 8 tokens 11.6
 // against 7.7 and 5.5 against 6.9.
 bool choose_few(int rows, int N, int K, bool b_aligned, double tc_us) {
     constexpr double kAligned[] = {0.14, 0.17, 0.23, 0.43}, kShifted[] = {0.27, 0.33, 0.41, 0.75};  // us a MB
