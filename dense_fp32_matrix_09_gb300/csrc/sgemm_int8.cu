@@ -255,15 +255,31 @@ __device__ __forceinline__ void int8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t
     hi = *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// Bytes p[k..k+15] of a row of K (zeros from K on): 16 bytes at once where `vec`
-// says that rows start on 16-byte boundaries; otherwise five words and a shift,
-// away from the row's ends (no byte outside the row is read).
-__device__ __forceinline__ uint4 load_int8x16(const int8_t *row, int k, int K, bool vec) {
+// The bytes of a matrix: [lo, hi).  Rows that do not start on 16-byte boundaries
+// are read in aligned pieces that reach over a row's ends, which is what most of
+// the loads below rest on; a piece that reaches over the matrix's own ends is read
+// byte by byte.
+struct Bytes {
+    const int8_t *lo, *hi;
+};
+__device__ __forceinline__ Bytes matrix_of(const int8_t *p, long long rows, long long ld, int K) {
+    return Bytes{p, p + (rows - 1) * ld + K};
+}
+
+// Bytes of v from the `left`-th on made zeros.
+__device__ __forceinline__ uint4 zeros_from(uint4 v, int left) {
+    auto keep = [&](uint32_t w, int n) { return n >= 4 ? w : n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u); };
+    return make_uint4(keep(v.x, left), keep(v.y, left - 4), keep(v.z, left - 8), keep(v.w, left - 12));
+}
+
+// Bytes k..k+15 of a row of K (zeros from K on): 16 bytes at once where `vec` says
+// that rows start on 16-byte boundaries, otherwise five words and a shift.
+__device__ __forceinline__ uint4 load_int8x16(const int8_t *row, int k, int K, bool vec, const Bytes &all) {
     const int8_t *p = row + k;
     if (vec && k + 16 <= K) return __ldcg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
     uint32_t w[5] = {};
-    if (k >= 16 && k + 20 <= K) {
-        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+    if (p - off >= all.lo && p - off + 20 <= all.hi) {
         const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
 #pragma unroll
         for (int i = 0; i < 5; ++i) w[i] = __ldcg(q + i);
@@ -274,7 +290,7 @@ __device__ __forceinline__ uint4 load_int8x16(const int8_t *row, int k, int K, b
         for (int i = 0; i < 16; ++i)
             if (k + i < K) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i % 4));
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return zeros_from(make_uint4(w[0], w[1], w[2], w[3]), K - k);
 }
 
 // Rows on any alignment, a warp at a time: lane l reads the aligned 16 bytes in
@@ -285,12 +301,6 @@ __device__ __forceinline__ uint4 load_int8x16(const int8_t *row, int k, int K, b
 // own ends [lo, hi), where it is put together byte by byte with zeros outside.
 // (Byte by byte at every row's ends, a load waits for them there: one token x 700 x
 // 700 4.1 us instead of 3.5.)
-struct Bytes {
-    const int8_t *lo, *hi;
-};
-__device__ __forceinline__ Bytes matrix_of(const int8_t *p, long long rows, long long ld, int K) {
-    return Bytes{p, p + (rows - 1) * ld + K};
-}
 template <bool ALIGNED>
 __device__ __forceinline__ uint4 load_chunk(const int8_t *row, int k, int K, const Bytes &all) {
     const int off = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u);
@@ -326,6 +336,7 @@ __device__ __forceinline__ uint4 join_next(const uint4 &v, const int8_t *row) {
 __device__ __forceinline__ void rows_to_f16(const Int8Copies &c, int block, int blocks, int *peak) {
     __shared__ int part[8];
     uint4 *dst = static_cast<uint4 *>(c.a_dst);
+    const Bytes all = matrix_of(c.A, c.a_rows, c.lda, c.K);
     const int per_row = c.a_ld / 16;
     const long long total = static_cast<long long>(c.a_rows) * per_row;
     int top = 0;
@@ -335,7 +346,7 @@ __device__ __forceinline__ void rows_to_f16(const Int8Copies &c, int block, int 
         if (i < total) {
             const long long row = div_floor(i, per_row);
             const int k = static_cast<int>(i - row * per_row) * 16;
-            if (k < c.K) v = load_int8x16(c.A + row * c.lda, k, c.K, c.a_vec);
+            if (k < c.K) v = load_int8x16(c.A + row * c.lda, k, c.K, c.a_vec, all);
             uint4 o0, o1;
             int8x4_to_f16(v.x, o0.x, o0.y);
             int8x4_to_f16(v.y, o0.z, o0.w);
@@ -531,7 +542,7 @@ __global__ void __launch_bounds__(kFewThreads, MT <= 4 ? 4 : 2) int8_few_kernel(
     griddep_wait();
     griddep_launch_dependents();
 
-    const Bytes all = matrix_of(a.B, a.N, a.ldb, a.K);
+    const Bytes all = matrix_of(a.B, a.N, a.ldb, a.K), all_a = matrix_of(a.A, a.rows, a.lda, a.K);
     int sum[MT][C] = {};
     uint4 raw[AHEAD][C];
     auto fetch = [&](int s0) {
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(kFewThreads, MT <= 4 ? 4 : 2) int8_few_kernel(
     fetch(0);
     for (int i = threadIdx.x; i < MT * pieces; i += kFewThreads) {
         const int t = i / pieces, k = (i - t * pieces) * 16;
-        rows[i] = t < a.rows ? load_int8x16(a.A + static_cast<long long>(t) * a.lda, k, a.K, a_vec) : make_uint4(0, 0, 0, 0);
+        rows[i] = t < a.rows ? load_int8x16(a.A + static_cast<long long>(t) * a.lda, k, a.K, a_vec, all_a) : make_uint4(0, 0, 0, 0);
     }
     __syncthreads();
     const int mine = (steps - member + split - 1) / split;  // this warp's steps
