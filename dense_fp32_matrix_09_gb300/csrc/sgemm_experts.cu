@@ -80,6 +80,8 @@ struct AccessOf<2> { using T = uint16_t; };
 template <>
 struct AccessOf<4> { using T = uint32_t; };
 template <>
+struct AccessOf<8> { using T = uint2; };
+template <>
 struct AccessOf<16> { using T = uint4; };
 
 template <class T, int TPR, int A>
@@ -120,13 +122,13 @@ constexpr float kSmallestMax = 127.f * 1.17549435e-38f;
 // to even) that sits in the low bits of the sum.
 constexpr float kRoundMagic = 12582912.f;
 
-template <class El, int TPR, int A>
+template <class El, int TPR, int A, int HELD>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int K, int8_t *__restrict__ Q,
                 long long ldq, float *__restrict__ scale, const int *__restrict__ rows, int choices) {
     using T = typename El::T;
     constexpr int kThreads = TPR < 256 ? 256 : TPR;
-    constexpr int kRows = kThreads / TPR, kHeld = 4;
+    constexpr int kRows = kThreads / TPR, kHeld = HELD;  // pieces in registers
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x % TPR;
@@ -212,12 +214,15 @@ cudaError_t quantize_typed(const MoveArgs &a, int num_sms, cudaStream_t stream) 
     int8_t *Q = static_cast<int8_t *>(a.Y);
     // Threads a row: enough that it stays in registers (32 elements a thread),
     // and, with too few rows to fill the GPU, more of them so that each thread
-    // loads less.
+    // loads less.  Rows of at most eight elements a thread take a kernel without the
+    // other three pieces' loads and stores (16 x 4096 BF16 2.1 us in a graph instead
+    // of 2.7, 7900 x 45 3.0 instead of 5.8).
     const bool few = a.tokens <= 4 * num_sms;
     const int per = few ? kV : 4 * kV;
     const int want = (a.width + per - 1) / per;
+    const bool one = want <= 512 && a.width <= kV * (want <= 32 ? 32 : want <= 128 ? 128 : want <= 256 ? 256 : 512);
 #define SG_QUANT(TPR)                                                                                            \
-    return launch_dependent(quantize_kernel<El, TPR, A>,                                                       \
+    return launch_dependent(one ? quantize_kernel<El, TPR, A, 1> : quantize_kernel<El, TPR, A, 4>,             \
                             dim3((a.tokens + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1)),    \
                             dim3(TPR < 256 ? 256 : TPR), 0, stream, 1, X, a.ldx, a.tokens, a.width, Q, a.ldy,    \
                             a.scale, a.rows, a.choices)
@@ -352,38 +357,40 @@ sort_kernel(const int *__restrict__ ids, int slots, int experts, int *__restrict
 
 // ---- rows to the experts --------------------------------------------------------
 // Row t of X to rows[t * choices + j] of Y: read once, written up to `choices`
-// times.  kMoves units (the widest that the rows' alignment allows, up to 16
-// bytes) a thread, all loaded before the first store.
-constexpr int kMoves = 4;
-
+// times.  PER threads a row, four units (the widest that the rows' alignment
+// allows, up to 16 bytes; eight of 2 bytes) each, all loaded before the first store.
 template <class Unit>
+constexpr int kMovesOf = sizeof(Unit) == 2 ? 8 : 4;
+
+template <class Unit, int PER>
 __global__ void __launch_bounds__(256)
 move_kernel(const Unit *__restrict__ X, long long ldx, int tokens, int choices, int width, const int *__restrict__ rows,
             Unit *__restrict__ Y, long long ldy) {
     griddep_wait();
     griddep_launch_dependents();
+    constexpr int kMoves = kMovesOf<Unit>;
     const int slots = tokens * choices;
-    const int c0 = blockIdx.x * (256 * kMoves) + threadIdx.x;
-    for (int t = blockIdx.y; t < tokens; t += gridDim.y) {
+    const int c0 = blockIdx.x * (PER * kMoves) + threadIdx.x % PER;
+    for (int t = blockIdx.y * (256 / PER) + threadIdx.x / PER; t < tokens; t += gridDim.y * (256 / PER)) {
         const Unit *x = X + static_cast<long long>(t) * ldx;
         Unit v[kMoves];
 #pragma unroll
-        for (int m = 0; m < kMoves; ++m) v[m] = c0 + m * 256 < width ? x[c0 + m * 256] : Unit{};
+        for (int m = 0; m < kMoves; ++m) v[m] = c0 + m * PER < width ? __ldcg(x + c0 + m * PER) : Unit{};
         for (int j = 0; j < choices; ++j) {
             const int r = row_of(rows, static_cast<long long>(t) * choices + j, slots);
             if (r < 0) continue;
             Unit *y = Y + static_cast<long long>(r) * ldy;
 #pragma unroll
             for (int m = 0; m < kMoves; ++m)
-                if (c0 + m * 256 < width) y[c0 + m * 256] = v[m];
+                if (c0 + m * PER < width) y[c0 + m * PER] = v[m];
         }
     }
 }
 
 // ---- rows from the experts ------------------------------------------------------
-// out[t] = sum_j w[t,j] * Y[rows[t,j]] (w NULL: the plain sum); four rows' loads
-// in flight at a time.
-template <class El, int A>
+// out[t] = sum_j w[t,j] * Y[rows[t,j]] (w NULL: the plain sum); J rows' loads in
+// flight at a time, TPR threads a token.
+template <class El, int J, int TPR, int A>
 __global__ void __launch_bounds__(256)
 gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, int choices, int width,
               const int *__restrict__ rows, const float *__restrict__ weights, typename El::T *__restrict__ out,
@@ -391,37 +398,37 @@ gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, i
     using T = typename El::T;
     griddep_wait();
     griddep_launch_dependents();
-    const int slots = tokens * choices, c = blockIdx.x, lane = threadIdx.x;
-    for (int t = blockIdx.y; t < tokens; t += gridDim.y) {
+    const int slots = tokens * choices, c = blockIdx.x, lane = threadIdx.x % TPR;
+    for (int t = blockIdx.y * (256 / TPR) + threadIdx.x / TPR; t < tokens; t += gridDim.y * (256 / TPR)) {
         float sum[kV] = {};
-        for (int j0 = 0; j0 < choices; j0 += 4) {
-            Pack8<T> y[4];
-            float w[4];
+        for (int j0 = 0; j0 < choices; j0 += J) {
+            Pack8<T> y[J];
+            float w[J];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < J; ++j) {
                 const long long slot = static_cast<long long>(t) * choices + j0 + j;
                 const int r = j0 + j < choices ? row_of(rows, slot, slots) : -1;
                 w[j] = r >= 0 && weights ? __ldca(weights + slot) : 1.f;
                 // (a row that does not exist has no elements: zeros)
-                y[j] = load8<T, 256, A>(Y + static_cast<long long>(r >= 0 ? r : 0) * ldy, c, lane, r >= 0 ? width : 0);
+                y[j] = load8<T, TPR, A>(Y + static_cast<long long>(r >= 0 ? r : 0) * ldy, c, lane, r >= 0 ? width : 0);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int e = 0; e < kV; ++e) sum[e] = fmaf(w[j], El::up(y[j].v[e]), sum[e]);
         }
         Pack8<T> o;
 #pragma unroll
         for (int e = 0; e < kV; ++e) o.v[e] = El::down(sum[e]);
-        store8<T, 256, A>(out + static_cast<long long>(t) * ldo, c, lane, width, o);
+        store8<T, TPR, A>(out + static_cast<long long>(t) * ldo, c, lane, width, o);
     }
 }
 
 // ---- gradient of the weighted return --------------------------------------------
-// dY[rows[t,j]] = w[t,j] * dO[t] and dw[t,j] = <dO[t], Y[rows[t,j]]>: 256
-// threads a token, J choices at a time; the dot products are reduced in a
-// fixed order (within the warp, then over the warps).
-template <class El, int J, int A>
+// dY[rows[t,j]] = w[t,j] * dO[t] and dw[t,j] = <dO[t], Y[rows[t,j]]>: TPR
+// threads a token (a warp or the block), J choices at a time; the dot products are
+// reduced in a fixed order (within the warp, then over the warps).
+template <class El, int J, int TPR, int A>
 __global__ void __launch_bounds__(256)
 combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const typename El::T *__restrict__ Y,
                     long long ldy, int tokens, int choices, int width, const int *__restrict__ rows,
@@ -431,8 +438,8 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
     __shared__ float part[8][J];
     griddep_wait();
     griddep_launch_dependents();
-    const int slots = tokens * choices, lane = threadIdx.x;
-    for (int t = blockIdx.x; t < tokens; t += gridDim.x) {
+    const int slots = tokens * choices, lane = threadIdx.x % TPR;
+    for (int t = blockIdx.x * (256 / TPR) + threadIdx.x / TPR; t < tokens; t += gridDim.x * (256 / TPR)) {
         const T *g = dO + static_cast<long long>(t) * lddo;
         for (int j0 = 0; j0 < choices; j0 += J) {
             int r[J];
@@ -444,12 +451,12 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
                 w[j] = r[j] >= 0 ? __ldca(weights + slot) : 0.f;
                 dot[j] = 0.f;
             }
-            for (int c = 0; c * 256 * kV < width; ++c) {
-                const Pack8<T> gv = load8<T, 256, A>(g, c, lane, width);
+            for (int c = 0; c * TPR * kV < width; ++c) {
+                const Pack8<T> gv = load8<T, TPR, A>(g, c, lane, width);
                 Pack8<T> y[J];
 #pragma unroll
                 for (int j = 0; j < J; ++j)
-                    y[j] = load8<T, 256, A>(Y + static_cast<long long>(r[j] >= 0 ? r[j] : 0) * ldy, c, lane,
+                    y[j] = load8<T, TPR, A>(Y + static_cast<long long>(r[j] >= 0 ? r[j] : 0) * ldy, c, lane,
                                               r[j] >= 0 ? width : 0);
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
@@ -460,7 +467,7 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
                         dot[j] = fmaf(d, El::up(y[j].v[e]), dot[j]);
                         o.v[e] = El::down(w[j] * d);
                     }
-                    if (r[j] >= 0) store8<T, 256, A>(dY + static_cast<long long>(r[j]) * lddy, c, lane, width, o);
+                    if (r[j] >= 0) store8<T, TPR, A>(dY + static_cast<long long>(r[j]) * lddy, c, lane, width, o);
                 }
             }
 #pragma unroll
@@ -468,8 +475,10 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
                 if (r[j] < 0) dot[j] = 0.f;  // not 0 * dO, which a non-finite dO makes NaN
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
-                if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = dot[j];
+                if (TPR > 32 && (threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = dot[j];
+                if (TPR == 32 && lane == 0 && j0 + j < choices) dw[static_cast<long long>(t) * choices + j0 + j] = dot[j];
             }
+            if (TPR == 32) continue;
             __syncthreads();
             if (threadIdx.x < J && j0 + threadIdx.x < choices) {
                 float sum = 0.f;
@@ -490,43 +499,70 @@ int common_alignment(Rows... rows) {
     return static_cast<int>(all & (~all + 1));
 }
 
-// Call f with the elements of an access (an integral constant): 16 bytes, 4 bytes
-// or one element.
+// Call f with the elements of an access (an integral constant): 16, 8 or 4 bytes or
+// one element.
 template <int SIZE, class F>
 cudaError_t with_access(int alignment, F &&f) {
     if (alignment >= 16) return f(std::integral_constant<int, 16 / SIZE>{});
+    if (alignment >= 8) return f(std::integral_constant<int, 8 / SIZE>{});
     if (SIZE < 4 && alignment >= 4) return f(std::integral_constant<int, SIZE < 4 ? 4 / SIZE : 1>{});
     return f(std::integral_constant<int, 1>{});
 }
 
 constexpr int kMaxGridY = 65535;
 
-template <class El>
-cudaError_t gather_typed(const MoveArgs &a, cudaStream_t stream) {
+template <class El, int J, int TPR>
+cudaError_t gather_tpr(const MoveArgs &a, cudaStream_t stream) {
     using T = typename El::T;
     constexpr int kSize = sizeof(T);
     const int al = common_alignment(reinterpret_cast<uintptr_t>(a.X), reinterpret_cast<uintptr_t>(a.Y), a.ldx * kSize,
                                     a.ldy * kSize, static_cast<long long>(a.width) * kSize);
-    const dim3 grid((a.width + 256 * kV - 1) / (256 * kV), a.tokens < kMaxGridY ? a.tokens : kMaxGridY);
+    const int blocks = (a.tokens + 256 / TPR - 1) / (256 / TPR);
+    const dim3 grid((a.width + TPR * kV - 1) / (TPR * kV), blocks < kMaxGridY ? blocks : kMaxGridY);
     return with_access<kSize>(al, [&](auto n) {
-        return launch_dependent(gather_kernel<El, decltype(n)::value>, grid, dim3(256), 0, stream, 1,
+        return launch_dependent(gather_kernel<El, J, TPR, decltype(n)::value>, grid, dim3(256), 0, stream, 1,
                                 static_cast<const T *>(a.Y), a.ldy, a.tokens, a.choices, a.width, a.rows, a.weights,
                                 static_cast<T *>(const_cast<void *>(a.X)), a.ldx);
     });
 }
 
+// A warp a token (and 256 elements) where a row does not give a block's threads eight
+// elements each: 3000 tokens, 4 choices, 512 elements of 16 bits 3.4 us against 6.4,
+// 1024 6.2 against 7.8; 4096 elements, 8192 tokens 56.1 against 54.9.
 template <class El, int J>
-cudaError_t combine_grad_j(const MoveArgs &a, cudaStream_t stream) {
+cudaError_t gather_j(const MoveArgs &a, cudaStream_t stream) {
+    return a.width < 256 * kV ? gather_tpr<El, J, 32>(a, stream) : gather_tpr<El, J, 256>(a, stream);
+}
+
+template <class El>
+cudaError_t gather_typed(const MoveArgs &a, cudaStream_t stream) {
+    if (a.choices == 1) return gather_j<El, 1>(a, stream);
+    if (a.choices == 2) return gather_j<El, 2>(a, stream);
+    return gather_j<El, 4>(a, stream);
+}
+
+template <class El, int J, int TPR>
+cudaError_t combine_grad_tpr(const MoveArgs &a, cudaStream_t stream) {
     using T = typename El::T;
     constexpr int kSize = sizeof(T);
     const int al = common_alignment(reinterpret_cast<uintptr_t>(a.X), reinterpret_cast<uintptr_t>(a.Y),
                                     reinterpret_cast<uintptr_t>(a.dY), a.ldx * kSize, a.ldy * kSize, a.lddy * kSize,
                                     static_cast<long long>(a.width) * kSize);
     return with_access<kSize>(al, [&](auto n) {
-        return launch_dependent(combine_grad_kernel<El, J, decltype(n)::value>, dim3(a.tokens), dim3(256), 0, stream, 1,
+        return launch_dependent(combine_grad_kernel<El, J, TPR, decltype(n)::value>,
+                                dim3((a.tokens + 256 / TPR - 1) / (256 / TPR)), dim3(256), 0, stream, 1,
                                 static_cast<const T *>(a.X), a.ldx, static_cast<const T *>(a.Y), a.ldy, a.tokens,
                                 a.choices, a.width, a.rows, a.weights, static_cast<T *>(a.dY), a.lddy, a.scale);
     });
+}
+
+// A warp a token under the same condition, if there are tokens enough that their
+// warps fill the GPU: with the forward 3000 tokens, 4 choices, 512 elements of 16 bits
+// 8.9 us against 17.4, 2048 28.2 either way, 8192 tokens of 4096 152.6 against 143.2;
+// 30 tokens of 1024 5.5 against 3.8.
+template <class El, int J>
+cudaError_t combine_grad_j(const MoveArgs &a, cudaStream_t stream) {
+    return a.width < 256 * kV && a.tokens >= a.width / 2 ? combine_grad_tpr<El, J, 32>(a, stream) : combine_grad_tpr<El, J, 256>(a, stream);
 }
 
 template <class El>
@@ -536,13 +572,22 @@ cudaError_t combine_grad_typed(const MoveArgs &a, cudaStream_t stream) {
     return combine_grad_j<El, 4>(a, stream);
 }
 
+template <class Unit, int PER>
+cudaError_t move_per(const MoveArgs &a, int size, int width, cudaStream_t stream) {
+    constexpr int kUnits = PER * kMovesOf<Unit>;
+    const int blocks = (a.tokens + 256 / PER - 1) / (256 / PER);
+    const dim3 grid((width + kUnits - 1) / kUnits, blocks < kMaxGridY ? blocks : kMaxGridY);
+    return launch_dependent(move_kernel<Unit, PER>, grid, dim3(256), 0, stream, 1, static_cast<const Unit *>(a.X),
+                            a.ldx * size / static_cast<int>(sizeof(Unit)), a.tokens, a.choices, width, a.rows,
+                            static_cast<Unit *>(a.Y), a.ldy * size / static_cast<int>(sizeof(Unit)));
+}
+
+// A warp a row where that leaves no thread of it more than its units, else the block.
 template <class Unit>
 cudaError_t move_units(const MoveArgs &a, int size, cudaStream_t stream) {
     const int width = static_cast<int>(static_cast<long long>(a.width) * size / static_cast<int>(sizeof(Unit)));
-    const dim3 grid((width + 256 * kMoves - 1) / (256 * kMoves), a.tokens < kMaxGridY ? a.tokens : kMaxGridY);
-    return launch_dependent(move_kernel<Unit>, grid, dim3(256), 0, stream, 1, static_cast<const Unit *>(a.X),
-                            a.ldx * size / static_cast<int>(sizeof(Unit)), a.tokens, a.choices, width, a.rows,
-                            static_cast<Unit *>(a.Y), a.ldy * size / static_cast<int>(sizeof(Unit)));
+    return width <= 32 * kMovesOf<Unit> ? move_per<Unit, 32>(a, size, width, stream)
+                                          : move_per<Unit, 256>(a, size, width, stream);
 }
 
 }  // namespace
