@@ -23,9 +23,12 @@
 //    experts, back, and the gradients; each reads and writes every row once
 //    (16 bytes a thread and step where alignment allows), sums in FP32 in
 //    ascending choice order and rounds once.  8192 tokens, 4 choices, 4096 elements
-//    of 16 bits: 51.6 us out (6.5 TB/s), 54.7 back (6.1), the weighted gradient 89.9
-//    (6.7); rows of an odd number of 16-bit elements, which take 2-byte accesses,
-//    run at half of that (2475 elements: 43, 59 and 90 us).
+//    of 16 bits: 51.6 us out (6.5 TB/s), 54.6 back (6.1), the weighted gradient 88
+//    (6.8).  Rows of an odd number of 16-bit elements take 2-byte accesses and up to
+//    twice as long a byte (2475 elements: 45, 60 and 89 us).  Put together instead from
+//    aligned 16-byte pieces of their rows by shuffles, with the stores on 16-byte
+//    boundaries, they took still longer (5453 rows of 3515 59 us instead of 23): the
+//    shifts' instructions then bound them.
 // No load is a read-only-cache load (ld.global.nc): what is read may have been
 // written by the kernel before, whose end the launch overlaps.  Rows, read once, go
 // past L1 (ld.global.cg); row numbers and weights, which a block's warps share, do
@@ -122,8 +125,14 @@ constexpr float kSmallestMax = 127.f * 1.17549435e-38f;
 // to even) that sits in the low bits of the sum.
 constexpr float kRoundMagic = 12582912.f;
 
+// 256-thread CTAs that an SM has to hold: five of four 16-bit pieces a thread (8192 x
+// 4096 17.7 us, four 18.7), four of 32-bit ones (25.4; five 32.2, the pieces no longer
+// fit the registers).
+template <class T>
+constexpr int quantize_ctas(int held) { return held == 1 ? 6 : sizeof(T) == 2 ? 5 : 4; }
+
 template <class El, int TPR, int A, int HELD>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR < 512 ? quantize_ctas<typename El::T>(HELD) : HELD == 1 ? 3 : 2)
 quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int K, int8_t *__restrict__ Q,
                 long long ldq, float *__restrict__ scale, const int *__restrict__ rows, int choices) {
     using T = typename El::T;
@@ -220,15 +229,17 @@ cudaError_t quantize_typed(const MoveArgs &a, int num_sms, cudaStream_t stream) 
     const bool few = a.tokens <= 4 * num_sms;
     const int per = few ? kV : 4 * kV;
     const int want = (a.width + per - 1) / per;
-    const bool one = want <= 512 && a.width <= kV * (want <= 32 ? 32 : want <= 128 ? 128 : want <= 256 ? 256 : 512);
+    const int share = want <= 32 ? 32 : want <= 64 ? 64 : want <= 128 ? 128 : want <= 256 ? 256 : 512;
+    const bool one = a.width <= kV * share;
 #define SG_QUANT(TPR)                                                                                            \
     return launch_dependent(one ? quantize_kernel<El, TPR, A, 1> : quantize_kernel<El, TPR, A, 4>,             \
                             dim3((a.tokens + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1)),    \
                             dim3(TPR < 256 ? 256 : TPR), 0, stream, 1, X, a.ldx, a.tokens, a.width, Q, a.ldy,    \
                             a.scale, a.rows, a.choices)
-    if (want <= 32) SG_QUANT(32);
-    if (want <= 128) SG_QUANT(128);
-    if (want <= 256) SG_QUANT(256);
+    if (share == 32) SG_QUANT(32);
+    if (share == 64) SG_QUANT(64);
+    if (share == 128) SG_QUANT(128);
+    if (share == 256) SG_QUANT(256);
     SG_QUANT(512);
 #undef SG_QUANT
 }
