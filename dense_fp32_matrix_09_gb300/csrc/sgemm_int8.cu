@@ -169,6 +169,33 @@ __device__ __forceinline__ int bound_of(const Int8Args &a, int e) {
     return min(max(__ldcg(a.offsets + e), 0), a.total_rows);
 }
 
+// ---- loads on any alignment -----------------------------------------------------
+// The bytes of a matrix: [lo, hi).  Rows that do not start on 16-byte boundaries
+// are read in aligned pieces that reach over a row's ends, which is what most of
+// the loads below rest on; a piece that reaches over the matrix's own ends is read
+// byte by byte.
+struct Bytes {
+    const int8_t *lo, *hi;
+};
+__device__ __forceinline__ Bytes matrix_of(const int8_t *p, long long rows, long long ld, int K) {
+    return Bytes{p, p + (rows - 1) * ld + K};
+}
+
+// Four bytes on any alignment.
+__device__ __forceinline__ uint32_t load_word(const int8_t *p, const Bytes &all) {
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+    const int8_t *q = p - off;
+    if (q >= all.lo && q + (off ? 8 : 4) <= all.hi) {
+        const uint32_t w0 = __ldcg(reinterpret_cast<const uint32_t *>(q));
+        const uint32_t w1 = off ? __ldcg(reinterpret_cast<const uint32_t *>(q) + 1) : 0u;
+        return __funnelshift_r(w0, w1, 8 * off);
+    }
+    uint32_t w = 0;
+    for (int i = 0; i < 4; ++i)
+        if (p + i < all.hi) w |= static_cast<uint32_t>(static_cast<uint8_t>(__ldcg(p + i))) << (8 * i);
+    return w;
+}
+
 // ---- generic kernel -----------------------------------------------------------
 // 64 x 64 tile of C, 64 k a step as 16 packed words a row, 4 x 4 sums a thread.
 constexpr int kGTile = 64, kGWords = 16;
@@ -179,8 +206,10 @@ __global__ void __launch_bounds__(256) int8_generic_kernel(const Int8Args a) {
     griddep_launch_dependents();
     const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
     const int n0 = blockIdx.x * kGTile;
+    const Bytes all_a = matrix_of(a.A, a.total_rows, a.lda, a.K);
     for (int e = blockIdx.z; e < a.experts; e += gridDim.z) {
         const int8_t *B = a.B + e * a.strideB;
+        const Bytes all_b = a.transB ? matrix_of(B, a.N, a.ldb, a.K) : matrix_of(B, a.K, a.ldb, a.N);
         const int lo = max(bound_of(a, e), a.row0), hi = min(bound_of(a, e + 1), a.row0 + a.rows);
         for (int m0 = lo + static_cast<int>(blockIdx.y) * kGTile; m0 < hi; m0 += static_cast<int>(gridDim.y) * kGTile) {
             int acc[4][4] = {};
@@ -188,17 +217,23 @@ __global__ void __launch_bounds__(256) int8_generic_kernel(const Int8Args a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int at = tid + r * 256, w = at % kGWords, i = at / kGWords;
+                    // (A's bytes from K on are zeros, so that B's may be any)
                     unsigned av = 0, bv = 0;
+                    const int k = k0 + 4 * w;
+                    if (k < a.K && m0 + i < hi) {
+                        av = load_word(a.A + static_cast<long long>(m0 + i) * a.lda + k, all_a);
+                        if (a.K - k < 4) av &= (1u << (8 * (a.K - k))) - 1u;
+                    }
+                    if (k < a.K && n0 + i < a.N) {
+                        if (a.transB) {
+                            bv = load_word(B + static_cast<long long>(n0 + i) * a.ldb + k, all_b);
+                        } else {
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int k = k0 + 4 * w + b;
-                        if (k >= a.K) break;
-                        if (m0 + i < hi)
-                            av |= static_cast<unsigned>(static_cast<uint8_t>(a.A[static_cast<long long>(m0 + i) * a.lda + k])) << (8 * b);
-                        if (n0 + i < a.N)
-                            bv |= static_cast<unsigned>(static_cast<uint8_t>(
-                                      a.transB ? B[static_cast<long long>(n0 + i) * a.ldb + k]
-                                               : B[static_cast<long long>(k) * a.ldb + n0 + i])) << (8 * b);
+                            for (int b = 0; b < 4; ++b)
+                                if (k + b < a.K)
+                                    bv |= static_cast<unsigned>(static_cast<uint8_t>(__ldcg(B + static_cast<long long>(k + b) * a.ldb + n0 + i)))
+                                          << (8 * b);
+                        }
                     }
                     As[w][i] = static_cast<int>(av);
                     Bs[w][i] = static_cast<int>(bv);
@@ -255,17 +290,6 @@ __device__ __forceinline__ void int8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t
     hi = *reinterpret_cast<const uint32_t *>(&b);
 }
 
-// The bytes of a matrix: [lo, hi).  Rows that do not start on 16-byte boundaries
-// are read in aligned pieces that reach over a row's ends, which is what most of
-// the loads below rest on; a piece that reaches over the matrix's own ends is read
-// byte by byte.
-struct Bytes {
-    const int8_t *lo, *hi;
-};
-__device__ __forceinline__ Bytes matrix_of(const int8_t *p, long long rows, long long ld, int K) {
-    return Bytes{p, p + (rows - 1) * ld + K};
-}
-
 // Bytes of v from the `left`-th on made zeros.
 __device__ __forceinline__ uint4 zeros_from(uint4 v, int left) {
     auto keep = [&](uint32_t w, int n) { return n >= 4 ? w : n <= 0 ? 0u : w & ((1u << (8 * n)) - 1u); };
@@ -288,7 +312,7 @@ __device__ __forceinline__ uint4 load_int8x16(const int8_t *row, int k, int K, b
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (k + i < K) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i % 4));
+            if (k + i < K) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldcg(p + i))) << (8 * (i % 4));
     }
     return zeros_from(make_uint4(w[0], w[1], w[2], w[3]), K - k);
 }
@@ -298,7 +322,8 @@ __device__ __forceinline__ uint4 load_int8x16(const int8_t *row, int k, int K, b
 // takes their end from lane l + 1, which reads the next ones; so 31 lanes get 16
 // bytes each.  A chunk that a row's first or last byte is in is read whole (bytes
 // between the matrix's rows with it, of whatever value), except at the matrix's
-// own ends [lo, hi), where it is put together byte by byte with zeros outside.
+// own ends [lo, hi), where it is put together from words, the one that an end is in
+// byte by byte, with zeros outside.
 // (Byte by byte at every row's ends, a load waits for them there: one token x 700 x
 // 700 4.1 us instead of 3.5.)
 template <bool ALIGNED>
@@ -308,10 +333,16 @@ __device__ __forceinline__ uint4 load_chunk(const int8_t *row, int k, int K, con
     if (first >= K) return make_uint4(0, 0, 0, 0);
     const int8_t *p = row + first;
     if (p >= all.lo && p + 16 <= all.hi) return __ldcg(reinterpret_cast<const uint4 *>(p));
-    uint32_t w[4] = {};
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (p + i >= all.lo && p + i < all.hi) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * (i % 4));
+    for (int i = 0; i < 4; ++i) {
+        const int8_t *q = p + 4 * i;
+        const bool whole = q >= all.lo && q + 4 <= all.hi;
+        w[i] = whole ? __ldcg(reinterpret_cast<const uint32_t *>(q)) : 0u;
+        if (!whole && q + 4 > all.lo && q < all.hi)  // a word that an end is in
+            for (int b = 0; b < 4; ++b)
+                if (q + b >= all.lo && q + b < all.hi) w[i] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldcg(q + b))) << (8 * b);
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // The 16 bytes that begin in this lane's chunk (lane 31: not its own).
@@ -420,7 +451,7 @@ __device__ __forceinline__ void transpose(const Int8Copies &c, int block, int bl
         // two words that they lie in, read whole.  What is beyond the row goes to
         // channels that do not exist; only at the matrix's own ends (rows on word
         // boundaries: at theirs) the bytes are read one by one.  (Byte by byte at every
-        // row's ends: 40 x 133 x 266 7.9 us instead of 6.2, 1000 x 1500 x 777 15.1
+        // row's ends: 40 x 133 x 266 7.9 us instead of 6.5, 1000 x 1500 x 777 15.1
         // instead of 14.1.)
         const Bytes all = matrix_of(src, c.K, c.ldb, c.N);
         uint32_t w[2][4];
@@ -445,7 +476,7 @@ __device__ __forceinline__ void transpose(const Int8Copies &c, int block, int bl
             uint32_t v = 0;
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-                if (n + b < c.N) v |= static_cast<uint32_t>(static_cast<uint8_t>(p[b])) << (8 * b);
+                if (n + b < c.N) v |= static_cast<uint32_t>(static_cast<uint8_t>(__ldcg(p + b))) << (8 * b);
             return v;
         };
         each([&](int h, int j, int n, const int8_t *p, uint32_t off, bool some, bool whole) {
