@@ -200,6 +200,23 @@ __device__ __forceinline__ uint32_t load_word(const int8_t *p, const Bytes &all)
 // 64 x 64 tile of C, 64 k a step as 16 packed words a row, 4 x 4 sums a thread.
 constexpr int kGTile = 64, kGWords = 16;
 
+// The largest of offsets[0 .. e], kept within the rows there are: expert e's first
+// row where the array is out of order too (its last row: that of e + 1).  The whole
+// block takes part.
+__device__ __forceinline__ int highest_bound(const Int8Args &a, int e) {
+    if (!a.offsets) return bound_of(a, e);
+    __shared__ int part[8];
+    int top = 0;
+    for (int i = threadIdx.x; i <= e; i += 256) top = max(top, bound_of(a, i));
+    top = __reduce_max_sync(0xffffffffu, top);
+    __syncthreads();  // the call before has been read
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = max(top, part[w]);
+    return top;
+}
+
 __global__ void __launch_bounds__(256) int8_generic_kernel(const Int8Args a) {
     __shared__ int As[kGWords][kGTile + 1], Bs[kGWords][kGTile + 1];
     griddep_wait();
@@ -210,7 +227,8 @@ __global__ void __launch_bounds__(256) int8_generic_kernel(const Int8Args a) {
     for (int e = blockIdx.z; e < a.experts; e += gridDim.z) {
         const int8_t *B = a.B + e * a.strideB;
         const Bytes all_b = a.transB ? matrix_of(B, a.N, a.ldb, a.K) : matrix_of(B, a.K, a.ldb, a.N);
-        const int lo = max(bound_of(a, e), a.row0), hi = min(bound_of(a, e + 1), a.row0 + a.rows);
+        const int first = highest_bound(a, e), last = max(first, bound_of(a, e + 1));
+        const int lo = max(first, a.row0), hi = min(last, a.row0 + a.rows);
         for (int m0 = lo + static_cast<int>(blockIdx.y) * kGTile; m0 < hi; m0 += static_cast<int>(gridDim.y) * kGTile) {
             int acc[4][4] = {};
             for (int k0 = 0; k0 < a.K; k0 += 4 * kGWords) {
