@@ -9,6 +9,7 @@ call raises -- there is no fallback of any kind.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -550,6 +551,25 @@ def _slots(rows, tokens=None) -> tuple[int, int]:
     return rows.shape[0], rows.shape[1]
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream, *tensors):
+    """The context in which a tensor method makes its results and enqueues its
+    kernels: on `stream` everything, so that the results' memory and what fills it
+    are in order with the kernels.  The memory of `tensors` (what the method reads or
+    is given to write) is kept from reuse until `stream` is done with it."""
+    if stream is None:
+        return _HERE
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
 def _result(out, M, N, out_dtype, device):
     import torch
     if out is None:
@@ -585,16 +605,20 @@ class Sgemm:
         return C
 
     # -- 8-bit products and expert routing on torch tensors: shapes and types are
-    #    checked here, results are new tensors on the inputs' device --------------
+    #    checked here, results are new tensors on the inputs' device.  They are made
+    #    on `stream` (None: the current one) like torch's own under
+    #    torch.cuda.stream(stream): the inputs have to be ready there, and another
+    #    stream that uses the results has to wait for it ----------------------------
     def quantize(self, X, stream=None):
         """(Q, scale): the rows of X (2-D, FP32/BF16/FP16) in int8 and their FP32 scales."""
         import torch
         kind = _element_type(X)
         _rows_of("X", X)
         M, K = X.shape
-        Q = torch.empty(M, K, dtype=torch.int8, device=X.device)
-        scale = torch.empty(M, dtype=torch.float32, device=X.device)
-        sgemm_quantize_rows(self.h, kind, M, K, X, _ld(X), Q, max(K, 1), scale, stream)
+        with _on(stream, X):
+            Q = torch.empty(M, K, dtype=torch.int8, device=X.device)
+            scale = torch.empty(M, dtype=torch.float32, device=X.device)
+            sgemm_quantize_rows(self.h, kind, M, K, X, _ld(X), Q, max(K, 1), scale)
         return Q, scale
 
     def matmul_int8(self, A, scaleA, B, scaleB, bias=None, out_dtype=None, out=None, stream=None):
@@ -610,9 +634,10 @@ class Sgemm:
         _vector("scaleB", scaleB, N)
         if bias is not None:
             _vector("bias", bias, N)
-        out = _result(out, M, N, out_dtype, A.device)
-        sgemm_run_int8(self.h, 1, _element_type(out), M, N, K, A, _ld(A), scaleA, B, _ld(B), scaleB, bias, out, _ld(out),
-                       stream)
+        with _on(stream, A, scaleA, B, scaleB, bias, out):
+            out = _result(out, M, N, out_dtype, A.device)
+            sgemm_run_int8(self.h, 1, _element_type(out), M, N, K, A, _ld(A), scaleA, B, _ld(B), scaleB, bias, out,
+                           _ld(out))
         return out
 
     def matmul_int8_experts(self, offsets, A, scaleA, B, scaleB, bias=None, out_dtype=None, out=None, stream=None):
@@ -629,11 +654,12 @@ class Sgemm:
         for name, t in (("scaleB", scaleB), ("bias", bias)):
             if t is not None and (tuple(t.shape) != (E, N) or t.dtype != torch.float32 or not t.is_contiguous()):
                 raise ValueError(f"{name} must be a contiguous {E} x {N} FP32 tensor")
-        if out is None:
-            out = torch.zeros(R, N, dtype=out_dtype or torch.bfloat16, device=A.device)
-        out = _result(out, R, N, out_dtype, A.device)
-        sgemm_run_int8_experts(self.h, 1, _element_type(out), E, R, N, K, offsets, A, _ld(A), scaleA, B, max(K, 1),
-                               N * K, scaleB, bias, out, _ld(out), stream)
+        with _on(stream, offsets, A, scaleA, B, scaleB, bias, out):
+            if out is None:
+                out = torch.zeros(R, N, dtype=out_dtype or torch.bfloat16, device=A.device)
+            out = _result(out, R, N, out_dtype, A.device)
+            sgemm_run_int8_experts(self.h, 1, _element_type(out), E, R, N, K, offsets, A, _ld(A), scaleA, B, max(K, 1),
+                                   N * K, scaleB, bias, out, _ld(out))
         return out
 
     def expert_sort(self, ids, experts, stream=None):
@@ -642,10 +668,11 @@ class Sgemm:
         if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
             raise ValueError("ids must be a contiguous tokens x choices int32 tensor")
         tokens, choices = ids.shape
-        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
-        rows = torch.empty(tokens, choices, dtype=torch.int32, device=ids.device)
-        source = torch.empty(tokens * choices, dtype=torch.int32, device=ids.device)
-        sgemm_expert_sort(self.h, tokens, choices, experts, ids, offsets, rows, source, stream)
+        with _on(stream, ids):
+            offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+            rows = torch.empty(tokens, choices, dtype=torch.int32, device=ids.device)
+            source = torch.empty(tokens * choices, dtype=torch.int32, device=ids.device)
+            sgemm_expert_sort(self.h, tokens, choices, experts, ids, offsets, rows, source)
         return offsets, rows, source
 
     def expert_dispatch(self, X, rows, stream=None):
@@ -653,8 +680,9 @@ class Sgemm:
         import torch
         _rows_of("X", X)
         tokens, choices = _slots(rows, X.shape[0])
-        Y = torch.zeros(tokens * choices, X.shape[1], dtype=X.dtype, device=X.device)
-        sgemm_expert_dispatch(self.h, _element_type(X), tokens, choices, X.shape[1], X, _ld(X), rows, Y, _ld(Y), stream)
+        with _on(stream, X, rows):
+            Y = torch.zeros(tokens * choices, X.shape[1], dtype=X.dtype, device=X.device)
+            sgemm_expert_dispatch(self.h, _element_type(X), tokens, choices, X.shape[1], X, _ld(X), rows, Y, _ld(Y))
         return Y
 
     def expert_dispatch_int8(self, X, rows, stream=None):
@@ -662,10 +690,11 @@ class Sgemm:
         import torch
         _rows_of("X", X)
         tokens, choices = _slots(rows, X.shape[0])
-        Q = torch.zeros(tokens * choices, X.shape[1], dtype=torch.int8, device=X.device)
-        scale = torch.zeros(tokens * choices, dtype=torch.float32, device=X.device)
-        sgemm_expert_dispatch_int8(self.h, _element_type(X), tokens, choices, X.shape[1], X, _ld(X), rows, Q, _ld(Q),
-                                   scale, stream)
+        with _on(stream, X, rows):
+            Q = torch.zeros(tokens * choices, X.shape[1], dtype=torch.int8, device=X.device)
+            scale = torch.zeros(tokens * choices, dtype=torch.float32, device=X.device)
+            sgemm_expert_dispatch_int8(self.h, _element_type(X), tokens, choices, X.shape[1], X, _ld(X), rows, Q,
+                                       _ld(Q), scale)
         return Q, scale
 
     def expert_dispatch_grad(self, dY, rows, stream=None):
@@ -675,9 +704,10 @@ class Sgemm:
         _rows_of("dY", dY)
         if dY.shape[0] != tokens * choices:
             raise ValueError(f"dY must have {tokens * choices} rows, got {dY.shape[0]}")
-        dX = torch.empty(tokens, dY.shape[1], dtype=dY.dtype, device=dY.device)
-        sgemm_expert_dispatch_grad(self.h, _element_type(dY), tokens, choices, dY.shape[1], dY, _ld(dY), rows, dX, _ld(dX),
-                                   stream)
+        with _on(stream, dY, rows):
+            dX = torch.empty(tokens, dY.shape[1], dtype=dY.dtype, device=dY.device)
+            sgemm_expert_dispatch_grad(self.h, _element_type(dY), tokens, choices, dY.shape[1], dY, _ld(dY), rows, dX,
+                                       _ld(dX))
         return dX
 
     def expert_combine(self, Y, rows, weights, stream=None):
@@ -688,9 +718,10 @@ class Sgemm:
         _weights(weights, tokens, choices)
         if Y.shape[0] != tokens * choices:
             raise ValueError(f"Y must have {tokens * choices} rows, got {Y.shape[0]}")
-        out = torch.empty(tokens, Y.shape[1], dtype=Y.dtype, device=Y.device)
-        sgemm_expert_combine(self.h, _element_type(Y), tokens, choices, Y.shape[1], Y, _ld(Y), rows, weights, out, _ld(out),
-                             stream)
+        with _on(stream, Y, rows, weights):
+            out = torch.empty(tokens, Y.shape[1], dtype=Y.dtype, device=Y.device)
+            sgemm_expert_combine(self.h, _element_type(Y), tokens, choices, Y.shape[1], Y, _ld(Y), rows, weights, out,
+                                 _ld(out))
         return out
 
     def expert_combine_grad(self, dout, Y, rows, weights, stream=None):
@@ -702,10 +733,11 @@ class Sgemm:
         _weights(weights, tokens, choices)
         if tuple(Y.shape) != (tokens * choices, dout.shape[1]):
             raise ValueError(f"Y must be {tokens * choices} x {dout.shape[1]}, got {tuple(Y.shape)}")
-        dY = torch.zeros_like(Y, memory_format=torch.contiguous_format)
-        dweights = torch.empty(tokens, choices, dtype=torch.float32, device=Y.device)
-        sgemm_expert_combine_grad(self.h, _element_type(Y), tokens, choices, Y.shape[1], dout, _ld(dout), Y, _ld(Y), rows,
-                                  weights, dY, _ld(dY), dweights, stream)
+        with _on(stream, dout, Y, rows, weights):
+            dY = torch.zeros_like(Y, memory_format=torch.contiguous_format)
+            dweights = torch.empty(tokens, choices, dtype=torch.float32, device=Y.device)
+            sgemm_expert_combine_grad(self.h, _element_type(Y), tokens, choices, Y.shape[1], dout, _ld(dout), Y, _ld(Y),
+                                      rows, weights, dY, _ld(dY), dweights)
         return dY, dweights
 
     @property
