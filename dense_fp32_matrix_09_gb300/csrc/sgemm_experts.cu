@@ -109,6 +109,9 @@ __device__ __forceinline__ void store8(T *row, int c, int lane, int width, const
         if (at + i * TPR * A < width) p[i * TPR] = s[i];
 }
 
+// (Tokens, rows and choices are counted in unsigned integers where a step may go past
+// the last one: there may be 2^31 - 1 of them.)
+
 // Sorted row of a slot, or -1 for one that has none: a value outside [0, slots)
 // is no row, whatever wrote it.
 __device__ __forceinline__ int row_of(const int *rows, long long slot, int slots) {
@@ -141,8 +144,8 @@ quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int 
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x % TPR;
-    const int i = blockIdx.x * kRows + threadIdx.x / TPR;
-    const bool live = i < M;
+    const unsigned i = blockIdx.x * kRows + threadIdx.x / TPR;
+    const bool live = i < static_cast<unsigned>(M);
     const T *x = X + static_cast<long long>(live ? i : 0) * ldx;
     const int width = live ? K : 0;
 
@@ -206,7 +209,7 @@ quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int 
 #pragma unroll
     for (int c = 0; c < kHeld; ++c) packed[c] = quantized(held[c]);
     for (int j = 0; j < choices; ++j) {
-        const int r = rows ? row_of(rows, static_cast<long long>(i) * choices + j, M * choices) : i;
+        const int r = rows ? row_of(rows, static_cast<long long>(i) * choices + j, M * choices) : static_cast<int>(i);
         if (r < 0) continue;
         int8_t *q = Q + static_cast<long long>(r) * ldq;
 #pragma unroll
@@ -215,6 +218,9 @@ quantize_kernel(const typename El::T *__restrict__ X, long long ldx, int M, int 
         if (lane == 0) scale[r] = s;
     }
 }
+
+// Blocks of `per` of n > 0 rows (n up to 2^31 - 1).
+constexpr unsigned blocks_of(int n, int per) { return static_cast<unsigned>((n - 1) / per + 1); }
 
 template <class El, int A>
 cudaError_t quantize_typed(const MoveArgs &a, int num_sms, cudaStream_t stream) {
@@ -233,7 +239,7 @@ cudaError_t quantize_typed(const MoveArgs &a, int num_sms, cudaStream_t stream) 
     const bool one = a.width <= kV * share;
 #define SG_QUANT(TPR)                                                                                            \
     return launch_dependent(one ? quantize_kernel<El, TPR, A, 1> : quantize_kernel<El, TPR, A, 4>,             \
-                            dim3((a.tokens + (TPR < 256 ? 256 / TPR : 1) - 1) / (TPR < 256 ? 256 / TPR : 1)),    \
+                            dim3(blocks_of(a.tokens, TPR < 256 ? 256 / TPR : 1)),                               \
                             dim3(TPR < 256 ? 256 : TPR), 0, stream, 1, X, a.ldx, a.tokens, a.width, Q, a.ldy,    \
                             a.scale, a.rows, a.choices)
     if (share == 32) SG_QUANT(32);
@@ -382,7 +388,8 @@ move_kernel(const Unit *__restrict__ X, long long ldx, int tokens, int choices, 
     constexpr int kMoves = kMovesOf<Unit>;
     const int slots = tokens * choices;
     const int c0 = blockIdx.x * (PER * kMoves) + threadIdx.x % PER;
-    for (int t = blockIdx.y * (256 / PER) + threadIdx.x / PER; t < tokens; t += gridDim.y * (256 / PER)) {
+    for (unsigned t = blockIdx.y * (256 / PER) + threadIdx.x / PER; t < static_cast<unsigned>(tokens);
+         t += gridDim.y * (256 / PER)) {
         const Unit *x = X + static_cast<long long>(t) * ldx;
         Unit v[kMoves];
 #pragma unroll
@@ -410,15 +417,16 @@ gather_kernel(const typename El::T *__restrict__ Y, long long ldy, int tokens, i
     griddep_wait();
     griddep_launch_dependents();
     const int slots = tokens * choices, c = blockIdx.x, lane = threadIdx.x % TPR;
-    for (int t = blockIdx.y * (256 / TPR) + threadIdx.x / TPR; t < tokens; t += gridDim.y * (256 / TPR)) {
+    for (unsigned t = blockIdx.y * (256 / TPR) + threadIdx.x / TPR; t < static_cast<unsigned>(tokens);
+         t += gridDim.y * (256 / TPR)) {
         float sum[kV] = {};
-        for (int j0 = 0; j0 < choices; j0 += J) {
+        for (unsigned j0 = 0; j0 < static_cast<unsigned>(choices); j0 += J) {
             Pack8<T> y[J];
             float w[J];
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const long long slot = static_cast<long long>(t) * choices + j0 + j;
-                const int r = j0 + j < choices ? row_of(rows, slot, slots) : -1;
+                const int r = j0 + j < static_cast<unsigned>(choices) ? row_of(rows, slot, slots) : -1;
                 w[j] = r >= 0 && weights ? __ldca(weights + slot) : 1.f;
                 // (a row that does not exist has no elements: zeros)
                 y[j] = load8<T, TPR, A>(Y + static_cast<long long>(r >= 0 ? r : 0) * ldy, c, lane, r >= 0 ? width : 0);
@@ -450,55 +458,56 @@ combine_grad_kernel(const typename El::T *__restrict__ dO, long long lddo, const
     griddep_wait();
     griddep_launch_dependents();
     const int slots = tokens * choices, lane = threadIdx.x % TPR;
-    for (int t = blockIdx.x * (256 / TPR) + threadIdx.x / TPR; t < tokens; t += gridDim.x * (256 / TPR)) {
-        const T *g = dO + static_cast<long long>(t) * lddo;
-        for (int j0 = 0; j0 < choices; j0 += J) {
-            int r[J];
-            float w[J], dot[J];
+    const unsigned t = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;  // (with a block a token, the whole block's)
+    if (t >= static_cast<unsigned>(tokens)) return;
+    const T *g = dO + static_cast<long long>(t) * lddo;
+    for (unsigned j0 = 0; j0 < static_cast<unsigned>(choices); j0 += J) {
+        int r[J];
+        float w[J], dot[J];
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const long long slot = static_cast<long long>(t) * choices + j0 + j;
-                r[j] = j0 + j < choices ? row_of(rows, slot, slots) : -1;
-                w[j] = r[j] >= 0 ? __ldca(weights + slot) : 0.f;
-                dot[j] = 0.f;
-            }
-            for (int c = 0; c * TPR * kV < width; ++c) {
-                const Pack8<T> gv = load8<T, TPR, A>(g, c, lane, width);
-                Pack8<T> y[J];
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-                    y[j] = load8<T, TPR, A>(Y + static_cast<long long>(r[j] >= 0 ? r[j] : 0) * ldy, c, lane,
-                                              r[j] >= 0 ? width : 0);
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    Pack8<T> o;
-#pragma unroll
-                    for (int e = 0; e < kV; ++e) {
-                        const float d = El::up(gv.v[e]);
-                        dot[j] = fmaf(d, El::up(y[j].v[e]), dot[j]);
-                        o.v[e] = El::down(w[j] * d);
-                    }
-                    if (r[j] >= 0) store8<T, TPR, A>(dY + static_cast<long long>(r[j]) * lddy, c, lane, width, o);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                if (r[j] < 0) dot[j] = 0.f;  // not 0 * dO, which a non-finite dO makes NaN
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
-                if (TPR > 32 && (threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = dot[j];
-                if (TPR == 32 && lane == 0 && j0 + j < choices) dw[static_cast<long long>(t) * choices + j0 + j] = dot[j];
-            }
-            if (TPR == 32) continue;
-            __syncthreads();
-            if (threadIdx.x < J && j0 + threadIdx.x < choices) {
-                float sum = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum += part[k][threadIdx.x];
-                dw[static_cast<long long>(t) * choices + j0 + threadIdx.x] = sum;
-            }
-            __syncthreads();
+        for (int j = 0; j < J; ++j) {
+            const long long slot = static_cast<long long>(t) * choices + j0 + j;
+            r[j] = j0 + j < static_cast<unsigned>(choices) ? row_of(rows, slot, slots) : -1;
+            w[j] = r[j] >= 0 ? __ldca(weights + slot) : 0.f;
+            dot[j] = 0.f;
         }
+        for (int c = 0; c * TPR * kV < width; ++c) {
+            const Pack8<T> gv = load8<T, TPR, A>(g, c, lane, width);
+            Pack8<T> y[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                y[j] = load8<T, TPR, A>(Y + static_cast<long long>(r[j] >= 0 ? r[j] : 0) * ldy, c, lane,
+                                          r[j] >= 0 ? width : 0);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                Pack8<T> o;
+#pragma unroll
+                for (int e = 0; e < kV; ++e) {
+                    const float d = El::up(gv.v[e]);
+                    dot[j] = fmaf(d, El::up(y[j].v[e]), dot[j]);
+                    o.v[e] = El::down(w[j] * d);
+                }
+                if (r[j] >= 0) store8<T, TPR, A>(dY + static_cast<long long>(r[j]) * lddy, c, lane, width, o);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (r[j] < 0) dot[j] = 0.f;  // not 0 * dO, which a non-finite dO makes NaN
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
+            if (TPR > 32 && (threadIdx.x & 31) == 0) part[threadIdx.x >> 5][j] = dot[j];
+            if (TPR == 32 && lane == 0 && j0 + j < static_cast<unsigned>(choices))
+                dw[static_cast<long long>(t) * choices + j0 + j] = dot[j];
+        }
+        if (TPR == 32) continue;
+        __syncthreads();
+        if (threadIdx.x < J && j0 + threadIdx.x < static_cast<unsigned>(choices)) {
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += part[k][threadIdx.x];
+            dw[static_cast<long long>(t) * choices + j0 + threadIdx.x] = sum;
+        }
+        __syncthreads();
     }
 }
 
@@ -520,7 +529,7 @@ cudaError_t with_access(int alignment, F &&f) {
     return f(std::integral_constant<int, 1>{});
 }
 
-constexpr int kMaxGridY = 65535;
+constexpr unsigned kMaxGridY = 65535;
 
 template <class El, int J, int TPR>
 cudaError_t gather_tpr(const MoveArgs &a, cudaStream_t stream) {
@@ -528,7 +537,7 @@ cudaError_t gather_tpr(const MoveArgs &a, cudaStream_t stream) {
     constexpr int kSize = sizeof(T);
     const int al = common_alignment(reinterpret_cast<uintptr_t>(a.X), reinterpret_cast<uintptr_t>(a.Y), a.ldx * kSize,
                                     a.ldy * kSize, static_cast<long long>(a.width) * kSize);
-    const int blocks = (a.tokens + 256 / TPR - 1) / (256 / TPR);
+    const unsigned blocks = blocks_of(a.tokens, 256 / TPR);
     const dim3 grid((a.width + TPR * kV - 1) / (TPR * kV), blocks < kMaxGridY ? blocks : kMaxGridY);
     return with_access<kSize>(al, [&](auto n) {
         return launch_dependent(gather_kernel<El, J, TPR, decltype(n)::value>, grid, dim3(256), 0, stream, 1,
@@ -561,7 +570,7 @@ cudaError_t combine_grad_tpr(const MoveArgs &a, cudaStream_t stream) {
                                     static_cast<long long>(a.width) * kSize);
     return with_access<kSize>(al, [&](auto n) {
         return launch_dependent(combine_grad_kernel<El, J, TPR, decltype(n)::value>,
-                                dim3((a.tokens + 256 / TPR - 1) / (256 / TPR)), dim3(256), 0, stream, 1,
+                                dim3(blocks_of(a.tokens, 256 / TPR)), dim3(256), 0, stream, 1,
                                 static_cast<const T *>(a.X), a.ldx, static_cast<const T *>(a.Y), a.ldy, a.tokens,
                                 a.choices, a.width, a.rows, a.weights, static_cast<T *>(a.dY), a.lddy, a.scale);
     });
@@ -586,7 +595,7 @@ cudaError_t combine_grad_typed(const MoveArgs &a, cudaStream_t stream) {
 template <class Unit, int PER>
 cudaError_t move_per(const MoveArgs &a, int size, int width, cudaStream_t stream) {
     constexpr int kUnits = PER * kMovesOf<Unit>;
-    const int blocks = (a.tokens + 256 / PER - 1) / (256 / PER);
+    const unsigned blocks = blocks_of(a.tokens, 256 / PER);
     const dim3 grid((width + kUnits - 1) / kUnits, blocks < kMaxGridY ? blocks : kMaxGridY);
     return launch_dependent(move_kernel<Unit, PER>, grid, dim3(256), 0, stream, 1, static_cast<const Unit *>(a.X),
                             a.ldx * size / static_cast<int>(sizeof(Unit)), a.tokens, a.choices, width, a.rows,
