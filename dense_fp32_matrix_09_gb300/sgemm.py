@@ -523,6 +523,19 @@ def _ld(t) -> int:
     return max(t.stride(0), t.shape[1], 1)
 
 
+def _on_device(**tensors) -> None:
+    """Every tensor (None: not given) is on the current CUDA device, whose addresses
+    the kernels can use."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU, got {t.device}")
+    import torch
+    current = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"{name} must be on the current device (cuda:{current}), got {t.device}")
+
+
 def _rows_of(name, t, dtype=None) -> None:
     if t.dim() != 2 or (t.numel() and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
         raise ValueError(f"{name} must be 2-D with unit column stride and rows that do not overlap")
@@ -604,14 +617,15 @@ class Sgemm:
                   max(C.stride(0), 1), stream)
         return C
 
-    # -- 8-bit products and expert routing on torch tensors: shapes and types are
-    #    checked here, results are new tensors on the inputs' device.  They are made
+    # -- 8-bit products and expert routing on torch tensors: devices, shapes and
+    #    types are checked here, results are new tensors on the inputs' device.  They are made
     #    on `stream` (None: the current one) like torch's own under
     #    torch.cuda.stream(stream): the inputs have to be ready there, and another
     #    stream that uses the results has to wait for it ----------------------------
     def quantize(self, X, stream=None):
         """(Q, scale): the rows of X (2-D, FP32/BF16/FP16) in int8 and their FP32 scales."""
         import torch
+        _on_device(X=X)
         kind = _element_type(X)
         _rows_of("X", X)
         M, K = X.shape
@@ -625,6 +639,7 @@ class Sgemm:
         """scaleA[:, None] * scaleB * (A @ B.T) + bias for int8 A (M x K) and B (N x K);
         `out_dtype` (BF16 unless given) or `out` says of which type."""
         import torch
+        _on_device(A=A, scaleA=scaleA, B=B, scaleB=scaleB, bias=bias, out=out)
         _rows_of("A", A, torch.int8)
         _rows_of("B", B, torch.int8)
         (M, K), (N, K2) = A.shape, B.shape
@@ -645,6 +660,7 @@ class Sgemm:
         of A with B[e] (experts x N x K, contiguous); scaleB, bias: experts x N.  Rows of
         no expert are left as they are in `out` (zeros without it)."""
         import torch
+        _on_device(offsets=offsets, A=A, scaleA=scaleA, B=B, scaleB=scaleB, bias=bias, out=out)
         _rows_of("A", A, torch.int8)
         if B.dim() != 3 or B.dtype != torch.int8 or not B.is_contiguous() or B.shape[2] != A.shape[1]:
             raise ValueError(f"B must be a contiguous experts x N x {A.shape[1]} int8 tensor, got {tuple(B.shape)}")
@@ -665,6 +681,7 @@ class Sgemm:
     def expert_sort(self, ids, experts, stream=None):
         """(offsets, rows, source) of ids (tokens x choices, int32)."""
         import torch
+        _on_device(ids=ids)
         if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
             raise ValueError("ids must be a contiguous tokens x choices int32 tensor")
         tokens, choices = ids.shape
@@ -678,6 +695,7 @@ class Sgemm:
     def expert_dispatch(self, X, rows, stream=None):
         """The tokens' rows in the experts' order (tokens * choices rows; those of no slot are zero)."""
         import torch
+        _on_device(X=X, rows=rows)
         _rows_of("X", X)
         tokens, choices = _slots(rows, X.shape[0])
         with _on(stream, X, rows):
@@ -688,6 +706,7 @@ class Sgemm:
     def expert_dispatch_int8(self, X, rows, stream=None):
         """(Q, scale): expert_dispatch and quantize in one pass."""
         import torch
+        _on_device(X=X, rows=rows)
         _rows_of("X", X)
         tokens, choices = _slots(rows, X.shape[0])
         with _on(stream, X, rows):
@@ -700,6 +719,7 @@ class Sgemm:
     def expert_dispatch_grad(self, dY, rows, stream=None):
         """dX from the gradient of expert_dispatch's result."""
         import torch
+        _on_device(dY=dY, rows=rows)
         tokens, choices = _slots(rows)
         _rows_of("dY", dY)
         if dY.shape[0] != tokens * choices:
@@ -713,6 +733,7 @@ class Sgemm:
     def expert_combine(self, Y, rows, weights, stream=None):
         """sum_j weights[t, j] * Y[rows[t, j]]."""
         import torch
+        _on_device(Y=Y, rows=rows, weights=weights)
         tokens, choices = _slots(rows)
         _rows_of("Y", Y)
         _weights(weights, tokens, choices)
@@ -727,6 +748,7 @@ class Sgemm:
     def expert_combine_grad(self, dout, Y, rows, weights, stream=None):
         """(dY, dweights) of expert_combine; rows of no slot have a zero gradient."""
         import torch
+        _on_device(dout=dout, Y=Y, rows=rows, weights=weights)
         tokens, choices = _slots(rows, dout.shape[0])
         _rows_of("dout", dout, Y.dtype)
         _rows_of("Y", Y)
