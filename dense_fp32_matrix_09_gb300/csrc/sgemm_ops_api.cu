@@ -283,6 +283,18 @@ int enter(sgemm_handle_t h) {
     return SGEMM_OK;
 }
 
+// A call that had nothing to do: what the getters report of it.
+int nothing(sgemm_handle_t h) {
+    sg::record_call(h, -1, 1, 0, 0);
+    return SGEMM_OK;
+}
+
+// The end of a call of one launch: recorded where it was enqueued.
+int launched(sgemm_handle_t h, cudaError_t e) {
+    if (e == cudaSuccess) sg::record_call(h, -1, 1, 1, 0);
+    return from_cuda(e);
+}
+
 // Sizes and the slots of a routing call.
 int check_slots(int tokens, int choices) {
     if (tokens < 0 || choices < 1) return SGEMM_ERR_INVALID_VALUE;
@@ -318,10 +330,7 @@ int sgemm_run_int8(sgemm_handle_t h, int transB, int out_type, int M, int N, int
     if (st == SGEMM_OK)
         st = check_int8(transB, out_type, 1, M, N, K, nullptr, false, A, lda, scaleA, B, ldb, 0, scaleB, bias, C, ldc);
     if (st != SGEMM_OK) return st;
-    if (M == 0 || N == 0) {
-        sg::record_call(h, -1, 1, 0, 0);
-        return SGEMM_OK;
-    }
+    if (M == 0 || N == 0) return nothing(h);
     return run_int8(h, transB, out_type, 1, M, N, K, nullptr, A, lda, scaleA, B, ldb, 0, scaleB, bias, C, ldc,
                     static_cast<cudaStream_t>(stream));
 }
@@ -335,10 +344,7 @@ int sgemm_run_int8_experts(sgemm_handle_t h, int transB, int out_type, int exper
         st = check_int8(transB, out_type, experts, rows, N, K, offsets, true, A, lda, scaleA, B, ldb, strideB,
                         scaleB, bias, C, ldc);
     if (st != SGEMM_OK) return st;
-    if (rows == 0 || N == 0) {
-        sg::record_call(h, -1, 1, 0, 0);
-        return SGEMM_OK;
-    }
+    if (rows == 0 || N == 0) return nothing(h);
     return run_int8(h, transB, out_type, experts, rows, N, K, offsets, A, lda, scaleA, B, ldb, strideB, scaleB, bias,
                     C, ldc, static_cast<cudaStream_t>(stream));
 }
@@ -350,8 +356,7 @@ int sgemm_quantize_rows(sgemm_handle_t h, int type, int M, int K, const void *X,
     if (M < 0 || check_row(type, K, ldx) != SGEMM_OK || ldq < std::max(1, K)) return SGEMM_ERR_INVALID_VALUE;
     sg::HandleView v;
     sg::view_of(h, &v);
-    sg::record_call(h, -1, 1, 0, 0);
-    if (M == 0) return SGEMM_OK;
+    if (M == 0) return nothing(h);
     if (scale == nullptr || (K > 0 && (X == nullptr || Q == nullptr))) return SGEMM_ERR_NULL;
     if (!aligned(X, size_of(type)) || !aligned(scale, 4)) return SGEMM_ERR_INVALID_VALUE;
     const Range x(X, M, K, ldx, size_of(type)), q(Q, M, K, ldq, 1), s(scale, 1, M, M, 4);
@@ -365,9 +370,7 @@ int sgemm_quantize_rows(sgemm_handle_t h, int type, int M, int K, const void *X,
     a.Y = Q;
     a.ldy = ldq;
     a.scale = scale;
-    const int rc = from_cuda(sg::launch_quantize(type, a, v.num_sms, static_cast<cudaStream_t>(stream)));
-    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 1, 0);
-    return rc;
+    return launched(h, sg::launch_quantize(type, a, v.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 int sgemm_expert_sort(sgemm_handle_t h, int tokens, int choices, int experts, const int *ids, int *offsets,
@@ -390,7 +393,7 @@ int sgemm_expert_sort(sgemm_handle_t h, int tokens, int choices, int experts, co
     int launches = 0;
     const int rc = from_cuda(sg::launch_sort(ids, slots, experts, offsets, rows, source, reinterpret_cast<int *>(v.d_ws),
                                              &launches, static_cast<cudaStream_t>(stream)));
-    sg::record_call(h, -1, 1, rc == SGEMM_OK ? launches : 0, 0);
+    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, launches, 0);
     return rc;
 }
 
@@ -401,8 +404,7 @@ int sgemm_expert_dispatch(sgemm_handle_t h, int type, int tokens, int choices, i
     if (st == SGEMM_OK) st = check_row(type, width, ldx);
     if (st == SGEMM_OK) st = check_row(type, width, ldy);
     if (st != SGEMM_OK) return st;
-    sg::record_call(h, -1, 1, 0, 0);
-    if (tokens == 0 || width == 0) return SGEMM_OK;
+    if (tokens == 0 || width == 0) return nothing(h);
     if (X == nullptr || Y == nullptr || rows == nullptr) return SGEMM_ERR_NULL;
     const int size = size_of(type);
     if (!aligned(X, size) || !aligned(Y, size) || !aligned(rows, 4)) return SGEMM_ERR_INVALID_VALUE;
@@ -418,9 +420,7 @@ int sgemm_expert_dispatch(sgemm_handle_t h, int type, int tokens, int choices, i
     a.rows = rows;
     a.Y = Y;
     a.ldy = ldy;
-    const int rc = from_cuda(sg::launch_dispatch(type, a, static_cast<cudaStream_t>(stream)));
-    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 1, 0);
-    return rc;
+    return launched(h, sg::launch_dispatch(type, a, static_cast<cudaStream_t>(stream)));
 }
 
 int sgemm_expert_dispatch_int8(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *X, int ldx,
@@ -430,8 +430,7 @@ int sgemm_expert_dispatch_int8(sgemm_handle_t h, int type, int tokens, int choic
     if (st == SGEMM_OK) st = check_row(type, width, ldx);
     if (st != SGEMM_OK) return st;
     if (ldq < std::max(1, width)) return SGEMM_ERR_INVALID_VALUE;
-    sg::record_call(h, -1, 1, 0, 0);
-    if (tokens == 0) return SGEMM_OK;
+    if (tokens == 0) return nothing(h);
     if (rows == nullptr || scale == nullptr || (width > 0 && (X == nullptr || Q == nullptr))) return SGEMM_ERR_NULL;
     const int size = size_of(type), slots = tokens * choices;
     if (!aligned(X, size) || !aligned(scale, 4) || !aligned(rows, 4)) return SGEMM_ERR_INVALID_VALUE;
@@ -450,9 +449,7 @@ int sgemm_expert_dispatch_int8(sgemm_handle_t h, int type, int tokens, int choic
     a.Y = Q;
     a.ldy = ldq;
     a.scale = scale;
-    const int rc = from_cuda(sg::launch_quantize(type, a, v.num_sms, static_cast<cudaStream_t>(stream)));
-    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 1, 0);
-    return rc;
+    return launched(h, sg::launch_quantize(type, a, v.num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 // out[t] = sum_j w[t][j] * Y[rows[t][j]] (weights NULL only from dispatch_grad).
@@ -463,8 +460,7 @@ static int run_gather(sgemm_handle_t h, int type, int tokens, int choices, int w
     if (st == SGEMM_OK) st = check_row(type, width, ldy);
     if (st == SGEMM_OK) st = check_row(type, width, ldo);
     if (st != SGEMM_OK) return st;
-    sg::record_call(h, -1, 1, 0, 0);
-    if (tokens == 0 || width == 0) return SGEMM_OK;
+    if (tokens == 0 || width == 0) return nothing(h);
     if (Y == nullptr || rows == nullptr || out == nullptr || (weighted && weights == nullptr)) return SGEMM_ERR_NULL;
     const int size = size_of(type), slots = tokens * choices;
     if (!aligned(Y, size) || !aligned(out, size) || !aligned(rows, 4) || !aligned(weights, 4))
@@ -482,9 +478,7 @@ static int run_gather(sgemm_handle_t h, int type, int tokens, int choices, int w
     a.weights = weights;
     a.Y = const_cast<void *>(Y);
     a.ldy = ldy;
-    const int rc = from_cuda(sg::launch_gather(type, a, static_cast<cudaStream_t>(stream)));
-    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 1, 0);
-    return rc;
+    return launched(h, sg::launch_gather(type, a, static_cast<cudaStream_t>(stream)));
 }
 
 int sgemm_expert_dispatch_grad(sgemm_handle_t h, int type, int tokens, int choices, int width, const void *dY,
@@ -506,8 +500,7 @@ int sgemm_expert_combine_grad(sgemm_handle_t h, int type, int tokens, int choice
     if (st == SGEMM_OK) st = check_row(type, width, ldy);
     if (st == SGEMM_OK) st = check_row(type, width, lddy);
     if (st != SGEMM_OK) return st;
-    sg::record_call(h, -1, 1, 0, 0);
-    if (tokens == 0) return SGEMM_OK;
+    if (tokens == 0) return nothing(h);
     if (rows == nullptr || weights == nullptr || dweights == nullptr ||
         (width > 0 && (dout == nullptr || Y == nullptr || dY == nullptr)))
         return SGEMM_ERR_NULL;
@@ -533,9 +526,7 @@ int sgemm_expert_combine_grad(sgemm_handle_t h, int type, int tokens, int choice
     a.dY = dY;
     a.lddy = lddy;
     a.scale = dweights;
-    const int rc = from_cuda(sg::launch_combine_grad(type, a, static_cast<cudaStream_t>(stream)));
-    if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 1, 0);
-    return rc;
+    return launched(h, sg::launch_combine_grad(type, a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
