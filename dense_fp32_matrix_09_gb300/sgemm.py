@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 
 from . import build as _build
@@ -179,7 +180,7 @@ def _current_stream_handle() -> int:
 def calls_module():
     """The CPython module that marshals the arguments of the enqueue calls
     (built next to the library by build.py), bound to the loaded library; None
-    when it was not built -- the two calls then go through ctypes."""
+    when it was not built -- the calls then go through ctypes."""
     global _calls, _calls_tried
     if not _calls_tried:
         _calls_tried = True
@@ -330,6 +331,15 @@ def sgemm_check_args_mixed(in_type, transA, transB, M, N, K, alpha, A, lda, B, l
                                         int(ldc))
 
 
+def _integer(x, kind) -> int:
+    """The value of an integer of any type (numpy's, which are buffers too, among
+    them) for a parameter of the C integer type `kind`."""
+    v = operator.index(x)
+    if kind(v).value != v:
+        raise OverflowError(f"{v} does not fit in a C {kind.__name__[2:]}")
+    return v
+
+
 def _enqueue(name: str, h, args, stream) -> None:
     """Call an enqueue function of the library through the marshalling module
     (every argument an int or a buffer), or through ctypes without it."""
@@ -337,7 +347,9 @@ def _enqueue(name: str, h, args, stream) -> None:
     if calls is not None:
         rc = calls.enqueue(name, h, args, stream)
     else:
-        rc = getattr(lib(), name)(h, *[a if isinstance(a, int) else _ptr(a) for a in args], _stream(stream))
+        fn = getattr(lib(), name)
+        values = [_ptr(a) if kind is ctypes.c_void_p else _integer(a, kind) for a, kind in zip(args, fn.argtypes[1:-1])]
+        rc = fn(h, *values, _stream(stream))
     if rc != OK:
         raise SgemmError(rc, name)
 

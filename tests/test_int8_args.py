@@ -126,3 +126,35 @@ def test_marshalling_rejects_malformed_arguments():
         calls.enqueue("sgemm_quantize_rows", None, (0, 1 << 40, *good[2:]), 0)
     with pytest.raises((TypeError, AttributeError)):
         calls.enqueue("sgemm_quantize_rows", None, (*good[:-1], object()), 0)
+
+
+@pytest.mark.parametrize("call,args", CALLS, ids=[c.__name__ for c, _ in CALLS])
+def test_numpy_integers_are_sizes_through_ctypes_too(call, args, monkeypatch):
+    """Without the marshalling module the values that reach the library are the same."""
+    import numpy as np
+    real = getattr(sgemm.lib(), call.__name__)
+    seen = []
+
+    class Library:
+        pass
+
+    def record(*values):
+        seen.append(tuple(v for v in values))
+        return OK
+
+    record.argtypes = real.argtypes
+    library = Library()
+    setattr(library, call.__name__, record)
+    monkeypatch.setattr(sgemm, "_calls", None)
+    monkeypatch.setattr(sgemm, "_calls_tried", True)
+    monkeypatch.setattr(sgemm, "lib", lambda: library)
+    call(None, *args, stream=0)
+    sizes = [t is not ctypes.c_void_p for t in real.argtypes[1:-1]]
+    call(None, *[np.int64(a) if s else a for a, s in zip(args, sizes)], stream=0)
+    assert seen[0] == (None, *args, 0) and seen[1] == seen[0]
+    assert all(type(v) is int or v is None for v in seen[1])
+    with pytest.raises(TypeError):
+        call(None, *[float(a) if s else a for a, s in zip(args, sizes)], stream=0)
+    with pytest.raises(OverflowError):
+        call(None, 1 << 40, *args[1:], stream=0)
+    assert len(seen) == 2
