@@ -549,7 +549,9 @@ def _on_device(**tensors) -> None:
 
 
 def _rows_of(name, t, dtype=None) -> None:
-    if t.dim() != 2 or (t.numel() and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+    # (of one column the stride says nothing: a contiguous tensor may have any there)
+    if t.dim() != 2 or (t.numel() and t.shape[1] > 1 and t.stride(1) != 1) or \
+            (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
         raise ValueError(f"{name} must be 2-D with unit column stride and rows that do not overlap")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")

@@ -71,3 +71,15 @@ def test_a_tensor_on_another_device_is_refused(g, method, name):
     args = {k: OnGpu(t, int(k == name)) for k, t in arguments()[method].items()}
     with pytest.raises(ValueError, match=f"{name} must be on the current device"):
         call(g, method, args)
+
+
+def test_rows_of_one_column_may_have_any_column_stride():
+    column = torch.zeros(1, 5).t()                     # 5 x 1, contiguous, strides (1, 5)
+    assert column.is_contiguous() and column.stride(1) != 1
+    sgemm._rows_of("X", column)
+    assert sgemm._ld(column) == 1
+    sgemm._rows_of("X", torch.zeros(5, 8)[:, 3:4])
+    assert sgemm._ld(torch.zeros(5, 8)[:, 3:4]) == 8
+    for bad in (torch.zeros(5, 4).t(), torch.zeros(1, 1).expand(5, 1), torch.zeros(1, 4).expand(5, 4), torch.zeros(5)):
+        with pytest.raises(ValueError):
+            sgemm._rows_of("X", bad)
