@@ -7,11 +7,15 @@ weights (an activation between them, quantized again) and the weighted way back.
 Training: dispatch and combine as autograd functions around FP32 products of
 each expert's rows (sgemm_run_ex), one step of gradient descent on a small target.
 
+The gradients are the library's results, not differentiable themselves: a second
+derivative is refused.
+
     python -m examples.expert_layer            # needs a GB300 and the built library
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from dense_fp32_matrix_09_gb300 import sgemm
 
@@ -50,6 +54,7 @@ class Dispatch(torch.autograd.Function):
         return g.expert_dispatch(x, rows)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         return ctx.g.expert_dispatch_grad(dy.contiguous(), ctx.rows), None, None
 
@@ -62,6 +67,7 @@ class Combine(torch.autograd.Function):
         return g.expert_combine(y, rows, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         y, weights = ctx.saved_tensors
         dy, dweights = ctx.g.expert_combine_grad(dout.contiguous(), y, ctx.rows, weights)
@@ -82,6 +88,7 @@ class ExpertProduct(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         (x, w), g, bounds = ctx.saved_tensors, ctx.g, ctx.bounds
         dy = dy.contiguous()
