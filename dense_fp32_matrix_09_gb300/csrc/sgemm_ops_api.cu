@@ -113,6 +113,14 @@ bool choose_few(int rows, int N, int K, bool b_aligned, double tc_us) {
     return few + 5e-5 * rows * K < tc_us + (b_aligned ? 0.0 : 2.0 + 0.28 * mb);
 }
 
+// Whether the kernel for few tokens beats the generic one, where the tensor cores
+// cannot run (B needs a copy that it may not or cannot have).  The generic kernel takes
+// 1.9 us for every 64 of K and reads 64 rows whatever the tokens: 1 token x 4096 x 4097
+// 128 us against 9.2, 8 tokens x 700 x 701 23 against 3.9, 8 x 4000 x 17 4.1 against 3.2.
+// On a short K its tiles are the better use of a wave, where channels make many: 8 x
+// 30000 x 17 6.7 against 17, 1 x 100000 x 129 34 against 38 (257: 53 against 45).
+bool few_beats_generic(int N, int K) { return N <= 8192 || K > 256; }
+
 int check_int8(int transB, int out_type, int experts, int rows, int N, int K, const int *offsets, bool grouped,
                const int8_t *A, int lda, const float *scaleA, const int8_t *B, int ldb, long long strideB,
                const float *scaleB, const float *bias, const void *C, int ldc) {
@@ -181,22 +189,22 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
     uint8_t *ws = reinterpret_cast<uint8_t *>(v.d_rl);
     size_t room = v.rl_bytes;
     const bool as_stored = transB && aligned(B, 16) && ldb % 16 == 0 && (experts == 1 || strideB % 16 == 0);
-    if (experts == 1 && !offsets && transB && K > 0 && rows <= sg::kI8FewRows &&
-        sg::int8_few_bytes(rows, K) <= sg::kI8FewBytes &&
-        (v.pinned == SGEMM_VARIANT_FEW_I8 ||
-         (v.pinned != SGEMM_VARIANT_TC_I8 && v.pinned != SGEMM_VARIANT_GENERIC_I8 && v.pinned != SGEMM_VARIANT_GENERIC &&
-          choose_few(rows, N, K, as_stored, tile.us)))) {
-        const cudaError_t e = sg::launch_int8_few(a, v.num_sms, stream);
-        if (e != cudaSuccess) return from_cuda(e);
-        sg::record_call(h, SGEMM_VARIANT_FEW_I8, 1, 1, 0);
-        return SGEMM_OK;
-    }
     const size_t b_bytes = as_stored ? 0 : static_cast<size_t>(experts) * N * kb;
     const size_t peak_room = direct ? 0 : sg::kI8Peaks * sizeof(int);
     const size_t b_room = (b_bytes + 1023) / 1024 * 1024 + peak_room;
     bool tc = v.pinned != SGEMM_VARIANT_GENERIC && v.pinned != SGEMM_VARIANT_GENERIC_I8 && K > 0 &&
               ((as_stored && a_as_stored) || ws != nullptr) && (as_stored || v.relayout_mode != SGEMM_RELAYOUT_OFF) &&
               b_room <= room && room - b_room >= a_row * std::min(rows, a.nt);
+    if (experts == 1 && !offsets && transB && K > 0 && rows <= sg::kI8FewRows &&
+        sg::int8_few_bytes(rows, K) <= sg::kI8FewBytes &&
+        (v.pinned == SGEMM_VARIANT_FEW_I8 ||
+         (v.pinned != SGEMM_VARIANT_TC_I8 && v.pinned != SGEMM_VARIANT_GENERIC_I8 && v.pinned != SGEMM_VARIANT_GENERIC &&
+          (tc ? choose_few(rows, N, K, as_stored, tile.us) : few_beats_generic(N, K))))) {
+        const cudaError_t e = sg::launch_int8_few(a, v.num_sms, stream);
+        if (e != cudaSuccess) return from_cuda(e);
+        sg::record_call(h, SGEMM_VARIANT_FEW_I8, 1, 1, 0);
+        return SGEMM_OK;
+    }
     const long long ch_tiles = cdiv(N, sg::kI8TileN);
     int per = rows;  // rows of one pass
     if (tc) {

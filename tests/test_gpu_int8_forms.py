@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from dense_fp32_matrix_09_gb300 import sgemm
-from tests.test_gpu_int8 import FILL, Experts, handle, pinned  # noqa: F401  (fixtures)
+from tests.test_gpu_int8 import FILL, Experts, Problem, handle, pinned  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,18 @@ def test_many_offsets_out_of_order(handle, pinned, variant):  # noqa: F811
     got = p.run(handle, offsets.cuda())
     p.offsets = in_order(offsets.tolist(), p.R)
     p.check(got)
+
+
+@pytest.mark.parametrize("M,N,K,variant", [(1, 300, 1001, V.VARIANT_FEW_I8), (8, 700, 701, V.VARIANT_FEW_I8),
+                                           (8, 4096, 4097, V.VARIANT_FEW_I8), (3, 9000, 301, V.VARIANT_FEW_I8),
+                                           (8, 9000, 33, V.VARIANT_GENERIC_I8), (9, 300, 1001, V.VARIANT_GENERIC_I8)])
+def test_few_tokens_where_b_may_not_be_copied(handle, pinned, M, N, K, variant):  # noqa: F811
+    """Without the copy the tensor cores cannot run: the kernel for few tokens, which
+    reads B in place, is weighed against the generic one and not against them."""
+    p = Problem(M, N, K, "bf16", bias=True, seed=9)
+    sgemm.sgemm_set_relayout(handle, V.RELAYOUT_OFF)
+    first = p.run(handle)
+    assert sgemm.sgemm_last_variant(handle)[0] == variant
+    p.check(first)
+    pinned(V.VARIANT_GENERIC_I8)
+    assert torch.equal(p.run(handle), first)
