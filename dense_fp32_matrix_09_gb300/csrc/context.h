@@ -18,6 +18,7 @@ struct HandleView {
     float *d_rl;       // operand re-layout workspace (NULL: none), rl_bytes bytes
     size_t rl_bytes;
     int pinned, relayout_mode, smem_override;
+    int i8_tokens, i8_split;  // test hook: the int8 products' token tile and K split (0: chosen)
 };
 
 bool is_live(sgemm_handle_t h);

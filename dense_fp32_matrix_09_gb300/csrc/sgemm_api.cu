@@ -98,6 +98,7 @@ struct sgemm_ctx {
     int ksplit_pin;                         // test hook: cluster split-K CTAs per tile (0 auto, 1 none)
     int sk_ctas_pin;                        // test hook: stream-K CTAs of a tail or split-all plan (0 auto)
     int sk_gap_pin = -1;                    // test hook: boundary charge of stream-K splits (-1 auto)
+    int i8_tokens, i8_split;                // test hook: token tile and K split of the int8 products (0 auto)
     int ws_tiles_limit;                     // test hook: workspace capacity the kernels are told (0: real)
     cudaStream_t copy_in, copy_out;         // sgemm_run_host: host->device, device->host
     cudaEvent_t ev_start, ev_done;          //   ordering events (no timing)
@@ -847,7 +848,7 @@ bool is_live(sgemm_handle_t h) { return alive(h); }
 
 void view_of(sgemm_handle_t h, HandleView *v) {
     *v = HandleView{h->device, h->num_sms, h->d_status, h->d_ws, h->ws_floats, h->d_rl,
-                    h->rl_floats * sizeof(float), h->pinned, h->relayout_mode, h->smem_override};
+                    h->rl_floats * sizeof(float), h->pinned, h->relayout_mode, h->smem_override, h->i8_tokens, h->i8_split};
 }
 
 void record_call(sgemm_handle_t h, int variant, int splits, int launches, int copied) {
@@ -1125,6 +1126,17 @@ int sgemm_debug_set_cluster_split(sgemm_handle_t h, int ksplit) {
     if (!alive(h)) return SGEMM_ERR_BAD_HANDLE;
     if (ksplit < 0 || ksplit > 8) return SGEMM_ERR_INVALID_VALUE;
     h->ksplit_pin = ksplit;
+    return SGEMM_OK;
+}
+
+int sgemm_debug_set_int8_tile(sgemm_handle_t h, int tokens, int ksplit) {
+    if (!alive(h)) return SGEMM_ERR_BAD_HANDLE;
+    const bool direct = (tokens == 16 || tokens == 32 || tokens == 64) &&
+                        (ksplit == 1 || ksplit == 2 || ksplit == 4 || ksplit == 8);
+    const bool pair = (tokens == 128 || tokens == 256) && ksplit == 1;
+    if (!direct && !pair && (tokens != 0 || ksplit != 0)) return SGEMM_ERR_INVALID_VALUE;
+    h->i8_tokens = tokens;
+    h->i8_split = ksplit;
     return SGEMM_OK;
 }
 

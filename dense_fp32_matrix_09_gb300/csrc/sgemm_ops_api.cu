@@ -177,7 +177,12 @@ int run_int8(sgemm_handle_t h, int transB, int out_type, int experts, int rows, 
     // Tiles of up to 64 tokens read the tokens' int8 rows, by TMA: rows on other
     // than 16-byte boundaries are copied first.  Wider tiles read them as FP16.
     const bool a_aligned = aligned(A, 16) && lda % 16 == 0;
-    const TileChoice tile = choose_tile(rows, experts, N, std::max(K, 1), v.num_sms, !a_aligned);
+    TileChoice tile = choose_tile(rows, experts, N, std::max(K, 1), v.num_sms, !a_aligned);
+    if (v.i8_tokens) {
+        tile.nt = v.i8_tokens;
+        tile.ksplit = v.i8_split;
+        while (tile.ksplit > 1 && tile.ksplit > cdiv(K, sg::kI8StageK)) tile.ksplit /= 2;
+    }
     a.nt = tile.nt;
     const bool direct = a.nt <= 64;
     const bool a_as_stored = direct && a_aligned;

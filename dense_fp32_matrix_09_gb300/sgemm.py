@@ -68,7 +68,7 @@ EXPORTS = ("sgemm_create", "sgemm_run", "sgemm_check_args", "sgemm_destroy", "sg
            "sgemm_set_relayout", "sgemm_last_relayout", "sgemm_relayout_capacity", "sgemm_debug_plan",
            "sgemm_debug_set_stream_k_sums", "sgemm_debug_set_cluster_split", "sgemm_debug_set_stream_k_ctas",
            "sgemm_debug_set_stream_k_gap", "sgemm_debug_leave_aborted_state", "sgemm_debug_tf32_probe",
-           "sgemm_debug_set_workspace_limit", "sgemm_run_int8", "sgemm_check_args_int8",
+           "sgemm_debug_set_workspace_limit", "sgemm_debug_set_int8_tile", "sgemm_run_int8", "sgemm_check_args_int8",
            "sgemm_run_int8_experts", "sgemm_check_args_int8_experts", "sgemm_quantize_rows", "sgemm_expert_sort",
            "sgemm_expert_dispatch", "sgemm_expert_dispatch_int8", "sgemm_expert_dispatch_grad",
            "sgemm_expert_combine", "sgemm_expert_combine_grad")
@@ -124,6 +124,7 @@ def lib() -> ctypes.CDLL:
         L.sgemm_debug_set_smem_override.argtypes = [vp, i32]
         L.sgemm_debug_set_stream_k_sums.argtypes = [vp, i32]
         L.sgemm_debug_set_cluster_split.argtypes = [vp, i32]
+        L.sgemm_debug_set_int8_tile.argtypes = [vp, i32, i32]
         L.sgemm_debug_set_stream_k_ctas.argtypes = [vp, i32]
         L.sgemm_debug_set_stream_k_gap.argtypes = [vp, i32]
         L.sgemm_debug_leave_aborted_state.argtypes = [vp]
@@ -514,6 +515,11 @@ def sgemm_debug_set_stream_k_gap(h, gap: int) -> None:
 def sgemm_debug_set_cluster_split(h, ksplit: int) -> None:
     """0: automatic; 1: no cluster split-K; 2..8: that many CTAs per tile."""
     _check(lib().sgemm_debug_set_cluster_split(h, int(ksplit)), "sgemm_debug_set_cluster_split")
+
+
+def sgemm_debug_set_int8_tile(h, tokens: int, ksplit: int) -> None:
+    """Token tile and K split of later int8 products on the tensor cores (test hook; 0, 0: the library's choice)."""
+    _check(lib().sgemm_debug_set_int8_tile(h, int(tokens), int(ksplit)), "sgemm_debug_set_int8_tile")
 
 
 def sgemm_debug_set_stream_k_sums(h, mode: int) -> None:

@@ -576,6 +576,13 @@ int sgemm_debug_set_stream_k_sums(sgemm_handle_t h, int mode);
  * SGEMM_ERR_INVALID_VALUE outside 0..8. */
 int sgemm_debug_set_cluster_split(sgemm_handle_t h, int ksplit);
 
+/* Test hook: the token tile of later int8 products on the tensor cores
+ * (SGEMM_VARIANT_TC_I8) and the CTAs that share a tile's K range.  0, 0 (the default):
+ * the library's choice.  tokens 16, 32 or 64 with ksplit 1, 2, 4 or 8 (taken down to
+ * the 128-wide steps that K has), or tokens 128 or 256 (CTA pairs) with ksplit 1.  Every
+ * one of them gives the same bits.  SGEMM_ERR_INVALID_VALUE otherwise. */
+int sgemm_debug_set_int8_tile(sgemm_handle_t h, int tokens, int ksplit);
+
 /* Test hook: the number of stream-K CTAs of later calls' stream-K plans (the
  * last wave of the whole-tile variants, and the 64 x 64 split variant); 0 (the
  * default): the library's choice.  The count is kept within what a plan
