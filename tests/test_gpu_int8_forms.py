@@ -61,3 +61,59 @@ def test_few_tokens_where_b_may_not_be_copied(handle, pinned, M, N, K, variant):
     p.check(first)
     pinned(V.VARIANT_GENERIC_I8)
     assert torch.equal(p.run(handle), first)
+
+
+# ---- B stored K x N past 2^31 elements ---------------------------------------------
+@pytest.mark.parametrize("variant", [V.VARIANT_TC_I8, V.VARIANT_GENERIC_I8])
+@pytest.mark.parametrize("off", [0, 1])
+def test_a_k_by_n_matrix_with_far_rows(handle, pinned, variant, off):  # noqa: F811
+    """Rows of B 2^19 bytes apart, the last ones past 2^31: copied, or read in place."""
+    M, N, K, ldb = 20, 72, 4200, (1 << 19) + off
+    g = torch.Generator(device="cuda").manual_seed(40)
+    B = torch.randint(-127, 128, ((K - 1) * ldb + N,), dtype=torch.int8, device="cuda", generator=g)
+    b = B.as_strided((K, N), (ldb, 1)).double()
+    A = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    sa, sb, C = torch.ones(M, device="cuda"), torch.ones(N, device="cuda"), torch.zeros(M, N, device="cuda")
+    pinned(variant)
+    sgemm.sgemm_run_int8(handle, 0, V.IN_F32, M, N, K, A, K, sa, B, ldb, sb, None, C, N)
+    torch.cuda.synchronize()
+    assert sgemm.sgemm_last_variant(handle)[0] == variant
+    assert sgemm.sgemm_last_relayout(handle) == (2 if variant == V.VARIANT_TC_I8 else 0)
+    assert torch.equal(C, (A.double() @ b).float())
+
+
+@pytest.mark.parametrize("variant", [V.VARIANT_TC_I8, V.VARIANT_GENERIC_I8])
+def test_far_experts_with_k_by_n_matrices(handle, pinned, variant):  # noqa: F811
+    """Experts' matrices 2^28 bytes apart: copied a small piece of each, or read in place."""
+    E, N, K, stride, rows = 10, 130, 200, 1 << 28, 40
+    g = torch.Generator(device="cuda").manual_seed(41)
+    B = torch.randint(-127, 128, ((E - 1) * stride + K * N,), dtype=torch.int8, device="cuda", generator=g)
+    A = torch.randint(-127, 128, (rows, K), dtype=torch.int8, device="cuda", generator=g)
+    offsets = torch.tensor([0, 3, 3, 10, 11, 11, 11, 20, 20, 25, 40], dtype=torch.int32, device="cuda")
+    sa, sb = torch.ones(rows, device="cuda"), torch.ones(E, N, device="cuda")
+    C = torch.zeros(rows, N, device="cuda")
+    pinned(variant)
+    sgemm.sgemm_run_int8_experts(handle, 0, V.IN_F32, E, rows, N, K, offsets, A, K, sa, B, N, stride, sb, None, C, N)
+    torch.cuda.synchronize()
+    assert sgemm.sgemm_last_variant(handle)[0] == variant
+    at = offsets.tolist()
+    for e in range(E):
+        b = B[e * stride:e * stride + K * N].view(K, N).double()
+        assert torch.equal(C[at[e]:at[e + 1]], (A[at[e]:at[e + 1]].double() @ b).float())
+
+
+def test_experts_beyond_the_workspace(handle):  # noqa: F811
+    """K x N matrices whose copies do not fit: the generic kernel, offsets past 2^31."""
+    E, N, K, rows = 9, 1 << 15, 8192, 6
+    g = torch.Generator(device="cuda").manual_seed(42)
+    B = torch.randint(-127, 128, (E, K, N), dtype=torch.int8, device="cuda", generator=g)
+    A = torch.randint(-127, 128, (rows, K), dtype=torch.int8, device="cuda", generator=g)
+    offsets = torch.tensor([0] * (E - 1) + [2, rows], dtype=torch.int32, device="cuda")
+    sa, sb = torch.ones(rows, device="cuda"), torch.ones(E, N, device="cuda")
+    C = torch.zeros(rows, N, device="cuda")
+    sgemm.sgemm_run_int8_experts(handle, 0, V.IN_F32, E, rows, N, K, offsets, A, K, sa, B, N, N * K, sb, None, C, N)
+    torch.cuda.synchronize()
+    assert sgemm.sgemm_last_variant(handle)[0] == V.VARIANT_GENERIC_I8
+    at = torch.tensor([0, 1, 777, N - 2, N - 1], device="cuda")
+    for e, lo, hi in [(E - 2, 0, 2), (E - 1, 2, rows)]:
+        assert torch.equal(C[lo:hi, at], (A[lo:hi].double() @ B[e][:, at].double()).float())
