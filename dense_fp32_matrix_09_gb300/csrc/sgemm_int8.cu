@@ -71,8 +71,12 @@
 //    as the TMA can read it (stored K x N, or not on 16-byte boundaries).
 // Every wait is bounded; on a timeout the kernel records it, waits (bounded)
 // for its own copies and MMAs in flight, frees the tensor memory and returns.
-// Plain loads go past L1 (ld.global.cg): what they read may have been written by
-// the kernel before, whose end the launch overlaps.
+// No load is a read-only-cache load (ld.global.nc): what is read may have been
+// written by the kernel before, whose end the launch overlaps.  Other loads are in
+// order after the wait for that kernel.  16-byte pieces of rows and what a thread alone
+// reads go past L1 (ld.global.cg); words and bytes whose sectors neighbouring threads
+// read too do not (B 8191 x 8191 stored K x N, 16 tokens 61 us instead of 69; one token x
+// 8190 x 8190 on the CUDA cores 17.0 instead of 20.1).
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -181,23 +185,36 @@ __device__ __forceinline__ Bytes matrix_of(const int8_t *p, long long rows, long
     return Bytes{p, p + (rows - 1) * ld + K};
 }
 
-// Four bytes on any alignment.
-__device__ __forceinline__ uint32_t load_word(const int8_t *p, const Bytes &all) {
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
-    const int8_t *q = p - off;
-    if (q >= all.lo && q + (off ? 8 : 4) <= all.hi) {
-        const uint32_t w0 = __ldcg(reinterpret_cast<const uint32_t *>(q));
-        const uint32_t w1 = off ? __ldcg(reinterpret_cast<const uint32_t *>(q) + 1) : 0u;
-        return __funnelshift_r(w0, w1, 8 * off);
-    }
-    uint32_t w = 0;
-    for (int i = 0; i < 4; ++i)
-        if (p + i < all.hi) w |= static_cast<uint32_t>(static_cast<uint8_t>(__ldcg(p + i))) << (8 * i);
+// Four bytes on any alignment in two steps, so that a thread's loads are all in
+// flight before the first is used: the two words that they lie in (`some`: where the
+// bytes exist at all), then the bytes -- read one by one at the matrix's own ends,
+// where a word would reach over them.
+struct Word {
+    uint32_t lo, hi, off;
+    bool whole;
+};
+__device__ __forceinline__ Word ask_word(const int8_t *p, bool some, const Bytes &all) {
+    Word w;
+    w.off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+    const int8_t *q = p - w.off;
+    w.whole = some && q >= all.lo && q + (w.off ? 8 : 4) <= all.hi;
+    w.lo = w.whole ? reinterpret_cast<const uint32_t *>(q)[0] : 0u;
+    w.hi = w.whole && w.off ? reinterpret_cast<const uint32_t *>(q)[1] : 0u;
     return w;
+}
+__device__ __forceinline__ uint32_t take_word(const Word &w, const int8_t *p, bool some, const Bytes &all) {
+    uint32_t v = __funnelshift_r(w.lo, w.hi, 8 * w.off);
+    if (some && !w.whole)
+        for (int i = 0; i < 4; ++i)
+            if (p + i < all.hi) v |= static_cast<uint32_t>(static_cast<uint8_t>(p[i])) << (8 * i);
+    return v;
 }
 
 // ---- generic kernel -----------------------------------------------------------
-// 64 x 64 tile of C, 64 k a step as 16 packed words a row, 4 x 4 sums a thread.
+// 64 x 64 tile of C, 64 k a step as 16 packed words a row, 4 x 4 sums a thread.  Bound
+// by the latency of a step's loads, which are all in flight at once: 64 tokens x 1000 x
+// 1000 26 us (with a branch around each load 46), x 8192 x 8192 182 (344), stored K x N
+// 328 (413).
 constexpr int kGTile = 64, kGWords = 16;
 
 // The largest of offsets[0 .. e], kept within the rows there are: expert e's first
@@ -232,30 +249,35 @@ __global__ void __launch_bounds__(256) int8_generic_kernel(const Int8Args a) {
         for (int m0 = lo + static_cast<int>(blockIdx.y) * kGTile; m0 < hi; m0 += static_cast<int>(gridDim.y) * kGTile) {
             int acc[4][4] = {};
             for (int k0 = 0; k0 < a.K; k0 += 4 * kGWords) {
+                Word wa[4], wb[4];
+                uint32_t kn[4] = {};  // B stored K x N: four rows' bytes
+                auto each = [&](auto f) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int at = tid + r * 256, w = at % kGWords, i = at / kGWords;
+                    for (int r = 0; r < 4; ++r) {
+                        const int at = tid + r * 256, w = at % kGWords, i = at / kGWords, k = k0 + 4 * w;
+                        f(r, w, i, k, a.A + static_cast<long long>(m0 + i) * a.lda + k, k < a.K && m0 + i < hi,
+                          B + static_cast<long long>(n0 + i) * a.ldb + k, k < a.K && n0 + i < a.N);
+                    }
+                };
+                each([&](int r, int, int i, int k, const int8_t *pa, bool some_a, const int8_t *pb, bool some_b) {
+                    wa[r] = ask_word(pa, some_a, all_a);
+                    if (a.transB) {
+                        wb[r] = ask_word(pb, some_b, all_b);
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (k + b < a.K && some_b)
+                                kn[r] |= static_cast<uint32_t>(static_cast<uint8_t>(
+                                             B[static_cast<long long>(k + b) * a.ldb + n0 + i])) << (8 * b);
+                    }
+                });
+                each([&](int r, int w, int i, int k, const int8_t *pa, bool some_a, const int8_t *pb, bool some_b) {
                     // (A's bytes from K on are zeros, so that B's may be any)
-                    unsigned av = 0, bv = 0;
-                    const int k = k0 + 4 * w;
-                    if (k < a.K && m0 + i < hi) {
-                        av = load_word(a.A + static_cast<long long>(m0 + i) * a.lda + k, all_a);
-                        if (a.K - k < 4) av &= (1u << (8 * (a.K - k))) - 1u;
-                    }
-                    if (k < a.K && n0 + i < a.N) {
-                        if (a.transB) {
-                            bv = load_word(B + static_cast<long long>(n0 + i) * a.ldb + k, all_b);
-                        } else {
-#pragma unroll
-                            for (int b = 0; b < 4; ++b)
-                                if (k + b < a.K)
-                                    bv |= static_cast<unsigned>(static_cast<uint8_t>(__ldcg(B + static_cast<long long>(k + b) * a.ldb + n0 + i)))
-                                          << (8 * b);
-                        }
-                    }
+                    uint32_t av = take_word(wa[r], pa, some_a, all_a);
+                    if (a.K - k < 4) av &= k < a.K ? (1u << (8 * (a.K - k))) - 1u : 0u;
                     As[w][i] = static_cast<int>(av);
-                    Bs[w][i] = static_cast<int>(bv);
-                }
+                    Bs[w][i] = static_cast<int>(a.transB ? take_word(wb[r], pb, some_b, all_b) : kn[r]);
+                });
                 __syncthreads();
 #pragma unroll
                 for (int w = 0; w < kGWords; ++w) {
@@ -324,13 +346,13 @@ __device__ __forceinline__ uint4 load_int8x16(const int8_t *row, int k, int K, b
     if (p - off >= all.lo && p - off + 20 <= all.hi) {
         const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
 #pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = __ldcg(q + i);
+        for (int i = 0; i < 5; ++i) w[i] = __ldca(q + i);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * off);
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (k + i < K) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldcg(p + i))) << (8 * (i % 4));
+            if (k + i < K) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldca(p + i))) << (8 * (i % 4));
     }
     return zeros_from(make_uint4(w[0], w[1], w[2], w[3]), K - k);
 }
@@ -356,10 +378,10 @@ __device__ __forceinline__ uint4 load_chunk(const int8_t *row, int k, int K, con
     for (int i = 0; i < 4; ++i) {
         const int8_t *q = p + 4 * i;
         const bool whole = q >= all.lo && q + 4 <= all.hi;
-        w[i] = whole ? __ldcg(reinterpret_cast<const uint32_t *>(q)) : 0u;
+        w[i] = whole ? __ldca(reinterpret_cast<const uint32_t *>(q)) : 0u;
         if (!whole && q + 4 > all.lo && q < all.hi)  // a word that an end is in
             for (int b = 0; b < 4; ++b)
-                if (q + b >= all.lo && q + b < all.hi) w[i] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldcg(q + b))) << (8 * b);
+                if (q + b >= all.lo && q + b < all.hi) w[i] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldca(q + b))) << (8 * b);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -494,13 +516,13 @@ __device__ __forceinline__ void transpose(const Int8Copies &c, int block, int bl
             uint32_t v = 0;
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-                if (n + b < c.N) v |= static_cast<uint32_t>(static_cast<uint8_t>(__ldcg(p + b))) << (8 * b);
+                if (n + b < c.N) v |= static_cast<uint32_t>(static_cast<uint8_t>(__ldca(p + b))) << (8 * b);
             return v;
         };
         each([&](int h, int j, int n, const int8_t *p, uint32_t off, bool some, bool whole) {
             const uint32_t *q = reinterpret_cast<const uint32_t *>(p - off);
-            w[h][j] = whole ? __ldcg(q) : WORDS && some ? bytes(p, n) : 0u;
-            next[h][j] = !WORDS && whole && off ? __ldcg(q + 1) : 0u;
+            w[h][j] = whole ? (WORDS ? __ldcg(q) : __ldca(q)) : WORDS && some ? bytes(p, n) : 0u;
+            next[h][j] = !WORDS && whole && off ? __ldca(q + 1) : 0u;
             ends |= !WORDS && some && !whole;
         });
         if (!WORDS)
@@ -556,9 +578,9 @@ __global__ void __launch_bounds__(256, WORDS ? 5 : 4) int8_copies_kernel(const I
 // against the tokens' rows in shared memory; warps of a CTA may share a channel's
 // K range (`split`).  One launch, no copies (B on any alignment), no cluster: a
 // step of one or a few tokens is made of the launch and one latency of HBM, and
-// for so few sums dp4a's rate does not show.  One token x 4096 x 4096 4.8 us (on the
-// tensor cores 7.6), x 8192 x 8192 13.7 (15.8; 4.9 TB/s), x 8190 x 8190 20.7 (36, with
-// B's copy); 4 tokens 6.9, 17.9, 30.4; 8 tokens 11.6 or more: choose_few in
+// for so few sums dp4a's rate does not show.  One token x 4096 x 4096 4.9 us (on the
+// tensor cores 6.8), x 8192 x 8192 13.5 (14.8; 5.0 TB/s), x 8190 x 8190 17.0 (36.7, with
+// B's copy); 4 tokens 6.8, 18.4, 24.5; 8 tokens 11.3 or more: choose_few in
 // sgemm_ops_api.cu says which kernel runs.
 constexpr int kFewThreads = 256;
 

@@ -102,24 +102,27 @@ TileChoice choose_tile(int rows, int experts, int N, int K, int num_sms, bool di
 // Whether the kernel for few tokens beats the tensor cores' `tc_us` (by the same
 // kind of model; B's copy, which only they need, counted): a launch, B at the rate
 // that a warp's arithmetic leaves (lower on rows that have to be shifted), and
-// the tokens' way into shared memory.  E.g. one token 4.8 us against 7.6 (4096 x 4096),
-// 4 tokens 17.9 against 15.8 (8192 x 8192) and 4.2 against 6.9 (700 x 700), 8 tokens 11.6
-// against 7.7 and 5.5 against 6.9.
+// the tokens' way into shared memory.  E.g. one token 4.9 us against 6.8 (4096 x 4096),
+// 17.0 against 36.7 (8190 x 8190, rows on no boundary), 4 tokens 18.4 against 14.7 (8192 x
+// 8192) and 2.7 against 6.1 (700 x 701), 8 tokens 11.3 against 6.9 and 3.0 against 6.1.
+// (Eight tokens on shifted rows take 0.42 to 0.65 us a MB; 0.9 makes up for what `tc_us`
+// overestimates there: 8 x 4096 x 4097 15.4 us against 13.9, x 2048 x 2049 8.5 against 8.4.)
 bool choose_few(int rows, int N, int K, bool b_aligned, double tc_us) {
-    constexpr double kAligned[] = {0.14, 0.17, 0.23, 0.43}, kShifted[] = {0.27, 0.33, 0.41, 0.75};  // us a MB
+    constexpr double kAligned[] = {0.14, 0.17, 0.23, 0.43}, kShifted[] = {0.205, 0.23, 0.3, 0.9};  // us a MB
     const int i = rows <= 1 ? 0 : rows <= 2 ? 1 : rows <= 4 ? 2 : 3;
     const double mb = 1e-6 * N * K;
-    const double few = b_aligned ? 2.9 + kAligned[i] * mb : 4.0 + kShifted[i] * mb;
+    const double few = 2.9 + (b_aligned ? kAligned[i] : kShifted[i]) * mb;
     return few + 5e-5 * rows * K < tc_us + (b_aligned ? 0.0 : 2.0 + 0.28 * mb);
 }
 
 // Whether the kernel for few tokens beats the generic one, where the tensor cores
 // cannot run (B needs a copy that it may not or cannot have).  The generic kernel takes
-// 1.9 us for every 64 of K and reads 64 rows whatever the tokens: 1 token x 4096 x 4097
-// 128 us against 9.2, 8 tokens x 700 x 701 23 against 3.9, 8 x 4000 x 17 4.1 against 3.2.
+// 1.4 us for every 64 of K and computes 64 rows whatever the tokens: 1 token x 4096 x 4097
+// 91 us against 6.1, 8 tokens x 700 x 701 17 against 3.1, 4 x 16384 x 129 8.7 against 6.2.
 // On a short K its tiles are the better use of a wave, where channels make many: 8 x
-// 30000 x 17 6.7 against 17, 1 x 100000 x 129 34 against 38 (257: 53 against 45).
-bool few_beats_generic(int N, int K) { return N <= 8192 || K > 256; }
+// 30000 x 17 7.6 us against 15.5, 4 x 16384 x 17 4.4 against 6.1 (8 x 100000 x 129 42
+// against 49; one to four tokens 42 against 26 to 30).
+bool few_beats_generic(int N, int K) { return N <= 8192 || K > 128; }
 
 int check_int8(int transB, int out_type, int experts, int rows, int N, int K, const int *offsets, bool grouped,
                const int8_t *A, int lda, const float *scaleA, const int8_t *B, int ldb, long long strideB,
