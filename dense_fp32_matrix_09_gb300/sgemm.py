@@ -541,17 +541,21 @@ def _ld(t) -> int:
     return max(t.stride(0), t.shape[1], 1)
 
 
+def _current_device() -> int:
+    if _raw_stream is not None:         # (the call beneath torch.cuda.current_device())
+        return _raw_stream[1]()
+    import torch
+    return torch.cuda.current_device()
+
+
 def _on_device(**tensors) -> None:
     """Every tensor (None: not given) is on the current CUDA device, whose addresses
     the kernels can use."""
+    current = _current_device()
     for name, t in tensors.items():
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must be on the GPU, got {t.device}")
-    import torch
-    current = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != current:
-            raise ValueError(f"{name} must be on the current device (cuda:{current}), got {t.device}")
+        if t is not None and t.get_device() != current:   # (-1 on the host)
+            raise ValueError(f"{name} must be on the current device (cuda:{current}), got {t.device}" if t.is_cuda else
+                             f"{name} must be on the GPU, got {t.device}")
 
 
 def _rows_of(name, t, dtype=None) -> None:
