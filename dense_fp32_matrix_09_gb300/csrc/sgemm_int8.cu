@@ -491,8 +491,8 @@ __device__ __forceinline__ void transpose(const Int8Copies &c, int block, int bl
         // two words that they lie in, read whole.  What is beyond the row goes to
         // channels that do not exist; only at the matrix's own ends (rows on word
         // boundaries: at theirs) the bytes are read one by one.  (Byte by byte at every
-        // row's ends: 40 x 133 x 266 7.9 us instead of 6.5, 1000 x 1500 x 777 15.1
-        // instead of 14.1.)
+        // row's ends: 40 x 133 x 266 7.9 us instead of 6.1, 1000 x 1500 x 777 15.1
+        // instead of 14.4.)
         const Bytes all = matrix_of(src, c.K, c.ldb, c.N);
         uint32_t w[2][4];
         uint32_t next[2][4];
