@@ -618,7 +618,13 @@ def _result(out, M, N, out_dtype, device):
 
 
 class Sgemm:
-    """A handle as a context manager: ``with Sgemm() as g: g.run(...)``."""
+    """A handle as a context manager: ``with Sgemm() as g: g.run(...)``.
+
+    The methods on torch tensors enqueue on `stream` (None: torch's current one).
+    Those that return new tensors make them there, as torch does under
+    ``torch.cuda.stream(stream)``: the inputs have to be ready on that stream, and
+    another stream that uses the results has to wait for it.
+    """
 
     def __init__(self, variant: int = VARIANT_AUTO):
         self.h = sgemm_create()
@@ -642,10 +648,7 @@ class Sgemm:
         return C
 
     # -- 8-bit products and expert routing on torch tensors: devices, shapes and
-    #    types are checked here, results are new tensors on the inputs' device.  They are made
-    #    on `stream` (None: the current one) like torch's own under
-    #    torch.cuda.stream(stream): the inputs have to be ready there, and another
-    #    stream that uses the results has to wait for it ----------------------------
+    #    types are checked here, results are new tensors on the inputs' device ------
     def quantize(self, X, stream=None):
         """(Q, scale): the rows of X (2-D, FP32/BF16/FP16) in int8 and their FP32 scales."""
         import torch
