@@ -316,4 +316,104 @@ cudaError_t int8_prepare();
 cudaError_t launch_int8_tc(const Int8Args &a, const CUtensorMap &tmB, const CUtensorMap &tmA, int num_sms,
                            int smem_override, cudaStream_t stream);
 
+// ---- RMS norm, rows to 4 bits and back (sgemm_norm.cu, sgemm_norm_grad.cu) ---------
+// One call's arguments after validation.  Rows of K elements: X (and R, added to it,
+// the sum written to H; NULL: none), weights W.  Y: the result's rows, in 4 bits ldy
+// bytes apart, with S their scales (words: fp4_words of them a row).
+struct RowArgs {
+    const void *X;
+    long long ldx;
+    const void *R;
+    long long ldr;
+    const void *W;
+    float eps;
+    void *H;
+    long long ldh;
+    int M, K;
+    void *Y;
+    long long ldy;
+    float *row;  // 1 / rms, or the rows' scales (NULL: not wanted)
+    uint8_t *S;
+    int format, words;
+    int vec;     // set by the launch: the result's rows may be written in units
+};
+enum class RowOut { kSame, kInt8, kFp4 };
+cudaError_t launch_rms_norm(int type, RowOut out, const RowArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_quantize_fp4(int type, const RowArgs &a, int num_sms, cudaStream_t stream);
+// X: the 4-bit rows (ldx in bytes), Y: the result.
+cudaError_t launch_dequantize_fp4(int type, const RowArgs &a, int num_sms, cudaStream_t stream);
+
+// Elements of a row that the threads of a block hold in registers.
+constexpr int kNormHeld = 512 * 32;
+struct NormGradArgs {
+    const void *dY;
+    long long lddy;
+    const void *dH;  // NULL: none
+    long long lddh;
+    const void *H;
+    long long ldh;
+    const void *W;
+    const float *rstd;
+    int M, K;
+    void *dX;
+    long long lddx;
+    float *dW;
+    float *parts;  // workspace: as many rows of K as fit, at least one (kNormHeld: 16)
+};
+int norm_grad_launches(int K);
+cudaError_t launch_rms_norm_grad(int type, const NormGradArgs &a, int num_sms, size_t ws_floats, cudaStream_t stream);
+
+// ---- 4-bit products (sgemm_fp4.cu) ------------------------------------------------
+struct Fp4Args {
+    int M, N, K, format, words;
+    const uint8_t *A;
+    long long lda;
+    const uint8_t *SA;
+    const float *rowA;
+    const uint8_t *B;
+    long long ldb;
+    const uint8_t *SB;
+    const float *rowB;
+    const float *bias;
+    void *C;
+    long long ldc;
+    int out_type;
+    int *status;
+    // tensor-core kernels: token tile (256: CTA pairs), CTAs that share a tile's K range
+    int nt, ksplit;
+};
+// Operands: bytes, box 128 x 128 (A on tiles of nt < 128 tokens: 128 x nt), 128-byte
+// swizzle; scales: 32-bit words, rows of 128 of them, one for every word of a tile of
+// 128 rows, boxes of the words that a stage of 256 elements has.
+struct Fp4Maps {
+    CUtensorMap A, B, SA, SB;
+};
+constexpr int kFp4StageK = 256;
+cudaError_t fp4_prepare();
+cudaError_t launch_fp4_tc(const Fp4Args &a, const Fp4Maps &m, int num_sms, int smem_override, cudaStream_t stream);
+cudaError_t launch_fp4_generic(const Fp4Args &a, cudaStream_t stream);
+
+// ---- a whole expert layer for a few tokens (sgemm_expert_layer.cu) ------------------
+constexpr int kLayerTokens = 64, kLayerSlots = 1024;
+struct LayerArgs {
+    int tokens, choices, experts, width, hidden, gated;
+    const void *X;
+    long long ldx;
+    const int *ids;
+    const float *weights;
+    const int8_t *up;  // experts x up_rows x width
+    const float *up_scale;
+    const int8_t *down;  // experts x width x hidden
+    const float *down_scale;
+    void *out;
+    long long ldo;
+    uint16_t *h;  // workspace, layer_floats floats: the hidden rows in BF16 parts
+    // set by the launch
+    int hidden_ld;
+    long long up_rows, h_part;
+};
+size_t layer_floats(int type, int slots, int hidden);
+cudaError_t layer_prepare();
+cudaError_t launch_expert_layer(int type, LayerArgs a, int num_sms, cudaStream_t stream);
+
 }  // namespace sg

@@ -24,11 +24,12 @@ typedef int (*run_ex_fn)(void *, int, int, int, int, int, float, const float *, 
                          long long, float, float *, int, long long, int, void *);
 
 /* The int8 and expert calls: every argument between the handle and the stream
- * is an int (i), a long long (l) or a buffer (p), so one parser serves them
+ * is an int (i), a long long (l), a float (f) or a buffer (p), so one parser serves them
  * all and a function of each call's own type passes the values on. */
 typedef union {
     int i;
     long long l;
+    float f;
     void *p;
 } arg;
 #define KMAX_ARGS 18
@@ -73,6 +74,45 @@ static int d_combine_grad(void *fn, void *h, const arg *v, void *s) {
                                                       v[7].i, v[8].p, v[9].p, v[10].p, v[11].i, v[12].p, s);
 }
 
+static int d_quantize_fp4(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, const void *, int, void *, int, void *, void *, void *))fn)(
+        h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].p, v[5].i, v[6].p, v[7].i, v[8].p, v[9].p, s);
+}
+static int d_dequantize_fp4(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, const void *, int, const void *, const void *, void *, int, void *))fn)(
+        h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].p, v[5].i, v[6].p, v[7].p, v[8].p, v[9].i, s);
+}
+static int d_run_fp4(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, int, const void *, int, const void *, const void *, const void *, int,
+                     const void *, const void *, const void *, void *, int, void *))fn)(
+        h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].i, v[5].p, v[6].i, v[7].p, v[8].p, v[9].p, v[10].i, v[11].p, v[12].p,
+        v[13].p, v[14].p, v[15].i, s);
+}
+/* the norm to its own type and to 8 bits */
+static int d_rms_norm(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, const void *, int, const void *, int, const void *, float, void *, int,
+                     void *, int, void *, void *))fn)(h, v[0].i, v[1].i, v[2].i, v[3].p, v[4].i, v[5].p, v[6].i, v[7].p,
+                                                      v[8].f, v[9].p, v[10].i, v[11].p, v[12].i, v[13].p, s);
+}
+static int d_rms_norm_fp4(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, const void *, int, const void *, int, const void *, float, void *, int,
+                     void *, int, void *, void *, void *))fn)(h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].p, v[5].i, v[6].p,
+                                                              v[7].i, v[8].p, v[9].f, v[10].p, v[11].i, v[12].p, v[13].i,
+                                                              v[14].p, v[15].p, s);
+}
+static int d_rms_norm_grad(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, const void *, int, const void *, int, const void *, int, const void *,
+                     const void *, void *, int, void *, void *))fn)(h, v[0].i, v[1].i, v[2].i, v[3].p, v[4].i, v[5].p,
+                                                                    v[6].i, v[7].p, v[8].i, v[9].p, v[10].p, v[11].p,
+                                                                    v[12].i, v[13].p, s);
+}
+static int d_expert_layer(void *fn, void *h, const arg *v, void *s) {
+    return ((int (*)(void *, int, int, int, int, int, int, int, const void *, int, const void *, const void *,
+                     const void *, const void *, const void *, const void *, void *, int, void *))fn)(
+        h, v[0].i, v[1].i, v[2].i, v[3].i, v[4].i, v[5].i, v[6].i, v[7].p, v[8].i, v[9].p, v[10].p, v[11].p, v[12].p,
+        v[13].p, v[14].p, v[15].p, v[16].i, s);
+}
+
 static struct {
     const char *name, *kinds;
     dispatch_fn call;
@@ -87,6 +127,14 @@ static struct {
     {"sgemm_expert_dispatch_grad", "iiiipippi", d_move, NULL},
     {"sgemm_expert_combine", "iiiipipppi", d_combine, NULL},
     {"sgemm_expert_combine_grad", "iiiipipipppip", d_combine_grad, NULL},
+    {"sgemm_quantize_fp4", "iiiipipipp", d_quantize_fp4, NULL},
+    {"sgemm_dequantize_fp4", "iiiipipppi", d_dequantize_fp4, NULL},
+    {"sgemm_run_fp4", "iiiiipipppippppi", d_run_fp4, NULL},
+    {"sgemm_rms_norm", "iiipipipfpipip", d_rms_norm, NULL},
+    {"sgemm_rms_norm_int8", "iiipipipfpipip", d_rms_norm, NULL},
+    {"sgemm_rms_norm_fp4", "iiiipipipfpipipp", d_rms_norm_fp4, NULL},
+    {"sgemm_rms_norm_grad", "iiipipipipppip", d_rms_norm_grad, NULL},
+    {"sgemm_expert_layer_int8", "iiiiiiipipppppppi", d_expert_layer, NULL},
 };
 #define KCALLS ((int)(sizeof(g_calls) / sizeof(g_calls[0])))
 
@@ -280,7 +328,10 @@ static PyObject *py_enqueue(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     if (as_handle(a[1], &h)) return NULL;
     for (Py_ssize_t k = 0; k < want; ++k) {
         PyObject *o = PyTuple_GET_ITEM(a[2], k);
-        const int bad = kinds[k] == 'i' ? as_int(o, &v[k].i) : kinds[k] == 'l' ? as_ll(o, &v[k].l) : as_ptr(o, &v[k].p);
+        const int bad = kinds[k] == 'i'   ? as_int(o, &v[k].i)
+                        : kinds[k] == 'l' ? as_ll(o, &v[k].l)
+                        : kinds[k] == 'f' ? as_float(o, &v[k].f)
+                                          : as_ptr(o, &v[k].p);
         if (bad) return NULL;
     }
     if (as_stream(a[3], &stream)) return NULL;

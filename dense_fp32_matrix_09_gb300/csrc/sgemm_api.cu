@@ -99,6 +99,7 @@ struct sgemm_ctx {
     int sk_ctas_pin;                        // test hook: stream-K CTAs of a tail or split-all plan (0 auto)
     int sk_gap_pin = -1;                    // test hook: boundary charge of stream-K splits (-1 auto)
     int i8_tokens, i8_split;                // test hook: token tile and K split of the int8 products (0 auto)
+    int f4_tokens, f4_split;                // and of the 4-bit products
     int ws_tiles_limit;                     // test hook: workspace capacity the kernels are told (0: real)
     cudaStream_t copy_in, copy_out;         // sgemm_run_host: host->device, device->host
     cudaEvent_t ev_start, ev_done;          //   ordering events (no timing)
@@ -745,7 +746,8 @@ CallPlan plan_call(const sgemm_ctx *h, int transA, int transB, int M, int N, int
     if (!tc_reachable && (variant == SGEMM_VARIANT_TC_3XTF32 || variant == SGEMM_VARIANT_TC_3XTF32_PAIR))
         variant = SGEMM_VARIANT_AUTO;
     if (variant == SGEMM_VARIANT_TC_F16_PAIR || variant == SGEMM_VARIANT_GENERIC_F16 ||
-        variant == SGEMM_VARIANT_TC_I8 || variant == SGEMM_VARIANT_GENERIC_I8 || variant == SGEMM_VARIANT_FEW_I8)
+        variant == SGEMM_VARIANT_TC_I8 || variant == SGEMM_VARIANT_GENERIC_I8 || variant == SGEMM_VARIANT_FEW_I8 ||
+        variant == SGEMM_VARIANT_TC_F4 || variant == SGEMM_VARIANT_TC_F4_PAIR || variant == SGEMM_VARIANT_GENERIC_F4)
         variant = SGEMM_VARIANT_AUTO;  // variants of the 16-bit and 8-bit calls only
     if (variant == SGEMM_VARIANT_AUTO) {
         // 3xTF32 mode: the CTA-pair tensor-core kernel once there are at least
@@ -848,7 +850,8 @@ bool is_live(sgemm_handle_t h) { return alive(h); }
 
 void view_of(sgemm_handle_t h, HandleView *v) {
     *v = HandleView{h->device, h->num_sms, h->d_status, h->d_ws, h->ws_floats, h->d_rl,
-                    h->rl_floats * sizeof(float), h->pinned, h->relayout_mode, h->smem_override, h->i8_tokens, h->i8_split};
+                    h->rl_floats * sizeof(float), h->pinned, h->relayout_mode, h->smem_override, h->i8_tokens, h->i8_split,
+                    h->f4_tokens, h->f4_split};
 }
 
 void record_call(sgemm_handle_t h, int variant, int splits, int launches, int copied) {
@@ -865,10 +868,14 @@ bool encode_map(CUtensorMap *map, MapType type, int dims, const void *base, long
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(plane_bytes)};
     cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    return g_encode(map, type == MapType::kInt8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+    return g_encode(map,
+                    type == MapType::kInt8  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                    : type == MapType::kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                            : CU_TENSOR_MAP_DATA_TYPE_UINT32,
                     static_cast<cuuint32_t>(dims), const_cast<void *>(base), dim, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    type == MapType::kWords ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace sg
@@ -912,6 +919,9 @@ const char *sgemm_variant_name(int v) {
         case SGEMM_VARIANT_TC_I8: return "tc_i8";
         case SGEMM_VARIANT_GENERIC_I8: return "generic_i8";
         case SGEMM_VARIANT_FEW_I8: return "few_i8";
+        case SGEMM_VARIANT_TC_F4: return "tc_f4";
+        case SGEMM_VARIANT_TC_F4_PAIR: return "tc_f4_pair";
+        case SGEMM_VARIANT_GENERIC_F4: return "generic_f4";
         default: return "unknown";
     }
 }
@@ -973,7 +983,8 @@ int sgemm_create(sgemm_handle_t *out) {
         if (occupancy[v] < 1) return SGEMM_ERR_CUDA;
     }
     if (sg::tc3x_prepare() != cudaSuccess || sg::tc3x_pair_prepare() != cudaSuccess ||
-        sg::tc16_prepare() != cudaSuccess || sg::int8_prepare() != cudaSuccess || sg::sort_prepare() != cudaSuccess)
+        sg::tc16_prepare() != cudaSuccess || sg::int8_prepare() != cudaSuccess || sg::sort_prepare() != cudaSuccess ||
+        sg::fp4_prepare() != cudaSuccess || sg::layer_prepare() != cudaSuccess)
         return SGEMM_ERR_CUDA;
     occupancy[SGEMM_VARIANT_TC_3XTF32] = 1;
     occupancy[SGEMM_VARIANT_TC_3XTF32_PAIR] = 1;
@@ -1137,6 +1148,16 @@ int sgemm_debug_set_int8_tile(sgemm_handle_t h, int tokens, int ksplit) {
     if (!direct && !pair && (tokens != 0 || ksplit != 0)) return SGEMM_ERR_INVALID_VALUE;
     h->i8_tokens = tokens;
     h->i8_split = ksplit;
+    return SGEMM_OK;
+}
+
+int sgemm_debug_set_fp4_tile(sgemm_handle_t h, int tokens, int ksplit) {
+    if (!alive(h)) return SGEMM_ERR_BAD_HANDLE;
+    const bool tile = (tokens == 16 || tokens == 32 || tokens == 64 || tokens == 128) &&
+                      (ksplit == 1 || ksplit == 2 || ksplit == 4 || ksplit == 8);
+    if (!tile && !(tokens == 256 && ksplit == 1) && (tokens != 0 || ksplit != 0)) return SGEMM_ERR_INVALID_VALUE;
+    h->f4_tokens = tokens;
+    h->f4_split = ksplit;
     return SGEMM_OK;
 }
 

@@ -1,0 +1,243 @@
+// The gradient of the RMS norm for sm_103a.  With y = h r w, r = 1 / sqrt(mean(h^2)
+// + eps) and g = w dy, row by row
+//     dh_p = r g_p - h_p r^3 (sum_q g_q h_q) / K  (+ the gradient that reaches h from elsewhere)
+//     dw_p = sum over the rows of dy_p h_p r
+//
+//  * norm_grad_kernel -- each row's threads go through rows a grid apart: dy, h and
+//    what reaches h are read once and stay in registers for the row's sum and its
+//    gradient, the columns' sums in registers from row to row; at the end each group
+//    of threads writes its sums, a row of `parts`.
+//  * columns_kernel -- dw: the rows of `parts` added up.
+//  * norm_grad_wide_kernel, columns_wide_kernel -- the same for rows longer than the
+//    registers of 512 threads hold: each row is read twice, and the columns' sums are
+//    taken from dy and h by a kernel of their own.
+//
+// Every sum is in FP32 and in an order that only the sizes and the GPU's SM count set: no
+// atomics, the same bits every time.
+#include "device_common.cuh"
+#include "internal.h"
+#include "rows.cuh"
+#include "sgemm.h"
+
+namespace sg {
+namespace {
+
+// Sum over the TPR threads of a row; `part` has a float for each of the block's warps.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float sum, float *part) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = sum;
+        __syncthreads();
+        const int w0 = threadIdx.x / TPR * (TPR / 32);
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < TPR / 32; ++w) sum += part[w0 + w];
+    }
+    return sum;
+}
+
+template <int TPR>
+constexpr int kGradThreads = TPR < 256 ? 256 : TPR;
+
+template <class El, int TPR, int A, int HELD>
+__global__ void __launch_bounds__(kGradThreads<TPR>, TPR < 512 ? 2 : 1)
+norm_grad_kernel(const NormGradArgs a) {
+    using T = typename El::T;
+    constexpr int kRows = kGradThreads<TPR> / TPR;
+    __shared__ float part[2][kGradThreads<TPR> / 32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x % TPR, group = blockIdx.x * kRows + threadIdx.x / TPR;
+    const unsigned step = gridDim.x * kRows;
+    const T *w = static_cast<const T *>(a.W);
+    Pack8<T> g[HELD];
+    float dw[HELD][kV];
+#pragma unroll
+    for (int c = 0; c < HELD; ++c) {
+        g[c] = load8<T, TPR, A, true>(w, c, lane, a.K);
+#pragma unroll
+        for (int e = 0; e < kV; ++e) dw[c][e] = 0.f;
+    }
+    // (every group makes as many rounds as the first: the barriers are the block's)
+    int turn = 0;
+    for (unsigned i0 = blockIdx.x * kRows; i0 < static_cast<unsigned>(a.M); i0 += step, turn ^= 1) {
+        const unsigned i = i0 + threadIdx.x / TPR;
+        const bool live = i < static_cast<unsigned>(a.M);
+        const long long row = live ? i : 0;
+        const int width = live ? a.K : 0;
+        const T *dy = static_cast<const T *>(a.dY) + row * a.lddy, *h = static_cast<const T *>(a.H) + row * a.ldh;
+        Pack8<T> d[HELD], x[HELD], more[HELD];
+#pragma unroll
+        for (int c = 0; c < HELD; ++c) {
+            d[c] = load8<T, TPR, A>(dy, c, lane, width);
+            x[c] = load8<T, TPR, A>(h, c, lane, width);
+        }
+        const float r = live ? __ldca(a.rstd + i) : 0.f;
+        if (a.dH) {
+            const T *dh = static_cast<const T *>(a.dH) + row * a.lddh;
+#pragma unroll
+            for (int c = 0; c < HELD; ++c) more[c] = load8<T, TPR, A>(dh, c, lane, width);
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < HELD; ++c)
+#pragma unroll
+            for (int e = 0; e < kV; ++e) sum = fmaf(El::up(d[c].v[e]) * El::up(g[c].v[e]), El::up(x[c].v[e]), sum);
+        sum = row_sum<TPR>(sum, part[turn]);
+        const float f = sum * r * r / static_cast<float>(a.K);
+        T *dx = static_cast<T *>(a.dX) + row * a.lddx;
+#pragma unroll
+        for (int c = 0; c < HELD; ++c) {
+            Pack8<T> o;
+#pragma unroll
+            for (int e = 0; e < kV; ++e) {
+                const float dv = El::up(d[c].v[e]), hv = El::up(x[c].v[e]);
+                // (lanes behind a row's end and rows behind the last hold zeros: nothing is added)
+                dw[c][e] = fmaf(dv, hv * r, dw[c][e]);
+                float v = r * fmaf(-hv, f, dv * El::up(g[c].v[e]));
+                if (a.dH) v += El::up(more[c].v[e]);
+                o.v[e] = El::down(v);
+            }
+            if (live) store8<T, TPR, A>(dx, c, lane, width, o);
+        }
+    }
+    float *to = a.parts + static_cast<long long>(group) * a.K;
+#pragma unroll
+    for (int c = 0; c < HELD; ++c) {
+        const int at = c * kV * TPR + lane * A;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) {
+            const int p = at + e / A * TPR * A + e % A;
+            if (p < a.K) to[p] = dw[c][e];
+        }
+    }
+}
+
+// dw[p] = sum of column p of `parts` (n rows): 32 columns a block, each warp's rows
+// 8 apart, then the warps' sums.
+__global__ void __launch_bounds__(1024) columns_kernel(const float *parts, int n, int K, float *dw) {
+    __shared__ float sums[32][33];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int p = blockIdx.x * 32 + lane;
+    float s[4] = {};
+    for (int i = warp; i < n; i += 128) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (p < K && i + 32 * j < n) s[j] += __ldcg(parts + static_cast<long long>(i + 32 * j) * K + p);
+    }
+    sums[warp][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+    __syncthreads();
+    // warp w adds up column w of this block's
+    float sum = sums[lane][warp];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0 && blockIdx.x * 32 + warp < K) dw[blockIdx.x * 32 + warp] = sum;
+}
+
+// Rows of any length: one block of 512 threads a row.
+template <class El>
+__global__ void __launch_bounds__(512) norm_grad_wide_kernel(const NormGradArgs a) {
+    using T = typename El::T;
+    __shared__ float part[16];
+    griddep_wait();
+    griddep_launch_dependents();
+    for (unsigned i = blockIdx.x; i < static_cast<unsigned>(a.M); i += gridDim.x) {
+        const T *dy = static_cast<const T *>(a.dY) + i * a.lddy, *h = static_cast<const T *>(a.H) + i * a.ldh;
+        const T *dh = a.dH ? static_cast<const T *>(a.dH) + i * a.lddh : nullptr, *w = static_cast<const T *>(a.W);
+        const float r = __ldca(a.rstd + i);
+        float sum = 0.f;
+        for (int p = threadIdx.x; p < a.K; p += 512)
+            sum = fmaf(El::up(__ldcg(dy + p)) * El::up(__ldca(w + p)), El::up(__ldcg(h + p)), sum);
+        sum = row_sum<512>(sum, part);
+        const float f = sum * r * r / static_cast<float>(a.K);
+        T *dx = static_cast<T *>(a.dX) + i * a.lddx;
+        for (int p = threadIdx.x; p < a.K; p += 512) {
+            float v = r * fmaf(-El::up(__ldcg(h + p)), f, El::up(__ldcg(dy + p)) * El::up(__ldca(w + p)));
+            if (dh) v += El::up(__ldcg(dh + p));
+            dx[p] = El::down(v);
+        }
+        __syncthreads();
+    }
+}
+
+// Column sums of dy h r over the rows blockIdx.y, blockIdx.y + gridDim.y, ...
+template <class El>
+__global__ void __launch_bounds__(256) columns_wide_kernel(const NormGradArgs a) {
+    using T = typename El::T;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int p = blockIdx.x * 256 + threadIdx.x;
+    if (p >= a.K) return;
+    float sum = 0.f;
+    for (unsigned i = blockIdx.y; i < static_cast<unsigned>(a.M); i += gridDim.y)
+        sum = fmaf(El::up(__ldcg(static_cast<const T *>(a.dY) + i * a.lddy + p)),
+                   El::up(__ldcg(static_cast<const T *>(a.H) + i * a.ldh + p)) * __ldca(a.rstd + i), sum);
+    a.parts[static_cast<long long>(blockIdx.y) * a.K + p] = sum;
+}
+
+cudaError_t add_parts(const NormGradArgs &a, int n, cudaStream_t stream) {
+    return launch_dependent(columns_kernel, dim3(blocks_of(a.K, 32)), dim3(1024), 0, stream, 1, static_cast<const float *>(a.parts), n, a.K, a.dW);
+}
+
+template <class El, int TPR, int A, int HELD>
+cudaError_t grad_typed(const NormGradArgs &a, int num_sms, size_t ws_floats, cudaStream_t stream) {
+    constexpr int kRows = kGradThreads<TPR> / TPR;
+    const size_t fit = ws_floats / (static_cast<size_t>(a.K) * kRows);  // blocks whose sums the workspace holds
+    size_t blocks = blocks_of(a.M, kRows);
+    blocks = blocks < static_cast<size_t>(2 * num_sms) ? blocks : static_cast<size_t>(2 * num_sms);
+    blocks = blocks < fit ? blocks : fit;
+    const cudaError_t e = launch_dependent(norm_grad_kernel<El, TPR, A, HELD>, dim3(static_cast<unsigned>(blocks)), dim3(kGradThreads<TPR>), 0, stream, 1, a);
+    return e != cudaSuccess ? e : add_parts(a, static_cast<int>(blocks) * kRows, stream);
+}
+
+template <class El, int A>
+cudaError_t grad_shared(const NormGradArgs &a, int num_sms, size_t ws_floats, cudaStream_t stream) {
+    // threads a row: 16 elements each where the rows are that long, 32 in the longest
+    if (a.K <= 256) return grad_typed<El, 32, A, 1>(a, num_sms, ws_floats, stream);
+    if (a.K <= 512) return grad_typed<El, 32, A, 2>(a, num_sms, ws_floats, stream);
+    if (a.K <= 2048) return grad_typed<El, 128, A, 2>(a, num_sms, ws_floats, stream);
+    if (a.K <= 4096) return grad_typed<El, 256, A, 2>(a, num_sms, ws_floats, stream);
+    if (a.K <= 8192) return grad_typed<El, 512, A, 2>(a, num_sms, ws_floats, stream);
+    return grad_typed<El, 512, A, 4>(a, num_sms, ws_floats, stream);
+}
+
+template <class El>
+cudaError_t grad_for(const NormGradArgs &a, int num_sms, size_t ws_floats, cudaStream_t stream) {
+    using T = typename El::T;
+    constexpr int V = 16 / sizeof(T);
+    if (a.K > kNormHeld) {
+        cudaError_t e = launch_dependent(norm_grad_wide_kernel<El>, dim3(a.M < 4 * num_sms ? a.M : 4 * num_sms), dim3(512), 0, stream, 1, a);
+        if (e != cudaSuccess) return e;
+        const size_t fit = ws_floats / a.K;  // at least one: checked where the call starts
+        const int most = a.M < 64 ? a.M : 64, n = fit < static_cast<size_t>(most) ? static_cast<int>(fit) : most;
+        e = launch_dependent(columns_wide_kernel<El>, dim3(blocks_of(a.K, 256), n), dim3(256), 0, stream, 1, a);
+        return e != cudaSuccess ? e : add_parts(a, n, stream);
+    }
+    auto unit = [](const void *p, long long ld, int n) {
+        return p == nullptr || (reinterpret_cast<uintptr_t>(p) % (n * sizeof(T)) == 0 && ld % n == 0);
+    };
+    auto fits = [&](int n) {
+        return a.K % n == 0 && unit(a.dY, a.lddy, n) && unit(a.H, a.ldh, n) && unit(a.dH, a.lddh, n) && unit(a.W, 0, n) && unit(a.dX, a.lddx, n);
+    };
+    if (fits(V)) return grad_shared<El, V>(a, num_sms, ws_floats, stream);
+    if (fits(2)) return grad_shared<El, 2>(a, num_sms, ws_floats, stream);
+    return grad_shared<El, 1>(a, num_sms, ws_floats, stream);
+}
+
+}  // namespace
+
+int norm_grad_launches(int K) { return K > kNormHeld ? 3 : 2; }
+
+cudaError_t launch_rms_norm_grad(int type, const NormGradArgs &a, int num_sms, size_t ws_floats, cudaStream_t stream) {
+    switch (type) {
+        case SGEMM_IN_F32: return grad_for<ElF32>(a, num_sms, ws_floats, stream);
+        case SGEMM_IN_BF16: return grad_for<ElBF16>(a, num_sms, ws_floats, stream);
+        default: return grad_for<ElF16>(a, num_sms, ws_floats, stream);
+    }
+}
+
+}  // namespace sg

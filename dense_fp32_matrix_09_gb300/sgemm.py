@@ -44,12 +44,17 @@ VARIANT_TMA_256x128 = 11
 VARIANT_TC_I8 = 12
 VARIANT_GENERIC_I8 = 13
 VARIANT_FEW_I8 = 14
-VARIANT_COUNT = 15
+VARIANT_TC_F4 = 15
+VARIANT_TC_F4_PAIR = 16
+VARIANT_GENERIC_F4 = 17
+VARIANT_COUNT = 18
 MATH_FP32 = 0
 MATH_3XTF32 = 1
 IN_F32 = 0
 IN_BF16 = 1
 IN_F16 = 2
+FP4_MX = 0
+FP4_NV = 1
 RELAYOUT_AUTO = 0
 RELAYOUT_OFF = 1
 RELAYOUT_ALWAYS = 2
@@ -71,7 +76,9 @@ EXPORTS = ("sgemm_create", "sgemm_run", "sgemm_check_args", "sgemm_destroy", "sg
            "sgemm_debug_set_workspace_limit", "sgemm_debug_set_int8_tile", "sgemm_run_int8", "sgemm_check_args_int8",
            "sgemm_run_int8_experts", "sgemm_check_args_int8_experts", "sgemm_quantize_rows", "sgemm_expert_sort",
            "sgemm_expert_dispatch", "sgemm_expert_dispatch_int8", "sgemm_expert_dispatch_grad",
-           "sgemm_expert_combine", "sgemm_expert_combine_grad")
+           "sgemm_expert_combine", "sgemm_expert_combine_grad", "sgemm_quantize_fp4", "sgemm_dequantize_fp4",
+           "sgemm_fp4_scale_bytes", "sgemm_run_fp4", "sgemm_check_args_fp4", "sgemm_rms_norm", "sgemm_rms_norm_int8",
+           "sgemm_rms_norm_fp4", "sgemm_rms_norm_grad", "sgemm_expert_layer_int8", "sgemm_debug_set_fp4_tile")
 
 
 class SgemmError(RuntimeError):
@@ -155,6 +162,21 @@ def lib() -> ctypes.CDLL:
         L.sgemm_expert_dispatch_grad.argtypes = [vp, i32, i32, i32, i32, vp, i32, vp, vp, i32, vp]
         L.sgemm_expert_combine.argtypes = [vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, i32, vp]
         L.sgemm_expert_combine_grad.argtypes = [vp, i32, i32, i32, i32, vp, i32, vp, i32, vp, vp, vp, i32, vp, vp]
+        L.sgemm_quantize_fp4.argtypes = [vp, i32, i32, i32, i32, vp, i32, vp, i32, vp, vp, vp]
+        L.sgemm_dequantize_fp4.argtypes = [vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, i32, vp]
+        L.sgemm_fp4_scale_bytes.argtypes = [i32, i32, i32]
+        L.sgemm_fp4_scale_bytes.restype = i64
+        fp4_args = [i32, i32, i32, i32, i32, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, i32]
+        L.sgemm_run_fp4.argtypes = [vp, *fp4_args, vp]
+        L.sgemm_check_args_fp4.argtypes = fp4_args
+        norm_in = [i32, i32, vp, i32, vp, i32, vp, f32, vp, i32]
+        L.sgemm_rms_norm.argtypes = [vp, i32, *norm_in, vp, i32, vp, vp]
+        L.sgemm_rms_norm_int8.argtypes = [vp, i32, *norm_in, vp, i32, vp, vp]
+        L.sgemm_rms_norm_fp4.argtypes = [vp, i32, i32, *norm_in, vp, i32, vp, vp, vp]
+        L.sgemm_rms_norm_grad.argtypes = [vp, i32, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, vp, i32, vp, vp]
+        L.sgemm_expert_layer_int8.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp,
+                                              vp, i32, vp]
+        L.sgemm_debug_set_fp4_tile.argtypes = [vp, i32, i32]
         _lib = L
     return _lib
 
@@ -349,7 +371,8 @@ def _enqueue(name: str, h, args, stream) -> None:
         rc = calls.enqueue(name, h, args, stream)
     else:
         fn = getattr(lib(), name)
-        values = [_ptr(a) if kind is ctypes.c_void_p else _integer(a, kind) for a, kind in zip(args, fn.argtypes[1:-1])]
+        values = [_ptr(a) if kind is ctypes.c_void_p else float(a) if kind is ctypes.c_float else _integer(a, kind)
+                  for a, kind in zip(args, fn.argtypes[1:-1])]
         rc = fn(h, *values, _stream(stream))
     if rc != OK:
         raise SgemmError(rc, name)
@@ -415,6 +438,59 @@ def sgemm_expert_combine_grad(h, in_type, tokens, choices, width, dout, lddo, Y,
     """dY[rows[t, j]] = weights[t, j] * dout[t]; dweights[t, j] = <dout[t], Y[rows[t, j]]>."""
     _enqueue("sgemm_expert_combine_grad", h, (in_type, tokens, choices, width, dout, lddo, Y, ldy, rows, weights,
                                               dY, lddy, dweights), stream)
+
+
+def sgemm_fp4_scale_bytes(fmt, rows, K) -> int:
+    """Bytes of the scales of `rows` rows of K elements in 4 bits (-1: unknown format, bad size)."""
+    return lib().sgemm_fp4_scale_bytes(int(fmt), int(rows), int(K))
+
+
+def sgemm_quantize_fp4(h, in_type, fmt, M, K, X, ldx, Q, ldq, S, row, stream=None) -> None:
+    """Q, S, row = the rows of X in 4-bit floating point with a scale a block (see include/sgemm.h)."""
+    _enqueue("sgemm_quantize_fp4", h, (in_type, fmt, M, K, X, ldx, Q, ldq, S, row), stream)
+
+
+def sgemm_dequantize_fp4(h, out_type, fmt, M, K, Q, ldq, S, row, Y, ldy, stream=None) -> None:
+    """Y = what the 4-bit rows stand for."""
+    _enqueue("sgemm_dequantize_fp4", h, (out_type, fmt, M, K, Q, ldq, S, row, Y, ldy), stream)
+
+
+def sgemm_run_fp4(h, fmt, out_type, M, N, K, A, lda, SA, rowA, B, ldb, SB, rowB, bias, C, ldc, stream=None) -> None:
+    """C = A @ B.T + bias for A and B in 4-bit floating point (see include/sgemm.h)."""
+    _enqueue("sgemm_run_fp4", h, (fmt, out_type, M, N, K, A, lda, SA, rowA, B, ldb, SB, rowB, bias, C, ldc), stream)
+
+
+def sgemm_check_args_fp4(fmt, out_type, M, N, K, A, lda, SA, rowA, B, ldb, SB, rowB, bias, C, ldc) -> int:
+    return lib().sgemm_check_args_fp4(int(fmt), int(out_type), int(M), int(N), int(K), _ptr(A), int(lda), _ptr(SA),
+                                      _ptr(rowA), _ptr(B), int(ldb), _ptr(SB), _ptr(rowB), _ptr(bias), _ptr(C), int(ldc))
+
+
+def sgemm_rms_norm(h, in_type, M, K, X, ldx, R, ldr, weight, eps, H, ldh, Y, ldy, rstd, stream=None) -> None:
+    """H = X + R; Y = H * weight / rms(H), rstd = 1 / rms (see include/sgemm.h)."""
+    _enqueue("sgemm_rms_norm", h, (in_type, M, K, X, ldx, R, ldr, weight, eps, H, ldh, Y, ldy, rstd), stream)
+
+
+def sgemm_rms_norm_int8(h, in_type, M, K, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, scale, stream=None) -> None:
+    """The same with the result in 8 bits and a scale a row."""
+    _enqueue("sgemm_rms_norm_int8", h, (in_type, M, K, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, scale), stream)
+
+
+def sgemm_rms_norm_fp4(h, in_type, fmt, M, K, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, S, row, stream=None) -> None:
+    """The same with the result in 4 bits, a scale a block and one a row."""
+    _enqueue("sgemm_rms_norm_fp4", h, (in_type, fmt, M, K, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, S, row), stream)
+
+
+def sgemm_rms_norm_grad(h, in_type, M, K, dY, lddy, dH, lddh, H, ldh, weight, rstd, dX, lddx, dweight, stream=None) -> None:
+    """dX and dweight of sgemm_rms_norm."""
+    _enqueue("sgemm_rms_norm_grad", h, (in_type, M, K, dY, lddy, dH, lddh, H, ldh, weight, rstd, dX, lddx, dweight),
+             stream)
+
+
+def sgemm_expert_layer_int8(h, in_type, gated, tokens, choices, experts, width, hidden, X, ldx, ids, weights, up,
+                            up_scale, down, down_scale, out, ldo, stream=None) -> None:
+    """out[t] = sum_j weights[t, j] * down_e(act(up_e(X[t]))) for a few tokens."""
+    _enqueue("sgemm_expert_layer_int8", h, (in_type, gated, tokens, choices, experts, width, hidden, X, ldx, ids,
+                                            weights, up, up_scale, down, down_scale, out, ldo), stream)
 
 
 def sgemm_debug_fma_probe(h, sink, ctas=0, iters=4096, stream=None) -> int:
@@ -520,6 +596,11 @@ def sgemm_debug_set_cluster_split(h, ksplit: int) -> None:
 def sgemm_debug_set_int8_tile(h, tokens: int, ksplit: int) -> None:
     """Token tile and K split of later int8 products on the tensor cores (test hook; 0, 0: the library's choice)."""
     _check(lib().sgemm_debug_set_int8_tile(h, int(tokens), int(ksplit)), "sgemm_debug_set_int8_tile")
+
+
+def sgemm_debug_set_fp4_tile(h, tokens: int, ksplit: int) -> None:
+    """Token tile and K split of later 4-bit products on the tensor cores (test hook; 0, 0: the library's choice)."""
+    _check(lib().sgemm_debug_set_fp4_tile(h, int(tokens), int(ksplit)), "sgemm_debug_set_fp4_tile")
 
 
 def sgemm_debug_set_stream_k_sums(h, mode: int) -> None:

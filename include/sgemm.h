@@ -111,7 +111,11 @@ typedef enum {
     SGEMM_VARIANT_GENERIC_I8 = 13,   /* the same calls: any layout and alignment, CUDA cores  */
     SGEMM_VARIANT_FEW_I8 = 14,       /* sgemm_run_int8 only: up to 8 rows of A, CUDA cores, B
                                         stored N x K on any alignment                         */
-    SGEMM_VARIANT_COUNT_ = 15
+    SGEMM_VARIANT_TC_F4 = 15,        /* sgemm_run_fp4 only: tensor cores with block scales, 128
+                                        channels x 16 to 128 tokens a CTA, K split over clusters */
+    SGEMM_VARIANT_TC_F4_PAIR = 16,   /* sgemm_run_fp4 only: the same on CTA pairs, 256 x 256     */
+    SGEMM_VARIANT_GENERIC_F4 = 17,   /* sgemm_run_fp4 only: any alignment, CUDA cores            */
+    SGEMM_VARIANT_COUNT_ = 18
     /* sgemm_run_ex: the TMA variants serve every (transA, transB) and any
      * batch up to 65535 when A and B are 16-byte aligned and lda, ldb (and,
      * for batch > 1, strideA, strideB) are multiples of 4, and operands that
@@ -172,6 +176,13 @@ typedef enum {
     SGEMM_RELAYOUT_OFF = 1,
     SGEMM_RELAYOUT_ALWAYS = 2
 } sgemm_relayout_t;
+
+/* Formats of rows in 4-bit floating point (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 with
+ * a sign) with a scale for every block of consecutive elements of a row. */
+typedef enum {
+    SGEMM_FP4_MX = 0,   /* blocks of 32, scales E8M0: 2^(byte - 127), 255 a NaN                */
+    SGEMM_FP4_NV = 1    /* blocks of 16, scales E4M3 (>= 0), and one FP32 scale a row          */
+} sgemm_fp4_t;
 
 /* Element type of A and B for sgemm_run_mixed (BF16 and FP16; C is always
  * FP32), of the rows that the quantization and expert calls read and write,
@@ -327,6 +338,109 @@ int sgemm_check_args_int8_experts(int transB, int out_type, int experts, int row
 int sgemm_quantize_rows(sgemm_handle_t h, int type, int M, int K, const void *X, int ldx, int8_t *Q, int ldq,
                         float *scale, void *stream);
 
+/* ---- rows in 4-bit floating point --------------------------------------------
+ *
+ * An element is row[i] * s[i][b] * q[i][p], b the block of p (sgemm_fp4_t; 32 or 16
+ * elements, the last of a row shorter where they do not divide K).
+ *   Q: two elements a byte, the even one in the low half; rows ldq >= ceil(K / 2)
+ *     BYTES apart, any alignment (multiples of 16 let the products read them in place).
+ *     The half byte behind an odd K is 0.
+ *   S: the scales in tiles of 128 rows x 4 blocks, sgemm_fp4_scale_bytes bytes, 16-byte
+ *     aligned.  With words = ceil(ceil(K / block) / 4), the scale of row i and block b is
+ *       S[((i / 128) * words + b / 4) * 512 + (i % 32) * 16 + (i / 32) % 4 * 4 + b % 4].
+ *     Scales of blocks behind a row's last within its last word are 0; those of rows
+ *     behind the last are not written and may hold anything.
+ *   row: one FP32 a row; required with SGEMM_FP4_NV, with SGEMM_FP4_MX NULL for ones.
+ * Buffers made elsewhere have to be laid out in the same way, the zeros included.
+ *
+ * sgemm_quantize_fp4 makes them from rows X of `type`.  Each step is correctly rounded
+ * in FP32, ties to even; m is the row's largest magnitude, m_b a block's:
+ *   MX: s = 2^e with e = floor(log2 m_b) - 2, at least -127 (a block of zeros: -127);
+ *       q = X / s to the nearest of the values, magnitudes above 6 to 6;
+ *       row (NULL allowed) = 1.  A block with an infinity or a NaN gets s = NaN, q = 0.
+ *   NV: row = m / 2688;  s = E4M3(m_b * (448 / m));  q = X * ((2688 / m) / s) likewise
+ *       (s = 0: q = 0).  A row with m < 2688 * 2^-126 (all zeros among them) gets row = 0,
+ *       s = 0, q = 0; a row with an infinity or a NaN row = NaN, s = 0, q = 0.
+ * Every product with a NaN scale is NaN.
+ * sgemm_dequantize_fp4 gives Y = row * s * q, rounded to FP32 and then to `type`.
+ *
+ * Checks, in order: handle, device, SGEMM_ERR_INVALID_VALUE (unknown type or format,
+ * negative size, M or K above 2^30, a leading dimension below its minimum), nothing
+ * is done when M == 0 or K == 0, SGEMM_ERR_NULL, SGEMM_ERR_INVALID_VALUE (alignment),
+ * SGEMM_ERR_ALIAS (an output overlaps another buffer). */
+int sgemm_quantize_fp4(sgemm_handle_t h, int type, int format, int M, int K, const void *X, int ldx, uint8_t *Q,
+                       int ldq, uint8_t *S, float *row, void *stream);
+int sgemm_dequantize_fp4(sgemm_handle_t h, int type, int format, int M, int K, const uint8_t *Q, int ldq,
+                         const uint8_t *S, const float *row, void *Y, int ldy, void *stream);
+
+/* Bytes of the scales of `rows` rows of K elements: whole tiles.  -1 for an unknown
+ * format or a size outside [0, 2^30].  Host only. */
+int64_t sgemm_fp4_scale_bytes(int format, int rows, int K);
+
+/*     C[i][j] = rowA[i] * rowB[j] * sum_p (sA q_A)[i][p] * (sB q_B)[j][p] + bias[j]
+ *
+ * for A (M tokens) and B (N channels, stored N x K) in the same 4-bit format, an optional
+ * FP32 bias a channel, and C (M x N) of type `out_type`.  lda and ldb in bytes, ldc in
+ * elements.  Products are exact, summed in FP32 by the tensor cores (not
+ * round-to-nearest, in an order that depends on the variant and the split; the same
+ * call gives the same bits every time); sum * rowB * rowA + bias is rounded to C's type.
+ * With SGEMM_FP4_MX either row scale may be NULL.  C is output only; K == 0 gives the bias.
+ *
+ * A and B are read in place where they are 16-byte aligned with rows multiples
+ * of 16 bytes apart, and otherwise first copied into the re-layout workspace
+ * (sgemm_last_relayout: bit 0 A, bit 1 B; one more launch for both).  Where the
+ * copies do not fit or SGEMM_RELAYOUT_OFF forbids them, or with SGEMM_VARIANT_GENERIC
+ * or _GENERIC_F4 pinned, the generic kernel runs.  SGEMM_VARIANT_TC_F4_PAIR may be pinned.
+ * sgemm_last_variant also reports the CTAs that share a tile's K range.
+ * Checks as for the 4-bit rows, nothing done when M == 0 or N == 0. */
+int sgemm_run_fp4(sgemm_handle_t h, int format, int out_type, int M, int N, int K, const uint8_t *A, int lda,
+                  const uint8_t *SA, const float *rowA, const uint8_t *B, int ldb, const uint8_t *SB,
+                  const float *rowB, const float *bias, void *C, int ldc, void *stream);
+
+/* Host-only validation of sgemm_run_fp4's arguments (same rules, no CUDA call). */
+int sgemm_check_args_fp4(int format, int out_type, int M, int N, int K, const uint8_t *A, int lda,
+                         const uint8_t *SA, const float *rowA, const uint8_t *B, int ldb, const uint8_t *SB,
+                         const float *rowB, const float *bias, const void *C, int ldc);
+
+/* ---- RMS norm ------------------------------------------------------------------
+ *
+ * Rows X (M x K) of `type`, weights (K) of the same type, eps >= 0:
+ *   H = X + R, rounded to `type`       (R NULL: H stands for X itself, and is written
+ *                                       where it is not NULL)
+ *   r = 1 / sqrt(sum_p H_p^2 / K + eps)
+ *   sgemm_rms_norm        Y = (H * r) * weight, and r to rstd (NULL: not wanted)
+ *   sgemm_rms_norm_int8   v = H * weight, m = max |v|:  Q = rint(v * (127 / m)),
+ *                         scale = m * r / 127
+ *   sgemm_rms_norm_fp4    v as by sgemm_quantize_fp4, the row scales times r (required
+ *                         with either format: with MX they are r)
+ * The quantized forms are the input of sgemm_run_int8 and sgemm_run_fp4; what v rounds to
+ * does not depend on r, so the integers and codes are the same whatever the order of
+ * a sum.  Special rows as by sgemm_quantize_rows and sgemm_quantize_fp4.  Sums are in FP32,
+ * in a fixed order; a row whose sum of squares overflows FP32 has r = 0.
+ *
+ * sgemm_rms_norm_grad, from dY, the gradient dH that reaches H from elsewhere (the
+ * residual's further way; NULL: none), H and rstd:
+ *   dX = r * (weight * dY) - H * r^3 / K * sum_p (weight dY H)_p + dH   (X's gradient and R's)
+ *   dweight_p = sum_i (dY * H * r)_ip                                    (FP32; M == 0: zeros)
+ * It adds up dweight in the handle's workspace: K up to 12582912.
+ *
+ * H may be X or R in place (same address, same leading dimension), and dX dH.
+ * Checks, in order: handle, device, SGEMM_ERR_INVALID_VALUE (sizes, type, format, leading
+ * dimensions, eps; K above 2^30, with 4 bits M too), nothing is done when M == 0 or K == 0,
+ * SGEMM_ERR_NULL (R without H among them), SGEMM_ERR_INVALID_VALUE (alignment to
+ * the element size, S to 16 bytes), SGEMM_ERR_ALIAS. */
+int sgemm_rms_norm(sgemm_handle_t h, int type, int M, int K, const void *X, int ldx, const void *R, int ldr,
+                   const void *weight, float eps, void *H, int ldh, void *Y, int ldy, float *rstd, void *stream);
+int sgemm_rms_norm_int8(sgemm_handle_t h, int type, int M, int K, const void *X, int ldx, const void *R, int ldr,
+                        const void *weight, float eps, void *H, int ldh, int8_t *Q, int ldq, float *scale,
+                        void *stream);
+int sgemm_rms_norm_fp4(sgemm_handle_t h, int type, int format, int M, int K, const void *X, int ldx, const void *R,
+                       int ldr, const void *weight, float eps, void *H, int ldh, uint8_t *Q, int ldq, uint8_t *S,
+                       float *row, void *stream);
+int sgemm_rms_norm_grad(sgemm_handle_t h, int type, int M, int K, const void *dY, int lddy, const void *dH, int lddh,
+                        const void *H, int ldh, const void *weight, const float *rstd, void *dX, int lddx,
+                        float *dweight, void *stream);
+
 /* ---- tokens to their experts and back ----------------------------------------
  *
  * A router gives each of `tokens` tokens `choices` experts: ids[t*choices + j].
@@ -378,6 +492,27 @@ int sgemm_expert_combine_grad(sgemm_handle_t h, int type, int tokens, int choice
                               int lddo, const void *Y, int ldy, const int *rows, const float *weights, void *dY,
                               int lddy, float *dweights, void *stream);
 
+/* A whole mixture-of-experts layer for a few tokens, in two launches:
+ *
+ *     out[t] = sum_j weights[t*choices + j] * D_e act(U_e X[t]),   e = ids[t*choices + j]
+ *
+ * with U_e = up_scale[e][f] * up[e][f][.] (rows x width, rows = hidden, with `gated`
+ * 2 * hidden) and D_e = down_scale[e][d] * down[e][d][.] (width x hidden) in int8,
+ * contiguous, as sgemm_run_int8_experts takes them (transB = 1).  act is silu(y) = y / (1 +
+ * exp(-y)), with `gated` silu(y[f]) * y[hidden + f].  Choices whose id is outside
+ * [0, experts) are left out, a token with none gets zeros; an expert that a token
+ * names twice counts with both weights.
+ *
+ * X is taken as it is (16 or 32 bits) and the products are summed in FP32; the hidden
+ * values keep 16 bits of fraction (24 with FP32 rows).  Only the experts that some
+ * token names are read.  tokens up to 64, tokens * choices up to 1024, experts up to 1024, and the hidden
+ * values (4 bytes each, 6 with FP32 rows, hidden rounded up to 64, one row a choice) up to 48 MiB, else
+ * SGEMM_ERR_INVALID_VALUE.  Other checks as for the routing calls. */
+int sgemm_expert_layer_int8(sgemm_handle_t h, int type, int gated, int tokens, int choices, int experts, int width,
+                            int hidden, const void *X, int ldx, const int *ids, const float *weights,
+                            const int8_t *up, const float *up_scale, const int8_t *down, const float *down_scale,
+                            void *out, int ldo, void *stream);
+
 /* C <- alpha*A*B + beta*C with A, B, C in HOST memory, transfers overlapped
  * with compute.  dA, dB, dC are caller-owned DEVICE buffers of the same
  * shapes and leading dimensions (M*lda, K*ldb, M*ldc floats at least).  On a
@@ -423,7 +558,7 @@ int sgemm_destroy(sgemm_handle_t h);
  * let the library choose).  SGEMM_ERR_INVALID_VALUE for an unknown value or
  * SGEMM_VARIANT_SCALE, which is chosen only by the alpha == 0 / K == 0 rule.
  * A pinned TMA variant fixes the tile; the re-layout mode still decides
- * whether operands are transposed first.  The 16-bit-input and int8 variants
+ * whether operands are transposed first.  The 16-bit-input, int8 and 4-bit variants
  * act as SGEMM_VARIANT_AUTO for FP32 calls. */
 int sgemm_set_variant(sgemm_handle_t h, int variant);
 
@@ -582,6 +717,12 @@ int sgemm_debug_set_cluster_split(sgemm_handle_t h, int ksplit);
  * the 128-wide steps that K has), or tokens 128 or 256 (CTA pairs) with ksplit 1.  Every
  * one of them gives the same bits.  SGEMM_ERR_INVALID_VALUE otherwise. */
 int sgemm_debug_set_int8_tile(sgemm_handle_t h, int tokens, int ksplit);
+
+/* Test hook: the same for sgemm_run_fp4 on the tensor cores.  tokens 16, 32, 64 (taken up
+ * to the call's tokens: such a tile is the only one) or 128 with ksplit 1, 2, 4 or 8 (taken
+ * down to the 256-wide steps that K has), or 256 (CTA pairs) with ksplit 1; 0, 0: the
+ * library's choice.  SGEMM_ERR_INVALID_VALUE otherwise. */
+int sgemm_debug_set_fp4_tile(sgemm_handle_t h, int tokens, int ksplit);
 
 /* Test hook: the number of stream-K CTAs of later calls' stream-K plans (the
  * last wave of the whole-tile variants, and the 64 x 64 split variant); 0 (the
