@@ -151,20 +151,28 @@ struct TileCfg {
     static_assert(kStages * kStage >= NT * kTileCh * 4, "the exchange");
 };
 
-// `cols` sums of channel n to the rows first .. of C, with the scales and the bias.
-template <class El, int COLS>
+// Scales of up to 32 tokens from `first` on, one a lane: the warp's lanes hand them
+// round (loaded token by token, each load waited for the store before it: an epilogue of
+// 256 x 256 took 8 us).
+__device__ __forceinline__ float token_scale(const Fp4Args &a, int first, int lane) {
+    return !a.rowA ? 1.f : first + lane < a.M ? __ldcg(a.rowA + first + lane) : 0.f;
+}
+
+// `cols` sums of channel n to the rows first .. of C, with the scales and the bias; `sa`
+// of lane FROM + j is the scale of sum j's token.
+template <class El, int COLS, int FROM>
 __device__ __forceinline__ void write_columns(const Fp4Args &a, int n, int first, int cols, const float (&acc)[COLS], float sb,
-                                              float bias, const float *row_a) {
+                                              float bias, float sa) {
     typename El::T *c = static_cast<typename El::T *>(a.C) + static_cast<long long>(first) * a.ldc + n;
+    if (n >= a.N) cols = 0;
 #pragma unroll
-    for (int j = 0; j < COLS; ++j) {
-        if (j >= cols) break;
-        const float sa = row_a ? __ldca(row_a + first + j) : 1.f;
-        if (n < a.N) c[static_cast<long long>(j) * a.ldc] = El::down(fmaf(acc[j] * sb, sa, bias));
+    for (int j = 0; j < COLS; ++j, c += a.ldc) {
+        const float v = fmaf(acc[j] * sb, __shfl_sync(0xffffffffu, sa, FROM + j), bias);
+        if (j < cols) *c = El::down(v);
     }
 }
 
-template <int FORMAT, int NT, bool SPLIT>
+template <int FORMAT, int NT, int KS>
 __global__ void __launch_bounds__(kTileThreads, 2)
 fp4_tile_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA,
                 const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmSA, const Fp4Args a) {
@@ -174,13 +182,12 @@ fp4_tile_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__
     uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     TileShared *sh = reinterpret_cast<TileShared *>(base + S * Cf::kStage);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int splits = SPLIT ? a.ksplit : 1, rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
-    const int unit = SPLIT ? static_cast<int>(blockIdx.x) / splits : static_cast<int>(blockIdx.x);
+    const int rank = KS > 1 ? static_cast<int>(cluster_ctarank()) : 0, unit = static_cast<int>(blockIdx.x) / KS;
     const int tok_tiles = (a.M + NT - 1) / NT;
     const int ch0 = unit / tok_tiles * kTileCh, t0 = unit % tok_tiles * NT;
     const int kt = (a.K + kStageK - 1) / kStageK;
-    const int k_first = static_cast<int>(static_cast<long long>(rank) * kt / splits);
-    const int k_last = static_cast<int>(static_cast<long long>(rank + 1) * kt / splits);
+    const int k_first = static_cast<int>(static_cast<long long>(rank) * kt / KS);
+    const int k_last = static_cast<int>(static_cast<long long>(rank + 1) * kt / KS);
 
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
@@ -264,38 +271,40 @@ fp4_tile_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__
     }
     const int n = ch0 + warp * 32 + lane;  // (the epilogue's warps)
     const uint32_t src = tmem + Cf::kD + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const float *row_a = a.rowA;
     float sb = 1.f, bias = 0.f;
     if (warp < 4 && n < a.N) {
         if (a.rowB) sb = __ldcg(a.rowB + n);
         if (a.bias) bias = __ldcg(a.bias + n);
     }
-    if (!SPLIT) {
+    if (KS == 1) {
         if (warp < 4 && ok) {
 #pragma unroll 1
             for (int c = 0; c < NT && t0 + c < a.M; c += 16) {
+                const float sa = token_scale(a, t0 + c, lane & 15);
                 float v[16];
                 tc::tmem_ld16(src + c, v);
                 with_type(a.out_type, [&](auto el) {
-                    write_columns<decltype(el), 16>(a, n, t0 + c, a.M - t0 - c, v, sb, bias, row_a);
+                    write_columns<decltype(el), 16, 0>(a, n, t0 + c, a.M - t0 - c, v, sb, bias, sa);
                 });
             }
         }
     } else {
-        // Rank r adds up the tokens [r * per, (r + 1) * per): every CTA's part of them
+        // Rank r adds up the tokens [r * kPer, (r + 1) * kPer): every CTA's part of them
         // goes to its shared memory, over the stages that no one needs any longer.
-        const int per = NT / splits;
+        constexpr int kPer = NT / KS;
+        const float sa = token_scale(a, t0 + rank * kPer, lane);  // (at most 64 tokens: lanes 0 to 31, and the second half below)
+        const float sa2 = kPer > 32 ? token_scale(a, t0 + rank * kPer + 32, lane) : 0.f;
         cluster_sync();
         if (warp < 4 && ok) {
-#pragma unroll 1
+            const uint32_t here = smem_u32(base) + static_cast<uint32_t>((rank * kPer * kTileCh + warp * 32 + lane) * 4);
+#pragma unroll
             for (int c = 0; c < NT; c += 16) {
                 float v[16];
                 tc::tmem_ld16(src + c, v);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const int to = (c + j) / per;
-                    const uint32_t at = dsmem_addr(base, static_cast<uint32_t>(to)) +
-                                        static_cast<uint32_t>(((rank * per + (c + j) % per) * kTileCh + warp * 32 + lane) * 4);
+                    const uint32_t at = tc::map_shared_rank(here, static_cast<uint32_t>((c + j) / kPer)) +
+                                        static_cast<uint32_t>((c + j) % kPer * kTileCh * 4);
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v[j]) : "memory");
                 }
             }
@@ -303,19 +312,29 @@ fp4_tile_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__
         // a CTA that gave up has left its part out: nothing is written by any of them
         if (!ok || *abort_flag) {
             if (lane == 0)
-                for (int q = 0; q < splits; ++q)
+                for (int q = 0; q < KS; ++q)
                     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_addr(&sh->abort, static_cast<uint32_t>(q))), "r"(1) : "memory");
         }
         cluster_sync();
         if (warp < 4 && !*abort_flag) {
             const float *mine = reinterpret_cast<const float *>(base) + warp * 32 + lane;
-            for (int j = 0; j < per; ++j) {
-                const int t = t0 + rank * per + j;
-                if (t >= a.M) break;
-                float sum = 0.f;
-                for (int q = 0; q < splits; ++q) sum += mine[(q * per + j) * kTileCh];
-                const float v[1] = {sum};
-                with_type(a.out_type, [&](auto el) { write_columns<decltype(el), 1>(a, n, t, 1, v, sb, bias, row_a); });
+            constexpr int kGo = kPer < 16 ? kPer : 16;
+            const int t = t0 + rank * kPer;
+#pragma unroll
+            for (int j0 = 0; j0 < kPer; j0 += kGo) {
+                if (t + j0 >= a.M) break;
+                float v[kGo];
+#pragma unroll
+                for (int j = 0; j < kGo; ++j) {
+                    v[j] = 0.f;
+#pragma unroll
+                    for (int q = 0; q < KS; ++q) v[j] += mine[(q * kPer + j0 + j) * kTileCh];
+                }
+                with_type(a.out_type, [&](auto el) {
+                    // (token j0 + j: lane (j0 + j) % 32 of one scale or the other)
+                    if (j0 % 32 == 0) write_columns<decltype(el), kGo, 0>(a, n, t + j0, a.M - t - j0, v, sb, bias, j0 < 32 ? sa : sa2);
+                    else write_columns<decltype(el), kGo, 32 - kGo>(a, n, t + j0, a.M - t - j0, v, sb, bias, j0 < 32 ? sa : sa2);
+                });
             }
         }
     }
@@ -478,6 +497,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__
                 if (a.rowB) sb = __ldcg(a.rowB + n);
                 if (a.bias) bias = __ldcg(a.bias + n);
             }
+            float sa[kCols / 32];
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) sa[c] = token_scale(a, t0 + c * 32, lane);
             if (!__all_sync(0xffffffffu, wait(&sh->dfull, round))) break;
             tc::fence_after_sync();
             uint32_t v[kCols / 16][16];
@@ -490,11 +512,11 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__
             if (lane == 0) tc::mbar_arrive_remote(dempty);
             with_type(a.out_type, [&](auto el) {
 #pragma unroll
-                for (int c = 0; c < kCols / 16; ++c) {
-                    float f[16];
+                for (int c = 0; c < kCols / 32; ++c) {
+                    float f[32];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[c][j]);
-                    if (t0 + c * 16 < a.M) write_columns<decltype(el), 16>(a, n, t0 + c * 16, a.M - t0 - c * 16, f, sb, bias, a.rowA);
+                    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[2 * c + j / 16][j % 16]);
+                    if (t0 + c * 32 < a.M) write_columns<decltype(el), 32, 0>(a, n, t0 + c * 32, a.M - t0 - c * 32, f, sb, bias, sa[c]);
                 }
             });
         }
@@ -575,12 +597,21 @@ __global__ void __launch_bounds__(256) fp4_generic_kernel(const Fp4Args a) {
     }
 }
 
+template <int FORMAT, int NT, int KS>
+cudaError_t launch_split(const Fp4Args &a, const Fp4Maps &m, int smem, cudaStream_t stream) {
+    const unsigned units = static_cast<unsigned>((a.N + kTileCh - 1) / kTileCh) * static_cast<unsigned>((a.M + NT - 1) / NT);
+    return launch_dependent(fp4_tile_kernel<FORMAT, NT, KS>, dim3(units * KS), dim3(kTileThreads), smem > 0 ? smem : TileCfg<FORMAT, NT>::kSmem,
+                            stream, KS, m.B, m.A, m.SB, m.SA, a);
+}
+
 template <int FORMAT, int NT>
 cudaError_t launch_tile(const Fp4Args &a, const Fp4Maps &m, int smem, cudaStream_t stream) {
-    const unsigned units = static_cast<unsigned>((a.N + kTileCh - 1) / kTileCh) * static_cast<unsigned>((a.M + NT - 1) / NT);
-    return launch_dependent(a.ksplit > 1 ? fp4_tile_kernel<FORMAT, NT, true> : fp4_tile_kernel<FORMAT, NT, false>,
-                            dim3(units * static_cast<unsigned>(a.ksplit)), dim3(kTileThreads), smem > 0 ? smem : TileCfg<FORMAT, NT>::kSmem, stream,
-                            a.ksplit, m.B, m.A, m.SB, m.SA, a);
+    switch (a.ksplit) {
+        case 1: return launch_split<FORMAT, NT, 1>(a, m, smem, stream);
+        case 2: return launch_split<FORMAT, NT, 2>(a, m, smem, stream);
+        case 4: return launch_split<FORMAT, NT, 4>(a, m, smem, stream);
+        default: return launch_split<FORMAT, NT, 8>(a, m, smem, stream);
+    }
 }
 
 template <int FORMAT>
@@ -601,8 +632,10 @@ cudaError_t launch_format(const Fp4Args &a, const Fp4Maps &m, int num_sms, int s
 
 template <int FORMAT, int NT>
 cudaError_t prepare_tile() {
-    const cudaError_t e = cudaFuncSetAttribute(fp4_tile_kernel<FORMAT, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<FORMAT, NT>::kSmem);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(fp4_tile_kernel<FORMAT, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<FORMAT, NT>::kSmem);
+    cudaError_t e = cudaSuccess;
+    for (auto *k : {fp4_tile_kernel<FORMAT, NT, 1>, fp4_tile_kernel<FORMAT, NT, 2>, fp4_tile_kernel<FORMAT, NT, 4>, fp4_tile_kernel<FORMAT, NT, 8>})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<FORMAT, NT>::kSmem);
+    return e;
 }
 
 template <int FORMAT>
