@@ -408,6 +408,7 @@ struct LayerArgs {
     void *out;
     long long ldo;
     uint16_t *h;  // workspace, layer_floats floats: the hidden rows in BF16 parts
+    int *status;
     // set by the launch
     int hidden_ld;
     long long up_rows, h_part;

@@ -14,11 +14,14 @@
 // multiplied by mma.sync (m16n8k16, BF16, FP32 sums), whose rate is far above what HBM
 // delivers for so few tokens: a tile of 16 channels x 8 tokens takes each weight once.
 // The order of k within an MMA is free, so a lane's 16 bytes are the k of four
-// MMAs.  An int8 is exact in BF16; the tokens' elements go in as sums of one (BF16), two
-// (FP16) or three (FP32) BF16 values, exact as well.  The hidden rows
+// MMAs.  An int8 is exact in BF16 and in FP16; the tokens' elements go in as they are or, FP32,
+// as sums of three BF16 values, exact as well.  The hidden rows
 // are kept as two such values, 16 bits of fraction, and with FP32 rows as three.  Within
 // a warp sums run along k; the warps' sums, the experts' and the choices' are added in a
 // fixed order in FP32.
+#include <type_traits>
+
+#include "context.h"
 #include "device_common.cuh"
 #include "internal.h"
 #include "rows.cuh"
@@ -27,15 +30,16 @@
 namespace sg {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;  // (those that multiply)
 constexpr int kChunk = 64;  // k of a step: 16 bytes of each of 16 channels from four lanes each
+constexpr int kPad = 128;   // hidden rows are made longer to a multiple of it, with zeros
 constexpr int kSlots = kLayerSlots;
 
 template <class El>
-struct Parts;  // BF16 values that an element and a hidden value become
-template <> struct Parts<ElBF16> { static constexpr int in = 1, hidden = 2; };
-template <> struct Parts<ElF16> { static constexpr int in = 2, hidden = 2; };
-template <> struct Parts<ElF32> { static constexpr int in = 3, hidden = 3; };
+struct Parts;  // 16-bit values that an element and a hidden value become, and the former's type
+template <> struct Parts<ElBF16> { static constexpr int in = 1, hidden = 2; using Mma = ElBF16; };
+template <> struct Parts<ElF16> { static constexpr int in = 1, hidden = 2; using Mma = ElF16; };  // (as they are, U in FP16)
+template <> struct Parts<ElF32> { static constexpr int in = 3, hidden = 3; using Mma = ElBF16; };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -56,10 +60,22 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&to)[P]) {
     }
 }
 
-// Four int8 to two pairs of BF16: 0x4300 + u is 128 + u for u < 128, and 0x4380 is 256,
-// so with a byte b's low seven bits u and its sign s, (0x4300 + u) - (0x4300 + 128 s)
-// is u - 128 s, exactly b.
+// Four int8 to two pairs of FP16: 0x6400 + u is 1024 + u, and with u = b + 128 (the byte's
+// sign bit flipped) less 1152 exactly b.  To two pairs of BF16: 0x4300 + u is 128 + u for u
+// < 128, and 0x4380 is 256, so with a byte b's low seven bits u and its sign s, (0x4300 +
+// u) - (0x4300 + 128 s) is u - 128 s, exactly b.
+template <class Mma>
 __device__ __forceinline__ void expand_int8(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if (std::is_same<Mma, ElF16>::value) {
+        w ^= 0x80808080u;
+        auto less = [](uint32_t p) {
+            const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&p), __half2{__ushort_as_half(0x6480), __ushort_as_half(0x6480)});
+            return *reinterpret_cast<const uint32_t *>(&d);
+        };
+        lo = less(__byte_perm(w, 0x64646464u, 0x4140));
+        hi = less(__byte_perm(w, 0x64646464u, 0x4342));
+        return;
+    }
     auto one = [](uint32_t p) {
         const uint32_t a = p & 0xff7fff7fu, s = p & 0xff80ff80u;
         const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&s));
@@ -69,10 +85,15 @@ __device__ __forceinline__ void expand_int8(uint32_t w, uint32_t &lo, uint32_t &
     hi = one(__byte_perm(w, 0x43434343u, 0x4342));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <class Mma>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+#define SG_MMA(T)                                                                                                       \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};" \
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                                                \
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1))
+    if (std::is_same<Mma, ElF16>::value) SG_MMA("f16");
+    else SG_MMA("bf16");
+#undef SG_MMA
 }
 
 // The routing, as every CTA works it out.  Columns: the choices that count, sorted
@@ -80,27 +101,34 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 // with the sum of both weights.
 struct Routing {
     int id[kSlots];            // the slot's expert, -1: none of its own
-    short token[kSlots];       // by column
-    float weight[kSlots];
+    struct Column {
+        int token;
+        float weight;
+    } column[kSlots];
     int start[kMaxExperts + 1];  // first column of an expert
-    int group_expert[kSlots], group_first[kSlots];  // first: column; a group ends with its expert's columns or after 8 * NT
+    struct alignas(8) Group {
+        int expert;
+        short first, cols;  // its columns: up to 8 * NT of one expert's
+    } group[kSlots];
     int groups;
 };
 
+template <int THREADS>
 __device__ void route(Routing &r, const LayerArgs &a, int per_group) {
+    constexpr int kEach = (kSlots + THREADS - 1) / THREADS;
     const int slots = a.tokens * a.choices, tid = threadIdx.x;
-    for (int e = tid; e <= a.experts; e += kThreads) r.start[e] = 0;
-    for (int s = tid; s < slots; s += kThreads) {
+    for (int e = tid; e <= a.experts; e += THREADS) r.start[e] = 0;
+    for (int s = tid; s < slots; s += THREADS) {
         const int id = __ldcg(a.ids + s);
         r.id[s] = static_cast<unsigned>(id) < static_cast<unsigned>(a.experts) ? id : -1;
     }
     __syncthreads();
     // slots that repeat an earlier choice of their token add to its weight
-    float mine[kSlots / kThreads];
-    bool own[kSlots / kThreads];
+    float mine[kEach];
+    bool own[kEach];
 #pragma unroll
-    for (int k = 0; k < kSlots / kThreads; ++k) {
-        const int s = tid + k * kThreads;
+    for (int k = 0; k < kEach; ++k) {
+        const int s = tid + k * THREADS;
         own[k] = s < slots && r.id[s] >= 0;
         mine[k] = 0.f;
         if (!own[k]) continue;
@@ -111,8 +139,8 @@ __device__ void route(Routing &r, const LayerArgs &a, int per_group) {
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kSlots / kThreads; ++k) {
-        const int s = tid + k * kThreads;
+    for (int k = 0; k < kEach; ++k) {
+        const int s = tid + k * THREADS;
         if (s >= slots) continue;
         if (own[k]) atomicAdd(&r.start[r.id[s]], 1);
         else r.id[s] = -1;
@@ -132,10 +160,9 @@ __device__ void route(Routing &r, const LayerArgs &a, int per_group) {
                 }
             }
             if (e < a.experts) r.start[e] = cols + sn - n;
-            for (int k = 0; k < g; ++k) {
-                r.group_expert[groups + sg - g + k] = e;
-                r.group_first[groups + sg - g + k] = cols + sn - n + k * per_group;
-            }
+            for (int k = 0; k < g; ++k)
+                r.group[groups + sg - g + k] = {e, static_cast<short>(cols + sn - n + k * per_group),
+                                                static_cast<short>(min(per_group, n - k * per_group))};
             cols += __shfl_sync(0xffffffffu, sn, 31);
             groups += __shfl_sync(0xffffffffu, sg, 31);
         }
@@ -146,21 +173,18 @@ __device__ void route(Routing &r, const LayerArgs &a, int per_group) {
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kSlots / kThreads; ++k) {
-        const int s = tid + k * kThreads;
+    for (int k = 0; k < kEach; ++k) {
+        const int s = tid + k * THREADS;
         if (s >= slots || r.id[s] < 0) continue;
         int c = r.start[r.id[s]];
         for (int q = 0; q < s; ++q) c += r.id[q] == r.id[s];
-        r.token[c] = static_cast<short>(s / a.choices);
-        r.weight[c] = mine[k];
+        r.column[c] = {s / a.choices, mine[k]};
     }
     __syncthreads();
 }
 
 // 16 bytes of a weight row from k on, zeros behind its end.
-template <bool VEC>
 __device__ __forceinline__ uint4 load_weights(const int8_t *row, int k, int K) {
-    if (VEC) return k < K ? __ldcg(reinterpret_cast<const uint4 *>(row + k)) : make_uint4(0, 0, 0, 0);
     uint32_t w[4] = {};
 #pragma unroll
     for (int e = 0; e < 16; ++e)
@@ -168,61 +192,159 @@ __device__ __forceinline__ uint4 load_weights(const int8_t *row, int k, int K) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 16 elements of a token from k on as P x 8 pairs of BF16, zeros behind its end.
+// 32 bytes on a 32-byte boundary in one access: a sector, of which two of 16 bytes would
+// each use half.
+__device__ __forceinline__ void load32(const void *p, uint32_t (&to)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(to[0]), "=r"(to[1]), "=r"(to[2]), "=r"(to[3]), "=r"(to[4]), "=r"(to[5]), "=r"(to[6]), "=r"(to[7])
+                 : "l"(p) : "memory");
+}
+
+// 16 elements of a token from k on, zeros behind its end, as they lie in memory and
+// as P x 8 pairs of BF16.
+template <class El>
+struct Raw {
+    alignas(16) typename El::T v[16];
+};
 template <class El, bool VEC>
-__device__ __forceinline__ void load_token(const typename El::T *row, int k, int K, uint32_t (&to)[Parts<El>::in][8]) {
+__device__ __forceinline__ Raw<El> fetch_token(const typename El::T *row, int k, int K) {
     using T = typename El::T;
-    constexpr int P = Parts<El>::in, V = 16 / sizeof(T);
-    alignas(16) T v[16];
+    constexpr int V = 16 / sizeof(T);
+    Raw<El> r;
     if (VEC) {
 #pragma unroll
-        for (int e = 0; e < 16; e += V)
-            *reinterpret_cast<uint4 *>(v + e) = k + e < K ? __ldca(reinterpret_cast<const uint4 *>(row + k + e)) : make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < 16; e += 2 * V) {
+            uint32_t w[8] = {};
+            if (row && k + e < K) load32(row + k + e, w);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) reinterpret_cast<uint32_t *>(r.v + e)[x] = w[x];
+        }
     } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = k + e < K ? __ldca(row + k + e) : El::down(0.f);
+        for (int e = 0; e < 16; ++e) r.v[e] = k + e < K ? __ldca(row + k + e) : El::down(0.f);
     }
+    return r;
+}
+template <class El>
+__device__ __forceinline__ void split_token(const Raw<El> &r, uint32_t (&to)[Parts<El>::in][8]) {
+    constexpr int P = Parts<El>::in;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         uint32_t p[P];
-        if (P == 1) p[0] = *reinterpret_cast<const uint32_t *>(v + 2 * e);
-        else split2<P>(El::up(v[2 * e]), El::up(v[2 * e + 1]), p);
+        if (P == 1) p[0] = *reinterpret_cast<const uint32_t *>(r.v + 2 * e);
+        else split2<P>(El::up(r.v[2 * e]), El::up(r.v[2 * e + 1]), p);
 #pragma unroll
         for (int q = 0; q < P; ++q) to[q][e] = p[q];
     }
 }
 
 // acc += 16 channels x 64 k (lo: channel g, hi: channel g + 8) times 8 tokens.
-template <int P>
+// (two chains of additions: an MMA waits for the one before it in its chain)
+template <class Mma, int P>
 __device__ __forceinline__ void multiply(float (&acc)[4], const uint32_t (&a)[4][4], const uint32_t (&x)[P][8]) {
+    float more[4] = {};
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 4; s += 2)
 #pragma unroll
-        for (int p = P - 1; p >= 0; --p) mma_bf16(acc, a[s], x[p][2 * s], x[p][2 * s + 1]);
+        for (int p = P - 1; p >= 0; --p) {
+            mma16<Mma>(more, a[s], x[p][2 * s], x[p][2 * s + 1]);
+            mma16<Mma>(acc, a[s + 1], x[p][2 * s + 2], x[p][2 * s + 3]);
+        }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] += more[c];
 }
+template <class Mma>
 __device__ __forceinline__ void expand_rows(const uint4 &lo, const uint4 &hi, uint32_t (&a)[4][4]) {
     const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-        expand_int8(l[s], a[s][0], a[s][2]);
-        expand_int8(h[s], a[s][1], a[s][3]);
+        expand_int8<Mma>(l[s], a[s][0], a[s][2]);
+        expand_int8<Mma>(h[s], a[s][1], a[s][3]);
     }
 }
 
+// The scales of the channels that a lane has of an MMA tile: g, and the one in its lower half.
+template <bool GATED>
+__device__ __forceinline__ void hidden_scales(const LayerArgs &a, int e, int f0, int g, float (&to)[2]) {
+    const int fl = f0 + g, fh = GATED ? fl : fl + 8;
+    const float *scale = a.up_scale + static_cast<long long>(e) * a.up_rows;
+    to[0] = fl < a.hidden ? __ldca(scale + fl) : 0.f;
+    to[1] = fh < a.hidden ? __ldca(scale + fh + (GATED ? a.hidden : 0)) : 0.f;
+}
+
+// The hidden values of 8 tokens from their sums: s.x, s.y channel g of tokens 2t and 2t + 1, s.z
+// and s.w of the MMA's lower channel.  Channels behind the last hidden one are written as zeros.
+template <bool GATED, int PH>
+__device__ __forceinline__ void write_hidden(const LayerArgs &a, int first, int cols, int f0, int n, int g, int t, const float4 &s,
+                                             const float (&scale)[2]) {
+    const int fl = f0 + g, fh = GATED ? fl : fl + 8;
+    const bool in_l = fl < a.hidden, in_h = fh < a.hidden;
+    auto silu = [](float v) { return v / (1.f + expf(-v)); };
+    auto put = [&](int col, int f, float v) {
+        if (col >= cols || f >= a.hidden_ld) return;
+        uint32_t p[PH];
+        split2<PH>(v, 0.f, p);
+#pragma unroll
+        for (int q = 0; q < PH; ++q)
+            a.h[q * a.h_part + static_cast<long long>(first + col) * a.hidden_ld + f] = static_cast<uint16_t>(p[q]);
+    };
+    const float y0 = silu(s.x * scale[0]), y1 = silu(s.y * scale[0]);
+    put(n * 8 + 2 * t, fl, in_l ? GATED ? y0 * (s.z * scale[1]) : y0 : 0.f);
+    put(n * 8 + 2 * t + 1, fl, in_l ? GATED ? y1 * (s.w * scale[1]) : y1 : 0.f);
+    if (!GATED) {
+        put(n * 8 + 2 * t, fh, in_h ? silu(s.z * scale[1]) : 0.f);
+        put(n * 8 + 2 * t + 1, fh, in_h ? silu(s.w * scale[1]) : 0.f);
+    }
+}
+
+// 16 hidden values from k on, PH x 8 pairs of BF16 (row NULL, a column that a group does not have:
+// zeros; what a lane fetches in vain takes its share of the SM's 128 bytes a cycle).
+template <int PH>
+__device__ __forceinline__ void load_hidden(const uint16_t *row, long long part, int k, uint32_t (&to)[PH][8]) {
+#pragma unroll
+    for (int q = 0; q < PH; ++q) {
+        if (row) load32(row + q * part + k, to[q]);
+        else
+#pragma unroll
+            for (int x = 0; x < 8; ++x) to[q][x] = 0u;
+    }
+}
+
+// A warp's sums of a group, scaled, to its own sums of the tokens.
+constexpr int kOutPitch = 17;
+template <int NT>
+__device__ __forceinline__ void add_out(const Routing &r, float *mine, int first, int cols, int g, int t, float sl, float sh,
+                                        const float (&acc)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int col = n * 8 + 2 * t + j;
+            if (col >= cols) continue;
+            const Routing::Column c = r.column[first + col];
+            float *to = mine + c.token * kOutPitch;
+            to[g] = fmaf(acc[n][j] * sl, c.weight, to[g]);
+            to[g + 8] = fmaf(acc[n][2 + j] * sh, c.weight, to[g + 8]);
+        }
+    __syncwarp();
+}
+
+// ---- any alignment: the weights straight into registers --------------------------------
 constexpr int kAhead = 4;  // chunks whose loads are in flight
 
 // hidden[part][column][f] = act(U x) of every group; an item is a group and 16 rows of
 // U: with a gate 8 channels of it and the 8 that it goes with, in the MMA's upper and
 // lower rows, so that one lane has both.  `share` warps of the CTA split an item's K.
-template <class El, int NT, bool GATED, bool VEC>
+template <class El, int NT, bool GATED>
 __global__ void __launch_bounds__(kThreads, 2) up_kernel(const LayerArgs a, int share) {
     using T = typename El::T;
+    using Mma = typename Parts<El>::Mma;
     constexpr int P = Parts<El>::in, PH = Parts<El>::hidden, kCh = GATED ? 8 : 16;
     __shared__ Routing r;
     __shared__ float4 sums[kWarps][NT][32];
     griddep_wait();
     griddep_launch_dependents();
-    route(r, a, 8 * NT);
+    route<kThreads>(r, a, 8 * NT);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int tiles = a.hidden_ld / kCh, teams = kWarps / share, team = warp / share, part = warp % share;
     const long long items = static_cast<long long>(r.groups) * tiles;
@@ -231,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const LayerArgs a, int 
         const long long item = i0 + team;
         const bool live = item < items;
         const int group = live ? static_cast<int>(item / tiles) : 0, f0 = live ? static_cast<int>(item % tiles) * kCh : 0;
-        const int e = r.group_expert[group], first = r.group_first[group], cols = min(r.start[e + 1] - first, 8 * NT);
+        const Routing::Group here = r.group[group];
+        const int e = here.expert, first = here.first, cols = here.cols;
         const int fl = f0 + g, fh = GATED ? fl : fl + 8;  // the hidden channels of the lane's rows
         const bool in_l = live && fl < a.hidden, in_h = live && fh < a.hidden;
         const long long row_l = static_cast<long long>(e) * a.up_rows + (in_l ? fl : 0);
@@ -240,28 +363,28 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const LayerArgs a, int 
         const T *x[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            x[n] = static_cast<const T *>(a.X) + static_cast<long long>(r.token[first + min(n * 8 + g, cols - 1)]) * a.ldx;
+            x[n] = static_cast<const T *>(a.X) + static_cast<long long>(r.column[first + min(n * 8 + g, cols - 1)].token) * a.ldx;
         float acc[NT][4] = {};
         for (int c0 = part; c0 < chunks; c0 += share * kAhead) {
             uint4 wl[kAhead], wh[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int at = (c0 + k * share) * kChunk + t * 16;
-                wl[k] = load_weights<VEC>(ul, at, in_l ? a.width : 0);
-                wh[k] = load_weights<VEC>(uh, at, in_h ? a.width : 0);
+                wl[k] = load_weights(ul, at, in_l ? a.width : 0);
+                wh[k] = load_weights(uh, at, in_h ? a.width : 0);
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 if (c0 + k * share >= chunks) break;
                 const int at = (c0 + k * share) * kChunk + t * 16;
                 uint32_t w[4][4];
-                expand_rows(wl[k], wh[k], w);
+                expand_rows<Mma>(wl[k], wh[k], w);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     if (n * 8 >= cols) break;
                     uint32_t v[P][8];
-                    load_token<El, VEC>(x[n], at, a.width, v);
-                    multiply<P>(acc[n], w, v);
+                    split_token<El>(fetch_token<El, false>(x[n], at, a.width), v);
+                    multiply<Mma, P>(acc[n], w, v);
                 }
             }
         }
@@ -278,25 +401,9 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const LayerArgs a, int 
                     s.z += v.z;
                     s.w += v.w;
                 }
-                const float sl = in_l ? __ldca(a.up_scale + row_l) : 0.f, sh = in_h ? __ldca(a.up_scale + row_h) : 0.f;
-                auto silu = [](float v) { return v / (1.f + expf(-v)); };
-                // tokens 2t, 2t + 1; channels behind the last hidden one are written as zeros
-                const float y0 = GATED ? silu(s.x * sl) * (s.z * sh) : silu(s.x * sl), y1 = GATED ? silu(s.y * sl) * (s.w * sh) : silu(s.y * sl);
-                const float z0 = GATED ? 0.f : silu(s.z * sh), z1 = GATED ? 0.f : silu(s.w * sh);
-                auto put = [&](int col, int f, float v) {
-                    if (col >= cols) return;
-                    uint32_t p[PH];
-                    split2<PH>(v, 0.f, p);
-#pragma unroll
-                    for (int q = 0; q < PH; ++q)
-                        a.h[q * a.h_part + static_cast<long long>(first + col) * a.hidden_ld + f] = static_cast<uint16_t>(p[q]);
-                };
-                put(n * 8 + 2 * t, fl, in_l ? y0 : 0.f);
-                put(n * 8 + 2 * t + 1, fl, in_l ? y1 : 0.f);
-                if (!GATED) {
-                    put(n * 8 + 2 * t, fh, in_h ? z0 : 0.f);
-                    put(n * 8 + 2 * t + 1, fh, in_h ? z1 : 0.f);
-                }
+                float scale[2];
+                hidden_scales<GATED>(a, e, f0, g, scale);
+                write_hidden<GATED, PH>(a, first, cols, f0, n, g, t, s, scale);
             }
         }
         __syncthreads();
@@ -306,8 +413,7 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const LayerArgs a, int 
 // out: an item is 16 channels of every token; the CTA's warps take consecutive runs of
 // (group, chunk of k) pairs.  At the end of its run or of a group a warp adds what it
 // has, scaled, to its own sums of the tokens.
-constexpr int kOutPitch = 17;
-template <class El, int NT, bool VEC>
+template <class El, int NT>
 __global__ void __launch_bounds__(kThreads, 2) down_kernel(const LayerArgs a) {
     constexpr int PH = Parts<El>::hidden;
     extern __shared__ float out_sums[];  // [warp][token][kOutPitch]
@@ -315,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const LayerArgs a) {
     // (the routing and the sums touch nothing that the kernel before writes, and that
     // one has waited for what came before it)
     for (int k = threadIdx.x; k < kWarps * a.tokens * kOutPitch; k += kThreads) out_sums[k] = 0.f;
-    route(r, a, 8 * NT);
+    route<kThreads>(r, a, 8 * NT);
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -329,7 +435,8 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const LayerArgs a) {
         const int group = static_cast<int>(u / chunks), c_first = static_cast<int>(u % chunks);
         const int c_last = static_cast<int>(min(static_cast<long long>(chunks), c_first + (u_last - u)));
         u += c_last - c_first;
-        const int e = r.group_expert[group], first = r.group_first[group], cols = min(r.start[e + 1] - first, 8 * NT);
+        const Routing::Group here = r.group[group];
+        const int e = here.expert, first = here.first, cols = here.cols;
         const long long row_l = static_cast<long long>(e) * a.width + (in_l ? dl : 0), row_h = static_cast<long long>(e) * a.width + (in_h ? dh : 0);
         const int8_t *wl = a.down + row_l * a.hidden, *wh = a.down + row_h * a.hidden;
         const uint16_t *h[NT];
@@ -341,42 +448,26 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const LayerArgs a) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int at = (c0 + k) * kChunk + t * 16;
-                vl[k] = load_weights<VEC>(wl, at, in_l && c0 + k < c_last ? a.hidden : 0);
-                vh[k] = load_weights<VEC>(wh, at, in_h && c0 + k < c_last ? a.hidden : 0);
+                vl[k] = load_weights(wl, at, in_l && c0 + k < c_last ? a.hidden : 0);
+                vh[k] = load_weights(wh, at, in_h && c0 + k < c_last ? a.hidden : 0);
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 if (c0 + k >= c_last) break;
                 const int at = (c0 + k) * kChunk + t * 16;
                 uint32_t w[4][4];
-                expand_rows(vl[k], vh[k], w);
+                expand_rows<ElBF16>(vl[k], vh[k], w);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     if (n * 8 >= cols) break;
                     uint32_t v[PH][8];
-#pragma unroll
-                    for (int q = 0; q < PH; ++q)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            *reinterpret_cast<uint4 *>(&v[q][4 * x]) =
-                                __ldca(reinterpret_cast<const uint4 *>(h[n] + q * a.h_part + at + 8 * x));
-                    multiply<PH>(acc[n], w, v);
+                    load_hidden<PH>(h[n], a.h_part, at, v);
+                    multiply<ElBF16, PH>(acc[n], w, v);
                 }
             }
         }
         const float sl = in_l ? __ldca(a.down_scale + row_l) : 0.f, sh = in_h ? __ldca(a.down_scale + row_h) : 0.f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int col = n * 8 + 2 * t + j;
-                if (col >= cols) continue;
-                float *to = mine + r.token[first + col] * kOutPitch;
-                const float w = r.weight[first + col];
-                to[g] = fmaf(acc[n][j] * sl, w, to[g]);
-                to[g + 8] = fmaf(acc[n][2 + j] * sh, w, to[g + 8]);
-            }
-        __syncwarp();
+        add_out<NT>(r, mine, first, cols, g, t, sl, sh, acc);
     }
     __syncthreads();
     for (int k = threadIdx.x; k < a.tokens * 16; k += kThreads) {
@@ -388,49 +479,448 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const LayerArgs a) {
     }
 }
 
-template <class El, int NT, bool VEC>
-cudaError_t layer_typed(const LayerArgs &a, int num_sms, cudaStream_t stream) {
+// ---- rows on 16-byte boundaries: the weights through shared memory --------------------
+// One lane streams the weights of all the CTA's items, one behind the other, into a ring
+// of stages of 1024 bytes of 32 or 16 rows by TMA, so that as many bytes are on their way while the others add up or
+// write as at any other time.  Sixteen warps take a 64-byte column of every 1024 bytes;
+// warps of their own add up the columns' sums and write the hidden values, their scales
+// fetched ahead, so that the ring is not held up.
+constexpr int kSeg = 1024;
+constexpr int kTakers = kSeg / kChunk;
+template <class El, int NT>
+struct StreamCfg {
+    static constexpr int kUpStages = NT <= 2 ? 4 : 3;              // of 32 rows
+    static constexpr int kSums = NT == 1 ? 2 : 1;                  // sets of sums
+    static constexpr int kSumBytes = kTakers * 2 * NT * 512;       // of a set
+    static constexpr int kUpThreads = (kTakers + 1 + NT) * 32, kDownThreads = (kTakers + 1) * 32;
+    static constexpr int kUpRing = 1024 + kUpStages * 32 * kSeg, kUpSmem = kUpRing + kSums * kSumBytes;
+    static constexpr int kDownStages = NT == 1 ? 8 : 6;            // of 16 rows
+    static constexpr int kDownRing = 1024 + kDownStages * 16 * kSeg;
+    static constexpr int down_smem(int tokens) { return kDownRing + kTakers * tokens * kOutPitch * 4; }
+    // the most tokens of a call on this configuration; the routing takes less than 25 KiB
+    static_assert(down_smem(NT == 1 ? 8 : kLayerTokens) <= 232448 - 25600 && kUpSmem <= 232448 - 25600, "shared memory");
+};
+constexpr int kPrefetch = 64;  // boxes of 2 KiB
+struct StreamShared {
+    uint64_t full[8], empty[8], sums_full[2], sums_empty[2];
+    int abort;
+};
+
+// First of the 16 k of a stage that a lane of a warp takes (see Stream::take).
+__device__ __forceinline__ int lane_k(int warp, int t) { return warp / 2 * 128 + (2 * t + (warp & 1)) * 16; }
+
+template <int STAGES, int ROWS>
+struct Stream {
+    static constexpr int kBytes = ROWS * kSeg;
+    uint8_t *ring;
+    StreamShared *sh;
+    int *status;
+    int s = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void step() {
+        if (++s == STAGES) {
+            s = 0;
+            round ^= 1u;
+        }
+    }
+    __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*static_cast<volatile int *>(&sh->abort)) return false;
+        if (mbar_wait(bar, parity, status)) return true;
+        *static_cast<volatile int *>(&sh->abort) = 1;
+        return false;
+    }
+    // The producing lane: a stage of 16 rows from `row0` and, of 32, 16 from `row1`.  After a wait
+    // that ran out: false, once no copy is in flight any longer.
+    __device__ __forceinline__ bool put(const CUtensorMap *map, int at, int row0, int row1) {
+        if (!wait(&sh->empty[s], round ^ 1u)) {
+            // (slot s still holds the last round's stage, the slots before it this round's)
+            for (int k = 0; k < STAGES; ++k, step()) mbar_wait(&sh->full[s], round ^ 1u, status);
+            return false;
+        }
+        mbar_arrive_expect_tx(&sh->full[s], kBytes);
+        uint8_t *to = ring + s * kBytes;
+#pragma unroll
+        for (int c = 0; c < kSeg / 128; ++c) {
+            tma_load_2d(to + c * 2048, map, &sh->full[s], at + c * 128, row0);
+            if (ROWS == 32) tma_load_2d(to + kBytes / 2 + c * 2048, map, &sh->full[s], at + c * 128, row1);
+        }
+        step();
+        return true;
+    }
+    // A taking warp: the next stage has landed.
+    __device__ __forceinline__ bool get() { return __all_sync(0xffffffffu, wait(&sh->full[s], round)); }
+    // 16 bytes of rows `lo` and `hi` (of the 32): piece `piece` of column `column` of 128.  With pieces
+    // 0, 2, 4, 6 or 1, 3, 5, 7 in a row's four lanes the swizzle puts any two rows that follow
+    // one another on all banks.
+    __device__ __forceinline__ void take(int lo_row, int hi_row, int column, int piece, uint4 &lo, uint4 &hi) const {
+        const uint8_t *at = ring + s * kBytes + column * 2048;
+        auto of = [&](int row) { return at + row / 16 * (16 * kSeg) + row % 16 * 128 + ((piece ^ (row & 7)) * 16); };
+        lo = *reinterpret_cast<const uint4 *>(of(lo_row));
+        hi = *reinterpret_cast<const uint4 *>(of(hi_row));
+    }
+    __device__ __forceinline__ void done(int lane) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->empty[s]);
+        step();
+    }
+};
+
+// The ring's barriers; the whole CTA, which meets at a barrier afterwards.
+template <int STAGES, int ROWS>
+__device__ __forceinline__ Stream<STAGES, ROWS> open_stream(uint8_t *smem, StreamShared *sh, int writers, int takers, int *status) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], takers);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sh->sums_full[s], kTakers);
+            mbar_init(&sh->sums_empty[s], writers);
+        }
+        sh->abort = 0;
+        fence_barrier_init();
+    }
+    Stream<STAGES, ROWS> q;
+    q.ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
+    q.sh = sh;
+    q.status = status;
+    return q;
+}
+
+// As up_kernel, an item 32 rows of U: the tokens' elements are then fetched and split once
+// for two MMA tiles.
+template <class El, int NT, bool GATED>
+__global__ void __launch_bounds__(StreamCfg<El, NT>::kUpThreads, 1)
+up_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap next_map, const LayerArgs a) {
+    using T = typename El::T;
+    using Mma = typename Parts<El>::Mma;
+    using Cf = StreamCfg<El, NT>;
+    constexpr int P = Parts<El>::in, PH = Parts<El>::hidden, kCh = GATED ? 16 : 32;
+    extern __shared__ uint8_t smem[];
+    __shared__ StreamShared shared;
+    __shared__ Routing r;
+    Stream<Cf::kUpStages, 32> q = open_stream<Cf::kUpStages, 32>(smem, &shared, NT, kTakers, a.status);
+    float4 *sums = reinterpret_cast<float4 *>(smem + Cf::kUpRing);  // [set][warp][tile][n][lane]
+    griddep_wait();
+    griddep_launch_dependents();
+    route<Cf::kUpThreads>(r, a, 8 * NT);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int tiles = (a.hidden_ld + kCh - 1) / kCh, items = r.groups * tiles, segs = (a.width + kSeg - 1) / kSeg;
+    if (warp == kTakers) {
+        if (lane > 0) return;
+        for (int i = blockIdx.x; i < items; i += gridDim.x) {
+            // (a tile behind the last hidden channel reads the rows that follow, and writes zeros)
+            const int row = static_cast<int>(r.group[i / tiles].expert * a.up_rows) + i % tiles * kCh;
+            for (int s = 0; s < segs; ++s)
+                if (!q.put(&map, s * kSeg, row, row + (GATED ? a.hidden : 16))) return;
+        }
+        // What this CTA's successor in down_stream_kernel reads first is fetched into L2 while
+        // it starts (its weights may be: see there).
+        int left = kPrefetch;
+        for (int i = blockIdx.x; i < (a.width + 15) / 16; i += gridDim.x)
+            for (int group = 0; group < r.groups; ++group)
+                for (int s = 0; s < (a.hidden + 127) / 128; ++s, --left) {
+                    if (left == 0) return;
+                    tma_prefetch_2d(&next_map, s * 128, r.group[group].expert * a.width + i * 16);
+                }
+        return;
+    }
+    if (warp > kTakers) {
+        // ------------------------------------------------ 8 tokens' sums to hidden values
+        const int n = warp - kTakers - 1;
+        int set = 0;
+        uint32_t round = 0;
+        for (int i = blockIdx.x; i < items; i += gridDim.x) {
+            const int group = i / tiles, f0 = i % tiles * kCh;
+            const Routing::Group here = r.group[group];
+            const int e = here.expert, first = here.first, cols = here.cols;
+            float scale[2][2];
+            if (n * 8 < cols)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) hidden_scales<GATED>(a, e, f0 + m * (kCh / 2), g, scale[m]);
+            if (!__all_sync(0xffffffffu, q.wait(&shared.sums_full[set], round))) return;
+            float4 s[2] = {};
+            if (n * 8 < cols)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int p = 0; p < kTakers; ++p) {
+                        const float4 v = sums[(((set * kTakers + p) * 2 + m) * NT + n) * 32 + lane];
+                        s[m].x += v.x;
+                        s[m].y += v.y;
+                        s[m].z += v.z;
+                        s[m].w += v.w;
+                    }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&shared.sums_empty[set]);
+            if (n * 8 < cols)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) write_hidden<GATED, PH>(a, first, cols, f0 + m * (kCh / 2), n, g, t, s[m], scale[m]);
+            if (++set == Cf::kSums) {
+                set = 0;
+                round ^= 1u;
+            }
+        }
+        return;
+    }
+    const int k0 = lane_k(warp, t);  // the lane's k of a stage
+    int set = 0;
+    uint32_t round = 0;
+    // the token row of the lane's column of an item's first eight
+    auto row_of = [&](int i) {
+        const Routing::Group of = r.group[i / tiles];
+        return g < of.cols ? static_cast<const T *>(a.X) + static_cast<long long>(r.column[of.first + g].token) * a.ldx : nullptr;
+    };
+    // One stage ahead: the elements come from L2 where L1 does not hold them, and a warp that
+    // waits for them holds the ring up.
+    Raw<El> ahead{};
+    if (static_cast<int>(blockIdx.x) < items) ahead = fetch_token<El, true>(row_of(blockIdx.x), k0, a.width);
+    for (int i = blockIdx.x; i < items; i += gridDim.x) {
+        const bool another = i + static_cast<int>(gridDim.x) < items;
+        const T *after = another ? row_of(i + gridDim.x) : nullptr;
+        const int group = i / tiles;
+        const Routing::Group here = r.group[group];
+        const int e = here.expert, first = here.first, cols = here.cols;
+        const T *x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            x[n] = n * 8 + g < cols ? static_cast<const T *>(a.X) + static_cast<long long>(r.column[first + n * 8 + g].token) * a.ldx : nullptr;
+        float acc[2][NT][4] = {};
+        for (int s = 0; s < segs; ++s) {
+            const int k = s * kSeg + k0;
+            uint32_t v[P][8];
+            split_token<El>(ahead, v);
+            if (s + 1 < segs) ahead = fetch_token<El, true>(x[0], k + kSeg, a.width);
+            else if (another) ahead = fetch_token<El, true>(after, k0, a.width);
+            if (!q.get()) return;
+            if (k - 2 * t * 16 < a.width) {  // (the warp's first k)
+                uint32_t w[2][4][4];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    uint4 lo, hi;
+                    q.take((GATED ? 8 : 16) * m + g, GATED ? 16 + 8 * m + g : 16 * m + 8 + g, warp / 2, 2 * t + (warp & 1), lo, hi);
+                    expand_rows<Mma>(lo, hi, w[m]);
+                    multiply<Mma, P>(acc[m][0], w[m], v);
+                }
+#pragma unroll
+                for (int n = 1; n < NT; ++n) {
+                    if (n * 8 >= cols) break;
+                    split_token<El>(fetch_token<El, true>(x[n], k, a.width), v);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) multiply<Mma, P>(acc[m][n], w[m], v);
+                }
+            }
+            q.done(lane);
+        }
+        if (!__all_sync(0xffffffffu, q.wait(&shared.sums_empty[set], round ^ 1u))) return;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (n * 8 < cols)
+                    sums[(((set * kTakers + warp) * 2 + m) * NT + n) * 32 + lane] = make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&shared.sums_full[set]);
+        if (++set == Cf::kSums) {
+            set = 0;
+            round ^= 1u;
+        }
+    }
+}
+
+// As down_kernel, with a grid of as many CTAs as run at once; a stage is 16 channels' rows of up
+// to 1024 hidden values of a group.  Two teams of eight warps take the groups in turn, 128
+// bytes of a row each: while one team's loads, sums and waits take their time, the other
+// multiplies (sixteen warps on every stage, 64 bytes each: 75 us for a batch of 8 tokens,
+// most of it instructions that are not the product's).  A lane fetches the hidden values of
+// its team's next stage when it has multiplied one, and the scales of its next group when it
+// begins one.
+template <class El, int NT>
+__global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_stream_kernel(const __grid_constant__ CUtensorMap map, const LayerArgs a) {
+    using Cf = StreamCfg<El, NT>;
+    constexpr int PH = Parts<El>::hidden, S = Cf::kDownStages;
+    extern __shared__ uint8_t smem[];
+    __shared__ StreamShared shared;
+    __shared__ Routing r;
+    Stream<S, 16> q = open_stream<S, 16>(smem, &shared, 1, kTakers / 2, a.status);
+    float *out_sums = reinterpret_cast<float *>(smem + Cf::kDownRing);  // [warp][token][kOutPitch]
+    for (int k = threadIdx.x; k < kTakers * a.tokens * kOutPitch; k += Cf::kDownThreads) out_sums[k] = 0.f;
+    route<Cf::kDownThreads>(r, a, 8 * NT);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int items = (a.width + 15) / 16, step = static_cast<int>(gridDim.x), groups = r.groups;
+    if (warp == kTakers) {
+        if (lane > 0) return;
+        // (the weights: the kernel before does not write them, and has waited for what came
+        // before it, so that they may be under way before its end)
+        for (int i = blockIdx.x; i < items; i += step)
+            for (int group = 0; group < groups; ++group)
+                for (int k = 0; k < a.hidden; k += kSeg)
+                    if (!q.put(&map, k, r.group[group].expert * a.width + i * 16, 0)) return;
+        return;
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    const int team = warp / (kTakers / 2), column = warp % (kTakers / 2);  // of 128 bytes
+    const bool idle = column * 128 >= a.hidden;                            // (short rows leave columns out)
+    float *mine = out_sums + warp * a.tokens * kOutPitch;
+    bool ok = true;
+    uint32_t ahead[2][PH][8] = {};
+    // the lane's 32 hidden values of a stage of the group's first eight columns
+    const uint16_t *h_lane = a.h + column * 128 + t * 32;
+    auto fetch = [&](const Routing::Group &of, int k) {
+        if (g < of.cols && k + column * 128 < a.hidden) {
+            const uint16_t *h = h_lane + (static_cast<long long>(of.first + g) * a.hidden_ld + k);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) load_hidden<PH>(h + c * 16, a.h_part, 0, ahead[c]);
+        }
+    };
+    // The team's groups: those of its parity, counted over all items, so that both have as many.
+    Routing::Group here{};
+    float next_l = 0.f, next_h = 0.f;
+    int group = team, item = blockIdx.x;  // the next of them
+    auto settle = [&]() {
+        while (group >= groups && item < items) {
+            group -= groups;
+            item += step;
+        }
+        if (item >= items) return false;
+        here = r.group[group];
+        const int d = item * 16 + g;
+        const float *scale = a.down_scale + (static_cast<long long>(here.expert) * a.width + d);
+        next_l = d < a.width ? __ldca(scale) : 0.f;
+        next_h = d + 8 < a.width ? __ldca(scale + 8) : 0.f;
+        return true;
+    };
+    bool another = groups > 0 && settle();
+    if (another) fetch(here, 0);
+    int turn = team;  // 0: the group is the team's
+    for (int i = blockIdx.x; i < items; i += step) {
+        for (int n_group = 0; n_group < groups; ++n_group, turn ^= 1) {
+            if (turn) {
+                for (int k = 0; k < a.hidden; k += kSeg) q.step();
+                continue;
+            }
+            const Routing::Group now = here;
+            const float sl = next_l, sh = next_h;
+            group += 2;
+            another = settle();
+            float acc[NT][4] = {};
+            for (int k = 0; k < a.hidden; k += kSeg) {
+                ok = ok && q.get();  // (after a wait that ran out the warps still meet at the barriers)
+                if (!ok) break;
+                if (k + column * 128 < a.hidden) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint4 lo, hi;
+                        q.take(g, 8 + g, column, 2 * t + c, lo, hi);
+                        uint32_t w[4][4];
+                        expand_rows<ElBF16>(lo, hi, w);
+                        multiply<ElBF16, PH>(acc[0], w, ahead[c]);
+#pragma unroll
+                        for (int n = 1; n < NT; ++n) {
+                            if (n * 8 >= now.cols) break;
+                            uint32_t v[PH][8];
+                            load_hidden<PH>(n * 8 + g < now.cols ? h_lane + static_cast<long long>(now.first + n * 8 + g) * a.hidden_ld : nullptr, a.h_part, k + c * 16, v);
+                            multiply<ElBF16, PH>(acc[n], w, v);
+                        }
+                    }
+                }
+                q.done(lane);
+                if (k + kSeg < a.hidden) fetch(now, k + kSeg);
+                else if (another) fetch(here, 0);
+            }
+            if (!idle) add_out<NT>(r, mine, now.first, now.cols, g, t, sl, sh, acc);
+        }
+        named_barrier_sync(1, kTakers * 32);
+        for (int k = threadIdx.x; k < a.tokens * 16; k += kTakers * 32) {
+            const int token = k / 16, d = i * 16 + k % 16;
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kTakers; ++w) {
+                float &part = out_sums[(w * a.tokens + token) * kOutPitch + k % 16];
+                sum += part;
+                part = 0.f;
+            }
+            if (ok && d < a.width) static_cast<typename El::T *>(a.out)[token * a.ldo + d] = El::down(sum);
+        }
+        named_barrier_sync(1, kTakers * 32);
+    }
+}
+
+// The weights' rows, boxes of 128 bytes x 16 rows with the 128-byte swizzle.
+struct LayerMaps {
+    CUtensorMap up, down;
+};
+constexpr long long kMostRows = (1ll << 31) - 64;  // coordinates are ints
+
+template <class El, int NT>
+cudaError_t layer_typed(const LayerArgs &a, bool boundaries, const LayerMaps &m, int num_sms, cudaStream_t stream) {
     // (the groups are on the device: so many there are at most)
     const long long slots = static_cast<long long>(a.tokens) * a.choices, asked = slots < a.experts ? slots : a.experts;
+    auto grid = [](long long ctas, long long most) { return dim3(static_cast<unsigned>(ctas < 1 ? 1 : ctas < most ? ctas : most)); };
+    if (boundaries) {
+        using Cf = StreamCfg<El, NT>;
+        const int kCh = a.gated ? 16 : 32;
+        cudaError_t e = launch_dependent(a.gated ? up_stream_kernel<El, NT, true> : up_stream_kernel<El, NT, false>, grid(slots * ((a.hidden_ld + kCh - 1) / kCh), num_sms),
+                                         dim3(Cf::kUpThreads), Cf::kUpSmem, stream, 1, m.up, m.down, a);
+        if (e != cudaSuccess) return e;
+        return launch_dependent(down_stream_kernel<El, NT>, grid((a.width + 15) / 16, num_sms), dim3(Cf::kDownThreads), Cf::down_smem(a.tokens), stream, 1, m.down, a);
+    }
     const long long items = asked * (a.hidden_ld / (a.gated ? 8 : 16));
     // warps that share an item's K: all eight unless that leaves a CTA many rounds
     int share = kWarps;
     while (share > 1 && items > 4ll * num_sms * (kWarps / share) && (a.width + kChunk - 1) / kChunk <= 2 * share) share /= 2;
-    const long long ctas = (items + kWarps / share - 1) / (kWarps / share), most = 2ll * num_sms;
-    const dim3 grid(static_cast<unsigned>(ctas < 1 ? 1 : ctas < most ? ctas : most));  // (no hidden channels: nothing to do)
-    cudaError_t e = launch_dependent(a.gated ? up_kernel<El, NT, true, VEC> : up_kernel<El, NT, false, VEC>, grid, dim3(kThreads), 0, stream, 1, a, share);
+    cudaError_t e = launch_dependent(a.gated ? up_kernel<El, NT, true> : up_kernel<El, NT, false>, grid((items + kWarps / share - 1) / (kWarps / share), 2ll * num_sms),
+                                     dim3(kThreads), 0, stream, 1, a, share);
     if (e != cudaSuccess) return e;
-    return launch_dependent(down_kernel<El, NT, VEC>, dim3((a.width + 15) / 16), dim3(kThreads), kWarps * a.tokens * kOutPitch * 4, stream, 1, a);
+    return launch_dependent(down_kernel<El, NT>, dim3((a.width + 15) / 16), dim3(kThreads), kWarps * a.tokens * kOutPitch * 4, stream, 1, a);
 }
 
 template <class El>
 cudaError_t layer_for(const LayerArgs &a, int num_sms, cudaStream_t stream) {
     auto at16 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-    const bool vec = at16(a.X) && at16(a.up) && at16(a.down) && a.ldx * sizeof(typename El::T) % 16 == 0 && a.width % 16 == 0 && a.hidden % 16 == 0;
-    // tokens that share an expert's weights in one go: 8 or 32
-    if (a.tokens <= 8) return vec ? layer_typed<El, 1, true>(a, num_sms, stream) : layer_typed<El, 1, false>(a, num_sms, stream);
-    return vec ? layer_typed<El, 4, true>(a, num_sms, stream) : layer_typed<El, 4, false>(a, num_sms, stream);
+    LayerMaps m{};
+    const long long up_rows = a.experts * a.up_rows, down_rows = static_cast<long long>(a.experts) * a.width;
+    const bool boundaries = reinterpret_cast<uintptr_t>(a.X) % 32 == 0 && at16(a.up) && at16(a.down) && a.ldx * sizeof(typename El::T) % 32 == 0 && a.width % 16 == 0 &&
+                            a.hidden % 16 == 0 && a.hidden > 0 && up_rows < kMostRows && down_rows < kMostRows &&
+                            encode_map(&m.up, MapType::kInt8, 2, a.up, a.width, up_rows, 1, a.width, 0, 128, 16) &&
+                            encode_map(&m.down, MapType::kInt8, 2, a.down, a.hidden, down_rows, 1, a.hidden, 0, 128, 16);
+    // tokens that share an expert's weights in one go: 8, 16 or 32
+    if (a.tokens <= 8) return layer_typed<El, 1>(a, boundaries, m, num_sms, stream);
+    if (a.tokens <= 16 || a.tokens * a.choices <= 12 * a.experts) return layer_typed<El, 2>(a, boundaries, m, num_sms, stream);
+    return layer_typed<El, 4>(a, boundaries, m, num_sms, stream);
+}
+
+template <class El, int NT>
+cudaError_t prepare_typed() {
+    constexpr int kSums = kWarps * kLayerTokens * kOutPitch * 4;
+    cudaError_t e = cudaFuncSetAttribute(down_kernel<El, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSums);
+    for (auto *k : {up_stream_kernel<El, NT, false>, up_stream_kernel<El, NT, true>})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<El, NT>::kUpSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(down_stream_kernel<El, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<El, NT>::down_smem(NT == 1 ? 8 : kLayerTokens));
+    return e;
 }
 
 }  // namespace
 
 size_t layer_floats(int type, int slots, int hidden) {
-    const size_t ld = (static_cast<size_t>(hidden) + kChunk - 1) / kChunk * kChunk;
+    const size_t ld = (static_cast<size_t>(hidden) + kPad - 1) / kPad * kPad;
     return (type == SGEMM_IN_F32 ? 3 : 2) * static_cast<size_t>(slots) * ld / 2;
 }
 
 cudaError_t layer_prepare() {
     cudaError_t e = cudaSuccess;
-    for (auto *k : {down_kernel<ElF32, 1, false>, down_kernel<ElF32, 1, true>, down_kernel<ElF32, 4, false>, down_kernel<ElF32, 4, true>,
-                    down_kernel<ElBF16, 1, false>, down_kernel<ElBF16, 1, true>, down_kernel<ElBF16, 4, false>, down_kernel<ElBF16, 4, true>,
-                    down_kernel<ElF16, 1, false>, down_kernel<ElF16, 1, true>, down_kernel<ElF16, 4, false>, down_kernel<ElF16, 4, true>})
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kLayerTokens * kOutPitch * 4);
+    for (cudaError_t r : {prepare_typed<ElF32, 1>(), prepare_typed<ElF32, 2>(), prepare_typed<ElF32, 4>(), prepare_typed<ElBF16, 1>(),
+                          prepare_typed<ElBF16, 2>(), prepare_typed<ElBF16, 4>(), prepare_typed<ElF16, 1>(), prepare_typed<ElF16, 2>(),
+                          prepare_typed<ElF16, 4>()})
+        if (e == cudaSuccess) e = r;
     return e;
 }
 
 cudaError_t launch_expert_layer(int type, LayerArgs a, int num_sms, cudaStream_t stream) {
-    a.hidden_ld = (a.hidden + kChunk - 1) / kChunk * kChunk;
+    a.hidden_ld = (a.hidden + kPad - 1) / kPad * kPad;
     a.up_rows = static_cast<long long>(a.gated ? 2 : 1) * a.hidden;
     a.h_part = static_cast<long long>(a.tokens) * a.choices * a.hidden_ld;
     switch (type) {

@@ -418,6 +418,7 @@ int sgemm_expert_layer_int8(sgemm_handle_t h, int type, int gated, int tokens, i
     a.out = out;
     a.ldo = ldo;
     a.h = reinterpret_cast<uint16_t *>(v.d_ws);
+    a.status = v.d_status;
     const int rc = from_cuda(sg::launch_expert_layer(type, a, v.num_sms, static_cast<cudaStream_t>(stream)));
     if (rc == SGEMM_OK) sg::record_call(h, -1, 1, 2, 0);
     return rc;
