@@ -59,6 +59,22 @@ __device__ __forceinline__ void row_reduce(float &sum, unsigned &top) {
     }
 }
 
+// The largest magnitude of three values; a NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Bits of the largest magnitude of N values, those of a NaN above infinity's.
+template <int N>
+__device__ __forceinline__ unsigned top_of(const float *v) {
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e + 1 < N; e += 2) m = max_abs(m, v[e], v[e + 1]);
+    if (N % 2) m = max_abs(m, v[N - 1], 0.f);
+    return __float_as_uint(m) & 0x7fffffffu;
+}
+
 // Bits of the largest magnitude of the block that this lane's A elements belong to:
 // `lanes` lanes hold it.
 __device__ __forceinline__ unsigned block_max(unsigned top, int lanes) {
@@ -80,10 +96,7 @@ __device__ __forceinline__ void put_fp4(const Fp4Row &r, int c, int lane, const 
     float f[kV / A];
 #pragma unroll
     for (int i = 0; i < kV / A; ++i) {
-        unsigned top = 0;
-#pragma unroll
-        for (int e = 0; e < A; ++e) top = max(top, __float_as_uint(v[i * A + e]) & 0x7fffffffu);
-        top = block_max(top, per);
+        const unsigned top = block_max(top_of<A>(v + i * A), per);
         uint32_t code;
         if (r.format == SGEMM_FP4_MX) {
             // floor(log2) of the block's largest value, less 2 (the exponent of the
@@ -108,8 +121,12 @@ __device__ __forceinline__ void put_fp4(const Fp4Row &r, int c, int lane, const 
     }
     float x[kV];
 #pragma unroll
-    for (int e = 0; e < kV; ++e) x[e] = f[e / A] == 0.f ? 0.f : __fmul_rn(v[e], f[e / A]);
+    for (int e = 0; e < kV; ++e) x[e] = __fmul_rn(v[e], f[e / A]);
     uint32_t w = to_e2m1x8(x);
+    // (a factor of 0: infinities and NaNs among them, whose products are no zeros)
+#pragma unroll
+    for (int i = 0; i < kV / A; ++i)
+        if (f[i] == 0.f) w &= ~((A == 8 ? 0xffffffffu : (1u << (4 * A % 32)) - 1u) << (4 * A * i));
 #pragma unroll
     for (int i = 0; i < kV / A; ++i) {
         const int p = at + i * TPR * A;
@@ -185,21 +202,22 @@ row_kernel(const RowArgs a) {
         float v[kV];
         if (OUT != OUT_Y) scaled(p, q, v);
 #pragma unroll
-        for (int e = 0; e < kV; ++e) {
+        for (int e = 0; e < kV; ++e)
             if (NORM) sum = fmaf(El::up(p.v[e]), El::up(p.v[e]), sum);
-            if (OUT != OUT_Y) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
-        }
+        if (OUT != OUT_Y) top = max(top, top_of<kV>(v));
     };
+    const bool whole = NORM || OUT == OUT_I8 || a.format == SGEMM_FP4_NV;  // whether anything is asked of the whole row
+    if (whole) {
 #pragma unroll
-    for (int c = 0; c < HELD; ++c) look(h[c], g[c]);
-    for (int c = HELD; c * kV * TPR < width; ++c) {
+        for (int c = 0; c < HELD; ++c) look(h[c], g[c]);
+    }
+    for (int c = HELD; whole && c * kV * TPR < width; ++c) {
         Pack8<T> p = load8<T, TPR, A>(x, c, lane, width), q = p;
         if (add) p = sum_of(p, load8<T, TPR, A>(add, c, lane, width));
         if (keep) store8<T, TPR, A>(keep, c, lane, width, p);
         if (NORM) q = load8<T, TPR, A, true>(w, c, lane, width);
         look(p, q);
     }
-    const bool whole = NORM || OUT == OUT_I8 || a.format == SGEMM_FP4_NV;  // whether anything is asked of the whole row
     if (whole) row_reduce<TPR>(sum, top);
     if (!live) return;
     const float r = NORM ? __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(a.K)), a.eps)) : 1.f;

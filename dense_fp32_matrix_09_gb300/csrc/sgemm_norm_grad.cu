@@ -60,47 +60,64 @@ norm_grad_kernel(const NormGradArgs a) {
 #pragma unroll
         for (int e = 0; e < kV; ++e) dw[c][e] = 0.f;
     }
-    // (every group makes as many rounds as the first: the barriers are the block's)
-    int turn = 0;
-    for (unsigned i0 = blockIdx.x * kRows; i0 < static_cast<unsigned>(a.M); i0 += step, turn ^= 1) {
-        const unsigned i = i0 + threadIdx.x / TPR;
+    struct Row {
+        Pack8<T> d[HELD], x[HELD], more[HELD];
+        float r;
+    };
+    auto load = [&](unsigned i) {
+        Row q;
         const bool live = i < static_cast<unsigned>(a.M);
         const long long row = live ? i : 0;
         const int width = live ? a.K : 0;
         const T *dy = static_cast<const T *>(a.dY) + row * a.lddy, *h = static_cast<const T *>(a.H) + row * a.ldh;
-        Pack8<T> d[HELD], x[HELD], more[HELD];
+        const T *dh = static_cast<const T *>(a.dH) + (a.dH ? row * a.lddh : 0);
 #pragma unroll
         for (int c = 0; c < HELD; ++c) {
-            d[c] = load8<T, TPR, A>(dy, c, lane, width);
-            x[c] = load8<T, TPR, A>(h, c, lane, width);
+            q.d[c] = load8<T, TPR, A>(dy, c, lane, width);
+            q.x[c] = load8<T, TPR, A>(h, c, lane, width);
         }
-        const float r = live ? __ldca(a.rstd + i) : 0.f;
         if (a.dH) {
-            const T *dh = static_cast<const T *>(a.dH) + row * a.lddh;
 #pragma unroll
-            for (int c = 0; c < HELD; ++c) more[c] = load8<T, TPR, A>(dh, c, lane, width);
+            for (int c = 0; c < HELD; ++c) q.more[c] = load8<T, TPR, A>(dh, c, lane, width);
         }
+        q.r = live ? __ldca(a.rstd + i) : 0.f;
+        return q;
+    };
+    // The next row is on its way while one is added up and written (one row at a time: 8192 x 4096
+    // BF16 with both gradients 71 us); rows of 32 elements a thread leave no registers for it.
+    constexpr bool kEarly = HELD < 4;
+    // (every group makes as many rounds as the first: the barriers are the block's)
+    int turn = 0;
+    unsigned i0 = blockIdx.x * kRows;
+    const unsigned mine = threadIdx.x / TPR;
+    Row next;
+    if (kEarly) next = load(i0 + mine);
+    for (; i0 < static_cast<unsigned>(a.M); i0 += step, turn ^= 1) {
+        const unsigned i = i0 + mine;
+        const bool live = i < static_cast<unsigned>(a.M);
+        const Row q = kEarly ? next : load(i);
+        if (kEarly && i0 + step < static_cast<unsigned>(a.M)) next = load(i + step);
         float sum = 0.f;
 #pragma unroll
         for (int c = 0; c < HELD; ++c)
 #pragma unroll
-            for (int e = 0; e < kV; ++e) sum = fmaf(El::up(d[c].v[e]) * El::up(g[c].v[e]), El::up(x[c].v[e]), sum);
+            for (int e = 0; e < kV; ++e) sum = fmaf(El::up(q.d[c].v[e]) * El::up(g[c].v[e]), El::up(q.x[c].v[e]), sum);
         sum = row_sum<TPR>(sum, part[turn]);
-        const float f = sum * r * r / static_cast<float>(a.K);
-        T *dx = static_cast<T *>(a.dX) + row * a.lddx;
+        const float f = sum * q.r * q.r / static_cast<float>(a.K);
+        T *dx = static_cast<T *>(a.dX) + (live ? i * a.lddx : 0);
 #pragma unroll
         for (int c = 0; c < HELD; ++c) {
             Pack8<T> o;
 #pragma unroll
             for (int e = 0; e < kV; ++e) {
-                const float dv = El::up(d[c].v[e]), hv = El::up(x[c].v[e]);
+                const float dv = El::up(q.d[c].v[e]), hv = El::up(q.x[c].v[e]);
                 // (lanes behind a row's end and rows behind the last hold zeros: nothing is added)
-                dw[c][e] = fmaf(dv, hv * r, dw[c][e]);
-                float v = r * fmaf(-hv, f, dv * El::up(g[c].v[e]));
-                if (a.dH) v += El::up(more[c].v[e]);
+                dw[c][e] = fmaf(dv, hv * q.r, dw[c][e]);
+                float v = q.r * fmaf(-hv, f, dv * El::up(g[c].v[e]));
+                if (a.dH) v += El::up(q.more[c].v[e]);
                 o.v[e] = El::down(v);
             }
-            if (live) store8<T, TPR, A>(dx, c, lane, width, o);
+            if (live) store8<T, TPR, A>(dx, c, lane, a.K, o);
         }
     }
     float *to = a.parts + static_cast<long long>(group) * a.K;
