@@ -1,7 +1,7 @@
 """ctypes binding of libsgemm.so, with the entry-point names of include/sgemm.h.
 
-Argument marshalling only: every step of C = alpha*A*B + beta*C, of the int8
-products and of the expert routing runs in the CUDA library.  Matrix arguments may be raw device addresses (int) or objects
+Argument marshalling only: every step of C = alpha*A*B + beta*C, of the int8 and
+4-bit products, the norm and the expert calls runs in the CUDA library.  Matrix arguments may be raw device addresses (int) or objects
 with ``data_ptr()`` (torch tensors); streams may be an int handle, a
 ``torch.cuda.Stream`` or ``None`` (torch's current stream).  A non-zero
 status raises ``SgemmError``.  If the library has not been built the first
@@ -13,6 +13,7 @@ import contextlib
 import ctypes
 import operator
 import os
+import typing
 
 from . import build as _build
 
@@ -698,6 +699,49 @@ def _result(out, M, N, out_dtype, device):
     return out
 
 
+class Fp4Rows(typing.NamedTuple):
+    """Rows in 4-bit floating point: what the tensor methods hand round (see include/sgemm.h)."""
+    Q: object        # rows x bytes, uint8: two elements a byte
+    S: object        # the blocks' scales in tiles of 128 rows x 4 blocks, uint8
+    row: object      # one FP32 a row, or None (MX only)
+    K: int           # elements a row
+    format: int      # FP4_MX or FP4_NV
+
+
+def fp4_blocks(fmt, K) -> int:
+    """Blocks of a row of K elements."""
+    return -(-K // (32 if fmt == FP4_MX else 16))
+
+
+def fp4_tile_scales(scales, fmt, K):
+    """Scale bytes of rows x blocks (uint8, as other libraries keep them) in the tiles that the 4-bit
+    calls read, zeros behind the last row and block."""
+    import torch
+    rows, blocks = scales.shape
+    if scales.dtype != torch.uint8 or blocks != fp4_blocks(fmt, K):
+        raise ValueError(f"scales must be uint8, rows x {fp4_blocks(fmt, K)}, got {scales.dtype} {tuple(scales.shape)}")
+    full = torch.zeros(-(-rows // 128) * 128, -(-blocks // 4) * 4, dtype=torch.uint8, device=scales.device)
+    full[:rows, :blocks] = scales
+    return full.view(-1, 4, 32, full.shape[1] // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1).contiguous()
+
+
+def _fp4(name, a) -> None:
+    """The parts of rows in 4 bits fit together."""
+    import torch
+    if a.format not in (FP4_MX, FP4_NV):
+        raise ValueError(f"{name}: unknown 4-bit format {a.format}")
+    _rows_of(f"{name}.Q", a.Q, torch.uint8)
+    rows, need = a.Q.shape[0], sgemm_fp4_scale_bytes(a.format, a.Q.shape[0], a.K)
+    if a.K < 0 or a.Q.shape[1] < (a.K + 1) // 2:
+        raise ValueError(f"{name}: rows of {a.Q.shape[1]} bytes do not hold {a.K} elements")
+    if a.S.dtype != torch.uint8 or a.S.dim() != 1 or not a.S.is_contiguous() or a.S.numel() < need:
+        raise ValueError(f"{name}.S must be a contiguous uint8 vector of at least {need}")
+    if a.row is not None:
+        _vector(f"{name}.row", a.row, rows)
+    elif a.format == FP4_NV:
+        raise ValueError(f"{name}.row is wanted with FP4_NV")
+
+
 class Sgemm:
     """A handle as a context manager: ``with Sgemm() as g: g.run(...)``.
 
@@ -869,6 +913,156 @@ class Sgemm:
             sgemm_expert_combine_grad(self.h, _element_type(Y), tokens, choices, Y.shape[1], dout, _ld(dout), Y, _ld(Y),
                                       rows, weights, dY, _ld(dY), dweights)
         return dY, dweights
+
+    # -- 4-bit floating point, the RMS norm and the whole expert layer --------------------
+    def quantize_fp4(self, X, format=FP4_MX, stream=None):
+        """The rows of X (2-D, FP32/BF16/FP16) in 4 bits, as Fp4Rows (row scales with FP4_NV)."""
+        _on_device(X=X)
+        kind = _element_type(X)
+        _rows_of("X", X)
+        with _on(stream, X):
+            out = self._fp4_out(X, format, format == FP4_NV)
+            sgemm_quantize_fp4(self.h, kind, format, X.shape[0], X.shape[1], X, _ld(X), out.Q, _ld(out.Q), out.S, out.row)
+        return out
+
+    @staticmethod
+    def _fp4_out(X, format, with_row):
+        import torch
+        (M, K), new = X.shape, dict(device=X.device)
+        n = sgemm_fp4_scale_bytes(format, M, K)
+        if n < 0:
+            raise ValueError(f"unknown 4-bit format {format}")
+        # rows on 16-byte boundaries; scales of rows behind the last are read with them, so zeros
+        return Fp4Rows(torch.empty(M, max(-(-K // 32) * 16, 1), dtype=torch.uint8, **new), torch.zeros(n, dtype=torch.uint8, **new),
+                       torch.empty(M, dtype=torch.float32, **new) if with_row else None, K, format)
+
+    def dequantize_fp4(self, A, out_dtype=None, out=None, stream=None):
+        """What 4-bit rows stand for (BF16 unless `out_dtype` or `out` says otherwise)."""
+        _on_device(Q=A.Q, S=A.S, row=A.row, out=out)
+        _fp4("A", A)
+        M = A.Q.shape[0]
+        with _on(stream, A.Q, A.S, A.row, out):
+            out = _result(out, M, A.K, out_dtype, A.Q.device)
+            sgemm_dequantize_fp4(self.h, _element_type(out), A.format, M, A.K, A.Q, _ld(A.Q), A.S, A.row, out, _ld(out))
+        return out
+
+    def matmul_fp4(self, A, B, bias=None, out_dtype=None, out=None, stream=None):
+        """A @ B.T + bias for A (M rows) and B (N rows) in the same 4-bit format; `out_dtype` (BF16
+        unless given) or `out` says of which type."""
+        _on_device(**{"A.Q": A.Q, "A.S": A.S, "A.row": A.row, "B.Q": B.Q, "B.S": B.S, "B.row": B.row, "bias": bias, "out": out})
+        _fp4("A", A)
+        _fp4("B", B)
+        if A.K != B.K or A.format != B.format:
+            raise ValueError(f"A and B differ: {A.K} and {B.K} elements a row, formats {A.format} and {B.format}")
+        M, N = A.Q.shape[0], B.Q.shape[0]
+        if bias is not None:
+            _vector("bias", bias, N)
+        with _on(stream, A.Q, A.S, A.row, B.Q, B.S, B.row, bias, out):
+            out = _result(out, M, N, out_dtype, A.Q.device)
+            sgemm_run_fp4(self.h, A.format, _element_type(out), M, N, A.K, A.Q, _ld(A.Q), A.S, A.row, B.Q, _ld(B.Q), B.S,
+                          B.row, bias, out, _ld(out))
+        return out
+
+    @staticmethod
+    def _norm_rows(X, weight, residual):
+        _on_device(X=X, weight=weight, residual=residual)
+        _element_type(X)
+        _rows_of("X", X)
+        _vector("weight", weight, X.shape[1], X.dtype)
+        if residual is not None:
+            _rows_of("residual", residual, X.dtype)
+            if residual.shape != X.shape:
+                raise ValueError(f"residual must be {tuple(X.shape)}, got {tuple(residual.shape)}")
+
+    @staticmethod
+    def _norm_args(X, weight, residual, eps, H):
+        return (X, _ld(X), residual, _ld(residual) if residual is not None else 0, weight, eps, H,
+                _ld(H) if H is not None else 0)
+
+    def rms_norm(self, X, weight, residual=None, eps=1e-5, stream=None):
+        """(Y, H, rstd): H = X + residual (X itself without one), Y = H * weight / rms(H), rstd = 1 / rms."""
+        import torch
+        self._norm_rows(X, weight, residual)
+        M, K = X.shape
+        with _on(stream, X, weight, residual):
+            Y = torch.empty(M, K, dtype=X.dtype, device=X.device)
+            H = torch.empty_like(Y) if residual is not None else None
+            # (rows of no elements are not touched)
+            rstd = torch.empty(M, dtype=torch.float32, device=X.device) if K else torch.zeros(M, device=X.device)
+            sgemm_rms_norm(self.h, _element_type(X), M, K, *self._norm_args(X, weight, residual, eps, H), Y, _ld(Y), rstd)
+        return Y, X if H is None else H, rstd
+
+    def rms_norm_int8(self, X, weight, residual=None, eps=1e-5, stream=None):
+        """(Q, scale, H): the normed rows in 8 bits with a scale a row, and H."""
+        import torch
+        self._norm_rows(X, weight, residual)
+        M, K = X.shape
+        with _on(stream, X, weight, residual):
+            Q = torch.empty(M, K, dtype=torch.int8, device=X.device)
+            scale = torch.zeros(M, dtype=torch.float32, device=X.device)
+            H = torch.empty(M, K, dtype=X.dtype, device=X.device) if residual is not None else None
+            sgemm_rms_norm_int8(self.h, _element_type(X), M, K, *self._norm_args(X, weight, residual, eps, H), Q, _ld(Q), scale)
+        return Q, scale, X if H is None else H
+
+    def rms_norm_fp4(self, X, weight, residual=None, eps=1e-5, format=FP4_MX, stream=None):
+        """(rows, H): the normed rows in 4 bits (Fp4Rows, with row scales in either format), and H."""
+        import torch
+        self._norm_rows(X, weight, residual)
+        M, K = X.shape
+        with _on(stream, X, weight, residual):
+            out = self._fp4_out(X, format, True)
+            H = torch.empty(M, K, dtype=X.dtype, device=X.device) if residual is not None else None
+            sgemm_rms_norm_fp4(self.h, _element_type(X), format, M, K, *self._norm_args(X, weight, residual, eps, H), out.Q,
+                               _ld(out.Q), out.S, out.row)
+        return out, X if H is None else H
+
+    def rms_norm_grad(self, dY, H, weight, rstd, dH=None, stream=None):
+        """(dX, dweight) of rms_norm from the gradients of its Y and, if it has one, of its H; dX is the
+        gradient of X and of the residual, dweight FP32."""
+        import torch
+        _on_device(dY=dY, H=H, weight=weight, rstd=rstd, dH=dH)
+        kind = _element_type(H)
+        _rows_of("H", H)
+        for name, t in (("dY", dY), ("dH", dH)):
+            if t is not None:
+                _rows_of(name, t, H.dtype)
+                if t.shape != H.shape:
+                    raise ValueError(f"{name} must be {tuple(H.shape)}, got {tuple(t.shape)}")
+        M, K = H.shape
+        _vector("weight", weight, K, H.dtype)
+        _vector("rstd", rstd, M)
+        with _on(stream, dY, H, weight, rstd, dH):
+            dX = torch.empty(M, K, dtype=H.dtype, device=H.device)
+            dweight = torch.empty(K, dtype=torch.float32, device=H.device)
+            sgemm_rms_norm_grad(self.h, kind, M, K, dY, _ld(dY), dH, _ld(dH) if dH is not None else 0, H, _ld(H), weight,
+                                rstd, dX, _ld(dX), dweight)
+        return dX, dweight
+
+    def expert_layer_int8(self, X, ids, weights, up, up_scale, down, down_scale, gated=False, stream=None):
+        """sum_j weights[t, j] * down_e(act(up_e(X[t]))), e = ids[t, j], for up to 64 tokens: up (experts x
+        hidden x width, with `gated` 2 * hidden: silu of the first half times the second) and down
+        (experts x width x hidden) in int8 with scales a channel."""
+        import torch
+        _on_device(X=X, ids=ids, weights=weights, up=up, up_scale=up_scale, down=down, down_scale=down_scale)
+        kind = _element_type(X)
+        _rows_of("X", X)
+        T, W = X.shape
+        if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous() or ids.shape[0] != T:
+            raise ValueError("ids must be a contiguous tokens x choices int32 tensor")
+        _weights(weights, T, ids.shape[1])
+        if down.dim() != 3 or down.shape[1] != W:
+            raise ValueError(f"down must be experts x {W} x hidden, got {tuple(down.shape)}")
+        E, _, F = down.shape
+        rows = (2 if gated else 1) * F
+        for name, t, shape, dtype in (("up", up, (E, rows, W), torch.int8), ("up_scale", up_scale, (E, rows), torch.float32),
+                                      ("down", down, (E, W, F), torch.int8), ("down_scale", down_scale, (E, W), torch.float32)):
+            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {' x '.join(map(str, shape))} {dtype} tensor, got {t.dtype} {tuple(t.shape)}")
+        with _on(stream, X, ids, weights, up, up_scale, down, down_scale):
+            out = torch.empty(T, W, dtype=X.dtype, device=X.device)
+            sgemm_expert_layer_int8(self.h, kind, int(gated), T, ids.shape[1], E, W, F, X, _ld(X), ids, weights, up, up_scale,
+                                    down, down_scale, out, _ld(out))
+        return out
 
     @property
     def last_variant(self):

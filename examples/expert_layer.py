@@ -1,8 +1,12 @@
 """A mixture-of-experts layer on the library's calls.
 
+Before it, a layer's norm with the residual's addition and its product in 4-bit floating
+point (ServedLinear), and the norm as an autograd function (Norm).
+
 Serving: the router's choices are sorted by expert, the tokens' rows are moved to
 their experts and quantized on the way, two int8 products with each expert's
-weights (an activation between them, quantized again) and the weighted way back.
+weights (an activation between them, quantized again) and the weighted way back; a
+few tokens go through the whole layer in two launches.
 
 Training: dispatch and combine as autograd functions around FP32 products of
 each expert's rows (sgemm_run_ex), one step of gradient descent on a small target.
@@ -45,6 +49,41 @@ class ServedExperts:
         q, scale = g.quantize(torch.nn.functional.silu(h))
         y = g.matmul_int8_experts(offsets, q, scale, self.down, self.down_scale, out_dtype=x.dtype)
         return g.expert_combine(y, rows, weights)
+
+    def few(self, x, ids, weights):
+        """The same layer for up to 64 tokens (a decode step) in two launches, its activations not quantized."""
+        return self.g.expert_layer_int8(x, ids, weights, self.up, self.up_scale, self.down, self.down_scale)
+
+
+class ServedLinear:
+    """The norm before a layer and the layer itself in 4 bits: weights quantized once, rows on their way."""
+
+    def __init__(self, g: sgemm.Sgemm, norm, weight, format=sgemm.FP4_NV):
+        self.g, self.norm, self.format = g, norm, format
+        self.weight = g.quantize_fp4(weight, format)
+
+    def __call__(self, x, residual, eps=1e-5):
+        """(norm(x + residual) @ weight.T, x + residual)."""
+        rows, h = self.g.rms_norm_fp4(x, self.norm, residual, eps, self.format)
+        return self.g.matmul_fp4(rows, self.weight, out_dtype=x.dtype), h
+
+
+class Norm(torch.autograd.Function):
+    """(norm(x + residual) * weight, x + residual); both are differentiable."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, g):
+        ctx.g = g
+        y, h, rstd = g.rms_norm(x, weight, residual, eps)
+        ctx.save_for_backward(h, weight, rstd)
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh):
+        h, weight, rstd = ctx.saved_tensors
+        dx, dweight = ctx.g.rms_norm_grad(dy.contiguous(), h, weight, rstd, dh.contiguous())
+        return dx, dx, dweight.to(weight.dtype), None, None
 
 
 class Dispatch(torch.autograd.Function):
@@ -133,6 +172,12 @@ def main() -> None:
         want = plain_forward(x.double(), ids, weights.double(), up.double(), down.double())
         served = ServedExperts(g, up, down)(x.bfloat16(), ids, weights)
         print(f"served (int8): relative error {float((served.double() - want).norm() / want.norm()):.4f}")
+        few = ServedExperts(g, up, down).few(x[:16].bfloat16(), ids[:16].contiguous(), weights[:16].contiguous())
+        print(f"served, 16 tokens in two launches: relative error {float((few.double() - want[:16]).norm() / want[:16].norm()):.4f}")
+        residual, norm, matrix = randn(tokens, width), 1 + randn(width) / 10, randn(hidden, width) / width ** 0.5
+        y, h = ServedLinear(g, norm.bfloat16(), matrix.bfloat16())(x.bfloat16(), residual.bfloat16())
+        plain = h.double() / (h.double().square().mean(1, keepdim=True) + 1e-5).sqrt() * norm.double() @ matrix.double().T
+        print(f"normed and multiplied in 4 bits: relative error {float((y.double() - plain).norm() / plain.norm()):.3f}")
         params = [t.clone().requires_grad_() for t in (x, weights, up, down)]
         out = trained_forward(g, params[0], ids, *params[1:])
         print(f"trained (FP32): relative error {float((out.detach().double() - want).norm() / want.norm()):.2e}")
