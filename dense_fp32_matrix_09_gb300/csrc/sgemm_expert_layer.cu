@@ -26,6 +26,7 @@
 #include "internal.h"
 #include "rows.cuh"
 #include "sgemm.h"
+#include "tcgen05.cuh"
 
 namespace sg {
 namespace {
@@ -100,12 +101,10 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
 // by expert, the earlier first.  A token that names an expert twice has one column
 // with the sum of both weights.
 struct Routing {
-    int id[kSlots];            // the slot's expert, -1: none of its own
     struct Column {
         int token;
         float weight;
     } column[kSlots];
-    int start[kMaxExperts + 1];  // first column of an expert
     struct alignas(8) Group {
         int expert;
         short first, cols;  // its columns: up to 8 * NT of one expert's
@@ -113,14 +112,68 @@ struct Routing {
     int groups;
 };
 
+// What the sort needs meanwhile.
+struct RouteScratch {
+    int id[kSlots];              // the slot's expert, -1: none of its own
+    float weight[kSlots];        // by slot
+    int start[kMaxExperts + 1];  // an expert's columns, then its first
+};
+
+// Up to 32 choices: one warp, a choice a lane.
+__device__ __forceinline__ void route_warp(Routing &r, const LayerArgs &a, int per_group) {
+    const int lane = threadIdx.x, slots = a.tokens * a.choices;
+    const int id0 = lane < slots ? __ldcg(a.ids + lane) : -1;
+    const float w0 = lane < slots ? __ldcg(a.weights + lane) : 0.f;
+    const int token = lane / a.choices;
+    int id = static_cast<unsigned>(id0) < static_cast<unsigned>(a.experts) ? id0 : -1;
+    float weight = 0.f;
+    bool own = id >= 0;
+    for (int q = 0; q < a.choices; ++q) {  // the token's choices, in their order
+        const int at = (token * a.choices + q) & 31, other = __shfl_sync(0xffffffffu, id, at);
+        const float w = __shfl_sync(0xffffffffu, w0, at);
+        if (other == id && at < lane) own = false;
+        if (other == id && at >= lane) weight += w;
+    }
+    if (!own) id = -1;
+    // columns before this lane's, columns of its expert; then the experts' groups before its own
+    int before = 0, same = 0, rank = 0;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+        const int other = __shfl_sync(0xffffffffu, id, q);
+        before += other >= 0 && other < id;
+        same += other == id;
+        rank += other == id && q < lane;
+    }
+    const bool leads = own && rank == 0;
+    const int mine = leads ? (same + per_group - 1) / per_group : 0;
+    int groups = 0, first_group = 0;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+        const int n = __shfl_sync(0xffffffffu, mine, q), other = __shfl_sync(0xffffffffu, id, q);
+        groups += n;
+        if (other < id) first_group += n;
+    }
+    for (int k = 0; k < mine; ++k)
+        r.group[first_group + k] = {id, static_cast<short>(before + k * per_group), static_cast<short>(min(per_group, same - k * per_group))};
+    if (own) r.column[before + rank] = {token, weight};
+    if (lane == 0) r.groups = groups;
+}
+
 template <int THREADS>
-__device__ void route(Routing &r, const LayerArgs &a, int per_group) {
+__device__ void route(Routing &r, RouteScratch &w, const LayerArgs &a, int per_group) {
     constexpr int kEach = (kSlots + THREADS - 1) / THREADS;
     const int slots = a.tokens * a.choices, tid = threadIdx.x;
-    for (int e = tid; e <= a.experts; e += THREADS) r.start[e] = 0;
+    if (slots <= 32) {
+        if (tid < 32) route_warp(r, a, per_group);
+        __syncthreads();
+        return;
+    }
+    for (int e = tid; e <= a.experts; e += THREADS) w.start[e] = 0;
     for (int s = tid; s < slots; s += THREADS) {
         const int id = __ldcg(a.ids + s);
-        r.id[s] = static_cast<unsigned>(id) < static_cast<unsigned>(a.experts) ? id : -1;
+        const float weight = __ldcg(a.weights + s);
+        w.id[s] = static_cast<unsigned>(id) < static_cast<unsigned>(a.experts) ? id : -1;
+        w.weight[s] = weight;
     }
     __syncthreads();
     // slots that repeat an earlier choice of their token add to its weight
@@ -129,27 +182,27 @@ __device__ void route(Routing &r, const LayerArgs &a, int per_group) {
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
         const int s = tid + k * THREADS;
-        own[k] = s < slots && r.id[s] >= 0;
+        own[k] = s < slots && w.id[s] >= 0;
         mine[k] = 0.f;
         if (!own[k]) continue;
         const int t0 = s / a.choices * a.choices;
-        for (int q = t0; q < s; ++q) own[k] = own[k] && r.id[q] != r.id[s];
+        for (int q = t0; q < s; ++q) own[k] = own[k] && w.id[q] != w.id[s];
         for (int q = s; q < t0 + a.choices; ++q)
-            if (r.id[q] == r.id[s]) mine[k] += __ldcg(a.weights + q);
+            if (w.id[q] == w.id[s]) mine[k] += w.weight[q];
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
         const int s = tid + k * THREADS;
         if (s >= slots) continue;
-        if (own[k]) atomicAdd(&r.start[r.id[s]], 1);
-        else r.id[s] = -1;
+        if (own[k]) atomicAdd(&w.start[w.id[s]], 1);
+        else w.id[s] = -1;
     }
     __syncthreads();
     if (tid < 32) {  // counts to first columns; the groups
         int cols = 0, groups = 0;
         for (int e0 = 0; e0 < a.experts; e0 += 32) {
-            const int e = e0 + tid, n = e < a.experts ? r.start[e] : 0, g = (n + per_group - 1) / per_group;
+            const int e = e0 + tid, n = e < a.experts ? w.start[e] : 0, g = (n + per_group - 1) / per_group;
             int sn = n, sg = g;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -159,25 +212,22 @@ __device__ void route(Routing &r, const LayerArgs &a, int per_group) {
                     sg += ug;
                 }
             }
-            if (e < a.experts) r.start[e] = cols + sn - n;
+            if (e < a.experts) w.start[e] = cols + sn - n;
             for (int k = 0; k < g; ++k)
                 r.group[groups + sg - g + k] = {e, static_cast<short>(cols + sn - n + k * per_group),
                                                 static_cast<short>(min(per_group, n - k * per_group))};
             cols += __shfl_sync(0xffffffffu, sn, 31);
             groups += __shfl_sync(0xffffffffu, sg, 31);
         }
-        if (tid == 0) {
-            r.start[a.experts] = cols;
-            r.groups = groups;
-        }
+        if (tid == 0) r.groups = groups;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
         const int s = tid + k * THREADS;
-        if (s >= slots || r.id[s] < 0) continue;
-        int c = r.start[r.id[s]];
-        for (int q = 0; q < s; ++q) c += r.id[q] == r.id[s];
+        if (s >= slots || w.id[s] < 0) continue;
+        int c = w.start[w.id[s]];
+        for (int q = 0; q < s; ++q) c += w.id[q] == w.id[s];
         r.column[c] = {s / a.choices, mine[k]};
     }
     __syncthreads();
@@ -239,19 +289,12 @@ __device__ __forceinline__ void split_token(const Raw<El> &r, uint32_t (&to)[Par
 }
 
 // acc += 16 channels x 64 k (lo: channel g, hi: channel g + 8) times 8 tokens.
-// (two chains of additions: an MMA waits for the one before it in its chain)
 template <class Mma, int P>
 __device__ __forceinline__ void multiply(float (&acc)[4], const uint32_t (&a)[4][4], const uint32_t (&x)[P][8]) {
-    float more[4] = {};
 #pragma unroll
-    for (int s = 0; s < 4; s += 2)
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int p = P - 1; p >= 0; --p) {
-            mma16<Mma>(more, a[s], x[p][2 * s], x[p][2 * s + 1]);
-            mma16<Mma>(acc, a[s + 1], x[p][2 * s + 2], x[p][2 * s + 3]);
-        }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] += more[c];
+        for (int p = P - 1; p >= 0; --p) mma16<Mma>(acc, a[s], x[p][2 * s], x[p][2 * s + 1]);
 }
 template <class Mma>
 __device__ __forceinline__ void expand_rows(const uint4 &lo, const uint4 &hi, uint32_t (&a)[4][4]) {
@@ -341,10 +384,11 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const LayerArgs a, int 
     using Mma = typename Parts<El>::Mma;
     constexpr int P = Parts<El>::in, PH = Parts<El>::hidden, kCh = GATED ? 8 : 16;
     __shared__ Routing r;
+    __shared__ RouteScratch scratch;
     __shared__ float4 sums[kWarps][NT][32];
     griddep_wait();
     griddep_launch_dependents();
-    route<kThreads>(r, a, 8 * NT);
+    route<kThreads>(r, scratch, a, 8 * NT);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int tiles = a.hidden_ld / kCh, teams = kWarps / share, team = warp / share, part = warp % share;
     const long long items = static_cast<long long>(r.groups) * tiles;
@@ -418,10 +462,11 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const LayerArgs a) {
     constexpr int PH = Parts<El>::hidden;
     extern __shared__ float out_sums[];  // [warp][token][kOutPitch]
     __shared__ Routing r;
+    __shared__ RouteScratch scratch;
     // (the routing and the sums touch nothing that the kernel before writes, and that
     // one has waited for what came before it)
     for (int k = threadIdx.x; k < kWarps * a.tokens * kOutPitch; k += kThreads) out_sums[k] = 0.f;
-    route<kThreads>(r, a, 8 * NT);
+    route<kThreads>(r, scratch, a, 8 * NT);
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -490,15 +535,19 @@ constexpr int kTakers = kSeg / kChunk;
 template <class El, int NT>
 struct StreamCfg {
     static constexpr int kUpStages = NT <= 2 ? 4 : 3;              // of 32 rows
-    static constexpr int kSums = NT == 1 ? 2 : 1;                  // sets of sums
+    static constexpr int kSums = NT <= 2 ? 2 : 1;                  // sets of sums
     static constexpr int kSumBytes = kTakers * 2 * NT * 512;       // of a set
     static constexpr int kUpThreads = (kTakers + 1 + NT) * 32, kDownThreads = (kTakers + 1) * 32;
     static constexpr int kUpRing = 1024 + kUpStages * 32 * kSeg, kUpSmem = kUpRing + kSums * kSumBytes;
-    static constexpr int kDownStages = NT == 1 ? 8 : 6;            // of 16 rows
+    // Hidden values of two of a warp's stages in shared memory, where that has room for them.
+    static constexpr bool kHeld = NT == 1 && Parts<El>::hidden == 2;
+    static constexpr int kHeldBytes = kHeld ? 2 * Parts<El>::hidden * 1024 : 0;  // of a stage
+    static constexpr int kDownStages = kHeld ? 4 : NT == 1 ? 8 : 6;  // of 16 rows, half of them a team's
     static constexpr int kDownRing = 1024 + kDownStages * 16 * kSeg;
-    static constexpr int down_smem(int tokens) { return kDownRing + kTakers * tokens * kOutPitch * 4; }
-    // the most tokens of a call on this configuration; the routing takes less than 25 KiB
-    static_assert(down_smem(NT == 1 ? 8 : kLayerTokens) <= 232448 - 25600 && kUpSmem <= 232448 - 25600, "shared memory");
+    static constexpr int down_smem(int tokens) { return kDownRing + kTakers * (2 * kHeldBytes + tokens * kOutPitch * 4); }
+    static_assert(sizeof(RouteScratch) <= 2 * 16 * kSeg, "the routing's scratch lies in the ring");
+    // the most tokens of a call on this configuration; the routing takes less than 17 KiB
+    static_assert(down_smem(NT == 1 ? 8 : kLayerTokens) <= 232448 - 17408 && kUpSmem <= 232448 - 17408, "shared memory");
 };
 constexpr int kPrefetch = 64;  // boxes of 2 KiB
 struct StreamShared {
@@ -509,11 +558,19 @@ struct StreamShared {
 // First of the 16 k of a stage that a lane of a warp takes (see Stream::take).
 __device__ __forceinline__ int lane_k(int warp, int t) { return warp / 2 * 128 + (2 * t + (warp & 1)) * 16; }
 
+// Where a stage has piece `piece` (16 bytes) of column `column` (128 bytes) of a row.  With
+// pieces 0, 2, 4, 6 or 1, 3, 5, 7 in a row's four lanes the swizzle puts any two rows that
+// follow one another on all banks.
+__device__ __forceinline__ int place_of(int row, int column, int piece) {
+    return row / 16 * (16 * kSeg) + column * 2048 + row % 16 * 128 + ((piece ^ (row & 7)) * 16);
+}
+
 template <int STAGES, int ROWS>
 struct Stream {
     static constexpr int kBytes = ROWS * kSeg;
     uint8_t *ring;
     StreamShared *sh;
+    uint64_t *full, *empty;  // its slots' barriers
     int *status;
     int s = 0;
     uint32_t round = 0;
@@ -530,47 +587,47 @@ struct Stream {
         *static_cast<volatile int *>(&sh->abort) = 1;
         return false;
     }
-    // The producing lane: a stage of 16 rows from `row0` and, of 32, 16 from `row1`.  After a wait
-    // that ran out: false, once no copy is in flight any longer.
+    // The producing lane: waits for its copies in flight.  Slot s still holds the last round's stage,
+    // the slots before it this round's (one that was never loaded stands at its first round).
+    __device__ __forceinline__ void drain() {
+        for (int k = 0; k < STAGES; ++k, step()) mbar_wait(&full[s], round ^ 1u, status);
+    }
+    // The producing lane: a stage of 16 rows from `row0` and, of 32, 16 from `row1`; false after a
+    // wait that ran out (drain is then due).
     __device__ __forceinline__ bool put(const CUtensorMap *map, int at, int row0, int row1) {
-        if (!wait(&sh->empty[s], round ^ 1u)) {
-            // (slot s still holds the last round's stage, the slots before it this round's)
-            for (int k = 0; k < STAGES; ++k, step()) mbar_wait(&sh->full[s], round ^ 1u, status);
-            return false;
-        }
-        mbar_arrive_expect_tx(&sh->full[s], kBytes);
+        if (!wait(&empty[s], round ^ 1u)) return false;
+        mbar_arrive_expect_tx(&full[s], kBytes);
         uint8_t *to = ring + s * kBytes;
 #pragma unroll
         for (int c = 0; c < kSeg / 128; ++c) {
-            tma_load_2d(to + c * 2048, map, &sh->full[s], at + c * 128, row0);
-            if (ROWS == 32) tma_load_2d(to + kBytes / 2 + c * 2048, map, &sh->full[s], at + c * 128, row1);
+            tma_load_2d(to + c * 2048, map, &full[s], at + c * 128, row0);
+            if (ROWS == 32) tma_load_2d(to + kBytes / 2 + c * 2048, map, &full[s], at + c * 128, row1);
         }
         step();
         return true;
     }
     // A taking warp: the next stage has landed.
-    __device__ __forceinline__ bool get() { return __all_sync(0xffffffffu, wait(&sh->full[s], round)); }
-    // 16 bytes of rows `lo` and `hi` (of the 32): piece `piece` of column `column` of 128.  With pieces
-    // 0, 2, 4, 6 or 1, 3, 5, 7 in a row's four lanes the swizzle puts any two rows that follow
-    // one another on all banks.
-    __device__ __forceinline__ void take(int lo_row, int hi_row, int column, int piece, uint4 &lo, uint4 &hi) const {
-        const uint8_t *at = ring + s * kBytes + column * 2048;
-        auto of = [&](int row) { return at + row / 16 * (16 * kSeg) + row % 16 * 128 + ((piece ^ (row & 7)) * 16); };
-        lo = *reinterpret_cast<const uint4 *>(of(lo_row));
-        hi = *reinterpret_cast<const uint4 *>(of(hi_row));
+    __device__ __forceinline__ bool get() { return __all_sync(0xffffffffu, wait(&full[s], round)); }
+    // The lane's 16 bytes of two rows of the stage, `lo` and `hi` bytes from its start (place_of).
+    __device__ __forceinline__ void take(int lo_at, int hi_at, uint4 &lo, uint4 &hi) const {
+        const uint8_t *at = ring + s * kBytes;
+        lo = *reinterpret_cast<const uint4 *>(at + lo_at);
+        hi = *reinterpret_cast<const uint4 *>(at + hi_at);
     }
     __device__ __forceinline__ void done(int lane) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->empty[s]);
+        if (lane == 0) mbar_arrive(&empty[s]);
         step();
     }
 };
 
-// The ring's barriers; the whole CTA, which meets at a barrier afterwards.
-template <int STAGES, int ROWS>
-__device__ __forceinline__ Stream<STAGES, ROWS> open_stream(uint8_t *smem, StreamShared *sh, int writers, int takers, int *status) {
+// The barriers of RINGS rings, one behind the other in shared memory, each read by `takers` warps;
+// the whole CTA, which meets at a barrier afterwards.
+template <int RINGS, int STAGES, int ROWS>
+__device__ __forceinline__ void open_streams(Stream<STAGES, ROWS> (&q)[RINGS], uint8_t *smem, StreamShared *sh, int writers, int takers, int *status) {
+    static_assert(RINGS * STAGES <= 8, "barriers");
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < RINGS * STAGES; ++s) {
             mbar_init(&sh->full[s], 1);
             mbar_init(&sh->empty[s], takers);
         }
@@ -581,11 +638,15 @@ __device__ __forceinline__ Stream<STAGES, ROWS> open_stream(uint8_t *smem, Strea
         sh->abort = 0;
         fence_barrier_init();
     }
-    Stream<STAGES, ROWS> q;
-    q.ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
-    q.sh = sh;
-    q.status = status;
-    return q;
+    smem += (1024u - (smem_u32(smem) & 1023u)) & 1023u;
+#pragma unroll
+    for (int r = 0; r < RINGS; ++r) {
+        q[r].ring = smem + r * STAGES * Stream<STAGES, ROWS>::kBytes;
+        q[r].sh = sh;
+        q[r].full = sh->full + r * STAGES;
+        q[r].empty = sh->empty + r * STAGES;
+        q[r].status = status;
+    }
 }
 
 // As up_kernel, an item 32 rows of U: the tokens' elements are then fetched and split once
@@ -600,11 +661,14 @@ up_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     extern __shared__ uint8_t smem[];
     __shared__ StreamShared shared;
     __shared__ Routing r;
-    Stream<Cf::kUpStages, 32> q = open_stream<Cf::kUpStages, 32>(smem, &shared, NT, kTakers, a.status);
+    Stream<Cf::kUpStages, 32> streams[1], &q = streams[0];
+    open_streams(streams, smem, &shared, NT, kTakers, a.status);
     float4 *sums = reinterpret_cast<float4 *>(smem + Cf::kUpRing);  // [set][warp][tile][n][lane]
     griddep_wait();
     griddep_launch_dependents();
-    route<Cf::kUpThreads>(r, a, 8 * NT);
+    route<Cf::kUpThreads>(r, *reinterpret_cast<RouteScratch *>(q.ring), a, 8 * NT);  // (before anything lands there)
+    tc::fence_proxy_async_smem();
+    __syncthreads();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int tiles = (a.hidden_ld + kCh - 1) / kCh, items = r.groups * tiles, segs = (a.width + kSeg - 1) / kSeg;
     if (warp == kTakers) {
@@ -613,7 +677,10 @@ up_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
             // (a tile behind the last hidden channel reads the rows that follow, and writes zeros)
             const int row = static_cast<int>(r.group[i / tiles].expert * a.up_rows) + i % tiles * kCh;
             for (int s = 0; s < segs; ++s)
-                if (!q.put(&map, s * kSeg, row, row + (GATED ? a.hidden : 16))) return;
+                if (!q.put(&map, s * kSeg, row, row + (GATED ? a.hidden : 16))) {
+                    q.drain();
+                    return;
+                }
         }
         // What this CTA's successor in down_stream_kernel reads first is fetched into L2 while
         // it starts (its weights may be: see there).
@@ -665,6 +732,7 @@ up_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
         return;
     }
     const int k0 = lane_k(warp, t);  // the lane's k of a stage
+    const int lo_at = place_of(g, warp / 2, 2 * t + (warp & 1)), hi_at = place_of(GATED ? 16 + g : 8 + g, warp / 2, 2 * t + (warp & 1));
     int set = 0;
     uint32_t round = 0;
     // the token row of the lane's column of an item's first eight
@@ -699,7 +767,7 @@ up_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     uint4 lo, hi;
-                    q.take((GATED ? 8 : 16) * m + g, GATED ? 16 + 8 * m + g : 16 * m + 8 + g, warp / 2, 2 * t + (warp & 1), lo, hi);
+                    q.take(lo_at + (GATED ? 1024 : 16 * kSeg) * m, hi_at + (GATED ? 1024 : 16 * kSeg) * m, lo, hi);
                     expand_rows<Mma>(lo, hi, w[m]);
                     multiply<Mma, P>(acc[m][0], w[m], v);
                 }
@@ -729,94 +797,151 @@ up_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     }
 }
 
+// 16 bytes to shared memory, past L1 and without a register.
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // As down_kernel, with a grid of as many CTAs as run at once; a stage is 16 channels' rows of up
 // to 1024 hidden values of a group.  Two teams of eight warps take the groups in turn, 128
 // bytes of a row each: while one team's loads, sums and waits take their time, the other
 // multiplies (sixteen warps on every stage, 64 bytes each: 75 us for a batch of 8 tokens,
 // most of it instructions that are not the product's).  A lane fetches the hidden values of
-// its team's next stage when it has multiplied one, and the scales of its next group when it
-// begins one.
+// its team's stages ahead, two where shared memory has room for them (one, in registers: 62 us
+// for that batch), and the scales of its next group when it begins one.
 template <class El, int NT>
 __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_stream_kernel(const __grid_constant__ CUtensorMap map, const LayerArgs a) {
     using Cf = StreamCfg<El, NT>;
-    constexpr int PH = Parts<El>::hidden, S = Cf::kDownStages;
+    constexpr int PH = Parts<El>::hidden, S = Cf::kDownStages / 2;
     extern __shared__ uint8_t smem[];
     __shared__ StreamShared shared;
     __shared__ Routing r;
-    Stream<S, 16> q = open_stream<S, 16>(smem, &shared, 1, kTakers / 2, a.status);
-    float *out_sums = reinterpret_cast<float *>(smem + Cf::kDownRing);  // [warp][token][kOutPitch]
+    // A ring for each team: one that skipped the other's stages in a common ring could take the
+    // parity of a slot's round before last for its own.
+    Stream<S, 16> streams[2];
+    open_streams(streams, smem, &shared, 1, kTakers / 2, a.status);
+    float *out_sums = reinterpret_cast<float *>(smem + Cf::kDownRing + kTakers * 2 * Cf::kHeldBytes);  // [warp][token][kOutPitch]
     for (int k = threadIdx.x; k < kTakers * a.tokens * kOutPitch; k += Cf::kDownThreads) out_sums[k] = 0.f;
-    route<Cf::kDownThreads>(r, a, 8 * NT);
+    route<Cf::kDownThreads>(r, *reinterpret_cast<RouteScratch *>(streams[0].ring), a, 8 * NT);  // (before anything lands there)
+    tc::fence_proxy_async_smem();
+    __syncthreads();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int items = (a.width + 15) / 16, step = static_cast<int>(gridDim.x), groups = r.groups;
     if (warp == kTakers) {
         if (lane > 0) return;
         // (the weights: the kernel before does not write them, and has waited for what came
         // before it, so that they may be under way before its end)
-        for (int i = blockIdx.x; i < items; i += step)
-            for (int group = 0; group < groups; ++group)
-                for (int k = 0; k < a.hidden; k += kSeg)
-                    if (!q.put(&map, k, r.group[group].expert * a.width + i * 16, 0)) return;
+        int turn = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; i < items && ok; i += step)
+            for (int group = 0; group < groups && ok; ++group, turn ^= 1)
+                for (int k = 0; k < a.hidden && ok; k += kSeg) {
+                    const int row = r.group[group].expert * a.width + i * 16;
+                    ok = turn ? streams[1].put(&map, k, row, 0) : streams[0].put(&map, k, row, 0);
+                }
+        if (!ok) {
+            streams[0].drain();
+            streams[1].drain();
+        }
         return;
     }
-    griddep_wait();
-    griddep_launch_dependents();
     const int team = warp / (kTakers / 2), column = warp % (kTakers / 2);  // of 128 bytes
+    Stream<S, 16> q = team ? streams[1] : streams[0];
+    const int place[2] = {place_of(g, column, 2 * t), place_of(g, column, 2 * t + 1)};
     const bool idle = column * 128 >= a.hidden;                            // (short rows leave columns out)
     float *mine = out_sums + warp * a.tokens * kOutPitch;
     bool ok = true;
-    uint32_t ahead[2][PH][8] = {};
-    // the lane's 32 hidden values of a stage of the group's first eight columns
-    const uint16_t *h_lane = a.h + column * 128 + t * 32;
-    auto fetch = [&](const Routing::Group &of, int k) {
-        if (g < of.cols && k + column * 128 < a.hidden) {
-            const uint16_t *h = h_lane + (static_cast<long long>(of.first + g) * a.hidden_ld + k);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) load_hidden<PH>(h + c * 16, a.h_part, 0, ahead[c]);
-        }
+    // The team's groups: every other one, counted over all items, so that both have as many.
+    struct Cursor {
+        int group, item;
     };
-    // The team's groups: those of its parity, counted over all items, so that both have as many.
-    Routing::Group here{};
-    float next_l = 0.f, next_h = 0.f;
-    int group = team, item = blockIdx.x;  // the next of them
-    auto settle = [&]() {
-        while (group >= groups && item < items) {
-            group -= groups;
-            item += step;
+    auto settle = [&](Cursor &c) {
+        while (c.group >= groups && c.item < items) {
+            c.group -= groups;
+            c.item += step;
         }
-        if (item >= items) return false;
-        here = r.group[group];
-        const int d = item * 16 + g;
-        const float *scale = a.down_scale + (static_cast<long long>(here.expert) * a.width + d);
+        return c.item < items;
+    };
+    // The channels' scales of the next group, on their way while one is multiplied (the first
+    // before the kernel before has ended, which does not write them).
+    float next_l = 0.f, next_h = 0.f;
+    Cursor coming{team, static_cast<int>(blockIdx.x)};
+    auto scales = [&]() {
+        if (!settle(coming)) return;
+        const int d = coming.item * 16 + g;
+        const float *scale = a.down_scale + (static_cast<long long>(r.group[coming.group].expert) * a.width + d);
         next_l = d < a.width ? __ldca(scale) : 0.f;
         next_h = d + 8 < a.width ? __ldca(scale + 8) : 0.f;
-        return true;
+        coming.group += 2;
     };
-    bool another = groups > 0 && settle();
-    if (another) fetch(here, 0);
+    if (groups > 0) scales();
+    griddep_wait();
+    griddep_launch_dependents();
+    // The lane's 32 hidden values of the team's stages, in the groups' first eight columns: two
+    // stages ahead in shared memory, or the next one's in registers.
+    const uint16_t *h_lane = a.h + column * 128 + t * 32;
+    uint8_t *held = smem + Cf::kDownRing + warp * (2 * Cf::kHeldBytes) + lane * 16;
+    uint32_t ahead[2][PH][8] = {};
+    Cursor fetched{team, static_cast<int>(blockIdx.x)};
+    int f_k = 0, f_slot = 0, slot = 0;
+    auto fetch = [&]() {
+        if (settle(fetched)) {
+            const Routing::Group of = r.group[fetched.group];
+            if (g < of.cols && f_k + column * 128 < a.hidden) {
+                const uint16_t *h = h_lane + (static_cast<long long>(of.first + g) * a.hidden_ld + f_k);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (!Cf::kHeld) load_hidden<PH>(h + c * 16, a.h_part, 0, ahead[c]);
+                    else
+#pragma unroll
+                        for (int p = 0; p < PH; ++p)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                copy_async16(held + f_slot * Cf::kHeldBytes + ((c * PH + p) * 2 + x) * 512, h + p * a.h_part + c * 16 + x * 8);
+                }
+            }
+            f_k += kSeg;
+            if (f_k >= a.hidden) {
+                f_k = 0;
+                fetched.group += 2;
+            }
+        }
+        f_slot ^= 1;
+        if (Cf::kHeld) copy_async_commit();
+    };
+    if (groups > 0) {
+        fetch();
+        if (Cf::kHeld) fetch();
+    }
     int turn = team;  // 0: the group is the team's
     for (int i = blockIdx.x; i < items; i += step) {
         for (int n_group = 0; n_group < groups; ++n_group, turn ^= 1) {
-            if (turn) {
-                for (int k = 0; k < a.hidden; k += kSeg) q.step();
-                continue;
-            }
-            const Routing::Group now = here;
+            if (turn) continue;
+            const Routing::Group now = r.group[n_group];
             const float sl = next_l, sh = next_h;
-            group += 2;
-            another = settle();
-            float acc[NT][4] = {};
+            scales();
+            float acc[NT][4] = {}, half[4] = {};  // (the first eight columns in two chains: an MMA waits for the one before it)
             for (int k = 0; k < a.hidden; k += kSeg) {
                 ok = ok && q.get();  // (after a wait that ran out the warps still meet at the barriers)
                 if (!ok) break;
+                if (Cf::kHeld) copy_async_wait<1>();
                 if (k + column * 128 < a.hidden) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
+                        if (Cf::kHeld)
+#pragma unroll
+                            for (int p = 0; p < PH; ++p)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+                                    *reinterpret_cast<uint4 *>(&ahead[c][p][4 * x]) = *reinterpret_cast<const uint4 *>(held + slot * Cf::kHeldBytes + ((c * PH + p) * 2 + x) * 512);
                         uint4 lo, hi;
-                        q.take(g, 8 + g, column, 2 * t + c, lo, hi);
+                        q.take(place[c], place[c] + 1024, lo, hi);
                         uint32_t w[4][4];
                         expand_rows<ElBF16>(lo, hi, w);
-                        multiply<ElBF16, PH>(acc[0], w, ahead[c]);
+                        multiply<ElBF16, PH>(c ? half : acc[0], w, ahead[c]);
 #pragma unroll
                         for (int n = 1; n < NT; ++n) {
                             if (n * 8 >= now.cols) break;
@@ -826,10 +951,12 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
                         }
                     }
                 }
+                slot ^= 1;
                 q.done(lane);
-                if (k + kSeg < a.hidden) fetch(now, k + kSeg);
-                else if (another) fetch(here, 0);
+                fetch();
             }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[0][c] += half[c];
             if (!idle) add_out<NT>(r, mine, now.first, now.cols, g, t, sl, sh, acc);
         }
         named_barrier_sync(1, kTakers * 32);
@@ -846,6 +973,7 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
         }
         named_barrier_sync(1, kTakers * 32);
     }
+    if (Cf::kHeld) copy_async_wait<0>();  // no copy outlives the CTA
 }
 
 // The weights' rows, boxes of 128 bytes x 16 rows with the 128-byte swizzle.
