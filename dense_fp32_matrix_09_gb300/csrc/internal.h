@@ -359,7 +359,9 @@ struct NormGradArgs {
     long long lddx;
     float *dW;
     float *parts;  // workspace: as many rows of K as fit, at least one (kNormHeld: 16)
+    int *status;
 };
+cudaError_t norm_prepare();
 int norm_grad_launches(int K);
 cudaError_t launch_rms_norm_grad(int type, const NormGradArgs &a, int num_sms, size_t ws_floats, cudaStream_t stream);
 

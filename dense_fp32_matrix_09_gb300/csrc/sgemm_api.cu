@@ -984,7 +984,7 @@ int sgemm_create(sgemm_handle_t *out) {
     }
     if (sg::tc3x_prepare() != cudaSuccess || sg::tc3x_pair_prepare() != cudaSuccess ||
         sg::tc16_prepare() != cudaSuccess || sg::int8_prepare() != cudaSuccess || sg::sort_prepare() != cudaSuccess ||
-        sg::fp4_prepare() != cudaSuccess || sg::layer_prepare() != cudaSuccess)
+        sg::fp4_prepare() != cudaSuccess || sg::layer_prepare() != cudaSuccess || sg::norm_prepare() != cudaSuccess)
         return SGEMM_ERR_CUDA;
     occupancy[SGEMM_VARIANT_TC_3XTF32] = 1;
     occupancy[SGEMM_VARIANT_TC_3XTF32_PAIR] = 1;

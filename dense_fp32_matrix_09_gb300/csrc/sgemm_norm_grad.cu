@@ -7,6 +7,7 @@
 //    what reaches h are read once and stay in registers for the row's sum and its
 //    gradient, the columns' sums in registers from row to row; at the end each group
 //    of threads writes its sums, a row of `parts`.
+//  * norm_grad_ring_kernel -- the same for long rows on 16-byte boundaries.
 //  * columns_kernel -- dw: the rows of `parts` added up.
 //  * norm_grad_wide_kernel, columns_wide_kernel -- the same for rows longer than the
 //    registers of 512 threads hold: each row is read twice, and the columns' sums are
@@ -132,6 +133,112 @@ norm_grad_kernel(const NormGradArgs a) {
     }
 }
 
+// The same for rows that start on 16-byte boundaries and are copied as a whole (cp.async.bulk)
+// into a ring of shared memory, several rows ahead of the one that is added up: as many
+// bytes are on their way as HBM's latency wants, where a row ahead in registers is half of that.
+// One row at a time for the whole block.
+constexpr int kGradStages = 4;
+template <class El, int TPR, int HELD>
+__global__ void __launch_bounds__(TPR, TPR == 256 ? 2 : 1)
+norm_grad_ring_kernel(const NormGradArgs a, int stages) {
+    using T = typename El::T;
+    constexpr int A = 16 / sizeof(T);
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full[kGradStages];
+    __shared__ float part[2][TPR / 32];
+    const int lane = threadIdx.x, step = gridDim.x;
+    const int row_bytes = a.K * static_cast<int>(sizeof(T)), arrays = a.dH ? 3 : 2, stage_bytes = 3 * ((row_bytes + 127) & ~127);
+    if (lane == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    auto part_of = [&](int s, int k) { return smem + s * stage_bytes + k * (stage_bytes / 3); };
+    auto issue = [&](int s, long long i) {
+        auto copy = [&](int k, const void *from, long long ld) {
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                         ::"r"(smem_u32(part_of(s, k))), "l"(static_cast<const T *>(from) + i * ld), "r"(row_bytes), "r"(smem_u32(&full[s])) : "memory");
+        };
+        mbar_arrive_expect_tx(&full[s], arrays * row_bytes);
+        copy(0, a.dY, a.lddy);
+        copy(1, a.H, a.ldh);
+        if (a.dH) copy(2, a.dH, a.lddh);
+    };
+    const long long first = blockIdx.x;
+    if (lane == 0)
+        for (int s = 0; s < stages && first + static_cast<long long>(s) * step < a.M; ++s) issue(s, first + static_cast<long long>(s) * step);
+    Pack8<T> g[HELD];
+    float dw[HELD][kV];
+#pragma unroll
+    for (int c = 0; c < HELD; ++c) {
+        g[c] = load8<T, TPR, A, true>(static_cast<const T *>(a.W), c, lane, a.K);
+#pragma unroll
+        for (int e = 0; e < kV; ++e) dw[c][e] = 0.f;
+    }
+    // one piece of a row in shared memory, as load8 takes it
+    auto piece = [&](const uint8_t *row, int c) {
+        Pack8<T> r;
+        const int at = c * kV * TPR + lane * A;
+#pragma unroll
+        for (int i = 0; i < kV / A; ++i)
+            reinterpret_cast<uint4 *>(&r)[i] = at + i * TPR * A < a.K ? *reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(row) + at + i * TPR * A) : uint4{};
+        return r;
+    };
+    int s = 0, turn = 0;
+    uint32_t round = 0;
+    bool ok = true;  // (after a wait that ran out the block still meets at its barriers)
+    float next_r = first < a.M ? __ldca(a.rstd + first) : 0.f;
+    for (long long i = first; i < a.M; i += step, turn ^= 1) {
+        const float r = next_r;
+        if (i + step < a.M) next_r = __ldca(a.rstd + i + step);
+        ok = ok && mbar_wait(&full[s], round, a.status);
+        Pack8<T> d[HELD], x[HELD], more[HELD];
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < HELD; ++c) {
+            d[c] = piece(part_of(s, 0), c);
+            x[c] = piece(part_of(s, 1), c);
+            if (a.dH) more[c] = piece(part_of(s, 2), c);
+#pragma unroll
+            for (int e = 0; e < kV; ++e) sum = fmaf(El::up(d[c].v[e]) * El::up(g[c].v[e]), El::up(x[c].v[e]), sum);
+        }
+        sum = row_sum<TPR>(sum, part[turn]);  // (and every thread has taken its part of the row)
+        const long long then = i + static_cast<long long>(stages) * step;
+        if (lane == 0 && ok && then < a.M) issue(s, then);
+        if (++s == stages) {
+            s = 0;
+            round ^= 1u;
+        }
+        const float f = sum * r * r / static_cast<float>(a.K);
+        T *dx = static_cast<T *>(a.dX) + i * a.lddx;
+#pragma unroll
+        for (int c = 0; c < HELD; ++c) {
+            Pack8<T> o;
+#pragma unroll
+            for (int e = 0; e < kV; ++e) {
+                const float dv = El::up(d[c].v[e]), hv = El::up(x[c].v[e]);
+                dw[c][e] = fmaf(dv, hv * r, dw[c][e]);
+                float v = r * fmaf(-hv, f, dv * El::up(g[c].v[e]));
+                if (a.dH) v += El::up(more[c].v[e]);
+                o.v[e] = El::down(v);
+            }
+            if (ok) store8<T, TPR, A>(dx, c, lane, a.K, o);
+        }
+    }
+    if (!ok && lane == 0)  // no copy outlives the CTA
+        for (int k = 0; k < stages; ++k) mbar_wait(&full[k], k < s ? round : round ^ 1u, a.status);
+    float *to = a.parts + static_cast<long long>(blockIdx.x) * a.K;
+#pragma unroll
+    for (int c = 0; c < HELD; ++c)
+#pragma unroll
+        for (int e = 0; e < kV; ++e) {
+            const int p = c * kV * TPR + lane * A + e / A * TPR * A + e % A;
+            if (p < a.K) to[p] = dw[c][e];
+        }
+}
+
 // dw[p] = sum of column p of `parts` (n rows): 32 columns a block, each warp's rows
 // 8 apart, then the warps' sums.
 __global__ void __launch_bounds__(1024) columns_kernel(const float *parts, int n, int K, float *dw) {
@@ -211,6 +318,21 @@ cudaError_t grad_typed(const NormGradArgs &a, int num_sms, size_t ws_floats, cud
     return e != cudaSuccess ? e : add_parts(a, static_cast<int>(blocks) * kRows, stream);
 }
 
+// Shared memory that a block of the ring kernel may take: two of 256 threads an SM, or one of 512.
+template <int TPR>
+constexpr int kRingRoom = TPR == 256 ? 112 << 10 : 224 << 10;
+
+template <class El, int TPR, int HELD>
+cudaError_t grad_ring(const NormGradArgs &a, int num_sms, size_t ws_floats, cudaStream_t stream) {
+    const int stage = 3 * ((a.K * static_cast<int>(sizeof(typename El::T)) + 127) & ~127);
+    const int fit = kRingRoom<TPR> / stage, stages = fit < kGradStages ? fit : kGradStages;
+    size_t blocks = static_cast<size_t>(TPR == 256 ? 2 : 1) * num_sms;
+    blocks = blocks < static_cast<size_t>(a.M) ? blocks : static_cast<size_t>(a.M);
+    blocks = blocks < ws_floats / a.K ? blocks : ws_floats / a.K;
+    const cudaError_t e = launch_dependent(norm_grad_ring_kernel<El, TPR, HELD>, dim3(static_cast<unsigned>(blocks)), dim3(TPR), stages * stage, stream, 1, a, stages);
+    return e != cudaSuccess ? e : add_parts(a, static_cast<int>(blocks), stream);
+}
+
 template <class El, int A>
 cudaError_t grad_shared(const NormGradArgs &a, int num_sms, size_t ws_floats, cudaStream_t stream) {
     // threads a row: 16 elements each where the rows are that long, 32 in the longest
@@ -240,12 +362,32 @@ cudaError_t grad_for(const NormGradArgs &a, int num_sms, size_t ws_floats, cudaS
     auto fits = [&](int n) {
         return a.K % n == 0 && unit(a.dY, a.lddy, n) && unit(a.H, a.ldh, n) && unit(a.dH, a.lddh, n) && unit(a.W, 0, n) && unit(a.dX, a.lddx, n);
     };
-    if (fits(V)) return grad_shared<El, V>(a, num_sms, ws_floats, stream);
+    if (fits(V)) {
+        // rows long enough that a block has one at a time, and enough of them to go round
+        if (a.K > 2048 && a.M > 4 * num_sms) {
+            if (a.K <= 4096) return grad_ring<El, 256, 2>(a, num_sms, ws_floats, stream);
+            if (a.K <= 8192) return grad_ring<El, 512, 2>(a, num_sms, ws_floats, stream);
+        }
+        return grad_shared<El, V>(a, num_sms, ws_floats, stream);
+    }
     if (fits(2)) return grad_shared<El, 2>(a, num_sms, ws_floats, stream);
     return grad_shared<El, 1>(a, num_sms, ws_floats, stream);
 }
 
 }  // namespace
+
+template <class El>
+static cudaError_t prepare_ring() {
+    const cudaError_t e = cudaFuncSetAttribute(norm_grad_ring_kernel<El, 256, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingRoom<256>);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(norm_grad_ring_kernel<El, 512, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingRoom<512>);
+}
+
+cudaError_t norm_prepare() {
+    cudaError_t e = cudaSuccess;
+    for (cudaError_t r : {prepare_ring<ElF32>(), prepare_ring<ElBF16>(), prepare_ring<ElF16>()})
+        if (e == cudaSuccess) e = r;
+    return e;
+}
 
 int norm_grad_launches(int K) { return K > kNormHeld ? 3 : 2; }
 

@@ -368,6 +368,7 @@ int sgemm_rms_norm_grad(sgemm_handle_t h, int type, int M, int K, const void *dY
     a.lddx = lddx;
     a.dW = dweight;
     a.parts = v.d_ws;
+    a.status = v.d_status;
     const int rc = from_cuda(sg::launch_rms_norm_grad(type, a, v.num_sms, v.ws_floats, s));
     if (rc == SGEMM_OK) sg::record_call(h, -1, 1, sg::norm_grad_launches(K), 0);
     return rc;

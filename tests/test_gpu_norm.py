@@ -210,7 +210,7 @@ def grad_reference(dy, dh, kept, w, r):
 
 
 @pytest.mark.parametrize("dtype", list(KINDS))
-@pytest.mark.parametrize("M,K", [s for s in SIZES if s[0]] + [(2000, 130), (700, 4096), (400, 16384), (3000, 16)])
+@pytest.mark.parametrize("M,K", [s for s in SIZES if s[0]] + [(2000, 130), (700, 4096), (400, 16384), (3000, 16), (1300, 2056), (2000, 8192), (1500, 5000)])
 def test_gradient(h, dtype, M, K):
     gen = torch.Generator().manual_seed(M + K)
     for form in (FORMS[0], FORMS[1], FORMS[2]):
