@@ -237,13 +237,18 @@ __device__ void route(Routing &r, RouteScratch &w, const LayerArgs &a, int per_g
     __syncthreads();
 }
 
-// 16 bytes of a weight row from k on, zeros behind its end.
+// 16 bytes of a weight row from k on, on any address: the five aligned words that they lie in,
+// shifted.  Words behind the row's last byte are zeros; bytes behind it within its last word
+// may be anything (they meet elements that are zero), and lie in memory that the row's do.
 __device__ __forceinline__ uint4 load_weights(const int8_t *row, int k, int K) {
-    uint32_t w[4] = {};
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + k);
+    const uint32_t *p = reinterpret_cast<const uint32_t *>(at & ~static_cast<uintptr_t>(3));
+    const int off = static_cast<int>(at & 3);  // of the first byte in the first word
+    uint32_t w[5];
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-        if (k + e < K) w[e / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldcg(row + k + e))) << (8 * (e % 4));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 5; ++i) w[i] = (i < 4 || off) && k + 4 * i - off < K ? __ldcg(p + i) : 0u;
+    const unsigned s = 8 * off;
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
 }
 
 // 32 bytes on a 32-byte boundary in one access: a sector, of which two of 16 bytes would
@@ -273,9 +278,22 @@ __device__ __forceinline__ Raw<El> fetch_token(const typename El::T *row, int k,
 #pragma unroll
             for (int x = 0; x < 8; ++x) reinterpret_cast<uint32_t *>(r.v + e)[x] = w[x];
         }
-    } else {
+    } else if (sizeof(T) == 4) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) r.v[e] = k + e < K ? __ldca(row + k + e) : El::down(0.f);
+    } else {  // the aligned words that they lie in, as load_weights
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + k);
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(at & ~static_cast<uintptr_t>(3));
+        const int off = static_cast<int>(at & 3) / 2;
+        uint32_t w[9];
+#pragma unroll
+        for (int i = 0; i < 9; ++i) w[i] = (i < 8 || off) && k + 2 * i - off < K ? __ldca(p + i) : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t v = __funnelshift_r(w[i], w[i + 1], 16 * off);
+            if (k + 2 * i + 1 >= K) v = k + 2 * i < K ? v & 0xffffu : 0u;
+            reinterpret_cast<uint32_t *>(r.v)[i] = v;
+        }
     }
     return r;
 }
