@@ -95,14 +95,19 @@ int check_fp4(int format, int out_type, int M, int N, int K, const uint8_t *A, i
 struct Fp4Choice {
     int nt, ksplit;
 };
+// Tile and split (us in graphs, NV).  CTA pairs from a fifth of the SMs' worth of their tiles on
+// (200 x 8192 x 4096 9.7 against 11.0 in tiles of 128, 2048 x 4096 x 4096 16.3 against 22.8; 300 x 2048
+// x 4096, 16 tiles, 9.0 against 7.7).  Otherwise the smallest tile that holds all tokens, and K split
+// while the CTAs make one wave and each split saves enough stages of 0.23 us for the exchange's 0.8 (1
+// x 4096 x 4096: whole 5.9, in two 4.9, four 4.0, eight, two CTAs an SM, 4.5; 1 x 8192 x 1024, four
+// stages: 3.1, 3.4, 3.9; 64 x 8192 x 8192: 12.9, 9.9, 10.5; 128 x 4096 x 4096: 8.8, 7.6, 7.0, 11.0).
 Fp4Choice choose_fp4(int M, int N, int K, int num_sms) {
-    const long long pair_units = cdiv(M, 256) * cdiv(N, 256);
-    if (M > 128 && pair_units >= num_sms / 4) return {256, 1};
+    if (M > 128 && cdiv(M, 256) * cdiv(N, 256) >= num_sms / 5) return {256, 1};
     const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     const long long tiles = cdiv(M, nt) * cdiv(N, 128);
     const int stages = static_cast<int>(cdiv(K, sg::kFp4StageK));
     int split = 1;
-    while (split < 8 && tiles * split * 2 <= 2 * num_sms && stages >= 4 * split) split *= 2;
+    while (split < 8 && 10 * tiles * split * 2 <= 11 * num_sms && stages >= std::max(8, 4 * split)) split *= 2;
     return {nt, split};
 }
 
