@@ -15,8 +15,8 @@
 // delivers for so few tokens: a tile of 16 channels x 8 tokens takes each weight once.
 // The order of k within an MMA is free, so a lane's 16 bytes are the k of four
 // MMAs.  An int8 is exact in BF16 and in FP16; the tokens' elements go in as they are or, FP32,
-// as sums of three BF16 values, exact as well.  The hidden
-// values take the rows' type, with FP32 rows as three parts again.  Within
+// as sums of three BF16 values, exact as well.  The hidden rows
+// are kept as two such values, 16 bits of fraction, and with FP32 rows as three.  Within
 // a warp sums run along k; the warps' sums, the experts' and the choices' are added in a
 // fixed order in FP32.
 #include <type_traits>
@@ -36,15 +36,11 @@ constexpr int kChunk = 64;  // k of a step: 16 bytes of each of 16 channels from
 constexpr int kPad = 128;   // hidden rows are made longer to a multiple of it, with zeros
 constexpr int kSlots = kLayerSlots;
 
-// 16-bit values that an element and a hidden value become, and their type.  Hidden values take the
-// rows' type, as between two calls they would: rounded once, to 8 or 11 bits, where the sum of
-// `hidden` products averages the errors and the result is rounded to as many bits again (kept in 16
-// bits they took twice the loads and MMAs).  Of FP32 rows 24 bits are kept.
 template <class El>
-struct Parts;
-template <> struct Parts<ElBF16> { static constexpr int n = 1; using Mma = ElBF16; };
-template <> struct Parts<ElF16> { static constexpr int n = 1; using Mma = ElF16; };
-template <> struct Parts<ElF32> { static constexpr int n = 3; using Mma = ElBF16; };
+struct Parts;  // 16-bit values that an element and a hidden value become, and the former's type
+template <> struct Parts<ElBF16> { static constexpr int in = 1, hidden = 2; using Mma = ElBF16; };
+template <> struct Parts<ElF16> { static constexpr int in = 1, hidden = 2; using Mma = ElF16; };  // (as they are, U in FP16)
+template <> struct Parts<ElF32> { static constexpr int in = 3, hidden = 3; using Mma = ElBF16; };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -298,8 +294,8 @@ __device__ __forceinline__ Raw<El> fetch_token(const typename El::T *row, int k,
     return r;
 }
 template <class El>
-__device__ __forceinline__ void split_token(const Raw<El> &r, uint32_t (&to)[Parts<El>::n][8]) {
-    constexpr int P = Parts<El>::n;
+__device__ __forceinline__ void split_token(const Raw<El> &r, uint32_t (&to)[Parts<El>::in][8]) {
+    constexpr int P = Parts<El>::in;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         uint32_t p[P];
@@ -339,7 +335,7 @@ __device__ __forceinline__ void hidden_scales(const LayerArgs &a, int e, int f0,
 
 // The hidden values of 8 tokens from their sums: s.x, s.y channel g of tokens 2t and 2t + 1, s.z
 // and s.w of the MMA's lower channel.  Channels behind the last hidden one are written as zeros.
-template <class El, bool GATED>
+template <bool GATED, int PH>
 __device__ __forceinline__ void write_hidden(const LayerArgs &a, int first, int cols, int f0, int n, int g, int t, const float4 &s,
                                              const float (&scale)[2]) {
     const int fl = f0 + g, fh = GATED ? fl : fl + 8;
@@ -347,15 +343,11 @@ __device__ __forceinline__ void write_hidden(const LayerArgs &a, int first, int 
     auto silu = [](float v) { return v / (1.f + expf(-v)); };
     auto put = [&](int col, int f, float v) {
         if (col >= cols || f >= a.hidden_ld) return;
-        uint16_t *to = a.h + static_cast<long long>(first + col) * a.hidden_ld + f;
-        if (Parts<El>::n == 1) {
-            *reinterpret_cast<typename Parts<El>::Mma::T *>(to) = Parts<El>::Mma::down(v);
-        } else {
-            uint32_t p[Parts<El>::n];
-            split2<Parts<El>::n>(v, 0.f, p);
+        uint32_t p[PH];
+        split2<PH>(v, 0.f, p);
 #pragma unroll
-            for (int q = 0; q < Parts<El>::n; ++q) to[q * a.h_part] = static_cast<uint16_t>(p[q]);
-        }
+        for (int q = 0; q < PH; ++q)
+            a.h[q * a.h_part + static_cast<long long>(first + col) * a.hidden_ld + f] = static_cast<uint16_t>(p[q]);
     };
     const float y0 = silu(s.x * scale[0]), y1 = silu(s.y * scale[0]);
     put(n * 8 + 2 * t, fl, in_l ? GATED ? y0 * (s.z * scale[1]) : y0 : 0.f);
@@ -408,7 +400,7 @@ template <class El, int NT, bool GATED>
 __global__ void __launch_bounds__(kThreads, 2) up_kernel(const LayerArgs a, int share) {
     using T = typename El::T;
     using Mma = typename Parts<El>::Mma;
-    constexpr int P = Parts<El>::n, kCh = GATED ? 8 : 16;
+    constexpr int P = Parts<El>::in, PH = Parts<El>::hidden, kCh = GATED ? 8 : 16;
     __shared__ Routing r;
     __shared__ RouteScratch scratch;
     __shared__ float4 sums[kWarps][NT][32];
@@ -473,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const LayerArgs a, int 
                 }
                 float scale[2];
                 hidden_scales<GATED>(a, e, f0, g, scale);
-                write_hidden<El, GATED>(a, first, cols, f0, n, g, t, s, scale);
+                write_hidden<GATED, PH>(a, first, cols, f0, n, g, t, s, scale);
             }
         }
         __syncthreads();
@@ -485,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const LayerArgs a, int 
 // has, scaled, to its own sums of the tokens.
 template <class El, int NT>
 __global__ void __launch_bounds__(kThreads, 2) down_kernel(const LayerArgs a) {
-    constexpr int PH = Parts<El>::n;
+    constexpr int PH = Parts<El>::hidden;
     extern __shared__ float out_sums[];  // [warp][token][kOutPitch]
     __shared__ Routing r;
     __shared__ RouteScratch scratch;
@@ -527,13 +519,13 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const LayerArgs a) {
                 if (c0 + k >= c_last) break;
                 const int at = (c0 + k) * kChunk + t * 16;
                 uint32_t w[4][4];
-                expand_rows<typename Parts<El>::Mma>(vl[k], vh[k], w);
+                expand_rows<ElBF16>(vl[k], vh[k], w);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     if (n * 8 >= cols) break;
                     uint32_t v[PH][8];
                     load_hidden<PH>(h[n], a.h_part, at, v);
-                    multiply<typename Parts<El>::Mma, PH>(acc[n], w, v);
+                    multiply<ElBF16, PH>(acc[n], w, v);
                 }
             }
         }
@@ -566,9 +558,9 @@ struct StreamCfg {
     static constexpr int kUpThreads = (kTakers + 1 + NT) * 32, kDownThreads = (kTakers + 1) * 32;
     static constexpr int kUpRing = 1024 + kUpStages * 32 * kSeg, kUpSmem = kUpRing + kSums * kSumBytes;
     // Hidden values of two of a warp's stages in shared memory, where that has room for them.
-    static constexpr bool kHeld = Parts<El>::n == 1;
-    static constexpr int kHeldBytes = kHeld ? 2 * Parts<El>::n * 1024 : 0;  // of a stage
-    static constexpr int kDownStages = NT == 1 ? 8 : kHeld ? 4 : 6;  // of 16 rows, half of them a team's
+    static constexpr bool kHeld = NT == 1 && Parts<El>::hidden == 2;
+    static constexpr int kHeldBytes = kHeld ? 2 * Parts<El>::hidden * 1024 : 0;  // of a stage
+    static constexpr int kDownStages = kHeld ? 4 : NT == 1 ? 8 : 6;  // of 16 rows, half of them a team's
     static constexpr int kDownRing = 1024 + kDownStages * 16 * kSeg;
     static constexpr int down_smem(int tokens) { return kDownRing + kTakers * (2 * kHeldBytes + tokens * kOutPitch * 4); }
     static_assert(sizeof(RouteScratch) <= 2 * 16 * kSeg, "the routing's scratch lies in the ring");
@@ -683,7 +675,7 @@ up_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     using T = typename El::T;
     using Mma = typename Parts<El>::Mma;
     using Cf = StreamCfg<El, NT>;
-    constexpr int P = Parts<El>::n, kCh = GATED ? 16 : 32;
+    constexpr int P = Parts<El>::in, PH = Parts<El>::hidden, kCh = GATED ? 16 : 32;
     extern __shared__ uint8_t smem[];
     __shared__ StreamShared shared;
     __shared__ Routing r;
@@ -749,7 +741,7 @@ up_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
             if (lane == 0) mbar_arrive(&shared.sums_empty[set]);
             if (n * 8 < cols)
 #pragma unroll
-                for (int m = 0; m < 2; ++m) write_hidden<El, GATED>(a, first, cols, f0 + m * (kCh / 2), n, g, t, s[m], scale[m]);
+                for (int m = 0; m < 2; ++m) write_hidden<GATED, PH>(a, first, cols, f0 + m * (kCh / 2), n, g, t, s[m], scale[m]);
             if (++set == Cf::kSums) {
                 set = 0;
                 round ^= 1u;
@@ -841,7 +833,7 @@ __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_
 template <class El, int NT>
 __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_stream_kernel(const __grid_constant__ CUtensorMap map, const LayerArgs a) {
     using Cf = StreamCfg<El, NT>;
-    constexpr int PH = Parts<El>::n, S = Cf::kDownStages / 2;
+    constexpr int PH = Parts<El>::hidden, S = Cf::kDownStages / 2;
     extern __shared__ uint8_t smem[];
     __shared__ StreamShared shared;
     __shared__ Routing r;
@@ -966,14 +958,14 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
                         uint4 lo, hi;
                         q.take(place[c], place[c] + 1024, lo, hi);
                         uint32_t w[4][4];
-                        expand_rows<typename Parts<El>::Mma>(lo, hi, w);
-                        multiply<typename Parts<El>::Mma, PH>(c ? half : acc[0], w, ahead[c]);
+                        expand_rows<ElBF16>(lo, hi, w);
+                        multiply<ElBF16, PH>(c ? half : acc[0], w, ahead[c]);
 #pragma unroll
                         for (int n = 1; n < NT; ++n) {
                             if (n * 8 >= now.cols) break;
                             uint32_t v[PH][8];
                             load_hidden<PH>(n * 8 + g < now.cols ? h_lane + static_cast<long long>(now.first + n * 8 + g) * a.hidden_ld : nullptr, a.h_part, k + c * 16, v);
-                            multiply<typename Parts<El>::Mma, PH>(acc[n], w, v);
+                            multiply<ElBF16, PH>(acc[n], w, v);
                         }
                     }
                 }
@@ -1061,7 +1053,7 @@ cudaError_t prepare_typed() {
 
 size_t layer_floats(int type, int slots, int hidden) {
     const size_t ld = (static_cast<size_t>(hidden) + kPad - 1) / kPad * kPad;
-    return (type == SGEMM_IN_F32 ? 3 : 1) * static_cast<size_t>(slots) * ld / 2;
+    return (type == SGEMM_IN_F32 ? 3 : 2) * static_cast<size_t>(slots) * ld / 2;
 }
 
 cudaError_t layer_prepare() {

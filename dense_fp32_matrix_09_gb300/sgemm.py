@@ -934,7 +934,8 @@ class Sgemm:
             raise ValueError(f"unknown 4-bit format {format}")
         # rows on 16-byte boundaries; scales of rows behind the last are read with them, so zeros
         return Fp4Rows(torch.empty(M, max(-(-K // 32) * 16, 1), dtype=torch.uint8, **new), torch.zeros(n, dtype=torch.uint8, **new),
-                       torch.empty(M, dtype=torch.float32, **new) if with_row else None, K, format)
+                       # (rows of no elements are not touched: their products are 0)
+                       (torch.empty if K else torch.zeros)(M, dtype=torch.float32, **new) if with_row else None, K, format)
 
     def dequantize_fp4(self, A, out_dtype=None, out=None, stream=None):
         """What 4-bit rows stand for (BF16 unless `out_dtype` or `out` says otherwise)."""

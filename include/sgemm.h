@@ -503,11 +503,10 @@ int sgemm_expert_combine_grad(sgemm_handle_t h, int type, int tokens, int choice
  * [0, experts) are left out, a token with none gets zeros; an expert that a token
  * names twice counts with both weights.
  *
- * X is taken as it is and the products are summed in FP32; the hidden values act(..) are
- * rounded to X's type (with FP32 rows to 24 bits; FP16 ones beyond 65504 become infinite).
- * Only the experts that some token names are read.  tokens up to 64, tokens * choices up to
- * 1024, experts up to 1024, and the hidden values (2 bytes each, 6 with FP32 rows, hidden
- * rounded up to 128, one row a choice) up to 48 MiB, else
+ * X is taken as it is (16 or 32 bits) and the products are summed in FP32; the hidden
+ * values keep 16 bits of fraction (24 with FP32 rows).  Only the experts that some
+ * token names are read.  tokens up to 64, tokens * choices up to 1024, experts up to 1024, and the hidden
+ * values (4 bytes each, 6 with FP32 rows, hidden rounded up to 128, one row a choice) up to 48 MiB, else
  * SGEMM_ERR_INVALID_VALUE.  Other checks as for the routing calls. */
 int sgemm_expert_layer_int8(sgemm_handle_t h, int type, int gated, int tokens, int choices, int experts, int width,
                             int hidden, const void *X, int ldx, const int *ids, const float *weights,
