@@ -8,11 +8,17 @@
 //    tokens: bound by the weights' way from HBM.  The channels are the MMA's M, so that
 //    a weight tile is used whole however few the tokens.  Up to 8 CTAs of a cluster
 //    share a tile's K range; their sums meet in distributed shared memory and are
-//    added in the order of the ranks, each CTA a slice of the tokens.
+//    added in the order of the ranks, each CTA a slice of the tokens.  In a graph 1 x 4096 x
+//    4096 4.0 us (NV; launch, tensor memory and first loads are 2.5 of them), 64 x 8192 x 8192
+//    9.9 (MX; 5.4 at HBM's rate, 128 of the SMs busy, 1 of exchange).
 //  * fp4_pair_kernel -- 256 channels x 256 tokens on a CTA pair (cta_group::2),
 //    persistent, for many tokens: each CTA holds 128 of the channels and 128 of the
 //    tokens.  The epilogue's eight warps take the whole accumulator into registers
-//    and leave it to the next tile's MMAs before they write C.
+//    and leave it to the next tile's MMAs before they write C.  8192^3: 161 us in short runs
+//    (NV, 6.8 PFLOP/s; MX 174), 180 when repeated until the power limit shows.  What bounds
+//    it: with a quarter of the MMAs 151 us, without the operands' loads 133 (2.5 GB cross from
+//    L2 to the SMs, 16.5 TB/s), without the writes of C 147 (the accumulator's way into
+//    registers, 1 us a tile, in which no MMA runs).
 //  * fp4_generic_kernel -- CUDA cores, any alignment, where the rows can neither be
 //    read as stored nor be copied.
 //

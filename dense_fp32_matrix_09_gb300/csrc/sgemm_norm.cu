@@ -12,7 +12,10 @@
 //    of a sum, whatever its order.  Without a norm v = x and r = 1.
 //    One pass over HBM: a row stays in the registers of the TPR threads that share
 //    it (up to 4 x 8 elements a thread; longer rows are read a second time, from L2).
-//  * dequantize_kernel -- 4-bit rows to what they stand for.
+//    8192 x 8192 BF16 with the residual to 8 bits 67.8 us, HBM's rate; 32 x 4096 2.1 us in
+//    a graph.  To 4 bits the instructions count too: 8192 x 8192 FP16 to MX 30 us (floor
+//    25), to NV, whose scales wait for the whole row, 38.
+//  * dequantize_kernel -- 4-bit rows to what they stand for: the same matrix 29 us (floor 25).
 //
 // No load is a read-only-cache load: what is read may have been written by the
 // kernel before, whose end the launch overlaps.

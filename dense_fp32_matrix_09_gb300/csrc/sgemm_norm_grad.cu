@@ -7,7 +7,9 @@
 //    what reaches h are read once and stay in registers for the row's sum and its
 //    gradient, the columns' sums in registers from row to row; at the end each group
 //    of threads writes its sums, a row of `parts`.
-//  * norm_grad_ring_kernel -- the same for long rows on 16-byte boundaries.
+//  * norm_grad_ring_kernel -- the same for long rows on 16-byte boundaries: 8192 x 4096 BF16
+//    with the gradient that reaches h 43 us, floor 40, and 5 for the columns' sums, which
+//    overlap.
 //  * columns_kernel -- dw: the rows of `parts` added up.
 //  * norm_grad_wide_kernel, columns_wide_kernel -- the same for rows longer than the
 //    registers of 512 threads hold: each row is read twice, and the columns' sums are
