@@ -412,7 +412,7 @@ struct LayerArgs {
     uint16_t *h;  // workspace, layer_floats floats: the hidden rows in BF16 parts
     int *status;
     // set by the launch
-    int hidden_ld;
+    int hidden_ld, channels;  // channels: of an item of down_stream_kernel
     long long up_rows, h_part;
 };
 size_t layer_floats(int type, int slots, int hidden);

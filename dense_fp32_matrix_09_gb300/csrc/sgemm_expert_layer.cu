@@ -7,11 +7,10 @@
 //
 //  * up_stream_kernel, down_stream_kernel -- rows on 16-byte boundaries: the weights stream
 //    through shared memory by TMA.  One token, four of 32 experts of 4096 x 2048, gated, BF16
-//    (100 MB): 33 us, 15 of them HBM's, 5 the launches, 4 the routing and the first loads of
-//    both kernels; 8 tokens (530 MB) 126 us, 4.3 TB/s.  The first kernel runs at 4.9 TB/s,
-//    the second at 3: each of its stages of 16 KB is little work for a long chain -- a wait,
-//    loads, the conversion, MMAs that wait for one another -- and its 256 items make 1.7 rounds
-//    of the SMs.
+//    (100 MB): 31 us, 15 of them HBM's, 5 the launches, 4 the routing and the first loads of
+//    both kernels; 8 tokens (530 MB) 117 us, 4.6 TB/s.  The first kernel runs at 5 TB/s,
+//    the second at 3.7: its instructions (half of the issue slots, by four warps a scheduler)
+//    and what they wait for, no one thing among it.
 //  * up_kernel, down_kernel -- any alignment: the weights straight into registers (the sizes
 //    above less one 71 us; 8 tokens, width 3001, 1501 hidden 198).
 //
@@ -25,8 +24,8 @@
 // is free, so a lane's 16 bytes are the k of four MMAs.  An int8 is exact in BF16 and in FP16;
 // the tokens' elements go in as they are or, FP32, as sums of three BF16 values, exact as well.
 // The hidden values are kept as two BF16 values, 16 bits of fraction, and with FP32 rows as three:
-// rounded to the rows' type they would halve the second kernel's loads and MMAs (8 tokens 116
-// us), but also add as much error to the result as its own rounding does, and in FP16 they
+// rounded to the rows' type they would halve the second kernel's loads and MMAs (8 tokens 126 us -> 116
+// with stages of 16 rows), but also add as much error to the result as its own rounding does, and in FP16 they
 // could overflow.  Within a warp sums run along k; the warps' sums, the experts' and the
 // choices' are added in a fixed order in FP32.
 #include <type_traits>
@@ -385,7 +384,7 @@ __device__ __forceinline__ void load_hidden(const uint16_t *row, long long part,
 constexpr int kOutPitch = 17;
 template <int NT>
 __device__ __forceinline__ void add_out(const Routing &r, float *mine, int first, int cols, int g, int t, float sl, float sh,
-                                        const float (&acc)[NT][4]) {
+                                        const float (&acc)[NT][4], int pitch = kOutPitch) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -393,7 +392,7 @@ __device__ __forceinline__ void add_out(const Routing &r, float *mine, int first
             const int col = n * 8 + 2 * t + j;
             if (col >= cols) continue;
             const Routing::Column c = r.column[first + col];
-            float *to = mine + c.token * kOutPitch;
+            float *to = mine + c.token * pitch;
             to[g] = fmaf(acc[n][j] * sl, c.weight, to[g]);
             to[g + 8] = fmaf(acc[n][2 + j] * sh, c.weight, to[g + 8]);
         }
@@ -567,15 +566,20 @@ struct StreamCfg {
     static constexpr int kSumBytes = kTakers * 2 * NT * 512;       // of a set
     static constexpr int kUpThreads = (kTakers + 1 + NT) * 32, kDownThreads = (kTakers + 1) * 32;
     static constexpr int kUpRing = 1024 + kUpStages * 32 * kSeg, kUpSmem = kUpRing + kSums * kSumBytes;
-    // Hidden values of two of a warp's stages in shared memory, where that has room for them.
+    // Hidden values of two of a warp's stages in shared memory, where that has room for them: of
+    // four columns.  What an expert has beyond is read where it is needed (with all eight kept the
+    // ring had half the stages: 8 tokens on the same experts 58 us against 54, on all of
+    // eight experts 86 against 73; on experts of their own 126 against 130, before the 32-row stages).
     static constexpr bool kHeld = NT == 1 && Parts<El>::hidden == 2;
-    static constexpr int kHeldBytes = kHeld ? 2 * Parts<El>::hidden * 1024 : 0;  // of a stage
-    static constexpr int kDownStages = kHeld ? 4 : NT == 1 ? 8 : 6;  // of 16 rows, half of them a team's
+    static constexpr int kHeldColumns = 4;
+    static constexpr int kHeldPiece = kHeldColumns * 64, kHeldBytes = kHeld ? 4 * Parts<El>::hidden * kHeldPiece : 0;  // of a stage
+    static constexpr int kMostTiles = NT == 1 ? 2 : 1;       // of 16 channels, of an item of down_stream_kernel
+    static constexpr int kDownStages = NT == 1 ? 8 : 6;  // of 16 rows, or half as many of 32; half of them a team's
     static constexpr int kDownRing = 1024 + kDownStages * 16 * kSeg;
-    static constexpr int down_smem(int tokens) { return kDownRing + kTakers * (2 * kHeldBytes + tokens * kOutPitch * 4); }
+    static constexpr int down_smem(int tokens, int tiles) { return kDownRing + kTakers * (2 * kHeldBytes + tokens * (tiles * 16 + 1) * 4); }
     static_assert(sizeof(RouteScratch) <= 2 * 16 * kSeg, "the routing's scratch lies in the ring");
     // the most tokens of a call on this configuration; the routing takes less than 17 KiB
-    static_assert(down_smem(NT == 1 ? 8 : kLayerTokens) <= 232448 - 17408 && kUpSmem <= 232448 - 17408, "shared memory");
+    static_assert(down_smem(NT == 1 ? 8 : kLayerTokens, kMostTiles) <= 232448 - 17408 && kUpSmem <= 232448 - 17408, "shared memory");
 };
 constexpr int kPrefetch = 64;  // boxes of 2 KiB
 struct StreamShared {
@@ -711,14 +715,21 @@ up_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
                 }
         }
         // What this CTA's successor in down_stream_kernel reads first is fetched into L2 while
-        // it starts (its weights may be: see there).
+        // it starts (its weights may be: see there).  The CTA ends no earlier than this
+        // loop, so that a load or a division in it shows: the expert looked up for every box, 1
+        // token 33 us against 31; none fetched 31.5, 128 boxes 33.8.
         int left = kPrefetch;
-        for (int i = blockIdx.x; i < (a.width + 15) / 16; i += gridDim.x)
-            for (int group = 0; group < r.groups; ++group)
-                for (int s = 0; s < (a.hidden + 127) / 128; ++s, --left) {
-                    if (left == 0) return;
-                    tma_prefetch_2d(&next_map, s * 128, r.group[group].expert * a.width + i * 16);
-                }
+        const int d0 = static_cast<int>(blockIdx.x) * a.channels;
+        if (d0 >= a.width) return;
+        for (int group = 0; group < r.groups; ++group) {
+            const int row = r.group[group].expert * a.width + d0;
+            for (int s = 0; s < a.hidden; s += 128) {
+                if (left <= 0) return;
+                tma_prefetch_2d(&next_map, s, row);
+                if (a.channels > 16) tma_prefetch_2d(&next_map, s, row + a.channels - 16);
+                left -= a.channels > 16 ? 2 : 1;
+            }
+        }
         return;
     }
     if (warp > kTakers) {
@@ -833,31 +844,36 @@ __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.com
 template <int N>
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// As down_kernel, with a grid of as many CTAs as run at once; a stage is 16 channels' rows of up
-// to 1024 hidden values of a group.  Two teams of eight warps take the groups in turn, 128
+// As down_kernel, with a grid of as many CTAs as run at once; a stage is 16 MT channels' rows of up
+// to 1024 hidden values of a group.  With MT = 2 a hidden value that a lane has fetched meets 32
+// rows, and an item has as many channels as fall to an SM in a round of all: of 4096 on 152 SMs
+// 27 each in 152 items, not 1.7 rounds of 16 (8 tokens, 4 of 32 experts, 4096 x 2048: 130 -> 117 us).
+// The second tile's rows end with the item's; those that both tiles have come from L2 twice.  Two teams of eight warps take the groups in turn, 128
 // bytes of a row each: while one team's loads, sums and waits take their time, the other
 // multiplies (sixteen warps on every stage, 64 bytes each: 75 us for a batch of 8 tokens,
 // most of it instructions that are not the product's).  A lane fetches the hidden values of
 // its team's stages ahead, two where shared memory has room for them (one, in registers: 62 us
 // for that batch), and the scales of its next group when it begins one.
-template <class El, int NT>
+template <class El, int NT, int MT>
 __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_stream_kernel(const __grid_constant__ CUtensorMap map, const LayerArgs a) {
     using Cf = StreamCfg<El, NT>;
-    constexpr int PH = Parts<El>::hidden, S = Cf::kDownStages / 2;
+    constexpr int PH = Parts<El>::hidden, S = Cf::kDownStages / 2 / MT, kPitch = MT * 16 + 1;
     extern __shared__ uint8_t smem[];
     __shared__ StreamShared shared;
     __shared__ Routing r;
     // A ring for each team: one that skipped the other's stages in a common ring could take the
     // parity of a slot's round before last for its own.
-    Stream<S, 16> streams[2];
+    Stream<S, MT * 16> streams[2];
     open_streams(streams, smem, &shared, 1, kTakers / 2, a.status);
-    float *out_sums = reinterpret_cast<float *>(smem + Cf::kDownRing + kTakers * 2 * Cf::kHeldBytes);  // [warp][token][kOutPitch]
-    for (int k = threadIdx.x; k < kTakers * a.tokens * kOutPitch; k += Cf::kDownThreads) out_sums[k] = 0.f;
+    float *out_sums = reinterpret_cast<float *>(smem + Cf::kDownRing + kTakers * 2 * Cf::kHeldBytes);  // [warp][token][kPitch]
+    for (int k = threadIdx.x; k < kTakers * a.tokens * kPitch; k += Cf::kDownThreads) out_sums[k] = 0.f;
     route<Cf::kDownThreads>(r, *reinterpret_cast<RouteScratch *>(streams[0].ring), a, 8 * NT);  // (before anything lands there)
     tc::fence_proxy_async_smem();
     __syncthreads();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const int items = (a.width + 15) / 16, step = static_cast<int>(gridDim.x), groups = r.groups;
+    // An item's second tile ends with its channels: those that the first has too are left there.
+    const int channels = MT == 1 ? 16 : a.channels, second = channels - 16;
+    const int items = (a.width + channels - 1) / channels, step = static_cast<int>(gridDim.x), groups = r.groups;
     if (warp == kTakers) {
         if (lane > 0) return;
         // (the weights: the kernel before does not write them, and has waited for what came
@@ -867,8 +883,8 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
         for (int i = blockIdx.x; i < items && ok; i += step)
             for (int group = 0; group < groups && ok; ++group, turn ^= 1)
                 for (int k = 0; k < a.hidden && ok; k += kSeg) {
-                    const int row = r.group[group].expert * a.width + i * 16;
-                    ok = turn ? streams[1].put(&map, k, row, 0) : streams[0].put(&map, k, row, 0);
+                    const int row = r.group[group].expert * a.width + i * channels;
+                    ok = turn ? streams[1].put(&map, k, row, row + second) : streams[0].put(&map, k, row, row + second);
                 }
         if (!ok) {
             streams[0].drain();
@@ -877,10 +893,10 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
         return;
     }
     const int team = warp / (kTakers / 2), column = warp % (kTakers / 2);  // of 128 bytes
-    Stream<S, 16> q = team ? streams[1] : streams[0];
+    Stream<S, MT * 16> q = team ? streams[1] : streams[0];
     const int place[2] = {place_of(g, column, 2 * t), place_of(g, column, 2 * t + 1)};
     const bool idle = column * 128 >= a.hidden;                            // (short rows leave columns out)
-    float *mine = out_sums + warp * a.tokens * kOutPitch;
+    float *mine = out_sums + warp * a.tokens * kPitch;
     bool ok = true;
     // The team's groups: every other one, counted over all items, so that both have as many.
     struct Cursor {
@@ -895,14 +911,17 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
     };
     // The channels' scales of the next group, on their way while one is multiplied (the first
     // before the kernel before has ended, which does not write them).
-    float next_l = 0.f, next_h = 0.f;
+    float next_l[MT] = {}, next_h[MT] = {};
     Cursor coming{team, static_cast<int>(blockIdx.x)};
     auto scales = [&]() {
         if (!settle(coming)) return;
-        const int d = coming.item * 16 + g;
-        const float *scale = a.down_scale + (static_cast<long long>(r.group[coming.group].expert) * a.width + d);
-        next_l = d < a.width ? __ldca(scale) : 0.f;
-        next_h = d + 8 < a.width ? __ldca(scale + 8) : 0.f;
+        const float *scale = a.down_scale + static_cast<long long>(r.group[coming.group].expert) * a.width;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int d = coming.item * channels + m * second + g;
+            next_l[m] = d < a.width ? __ldca(scale + d) : 0.f;
+            next_h[m] = d + 8 < a.width ? __ldca(scale + d + 8) : 0.f;
+        }
         coming.group += 2;
     };
     if (groups > 0) scales();
@@ -918,7 +937,7 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
     auto fetch = [&]() {
         if (settle(fetched)) {
             const Routing::Group of = r.group[fetched.group];
-            if (g < of.cols && f_k + column * 128 < a.hidden) {
+            if (g < of.cols && (!Cf::kHeld || g < Cf::kHeldColumns) && f_k + column * 128 < a.hidden) {
                 const uint16_t *h = h_lane + (static_cast<long long>(of.first + g) * a.hidden_ld + f_k);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -928,7 +947,7 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
                         for (int p = 0; p < PH; ++p)
 #pragma unroll
                             for (int x = 0; x < 2; ++x)
-                                copy_async16(held + f_slot * Cf::kHeldBytes + ((c * PH + p) * 2 + x) * 512, h + p * a.h_part + c * 16 + x * 8);
+                                copy_async16(held + f_slot * Cf::kHeldBytes + ((c * PH + p) * 2 + x) * Cf::kHeldPiece, h + p * a.h_part + c * 16 + x * 8);
                 }
             }
             f_k += kSeg;
@@ -949,9 +968,14 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
         for (int n_group = 0; n_group < groups; ++n_group, turn ^= 1) {
             if (turn) continue;
             const Routing::Group now = r.group[n_group];
-            const float sl = next_l, sh = next_h;
+            float sl[MT], sh[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                sl[m] = next_l[m];
+                sh[m] = next_h[m];
+            }
             scales();
-            float acc[NT][4] = {}, half[4] = {};  // (the first eight columns in two chains: an MMA waits for the one before it)
+            float acc[MT][NT][4] = {}, half[4] = {};  // (two chains, of the tiles or of a tile's halves: an MMA waits for the one before it)
             for (int k = 0; k < a.hidden; k += kSeg) {
                 ok = ok && q.get();  // (after a wait that ran out the warps still meet at the barriers)
                 if (!ok) break;
@@ -959,23 +983,28 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
                 if (k + column * 128 < a.hidden) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        if (Cf::kHeld)
+                        if (Cf::kHeld && g >= Cf::kHeldColumns) {
+                            if (g < now.cols) load_hidden<PH>(h_lane + static_cast<long long>(now.first + g) * a.hidden_ld, a.h_part, k + c * 16, ahead[c]);
+                        } else if (Cf::kHeld)
 #pragma unroll
                             for (int p = 0; p < PH; ++p)
 #pragma unroll
                                 for (int x = 0; x < 2; ++x)
-                                    *reinterpret_cast<uint4 *>(&ahead[c][p][4 * x]) = *reinterpret_cast<const uint4 *>(held + slot * Cf::kHeldBytes + ((c * PH + p) * 2 + x) * 512);
-                        uint4 lo, hi;
-                        q.take(place[c], place[c] + 1024, lo, hi);
-                        uint32_t w[4][4];
-                        expand_rows<ElBF16>(lo, hi, w);
-                        multiply<ElBF16, PH>(c ? half : acc[0], w, ahead[c]);
+                                    *reinterpret_cast<uint4 *>(&ahead[c][p][4 * x]) = *reinterpret_cast<const uint4 *>(held + slot * Cf::kHeldBytes + ((c * PH + p) * 2 + x) * Cf::kHeldPiece);
 #pragma unroll
-                        for (int n = 1; n < NT; ++n) {
-                            if (n * 8 >= now.cols) break;
-                            uint32_t v[PH][8];
-                            load_hidden<PH>(n * 8 + g < now.cols ? h_lane + static_cast<long long>(now.first + n * 8 + g) * a.hidden_ld : nullptr, a.h_part, k + c * 16, v);
-                            multiply<ElBF16, PH>(acc[n], w, v);
+                        for (int m = 0; m < MT; ++m) {
+                            uint4 lo, hi;
+                            q.take(place[c] + m * (16 * kSeg), place[c] + m * (16 * kSeg) + 1024, lo, hi);
+                            uint32_t w[4][4];
+                            expand_rows<ElBF16>(lo, hi, w);
+                            multiply<ElBF16, PH>(MT == 1 && c ? half : acc[m][0], w, ahead[c]);
+#pragma unroll
+                            for (int n = 1; n < NT; ++n) {
+                                if (n * 8 >= now.cols) break;
+                                uint32_t v[PH][8];
+                                load_hidden<PH>(n * 8 + g < now.cols ? h_lane + static_cast<long long>(now.first + n * 8 + g) * a.hidden_ld : nullptr, a.h_part, k + c * 16, v);
+                                multiply<ElBF16, PH>(acc[m][n], w, v);
+                            }
                         }
                     }
                 }
@@ -984,16 +1013,20 @@ __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_strea
                 fetch();
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[0][c] += half[c];
-            if (!idle) add_out<NT>(r, mine, now.first, now.cols, g, t, sl, sh, acc);
+            for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[m][0][c] += half[c];
+                if (!idle) add_out<NT>(r, mine + m * 16, now.first, now.cols, g, t, sl[m], sh[m], acc[m], kPitch);
+            }
         }
         named_barrier_sync(1, kTakers * 32);
-        for (int k = threadIdx.x; k < a.tokens * 16; k += kTakers * 32) {
-            const int token = k / 16, d = i * 16 + k % 16;
+        for (int k = threadIdx.x; k < a.tokens * channels; k += kTakers * 32) {
+            const int token = k / channels, at = k - token * channels, d = i * channels + at;
+            const int slot = MT == 1 || at < 16 ? at : at - second + 16;
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kTakers; ++w) {
-                float &part = out_sums[(w * a.tokens + token) * kOutPitch + k % 16];
+                float &part = out_sums[(w * a.tokens + token) * kPitch + slot];
                 sum += part;
                 part = 0.f;
             }
@@ -1011,17 +1044,23 @@ struct LayerMaps {
 constexpr long long kMostRows = (1ll << 31) - 64;  // coordinates are ints
 
 template <class El, int NT>
-cudaError_t layer_typed(const LayerArgs &a, bool boundaries, const LayerMaps &m, int num_sms, cudaStream_t stream) {
+cudaError_t layer_typed(LayerArgs a, bool boundaries, const LayerMaps &m, int num_sms, cudaStream_t stream) {
     // (the groups are on the device: so many there are at most)
     const long long slots = static_cast<long long>(a.tokens) * a.choices, asked = slots < a.experts ? slots : a.experts;
     auto grid = [](long long ctas, long long most) { return dim3(static_cast<unsigned>(ctas < 1 ? 1 : ctas < most ? ctas : most)); };
     if (boundaries) {
         using Cf = StreamCfg<El, NT>;
         const int kCh = a.gated ? 16 : 32;
+        // An item of the second product: 16 channels or, where the SMs would take more than one
+        // such each, up to 32, as many in each item of a round of all SMs.
+        const int rounds = (a.width + 32 * num_sms - 1) / (32 * num_sms);
+        const bool wide = Cf::kMostTiles == 2 && a.width > 16 * num_sms;
+        a.channels = wide ? (a.width + rounds * num_sms - 1) / (rounds * num_sms) : 16;
         cudaError_t e = launch_dependent(a.gated ? up_stream_kernel<El, NT, true> : up_stream_kernel<El, NT, false>, grid(slots * ((a.hidden_ld + kCh - 1) / kCh), num_sms),
                                          dim3(Cf::kUpThreads), Cf::kUpSmem, stream, 1, m.up, m.down, a);
         if (e != cudaSuccess) return e;
-        return launch_dependent(down_stream_kernel<El, NT>, grid((a.width + 15) / 16, num_sms), dim3(Cf::kDownThreads), Cf::down_smem(a.tokens), stream, 1, m.down, a);
+        return launch_dependent(wide ? down_stream_kernel<El, NT, Cf::kMostTiles> : down_stream_kernel<El, NT, 1>, grid((a.width + a.channels - 1) / a.channels, num_sms), dim3(Cf::kDownThreads),
+                                Cf::down_smem(a.tokens, wide ? 2 : 1), stream, 1, m.down, a);
     }
     const long long items = asked * (a.hidden_ld / (a.gated ? 8 : 16));
     // warps that share an item's K: all eight unless that leaves a CTA many rounds
@@ -1054,8 +1093,9 @@ cudaError_t prepare_typed() {
     cudaError_t e = cudaFuncSetAttribute(down_kernel<El, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSums);
     for (auto *k : {up_stream_kernel<El, NT, false>, up_stream_kernel<El, NT, true>})
         if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<El, NT>::kUpSmem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(down_stream_kernel<El, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, StreamCfg<El, NT>::down_smem(NT == 1 ? 8 : kLayerTokens));
+    using Cf = StreamCfg<El, NT>;
+    for (auto *k : {down_stream_kernel<El, NT, 1>, down_stream_kernel<El, NT, Cf::kMostTiles>})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::down_smem(NT == 1 ? 8 : kLayerTokens, Cf::kMostTiles));
     return e;
 }
 

@@ -115,6 +115,15 @@ def test_odd_sizes_and_addresses(h, kind, gated, T, J, E, W, F):
     check(h, kind, gated, p, pad=3, off=1)
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,J,E,W,F", [(8, 2, 3, 2448, 80), (5, 1, 1, 4096, 1040), (1, 3, 5, 4880, 64), (8, 1, 1, 6992, 144), (8, 4, 9, 2560, 2064), (8, 3, 4, 9744, 16)])
+def test_wide_rows_of_a_few_tokens(h, kind, gated, T, J, E, W, F):
+    """More channels than 16 an SM: items of up to 32, the last one cut, one round or more of them; experts
+    of one column and of all eight."""
+    check(h, kind, gated, problem(kind, gated, T, J, E, W, F))
+
+
 @pytest.mark.parametrize("T", [4, 40])
 def test_dropped_repeated_and_crowded_choices(h, T):
     J, E, W, F = 3, 5, 96, 64
