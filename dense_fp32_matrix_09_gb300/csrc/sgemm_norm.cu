@@ -31,9 +31,12 @@ namespace {
 constexpr int OUT_Y = 0, OUT_I8 = 1, OUT_F4 = 2;
 
 constexpr unsigned kInfBits = 0x7f800000u;
-// Below these row maxima a quotient of the quantization overflows: the row is stored
-// as zeros.
-constexpr float kLeastI8 = 127.f * 1.17549435e-38f, kLeastNV = 2688.f * 1.17549435e-38f;
+// Below these row maxima the quotient 127 / m or 2688 / m overflows: the row is stored as
+// zeros.
+constexpr float kLeastI8 = 127.f * 0x1p-126f, kLeastNV = 2688.f * 0x1p-126f;
+// From kLeastNV up to here (2688 / m) / s may overflow, s being 2^-9 or more.  Such a row is
+// taken 2^16 times larger, which is exact and changes none of its codes and scales.
+constexpr float kTinyNV = 2688.f * 0x1p-118f, kLiftNV = 0x1p16f;
 constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23: added to a value below 2^22 it rounds it to an integer
 
 // Sum and maximum over the TPR threads of a row, in the same order on every call.
@@ -89,7 +92,7 @@ __device__ __forceinline__ unsigned block_max(unsigned top, int lanes) {
 struct Fp4Row {
     uint8_t *q, *s;  // s: the row's first word of scales
     int K, format, words, vec;
-    float up, near;  // NV: 2688 / m, 448 / m
+    float up, near;  // NV: 2688 / m, 448 / m; up below 0 where v is taken -2^16 times
 };
 
 // One piece (see load8) of a row to 4 bits.  The whole warp.
@@ -275,12 +278,12 @@ row_kernel(const RowArgs a) {
         });
         return;
     }
-    Fp4Row f{static_cast<uint8_t *>(a.Y) + row * a.ldy, a.S + fp4_scale_word(row, 0, a.words), a.K, a.format, a.words, a.vec, 0.f, 0.f};
-    bool blank = false;  // an NV row of zeros: every scale 0
+    Fp4Row f{static_cast<uint8_t *>(a.Y) + row * a.ldy, a.S + fp4_scale_word(row, 0, a.words), a.K, a.format, a.words, a.vec, 1.f, 0.f};
     if (a.format == SGEMM_FP4_NV) {
-        blank = !number || m < kLeastNV;
-        f.up = blank ? 0.f : __fdiv_rn(2688.f, m);
-        f.near = blank ? 0.f : __fdiv_rn(448.f, m);
+        const bool blank = !number || m < kLeastNV;  // a row of zeros: every scale 0
+        const float top_value = m < kTinyNV ? m * -kLiftNV : m;
+        f.up = blank ? 0.f : __fdiv_rn(2688.f, top_value);
+        f.near = blank ? 0.f : __fdiv_rn(448.f, fabsf(top_value));
         if (lane == 0) a.row[i] = !number ? nan : blank ? 0.f : __fmul_rn(__fdiv_rn(m, 2688.f), r);
     } else if (lane == 0 && a.row) {
         a.row[i] = r;
@@ -289,9 +292,10 @@ row_kernel(const RowArgs a) {
         if (c * kV * TPR >= a.K) return;  // (the whole row's threads)
         float v[kV];
         scaled(p, q, v);
-        if (blank)
+        if (f.up <= 0.f) {
 #pragma unroll
-            for (int e = 0; e < kV; ++e) v[e] = 0.f;
+            for (int e = 0; e < kV; ++e) v[e] = f.up < 0.f ? v[e] * -kLiftNV : 0.f;
+        }
         put_fp4<TPR, A>(f, c, lane, v);
     });
 }

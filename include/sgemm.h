@@ -359,8 +359,9 @@ int sgemm_quantize_rows(sgemm_handle_t h, int type, int M, int K, const void *X,
  *       q = X / s to the nearest of the values, magnitudes above 6 to 6;
  *       row (NULL allowed) = 1.  A block with an infinity or a NaN gets s = NaN, q = 0.
  *   NV: row = m / 2688;  s = E4M3(m_b * (448 / m));  q = X * ((2688 / m) / s) likewise
- *       (s = 0: q = 0).  A row with m < 2688 * 2^-126 (all zeros among them) gets row = 0,
- *       s = 0, q = 0; a row with an infinity or a NaN row = NaN, s = 0, q = 0.
+ *       (s = 0: q = 0; the quotient, which can pass FP32's range where m < 2688 * 2^-118, as
+ *       with an exponent without bounds).  A row with m < 2688 * 2^-126 (all zeros among them)
+ *       gets row = 0, s = 0, q = 0; a row with an infinity or a NaN row = NaN, s = 0, q = 0.
  * Every product with a NaN scale is NaN.
  * sgemm_dequantize_fp4 gives Y = row * s * q, rounded to FP32 and then to `type`.
  *
