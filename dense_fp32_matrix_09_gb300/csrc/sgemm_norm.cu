@@ -286,7 +286,8 @@ row_kernel(const RowArgs a) {
         f.near = blank ? 0.f : __fdiv_rn(448.f, fabsf(top_value));
         if (lane == 0) a.row[i] = !number ? nan : blank ? 0.f : __fmul_rn(__fdiv_rn(m, 2688.f), r);
     } else if (lane == 0 && a.row) {
-        a.row[i] = r;
+        // (a row of zeros is one whatever r, which without eps is an infinity)
+        a.row[i] = top == 0 && r >= __uint_as_float(kInfBits) ? 0.f : r;
     }
     each([&](int c, const Pack8<T> &p, const Pack8<T> &q) {
         if (c * kV * TPR >= a.K) return;  // (the whole row's threads)

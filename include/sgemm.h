@@ -417,7 +417,9 @@ int sgemm_check_args_fp4(int format, int out_type, int M, int N, int K, const ui
  * The quantized forms are the input of sgemm_run_int8 and sgemm_run_fp4; what v rounds to
  * does not depend on r, so the integers and codes are the same whatever the order of
  * a sum.  Special rows as by sgemm_quantize_rows and sgemm_quantize_fp4.  Sums are in FP32,
- * in a fixed order; a row whose sum of squares overflows FP32 has r = 0.
+ * in a fixed order; a row whose sum of squares overflows FP32 has r = 0.  With eps = 0 a row
+ * whose sum of squares is 0 has r = infinity: of a row of zeros the Y of sgemm_rms_norm (and
+ * its gradient) is NaN, the quantized forms make zeros with row scales of 0.
  *
  * sgemm_rms_norm_grad, from dY, the gradient dH that reaches H from elsewhere (the
  * residual's further way; NULL: none), H and rstd:
