@@ -101,8 +101,8 @@ struct Fp4Choice {
 // while the CTAs make one wave and each split saves enough stages of 0.23 us for the exchange's 0.8 (1
 // x 4096 x 4096: whole 5.9, in two 4.9, four 4.0, eight, two CTAs an SM, 4.5; 1 x 8192 x 1024, four
 // stages: 3.1, 3.4, 3.9; 64 x 8192 x 8192: 12.9, 9.9, 10.5; 128 x 4096 x 4096: 8.8, 7.6, 7.0, 11.0).
-Fp4Choice choose_fp4(int M, int N, int K, int num_sms) {
-    if (M > 128 && cdiv(M, 256) * cdiv(N, 256) >= num_sms / 5) return {256, 1};
+Fp4Choice choose_fp4(int M, int N, int K, int num_sms, bool pairs) {
+    if (pairs && M > 128 && cdiv(M, 256) * cdiv(N, 256) >= num_sms / 5) return {256, 1};
     const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     const long long tiles = cdiv(M, nt) * cdiv(N, 128);
     const int stages = static_cast<int>(cdiv(K, sg::kFp4StageK));
@@ -124,7 +124,7 @@ int run_fp4(sgemm_handle_t h, sg::Fp4Args a, cudaStream_t stream) {
     bool tc = a.K > 0 && v.pinned != SGEMM_VARIANT_GENERIC && v.pinned != SGEMM_VARIANT_GENERIC_F4 &&
               (!copies || (v.d_rl != nullptr && v.relayout_mode != SGEMM_RELAYOUT_OFF && a_bytes + b_bytes <= v.rl_bytes)) &&
               std::max(cdiv(a.M, 128), cdiv(a.N, 128)) * a.words < INT_MAX;
-    Fp4Choice pick = choose_fp4(a.M, a.N, a.K, v.num_sms);
+    Fp4Choice pick = choose_fp4(a.M, a.N, a.K, v.num_sms, v.pinned != SGEMM_VARIANT_TC_F4);
     if (v.f4_tokens) {
         pick = {v.f4_tokens, v.f4_split};
         // (a tile of fewer than 128 tokens has to be the call's only one)

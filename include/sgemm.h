@@ -391,7 +391,8 @@ int64_t sgemm_fp4_scale_bytes(int format, int rows, int K);
  * of 16 bytes apart, and otherwise first copied into the re-layout workspace
  * (sgemm_last_relayout: bit 0 A, bit 1 B; one more launch for both).  Where the
  * copies do not fit or SGEMM_RELAYOUT_OFF forbids them, or with SGEMM_VARIANT_GENERIC
- * or _GENERIC_F4 pinned, the generic kernel runs.  SGEMM_VARIANT_TC_F4_PAIR may be pinned.
+ * or _GENERIC_F4 pinned, the generic kernel runs.  SGEMM_VARIANT_TC_F4 and _TC_F4_PAIR may be
+ * pinned; then they run at any size where the generic kernel need not.
  * sgemm_last_variant also reports the CTAs that share a tile's K range.
  * Checks as for the 4-bit rows, nothing done when M == 0 or N == 0. */
 int sgemm_run_fp4(sgemm_handle_t h, int format, int out_type, int M, int N, int K, const uint8_t *A, int lda,
