@@ -710,6 +710,8 @@ class Fp4Rows(typing.NamedTuple):
 
 def fp4_blocks(fmt, K) -> int:
     """Blocks of a row of K elements."""
+    if fmt not in (FP4_MX, FP4_NV):
+        raise ValueError(f"unknown 4-bit format {fmt}")
     return -(-K // (32 if fmt == FP4_MX else 16))
 
 
@@ -722,7 +724,7 @@ def fp4_tile_scales(scales, fmt, K):
         raise ValueError(f"scales must be uint8, rows x {fp4_blocks(fmt, K)}, got {scales.dtype} {tuple(scales.shape)}")
     full = torch.zeros(-(-rows // 128) * 128, -(-blocks // 4) * 4, dtype=torch.uint8, device=scales.device)
     full[:rows, :blocks] = scales
-    return full.view(-1, 4, 32, full.shape[1] // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1).contiguous()
+    return full.view(full.shape[0] // 128, 4, 32, full.shape[1] // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1).contiguous()
 
 
 def _fp4(name, a) -> None:
