@@ -690,7 +690,7 @@ up_stream_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant_
     using Mma = typename Parts<El>::Mma;
     using Cf = StreamCfg<El, NT>;
     constexpr int P = Parts<El>::in, PH = Parts<El>::hidden, kCh = GATED ? 16 : 32;
-    extern __shared__ uint8_t smem[];
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ StreamShared shared;
     __shared__ Routing r;
     Stream<Cf::kUpStages, 32> streams[1], &q = streams[0];
@@ -858,7 +858,7 @@ template <class El, int NT, int MT>
 __global__ void __launch_bounds__(StreamCfg<El, NT>::kDownThreads, 1) down_stream_kernel(const __grid_constant__ CUtensorMap map, const LayerArgs a) {
     using Cf = StreamCfg<El, NT>;
     constexpr int PH = Parts<El>::hidden, S = Cf::kDownStages / 2 / MT, kPitch = MT * 16 + 1;
-    extern __shared__ uint8_t smem[];
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ StreamShared shared;
     __shared__ Routing r;
     // A ring for each team: one that skipped the other's stages in a common ring could take the
