@@ -69,9 +69,11 @@ __device__ __forceinline__ float from_e4m3(uint32_t code) {
 // 2^n for n in [-126, 127].
 __device__ __forceinline__ float exp2_of(int n) { return __int_as_float((n + 127) << 23); }
 
-// The value of an E8M0 scale: 2^(code - 127), 255 a NaN.
+// The value of an E8M0 scale: 2^(code - 127), 255 a NaN (BF16 has all of them).
 __device__ __forceinline__ float from_e8m0(uint32_t code) {
-    return code == 255u ? __int_as_float(0x7fc00000) : code == 0u ? __int_as_float(0x00400000) : __uint_as_float(code << 23);
+    uint32_t b;
+    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(b) : "h"(static_cast<uint16_t>(code)));
+    return __uint_as_float(b << 16);
 }
 template <int FORMAT>
 __device__ __forceinline__ float fp4_scale(uint32_t code) {

@@ -539,8 +539,12 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__
 // ---- any layout: CUDA cores ----------------------------------------------------------
 constexpr int kGTile = 64, kGK = 32;
 
+// An element of format MX may pass FP32's range with its scale (2^126 and 2^127) where its products do
+// not: both operands are taken at a quarter, which is exact, and the sum 16 times (exact, as are the
+// products, but for sums that would be subnormal: those are off by 2^-145 a term at most).
 template <int FORMAT>
 __global__ void __launch_bounds__(256) fp4_generic_kernel(const Fp4Args a) {
+    constexpr float kLess = FORMAT == SGEMM_FP4_MX ? 0.25f : 1.f;
     __shared__ float at[kGK][kGTile + 4], bt[kGK][kGTile + 4];
     griddep_wait();
     griddep_launch_dependents();
@@ -561,7 +565,7 @@ __global__ void __launch_bounds__(256) fp4_generic_kernel(const Fp4Args a) {
                 }
                 uint32_t h[4];
                 from_e2m1x8(code, h);
-                const float f = fp4_scale<FORMAT>(scale);
+                const float f = fp4_scale<FORMAT>(scale) * kLess;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     to[tid % 4 * 8 + e][r] = __half2float(__ushort_as_half(static_cast<uint16_t>(h[e / 2] >> (16 * (e & 1))))) * f;
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(256) fp4_generic_kernel(const Fp4Args a) {
                     const int n = n0 + tx * 4 + j;
                     if (n >= a.N) break;
                     const float sb = a.rowB ? __ldcg(a.rowB + n) : 1.f;
-                    static_cast<typename El::T *>(a.C)[m * a.ldc + n] = El::down(fmaf(acc[i][j] * sb, sa, a.bias ? __ldcg(a.bias + n) : 0.f));
+                    static_cast<typename El::T *>(a.C)[m * a.ldc + n] = El::down(fmaf(acc[i][j] * (1.f / (kLess * kLess)) * sb, sa, a.bias ? __ldcg(a.bias + n) : 0.f));
                 }
             }
         });

@@ -390,21 +390,28 @@ dequantize_kernel(const RowArgs a, unsigned across) {
             scale[k] = __ldca(s + static_cast<long long>(blk / 4) * 512 + (blk & 3));
         }
         const float row = a.row ? __ldca(a.row + i) : 1.f;
+        auto put = [&](float less, float row) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-            const int p = at + k * 256 * A;
-            if (p >= a.K) continue;
-            uint32_t h[4];
-            from_e2m1x8(code[k], h);
-            const float f = fp4_scale<FORMAT>(scale[k]);
-            alignas(16) T o[A];
+            for (int k = 0; k < kSteps; ++k) {
+                const int p = at + k * 256 * A;
+                if (p >= a.K) continue;
+                uint32_t h[4];
+                from_e2m1x8(code[k], h);
+                const float f = fp4_scale<FORMAT>(scale[k]) * less;
+                alignas(16) T o[A];
 #pragma unroll
-            for (int e = 0; e < A; ++e) {
-                const float v = __half2float(__ushort_as_half(static_cast<uint16_t>(h[e / 2] >> (16 * (e & 1)))));
-                o[e] = El::down(__fmul_rn(__fmul_rn(v, f), row));
+                for (int e = 0; e < A; ++e) {
+                    const float v = __half2float(__ushort_as_half(static_cast<uint16_t>(h[e / 2] >> (16 * (e & 1)))));
+                    o[e] = El::down(__fmul_rn(__fmul_rn(v, f), row));
+                }
+                *reinterpret_cast<W *>(y + p) = *reinterpret_cast<const W *>(o);
             }
-            *reinterpret_cast<W *>(y + p) = *reinterpret_cast<const W *>(o);
-        }
+        };
+        // A code times 2^126 or 2^127 (MX) may pass FP32's range where that times a small row scale does
+        // not: such scales are taken at a quarter and the row's four times, both exact.
+        const bool large = FORMAT == SGEMM_FP4_MX && max(max(scale[0], scale[1]), max(scale[2], scale[3])) >= 253u;
+        if (large && fabsf(row) < 0x1p126f) put(0.25f, row * 4.f);
+        else put(1.f, row);
     }
 }
 
