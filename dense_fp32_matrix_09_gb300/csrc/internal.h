@@ -358,7 +358,7 @@ struct NormGradArgs {
     void *dX;
     long long lddx;
     float *dW;
-    float *parts;  // workspace: as many rows of K as fit, at least one (kNormHeld: 16)
+    float *parts;  // workspace: as many rows of K as fit, at least one (of kNormHeld elements: 768)
     int *status;
 };
 cudaError_t norm_prepare();

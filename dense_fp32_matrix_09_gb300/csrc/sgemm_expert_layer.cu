@@ -22,7 +22,8 @@
 // each weight once.  (The MMA's rate does not show: without the MMAs the kernels take 5 %
 // less.  What does is the conversion, two instructions a weight.)  The order of k within an MMA
 // is free, so a lane's 16 bytes are the k of four MMAs.  An int8 is exact in BF16 and in FP16;
-// the tokens' elements go in as they are or, FP32, as sums of three BF16 values, exact as well.
+// the tokens' elements go in as they are or, FP32, as sums of three BF16 values, exact as well (but
+// from 3.396e38 on, which BF16 rounds to infinity, and what is below 2^-133 of tiny ones).
 // The hidden values are kept as two BF16 values, 16 bits of fraction, and with FP32 rows as three:
 // rounded to the rows' type they would halve the second kernel's loads and MMAs (8 tokens 126 us -> 116
 // with stages of 16 rows), but also add as much error to the result as its own rounding does, and in FP16 they
@@ -1063,7 +1064,8 @@ cudaError_t layer_typed(LayerArgs a, bool boundaries, const LayerMaps &m, int nu
                                 Cf::down_smem(a.tokens, wide ? 2 : 1), stream, 1, m.down, a);
     }
     const long long items = asked * (a.hidden_ld / (a.gated ? 8 : 16));
-    // warps that share an item's K: all eight unless that leaves a CTA many rounds
+    // Warps that share an item's K: all eight unless that leaves a CTA many rounds (us, eight against the
+    // rule: 16 tokens, 4 of 32 experts, 65 x 1001 66, 53; 64 tokens 100, 82; 64 tokens, 129 x 2001 199, 158).
     int share = kWarps;
     while (share > 1 && items > 4ll * num_sms * (kWarps / share) && (a.width + kChunk - 1) / kChunk <= 2 * share) share /= 2;
     cudaError_t e = launch_dependent(a.gated ? up_kernel<El, NT, true> : up_kernel<El, NT, false>, grid((items + kWarps / share - 1) / (kWarps / share), 2ll * num_sms),
@@ -1081,7 +1083,10 @@ cudaError_t layer_for(const LayerArgs &a, int num_sms, cudaStream_t stream) {
                             a.hidden % 16 == 0 && a.hidden > 0 && up_rows < kMostRows && down_rows < kMostRows &&
                             encode_map(&m.up, MapType::kInt8, 2, a.up, a.width, up_rows, 1, a.width, 0, 128, 16) &&
                             encode_map(&m.down, MapType::kInt8, 2, a.down, a.hidden, down_rows, 1, a.hidden, 0, 128, 16);
-    // tokens that share an expert's weights in one go: 8, 16 or 32
+    // Tokens that share an expert's weights in one go: 8, 16 or 32, the last where there are more than 12
+    // choices an expert (us in 16s and in 32s, gated, 2048 x 1408: 8 an expert, 64 tokens, 2 of 16: 71.5,
+    // 89.5; 12, 24 tokens, 2 of 4: 28.8, 34.2; 16, 64 tokens, 4 of 16: 111, 120; 24, 48 tokens, 4 of 8: 83.5,
+    // 77.2; but 32, 64 tokens, 2 of 4: 53.3, 60.6).
     if (a.tokens <= 8) return layer_typed<El, 1>(a, boundaries, m, num_sms, stream);
     if (a.tokens <= 16 || a.tokens * a.choices <= 12 * a.experts) return layer_typed<El, 2>(a, boundaries, m, num_sms, stream);
     return layer_typed<El, 4>(a, boundaries, m, num_sms, stream);

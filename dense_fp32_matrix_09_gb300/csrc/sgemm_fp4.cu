@@ -15,7 +15,7 @@
 //    persistent, for many tokens: each CTA holds 128 of the channels and 128 of the
 //    tokens.  The epilogue's eight warps take the whole accumulator into registers
 //    and leave it to the next tile's MMAs before they write C.  8192^3: 161 us in short runs
-//    (NV, 6.8 PFLOP/s; MX 174), 180 when repeated until the power limit shows.  What bounds
+//    (NV, 6.8 PFLOP/s; MX 174), 182 to 187 when repeated until the power limit shows.  What bounds
 //    it: with a quarter of the MMAs 151 us, without the operands' loads 133 (2.5 GB cross from
 //    L2 to the SMs, 16.5 TB/s), without the writes of C 147 (the accumulator's way into
 //    registers, 1 us a tile, in which no MMA runs).

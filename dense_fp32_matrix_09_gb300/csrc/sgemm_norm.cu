@@ -13,9 +13,9 @@
 //    One pass over HBM: a row stays in the registers of the TPR threads that share
 //    it (up to 4 x 8 elements a thread; longer rows are read a second time, from L2).
 //    8192 x 8192 BF16 with the residual to 8 bits 67.8 us, HBM's rate; 32 x 4096 2.1 us in
-//    a graph.  To 4 bits the instructions count too: 8192 x 8192 FP16 to MX 30 us (floor
-//    25), to NV, whose scales wait for the whole row, 38.
-//  * dequantize_kernel -- 4-bit rows to what they stand for: the same matrix 29 us (floor 25).
+//    a graph.  To 4 bits the instructions count too: 8192 x 8192 FP16 to MX 29.5 us (floor
+//    25), to NV, whose scales wait for the whole row, 37.4.
+//  * dequantize_kernel -- 4-bit rows to what they stand for: the same matrix 27.7 us (floor 25).
 //
 // No load is a read-only-cache load: what is read may have been written by the
 // kernel before, whose end the launch overlaps.
@@ -303,7 +303,10 @@ row_kernel(const RowArgs a) {
 
 // Threads a row: enough that it stays in registers (32 elements a thread), and, with
 // too few rows to fill the GPU, more of them so that each thread loads less; rows of
-// at most eight elements a thread take a kernel of one piece.
+// at most eight elements a thread take a kernel of one piece.  (us, BF16 to 8 bits with the
+// residual, 8 elements a thread against 32: 32 x 4096 2.05, 2.44; 304 x 2048 2.1, 2.4; 912 x 4096 6.1,
+// 4.2; 4864 x 512 7.1, 4.8.  Rows of 8192 have 16 a thread at best and lose by it: 304 of them
+// 5.7, 3.3.)
 template <class El, int A, bool NORM, int OUT>
 cudaError_t row_typed(const RowArgs &a, int num_sms, cudaStream_t stream) {
     const int per = a.M <= 4 * num_sms ? kV : 4 * kV;

@@ -241,8 +241,8 @@ norm_grad_ring_kernel(const NormGradArgs a, int stages) {
         }
 }
 
-// dw[p] = sum of column p of `parts` (n rows): 32 columns a block, each warp's rows
-// 8 apart, then the warps' sums.
+// dw[p] = sum of column p of `parts` (n rows): 32 columns a block, each of its 32 warps
+// the rows 32 apart, then the warps' sums.
 __global__ void __launch_bounds__(1024) columns_kernel(const float *parts, int n, int K, float *dw) {
     __shared__ float sums[32][33];
     griddep_wait();
@@ -365,7 +365,10 @@ cudaError_t grad_for(const NormGradArgs &a, int num_sms, size_t ws_floats, cudaS
         return a.K % n == 0 && unit(a.dY, a.lddy, n) && unit(a.H, a.ldh, n) && unit(a.dH, a.lddh, n) && unit(a.W, 0, n) && unit(a.dX, a.lddx, n);
     };
     if (fits(V)) {
-        // rows long enough that a block has one at a time, and enough of them to go round
+        // Rows long enough that a block has one at a time, and enough of them to go round (us with the
+        // columns' sums, BF16 with both gradients, ring against registers: 8192 x 4096 47.4, 61.3; 912 x 2056
+        // 8.9, 9.7; 640 x 4096 11.3, 12.0).  With fewer the two are near (608 x 4096 11.5, 11.9; 64 x 2056 4.5,
+        // 4.3) but in rows of 8192, which take the registers of 512 threads (608 of them 14.2, 21.4).
         if (a.K > 2048 && a.M > 4 * num_sms) {
             if (a.K <= 4096) return grad_ring<El, 256, 2>(a, num_sms, ws_floats, stream);
             if (a.K <= 8192) return grad_ring<El, 512, 2>(a, num_sms, ws_floats, stream);

@@ -934,7 +934,8 @@ class Sgemm:
         n = sgemm_fp4_scale_bytes(format, M, K)
         if n < 0:
             raise ValueError(f"unknown 4-bit format {format}")
-        # rows on 16-byte boundaries; scales of rows behind the last are read with them, so zeros
+        # rows on 16-byte boundaries; scales of rows behind the last, which the kernels leave alone, are
+        # zeros, so that the whole buffer may be stored or compared
         return Fp4Rows(torch.empty(M, max(-(-K // 32) * 16, 1), dtype=torch.uint8, **new), torch.zeros(n, dtype=torch.uint8, **new),
                        # (rows of no elements are not touched: their products are 0)
                        (torch.empty if K else torch.zeros)(M, dtype=torch.float32, **new) if with_row else None, K, format)
