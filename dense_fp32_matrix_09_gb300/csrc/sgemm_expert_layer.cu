@@ -316,13 +316,23 @@ __device__ __forceinline__ void split_token(const Raw<El> &r, uint32_t (&to)[Par
     }
 }
 
-// acc += 16 channels x 64 k (lo: channel g, hi: channel g + 8) times 8 tokens.
+// acc += 16 channels x 64 k (lo: channel g, hi: channel g + 8) times 8 tokens.  An MMA truncates its sum:
+// FP32 tokens' 64 k are summed by themselves, the low parts first, and added with rounding to nearest
+// (a chain of 12 MMAs every 64 k: errors of 2e-6 to 4e-6 of the result where FP32 products on the
+// CUDA cores have 2e-7 to 4e-7).
 template <class Mma, int P>
 __device__ __forceinline__ void multiply(float (&acc)[4], const uint32_t (&a)[4][4], const uint32_t (&x)[P][8]) {
+    float sum[4] = {};
+    float(&to)[4] = P == 3 ? sum : acc;
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int q = 0; q < 4 * P; ++q) {
+        const int s = P == 3 ? q % 4 : q / P, p = P == 3 ? P - 1 - q / 4 : P - 1 - q % P;
+        mma16<Mma>(to, a[s], x[p][2 * s], x[p][2 * s + 1]);
+    }
+    if (P == 3) {
 #pragma unroll
-        for (int p = P - 1; p >= 0; --p) mma16<Mma>(acc, a[s], x[p][2 * s], x[p][2 * s + 1]);
+        for (int j = 0; j < 4; ++j) acc[j] += sum[j];
+    }
 }
 template <class Mma>
 __device__ __forceinline__ void expand_rows(const uint4 &lo, const uint4 &hi, uint32_t (&a)[4][4]) {
